@@ -95,9 +95,10 @@ enum {
 };
 
 /* Library version, as MAJOR*10000 + MINOR*100 + PATCH.  The minor number changes with every
- * change of an entry point's arguments; a caller built against this header should check that
- * m2rnn_version() == M2RNN_VERSION before calling anything else. */
-#define M2RNN_VERSION 400
+ * change of an entry point's arguments, the patch number when entry points are added; a caller
+ * built against this header should check that m2rnn_version() == M2RNN_VERSION before calling
+ * anything else. */
+#define M2RNN_VERSION 401
 int m2rnn_version(void);
 
 /* Human-readable text for a status code (static storage). */
@@ -376,6 +377,68 @@ int m2rnn_conv4_silu_bwd_workspace_size(int64_t B, int64_t T, int64_t C, size_t*
 int m2rnn_conv4_silu_bwd(int64_t B, int64_t T, int64_t C, int dtype, const void* x, const float* w,
                          const float* bias, const float* du, float* dx, float* dw, float* dbias,
                          void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Selective state space scan: the linear recurrence with a scalar decay per head that hybrid stacks
+ * place next to M²RNN blocks.  Per (b, n), from H_0 (zeros, or a given state),
+ *
+ *     D_t = softplus(a_t + beta),     f_t = exp(-alpha D_t)
+ *     H_t = f_t H_{t-1} + D_t k_t v_t^T
+ *     y_t = H_t^T q_t + w_r (.) v_t
+ *
+ * f_t is the M²RNN gate (m2rnn_gate_fwd) of the same a, alpha, beta; the step size D_t also scales
+ * the write.  alpha >= 0 keeps f in [0, 1] (not checked, computed as given).
+ *
+ *   dims       as above, with K a multiple of 16 up to 128, and Nqk 0 (= N) or any divisor of N: query/key
+ *              j serves the heads j N/Nqk .. (j + 1) N/Nqk - 1.  Tensors may exceed 4 GiB; B N (T / 32 + 64)
+ *              must stay below 2^28.
+ *   a          gate pre-activation [B,T,N] fp32; alpha, beta [N] fp32; w_r [N,V] fp32 (a, alpha, beta
+ *              and lens 4-byte aligned, everything else 16-byte).
+ *   lens       [B] int32 device array or NULL: the steps of each batch entry, clamped to [0, T] (NULL:
+ *              all T).  Steps at or past a sequence's end are not read (whatever they hold), their
+ *              y is written as zeros, H_T is the state after the last step within, and their
+ *              gradients are zeros.
+ *   y          [B,T,N,V] fp32; H_T [B,N,K,V] fp32, or NULL to skip it.
+ *   ckpt       m2rnn_ssm_fwd_ckpt also keeps the states that enter every I-th step for the backward,
+ *              [B,N,ceil(T/I),K,V] fp32 with I = m2rnn_ssm_checkpoint_interval().
+ *   workspace  at least the *_workspace_size() bytes (NULL if that is 0).  Long sequences with few heads
+ *              run as time segments whose entering states are kept there.
+ *
+ * Products run on the bf16 MFMA with fp32 accumulation, every computed fp32 operand (decayed scores,
+ * states, gradients) and fp32 input split into three bf16 planes (24 bits), so results are those
+ * of fp32 arithmetic; the sums of log decays within a chunk are formed in fp64.  Operands must lie
+ * within the bf16 (= fp32) range; values below 2^-110 may lose low bits.
+ * Two calls on the same inputs give the same bits, and need not equal another segmentation's.
+ *
+ * m2rnn_ssm_bwd gives the gradients of L = sum <dy, y> + <dH_T, H_T>: dq, dk [B,T,Nqk,K] (summed
+ * over the heads that share them), dv [B,T,N,V], da [B,T,N], dalpha, dbeta [N], dw_r [N,V] and dH0
+ * [B,N,K,V] (NULL to skip), all fp32, from m2rnn_ssm_fwd_ckpt's ckpt on the same inputs.
+ */
+int m2rnn_ssm_checkpoint_interval(int qkv_dtype, int64_t* steps);
+int m2rnn_ssm_fwd_workspace_size(const m2rnn_dims* dims, int qkv_dtype, size_t* bytes);
+int m2rnn_ssm_fwd(const m2rnn_dims* dims, int qkv_dtype, const void* q, const void* k, const void* v,
+                  const float* a, const float* alpha, const float* beta, const float* w_r,
+                  const int32_t* lens, const float* H0, float* y, float* H_T, void* workspace,
+                  size_t workspace_bytes, void* stream);
+int m2rnn_ssm_fwd_ckpt(const m2rnn_dims* dims, int qkv_dtype, const void* q, const void* k, const void* v,
+                       const float* a, const float* alpha, const float* beta, const float* w_r,
+                       const int32_t* lens, const float* H0, float* y, float* H_T, float* ckpt,
+                       void* workspace, size_t workspace_bytes, void* stream);
+int m2rnn_ssm_bwd_workspace_size(const m2rnn_dims* dims, int qkv_dtype, size_t* bytes);
+int m2rnn_ssm_bwd(const m2rnn_dims* dims, int qkv_dtype, const void* q, const void* k, const void* v,
+                  const float* a, const float* alpha, const float* beta, const float* w_r,
+                  const int32_t* lens, const float* ckpt, const float* dy, const float* dH_T, float* dq,
+                  float* dk, float* dv, float* da, float* dalpha, float* dbeta, float* dw_r, float* dH0,
+                  void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * One step of the selective scan for every (b, n), the state in device memory (dims->T = 1; layouts
+ * with T = 1).  H_in NULL: zeros.  H_out == H_in updates in place; any other overlap of the two is
+ * rejected (M2RNN_EINVAL).  No workspace.  fp32 arithmetic.
+ */
+int m2rnn_ssm_step(const m2rnn_dims* dims, int qkv_dtype, const void* q, const void* k, const void* v,
+                   const float* a, const float* alpha, const float* beta, const float* w_r,
+                   const float* H_in, float* H_out, float* y, void* stream);
 
 #ifdef __cplusplus
 }

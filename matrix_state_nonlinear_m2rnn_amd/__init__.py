@@ -9,6 +9,7 @@ call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import sys
@@ -37,6 +38,8 @@ EXPORTED = (
     "m2rnn_conv4_silu_fwd", "m2rnn_conv4_silu_bwd_workspace_size", "m2rnn_conv4_silu_bwd",
     "m2rnn_fwd_block_workspace_size", "m2rnn_fwd_block", "m2rnn_overlap_create", "m2rnn_overlap_destroy",
     "m2rnn_fwd_noalloc", "m2rnn_fwd_noalloc_max_bytes", "m2rnn_scan_bwd", "m2rnn_scan_bwd_finish",
+    "m2rnn_ssm_checkpoint_interval", "m2rnn_ssm_fwd_workspace_size", "m2rnn_ssm_fwd", "m2rnn_ssm_fwd_ckpt",
+    "m2rnn_ssm_bwd_workspace_size", "m2rnn_ssm_bwd", "m2rnn_ssm_step",
 )
 
 
@@ -55,7 +58,7 @@ class M2RNNError(RuntimeError):
 _lib = None
 
 # The C ABI version these bindings are written for (M2RNN_VERSION in include/m2rnn.h).
-ABI_VERSION = 400
+ABI_VERSION = 401
 
 
 def lib() -> ctypes.CDLL:
@@ -131,6 +134,18 @@ def lib() -> ctypes.CDLL:
         L.m2rnn_fwd_block.restype = ci
         L.m2rnn_fwd_block.argtypes = ([dp, ci, ci, ci] + [vp] * 3 + [vp] * 3 + [vp] * 3 + [vp, ci, vp, cf]
                                       + [vp, vp] + [vp, sz, vp, vp])
+        for name, args in (
+            ("m2rnn_ssm_checkpoint_interval", [ci, ctypes.POINTER(i64)]),
+            ("m2rnn_ssm_fwd_workspace_size", [dp, ci, ctypes.POINTER(sz)]),
+            ("m2rnn_ssm_fwd", [dp, ci] + [vp] * 11 + [vp, sz, vp]),
+            ("m2rnn_ssm_fwd_ckpt", [dp, ci] + [vp] * 12 + [vp, sz, vp]),
+            ("m2rnn_ssm_bwd_workspace_size", [dp, ci, ctypes.POINTER(sz)]),
+            ("m2rnn_ssm_bwd", [dp, ci] + [vp] * 19 + [vp, sz, vp]),
+            ("m2rnn_ssm_step", [dp, ci] + [vp] * 10 + [vp]),
+        ):
+            fn = getattr(L, name)
+            fn.restype = ci
+            fn.argtypes = args
         L.m2rnn_decode_step.restype = ci
         L.m2rnn_decode_step.argtypes = [dp, ci, ci] + [vp] * 3 + [vp] * 3 + [vp, vp, vp, vp]
         _lib = L
@@ -649,3 +664,159 @@ def m2rnn_conv4_silu_bwd(x, w, bias, du, *, workspace=None, stream=None) -> Dict
         B, T, C, _dtype_code(x), _ptr(x), _ptr(w), _ptr(bias), _ptr(du), _ptr(out["dx"]), _ptr(out["dw"]),
         _ptr(out["dbias"]), _ptr(ws), nbytes, _stream(stream)))
     return out
+
+
+# ---------------------------------------------------------------- selective state space scan
+
+@contextlib.contextmanager
+def _call_on(dev, stream):
+    """The device and stream of a call, for its allocations too: a workspace that returns to the caching
+    allocator is then only handed out again behind the call's own work."""
+    import torch
+    with torch.cuda.device(dev):
+        if stream is None:
+            yield
+        else:
+            with torch.cuda.stream(stream):
+                yield
+
+
+def _ssm_dims(q, k, v, a, alpha, beta, w_r, token):
+    """Checks the scan's inputs and returns (dims, dtype code).  token: no time axis."""
+    import torch
+    lead = 1 if token else 2
+    if q.dim() != lead + 2 or v.dim() != lead + 2:
+        raise ValueError("q must be [B,Nqk,K] and v [B,N,V]" if token else "q must be [B,T,Nqk,K] and v [B,T,N,V]")
+    B, T = q.shape[0], 1 if token else q.shape[1]
+    Nqk, K = q.shape[-2:]
+    N, V = v.shape[-2:]
+    if N > 0 and (Nqk < 1 or N % Nqk):
+        raise ValueError(f"q and k carry {Nqk} heads: expected a divisor of {N}")
+    dev = q.device
+    if dev.type != "cuda":
+        raise ValueError("inputs must be on a GPU (HIP) device")
+    if q.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError("q, k, v must be float32 or bfloat16")
+    top = tuple(q.shape[:lead])
+    _require(q, "q", q.dtype, top + (Nqk, K), dev)
+    _require(k, "k", q.dtype, top + (Nqk, K), dev)
+    _require(v, "v", q.dtype, top + (N, V), dev)
+    _require(a, "a", torch.float32, top + (N,), dev)
+    _require(alpha, "alpha", torch.float32, (N,), dev)
+    _require(beta, "beta", torch.float32, (N,), dev)
+    _require(w_r, "w_r", torch.float32, (N, V), dev)
+    return Dims(B, T, N, K, V, Nqk), DTYPE_BF16 if q.dtype == torch.bfloat16 else DTYPE_F32
+
+
+def ssm_checkpoint_interval(qkv_dtype: int) -> int:
+    """Steps between the checkpoints of m2rnn_ssm_fwd_ckpt for a dtype code (DTYPE_BF16, DTYPE_F32)."""
+    n = ctypes.c_int64(0)
+    _check("m2rnn_ssm_checkpoint_interval", lib().m2rnn_ssm_checkpoint_interval(qkv_dtype, ctypes.byref(n)))
+    return int(n.value)
+
+
+def _ssm_fwd(q, k, v, a, alpha, beta, w_r, H0, lens, y, H_T, ckpt, keep, return_state, workspace, stream):
+    import torch
+    dims, dt = _ssm_dims(q, k, v, a, alpha, beta, w_r, False)
+    B, T, N, K, V = dims.B, dims.T, dims.N, dims.K, dims.V
+    dev = q.device
+    if H0 is not None:
+        _require(H0, "H0", torch.float32, (B, N, K, V), dev)
+    if lens is not None:
+        _require(lens, "lens", torch.int32, (B,), dev)
+    with _call_on(dev, stream):
+        if y is None:
+            y = torch.empty((B, T, N, V), dtype=torch.float32, device=dev)
+        _require(y, "y", torch.float32, (B, T, N, V), dev)
+        if H_T is None and return_state:
+            H_T = torch.empty((B, N, K, V), dtype=torch.float32, device=dev)
+        if H_T is not None:
+            _require(H_T, "H_T", torch.float32, (B, N, K, V), dev)
+        nbytes = _size_query("m2rnn_ssm_fwd_workspace_size", ctypes.byref(dims), dt)
+        ws = _workspace(nbytes, dev, workspace)
+        args = [ctypes.byref(dims), dt, _ptr(q), _ptr(k), _ptr(v), _ptr(a), _ptr(alpha), _ptr(beta), _ptr(w_r),
+                _ptr(lens), _ptr(H0), _ptr(y), _ptr(H_T)]
+        if not keep:
+            _check("m2rnn_ssm_fwd", lib().m2rnn_ssm_fwd(*args, _ptr(ws), nbytes, _stream(stream)))
+            return y, H_T
+        shape = (B, N, -(-T // ssm_checkpoint_interval(dt)), K, V)
+        if ckpt is None:
+            ckpt = torch.empty(shape, dtype=torch.float32, device=dev)
+        _require(ckpt, "ckpt", torch.float32, shape, dev)
+        _check("m2rnn_ssm_fwd_ckpt", lib().m2rnn_ssm_fwd_ckpt(*args, _ptr(ckpt), _ptr(ws), nbytes, _stream(stream)))
+        return y, H_T, ckpt
+
+
+def m2rnn_ssm_fwd(q, k, v, a, alpha, beta, w_r, H0=None, *, lens=None, y=None, H_T=None, return_state: bool = True,
+                  workspace=None, stream=None) -> Tuple[object, object]:
+    """Selective state space scan: D = softplus(a + beta), f = exp(-alpha D), H_t = f_t H_{t-1} + D_t k_t v_t^T,
+    y_t = H_t^T q_t + w_r (.) v_t.
+
+    q, k: [B,T,Nqk,K] (Nqk divides N: each query/key serves N/Nqk consecutive heads); v: [B,T,N,V]
+    (float32 or bfloat16, all alike); a: [B,T,N]; alpha, beta: [N]; w_r: [N,V]; H0: [B,N,K,V] or None,
+    all float32; lens: [B] int32 or None (steps at or past a sequence's end are not read and give
+    y = 0).  Returns (y [B,T,N,V], H_T [B,N,K,V])."""
+    return _ssm_fwd(q, k, v, a, alpha, beta, w_r, H0, lens, y, H_T, None, False, return_state, workspace, stream)
+
+
+def m2rnn_ssm_fwd_ckpt(q, k, v, a, alpha, beta, w_r, H0=None, *, lens=None, y=None, H_T=None, ckpt=None,
+                       return_state: bool = True, workspace=None, stream=None) -> Tuple[object, object, object]:
+    """m2rnn_ssm_fwd that also keeps the states m2rnn_ssm_bwd takes; returns (y, H_T, ckpt)."""
+    return _ssm_fwd(q, k, v, a, alpha, beta, w_r, H0, lens, y, H_T, ckpt, True, return_state, workspace, stream)
+
+
+def m2rnn_ssm_bwd(q, k, v, a, alpha, beta, w_r, ckpt, dy, dH_T=None, *, lens=None, want_dH0: bool = True,
+                  workspace=None, stream=None, out=None) -> Dict[str, object]:
+    """Gradients of L = sum <dy, y> + <dH_T, H_T> of the selective scan, from the checkpoints that
+    m2rnn_ssm_fwd_ckpt kept on the same inputs (and lens): dq, dk (summed over the heads that share them),
+    dv, da, dalpha, dbeta, dw_r, dH0 (None unless want_dH0).  `out` may hold the tensors to write."""
+    import torch
+    dims, dt = _ssm_dims(q, k, v, a, alpha, beta, w_r, False)
+    B, T, N, K, V, Nqk = dims.B, dims.T, dims.N, dims.K, dims.V, dims.Nqk
+    dev = q.device
+    _require(ckpt, "ckpt", torch.float32, (B, N, -(-T // ssm_checkpoint_interval(dt)), K, V), dev)
+    _require(dy, "dy", torch.float32, (B, T, N, V), dev)
+    if dH_T is not None:
+        _require(dH_T, "dH_T", torch.float32, (B, N, K, V), dev)
+    if lens is not None:
+        _require(lens, "lens", torch.int32, (B,), dev)
+    shapes = {"dq": (B, T, Nqk, K), "dk": (B, T, Nqk, K), "dv": (B, T, N, V), "da": (B, T, N), "dalpha": (N,),
+              "dbeta": (N,), "dw_r": (N, V), "dH0": (B, N, K, V)}
+    with _call_on(dev, stream):
+        if out is None:
+            out = {x: torch.empty(s, dtype=torch.float32, device=dev) if x != "dH0" or want_dH0 else None
+                   for x, s in shapes.items()}
+        for x, s in shapes.items():
+            if x != "dH0" or out.get(x) is not None:
+                _require(out.get(x), x, torch.float32, s, dev)
+        nbytes = _size_query("m2rnn_ssm_bwd_workspace_size", ctypes.byref(dims), dt)
+        ws = _workspace(nbytes, dev, workspace)
+        _check("m2rnn_ssm_bwd", lib().m2rnn_ssm_bwd(
+            ctypes.byref(dims), dt, _ptr(q), _ptr(k), _ptr(v), _ptr(a), _ptr(alpha), _ptr(beta), _ptr(w_r), _ptr(lens),
+            _ptr(ckpt), _ptr(dy), _ptr(dH_T), *(_ptr(out.get(x)) for x in shapes), _ptr(ws), nbytes, _stream(stream)))
+    return out
+
+
+def m2rnn_ssm_step(q, k, v, a, alpha, beta, w_r, H=None, *, H_out=None, y=None, stream=None) -> Tuple[object, object]:
+    """One step of the selective scan with the state in device memory (decode).
+
+    q, k: [B,Nqk,K]; v: [B,N,V] (float32 or bfloat16, all alike); a: [B,N]; alpha, beta: [N]; w_r: [N,V];
+    H: the state [B,N,K,V] fp32 or None (zeros).  Returns (y [B,N,V], H_out [B,N,K,V]).  Pass ``H_out=H``
+    to update the state in place."""
+    import torch
+    dims, dt = _ssm_dims(q, k, v, a, alpha, beta, w_r, True)
+    B, N, K, V = dims.B, dims.N, dims.K, dims.V
+    dev = q.device
+    if H is not None:
+        _require(H, "H", torch.float32, (B, N, K, V), dev)
+    with _call_on(dev, stream):
+        if H_out is None:
+            H_out = torch.empty((B, N, K, V), dtype=torch.float32, device=dev)
+        _require(H_out, "H_out", torch.float32, (B, N, K, V), dev)
+        if y is None:
+            y = torch.empty((B, N, V), dtype=torch.float32, device=dev)
+        _require(y, "y", torch.float32, (B, N, V), dev)
+        _check("m2rnn_ssm_step", lib().m2rnn_ssm_step(
+            ctypes.byref(dims), dt, _ptr(q), _ptr(k), _ptr(v), _ptr(a), _ptr(alpha), _ptr(beta), _ptr(w_r), _ptr(H),
+            _ptr(H_out), _ptr(y), _stream(stream)))
+    return y, H_out

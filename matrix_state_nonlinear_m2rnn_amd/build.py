@@ -25,6 +25,11 @@ SOURCES = [
     "m2rnn_fwd_bf16.hip",
     "m2rnn_decode.hip",
     "m2rnn_block.hip",
+    "m2rnn_ssm.hip",
+    "m2rnn_ssm_bf16.hip",
+    "m2rnn_ssm_f32.hip",
+    "m2rnn_ssm_bwd_bf16.hip",
+    "m2rnn_ssm_bwd_f32.hip",
 ]
 
 # Packed fp32 VALU ops stay off: hipcc -O3 would otherwise form v_pk_{add,mul,fma}_f32.

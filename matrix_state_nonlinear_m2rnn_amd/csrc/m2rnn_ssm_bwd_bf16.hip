@@ -1,0 +1,6 @@
+// The selective scan's backward kernels for bf16 q, k, v.
+#include "m2rnn_ssm_select.h"
+
+namespace m2rnn {
+const void* ssm_bwd_kernel_bf16(int KP, int VB) { return ssm_pick_bwd<true>(KP, VB); }
+}  // namespace m2rnn

@@ -1,0 +1,6 @@
+// The selective scan's backward kernels for f32 q, k, v.
+#include "m2rnn_ssm_select.h"
+
+namespace m2rnn {
+const void* ssm_bwd_kernel_f32(int KP, int VB) { return ssm_pick_bwd<false>(KP, VB); }
+}  // namespace m2rnn

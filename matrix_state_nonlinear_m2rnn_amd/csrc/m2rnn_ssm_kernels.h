@@ -1,0 +1,1047 @@
+// Kernels of the selective state space scan (mathematics and precision: m2rnn_ssm_device.h).
+//
+//   m2rnn_ssm_state_kernel    what each time segment adds to the state (k, v and a alone), or in the
+//                             reverse scan what each chunk and segment adds to the gradient's state
+//   m2rnn_ssm_combine_kernel  the states that enter the segments, from those parts and the first state
+//   m2rnn_ssm_fwd_kernel      y (and checkpoints and H_T), segment by segment, chunk after chunk
+//   m2rnn_ssm_bwd_kernel      all gradients of one chunk, from the states on both of its sides
+//   m2rnn_ssm_step_kernel     one token with the state in HBM
+//
+// Segments.  Within a workgroup the chunks of a segment follow each other with the state in
+// registers; the launch cuts the sequence into as many segments as fill the chip.  The extra cost
+// is reading k and v a second time (a third of the bytes at K = V); one kernel with a workgroup per
+// (b, n) would leave 3/4 of the CUs idle at 64 pairs.
+#pragma once
+
+#include "m2rnn_ssm_device.h"
+
+namespace m2rnn {
+
+struct SsmArgs {
+  const void *q, *k, *v;                   // [B,T,G,K], [B,T,G,K], [B,T,N,V]
+  const float *a, *alpha, *beta, *w_r;     // [B,T,N], [N], [N], [N,V]
+  const int* lens;                         // [B] or null (T)
+  const float *H0, *dy, *dH_T;             // [B,N,K,V], [B,T,N,V], [B,N,K,V]
+  float *y, *H_T, *ckpt;                   // ckpt [B,N,nch,K,V]
+  float* seg;                              // [B,N,S,K,V] ([V,K] in the reverse scan)
+  float* segdec;                           // [B,N,S] log2 decay of each segment
+  float* rloc;                             // [B,N,nch,V,K] reverse: the part of the segment's later chunks
+  float* cdec;                             // [B,N,nch] reverse: log2 decay from the chunk's end to the segment's
+  float *dq, *dk, *dv, *da;                // dq, dk: HS planes of [B,T,G,K]
+  float *part_gate, *part_wr;              // [B nch][2N] (dbeta, dalpha), [B nch][N V]
+  float* dH0;
+  int B, T, N, G, K, V;
+  int S, cps, nch;                         // segments, chunks per segment, chunks
+  int HB, CB, HS;                          // head blocks per group, column blocks per head, head splits (backward)
+};
+
+// Steps of batch entry b (lens is clamped, so a value out of range cannot lead past the arrays).
+__device__ __forceinline__ int ssm_len(const SsmArgs& A, int b) {
+  if (!A.lens) return A.T;
+  const int n = A.lens[b];
+  return n < 0 ? 0 : (n > A.T ? A.T : n);
+}
+
+// blockIdx -> (unit, share): the `share` workgroups of a unit read the same q and k rows.  They get
+// ids that agree mod 8, which the dispatcher places on one XCD, so its L2 serves them.
+__device__ __forceinline__ void ssm_unit(int shares, int units, int& unit, int& share) {
+  const int id = blockIdx.x;
+  if (shares > 1 && units % 8 == 0) {
+    const int r = id / 8;
+    share = r % shares;
+    unit = (r / shares) * 8 + id % 8;
+  } else {
+    unit = id / shares;
+    share = id % shares;
+  }
+}
+
+// Row and column tile of the t-th lower-triangular tile (t = I (I + 1) / 2 + J).
+__device__ __forceinline__ void tri_tile(int t, int& I, int& J) {
+  I = t >= 6 ? 3 : (t >= 3 ? 2 : (t >= 1 ? 1 : 0));
+  J = t - I * (I + 1) / 2;
+}
+
+// Decay factors 2^{c_i - c_j} of accumulator tile (I, J): lane column i = 16 I + n, rows
+// j = 16 J + 4 g + r.  FD: the table's f carries D_j, and the diagonal tile gets it too.
+template <int L, bool FD>
+__device__ __forceinline__ void ssm_decay(const SsmTab<L>& tab, int I, int J, int g, int n, float (&o)[4]) {
+  if (I != J) {
+    const float x = tab.x[16 * I + n];
+    const float4 f = *(const float4*)&tab.f[I - 1][16 * J + 4 * g];
+    o[0] = x * f.x;
+    o[1] = x * f.y;
+    o[2] = x * f.z;
+    o[3] = x * f.w;
+  } else {
+    const float hi = tab.chi[16 * I + n], lo = tab.clo[16 * I + n];
+    const float4 h = *(const float4*)&tab.chi[16 * J + 4 * g];
+    const float4 l = *(const float4*)&tab.clo[16 * J + 4 * g];
+    float4 d = make_float4(1.0f, 1.0f, 1.0f, 1.0f);
+    if constexpr (FD) d = *(const float4*)&tab.d[16 * J + 4 * g];
+    const float hj[4] = {h.x, h.y, h.z, h.w}, lj[4] = {l.x, l.y, l.z, l.w}, dj[4] = {d.x, d.y, d.z, d.w};
+#pragma unroll
+    for (int r = 0; r < 4; ++r) o[r] = 4 * g + r <= n ? dj[r] * exp2_((hi - hj[r]) + (lo - lj[r])) : 0.0f;
+  }
+}
+
+// Four consecutive values of a bf16 plane set (NP planes, `plane` elements apart).
+template <int NP>
+__device__ __forceinline__ void lds_vals4(const uint16_t* p, int plane, float (&o)[4]) {
+  const uint2 u = *(const uint2*)p;
+  o[0] = bf16_lo_to_f32(u.x);
+  o[1] = bf16_hi_to_f32(u.x);
+  o[2] = bf16_lo_to_f32(u.y);
+  o[3] = bf16_hi_to_f32(u.y);
+#pragma unroll
+  for (int i = 1; i < NP; ++i) {
+    const uint2 w = *(const uint2*)(p + i * plane);
+    o[0] += bf16_lo_to_f32(w.x);
+    o[1] += bf16_hi_to_f32(w.x);
+    o[2] += bf16_lo_to_f32(w.y);
+    o[3] += bf16_hi_to_f32(w.y);
+  }
+}
+
+// The step size and log2 decay of lane j's step from its gate pre-activation (live: within the
+// sequence and the chunk).
+__device__ __forceinline__ void ssm_gate(bool live, float a, float alpha, float beta, float& delta, double& lg) {
+  delta = 0.0f;
+  lg = 0.0;
+  if (live) {
+    delta = softplus_exact(a + beta);
+    lg = log2_decay(alpha, delta);
+  }
+}
+
+// ------------------------------------------------------------------ forward
+
+// One workgroup per (b, query/key group, HPW heads or VB columns of one head, segment).  A wave owns
+// 16 value columns and their K x 16 part of the state, which stays in registers in the
+// accumulator layout; that layout is also the operand layout of H^T q, so the state never moves.
+// HPW > 1 (V = 16 heads sharing q and k): one wave per head, q k^T formed once for all of them.
+// Otherwise the waves of a head share its masked and decayed q k^T through LDS.
+template <bool BF16, int KP, int VB, int HPW>
+__global__ void __launch_bounds__(HPW * VB * 4) m2rnn_ssm_fwd_kernel(SsmArgs A) {
+  constexpr int L = ssm_chunk<BF16>(), NI = L / 16, NS = L / 32, KS = KP / 32, KM = KP / 16, NP = BF16 ? 1 : 3;
+  constexpr int WPH = VB / 16, NW = HPW * WPH, NTH = 64 * NW, VT = HPW * VB;
+  constexpr int STK = ssm_stride(KP), STV = ssm_stride(VT), NT = NI * (NI + 1) / 2;
+  constexpr int SETS = (NI / 2) * (NI / 2 + 1);  // (I, s) operand sets of P
+  constexpr bool SHARE_P = WPH > 1, SHARE_G = HPW > 1;
+  static_assert(!(SHARE_P && SHARE_G), "several heads per workgroup: one wave each");
+  __shared__ __attribute__((aligned(16))) uint16_t sq[NP * L * STK];
+  __shared__ __attribute__((aligned(16))) uint16_t sk[NP * L * STK];
+  __shared__ __attribute__((aligned(16))) uint16_t sv[NP * L * STV];
+  __shared__ __attribute__((aligned(16))) SsmTab<L> tab[HPW];
+  __shared__ __attribute__((aligned(16))) float4 gbuf[SHARE_G ? NT * 64 : 1];
+  __shared__ __attribute__((aligned(16))) uint2 pbuf[SHARE_P ? SETS * 3 * 2 * 64 : 1];
+
+  const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, n = lane & 15;
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  int unit, share;
+  ssm_unit(A.HB * A.CB, A.B * A.G * A.S, unit, share);
+  const int s_ = unit % A.S, bg = unit / A.S;
+  const int b = bg / A.G, grp = bg % A.G;
+  const int hpg = A.N / A.G;                              // heads per group
+  const int h0 = grp * hpg + (share / A.CB) * HPW;        // first head
+  const int hn = min(HPW, (grp + 1) * hpg - h0);          // heads here
+  const int cb = share % A.CB;
+  const int head = h0 + w / WPH;                          // this wave's head
+  const bool mine = w / WPH < hn;
+  const int c0 = cb * VB + (w % WPH) * 16;                // its first column within the head
+  const int lc = w * 16;                                  // and within the workgroup's block
+  const int K = A.K, V = A.V, T = A.T;
+  const int Tb = ssm_len(A, b);
+  const long krow = (long)A.G * K, vrow = (long)A.N * V;
+  const char* esz_base_q = (const char*)A.q + (((long)b * T * A.G + grp) * K) * (BF16 ? 2 : 4);
+  const char* esz_base_k = (const char*)A.k + (((long)b * T * A.G + grp) * K) * (BF16 ? 2 : 4);
+  const char* esz_base_v = (const char*)A.v + ((long)b * T * vrow + (long)h0 * V + cb * VB) * (BF16 ? 2 : 4);
+  const int vcols = HPW > 1 ? hn * V : VB;
+
+  // the state that enters the segment
+  f32x4 H[KM];
+  const float* Hin = A.S > 1 ? A.seg + (((long)b * A.N + head) * A.S + s_) * K * V
+                             : (A.H0 ? A.H0 + ((long)b * A.N + head) * K * V : nullptr);
+#pragma unroll
+  for (int m = 0; m < KM; ++m)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int kk = 16 * m + 4 * g + r;
+      H[m][r] = (Hin && mine && kk < K) ? Hin[(long)kk * V + c0 + n] : 0.0f;
+    }
+  float wr[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (mine) {
+#pragma unroll
+    for (int r = 0; r < 4; ++r) wr[r] = A.w_r[(long)head * V + c0 + 4 * g + r];
+  }
+  const bool preps = w % WPH == 0;
+  const float alpha = mine ? A.alpha[head] : 0.0f, beta = mine ? A.beta[head] : 0.0f;
+
+  SsmPieces<BF16, L, KP, NTH> pq, pk;
+  SsmPieces<BF16, L, VT, NTH> pv;
+  float pa = 0.0f;
+  auto fetch = [&](int ch) {
+    const int t0 = ch * L, rows = min(L, Tb - t0);
+    pq.load(esz_base_q + (long)t0 * krow * (BF16 ? 2 : 4), krow, K, rows, tid);
+    pk.load(esz_base_k + (long)t0 * krow * (BF16 ? 2 : 4), krow, K, rows, tid);
+    pv.load(esz_base_v + (long)t0 * vrow * (BF16 ? 2 : 4), vrow, vcols, rows, tid);
+    if (preps && mine && lane < rows) pa = A.a[((long)b * T + t0 + lane) * A.N + head];
+  };
+  const int ch0 = s_ * A.cps, ch1 = min(A.nch, ch0 + A.cps);
+  if (ch0 < ch1) fetch(ch0);
+  for (int ch = ch0; ch < ch1; ++ch) {
+    const int t0 = ch * L;
+    if (A.ckpt && mine) {
+      float* o = A.ckpt + (((long)b * A.N + head) * A.nch + ch) * K * V + c0 + n;
+#pragma unroll
+      for (int m = 0; m < KM; ++m)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int kk = 16 * m + 4 * g + r;
+          if (kk < K) o[(long)kk * V] = H[m][r];
+        }
+    }
+    if (t0 >= Tb) {  // past the sequence's end (the same for the whole workgroup): zeros, the state as it is
+      if (mine) {
+#pragma unroll
+        for (int I = 0; I < NI; ++I) {
+          const int t = t0 + 16 * I + n;
+          if (t < T)
+            *(float4*)(A.y + ((long)b * T + t) * vrow + (long)head * V + c0 + 4 * g) = make_float4(0, 0, 0, 0);
+        }
+      }
+      continue;
+    }
+    __syncthreads();  // the previous chunk's reads are done
+    pq.store(sq, tid);
+    pk.store(sk, tid);
+    pv.store(sv, tid);
+    if (preps) {
+      float delta;
+      double lg;
+      ssm_gate(lane < L && t0 + lane < Tb, pa, alpha, beta, delta, lg);
+      ssm_tables<L, true, true, false>(tab[w / WPH], lane, delta, lg);
+    }
+    __syncthreads();
+    if (ch + 1 < ch1) fetch(ch + 1);
+
+    const SsmTab<L>& tb = tab[w / WPH];
+    // q k^T tile (I, J): lane column i, rows j
+    auto qk_tile = [&](int I, int J) {
+      f32x4 acc = {0, 0, 0, 0};
+#pragma unroll
+      for (int s = 0; s < KS; ++s) {
+        uint4 ko[NP], qo[NP];
+#pragma unroll
+        for (int p = 0; p < NP; ++p) {
+          ko[p] = lds_row(sk + p * L * STK, STK, 16 * J, 32 * s, g, n);
+          qo[p] = lds_row(sq + p * L * STK, STK, 16 * I, 32 * s, g, n);
+        }
+        acc = mfma_planes<NP, NP>(ko, qo, acc);
+      }
+      return acc;
+    };
+    if constexpr (SHARE_P) {
+      for (int t = w; t < NT; t += NW) {
+        int I, J;
+        tri_tile(t, I, J);
+        const f32x4 acc = qk_tile(I, J);
+        float d[4], x[4];
+        ssm_decay<L, true>(tb, I, J, g, n, d);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) x[r] = acc[r] * d[r];
+        uint2 pl[3];
+        split3x4(x, pl);
+        const int set = (I / 2) * (I / 2 + 1) + (I & 1) * (I / 2 + 1) + J / 2;
+#pragma unroll
+        for (int p = 0; p < 3; ++p) pbuf[((set * 3 + p) * 2 + (J & 1)) * 64 + lane] = pl[p];
+      }
+      __syncthreads();
+    } else if constexpr (SHARE_G) {
+      for (int t = w; t < NT; t += NW) {
+        int I, J;
+        tri_tile(t, I, J);
+        const f32x4 acc = qk_tile(I, J);
+        gbuf[t * 64 + lane] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+      }
+      __syncthreads();
+    }
+
+    uint4 vop[NS][NP];
+#pragma unroll
+    for (int s = 0; s < NS; ++s)
+#pragma unroll
+      for (int p = 0; p < NP; ++p) vop[s][p] = lds_col(sv + p * L * STV, STV, 32 * s, lc, g, n);
+    uint4 hp[KS][3];
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+      uint2 x[3], y2[3];
+      const float h0v[4] = {H[2 * s][0], H[2 * s][1], H[2 * s][2], H[2 * s][3]};
+      const float h1v[4] = {H[2 * s + 1][0], H[2 * s + 1][1], H[2 * s + 1][2], H[2 * s + 1][3]};
+      split3x4(h0v, x);
+      split3x4(h1v, y2);
+#pragma unroll
+      for (int p = 0; p < 3; ++p) hp[s][p] = cat(x[p], y2[p]);
+    }
+#pragma unroll
+    for (int I = 0; I < NI; ++I) {
+      f32x4 acc = {0, 0, 0, 0};
+#pragma unroll
+      for (int s = 0; s < KS; ++s) {
+        uint4 qo[NP];
+#pragma unroll
+        for (int p = 0; p < NP; ++p) qo[p] = lds_row_acc(sq + p * L * STK, STK, 16 * I, 32 * s, g, n);
+        acc = mfma_planes<3, NP>(hp[s], qo, acc);
+      }
+      const float e = tb.e[16 * I + n];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) acc[r] *= e;
+#pragma unroll
+      for (int s = 0; s <= I / 2; ++s) {
+        uint4 po[3];
+        if constexpr (SHARE_P) {
+          const int set = (I / 2) * (I / 2 + 1) + (I & 1) * (I / 2 + 1) + s;
+#pragma unroll
+          for (int p = 0; p < 3; ++p) {
+            const uint2* pb = &pbuf[((set * 3 + p) * 2) * 64 + lane];
+            po[p] = cat(pb[0], 2 * s + 1 <= I ? pb[64] : make_uint2(0, 0));
+          }
+        } else {
+          uint2 half[2][3];
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) {
+            const int J = 2 * s + hf;
+            if (J <= I) {
+              f32x4 qk;
+              if constexpr (SHARE_G) {
+                const float4 t4 = gbuf[(I * (I + 1) / 2 + J) * 64 + lane];
+                qk = f32x4{t4.x, t4.y, t4.z, t4.w};
+              } else {
+                qk = qk_tile(I, J);
+              }
+              float d[4], x[4];
+              ssm_decay<L, true>(tb, I, J, g, n, d);
+#pragma unroll
+              for (int r = 0; r < 4; ++r) x[r] = qk[r] * d[r];
+              split3x4(x, half[hf]);
+            } else {
+#pragma unroll
+              for (int p = 0; p < 3; ++p) half[hf][p] = make_uint2(0, 0);
+            }
+          }
+#pragma unroll
+          for (int p = 0; p < 3; ++p) po[p] = cat(half[0][p], half[1][p]);
+        }
+        acc = mfma_planes<NP, 3>(vop[s], po, acc);
+      }
+      float vv[4];
+      lds_vals4<NP>(sv + (16 * I + n) * STV + lc + 4 * g, L * STV, vv);
+      const int t = t0 + 16 * I + n;
+      if (mine && t < T) {
+        const bool live = t < Tb;
+        float4 o;
+        o.x = live ? acc[0] + wr[0] * vv[0] : 0.0f;
+        o.y = live ? acc[1] + wr[1] * vv[1] : 0.0f;
+        o.z = live ? acc[2] + wr[2] * vv[2] : 0.0f;
+        o.w = live ? acc[3] + wr[3] * vv[3] : 0.0f;
+        *(float4*)(A.y + ((long)b * T + t) * vrow + (long)head * V + c0 + 4 * g) = o;
+      }
+    }
+    // the state that leaves the chunk
+    const float dl = tb.e[L - 1];
+#pragma unroll
+    for (int m = 0; m < KM; ++m)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) H[m][r] *= dl;
+#pragma unroll
+    for (int s = 0; s < NS; ++s) {
+      uint2 half[2][3];
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        const float4 w4 = *(const float4*)&tb.w[32 * s + 16 * hf + 4 * g];
+        float x[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int p = NP - 1; p >= 0; --p) {
+          const uint32_t u0 = hf ? vop[s][p].z : vop[s][p].x, u1 = hf ? vop[s][p].w : vop[s][p].y;
+          x[0] += bf16_lo_to_f32(u0);
+          x[1] += bf16_hi_to_f32(u0);
+          x[2] += bf16_lo_to_f32(u1);
+          x[3] += bf16_hi_to_f32(u1);
+        }
+        x[0] *= w4.x;
+        x[1] *= w4.y;
+        x[2] *= w4.z;
+        x[3] *= w4.w;
+        split3x4(x, half[hf]);
+      }
+      uint4 vs[3];
+#pragma unroll
+      for (int p = 0; p < 3; ++p) vs[p] = cat(half[0][p], half[1][p]);
+#pragma unroll
+      for (int m = 0; m < KM; ++m) {
+        uint4 ko[NP];
+#pragma unroll
+        for (int p = 0; p < NP; ++p) ko[p] = lds_col(sk + p * L * STK, STK, 32 * s, 16 * m, g, n);
+        H[m] = mfma_planes<NP, 3>(ko, vs, H[m]);
+      }
+    }
+  }
+  if (A.H_T && s_ == A.S - 1 && mine) {
+    float* o = A.H_T + ((long)b * A.N + head) * K * V + c0 + n;
+#pragma unroll
+    for (int m = 0; m < KM; ++m)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int kk = 16 * m + 4 * g + r;
+        if (kk < K) o[(long)kk * V] = H[m][r];
+      }
+  }
+}
+
+// ------------------------------------------------------------------ what a segment adds to the state
+
+// REV = false: seg = sum over the segment's steps of their decayed D_j k_j v_j^T, as [K,V].
+// REV = true: the gradient's state R, chunks last to first, seg = sum of the decayed q_i dy_i^T that
+// leaves the segment backwards, as [V,K]; before each chunk the part accumulated so far (what the
+// segment's later chunks send to it) goes to rloc, and its log2 decay to cdec.
+// Work split as in the forward; the weights multiply v (or dy) as it is staged.
+template <bool BF16, int KP, int VB, int HPW, bool REV>
+__global__ void __launch_bounds__(HPW * VB * 4) m2rnn_ssm_state_kernel(SsmArgs A) {
+  constexpr int L = ssm_chunk<BF16>(), NS = L / 32, KM = KP / 16, NP = BF16 ? 1 : 3;
+  constexpr int WPH = VB / 16, NW = HPW * WPH, NTH = 64 * NW, VT = HPW * VB;
+  constexpr int STK = ssm_stride(KP), STV = ssm_stride(VT);
+  constexpr bool BF16V = BF16 && !REV;
+  __shared__ __attribute__((aligned(16))) uint16_t sk[NP * L * STK];
+  __shared__ __attribute__((aligned(16))) uint16_t sv[3 * L * STV];
+  __shared__ __attribute__((aligned(16))) SsmTab<L> tab[HPW];
+  __shared__ float sdec[HPW];
+
+  const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, n = lane & 15;
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  int unit, share;
+  ssm_unit(A.HB * A.CB, A.B * A.G * A.S, unit, share);
+  const int s_ = unit % A.S, bg = unit / A.S;
+  if (!REV && s_ == A.S - 1) return;  // nothing follows the last segment
+  const int b = bg / A.G, grp = bg % A.G;
+  const int hpg = A.N / A.G;
+  const int h0 = grp * hpg + (share / A.CB) * HPW;
+  const int hn = min(HPW, (grp + 1) * hpg - h0);
+  const int cb = share % A.CB;
+  const int head = h0 + w / WPH;
+  const bool mine = w / WPH < hn;
+  const int c0 = cb * VB + (w % WPH) * 16, lc = w * 16;
+  const int K = A.K, V = A.V, T = A.T;
+  const int Tb = ssm_len(A, b);
+  const long krow = (long)A.G * K, vrow = (long)A.N * V;
+  const char* kbase = (const char*)(REV ? A.q : A.k) + (((long)b * T * A.G + grp) * K) * (BF16 ? 2 : 4);
+  const char* vbase = (const char*)(REV ? (const void*)A.dy : A.v) +
+                      ((long)b * T * vrow + (long)h0 * V + cb * VB) * (BF16V ? 2 : 4);
+  const int vcols = HPW > 1 ? hn * V : VB;
+  const bool preps = w % WPH == 0;
+  const float alpha = mine ? A.alpha[head] : 0.0f, beta = mine ? A.beta[head] : 0.0f;
+  double dec = 0.0;  // log2 decay of the chunks done (in the preparing waves)
+
+  f32x4 H[KM];
+#pragma unroll
+  for (int m = 0; m < KM; ++m) H[m] = f32x4{0, 0, 0, 0};
+  SsmPieces<BF16, L, KP, NTH> pk;
+  SsmPieces<BF16V, L, VT, NTH> pv;
+  float pa = 0.0f;
+  auto fetch = [&](int ch) {
+    const int t0 = ch * L, rows = min(L, Tb - t0);
+    pk.load(kbase + (long)t0 * krow * (BF16 ? 2 : 4), krow, K, rows, tid);
+    pv.load(vbase + (long)t0 * vrow * (BF16V ? 2 : 4), vrow, vcols, rows, tid);
+    if (preps && mine && lane < rows) pa = A.a[((long)b * T + t0 + lane) * A.N + head];
+  };
+  const int ch0 = s_ * A.cps, ch1 = min(A.nch, ch0 + A.cps);
+  const int first = REV ? ch1 - 1 : ch0, step = REV ? -1 : 1;
+  if (ch0 < ch1) fetch(first);
+  for (int c = 0; c < ch1 - ch0; ++c) {
+    const int ch = first + step * c, t0 = ch * L;
+    if constexpr (REV) {
+      if (mine) {
+        float* o = A.rloc + ((((long)b * A.N + head) * A.nch + ch) * V + c0 + n) * K;
+#pragma unroll
+        for (int m = 0; m < KM; ++m)
+          if (16 * m + 4 * g < K) *(float4*)(o + 16 * m + 4 * g) = make_float4(H[m][0], H[m][1], H[m][2], H[m][3]);
+        if (preps && lane == 0 && cb == 0) A.cdec[((long)b * A.N + head) * A.nch + ch] = (float)dec;
+      }
+    }
+    __syncthreads();
+    if (preps) {
+      float delta;
+      double lg;
+      ssm_gate(lane < L && t0 + lane < Tb, pa, alpha, beta, delta, lg);
+      const double cl = ssm_tables<L, false, false, REV>(tab[w / WPH], lane, delta, lg);
+      dec += cl;
+      if (lane == 0) sdec[w / WPH] = exp2_((float)cl);
+    }
+    pk.store(sk, tid);
+    __syncthreads();
+    pv.template store_scaled<VB>(sv, tab, tid);
+    __syncthreads();
+    if (c + 1 < ch1 - ch0) fetch(ch + step);
+    const float dl = sdec[w / WPH];
+#pragma unroll
+    for (int m = 0; m < KM; ++m)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) H[m][r] *= dl;
+#pragma unroll
+    for (int s = 0; s < NS; ++s) {
+      uint4 vs[3];
+#pragma unroll
+      for (int p = 0; p < 3; ++p) vs[p] = lds_col(sv + p * L * STV, STV, 32 * s, lc, g, n);
+#pragma unroll
+      for (int m = 0; m < KM; ++m) {
+        uint4 ko[NP];
+#pragma unroll
+        for (int p = 0; p < NP; ++p) ko[p] = lds_col(sk + p * L * STK, STK, 32 * s, 16 * m, g, n);
+        H[m] = mfma_planes<NP, 3>(ko, vs, H[m]);
+      }
+    }
+  }
+  if (mine) {
+    float* o = A.seg + (((long)b * A.N + head) * A.S + s_) * K * V;
+#pragma unroll
+    for (int m = 0; m < KM; ++m) {
+      if constexpr (REV) {
+        if (16 * m + 4 * g < K)
+          *(float4*)(o + (long)(c0 + n) * K + 16 * m + 4 * g) = make_float4(H[m][0], H[m][1], H[m][2], H[m][3]);
+      } else {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int kk = 16 * m + 4 * g + r;
+          if (kk < K) o[(long)kk * V + c0 + n] = H[m][r];
+        }
+      }
+    }
+    if (preps && lane == 0 && cb == 0) A.segdec[((long)b * A.N + head) * A.S + s_] = (float)dec;
+  }
+}
+
+// ------------------------------------------------------------------ the states that enter the segments
+
+// seg[s] <- the state that enters segment s, from the segments' own parts: forwards from H0 (first to
+// last), in the reverse scan from dH_T (last to first, [V,K]), which also leaves dH0.  One thread
+// per element of a pair's state; the segments are few and their reads independent of the carry.
+template <bool REV>
+__global__ void __launch_bounds__(256) m2rnn_ssm_combine_kernel(SsmArgs A) {
+  const long KV = (long)A.K * A.V;
+  const unsigned per = (unsigned)((KV + 255) / 256);
+  const long e = (long)(blockIdx.x % per) * 256 + threadIdx.x;
+  const long pair = blockIdx.x / per;
+  if (e >= KV) return;
+  // the element's place in a [K,V] state
+  const long at = REV ? (e % A.K) * A.V + e / A.K : e;
+  const float* first = REV ? A.dH_T : A.H0;
+  float carry = first ? first[pair * KV + at] : 0.0f;
+  float* p = A.seg + pair * A.S * KV + e;
+  const float* d = A.segdec + pair * A.S;
+  for (int i = 0; i < A.S; ++i) {
+    const int s = REV ? A.S - 1 - i : i;
+    const float own = p[s * KV];
+    p[s * KV] = carry;
+    carry = __builtin_fmaf(exp2_(d[s]), carry, own);
+  }
+  if (REV && A.dH0) A.dH0[pair * KV + at] = carry;
+}
+
+// ------------------------------------------------------------------ backward
+
+constexpr int kSsmBwdWaves = 8;
+
+// Eight values p[0], p[st], .. as the three planes of an MFMA operand.
+__device__ __forceinline__ void split3x8(const float (&x)[8], uint4 (&o)[3]) {
+  const float a[4] = {x[0], x[1], x[2], x[3]}, b[4] = {x[4], x[5], x[6], x[7]};
+  uint2 pa[3], pb[3];
+  split3x4(a, pa);
+  split3x4(b, pb);
+#pragma unroll
+  for (int p = 0; p < 3; ++p) o[p] = cat(pa[p], pb[p]);
+}
+
+// All gradients of one chunk of one query/key group (or of a part of its heads).  With u = dy,
+// H the state that enters the chunk, R the gradient of the state that leaves it, and
+//     P_ij = 2^{c_i - c_j} D_j (q_i . k_j),   X_ij = 2^{c_i - c_j} D_j (u_i . v_j)   (j <= i):
+//     dv_j = sum_i P_ij u_i + D_j 2^{c_L - c_j} R^T k_j + w_r (.) u_j
+//     dq_i = sum_j X_ij k_j + 2^{c_i} H u_i
+//     dk_j = sum_i X_ij q_i + D_j 2^{c_L - c_j} R v_j
+// and for the decays, with M_ij = 2^{c_i - c_j} (q_i . k_j)(u_i . v_j),
+//     g_t = <R_t, f_t H_{t-1}> = sum_{i >= t > j} D_j M_ij + sum_{i >= t} q_i . 2^{c_i} H u_i
+//           + sum_{j < t} D_j k_j . 2^{c_L - c_j} R v_j + 2^{c_L} <R, H>
+//     dD_t = sum_{i >= t} M_it + k_t . 2^{c_L - c_t} R v_t - alpha g_t.
+// The double sum telescopes (row sums less column sums of the strict triangle); both are taken of
+// the same M_ij and added in fp64, so what cancels cancels exactly and a decay that forgets at once
+// leaves no residue of the terms on the diagonal.
+//
+// Every chunk has its own workgroup (no chain), which walks its heads one after the other, adding
+// dq and dk in registers; heads of 128 value columns go as two blocks of 64, since all gradients are
+// sums over value columns.  Per head three barriers: stage; tiles of X, P and M; the products.
+template <bool BF16, int KP, int VB>
+__global__ void __launch_bounds__(64 * kSsmBwdWaves) m2rnn_ssm_bwd_kernel(SsmArgs A) {
+  constexpr int L = ssm_chunk<BF16>(), NI = L / 16, NS = L / 32, KS = KP / 32, KM = KP / 16, NP = BF16 ? 1 : 3;
+  constexpr int NW = kSsmBwdWaves, NTH = 64 * NW;
+  constexpr int VP = VB < 32 ? 32 : VB, VS = VP / 32, VM = VB / 16;  // columns in LDS, contraction steps, tiles
+  constexpr int STK = ssm_stride(KP), STV = ssm_stride(VP), STP = ssm_stride(L);
+  constexpr int NT = NI * (NI + 1) / 2, TPT = (NT + NW - 1) / NW;    // lower tiles; per wave
+  constexpr int TPQ = KM * NI >= NW ? KM * NI / NW : 1;              // dq (dk) tiles per wave, one K tile
+  constexpr int TPV = VM * NI >= NW ? VM * NI / NW : 1;              // dv tiles per wave, one V tile
+  __shared__ __attribute__((aligned(16))) uint16_t sq[NP * L * STK];
+  __shared__ __attribute__((aligned(16))) uint16_t sk[NP * L * STK];
+  __shared__ __attribute__((aligned(16))) uint16_t sv[NP * L * STV];
+  __shared__ __attribute__((aligned(16))) uint16_t su[3 * L * STV];
+  __shared__ __attribute__((aligned(16))) uint16_t sx[3 * L * STP];  // X, then the same of P
+  __shared__ __attribute__((aligned(16))) uint16_t sp[3 * L * STP];
+  __shared__ __attribute__((aligned(16))) SsmTab<L> tab;
+  __shared__ double rowp[NI][L], colp[NI][L], ap[KM][L], bp[KM][L], rh[KM];
+  __shared__ float dgp[L], dwp[NI][VB];
+
+  const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, n = lane & 15;
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  int unit, hs;
+  ssm_unit(A.HS, A.B * A.G * A.nch, unit, hs);
+  const int ch = unit % A.nch, bg = unit / A.nch;
+  const int b = bg / A.G, grp = bg % A.G;
+  const int K = A.K, V = A.V, T = A.T, N = A.N;
+  const int hpg = N / A.G, per = (hpg + A.HS - 1) / A.HS;
+  const int hb = grp * hpg + hs * per, he = min(grp * hpg + hpg, hb + per);
+  const int CB = A.CB, blocks = (he > hb ? he - hb : 0) * CB;
+  const int t0 = ch * L;
+  const int Tb = ssm_len(A, b);
+  const int rows = min(L, Tb - t0);
+  const long krow = (long)A.G * K, vrow = (long)N * V, row0 = (long)b * T + t0;
+
+  // this wave's tiles
+  const int mq = (w * TPQ) / NI, iq0 = (w * TPQ) % NI;
+  const bool hasq = w * TPQ < KM * NI;
+  const int mv = (w * TPV) / NI, jv0 = (w * TPV) % NI;
+  const bool hasv = w * TPV < VM * NI;
+
+  SsmPieces<BF16, L, VP, NTH> pv;
+  SsmPieces<false, L, VP, NTH> pu;
+  float pa = 0.0f;
+  auto fetch = [&](int blk) {
+    const int h = hb + blk / CB;
+    const long off = row0 * vrow + (long)h * V + (blk % CB) * VB;
+    pv.load(BF16 ? (const void*)((const uint16_t*)A.v + off) : (const void*)((const float*)A.v + off), vrow, VB, rows,
+            tid);
+    pu.load(A.dy + off, vrow, VB, rows, tid);
+    if (w == 0 && lane < rows) pa = A.a[(row0 + lane) * N + h];
+  };
+  if (blocks > 0) fetch(0);
+  {
+    SsmPieces<BF16, L, KP, NTH> pq, pk;
+    const long off = row0 * krow + (long)grp * K;
+    pq.load(BF16 ? (const void*)((const uint16_t*)A.q + off) : (const void*)((const float*)A.q + off), krow, K, rows,
+            tid);
+    pk.load(BF16 ? (const void*)((const uint16_t*)A.k + off) : (const void*)((const float*)A.k + off), krow, K, rows,
+            tid);
+    pq.store(sq, tid);
+    pk.store(sk, tid);
+  }
+  // X and P: the tiles right of the diagonal that a 32-wide contraction covers stay zero
+  for (int i = tid; i < 3 * L * STP / 2; i += NTH) {
+    ((uint32_t*)sx)[i] = 0;
+    ((uint32_t*)sp)[i] = 0;
+  }
+  __syncthreads();
+  // q k^T of this wave's lower tiles: the same for all heads
+  f32x4 qk[TPT];
+#pragma unroll
+  for (int p = 0; p < TPT; ++p) {
+    qk[p] = f32x4{0, 0, 0, 0};
+    const int t = w + NW * p;
+    if (t < NT) {
+      int I, J;
+      tri_tile(t, I, J);
+#pragma unroll
+      for (int s = 0; s < KS; ++s) {
+        uint4 ko[NP], qo[NP];
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+          ko[i] = lds_row(sk + i * L * STK, STK, 16 * J, 32 * s, g, n);
+          qo[i] = lds_row(sq + i * L * STK, STK, 16 * I, 32 * s, g, n);
+        }
+        qk[p] = mfma_planes<NP, NP>(ko, qo, qk[p]);
+      }
+    }
+  }
+  f32x4 dq[TPQ], dk[TPQ];
+#pragma unroll
+  for (int p = 0; p < TPQ; ++p) dq[p] = dk[p] = f32x4{0, 0, 0, 0};
+  // wave 0, lane t: what g and dD hold of the head's column blocks done so far
+  double gsum = 0.0, dsum = 0.0, delta64 = 0.0;
+
+  for (int blk = 0; blk < blocks; ++blk) {
+    const int head = hb + blk / CB, cb = blk % CB;
+    const long pair = (long)b * N + head;
+    __syncthreads();  // the previous block's reads are done
+    pv.store(sv, tid);
+    pu.store(su, tid);
+    if (w == 0 && cb == 0) {
+      float delta;
+      double lg;
+      ssm_gate(lane < L && t0 + lane < Tb, pa, A.alpha[head], A.beta[head], delta, lg);
+      ssm_tables<L, true, false, false>(tab, lane, delta, lg);
+      delta64 = delta;
+    }
+    const float pa_now = pa;
+    __syncthreads();
+    if (blk + 1 < blocks) fetch(blk + 1);
+
+    // X, P and M of the lower tiles
+#pragma unroll
+    for (int p = 0; p < TPT; ++p) {
+      const int t = w + NW * p;
+      if (t < NT) {
+        int I, J;
+        tri_tile(t, I, J);
+        f32x4 uv = {0, 0, 0, 0};
+#pragma unroll
+        for (int s = 0; s < VS; ++s) {
+          uint4 vo[NP], uo[3];
+#pragma unroll
+          for (int i = 0; i < NP; ++i) vo[i] = lds_row(sv + i * L * STV, STV, 16 * J, 32 * s, g, n);
+#pragma unroll
+          for (int i = 0; i < 3; ++i) uo[i] = lds_row(su + i * L * STV, STV, 16 * I, 32 * s, g, n);
+          uv = mfma_planes<NP, 3>(vo, uo, uv);
+        }
+        float d[4];
+        ssm_decay<L, false>(tab, I, J, g, n, d);
+        const float4 dj = *(const float4*)&tab.d[16 * J + 4 * g];
+        const float dl[4] = {dj.x, dj.y, dj.z, dj.w};
+        float xx[4], pp[4];
+        double mm[4], row = 0.0;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const float x0 = uv[r] * d[r];
+          const float m = x0 * qk[p][r];
+          mm[r] = m;
+          xx[r] = x0 * dl[r];
+          pp[r] = qk[p][r] * (d[r] * dl[r]);
+          const bool diag = I == J && 4 * g + r == n;
+          if (diag) dgp[16 * I + n] = m;
+          row += diag ? 0.0 : mm[r] * (double)dl[r];
+        }
+        uint2 px[3], pq2[3];
+        split3x4(xx, px);
+        split3x4(pp, pq2);
+        uint16_t* ox = sx + (16 * I + n) * STP + 16 * J + 4 * g;
+        uint16_t* op = sp + (16 * I + n) * STP + 16 * J + 4 * g;
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+          *(uint2*)(ox + i * L * STP) = px[i];
+          *(uint2*)(op + i * L * STP) = pq2[i];
+        }
+        row = group_sum64(row);
+        if (g == 0) rowp[J][16 * I + n] = row;
+        const double col = row16_sum4_64(mm, lane);
+        if ((n & 3) == 0) colp[I][16 * J + 4 * g + (n >> 2)] = col;
+      }
+    }
+    __syncthreads();
+
+    const float* Hp = A.ckpt + (pair * A.nch + ch) * K * V + cb * VB;          // [K][V]
+    const float* Rp = A.rloc + ((pair * A.nch + ch) * V + cb * VB) * K;        // [V][K]
+    const float* Ip = A.seg + ((pair * A.S + ch / A.cps) * V + cb * VB) * K;   // [V][K]
+    const float idec = exp2_(A.cdec[pair * A.nch + ch]);
+    if (hasv) {
+      // dv^T: rows c of tile mv, columns j
+      uint4 Ro[KS][3];
+#pragma unroll
+      for (int s = 0; s < KS; ++s) {
+        float x[8];
+        const int kk = 32 * s + 8 * g;
+        const long at = (long)(16 * mv + n) * K + kk;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float4 a4 = make_float4(0, 0, 0, 0), i4 = a4;
+          if (kk + 4 * h < K) {
+            a4 = *(const float4*)(Rp + at + 4 * h);
+            i4 = *(const float4*)(Ip + at + 4 * h);
+          }
+          x[4 * h + 0] = __builtin_fmaf(idec, i4.x, a4.x);
+          x[4 * h + 1] = __builtin_fmaf(idec, i4.y, a4.y);
+          x[4 * h + 2] = __builtin_fmaf(idec, i4.z, a4.z);
+          x[4 * h + 3] = __builtin_fmaf(idec, i4.w, a4.w);
+        }
+        split3x8(x, Ro[s]);
+      }
+      uint4 uo[NS][3];
+#pragma unroll
+      for (int s = 0; s < NS; ++s)
+#pragma unroll
+        for (int i = 0; i < 3; ++i) uo[s][i] = lds_col(su + i * L * STV, STV, 32 * s, 16 * mv, g, n);
+      float wr[4];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) wr[r] = A.w_r[(long)head * V + cb * VB + 16 * mv + 4 * g + r];
+#pragma unroll
+      for (int p = 0; p < TPV; ++p) {
+        const int J = jv0 + p;
+        f32x4 acc = {0, 0, 0, 0};
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+          uint4 ko[NP];
+#pragma unroll
+          for (int i = 0; i < NP; ++i) ko[i] = lds_row(sk + i * L * STK, STK, 16 * J, 32 * s, g, n);
+          acc = mfma_planes<3, NP>(Ro[s], ko, acc);
+        }
+        const float wj = tab.w[16 * J + n];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) acc[r] *= wj;
+#pragma unroll
+        for (int s = 0; s < NS; ++s) {
+          if (s < J / 2) continue;
+          uint4 po[3];
+#pragma unroll
+          for (int i = 0; i < 3; ++i) po[i] = lds_col(sp + i * L * STP, STP, 32 * s, 16 * J, g, n);
+          acc = mfma_planes<3, 3>(uo[s], po, acc);
+        }
+        float uj[4], vj[4];
+        lds_vals4<3>(su + (16 * J + n) * STV + 16 * mv + 4 * g, L * STV, uj);
+        lds_vals4<NP>(sv + (16 * J + n) * STV + 16 * mv + 4 * g, L * STV, vj);
+        const int t = t0 + 16 * J + n;
+        if (t < T)
+          *(float4*)(A.dv + ((long)b * T + t) * vrow + (long)head * V + cb * VB + 16 * mv + 4 * g) =
+              make_float4(acc[0] + wr[0] * uj[0], acc[1] + wr[1] * uj[1], acc[2] + wr[2] * uj[2],
+                          acc[3] + wr[3] * uj[3]);
+        const float sum = row16_sum4(uj[0] * vj[0], uj[1] * vj[1], uj[2] * vj[2], uj[3] * vj[3], lane);
+        if ((n & 3) == 0) dwp[J][16 * mv + 4 * g + (n >> 2)] = sum;
+      }
+    }
+    if (hasq) {
+      // dq^T and dk^T: rows kk of tile mq, columns i (j)
+      uint4 Ho[VS][3], Ro[VS][3];
+      double dot = 0.0;  // <R, H>: every step of the chunk gets it, so its error would add up in dalpha and dbeta
+      const int kk = 16 * mq + n;
+#pragma unroll
+      for (int s = 0; s < VS; ++s) {
+        float x[8], y[8];
+        const int c = 32 * s + 8 * g;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = y[e] = 0.0f;
+        if (kk < K && c < VB) {
+          const float4 a4 = *(const float4*)(Hp + (long)kk * V + c), b4 = *(const float4*)(Hp + (long)kk * V + c + 4);
+          x[0] = a4.x; x[1] = a4.y; x[2] = a4.z; x[3] = a4.w;
+          x[4] = b4.x; x[5] = b4.y; x[6] = b4.z; x[7] = b4.w;
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            y[e] = __builtin_fmaf(idec, Ip[(long)(c + e) * K + kk], Rp[(long)(c + e) * K + kk]);
+        }
+        if (iq0 == 0) {  // one wave per K tile
+#pragma unroll
+          for (int e = 0; e < 8; ++e) dot = __builtin_fma((double)x[e], (double)y[e], dot);
+        }
+        split3x8(x, Ho[s]);
+        split3x8(y, Ro[s]);
+      }
+      if (iq0 == 0) {
+        dot = prefix64(dot);
+        if (lane == 63) rh[mq] = dot;
+      }
+      uint4 kc[NS][NP], qc[NS][NP];
+#pragma unroll
+      for (int s = 0; s < NS; ++s)
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+          kc[s][i] = lds_col(sk + i * L * STK, STK, 32 * s, 16 * mq, g, n);
+          qc[s][i] = lds_col(sq + i * L * STK, STK, 32 * s, 16 * mq, g, n);
+        }
+#pragma unroll
+      for (int p = 0; p < TPQ; ++p) {
+        const int I = iq0 + p;
+        f32x4 acc = {0, 0, 0, 0};
+#pragma unroll
+        for (int s = 0; s < VS; ++s) {
+          uint4 uo[3];
+#pragma unroll
+          for (int i = 0; i < 3; ++i) uo[i] = lds_row(su + i * L * STV, STV, 16 * I, 32 * s, g, n);
+          acc = mfma_planes<3, 3>(Ho[s], uo, acc);
+        }
+        const float e = tab.e[16 * I + n];
+        float qv[4];
+        double dot_a = 0.0;
+        lds_vals4<NP>(sq + (16 * I + n) * STK + 16 * mq + 4 * g, L * STK, qv);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          acc[r] *= e;
+          dot_a = __builtin_fma((double)qv[r], (double)acc[r], dot_a);
+          dq[p][r] += acc[r];
+        }
+        dot_a = group_sum64(dot_a);
+        if (g == 0) ap[mq][16 * I + n] = dot_a;
+#pragma unroll
+        for (int s = 0; s < NS; ++s) {
+          if (s > I / 2) continue;
+          uint4 xo[3];
+#pragma unroll
+          for (int i = 0; i < 3; ++i) xo[i] = lds_row_acc(sx + i * L * STP, STP, 16 * I, 32 * s, g, n);
+          dq[p] = mfma_planes<NP, 3>(kc[s], xo, dq[p]);
+        }
+        // dk, the same tile of steps
+        f32x4 bcc = {0, 0, 0, 0};
+#pragma unroll
+        for (int s = 0; s < VS; ++s) {
+          uint4 vo[NP];
+#pragma unroll
+          for (int i = 0; i < NP; ++i) vo[i] = lds_row(sv + i * L * STV, STV, 16 * I, 32 * s, g, n);
+          bcc = mfma_planes<3, NP>(Ro[s], vo, bcc);
+        }
+        // without D_j: its factor w / D_j is 2^{c_L - c_j}
+        const float dj = tab.d[16 * I + n];
+        const float hi = tab.chi[L - 1] - tab.chi[16 * I + n], lo = tab.clo[L - 1] - tab.clo[16 * I + n];
+        const float ej = exp2_(hi + lo);
+        float kv[4];
+        double dot_b = 0.0;
+        lds_vals4<NP>(sk + (16 * I + n) * STK + 16 * mq + 4 * g, L * STK, kv);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          bcc[r] *= ej;
+          dot_b = __builtin_fma((double)kv[r], (double)bcc[r], dot_b);
+          dk[p][r] = __builtin_fmaf(dj, bcc[r], dk[p][r]);
+        }
+        dot_b = group_sum64(dot_b);
+        if (g == 0) bp[mq][16 * I + n] = dot_b;
+#pragma unroll
+        for (int s = 0; s < NS; ++s) {
+          if (s < I / 2) continue;
+          uint4 xo[3];
+#pragma unroll
+          for (int i = 0; i < 3; ++i) xo[i] = lds_col(sx + i * L * STP, STP, 32 * s, 16 * I, g, n);
+          dk[p] = mfma_planes<NP, 3>(qc[s], xo, dk[p]);
+        }
+      }
+    }
+    __syncthreads();
+
+    if (w == 0) {
+      const int t = lane;
+      double row = 0.0, col = 0.0, diag = 0.0, aa = 0.0, bb = 0.0, through = 0.0;
+      if (t < L) {
+        const int It = t / 16;
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+          row += i <= It ? rowp[i][t] : 0.0;
+          col += i >= It ? colp[i][t] : 0.0;
+        }
+        diag = dgp[t];
+#pragma unroll
+        for (int m = 0; m < KM; ++m) {
+          aa += ap[m][t];
+          bb += bp[m][t];
+        }
+      }
+#pragma unroll
+      for (int m = 0; m < KM; ++m) through += rh[m];
+      through *= exp2((double)tab.chi[L - 1] + (double)tab.clo[L - 1]);
+      const double x = row - delta64 * (col - diag) + aa, y = delta64 * bb;
+      // sum over i >= t of x, sum over j < t of y, each without a subtraction that would leave a residue
+      const double sx64 = __shfl(prefix64(__shfl(x, 63 - lane)), 63 - lane);
+      gsum += sx64 + prefix64(dpp64<0x138, 0xF>(y)) + through;
+      dsum += col + bb;
+      if (cb == CB - 1) {
+        const double al = A.alpha[head];
+        const bool live = t < L && t0 + t < Tb;
+        const float z = pa_now + A.beta[head];
+        const float da = live ? (float)(dsum - al * gsum) / (1.0f + expf(-z)) : 0.0f;
+        if (t < L && t0 + t < T) A.da[(row0 + t) * N + head] = da;
+        const double sb = prefix64(da), sa = prefix64(live ? -delta64 * gsum : 0.0);
+        if (lane == 63) {
+          float* o = A.part_gate + ((long)b * A.nch + ch) * 2 * N;
+          o[head] = (float)sb;
+          o[N + head] = (float)sa;
+        }
+        gsum = dsum = 0.0;
+      }
+    } else if (w == 1 && lane < VB) {
+      float sum = 0.0f;
+#pragma unroll
+      for (int i = 0; i < NI; ++i) sum += dwp[i][lane];
+      A.part_wr[((long)b * A.nch + ch) * vrow + (long)head * V + cb * VB + lane] = sum;
+    }
+  }
+  if (hasq) {
+    const long plane = (long)hs * A.B * T * krow;
+#pragma unroll
+    for (int p = 0; p < TPQ; ++p) {
+      const int t = t0 + 16 * (iq0 + p) + n, kk = 16 * mq + 4 * g;
+      if (t < T && kk < K) {
+        const long at = plane + ((long)b * T + t) * krow + (long)grp * K + kk;
+        *(float4*)(A.dq + at) = make_float4(dq[p][0], dq[p][1], dq[p][2], dq[p][3]);
+        *(float4*)(A.dk + at) = make_float4(dk[p][0], dk[p][1], dk[p][2], dk[p][3]);
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------------ one token
+
+// One step for every (b, n), the state in HBM: reads it, advances it and writes it back, in place or
+// not (a thread reads its own elements before it writes them).  One workgroup per pair and VC of its
+// V columns; a thread owns four columns of every (256 / (VC / 4))-th row, so a wave's accesses are
+// whole rows of the block, and the readout's sum over rows ends in LDS.
+template <bool BF16, int VC>
+__global__ void __launch_bounds__(256) m2rnn_ssm_step_kernel(const void* q, const void* k, const void* v,
+                                                             const float* a, const float* alpha, const float* beta,
+                                                             const float* w_r, const float* H_in, float* H_out,
+                                                             float* y, int N, int G, int K, int V) {
+  constexpr int VQ = VC / 4, RP = 256 / VQ;  // column groups; rows per pass
+  __shared__ __attribute__((aligned(16))) float red[4][VC];
+  const int tid = threadIdx.x, w = tid >> 6;
+  const int CB = V / VC;
+  const long pair = blockIdx.x / CB;
+  const int cb = blockIdx.x % CB;
+  const int head = (int)(pair % N);
+  const long qk = (pair / N * G + head / (N / G)) * K;
+  const int c = cb * VC + (tid % VQ) * 4;
+  const int r0 = tid / VQ;
+  float delta;
+  double lg;
+  ssm_gate(true, a[pair], alpha[head], beta[head], delta, lg);
+  const float f = exp2_((float)lg);
+  auto val = [](const void* p, long i) {
+    if constexpr (BF16) return bf16_lo_to_f32(((const uint16_t*)p)[i]);
+    return ((const float*)p)[i];
+  };
+  float4 vv;
+  if constexpr (BF16) {
+    const uint2 u = *(const uint2*)((const uint16_t*)v + pair * V + c);
+    vv = make_float4(bf16_lo_to_f32(u.x), bf16_hi_to_f32(u.x), bf16_lo_to_f32(u.y), bf16_hi_to_f32(u.y));
+  } else {
+    vv = *(const float4*)((const float*)v + pair * V + c);
+  }
+  const float4 dv = make_float4(delta * vv.x, delta * vv.y, delta * vv.z, delta * vv.w);
+  const float* hi = H_in ? H_in + pair * K * V + c : nullptr;
+  float* ho = H_out + pair * K * V + c;
+  float4 acc = make_float4(0, 0, 0, 0);
+#pragma unroll 4
+  for (int r = r0; r < K; r += RP) {
+    float4 h = hi ? *(const float4*)(hi + (long)r * V) : make_float4(0, 0, 0, 0);
+    const float kr = val(k, qk + r), qr = val(q, qk + r);
+    h.x = __builtin_fmaf(kr, dv.x, f * h.x);
+    h.y = __builtin_fmaf(kr, dv.y, f * h.y);
+    h.z = __builtin_fmaf(kr, dv.z, f * h.z);
+    h.w = __builtin_fmaf(kr, dv.w, f * h.w);
+    *(float4*)(ho + (long)r * V) = h;
+    acc.x = __builtin_fmaf(qr, h.x, acc.x);
+    acc.y = __builtin_fmaf(qr, h.y, acc.y);
+    acc.z = __builtin_fmaf(qr, h.z, acc.z);
+    acc.w = __builtin_fmaf(qr, h.w, acc.w);
+  }
+#pragma unroll
+  for (int o = VQ; o < 64; o <<= 1) {
+    acc.x += __shfl_xor(acc.x, o);
+    acc.y += __shfl_xor(acc.y, o);
+    acc.z += __shfl_xor(acc.z, o);
+    acc.w += __shfl_xor(acc.w, o);
+  }
+  if ((tid & 63) < VQ) *(float4*)&red[w][(tid & 63) * 4] = acc;
+  __syncthreads();
+  if (tid < VC) {
+    const int col = cb * VC + tid;
+    y[pair * V + col] =
+        ((red[0][tid] + red[1][tid]) + (red[2][tid] + red[3][tid])) + w_r[(long)head * V + col] * val(v, pair * V + col);
+  }
+}
+
+}  // namespace m2rnn
