@@ -440,6 +440,75 @@ int m2rnn_ssm_step(const m2rnn_dims* dims, int qkv_dtype, const void* q, const v
                    const float* a, const float* alpha, const float* beta, const float* w_r,
                    const float* H_in, float* H_out, float* y, void* stream);
 
+/*
+ * The causal conv4 + SiLU for prompts and single tokens: m2rnn_conv4_silu_fwd with the three inputs
+ * before the first step, and the three that the next call needs.
+ *   win        [B,3,C] in `dtype`, oldest first: x_{-3}, x_{-2}, x_{-1}; NULL: zeros.
+ *   win_out    [B,3,C]: the last three inputs of each sequence (of win and x together).
+ *   lens       [B] int32 or NULL, as in m2rnn_ssm_fwd: x at or past a sequence's end is not read, its u is
+ *              zeros.
+ * In m2rnn_conv4_silu_fwd_state win and win_out must not overlap (M2RNN_EINVAL); T = 0 copies the
+ * window.  m2rnn_conv4_silu_step takes x, u [B,C], and win_out may be win (any other overlap:
+ * M2RNN_EINVAL).  x, u, win and win_out are aligned to four elements (8 bytes in bf16), w and bias to 16.
+ */
+int m2rnn_conv4_silu_fwd_state(int64_t B, int64_t T, int64_t C, int dtype, const void* x, const float* w,
+                               const float* bias, const int32_t* lens, const void* win, void* u,
+                               void* win_out, void* stream);
+int m2rnn_conv4_silu_step(int64_t B, int64_t C, int dtype, const void* x, const float* w, const float* bias,
+                          const void* win, void* u, void* win_out, void* stream);
+
+/*
+ * Norm of queries and keys per head, with the position rotation in the same pass (between the conv
+ * and a scan or an attention):
+ *     xn = gamma (.) x / sqrt(mean_j x_j^2 + eps) over the K features of each head, then the pairs
+ *     p < R/2 of features (p, p + R/2), or (2p, 2p + 1) if `interleaved`, turned by pos * inv_freq[p]:
+ *     (a, b) -> (a cos - b sin, b cos + a sin).  The last K - R features are not turned (R = 0: norm only).
+ *   q [B,T,Nq,K], k [B,T,Nk,K] and q_out, k_out alike in `dtype` (fp32 or bf16); gamma_q, gamma_k
+ *   [K] fp32; pos [B,T] int32 (any value, also negative); inv_freq [R/2] fp64, in radians per position.
+ *   K a multiple of 16 up to 256, R a multiple of 8 up to K; Nq or Nk may be 0 (their pointers NULL).
+ *   Angles are formed in fp64, so far positions keep their angle.  Pointers 16-byte aligned (pos 4).
+ * The backward takes the gradients of the outputs (fp32) and gives dq, dk (fp32) and dgamma_q, dgamma_k
+ * [K], summed over batch, time and heads in a fixed order.
+ */
+int m2rnn_qk_norm_rope_fwd(int64_t B, int64_t T, int64_t Nq, int64_t Nk, int64_t K, int64_t R,
+                           int interleaved, int dtype, const void* q, const void* k, const float* gamma_q,
+                           const float* gamma_k, const int32_t* pos, const double* inv_freq, float eps,
+                           void* q_out, void* k_out, void* stream);
+int m2rnn_qk_norm_rope_bwd_workspace_size(int64_t B, int64_t T, int64_t Nq, int64_t Nk, int64_t K,
+                                          size_t* bytes);
+int m2rnn_qk_norm_rope_bwd(int64_t B, int64_t T, int64_t Nq, int64_t Nk, int64_t K, int64_t R,
+                           int interleaved, int dtype, const void* q, const void* k, const float* gamma_q,
+                           const float* gamma_k, const int32_t* pos, const double* inv_freq, float eps,
+                           const float* dq_out, const float* dk_out, float* dq, float* dk, float* dgamma_q,
+                           float* dgamma_k, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Global gradient norm and clipping over many tensors (a training step clips at a norm of 1).
+ *     norm = sqrt(sum over all elements of all tensors of g^2)
+ *     g <- g max_norm / norm where norm > max_norm, else unchanged
+ * The list is a host array, read during the call only (a captured graph keeps its own copy).  A tensor
+ * has any number of elements (also none), contiguous, aligned to its element, in fp32 or bf16.
+ * Squares are summed in fp64 in a fixed order.
+ *   norm       device fp32 scalar: m2rnn_grad_norm writes it, m2rnn_grad_clip reads it (in between a
+ *              caller may combine the norms of several ranks).  No tensors: 0.
+ *   out        NULL: in place.  Otherwise a host array of `count` device pointers (NULL entries: in place)
+ *              of the tensors' own types and sizes.  An output that overlaps another output, another
+ *              tensor, or a part of its own tensor is rejected (M2RNN_EINVAL).
+ *   max_norm   >= 0 (negative or NaN: M2RNN_EINVAL).
+ * A norm that is not finite leaves the gradients unchanged (out of place: copied): the caller finds it
+ * in `norm` and skips the step.
+ */
+typedef struct m2rnn_tensor {
+  void* data;    /* device pointer */
+  int64_t numel; /* elements */
+  int64_t dtype; /* M2RNN_DTYPE_F32 or M2RNN_DTYPE_BF16 */
+} m2rnn_tensor;
+int m2rnn_grad_norm_workspace_size(const m2rnn_tensor* grads, int64_t count, size_t* bytes);
+int m2rnn_grad_norm(const m2rnn_tensor* grads, int64_t count, float* norm, void* workspace,
+                    size_t workspace_bytes, void* stream);
+int m2rnn_grad_clip(const m2rnn_tensor* grads, int64_t count, void* const* out, const float* norm,
+                    float max_norm, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

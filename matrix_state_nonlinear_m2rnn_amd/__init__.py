@@ -40,6 +40,9 @@ EXPORTED = (
     "m2rnn_fwd_noalloc", "m2rnn_fwd_noalloc_max_bytes", "m2rnn_scan_bwd", "m2rnn_scan_bwd_finish",
     "m2rnn_ssm_checkpoint_interval", "m2rnn_ssm_fwd_workspace_size", "m2rnn_ssm_fwd", "m2rnn_ssm_fwd_ckpt",
     "m2rnn_ssm_bwd_workspace_size", "m2rnn_ssm_bwd", "m2rnn_ssm_step",
+    "m2rnn_conv4_silu_fwd_state", "m2rnn_conv4_silu_step", "m2rnn_qk_norm_rope_fwd",
+    "m2rnn_qk_norm_rope_bwd_workspace_size", "m2rnn_qk_norm_rope_bwd", "m2rnn_grad_norm_workspace_size",
+    "m2rnn_grad_norm", "m2rnn_grad_clip",
 )
 
 
@@ -142,6 +145,14 @@ def lib() -> ctypes.CDLL:
             ("m2rnn_ssm_bwd_workspace_size", [dp, ci, ctypes.POINTER(sz)]),
             ("m2rnn_ssm_bwd", [dp, ci] + [vp] * 19 + [vp, sz, vp]),
             ("m2rnn_ssm_step", [dp, ci] + [vp] * 10 + [vp]),
+            ("m2rnn_conv4_silu_fwd_state", [i64] * 3 + [ci] + [vp] * 7 + [vp]),
+            ("m2rnn_conv4_silu_step", [i64] * 2 + [ci] + [vp] * 6 + [vp]),
+            ("m2rnn_qk_norm_rope_fwd", [i64] * 6 + [ci, ci] + [vp] * 6 + [cf, vp, vp, vp]),
+            ("m2rnn_qk_norm_rope_bwd_workspace_size", [i64] * 5 + [ctypes.POINTER(sz)]),
+            ("m2rnn_qk_norm_rope_bwd", [i64] * 6 + [ci, ci] + [vp] * 6 + [cf] + [vp] * 6 + [vp, sz, vp]),
+            ("m2rnn_grad_norm_workspace_size", [vp, i64, ctypes.POINTER(sz)]),
+            ("m2rnn_grad_norm", [vp, i64, vp, vp, sz, vp]),
+            ("m2rnn_grad_clip", [vp, i64, vp, vp, cf, vp]),
         ):
             fn = getattr(L, name)
             fn.restype = ci
@@ -820,3 +831,207 @@ def m2rnn_ssm_step(q, k, v, a, alpha, beta, w_r, H=None, *, H_out=None, y=None, 
             ctypes.byref(dims), dt, _ptr(q), _ptr(k), _ptr(v), _ptr(a), _ptr(alpha), _ptr(beta), _ptr(w_r), _ptr(H),
             _ptr(H_out), _ptr(y), _stream(stream)))
     return y, H_out
+
+
+# ---------------------------------------------------------------- the convolution's window
+
+def m2rnn_conv4_silu_fwd_state(x, w, bias=None, win=None, *, lens=None, u=None, win_out=None,
+                               stream=None) -> Tuple[object, object]:
+    """Causal conv4 + SiLU of a prompt that continues: x [B,T,C] fp32/bf16, w [C,4], bias [C] or None,
+    win [B,3,C] (the three inputs before x, oldest first, in x's dtype) or None (zeros), lens [B] int32
+    or None.  Returns (u [B,T,C], the window for the next call [B,3,C])."""
+    import torch
+    if x.dim() != 3:
+        raise ValueError("x must be [B,T,C]")
+    B, T, C = x.shape
+    dev = x.device
+    _conv_inputs(x, w, bias, win, (B, T, C))
+    if lens is not None:
+        _require(lens, "lens", torch.int32, (B,), dev)
+    with _call_on(dev, stream):
+        if u is None:
+            u = torch.empty_like(x)
+        _require(u, "u", x.dtype, (B, T, C), dev)
+        if win_out is None:
+            win_out = torch.empty((B, 3, C), dtype=x.dtype, device=dev)
+        _require(win_out, "win_out", x.dtype, (B, 3, C), dev)
+        _check("m2rnn_conv4_silu_fwd_state", lib().m2rnn_conv4_silu_fwd_state(
+            B, T, C, _dtype_code(x), _ptr(x), _ptr(w), _ptr(bias), _ptr(lens), _ptr(win), _ptr(u), _ptr(win_out),
+            _stream(stream)))
+    return u, win_out
+
+
+def m2rnn_conv4_silu_step(x, w, bias=None, win=None, *, u=None, win_out=None, stream=None) -> Tuple[object, object]:
+    """One step of the causal conv4 + SiLU: x [B,C]; the rest as in m2rnn_conv4_silu_fwd_state.  Pass
+    ``win_out=win`` to move the window on in place."""
+    import torch
+    if x.dim() != 2:
+        raise ValueError("x must be [B,C]")
+    B, C = x.shape
+    dev = x.device
+    _conv_inputs(x, w, bias, win, (B, C))
+    with _call_on(dev, stream):
+        if u is None:
+            u = torch.empty_like(x)
+        _require(u, "u", x.dtype, (B, C), dev)
+        if win_out is None:
+            win_out = torch.empty((B, 3, C), dtype=x.dtype, device=dev)
+        _require(win_out, "win_out", x.dtype, (B, 3, C), dev)
+        _check("m2rnn_conv4_silu_step", lib().m2rnn_conv4_silu_step(
+            B, C, _dtype_code(x), _ptr(x), _ptr(w), _ptr(bias), _ptr(win), _ptr(u), _ptr(win_out), _stream(stream)))
+    return u, win_out
+
+
+def _conv_inputs(x, w, bias, win, shape):
+    import torch
+    dev = x.device
+    if dev.type != "cuda":
+        raise ValueError("inputs must be on a GPU (HIP) device")
+    B, C = shape[0], shape[-1]
+    _require(x, "x", (torch.float32, torch.bfloat16), shape, dev)
+    _require(w, "w", torch.float32, (C, 4), dev)
+    if bias is not None:
+        _require(bias, "bias", torch.float32, (C,), dev)
+    if win is not None:
+        _require(win, "win", x.dtype, (B, 3, C), dev)
+
+
+# ---------------------------------------------------------------- norm of q and k with rotation
+
+def _qk_inputs(q, k, gamma_q, gamma_k, pos, inv_freq):
+    import torch
+    if q.dim() != 4 or k.dim() != 4:
+        raise ValueError("q must be [B,T,Nq,K] and k [B,T,Nk,K]")
+    B, T, Nq, K = q.shape
+    Nk = k.shape[2]
+    dev = q.device
+    if dev.type != "cuda":
+        raise ValueError("inputs must be on a GPU (HIP) device")
+    _require(q, "q", (torch.float32, torch.bfloat16), (B, T, Nq, K), dev)
+    _require(k, "k", q.dtype, (B, T, Nk, K), dev)
+    _require(gamma_q, "gamma_q", torch.float32, (K,), dev)
+    _require(gamma_k, "gamma_k", torch.float32, (K,), dev)
+    _require(pos, "pos", torch.int32, (B, T), dev)
+    _require(inv_freq, "inv_freq", torch.float64, (inv_freq.numel(),), dev)
+    return B, T, Nq, Nk, K, 2 * inv_freq.numel(), dev
+
+
+def m2rnn_qk_norm_rope_fwd(q, k, gamma_q, gamma_k, pos, inv_freq, eps: float = 1e-6, *, interleaved: bool = False,
+                           q_out=None, k_out=None, stream=None) -> Tuple[object, object]:
+    """RMSNorm of each head of q [B,T,Nq,K] and k [B,T,Nk,K] (fp32/bf16) with the scales gamma_q, gamma_k [K],
+    then the rotation of its first R = 2 len(inv_freq) features by pos * inv_freq: pos [B,T] int32,
+    inv_freq [R/2] float64; pairs (p, p + R/2), or (2p, 2p + 1) if interleaved.  Returns (q_out, k_out)."""
+    import torch
+    B, T, Nq, Nk, K, R, dev = _qk_inputs(q, k, gamma_q, gamma_k, pos, inv_freq)
+    with _call_on(dev, stream):
+        if q_out is None:
+            q_out = torch.empty_like(q)
+        if k_out is None:
+            k_out = torch.empty_like(k)
+        _require(q_out, "q_out", q.dtype, (B, T, Nq, K), dev)
+        _require(k_out, "k_out", q.dtype, (B, T, Nk, K), dev)
+        _check("m2rnn_qk_norm_rope_fwd", lib().m2rnn_qk_norm_rope_fwd(
+            B, T, Nq, Nk, K, R, int(interleaved), _dtype_code(q), _ptr(q), _ptr(k), _ptr(gamma_q), _ptr(gamma_k),
+            _ptr(pos), _ptr(inv_freq), float(eps), _ptr(q_out), _ptr(k_out), _stream(stream)))
+    return q_out, k_out
+
+
+def m2rnn_qk_norm_rope_bwd(q, k, gamma_q, gamma_k, pos, inv_freq, dq_out, dk_out, eps: float = 1e-6, *,
+                           interleaved: bool = False, workspace=None, stream=None, out=None) -> Dict[str, object]:
+    """dq, dk (fp32), dgamma_q, dgamma_k of the norm with rotation for the upstream dq_out, dk_out (fp32).
+    `out` may hold the tensors to write."""
+    import torch
+    B, T, Nq, Nk, K, R, dev = _qk_inputs(q, k, gamma_q, gamma_k, pos, inv_freq)
+    _require(dq_out, "dq_out", torch.float32, (B, T, Nq, K), dev)
+    _require(dk_out, "dk_out", torch.float32, (B, T, Nk, K), dev)
+    shapes = {"dq": (B, T, Nq, K), "dk": (B, T, Nk, K), "dgamma_q": (K,), "dgamma_k": (K,)}
+    with _call_on(dev, stream):
+        if out is None:
+            out = {n: torch.empty(s, dtype=torch.float32, device=dev) for n, s in shapes.items()}
+        for n, s in shapes.items():
+            _require(out.get(n), n, torch.float32, s, dev)
+        nbytes = _size_query("m2rnn_qk_norm_rope_bwd_workspace_size", B, T, Nq, Nk, K)
+        ws = _workspace(nbytes, dev, workspace)
+        _check("m2rnn_qk_norm_rope_bwd", lib().m2rnn_qk_norm_rope_bwd(
+            B, T, Nq, Nk, K, R, int(interleaved), _dtype_code(q), _ptr(q), _ptr(k), _ptr(gamma_q), _ptr(gamma_k),
+            _ptr(pos), _ptr(inv_freq), float(eps), _ptr(dq_out), _ptr(dk_out), *(_ptr(out[n]) for n in shapes),
+            _ptr(ws), nbytes, _stream(stream)))
+    return out
+
+
+# ---------------------------------------------------------------- gradient norm and clipping
+
+def _tensor_list(tensors, name):
+    """(the tensors, an array of m2rnn_tensor, their device) of a list of contiguous fp32/bf16 tensors."""
+    import torch
+    tensors = list(tensors)
+    if not tensors:
+        raise ValueError(f"{name} is empty")
+    codes = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16}
+    dev = tensors[0].device
+    if dev.type != "cuda":
+        raise ValueError(f"{name} must be on a GPU (HIP) device")
+    flat = []
+    for i, t in enumerate(tensors):
+        code = codes.get(t.dtype)
+        if code is None:
+            raise TypeError(f"{name}[{i}] has dtype {t.dtype}, expected float32 or bfloat16")
+        if t.device != dev:
+            raise ValueError(f"{name}[{i}] is on {t.device}, expected {dev}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name}[{i}] must be contiguous")
+        flat += (t.data_ptr(), t.numel(), code)
+    return tensors, (ctypes.c_int64 * len(flat))(*flat), dev
+
+
+def _grad_norm(arr, count, dev, norm, workspace, stream):
+    import torch
+    if norm is None:
+        norm = torch.empty((), dtype=torch.float32, device=dev)
+    nbytes = _size_query("m2rnn_grad_norm_workspace_size", arr, count)
+    ws = _workspace(nbytes, dev, workspace)
+    _check("m2rnn_grad_norm", lib().m2rnn_grad_norm(arr, count, _ptr(norm), _ptr(ws), nbytes, _stream(stream)))
+    return norm
+
+
+def _require_scalar(norm, dev):
+    import torch
+    if norm.device != dev or norm.dtype != torch.float32 or norm.numel() != 1:
+        raise ValueError(f"norm must be a float32 scalar on {dev}")
+
+
+def m2rnn_grad_norm(grads, *, norm=None, workspace=None, stream=None):
+    """The 2-norm over all elements of a list of contiguous fp32/bf16 tensors, as a float32 scalar on
+    their device."""
+    grads, arr, dev = _tensor_list(grads, "grads")
+    if norm is not None:
+        _require_scalar(norm, dev)
+    with _call_on(dev, stream):
+        return _grad_norm(arr, len(grads), dev, norm, workspace, stream)
+
+
+def m2rnn_grad_clip(grads, max_norm: float, *, norm=None, out=None, workspace=None, stream=None):
+    """Scales the gradients by max_norm / norm where their norm exceeds max_norm, in place or into the
+    tensors of `out`; returns the norm (float32 scalar on their device).  `norm`: an already known
+    total (for instance combined over ranks), instead of these tensors' own.  A norm that is not finite
+    leaves the gradients as they are."""
+    grads, arr, dev = _tensor_list(grads, "grads")
+    if not float(max_norm) >= 0.0:
+        raise ValueError(f"max_norm must be >= 0, got {max_norm}")
+    dst = None
+    if out is not None:
+        out = list(out)
+        if len(out) != len(grads):
+            raise ValueError(f"out has {len(out)} tensors, expected {len(grads)}")
+        for i, (o, g) in enumerate(zip(out, grads)):
+            if o.shape != g.shape or o.dtype != g.dtype or o.device != dev or not o.is_contiguous():
+                raise ValueError(f"out[{i}] must be contiguous and like grads[{i}]")
+        dst = (ctypes.c_void_p * len(out))(*[o.data_ptr() for o in out])
+    if norm is not None:
+        _require_scalar(norm, dev)
+    with _call_on(dev, stream):
+        if norm is None:
+            norm = _grad_norm(arr, len(grads), dev, None, workspace, stream)
+        _check("m2rnn_grad_clip", lib().m2rnn_grad_clip(arr, len(grads), dst, _ptr(norm), float(max_norm),
+                                                        _stream(stream)))
+    return norm

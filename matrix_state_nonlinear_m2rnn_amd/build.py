@@ -30,6 +30,8 @@ SOURCES = [
     "m2rnn_ssm_f32.hip",
     "m2rnn_ssm_bwd_bf16.hip",
     "m2rnn_ssm_bwd_f32.hip",
+    "m2rnn_qk.hip",
+    "m2rnn_grad.hip",
 ]
 
 # Packed fp32 VALU ops stay off: hipcc -O3 would otherwise form v_pk_{add,mul,fma}_f32.

@@ -115,6 +115,13 @@ size_t conv_ws_bytes(int64_t B, int64_t T, int64_t C) {
   return round_up256((size_t)parts * 5 * C * sizeof(float)) + round_up256(reduce_scratch(parts, 5 * C) * sizeof(float));
 }
 
+// The window's entry points take rows of C values (C a multiple of 4), so a token of a longer array is as
+// good as an array of its own: alignment to four values.
+bool conv_aligned(int dtype, const void* x, const void* win, const void* u, const void* win_out) {
+  const uintptr_t mask = dtype == M2RNN_DTYPE_BF16 ? 7 : 15;
+  return (((uintptr_t)x | (uintptr_t)win | (uintptr_t)u | (uintptr_t)win_out) & mask) == 0;
+}
+
 // Workgroups of the conv kernels: one wave per (b, chunk of `chunk` steps, 64 groups of 4 channels).
 long conv_blocks(int64_t B, int64_t T, int64_t C, int chunk) {
   return ceil_div(B * ceil_div(T, chunk) * ceil_div(C / 4, 64), kBlkThreads / 64);
@@ -295,6 +302,46 @@ int m2rnn_conv4_silu_bwd(int64_t B, int64_t T, int64_t C, int dtype, const void*
                          du, (int)B, (int)T, (int)C, chunk, dx, part);
   }
   reduce_rows(part, parts, 5 * C, 5 * C, dw, 4 * C, dbias, scratch, s);
+  return status(hipGetLastError());
+}
+
+int m2rnn_conv4_silu_fwd_state(int64_t B, int64_t T, int64_t C, int dtype, const void* x, const float* w,
+                               const float* bias, const int32_t* lens, const void* win, void* u, void* win_out,
+                               void* stream) {
+  int st = check_conv(B, T, C, dtype);
+  if (st) return st;
+  if (B == 0) return M2RNN_OK;
+  if (!w || !win_out || (T > 0 && (!x || !u))) return M2RNN_EINVAL;
+  if (!conv_aligned(dtype, x, win, u, win_out) || !al16(w) || !al16(bias)) return M2RNN_EINVAL;
+  if (!al4(lens)) return M2RNN_EINVAL;
+  // several threads read a window that one of them writes: the two must not overlap
+  const uintptr_t bytes = (uintptr_t)B * 3 * C * (dtype == M2RNN_DTYPE_BF16 ? 2 : 4);
+  const uintptr_t in = (uintptr_t)win, out = (uintptr_t)win_out;
+  if (win && in < out + bytes && out < in + bytes) return M2RNN_EINVAL;
+  const int64_t Tc = T > 0 ? T : 1;
+  const int chunk = conv_chunk(B, Tc, C, kConvChunkFwd);
+  const long blocks = conv_blocks(B, Tc, C, chunk);
+  const auto kern = dtype == M2RNN_DTYPE_BF16 ? &m2rnn_conv4_silu_state_kernel<true>
+                                              : &m2rnn_conv4_silu_state_kernel<false>;
+  hipLaunchKernelGGL(kern, dim3((unsigned)blocks), dim3(kBlkThreads), 0, (hipStream_t)stream, x, w, bias,
+                     (const int*)lens, win, (int)B, (int)T, (int)C, chunk, u, win_out);
+  return status(hipGetLastError());
+}
+
+int m2rnn_conv4_silu_step(int64_t B, int64_t C, int dtype, const void* x, const float* w, const float* bias,
+                          const void* win, void* u, void* win_out, void* stream) {
+  int st = check_conv(B, 1, C, dtype);
+  if (st) return st;
+  if (B == 0) return M2RNN_OK;
+  if (!x || !w || !u || !win_out) return M2RNN_EINVAL;
+  if (!conv_aligned(dtype, x, win, u, win_out) || !al16(w) || !al16(bias)) return M2RNN_EINVAL;
+  const uintptr_t bytes = (uintptr_t)B * 3 * C * (dtype == M2RNN_DTYPE_BF16 ? 2 : 4);
+  const uintptr_t in = (uintptr_t)win, out = (uintptr_t)win_out;
+  if (win && in != out && in < out + bytes && out < in + bytes) return M2RNN_EINVAL;
+  const auto kern = dtype == M2RNN_DTYPE_BF16 ? &m2rnn_conv4_silu_step_kernel<true>
+                                              : &m2rnn_conv4_silu_step_kernel<false>;
+  hipLaunchKernelGGL(kern, dim3((unsigned)ceil_div(B * (C / 4), kBlkThreads)), dim3(kBlkThreads), 0,
+                     (hipStream_t)stream, x, w, bias, win, (long)B, (int)C, u, win_out);
   return status(hipGetLastError());
 }
 

@@ -5,11 +5,9 @@
 // bit-reproducible.
 #pragma once
 
-#include "m2rnn_device.h"
+#include "m2rnn_stream.h"
 
 namespace m2rnn {
-
-constexpr int kBlkThreads = 256;
 
 // e^x and ln x from the hardware's 2^x and log2 x (v_exp_f32, v_log_f32), about 1 ulp each plus the
 // rounding of the base change; 1/x from v_rcp_f32.
@@ -29,53 +27,6 @@ __device__ __forceinline__ float silu_gradf_(float x) {
 // pre-activation a and the head's alpha, beta.
 __device__ __forceinline__ float gate_f(float a, float alpha, float beta) {
   return exp_(-alpha * softplusf_(a + beta));
-}
-
-template <bool BF16>
-__device__ __forceinline__ float4 load4(const void* base, long i) {
-  if constexpr (BF16) {
-    const uint2 r = *(const uint2*)((const uint16_t*)base + i);
-    return make_float4(bf16_lo_to_f32(r.x), bf16_hi_to_f32(r.x), bf16_lo_to_f32(r.y), bf16_hi_to_f32(r.y));
-  }
-  return *(const float4*)((const float*)base + i);
-}
-
-// load4 as a non-temporal load, for streams read once.  (It helps the RMSNorm and the conv
-// backward by 2-4%; the conv forward, whose x rows are also read by the neighbouring chunk's
-// window, runs slower with it.)
-template <bool BF16>
-__device__ __forceinline__ float4 load4_nt(const void* base, long i) {
-  if constexpr (BF16) {
-    typedef unsigned u2v __attribute__((ext_vector_type(2)));
-    const u2v r = __builtin_nontemporal_load((const u2v*)((const uint16_t*)base + i));
-    return make_float4(bf16_lo_to_f32(r[0]), bf16_hi_to_f32(r[0]), bf16_lo_to_f32(r[1]), bf16_hi_to_f32(r[1]));
-  }
-  const f32x4 t = __builtin_nontemporal_load((const f32x4*)((const float*)base + i));
-  return make_float4(t[0], t[1], t[2], t[3]);
-}
-
-template <bool BF16>
-__device__ __forceinline__ void store4(void* base, long i, float4 v) {
-  if constexpr (BF16) {
-    *(uint2*)((uint16_t*)base + i) = make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
-  } else {
-    *(float4*)((float*)base + i) = v;
-  }
-}
-
-// store4 as a non-temporal store: the caches need not keep a stream written once and not read
-// back by the kernel.
-template <bool BF16>
-__device__ __forceinline__ void store4_nt(void* base, long i, const float (&o)[4]) {
-  if constexpr (BF16) {
-    typedef unsigned u2v __attribute__((ext_vector_type(2)));
-    const u2v v = {pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3])};
-    __builtin_nontemporal_store(v, (u2v*)((uint16_t*)base + i));
-  } else {
-    typedef float f4v __attribute__((ext_vector_type(4)));
-    const f4v v = {o[0], o[1], o[2], o[3]};
-    __builtin_nontemporal_store(v, (f4v*)((float*)base + i));
-  }
 }
 
 // Sum over the workgroup (kBlkThreads threads) of a pair of values, in a fixed order; every
@@ -603,6 +554,112 @@ __global__ void __launch_bounds__(kBlkThreads) m2rnn_conv4_silu_bwd_kernel(const
     *(float4*)(pp + (c + e) * 4) = make_float4(aw[e][0], aw[e][1], aw[e][2], aw[e][3]);
     pp[4 * C + c + e] = ab[e];
   }
+}
+
+// The forward with the three inputs before the first step (win [B,3,C], oldest first; null: zeros) and
+// the window after each sequence's last step (of lens[b], clamped to [0, T]; null: T) out.  Steps
+// past a sequence's end are not read and give zeros.  Same layout as the forward; the threads of a
+// sequence's first chunk write its window.
+template <bool BF16>
+__global__ void __launch_bounds__(kBlkThreads) m2rnn_conv4_silu_state_kernel(
+    const void* __restrict__ x, const float* __restrict__ w, const float* __restrict__ bias,
+    const int* __restrict__ lens, const void* __restrict__ win, int B, int T, int C, int CHUNK, void* __restrict__ u,
+    void* __restrict__ win_out) {
+  int b, chunk, c4;
+  if (!conv_pos(B, T > 0 ? T : 1, C, CHUNK, b, chunk, c4)) return;
+  const int c = 4 * c4;
+  const int len = lens ? min(max(lens[b], 0), T) : T;
+  const long row = (long)b * T;
+  // input at step t >= -3 of the sequence
+  auto seen = [&](int t, float (&o)[4]) {
+    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (t >= 0)
+      v = load4<BF16>(x, (row + t) * C + c);
+    else if (win)
+      v = load4<BF16>(win, ((long)b * 3 + 3 + t) * C + c);
+    o[0] = v.x; o[1] = v.y; o[2] = v.z; o[3] = v.w;
+  };
+  if (chunk == 0 && win_out) {
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+      float o[4];
+      seen(len - 3 + i, o);
+      store4<BF16>(win_out, ((long)b * 3 + i) * C + c, make_float4(o[0], o[1], o[2], o[3]));
+    }
+  }
+  const int t0 = chunk * CHUNK, t1 = min(T, t0 + CHUNK), te = min(len, t1);
+  const float zero[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (t0 < te) {
+    float wk[4][4];  // [channel][tap]
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float4 t4 = *(const float4*)(w + (long)(c + e) * 4);
+      wk[e][0] = t4.x; wk[e][1] = t4.y; wk[e][2] = t4.z; wk[e][3] = t4.w;
+    }
+    const float4 bv = bias ? *(const float4*)(bias + c) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    const float bs[4] = {bv.x, bv.y, bv.z, bv.w};
+    float xs[3][4];
+#pragma unroll
+    for (int i = 0; i < 3; ++i) seen(t0 - 3 + i, xs[i]);
+    auto issue = [&](int tb, float4(&o)[kConvBatch]) {
+#pragma unroll
+      for (int k = 0; k < kConvBatch; ++k) o[k] = load4<BF16>(x, (row + min(tb + k, te - 1)) * C + c);
+    };
+    float4 xv[kConvBatch];
+    issue(t0, xv);
+    for (int tb = t0; tb < te; tb += kConvBatch) {
+      float4 xn[kConvBatch];
+      issue(tb + kConvBatch, xn);
+#pragma unroll
+      for (int k = 0; k < kConvBatch; ++k) {
+        if (tb + k < te) {
+          const float xc[4] = {xv[k].x, xv[k].y, xv[k].z, xv[k].w};
+          float o[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            o[e] = siluf_(wk[e][0] * xs[0][e] + wk[e][1] * xs[1][e] + wk[e][2] * xs[2][e] + wk[e][3] * xc[e] + bs[e]);
+            xs[0][e] = xs[1][e];
+            xs[1][e] = xs[2][e];
+            xs[2][e] = xc[e];
+          }
+          store4_nt<BF16>(u, (row + tb + k) * C + c, o);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < kConvBatch; ++k) xv[k] = xn[k];
+    }
+  }
+  for (int t = max(t0, te); t < t1; ++t) store4_nt<BF16>(u, (row + t) * C + c, zero);
+}
+
+// One step: thread (b, 4 channels).  It reads its window before it writes the next, so win_out may be win.
+template <bool BF16>
+__global__ void __launch_bounds__(kBlkThreads) m2rnn_conv4_silu_step_kernel(const void* x, const float* w,
+                                                                             const float* bias, const void* win,
+                                                                             long B, int C, void* u, void* win_out) {
+  const int C4 = C / 4;
+  const long i = (long)blockIdx.x * kBlkThreads + threadIdx.x;
+  if (i >= B * C4) return;
+  const long b = i / C4;
+  const int c = 4 * (int)(i % C4);
+  float4 s[4];
+#pragma unroll
+  for (int k = 0; k < 3; ++k)
+    s[k] = win ? load4<BF16>(win, (b * 3 + k) * C + c) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  s[3] = load4<BF16>(x, b * C + c);
+  const float4 bv = bias ? *(const float4*)(bias + c) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  const float bs[4] = {bv.x, bv.y, bv.z, bv.w};
+  float o[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float4 t4 = *(const float4*)(w + (long)(c + e) * 4);
+    const float x0 = ((const float*)&s[0])[e], x1 = ((const float*)&s[1])[e], x2 = ((const float*)&s[2])[e],
+                x3 = ((const float*)&s[3])[e];
+    o[e] = siluf_(t4.x * x0 + t4.y * x1 + t4.z * x2 + t4.w * x3 + bs[e]);
+  }
+#pragma unroll
+  for (int k = 0; k < 3; ++k) store4<BF16>(win_out, (b * 3 + k) * C + c, s[k + 1]);
+  store4<BF16>(u, b * C + c, make_float4(o[0], o[1], o[2], o[3]));
 }
 
 }  // namespace m2rnn
