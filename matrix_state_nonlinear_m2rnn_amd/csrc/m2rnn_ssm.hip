@@ -46,7 +46,7 @@ constexpr long kSsmWaves = 2048;
 // A segment is at least this many chunks: shorter ones spend their time filling the pipeline.
 constexpr int kSsmMinChunks = 2;
 // Workgroups that the backward's launch aims for where a group's heads can be split.
-constexpr long kSsmBwdGroups = 256;
+constexpr long kSsmBwdGroups = 1024;
 
 int check_ssm(const m2rnn_dims* d, int dtype) {
   if (!d) return M2RNN_EINVAL;
@@ -281,11 +281,12 @@ int m2rnn_ssm_bwd(const m2rnn_dims* dims, int qkv_dtype, const void* q, const vo
   hipStream_t s = (hipStream_t)stream;
   hipError_t e = hipSuccess;
   const long parts = (long)A.B * A.nch;
+  const bool one = A.N == A.G * A.HS && A.CB == 1;  // one head and one block for each workgroup
   if (A.B > 0) {
     e = launch(pick(p, SSM_STATE_REV), p.units * A.S, p.HPW * p.VB * 4, A, s);
     if (e == hipSuccess) e = launch_combine(A, true, s);
     if (e == hipSuccess && A.nch > 0)
-      e = launch(p.bf16 ? ssm_bwd_kernel_bf16(p.KP, p.VB) : ssm_bwd_kernel_f32(p.KP, p.VB),
+      e = launch(p.bf16 ? ssm_bwd_kernel_bf16(p.KP, p.VB, one) : ssm_bwd_kernel_f32(p.KP, p.VB, one),
                  (long)A.B * A.G * A.nch * A.HS, 64 * kSsmBwdWaves, A, s);
     if (e != hipSuccess) return status(e);
     if (A.HS > 1 && count > 0) {

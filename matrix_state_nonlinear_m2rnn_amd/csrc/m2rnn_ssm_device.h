@@ -34,6 +34,13 @@ constexpr int ssm_chunk() {
 // of them) the 8 rows that a transposing read touches at a time fall on different banks.
 constexpr int ssm_stride(int cols) { return cols + (cols > 16 ? 16 : 8); }
 
+// A lane index made opaque at this point.  Addresses formed from it are formed anew here, instead of
+// being kept in registers from one phase of a loop to the next.
+__device__ __forceinline__ int fresh(int x) {
+  asm volatile("" : "+v"(x));
+  return x;
+}
+
 __device__ __forceinline__ float exp2_(float x) { return __builtin_amdgcn_exp2f(x); }
 
 // x = hi + mid + lo exactly; the three bf16 are the high halves of the words.
@@ -67,6 +74,20 @@ __device__ __forceinline__ f32x4 mfma_planes(const uint4 (&A)[NA], const uint4 (
     for (int i = 0; i < NA; ++i) {
       const int j = s - i;
       if (j >= 0 && j < NB) acc = mfma_bf16(A[i], B[j], acc);
+    }
+  return acc;
+}
+
+// The same sum with the operands' roles turned: the passes follow in the same order, so the transposed
+// tile holds the same bits.
+template <int NA, int NB>
+__device__ __forceinline__ f32x4 mfma_planes_turned(const uint4 (&A)[NA], const uint4 (&B)[NB], f32x4 acc) {
+#pragma unroll
+  for (int s = 2; s >= 0; --s)
+#pragma unroll
+    for (int j = 0; j < NB; ++j) {
+      const int i = s - j;
+      if (i >= 0 && i < NA) acc = mfma_bf16(A[i], B[j], acc);
     }
   return acc;
 }

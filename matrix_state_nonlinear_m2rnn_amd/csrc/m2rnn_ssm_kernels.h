@@ -85,22 +85,23 @@ __device__ __forceinline__ void ssm_decay(const SsmTab<L>& tab, int I, int J, in
   }
 }
 
-// Four consecutive values of a bf16 plane set (NP planes, `plane` elements apart).
+// Four values as NP bf16 planes put together again.
+template <int NP>
+__device__ __forceinline__ void planes_vals4(const uint2 (&u)[NP], float (&o)[4]) {
+#pragma unroll
+  for (int i = NP - 1; i >= 0; --i) {
+    const float x[4] = {bf16_lo_to_f32(u[i].x), bf16_hi_to_f32(u[i].x), bf16_lo_to_f32(u[i].y), bf16_hi_to_f32(u[i].y)};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[e] = i == NP - 1 ? x[e] : o[e] + x[e];
+  }
+}
+// Four consecutive values of a bf16 plane set in LDS (NP planes, `plane` elements apart).
 template <int NP>
 __device__ __forceinline__ void lds_vals4(const uint16_t* p, int plane, float (&o)[4]) {
-  const uint2 u = *(const uint2*)p;
-  o[0] = bf16_lo_to_f32(u.x);
-  o[1] = bf16_hi_to_f32(u.x);
-  o[2] = bf16_lo_to_f32(u.y);
-  o[3] = bf16_hi_to_f32(u.y);
+  uint2 u[NP];
 #pragma unroll
-  for (int i = 1; i < NP; ++i) {
-    const uint2 w = *(const uint2*)(p + i * plane);
-    o[0] += bf16_lo_to_f32(w.x);
-    o[1] += bf16_hi_to_f32(w.x);
-    o[2] += bf16_lo_to_f32(w.y);
-    o[3] += bf16_hi_to_f32(w.y);
-  }
+  for (int i = 0; i < NP; ++i) u[i] = *(const uint2*)(p + i * plane);
+  planes_vals4<NP>(u, o);
 }
 
 // The step size and log2 decay of lane j's step from its gate pre-activation (live: within the
@@ -548,9 +549,9 @@ __global__ void __launch_bounds__(256) m2rnn_ssm_combine_kernel(SsmArgs A) {
 
 // ------------------------------------------------------------------ backward
 
-constexpr int kSsmBwdWaves = 8;
+constexpr int kSsmBwdWaves = 4;
 
-// Eight values p[0], p[st], .. as the three planes of an MFMA operand.
+// Eight consecutive slots of an operand as its three planes.
 __device__ __forceinline__ void split3x8(const float (&x)[8], uint4 (&o)[3]) {
   const float a[4] = {x[0], x[1], x[2], x[3]}, b[4] = {x[4], x[5], x[6], x[7]};
   uint2 pa[3], pb[3];
@@ -560,10 +561,31 @@ __device__ __forceinline__ void split3x8(const float (&x)[8], uint4 (&o)[3]) {
   for (int p = 0; p < 3; ++p) o[p] = cat(pa[p], pb[p]);
 }
 
+// The factors of ssm_decay with the roles turned: lane column j = 16 J + n, rows i = 16 I + 4 g + r.  The
+// same products and differences, so both tiles hold the same numbers.
+template <int L>
+__device__ __forceinline__ void ssm_decay_col(const SsmTab<L>& tab, int I, int J, int g, int n, float (&o)[4]) {
+  if (I != J) {
+    const float f = tab.f[I - 1][16 * J + n];
+    const float4 x = *(const float4*)&tab.x[16 * I + 4 * g];
+    o[0] = x.x * f;
+    o[1] = x.y * f;
+    o[2] = x.z * f;
+    o[3] = x.w * f;
+  } else {
+    const float hi = tab.chi[16 * J + n], lo = tab.clo[16 * J + n];
+    const float4 h = *(const float4*)&tab.chi[16 * I + 4 * g];
+    const float4 l = *(const float4*)&tab.clo[16 * I + 4 * g];
+    const float hj[4] = {h.x, h.y, h.z, h.w}, lj[4] = {l.x, l.y, l.z, l.w};
+#pragma unroll
+    for (int r = 0; r < 4; ++r) o[r] = n <= 4 * g + r ? exp2_((hj[r] - hi) + (lj[r] - lo)) : 0.0f;
+  }
+}
+
 // All gradients of one chunk of one query/key group (or of a part of its heads).  With u = dy,
 // H the state that enters the chunk, R the gradient of the state that leaves it, and
-//     P_ij = 2^{c_i - c_j} D_j (q_i . k_j),   X_ij = 2^{c_i - c_j} D_j (u_i . v_j)   (j <= i):
-//     dv_j = sum_i P_ij u_i + D_j 2^{c_L - c_j} R^T k_j + w_r (.) u_j
+//     P_ij = 2^{c_i - c_j} (q_i . k_j),   X_ij = 2^{c_i - c_j} D_j (u_i . v_j)   (j <= i):
+//     dv_j = D_j (sum_i P_ij u_i + 2^{c_L - c_j} R^T k_j) + w_r (.) u_j
 //     dq_i = sum_j X_ij k_j + 2^{c_i} H u_i
 //     dk_j = sum_i X_ij q_i + D_j 2^{c_L - c_j} R v_j
 // and for the decays, with M_ij = 2^{c_i - c_j} (q_i . k_j)(u_i . v_j),
@@ -574,29 +596,39 @@ __device__ __forceinline__ void split3x8(const float (&x)[8], uint4 (&o)[3]) {
 // the same M_ij and added in fp64, so what cancels cancels exactly and a decay that forgets at once
 // leaves no residue of the terms on the diagonal.
 //
-// Every chunk has its own workgroup (no chain), which walks its heads one after the other, adding
-// dq and dk in registers; heads of 128 value columns go as two blocks of 64, since all gradients are
-// sums over value columns.  Per head three barriers: stage; tiles of X, P and M; the products.
-template <bool BF16, int KP, int VB>
-__global__ void __launch_bounds__(64 * kSsmBwdWaves) m2rnn_ssm_bwd_kernel(SsmArgs A) {
+// Every chunk has its own workgroup (no chain), which walks its heads one after the other; heads of
+// 128 value columns go as two blocks of 64, since all gradients are sums over value columns.
+// X is summed over the heads before it meets k and q (one product for all heads that share them).
+// A wave owns a 16-step tile of rows (X for dq, row sums of M) and the same tile of columns (X for dk,
+// P, column sums of M), five tiles for every wave: formed in both orientations, X needs no exchange
+// and only P goes through LDS.  H and R come from HBM straight into operands: each wave takes 16
+// of the K rows of H and R for the terms that enter and leave, 16 value columns for dv.
+// ONE: the workgroup has one head of one block, so nothing lives from one pass of the loop to the next.
+template <bool BF16, int KP, int VB, bool ONE>
+__global__ void __launch_bounds__(64 * kSsmBwdWaves, KP == 128 ? 1 : 2) m2rnn_ssm_bwd_kernel(SsmArgs A) {
   constexpr int L = ssm_chunk<BF16>(), NI = L / 16, NS = L / 32, KS = KP / 32, KM = KP / 16, NP = BF16 ? 1 : 3;
   constexpr int NW = kSsmBwdWaves, NTH = 64 * NW;
   constexpr int VP = VB < 32 ? 32 : VB, VS = VP / 32, VM = VB / 16;  // columns in LDS, contraction steps, tiles
-  constexpr int STK = ssm_stride(KP), STV = ssm_stride(VP), STP = ssm_stride(L);
-  constexpr int NT = NI * (NI + 1) / 2, TPT = (NT + NW - 1) / NW;    // lower tiles; per wave
-  constexpr int TPQ = KM * NI >= NW ? KM * NI / NW : 1;              // dq (dk) tiles per wave, one K tile
+  constexpr int STK = ssm_stride(KP), STV = ssm_stride(VP);
+  constexpr int MPW = KM >= NW ? KM / NW : 1;                        // K tiles per wave
   constexpr int TPV = VM * NI >= NW ? VM * NI / NW : 1;              // dv tiles per wave, one V tile
-  __shared__ __attribute__((aligned(16))) uint16_t sq[NP * L * STK];
+  constexpr bool AHEAD = VB <= 32;                                   // the next block's v and u fit in registers meanwhile
+  constexpr int SETS = NI == 4 ? 6 : 2;                              // (J, s) operand sets of P
+  constexpr int QW = NP * L * STK, PW = SETS * 3 * 2 * 64 * 4;       // elements of the q and P blocks
+  constexpr int XW = (KP * L * 2 > 3 * L * STV ? KP * L * 2 : 3 * L * STV);
   __shared__ __attribute__((aligned(16))) uint16_t sk[NP * L * STK];
+  __shared__ __attribute__((aligned(16))) uint16_t sqp[QW > PW ? QW : PW];  // q before and after the heads, P between
   __shared__ __attribute__((aligned(16))) uint16_t sv[NP * L * STV];
-  __shared__ __attribute__((aligned(16))) uint16_t su[3 * L * STV];
-  __shared__ __attribute__((aligned(16))) uint16_t sx[3 * L * STP];  // X, then the same of P
-  __shared__ __attribute__((aligned(16))) uint16_t sp[3 * L * STP];
-  __shared__ __attribute__((aligned(16))) SsmTab<L> tab;
-  __shared__ double rowp[NI][L], colp[NI][L], ap[KM][L], bp[KM][L], rh[KM];
+  __shared__ __attribute__((aligned(16))) uint16_t su[XW];                 // u; dq's or dk's entering terms at the end
+  __shared__ __attribute__((aligned(16))) SsmTab<L> tabs[2];
+  __shared__ double rowp[L], colp[L], ap[KM][L], bp[KM][L], rh[KM];
   __shared__ float dgp[L], dwp[NI][VB];
+  uint16_t* const sq = sqp;
+  uint2* const pbuf = (uint2*)sqp;
 
-  const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, n = lane & 15;
+  int tid = threadIdx.x;
+  const int lane = tid & 63;
+  int g = lane >> 4, n = lane & 15;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
   int unit, hs;
   ssm_unit(A.HS, A.B * A.G * A.nch, unit, hs);
@@ -605,139 +637,196 @@ __global__ void __launch_bounds__(64 * kSsmBwdWaves) m2rnn_ssm_bwd_kernel(SsmArg
   const int K = A.K, V = A.V, T = A.T, N = A.N;
   const int hpg = N / A.G, per = (hpg + A.HS - 1) / A.HS;
   const int hb = grp * hpg + hs * per, he = min(grp * hpg + hpg, hb + per);
-  const int CB = A.CB, blocks = (he > hb ? he - hb : 0) * CB;
+  const int CB = ONE ? 1 : A.CB, blocks = ONE ? 1 : (he > hb ? he - hb : 0) * CB;
   const int t0 = ch * L;
   const int Tb = ssm_len(A, b);
   const int rows = min(L, Tb - t0);
   const long krow = (long)A.G * K, vrow = (long)N * V, row0 = (long)b * T + t0;
 
-  // this wave's tiles
-  const int mq = (w * TPQ) / NI, iq0 = (w * TPQ) % NI;
-  const bool hasq = w * TPQ < KM * NI;
+  // this wave's tiles: rows It, columns Jt of the triangle (four tiles: one of each; two: waves 0, 1 the
+  // rows, 2, 3 the columns), K tiles m0 .. m0 + MPW - 1 (with two: waves 0, 1 for dq, 2, 3 for dk)
+  const int It = NI == 4 ? w : w, Jt = NI == 4 ? w : w - 2;
+  const bool hasI = It < NI, hasJ = Jt >= 0;
+  const bool hasdq = KM >= NW || w < KM, hasdk = KM >= NW || w >= NW - KM;
+  const int mq = KM >= NW ? w * MPW : w, mk = KM >= NW ? w * MPW : w - (NW - KM);
   const int mv = (w * TPV) / NI, jv0 = (w * TPV) % NI;
   const bool hasv = w * TPV < VM * NI;
 
   SsmPieces<BF16, L, VP, NTH> pv;
   SsmPieces<false, L, VP, NTH> pu;
-  float pa = 0.0f;
   auto fetch = [&](int blk) {
     const int h = hb + blk / CB;
     const long off = row0 * vrow + (long)h * V + (blk % CB) * VB;
     pv.load(BF16 ? (const void*)((const uint16_t*)A.v + off) : (const void*)((const float*)A.v + off), vrow, VB, rows,
             tid);
     pu.load(A.dy + off, vrow, VB, rows, tid);
-    if (w == 0 && lane < rows) pa = A.a[(row0 + lane) * N + h];
   };
-  if (blocks > 0) fetch(0);
-  {
-    SsmPieces<BF16, L, KP, NTH> pq, pk;
+  // wave NW - 1 forms the tables of head h (its lanes: the chunk's steps)
+  auto tables = [&](int h, SsmTab<L>& tab) {
+    const bool live = lane < L && t0 + lane < Tb;
+    const float a = live ? A.a[(row0 + lane) * N + h] : 0.0f;
+    float delta;
+    double lg;
+    ssm_gate(live, a, A.alpha[h], A.beta[h], delta, lg);
+    ssm_tables<L, true, false, false>(tab, lane, delta, lg);
+  };
+  SsmPieces<BF16, L, KP, NTH> pq;
+  auto fetch_q = [&]() {
     const long off = row0 * krow + (long)grp * K;
     pq.load(BF16 ? (const void*)((const uint16_t*)A.q + off) : (const void*)((const float*)A.q + off), krow, K, rows,
             tid);
+  };
+  if (blocks > 0) fetch(0);
+  {
+    SsmPieces<BF16, L, KP, NTH> pk;
+    const long off = row0 * krow + (long)grp * K;
     pk.load(BF16 ? (const void*)((const uint16_t*)A.k + off) : (const void*)((const float*)A.k + off), krow, K, rows,
             tid);
-    pq.store(sq, tid);
+    fetch_q();
     pk.store(sk, tid);
+    pq.store(sq, tid);
   }
-  // X and P: the tiles right of the diagonal that a 32-wide contraction covers stay zero
-  for (int i = tid; i < 3 * L * STP / 2; i += NTH) {
-    ((uint32_t*)sx)[i] = 0;
-    ((uint32_t*)sp)[i] = 0;
-  }
+  if (w == NW - 1 && blocks > 0) tables(hb, tabs[0]);
   __syncthreads();
-  // q k^T of this wave's lower tiles: the same for all heads
-  f32x4 qk[TPT];
+  // q k^T of this wave's row and column tiles, and q of its entering terms' rows: the same for all heads
+  f32x4 qkr[NI], qkc[NI];
 #pragma unroll
-  for (int p = 0; p < TPT; ++p) {
-    qk[p] = f32x4{0, 0, 0, 0};
-    const int t = w + NW * p;
-    if (t < NT) {
-      int I, J;
-      tri_tile(t, I, J);
+  for (int J = 0; J < NI; ++J) {
+    qkr[J] = f32x4{0, 0, 0, 0};
+    if (hasI && J <= It) {
 #pragma unroll
       for (int s = 0; s < KS; ++s) {
         uint4 ko[NP], qo[NP];
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
           ko[i] = lds_row(sk + i * L * STK, STK, 16 * J, 32 * s, g, n);
-          qo[i] = lds_row(sq + i * L * STK, STK, 16 * I, 32 * s, g, n);
+          qo[i] = lds_row(sq + i * L * STK, STK, 16 * It, 32 * s, g, n);
         }
-        qk[p] = mfma_planes<NP, NP>(ko, qo, qk[p]);
+        qkr[J] = mfma_planes<NP, NP>(ko, qo, qkr[J]);
       }
     }
   }
-  f32x4 dq[TPQ], dk[TPQ];
 #pragma unroll
-  for (int p = 0; p < TPQ; ++p) dq[p] = dk[p] = f32x4{0, 0, 0, 0};
+  for (int I = 0; I < NI; ++I) {
+    qkc[I] = f32x4{0, 0, 0, 0};
+    if (hasJ && I >= Jt) {
+#pragma unroll
+      for (int s = 0; s < KS; ++s) {
+        uint4 ko[NP], qo[NP];
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+          ko[i] = lds_row(sk + i * L * STK, STK, 16 * Jt, 32 * s, g, n);
+          qo[i] = lds_row(sq + i * L * STK, STK, 16 * I, 32 * s, g, n);
+        }
+        qkc[I] = mfma_planes_turned<NP, NP>(qo, ko, qkc[I]);
+      }
+    }
+  }
+  uint2 qv[MPW][NI][NP];
+#pragma unroll
+  for (int p = 0; p < MPW; ++p)
+#pragma unroll
+    for (int I = 0; I < NI; ++I)
+#pragma unroll
+      for (int i = 0; i < NP; ++i)
+        qv[p][I][i] = *(const uint2*)(sq + i * L * STK + (16 * I + n) * STK + 16 * ((hasdq ? mq : 0) + p) + 4 * g);
+  f32x4 xr[NI], xc[NI], dqi[MPW][NI], dki[MPW][NI];
+#pragma unroll
+  for (int i = 0; i < NI; ++i) {
+    xr[i] = xc[i] = f32x4{0, 0, 0, 0};
+#pragma unroll
+    for (int p = 0; p < MPW; ++p) dqi[p][i] = dki[p][i] = f32x4{0, 0, 0, 0};
+  }
   // wave 0, lane t: what g and dD hold of the head's column blocks done so far
-  double gsum = 0.0, dsum = 0.0, delta64 = 0.0;
+  double gsum = 0.0, dsum = 0.0;
 
   for (int blk = 0; blk < blocks; ++blk) {
     const int head = hb + blk / CB, cb = blk % CB;
     const long pair = (long)b * N + head;
+    const SsmTab<L>& tab = tabs[(blk / CB) & 1];
     __syncthreads();  // the previous block's reads are done
+    g = fresh(g);
+    n = fresh(n);
+    tid = fresh(tid);
     pv.store(sv, tid);
     pu.store(su, tid);
-    if (w == 0 && cb == 0) {
-      float delta;
-      double lg;
-      ssm_gate(lane < L && t0 + lane < Tb, pa, A.alpha[head], A.beta[head], delta, lg);
-      ssm_tables<L, true, false, false>(tab, lane, delta, lg);
-      delta64 = delta;
-    }
-    const float pa_now = pa;
     __syncthreads();
-    if (blk + 1 < blocks) fetch(blk + 1);
+    if (AHEAD && blk + 1 < blocks) fetch(blk + 1);
 
-    // X, P and M of the lower tiles
+    // rows It: X and the row sums of M
+    if (hasI) {
+      uint4 uo[VS][3];
 #pragma unroll
-    for (int p = 0; p < TPT; ++p) {
-      const int t = w + NW * p;
-      if (t < NT) {
-        int I, J;
-        tri_tile(t, I, J);
+      for (int s = 0; s < VS; ++s)
+#pragma unroll
+        for (int i = 0; i < 3; ++i) uo[s][i] = lds_row(su + i * L * STV, STV, 16 * It, 32 * s, g, n);
+      double row = 0.0;
+#pragma unroll
+      for (int J = 0; J < NI; ++J) {
+        if (J > It) continue;
         f32x4 uv = {0, 0, 0, 0};
 #pragma unroll
         for (int s = 0; s < VS; ++s) {
-          uint4 vo[NP], uo[3];
+          uint4 vo[NP];
 #pragma unroll
           for (int i = 0; i < NP; ++i) vo[i] = lds_row(sv + i * L * STV, STV, 16 * J, 32 * s, g, n);
-#pragma unroll
-          for (int i = 0; i < 3; ++i) uo[i] = lds_row(su + i * L * STV, STV, 16 * I, 32 * s, g, n);
-          uv = mfma_planes<NP, 3>(vo, uo, uv);
+          uv = mfma_planes<NP, 3>(vo, uo[s], uv);
         }
         float d[4];
-        ssm_decay<L, false>(tab, I, J, g, n, d);
+        ssm_decay<L, false>(tab, It, J, g, n, d);
         const float4 dj = *(const float4*)&tab.d[16 * J + 4 * g];
         const float dl[4] = {dj.x, dj.y, dj.z, dj.w};
-        float xx[4], pp[4];
-        double mm[4], row = 0.0;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          const float x0 = uv[r] * d[r];
-          const float m = x0 * qk[p][r];
-          mm[r] = m;
-          xx[r] = x0 * dl[r];
-          pp[r] = qk[p][r] * (d[r] * dl[r]);
-          const bool diag = I == J && 4 * g + r == n;
-          if (diag) dgp[16 * I + n] = m;
-          row += diag ? 0.0 : mm[r] * (double)dl[r];
+          const float x0 = uv[r] * d[r], m = x0 * qkr[J][r];
+          xr[J][r] = __builtin_fmaf(x0, dl[r], xr[J][r]);
+          const bool diag = It == J && 4 * g + r == n;
+          if (diag) dgp[16 * It + n] = m;
+          row = __builtin_fma((double)(diag ? 0.0f : m), (double)dl[r], row);
         }
-        uint2 px[3], pq2[3];
-        split3x4(xx, px);
-        split3x4(pp, pq2);
-        uint16_t* ox = sx + (16 * I + n) * STP + 16 * J + 4 * g;
-        uint16_t* op = sp + (16 * I + n) * STP + 16 * J + 4 * g;
-#pragma unroll
-        for (int i = 0; i < 3; ++i) {
-          *(uint2*)(ox + i * L * STP) = px[i];
-          *(uint2*)(op + i * L * STP) = pq2[i];
-        }
-        row = group_sum64(row);
-        if (g == 0) rowp[J][16 * I + n] = row;
-        const double col = row16_sum4_64(mm, lane);
-        if ((n & 3) == 0) colp[I][16 * J + 4 * g + (n >> 2)] = col;
       }
+      row = group_sum64(row);
+      if (g == 0) rowp[16 * It + n] = row;
+    }
+    g = fresh(g);
+    n = fresh(n);
+    // columns Jt: X, P and the column sums of M
+    if (hasJ) {
+      uint4 vo[VS][NP];
+#pragma unroll
+      for (int s = 0; s < VS; ++s)
+#pragma unroll
+        for (int i = 0; i < NP; ++i) vo[s][i] = lds_row(sv + i * L * STV, STV, 16 * Jt, 32 * s, g, n);
+      const float dj = tab.d[16 * Jt + n];
+      double col = 0.0;
+#pragma unroll
+      for (int I = 0; I < NI; ++I) {
+        if (I < Jt) continue;
+        f32x4 uv = {0, 0, 0, 0};
+#pragma unroll
+        for (int s = 0; s < VS; ++s) {
+          uint4 uo[3];
+#pragma unroll
+          for (int i = 0; i < 3; ++i) uo[i] = lds_row(su + i * L * STV, STV, 16 * I, 32 * s, g, n);
+          uv = mfma_planes_turned<3, NP>(uo, vo[s], uv);
+        }
+        float d[4], pp[4];
+        ssm_decay_col<L>(tab, I, Jt, g, n, d);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const float x0 = uv[r] * d[r], m = x0 * qkc[I][r];
+          xc[I][r] = __builtin_fmaf(x0, dj, xc[I][r]);
+          pp[r] = qkc[I][r] * d[r];
+          col += (double)m;
+        }
+        uint2 pl[3];
+        split3x4(pp, pl);
+        const int set = NI == 4 ? (Jt < 2 ? 2 * Jt + I / 2 : Jt + 2) : Jt;
+#pragma unroll
+        for (int i = 0; i < 3; ++i) pbuf[((set * 3 + i) * 2 + (I & 1)) * 64 + lane] = pl[i];
+      }
+      col = group_sum64(col);
+      if (g == 0) colp[16 * Jt + n] = col;
     }
     __syncthreads();
 
@@ -745,6 +834,8 @@ __global__ void __launch_bounds__(64 * kSsmBwdWaves) m2rnn_ssm_bwd_kernel(SsmArg
     const float* Rp = A.rloc + ((pair * A.nch + ch) * V + cb * VB) * K;        // [V][K]
     const float* Ip = A.seg + ((pair * A.S + ch / A.cps) * V + cb * VB) * K;   // [V][K]
     const float idec = exp2_(A.cdec[pair * A.nch + ch]);
+    g = fresh(g);
+    n = fresh(n);
     if (hasv) {
       // dv^T: rows c of tile mv, columns j
       uint4 Ro[KS][3];
@@ -752,7 +843,7 @@ __global__ void __launch_bounds__(64 * kSsmBwdWaves) m2rnn_ssm_bwd_kernel(SsmArg
       for (int s = 0; s < KS; ++s) {
         float x[8];
         const int kk = 32 * s + 8 * g;
-        const long at = (long)(16 * mv + n) * K + kk;
+        const unsigned at = (unsigned)((16 * mv + n) * K + kk);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           float4 a4 = make_float4(0, 0, 0, 0), i4 = a4;
@@ -786,15 +877,20 @@ __global__ void __launch_bounds__(64 * kSsmBwdWaves) m2rnn_ssm_bwd_kernel(SsmArg
           for (int i = 0; i < NP; ++i) ko[i] = lds_row(sk + i * L * STK, STK, 16 * J, 32 * s, g, n);
           acc = mfma_planes<3, NP>(Ro[s], ko, acc);
         }
-        const float wj = tab.w[16 * J + n];
+        const float hi = tab.chi[L - 1] - tab.chi[16 * J + n], lo = tab.clo[L - 1] - tab.clo[16 * J + n];
+        const float ej = exp2_(hi + lo), dj = tab.d[16 * J + n];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) acc[r] *= wj;
+        for (int r = 0; r < 4; ++r) acc[r] *= ej;
 #pragma unroll
         for (int s = 0; s < NS; ++s) {
           if (s < J / 2) continue;
+          const int set = NI == 4 ? (J < 2 ? 2 * J + s : J + 2) : J;
           uint4 po[3];
 #pragma unroll
-          for (int i = 0; i < 3; ++i) po[i] = lds_col(sp + i * L * STP, STP, 32 * s, 16 * J, g, n);
+          for (int i = 0; i < 3; ++i) {
+            const uint2* pb = &pbuf[((set * 3 + i) * 2) * 64 + lane];
+            po[i] = cat(2 * s >= J ? pb[0] : make_uint2(0, 0), pb[64]);
+          }
           acc = mfma_planes<3, 3>(uo[s], po, acc);
         }
         float uj[4], vj[4];
@@ -803,128 +899,116 @@ __global__ void __launch_bounds__(64 * kSsmBwdWaves) m2rnn_ssm_bwd_kernel(SsmArg
         const int t = t0 + 16 * J + n;
         if (t < T)
           *(float4*)(A.dv + ((long)b * T + t) * vrow + (long)head * V + cb * VB + 16 * mv + 4 * g) =
-              make_float4(acc[0] + wr[0] * uj[0], acc[1] + wr[1] * uj[1], acc[2] + wr[2] * uj[2],
-                          acc[3] + wr[3] * uj[3]);
+              make_float4(dj * acc[0] + wr[0] * uj[0], dj * acc[1] + wr[1] * uj[1], dj * acc[2] + wr[2] * uj[2],
+                          dj * acc[3] + wr[3] * uj[3]);
         const float sum = row16_sum4(uj[0] * vj[0], uj[1] * vj[1], uj[2] * vj[2], uj[3] * vj[3], lane);
         if ((n & 3) == 0) dwp[J][16 * mv + 4 * g + (n >> 2)] = sum;
       }
     }
-    if (hasq) {
-      // dq^T and dk^T: rows kk of tile mq, columns i (j)
-      uint4 Ho[VS][3], Ro[VS][3];
-      double dot = 0.0;  // <R, H>: every step of the chunk gets it, so its error would add up in dalpha and dbeta
-      const int kk = 16 * mq + n;
+    g = fresh(g);
+    n = fresh(n);
+#pragma unroll
+    for (int p = 0; p < MPW; ++p) {
+      // the terms of H and R: rows kk of this wave's K tiles, columns i (j)
+      float x[VS][8], y[VS][8];
 #pragma unroll
       for (int s = 0; s < VS; ++s) {
-        float x[8], y[8];
-        const int c = 32 * s + 8 * g;
+        const int c = 32 * s + 8 * g, kq = 16 * (mq + p) + n, kr = 16 * (mk + p) + n;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = y[e] = 0.0f;
-        if (kk < K && c < VB) {
-          const float4 a4 = *(const float4*)(Hp + (long)kk * V + c), b4 = *(const float4*)(Hp + (long)kk * V + c + 4);
-          x[0] = a4.x; x[1] = a4.y; x[2] = a4.z; x[3] = a4.w;
-          x[4] = b4.x; x[5] = b4.y; x[6] = b4.z; x[7] = b4.w;
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            y[e] = __builtin_fmaf(idec, Ip[(long)(c + e) * K + kk], Rp[(long)(c + e) * K + kk]);
+        for (int e = 0; e < 8; ++e) x[s][e] = y[s][e] = 0.0f;
+        if ((hasdq || KM < NW) && c < VB) {
+          const int kk = hasdq ? kq : kr;  // two K tiles: the waves of dk take H for <R, H>
+          if (kk < K) {
+            const float4 a4 = *(const float4*)(Hp + (unsigned)(kk * V + c)), b4 = *(const float4*)(Hp + (unsigned)(kk * V + c + 4));
+            x[s][0] = a4.x; x[s][1] = a4.y; x[s][2] = a4.z; x[s][3] = a4.w;
+            x[s][4] = b4.x; x[s][5] = b4.y; x[s][6] = b4.z; x[s][7] = b4.w;
+          }
         }
-        if (iq0 == 0) {  // one wave per K tile
+        if (hasdk && kr < K && c < VB) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) dot = __builtin_fma((double)x[e], (double)y[e], dot);
+          for (int e = 0; e < 8; ++e) {
+            const unsigned at = (unsigned)((c + e) * K + kr);
+            y[s][e] = __builtin_fmaf(idec, Ip[at], Rp[at]);
+          }
         }
-        split3x8(x, Ho[s]);
-        split3x8(y, Ro[s]);
       }
-      if (iq0 == 0) {
+      if (hasdk) {
+        double dot = 0.0;  // <R, H>: every step of the chunk gets it, so its error would add up in dalpha and dbeta
+#pragma unroll
+        for (int s = 0; s < VS; ++s)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) dot = __builtin_fma((double)x[s][e], (double)y[s][e], dot);
         dot = prefix64(dot);
-        if (lane == 63) rh[mq] = dot;
+        if (lane == 63) rh[mk + p] = dot;
+        uint4 Ro[VS][3];
+#pragma unroll
+        for (int s = 0; s < VS; ++s) split3x8(y[s], Ro[s]);
+#pragma unroll
+        for (int J = 0; J < NI; ++J) {
+          f32x4 acc = {0, 0, 0, 0};
+#pragma unroll
+          for (int s = 0; s < VS; ++s) {
+            uint4 vo[NP];
+#pragma unroll
+            for (int i = 0; i < NP; ++i) vo[i] = lds_row(sv + i * L * STV, STV, 16 * J, 32 * s, g, n);
+            acc = mfma_planes<3, NP>(Ro[s], vo, acc);
+          }
+          const float hi = tab.chi[L - 1] - tab.chi[16 * J + n], lo = tab.clo[L - 1] - tab.clo[16 * J + n];
+          const float ej = exp2_(hi + lo), dj = tab.d[16 * J + n];
+          double dot_b = 0.0;
+          float kv[4];
+          lds_vals4<NP>(sk + (16 * J + n) * STK + 16 * (mk + p) + 4 * g, L * STK, kv);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            acc[r] *= ej;
+            dot_b = __builtin_fma((double)kv[r], (double)acc[r], dot_b);
+            dki[p][J][r] = __builtin_fmaf(dj, acc[r], dki[p][J][r]);
+          }
+          dot_b = group_sum64(dot_b);
+          if (g == 0) bp[mk + p][16 * J + n] = dot_b;
+        }
       }
-      uint4 kc[NS][NP], qc[NS][NP];
+      if (hasdq) {
+        uint4 Ho[VS][3];
 #pragma unroll
-      for (int s = 0; s < NS; ++s)
+        for (int s = 0; s < VS; ++s) split3x8(x[s], Ho[s]);
 #pragma unroll
-        for (int i = 0; i < NP; ++i) {
-          kc[s][i] = lds_col(sk + i * L * STK, STK, 32 * s, 16 * mq, g, n);
-          qc[s][i] = lds_col(sq + i * L * STK, STK, 32 * s, 16 * mq, g, n);
-        }
+        for (int I = 0; I < NI; ++I) {
+          f32x4 acc = {0, 0, 0, 0};
 #pragma unroll
-      for (int p = 0; p < TPQ; ++p) {
-        const int I = iq0 + p;
-        f32x4 acc = {0, 0, 0, 0};
+          for (int s = 0; s < VS; ++s) {
+            uint4 uo[3];
 #pragma unroll
-        for (int s = 0; s < VS; ++s) {
-          uint4 uo[3];
+            for (int i = 0; i < 3; ++i) uo[i] = lds_row(su + i * L * STV, STV, 16 * I, 32 * s, g, n);
+            acc = mfma_planes<3, 3>(Ho[s], uo, acc);
+          }
+          const float e = tab.e[16 * I + n];
+          double dot_a = 0.0;
+          float qf[4];
+          planes_vals4<NP>(qv[p][I], qf);
 #pragma unroll
-          for (int i = 0; i < 3; ++i) uo[i] = lds_row(su + i * L * STV, STV, 16 * I, 32 * s, g, n);
-          acc = mfma_planes<3, 3>(Ho[s], uo, acc);
-        }
-        const float e = tab.e[16 * I + n];
-        float qv[4];
-        double dot_a = 0.0;
-        lds_vals4<NP>(sq + (16 * I + n) * STK + 16 * mq + 4 * g, L * STK, qv);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          acc[r] *= e;
-          dot_a = __builtin_fma((double)qv[r], (double)acc[r], dot_a);
-          dq[p][r] += acc[r];
-        }
-        dot_a = group_sum64(dot_a);
-        if (g == 0) ap[mq][16 * I + n] = dot_a;
-#pragma unroll
-        for (int s = 0; s < NS; ++s) {
-          if (s > I / 2) continue;
-          uint4 xo[3];
-#pragma unroll
-          for (int i = 0; i < 3; ++i) xo[i] = lds_row_acc(sx + i * L * STP, STP, 16 * I, 32 * s, g, n);
-          dq[p] = mfma_planes<NP, 3>(kc[s], xo, dq[p]);
-        }
-        // dk, the same tile of steps
-        f32x4 bcc = {0, 0, 0, 0};
-#pragma unroll
-        for (int s = 0; s < VS; ++s) {
-          uint4 vo[NP];
-#pragma unroll
-          for (int i = 0; i < NP; ++i) vo[i] = lds_row(sv + i * L * STV, STV, 16 * I, 32 * s, g, n);
-          bcc = mfma_planes<3, NP>(Ro[s], vo, bcc);
-        }
-        // without D_j: its factor w / D_j is 2^{c_L - c_j}
-        const float dj = tab.d[16 * I + n];
-        const float hi = tab.chi[L - 1] - tab.chi[16 * I + n], lo = tab.clo[L - 1] - tab.clo[16 * I + n];
-        const float ej = exp2_(hi + lo);
-        float kv[4];
-        double dot_b = 0.0;
-        lds_vals4<NP>(sk + (16 * I + n) * STK + 16 * mq + 4 * g, L * STK, kv);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          bcc[r] *= ej;
-          dot_b = __builtin_fma((double)kv[r], (double)bcc[r], dot_b);
-          dk[p][r] = __builtin_fmaf(dj, bcc[r], dk[p][r]);
-        }
-        dot_b = group_sum64(dot_b);
-        if (g == 0) bp[mq][16 * I + n] = dot_b;
-#pragma unroll
-        for (int s = 0; s < NS; ++s) {
-          if (s < I / 2) continue;
-          uint4 xo[3];
-#pragma unroll
-          for (int i = 0; i < 3; ++i) xo[i] = lds_col(sx + i * L * STP, STP, 32 * s, 16 * I, g, n);
-          dk[p] = mfma_planes<NP, 3>(qc[s], xo, dk[p]);
+          for (int r = 0; r < 4; ++r) {
+            acc[r] *= e;
+            dot_a = __builtin_fma((double)qf[r], (double)acc[r], dot_a);
+            dqi[p][I][r] += acc[r];
+          }
+          dot_a = group_sum64(dot_a);
+          if (g == 0) ap[mq + p][16 * I + n] = dot_a;
         }
       }
     }
+    if (w == NW - 1 && cb == CB - 1 && blk + 1 < blocks) tables(head + 1, tabs[(blk / CB + 1) & 1]);
+    if (!AHEAD && blk + 1 < blocks) fetch(blk + 1);
     __syncthreads();
 
     if (w == 0) {
       const int t = lane;
-      double row = 0.0, col = 0.0, diag = 0.0, aa = 0.0, bb = 0.0, through = 0.0;
+      double row = 0.0, col = 0.0, diag = 0.0, aa = 0.0, bb = 0.0, through = 0.0, delta64 = 0.0;
       if (t < L) {
-        const int It = t / 16;
-#pragma unroll
-        for (int i = 0; i < NI; ++i) {
-          row += i <= It ? rowp[i][t] : 0.0;
-          col += i >= It ? colp[i][t] : 0.0;
-        }
+        row = rowp[t];
+        col = colp[t];
         diag = dgp[t];
+        delta64 = tab.d[t];
 #pragma unroll
         for (int m = 0; m < KM; ++m) {
           aa += ap[m][t];
@@ -940,10 +1024,9 @@ __global__ void __launch_bounds__(64 * kSsmBwdWaves) m2rnn_ssm_bwd_kernel(SsmArg
       gsum += sx64 + prefix64(dpp64<0x138, 0xF>(y)) + through;
       dsum += col + bb;
       if (cb == CB - 1) {
-        const double al = A.alpha[head];
         const bool live = t < L && t0 + t < Tb;
-        const float z = pa_now + A.beta[head];
-        const float da = live ? (float)(dsum - al * gsum) / (1.0f + expf(-z)) : 0.0f;
+        const float z = (live ? A.a[(row0 + t) * N + head] : 0.0f) + A.beta[head];
+        const float da = live ? (float)(dsum - (double)A.alpha[head] * gsum) / (1.0f + expf(-z)) : 0.0f;
         if (t < L && t0 + t < T) A.da[(row0 + t) * N + head] = da;
         const double sb = prefix64(da), sa = prefix64(live ? -delta64 * gsum : 0.0);
         if (lane == 63) {
@@ -960,17 +1043,57 @@ __global__ void __launch_bounds__(64 * kSsmBwdWaves) m2rnn_ssm_bwd_kernel(SsmArg
       A.part_wr[((long)b * A.nch + ch) * vrow + (long)head * V + cb * VB + lane] = sum;
     }
   }
-  if (hasq) {
-    const long plane = (long)hs * A.B * T * krow;
+
+  // dq and dk: X of all heads times k and q, by step tiles, plus the terms of H and R, by K tiles, through LDS
+  fetch_q();
+  __syncthreads();
+  pq.store(sq, tid);
+  float* const ex = (float*)su;  // [L][KP]
+  const long plane = (long)hs * A.B * T * krow;
 #pragma unroll
-    for (int p = 0; p < TPQ; ++p) {
-      const int t = t0 + 16 * (iq0 + p) + n, kk = 16 * mq + 4 * g;
-      if (t < T && kk < K) {
-        const long at = plane + ((long)b * T + t) * krow + (long)grp * K + kk;
-        *(float4*)(A.dq + at) = make_float4(dq[p][0], dq[p][1], dq[p][2], dq[p][3]);
-        *(float4*)(A.dk + at) = make_float4(dk[p][0], dk[p][1], dk[p][2], dk[p][3]);
+  for (int which = 0; which < 2; ++which) {
+    if (which ? hasdk : hasdq) {
+#pragma unroll
+      for (int p = 0; p < MPW; ++p)
+#pragma unroll
+        for (int I = 0; I < NI; ++I) {
+          const f32x4& t = which ? dki[p][I] : dqi[p][I];
+          *(float4*)(ex + (16 * I + n) * KP + 16 * ((which ? mk : mq) + p) + 4 * g) = make_float4(t[0], t[1], t[2], t[3]);
+        }
+    }
+    __syncthreads();
+    if (which ? hasJ : hasI) {
+      const int own = which ? Jt : It;
+      uint4 xo[NS][3];
+#pragma unroll
+      for (int s = 0; s < NS; ++s) {
+        uint2 h0[3], h1[3];
+        const f32x4 &a4 = which ? xc[2 * s] : xr[2 * s], &b4 = which ? xc[2 * s + 1] : xr[2 * s + 1];
+        const float av[4] = {a4[0], a4[1], a4[2], a4[3]}, bv[4] = {b4[0], b4[1], b4[2], b4[3]};
+        split3x4(av, h0);
+        split3x4(bv, h1);
+#pragma unroll
+        for (int i = 0; i < 3; ++i) xo[s][i] = cat(h0[i], h1[i]);
+      }
+      float* out = (which ? A.dk : A.dq) + plane;
+      const int t = t0 + 16 * own + n;
+#pragma unroll
+      for (int m = 0; m < KM; ++m) {
+        const float4 t4 = *(const float4*)(ex + (16 * own + n) * KP + 16 * m + 4 * g);
+        f32x4 acc = {t4.x, t4.y, t4.z, t4.w};
+#pragma unroll
+        for (int s = 0; s < NS; ++s) {
+          uint4 ko[NP];
+#pragma unroll
+          for (int i = 0; i < NP; ++i) ko[i] = lds_col((which ? sq : sk) + i * L * STK, STK, 32 * s, 16 * m, g, n);
+          acc = mfma_planes<NP, 3>(ko, xo[s], acc);
+        }
+        const int kk = 16 * m + 4 * g;
+        if (t < T && kk < K)
+          *(float4*)(out + ((long)b * T + t) * krow + (long)grp * K + kk) = make_float4(acc[0], acc[1], acc[2], acc[3]);
       }
     }
+    if (which == 0) __syncthreads();
   }
 }
 

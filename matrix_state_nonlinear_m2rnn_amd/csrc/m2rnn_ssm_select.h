@@ -29,23 +29,28 @@ const void* ssm_pick(int KP, int VB, int HPW, int which) {
   if (KP == 64) return ssm_pick_k<BF16, 64>(VB, HPW, which);
   return ssm_pick_k<BF16, 128>(VB, HPW, which);
 }
+template <bool BF16, int KP, int VB>
+const void* ssm_pick_bwd_kv(bool one) {
+  return one ? (const void*)&m2rnn_ssm_bwd_kernel<BF16, KP, VB, true>
+             : (const void*)&m2rnn_ssm_bwd_kernel<BF16, KP, VB, false>;
+}
 template <bool BF16, int KP>
-const void* ssm_pick_bwd_k(int VB) {
-  if (VB == 16) return (const void*)&m2rnn_ssm_bwd_kernel<BF16, KP, 16>;
-  if (VB == 32) return (const void*)&m2rnn_ssm_bwd_kernel<BF16, KP, 32>;
-  return (const void*)&m2rnn_ssm_bwd_kernel<BF16, KP, 64>;
+const void* ssm_pick_bwd_k(int VB, bool one) {
+  if (VB == 16) return ssm_pick_bwd_kv<BF16, KP, 16>(one);
+  if (VB == 32) return ssm_pick_bwd_kv<BF16, KP, 32>(one);
+  return ssm_pick_bwd_kv<BF16, KP, 64>(one);
 }
 template <bool BF16>
-const void* ssm_pick_bwd(int KP, int VB) {
-  if (KP == 32) return ssm_pick_bwd_k<BF16, 32>(VB);
-  if (KP == 64) return ssm_pick_bwd_k<BF16, 64>(VB);
-  return ssm_pick_bwd_k<BF16, 128>(VB);
+const void* ssm_pick_bwd(int KP, int VB, bool one) {
+  if (KP == 32) return ssm_pick_bwd_k<BF16, 32>(VB, one);
+  if (KP == 64) return ssm_pick_bwd_k<BF16, 64>(VB, one);
+  return ssm_pick_bwd_k<BF16, 128>(VB, one);
 }
 
 // Defined in m2rnn_ssm_<bf16|f32>.hip and m2rnn_ssm_bwd_<bf16|f32>.hip.
 const void* ssm_kernel_bf16(int KP, int VB, int HPW, int which);
 const void* ssm_kernel_f32(int KP, int VB, int HPW, int which);
-const void* ssm_bwd_kernel_bf16(int KP, int VB);
-const void* ssm_bwd_kernel_f32(int KP, int VB);
+const void* ssm_bwd_kernel_bf16(int KP, int VB, bool one);
+const void* ssm_bwd_kernel_f32(int KP, int VB, bool one);
 
 }  // namespace m2rnn
