@@ -115,6 +115,14 @@ __device__ __forceinline__ uint4 lds_col(const uint16_t* p, int ST, int r0, int 
   return cat(__builtin_bit_cast(uint2, a), __builtin_bit_cast(uint2, b));
 }
 
+// The column operand with 16 contraction slots: rows r0 .. r0 + 15, lane group g rows r0 + 4g .. + 3.
+__device__ __forceinline__ uint2 lds_col16(const uint16_t* p, int ST, int r0, int c0, int g, int n) {
+  typedef short v4s __attribute__((ext_vector_type(4)));
+  typedef __attribute__((address_space(3))) v4s* lds_v4s;
+  return __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                                       (lds_v4s)(p + (r0 + 4 * g + (n >> 2)) * ST + c0 + 4 * (n & 3))));
+}
+
 // ------------------------------------------------------------------ cross-lane helpers in fp64
 
 template <int CTRL, int ROWS>
@@ -151,10 +159,43 @@ __device__ __forceinline__ double row16_sum4_64(const double (&x)[4], int lane) 
   c += dpp64<kDppQuadXor2, 0xF>(c);
   return c;
 }
+// The two words of each of two doubles exchanged between the wave's halves (32) or between the odd rows
+// of 16 of the first and the even rows of the second (16), and added.
+template <bool HALVES>
+__device__ __forceinline__ double swap_add64(double x, double y) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, x), v = __builtin_bit_cast(uint64_t, y);
+  const auto swap = [](uint32_t p, uint32_t q) {
+    if constexpr (HALVES)
+      return __builtin_amdgcn_permlane32_swap(p, q, false, false);
+    else
+      return __builtin_amdgcn_permlane16_swap(p, q, false, false);
+  };
+  const auto lo = swap((uint32_t)u, (uint32_t)v), hi = swap((uint32_t)(u >> 32), (uint32_t)(v >> 32));
+  return __builtin_bit_cast(double, ((uint64_t)hi[0] << 32) | lo[0]) +
+         __builtin_bit_cast(double, ((uint64_t)hi[1] << 32) | lo[1]);
+}
 // Sum over the four lanes n, n + 16, n + 32, n + 48, in each of them.
 __device__ __forceinline__ double group_sum64(double x) {
-  x += __shfl_xor(x, 16);
-  return x + __shfl_xor(x, 32);
+  x = swap_add64<false>(x, x);
+  return swap_add64<true>(x, x);
+}
+// Four such sums at once: lane group g gets the one of x[g].
+__device__ __forceinline__ double group_sum64_4(const double (&x)[4]) {
+  return swap_add64<false>(swap_add64<true>(x[0], x[2]), swap_add64<true>(x[1], x[3]));
+}
+
+// out[16 I + n] = the sum of x[I] over the lane groups.
+template <int NI>
+__device__ __forceinline__ void put_group_sums(double* out, const double (&x)[NI], int g, int n) {
+  if constexpr (NI == 4) {
+    out[16 * g + n] = group_sum64_4(x);
+  } else {
+#pragma unroll
+    for (int I = 0; I < NI; ++I) {
+      const double t = group_sum64(x[I]);
+      if (g == 0) out[16 * I + n] = t;
+    }
+  }
 }
 
 // ------------------------------------------------------------------ the chunk's decays
@@ -171,9 +212,9 @@ __device__ __forceinline__ double log2_decay(float alpha, float delta) {
   return x > 16384.0 ? 16384.0 : x;
 }
 
-// Decay tables of one head's chunk in LDS, by step: e = 2^{c_i}; w = D_j 2^{c_L - c_j}; x = 2^{c_i - c at
+// Decay tables of one head's chunk in LDS, by step: e = 2^{c_i}; w = 2^{c_L - c_j}; x = 2^{c_i - c at
 // the step before i's 16-step tile}; f[I - 1] = 2^{(c at the step before tile I) - c_j} for j below
-// tile I, times D_j if FD; d = D_j; and c itself as a pair of floats (chi + clo) for the diagonal
+// tile I (w and f times D_j if FD, the forward's form); d = D_j; and c itself as a pair of floats (chi + clo) for the diagonal
 // tiles, whose factors are formed one by one.
 template <int L>
 struct SsmTab {
@@ -209,7 +250,7 @@ __device__ __forceinline__ double ssm_tables(SsmTab<L>& tab, int lane, float del
       tab.clo[lane] = (float)(c - (double)hi);
       tab.d[lane] = delta;
       tab.e[lane] = exp2_((float)c);
-      tab.w[lane] = delta * exp2_((float)(cl - c));
+      tab.w[lane] = (FD ? delta : 1.0f) * exp2_((float)(cl - c));
     } else {
       tab.w[lane] = REV ? exp2_((float)c) : delta * exp2_((float)(cl - c));
     }

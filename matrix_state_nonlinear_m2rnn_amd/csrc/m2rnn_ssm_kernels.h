@@ -877,8 +877,7 @@ __global__ void __launch_bounds__(64 * kSsmBwdWaves, KP == 128 ? 1 : 2) m2rnn_ss
           for (int i = 0; i < NP; ++i) ko[i] = lds_row(sk + i * L * STK, STK, 16 * J, 32 * s, g, n);
           acc = mfma_planes<3, NP>(Ro[s], ko, acc);
         }
-        const float hi = tab.chi[L - 1] - tab.chi[16 * J + n], lo = tab.clo[L - 1] - tab.clo[16 * J + n];
-        const float ej = exp2_(hi + lo), dj = tab.d[16 * J + n];
+        const float ej = tab.w[16 * J + n], dj = tab.d[16 * J + n];
 #pragma unroll
         for (int r = 0; r < 4; ++r) acc[r] *= ej;
 #pragma unroll
@@ -943,6 +942,7 @@ __global__ void __launch_bounds__(64 * kSsmBwdWaves, KP == 128 ? 1 : 2) m2rnn_ss
         uint4 Ro[VS][3];
 #pragma unroll
         for (int s = 0; s < VS; ++s) split3x8(y[s], Ro[s]);
+        double part[NI];
 #pragma unroll
         for (int J = 0; J < NI; ++J) {
           f32x4 acc = {0, 0, 0, 0};
@@ -953,25 +953,24 @@ __global__ void __launch_bounds__(64 * kSsmBwdWaves, KP == 128 ? 1 : 2) m2rnn_ss
             for (int i = 0; i < NP; ++i) vo[i] = lds_row(sv + i * L * STV, STV, 16 * J, 32 * s, g, n);
             acc = mfma_planes<3, NP>(Ro[s], vo, acc);
           }
-          const float hi = tab.chi[L - 1] - tab.chi[16 * J + n], lo = tab.clo[L - 1] - tab.clo[16 * J + n];
-          const float ej = exp2_(hi + lo), dj = tab.d[16 * J + n];
-          double dot_b = 0.0;
+          const float ej = tab.w[16 * J + n], dj = tab.d[16 * J + n];
+          part[J] = 0.0;
           float kv[4];
           lds_vals4<NP>(sk + (16 * J + n) * STK + 16 * (mk + p) + 4 * g, L * STK, kv);
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
             acc[r] *= ej;
-            dot_b = __builtin_fma((double)kv[r], (double)acc[r], dot_b);
+            part[J] = __builtin_fma((double)kv[r], (double)acc[r], part[J]);
             dki[p][J][r] = __builtin_fmaf(dj, acc[r], dki[p][J][r]);
           }
-          dot_b = group_sum64(dot_b);
-          if (g == 0) bp[mk + p][16 * J + n] = dot_b;
         }
+        put_group_sums<NI>(bp[mk + p], part, g, n);
       }
       if (hasdq) {
         uint4 Ho[VS][3];
 #pragma unroll
         for (int s = 0; s < VS; ++s) split3x8(x[s], Ho[s]);
+        double part[NI];
 #pragma unroll
         for (int I = 0; I < NI; ++I) {
           f32x4 acc = {0, 0, 0, 0};
@@ -983,18 +982,17 @@ __global__ void __launch_bounds__(64 * kSsmBwdWaves, KP == 128 ? 1 : 2) m2rnn_ss
             acc = mfma_planes<3, 3>(Ho[s], uo, acc);
           }
           const float e = tab.e[16 * I + n];
-          double dot_a = 0.0;
+          part[I] = 0.0;
           float qf[4];
           planes_vals4<NP>(qv[p][I], qf);
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
             acc[r] *= e;
-            dot_a = __builtin_fma((double)qf[r], (double)acc[r], dot_a);
+            part[I] = __builtin_fma((double)qf[r], (double)acc[r], part[I]);
             dqi[p][I][r] += acc[r];
           }
-          dot_a = group_sum64(dot_a);
-          if (g == 0) ap[mq + p][16 * I + n] = dot_a;
         }
+        put_group_sums<NI>(ap[mq + p], part, g, n);
       }
     }
     if (w == NW - 1 && cb == CB - 1 && blk + 1 < blocks) tables(head + 1, tabs[(blk / CB + 1) & 1]);
@@ -1025,8 +1023,8 @@ __global__ void __launch_bounds__(64 * kSsmBwdWaves, KP == 128 ? 1 : 2) m2rnn_ss
       dsum += col + bb;
       if (cb == CB - 1) {
         const bool live = t < L && t0 + t < Tb;
-        const float z = (live ? A.a[(row0 + t) * N + head] : 0.0f) + A.beta[head];
-        const float da = live ? (float)(dsum - (double)A.alpha[head] * gsum) / (1.0f + expf(-z)) : 0.0f;
+        // sigma(z) = 1 - e^{-softplus(z)}
+        const float da = live ? (float)(dsum - (double)A.alpha[head] * gsum) * -expm1f(-(float)delta64) : 0.0f;
         if (t < L && t0 + t < T) A.da[(row0 + t) * N + head] = da;
         const double sb = prefix64(da), sa = prefix64(live ? -delta64 * gsum : 0.0);
         if (lane == 63) {
@@ -1074,6 +1072,448 @@ __global__ void __launch_bounds__(64 * kSsmBwdWaves, KP == 128 ? 1 : 2) m2rnn_ss
         split3x4(bv, h1);
 #pragma unroll
         for (int i = 0; i < 3; ++i) xo[s][i] = cat(h0[i], h1[i]);
+      }
+      float* out = (which ? A.dk : A.dq) + plane;
+      const int t = t0 + 16 * own + n;
+#pragma unroll
+      for (int m = 0; m < KM; ++m) {
+        const float4 t4 = *(const float4*)(ex + (16 * own + n) * KP + 16 * m + 4 * g);
+        f32x4 acc = {t4.x, t4.y, t4.z, t4.w};
+#pragma unroll
+        for (int s = 0; s < NS; ++s) {
+          uint4 ko[NP];
+#pragma unroll
+          for (int i = 0; i < NP; ++i) ko[i] = lds_col((which ? sq : sk) + i * L * STK, STK, 32 * s, 16 * m, g, n);
+          acc = mfma_planes<NP, 3>(ko, xo[s], acc);
+        }
+        const int kk = 16 * m + 4 * g;
+        if (t < T && kk < K)
+          *(float4*)(out + ((long)b * T + t) * krow + (long)grp * K + kk) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+      }
+    }
+    if (which == 0) __syncthreads();
+  }
+}
+
+// ------------------------------------------------------------------ backward of narrow heads
+
+// The operand with 16 contraction slots (four values a lane): products over the 16 value columns.
+template <int NA, int NB>
+__device__ __forceinline__ f32x4 mfma16_planes(const uint2 (&A)[NA], const uint2 (&B)[NB], f32x4 acc) {
+#pragma unroll
+  for (int s = 2; s >= 0; --s)
+#pragma unroll
+    for (int i = 0; i < NA; ++i) {
+      const int j = s - i;
+      if (j >= 0 && j < NB) acc = mfma16_bf16(A[i], B[j], acc);
+    }
+  return acc;
+}
+template <int NA, int NB>
+__device__ __forceinline__ f32x4 mfma16_planes_turned(const uint2 (&A)[NA], const uint2 (&B)[NB], f32x4 acc) {
+#pragma unroll
+  for (int s = 2; s >= 0; --s)
+#pragma unroll
+    for (int j = 0; j < NB; ++j) {
+      const int i = s - j;
+      if (i >= 0 && i < NA) acc = mfma16_bf16(A[i], B[j], acc);
+    }
+  return acc;
+}
+
+// The backward of one chunk for heads of 16 value columns (mathematics: m2rnn_ssm_bwd_kernel above), which
+// usually share a query/key: the walk over the heads is what counts, so everything in it runs one
+// head ahead.  A wave owns the same 16 steps as rows and as columns; with 16 value columns it forms
+// its dv tile from its own P, so nothing is exchanged within a head: v, dy and R of the next head
+// go to the other half of a double buffer while this one is computed, one barrier a head.  Wave 3
+// forms the next head's decay tables, wave 0 finishes the previous head's da, meanwhile.  R is read
+// once, as planes in LDS that serve as R (transposing reads) and as R^T; H goes straight into the
+// operand of the wave that owns its 16 K rows.  X is summed over the heads in registers.
+template <bool BF16, int KP>
+__global__ void __launch_bounds__(64 * kSsmBwdWaves, KP == 128 ? 1 : 2) m2rnn_ssm_bwd_narrow_kernel(SsmArgs A) {
+  constexpr int L = ssm_chunk<BF16>(), NI = L / 16, NS = L / 32, KS = KP / 32, KM = KP / 16, NP = BF16 ? 1 : 3;
+  constexpr int NW = kSsmBwdWaves, NTH = 64 * NW, V = 16;
+  constexpr int STK = ssm_stride(KP), STV = ssm_stride(V), STR = ssm_stride(KP);
+  constexpr int MPW = KM >= NW ? KM / NW : 1;
+  constexpr int RP = (V * KP / 4 + NTH - 1) / NTH;                   // pieces of R (4 values) per thread
+  constexpr int OV = 0, OU = NP * L * STV, OR = OU + 3 * L * STV, BUF = OR + 3 * V * STR;  // one buffer, in elements
+  constexpr int POOL = 2 * BUF * 2 > L * KP * 4 ? 2 * BUF : L * KP * 2;
+  struct Small {
+    double row[L], col[L], a[KM][L], b[KM][L], rh[KM];
+    float dg[L], dw[NI][V];
+  };
+  __shared__ __attribute__((aligned(16))) uint16_t sk[NP * L * STK];
+  __shared__ __attribute__((aligned(16))) uint16_t sq[NP * L * STK];
+  __shared__ __attribute__((aligned(16))) uint16_t pool[POOL];  // the double buffer; at the end the exchange of dq, dk
+  __shared__ __attribute__((aligned(16))) SsmTab<L> tabs[3];
+  __shared__ Small small[2];
+
+  const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, n = lane & 15;
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  int unit, hs;
+  ssm_unit(A.HS, A.B * A.G * A.nch, unit, hs);
+  const int ch = unit % A.nch, bg = unit / A.nch;
+  const int b = bg / A.G, grp = bg % A.G;
+  const int K = A.K, T = A.T, N = A.N;
+  const int hpg = N / A.G, per = (hpg + A.HS - 1) / A.HS;
+  const int hb = grp * hpg + hs * per, he = min(grp * hpg + hpg, hb + per);
+  const int t0 = ch * L;
+  const int Tb = ssm_len(A, b);
+  const int rows = min(L, Tb - t0);
+  const long krow = (long)A.G * K, vrow = (long)N * V, row0 = (long)b * T + t0;
+  const int It = w, Jt = NI == 4 ? w : w - 2;
+  const bool hasI = It < NI, hasJ = Jt >= 0;
+  const bool hasdq = KM >= NW || w < KM, hasdk = KM >= NW || w >= NW - KM;
+  const int mq = KM >= NW ? w * MPW : w, mk = KM >= NW ? w * MPW : w - (NW - KM);
+  const int mh = hasdq ? mq : mk;  // the K tiles whose H this wave reads
+
+  SsmPieces<BF16, L, V, NTH> pv;
+  SsmPieces<false, L, V, NTH> pu;
+  float4 pr[RP], pi[RP];
+  float idec;
+  auto fetch = [&](int h) {  // v, dy, R of head h
+    const long off = row0 * vrow + (long)h * V;
+    pv.load(BF16 ? (const void*)((const uint16_t*)A.v + off) : (const void*)((const float*)A.v + off), vrow, V, rows, tid);
+    pu.load(A.dy + off, vrow, V, rows, tid);
+    const long pair = (long)b * N + h;
+    const float* Rp = A.rloc + (pair * A.nch + ch) * V * K;        // [V][K]
+    const float* Ip = A.seg + (pair * A.S + ch / A.cps) * V * K;   // [V][K]
+    idec = A.cdec[pair * A.nch + ch];
+#pragma unroll
+    for (int p = 0; p < RP; ++p) {
+      const int i = tid + p * NTH, c = i / (KP / 4), kk = (i % (KP / 4)) * 4;
+      pr[p] = pi[p] = make_float4(0, 0, 0, 0);
+      if (c < V && kk < K) {
+        pr[p] = *(const float4*)(Rp + (unsigned)(c * K + kk));
+        pi[p] = *(const float4*)(Ip + (unsigned)(c * K + kk));
+      }
+    }
+  };
+  auto stage = [&](uint16_t* buf) {
+    pv.store(buf + OV, tid);
+    pu.store(buf + OU, tid);
+    const float d = exp2_(idec);
+#pragma unroll
+    for (int p = 0; p < RP; ++p) {
+      const int i = tid + p * NTH, c = i / (KP / 4), kk = (i % (KP / 4)) * 4;
+      if (c < V) {
+        const float x[4] = {__builtin_fmaf(d, pi[p].x, pr[p].x), __builtin_fmaf(d, pi[p].y, pr[p].y),
+                            __builtin_fmaf(d, pi[p].z, pr[p].z), __builtin_fmaf(d, pi[p].w, pr[p].w)};
+        uint2 pl[3];
+        split3x4(x, pl);
+#pragma unroll
+        for (int q = 0; q < 3; ++q) *(uint2*)(buf + OR + (q * V + c) * STR + kk) = pl[q];
+      }
+    }
+  };
+  float4 ph[MPW];
+  auto fetch_H = [&](int h) {
+    const float* Hp = A.ckpt + (((long)b * N + h) * A.nch + ch) * K * V;  // [K][V]
+#pragma unroll
+    for (int p = 0; p < MPW; ++p) {
+      const int kk = 16 * (mh + p) + n;
+      ph[p] = make_float4(0, 0, 0, 0);
+      if (kk < K) ph[p] = *(const float4*)(Hp + (unsigned)(kk * V + 4 * g));
+    }
+  };
+  const bool live = lane < L && t0 + lane < Tb;
+  float pa = 0.0f;
+  auto fetch_a = [&](int h) { pa = live ? A.a[(row0 + lane) * N + h] : 0.0f; };
+  auto tables = [&](int h) {
+    float delta;
+    double lg;
+    ssm_gate(live, pa, A.alpha[h], A.beta[h], delta, lg);
+    ssm_tables<L, true, false, false>(tabs[(h - hb) % 3], lane, delta, lg);
+  };
+  // da, and the partial sums of dalpha, dbeta and dw_r, of a head whose products are done
+  auto finish = [&](int h) {
+    const Small& sm = small[(h - hb) & 1];
+    const SsmTab<L>& tab = tabs[(h - hb) % 3];
+    double row = 0.0, col = 0.0, diag = 0.0, aa = 0.0, bb = 0.0, through = 0.0;
+    float delta = 0.0f;
+    if (lane < L) {
+      row = sm.row[lane];
+      col = sm.col[lane];
+      diag = sm.dg[lane];
+      delta = tab.d[lane];
+#pragma unroll
+      for (int m = 0; m < KM; ++m) {
+        aa += sm.a[m][lane];
+        bb += sm.b[m][lane];
+      }
+    }
+#pragma unroll
+    for (int m = 0; m < KM; ++m) through += sm.rh[m];
+    through *= exp2((double)tab.chi[L - 1] + (double)tab.clo[L - 1]);
+    const double x = row - (double)delta * (col - diag) + aa, y = (double)delta * bb;
+    const double gs = __shfl(prefix64(__shfl(x, 63 - lane)), 63 - lane) + prefix64(dpp64<0x138, 0xF>(y)) + through;
+    // sigma(z) = 1 - e^{-softplus(z)}
+    const float da = live ? (float)(col + bb - (double)A.alpha[h] * gs) * -expm1f(-delta) : 0.0f;
+    if (lane < L && t0 + lane < T) A.da[(row0 + lane) * N + h] = da;
+    const double sb = prefix64(da), sa = prefix64(live ? -(double)delta * gs : 0.0);
+    if (lane == 63) {
+      float* o = A.part_gate + ((long)b * A.nch + ch) * 2 * N;
+      o[h] = (float)sb;
+      o[N + h] = (float)sa;
+    }
+    if (lane < V) {
+      float sum = 0.0f;
+#pragma unroll
+      for (int i = 0; i < NI; ++i) sum += sm.dw[i][lane];
+      A.part_wr[((long)b * A.nch + ch) * vrow + (long)h * V + lane] = sum;
+    }
+  };
+
+  if (hb < he) {
+    fetch(hb);
+    if (w == NW - 1) fetch_a(hb);
+  }
+  {
+    SsmPieces<BF16, L, KP, NTH> pq, pk;
+    const long off = row0 * krow + (long)grp * K;
+    pk.load(BF16 ? (const void*)((const uint16_t*)A.k + off) : (const void*)((const float*)A.k + off), krow, K, rows, tid);
+    pq.load(BF16 ? (const void*)((const uint16_t*)A.q + off) : (const void*)((const float*)A.q + off), krow, K, rows, tid);
+    pk.store(sk, tid);
+    pq.store(sq, tid);
+  }
+  if (hb < he) {
+    if (w == NW - 1) {
+      tables(hb);
+      if (hb + 1 < he) fetch_a(hb + 1);
+    }
+    stage(pool);
+    fetch_H(hb);
+    if (hb + 1 < he) fetch(hb + 1);
+  }
+  __syncthreads();
+  // q k^T of this wave's row and column tiles: the same for all heads
+  f32x4 qkr[NI], qkc[NI], xr[NI], xc[NI], dqi[MPW][NI], dki[MPW][NI];
+#pragma unroll
+  for (int i = 0; i < NI; ++i) {
+    qkr[i] = qkc[i] = xr[i] = xc[i] = f32x4{0, 0, 0, 0};
+#pragma unroll
+    for (int p = 0; p < MPW; ++p) dqi[p][i] = dki[p][i] = f32x4{0, 0, 0, 0};
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+      uint4 ko[NP], qo[NP];
+      if (hasI && i <= It) {
+#pragma unroll
+        for (int p = 0; p < NP; ++p) {
+          ko[p] = lds_row(sk + p * L * STK, STK, 16 * i, 32 * s, g, n);
+          qo[p] = lds_row(sq + p * L * STK, STK, 16 * It, 32 * s, g, n);
+        }
+        qkr[i] = mfma_planes<NP, NP>(ko, qo, qkr[i]);
+      }
+      if (hasJ && i >= Jt) {
+#pragma unroll
+        for (int p = 0; p < NP; ++p) {
+          ko[p] = lds_row(sk + p * L * STK, STK, 16 * Jt, 32 * s, g, n);
+          qo[p] = lds_row(sq + p * L * STK, STK, 16 * i, 32 * s, g, n);
+        }
+        qkc[i] = mfma_planes_turned<NP, NP>(qo, ko, qkc[i]);
+      }
+    }
+  }
+
+  for (int h = hb; h < he; ++h) {
+    const int it = h - hb;
+    const SsmTab<L>& tab = tabs[it % 3];
+    Small& sm = small[it & 1];
+    uint16_t* const buf = pool + (it & 1) * BUF;
+    const uint16_t *sv = buf + OV, *su = buf + OU, *sr = buf + OR;
+    const int n = fresh(lane & 15), g = fresh(lane >> 4);  // (addresses formed per head, not held across them)
+    if (w == 0 && h > hb) finish(h - 1);
+
+    // rows It: X and the row sums of M
+    if (hasI) {
+      uint2 uo[3];
+#pragma unroll
+      for (int i = 0; i < 3; ++i) uo[i] = *(const uint2*)(su + (i * L + 16 * It + n) * STV + 4 * g);
+      double row = 0.0;
+#pragma unroll
+      for (int J = 0; J < NI; ++J) {
+        if (J > It) continue;
+        uint2 vo[NP];
+#pragma unroll
+        for (int i = 0; i < NP; ++i) vo[i] = *(const uint2*)(sv + (i * L + 16 * J + n) * STV + 4 * g);
+        const f32x4 uv = mfma16_planes<NP, 3>(vo, uo, f32x4{0, 0, 0, 0});
+        float d[4];
+        ssm_decay<L, false>(tab, It, J, g, n, d);
+        const float4 dj = *(const float4*)&tab.d[16 * J + 4 * g];
+        const float dl[4] = {dj.x, dj.y, dj.z, dj.w};
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const float x0 = uv[r] * d[r], m = x0 * qkr[J][r];
+          xr[J][r] = __builtin_fmaf(x0, dl[r], xr[J][r]);
+          const bool diag = It == J && 4 * g + r == n;
+          if (diag) sm.dg[16 * It + n] = m;
+          row = __builtin_fma((double)(diag ? 0.0f : m), (double)dl[r], row);
+        }
+      }
+      row = group_sum64(row);
+      if (g == 0) sm.row[16 * It + n] = row;
+    }
+    // columns Jt: X, P and the column sums of M, and dv
+    if (hasJ) {
+      uint2 vo[NP], pl[NI][3];
+#pragma unroll
+      for (int i = 0; i < NP; ++i) vo[i] = *(const uint2*)(sv + (i * L + 16 * Jt + n) * STV + 4 * g);
+      const float dj = tab.d[16 * Jt + n];
+      double col = 0.0;
+#pragma unroll
+      for (int I = 0; I < NI; ++I) {
+#pragma unroll
+        for (int i = 0; i < 3; ++i) pl[I][i] = make_uint2(0, 0);
+        if (I < Jt) continue;
+        uint2 uo[3];
+#pragma unroll
+        for (int i = 0; i < 3; ++i) uo[i] = *(const uint2*)(su + (i * L + 16 * I + n) * STV + 4 * g);
+        const f32x4 uv = mfma16_planes_turned<3, NP>(uo, vo, f32x4{0, 0, 0, 0});
+        float d[4], pp[4];
+        ssm_decay_col<L>(tab, I, Jt, g, n, d);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const float x0 = uv[r] * d[r], m = x0 * qkc[I][r];
+          xc[I][r] = __builtin_fmaf(x0, dj, xc[I][r]);
+          pp[r] = qkc[I][r] * d[r];
+          col += (double)m;
+        }
+        split3x4(pp, pl[I]);
+      }
+      col = group_sum64(col);
+      if (g == 0) sm.col[16 * Jt + n] = col;
+      // dv^T: the value columns, steps Jt
+      f32x4 acc = {0, 0, 0, 0};
+#pragma unroll
+      for (int s = 0; s < KS; ++s) {
+        uint4 ko[NP], ro[3];
+#pragma unroll
+        for (int i = 0; i < NP; ++i) ko[i] = lds_row(sk + i * L * STK, STK, 16 * Jt, 32 * s, g, n);
+#pragma unroll
+        for (int i = 0; i < 3; ++i) ro[i] = lds_row(sr + i * V * STR, STR, 0, 32 * s, g, n);
+        acc = mfma_planes<3, NP>(ro, ko, acc);
+      }
+      const float ej = tab.w[16 * Jt + n];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) acc[r] *= ej;
+#pragma unroll
+      for (int s = 0; s < NS; ++s) {
+        if (2 * s + 1 < Jt) continue;
+        uint4 uo[3], po[3];
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+          uo[i] = lds_col(su + i * L * STV, STV, 32 * s, 0, g, n);
+          po[i] = cat(pl[2 * s][i], pl[2 * s + 1][i]);
+        }
+        acc = mfma_planes<3, 3>(uo, po, acc);
+      }
+      float uj[4], vj[4];
+      lds_vals4<3>(su + (16 * Jt + n) * STV + 4 * g, L * STV, uj);
+      lds_vals4<NP>(sv + (16 * Jt + n) * STV + 4 * g, L * STV, vj);
+      const float4 wr = *(const float4*)(A.w_r + (long)h * V + 4 * g);
+      const int t = t0 + 16 * Jt + n;
+      if (t < T)
+        *(float4*)(A.dv + ((long)b * T + t) * vrow + (long)h * V + 4 * g) =
+            make_float4(dj * acc[0] + wr.x * uj[0], dj * acc[1] + wr.y * uj[1], dj * acc[2] + wr.z * uj[2],
+                        dj * acc[3] + wr.w * uj[3]);
+      const float sum = row16_sum4(uj[0] * vj[0], uj[1] * vj[1], uj[2] * vj[2], uj[3] * vj[3], lane);
+      if ((n & 3) == 0) sm.dw[Jt][4 * g + (n >> 2)] = sum;
+    }
+    // the terms of H and R: rows kk of this wave's K tiles, columns i (j)
+#pragma unroll
+    for (int p = 0; p < MPW; ++p) {
+      const float hx[4] = {ph[p].x, ph[p].y, ph[p].z, ph[p].w};
+      if (hasdk) {
+        uint2 ro[3];
+#pragma unroll
+        for (int i = 0; i < 3; ++i) ro[i] = lds_col16(sr + i * V * STR, STR, 0, 16 * (mk + p), g, n);
+        float rx[4];
+        planes_vals4<3>(ro, rx);
+        double dot = 0.0;  // <R, H>: every step of the chunk gets it, so its error would add up in dalpha and dbeta
+#pragma unroll
+        for (int e = 0; e < 4; ++e) dot = __builtin_fma((double)hx[e], (double)rx[e], dot);
+        dot = prefix64(dot);
+        if (lane == 63) sm.rh[mk + p] = dot;
+        double part[NI];
+#pragma unroll
+        for (int J = 0; J < NI; ++J) {
+          uint2 vo[NP];
+#pragma unroll
+          for (int i = 0; i < NP; ++i) vo[i] = *(const uint2*)(sv + (i * L + 16 * J + n) * STV + 4 * g);
+          f32x4 acc = mfma16_planes<3, NP>(ro, vo, f32x4{0, 0, 0, 0});
+          const float ej = tab.w[16 * J + n], dj = tab.d[16 * J + n];
+          float kv[4];
+          lds_vals4<NP>(sk + (16 * J + n) * STK + 16 * (mk + p) + 4 * g, L * STK, kv);
+          part[J] = 0.0;
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            acc[r] *= ej;
+            part[J] = __builtin_fma((double)kv[r], (double)acc[r], part[J]);
+            dki[p][J][r] = __builtin_fmaf(dj, acc[r], dki[p][J][r]);
+          }
+        }
+        put_group_sums<NI>(sm.b[mk + p], part, g, n);
+      }
+      if (hasdq) {
+        uint2 ho[3];
+        split3x4(hx, ho);
+        double part[NI];
+#pragma unroll
+        for (int I = 0; I < NI; ++I) {
+          uint2 uo[3];
+#pragma unroll
+          for (int i = 0; i < 3; ++i) uo[i] = *(const uint2*)(su + (i * L + 16 * I + n) * STV + 4 * g);
+          f32x4 acc = mfma16_planes<3, 3>(ho, uo, f32x4{0, 0, 0, 0});
+          const float e = tab.e[16 * I + n];
+          float qf[4];
+          lds_vals4<NP>(sq + (16 * I + n) * STK + 16 * (mq + p) + 4 * g, L * STK, qf);
+          part[I] = 0.0;
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            acc[r] *= e;
+            part[I] = __builtin_fma((double)qf[r], (double)acc[r], part[I]);
+            dqi[p][I][r] += acc[r];
+          }
+        }
+        put_group_sums<NI>(sm.a[mq + p], part, g, n);
+      }
+    }
+    if (h + 1 < he) {
+      if (w == NW - 1) {
+        tables(h + 1);
+        if (h + 2 < he) fetch_a(h + 2);
+      }
+      stage(pool + ((it + 1) & 1) * BUF);
+      fetch_H(h + 1);
+      if (h + 2 < he) fetch(h + 2);
+    }
+    __syncthreads();
+  }
+  if (w == 0 && hb < he) finish(he - 1);
+
+  // dq and dk: X of all heads times k and q, by step tiles, plus the terms of H and R, by K tiles, through LDS
+  float* const ex = (float*)pool;  // [L][KP]
+  const long plane = (long)hs * A.B * T * krow;
+#pragma unroll
+  for (int which = 0; which < 2; ++which) {
+    if (which ? hasdk : hasdq) {
+#pragma unroll
+      for (int p = 0; p < MPW; ++p)
+#pragma unroll
+        for (int I = 0; I < NI; ++I) {
+          const f32x4& t = which ? dki[p][I] : dqi[p][I];
+          *(float4*)(ex + (16 * I + n) * KP + 16 * ((which ? mk : mq) + p) + 4 * g) = make_float4(t[0], t[1], t[2], t[3]);
+        }
+    }
+    __syncthreads();
+    if (which ? hasJ : hasI) {
+      const int own = which ? Jt : It;
+      uint4 xo[NS][3];
+#pragma unroll
+      for (int s = 0; s < NS; ++s) {
+        const f32x4 &a4 = which ? xc[2 * s] : xr[2 * s], &b4 = which ? xc[2 * s + 1] : xr[2 * s + 1];
+        const float x8[8] = {a4[0], a4[1], a4[2], a4[3], b4[0], b4[1], b4[2], b4[3]};
+        split3x8(x8, xo[s]);
       }
       float* out = (which ? A.dk : A.dq) + plane;
       const int t = t0 + 16 * own + n;

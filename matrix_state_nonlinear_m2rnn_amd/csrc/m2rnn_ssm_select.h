@@ -36,7 +36,7 @@ const void* ssm_pick_bwd_kv(bool one) {
 }
 template <bool BF16, int KP>
 const void* ssm_pick_bwd_k(int VB, bool one) {
-  if (VB == 16) return ssm_pick_bwd_kv<BF16, KP, 16>(one);
+  if (VB == 16) return (const void*)&m2rnn_ssm_bwd_narrow_kernel<BF16, KP>;
   if (VB == 32) return ssm_pick_bwd_kv<BF16, KP, 32>(one);
   return ssm_pick_bwd_kv<BF16, KP, 64>(one);
 }
