@@ -538,11 +538,23 @@ __global__ void __launch_bounds__(256) m2rnn_ssm_combine_kernel(SsmArgs A) {
   float carry = first ? first[pair * KV + at] : 0.0f;
   float* p = A.seg + pair * A.S * KV + e;
   const float* d = A.segdec + pair * A.S;
-  for (int i = 0; i < A.S; ++i) {
-    const int s = REV ? A.S - 1 - i : i;
-    const float own = p[s * KV];
-    p[s * KV] = carry;
-    carry = __builtin_fmaf(exp2_(d[s]), carry, own);
+  // the segments' parts do not depend on the carry: eight of them in flight at a time
+  for (int i = 0; i < A.S; i += 8) {
+    float own[8], dec[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int s = REV ? A.S - 1 - i - j : i + j;
+      own[j] = i + j < A.S ? p[s * KV] : 0.0f;
+      dec[j] = i + j < A.S ? d[s] : 0.0f;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int s = REV ? A.S - 1 - i - j : i + j;
+      if (i + j < A.S) {
+        p[s * KV] = carry;
+        carry = __builtin_fmaf(exp2_(dec[j]), carry, own[j]);
+      }
+    }
   }
   if (REV && A.dH0) A.dH0[pair * KV + at] = carry;
 }
@@ -662,12 +674,17 @@ __global__ void __launch_bounds__(64 * kSsmBwdWaves, KP == 128 ? 1 : 2) m2rnn_ss
     pu.load(A.dy + off, vrow, VB, rows, tid);
   };
   // wave NW - 1 forms the tables of head h (its lanes: the chunk's steps)
-  auto tables = [&](int h, SsmTab<L>& tab) {
-    const bool live = lane < L && t0 + lane < Tb;
-    const float a = live ? A.a[(row0 + lane) * N + h] : 0.0f;
+  const bool live = lane < L && t0 + lane < Tb;
+  float pa = 0.0f, alpha = 0.0f, beta = 0.0f;
+  auto fetch_a = [&](int h) {
+    pa = live ? A.a[(row0 + lane) * N + h] : 0.0f;
+    alpha = A.alpha[h];
+    beta = A.beta[h];
+  };
+  auto tables = [&](SsmTab<L>& tab) {
     float delta;
     double lg;
-    ssm_gate(live, a, A.alpha[h], A.beta[h], delta, lg);
+    ssm_gate(live, pa, alpha, beta, delta, lg);
     ssm_tables<L, true, false, false>(tab, lane, delta, lg);
   };
   SsmPieces<BF16, L, KP, NTH> pq;
@@ -676,17 +693,82 @@ __global__ void __launch_bounds__(64 * kSsmBwdWaves, KP == 128 ? 1 : 2) m2rnn_ss
     pq.load(BF16 ? (const void*)((const uint16_t*)A.q + off) : (const void*)((const float*)A.q + off), krow, K, rows,
             tid);
   };
-  if (blocks > 0) fetch(0);
+  // H and R as this wave's products take them: R^T for dv (rows c, contraction kk), H and R for dq and dk (rows
+  // kk, contraction c)
+  float4 tR[KS][2], tI[KS][2];
+  float hx[MPW][VS][8], rx[MPW][VS][8], ix[MPW][VS][8], idec;
+  auto fetch_RT = [&](int blk) {
+    const long pair = (long)b * N + hb + blk / CB;
+    const int cb = blk % CB;
+    const float* Rp = A.rloc + ((pair * A.nch + ch) * V + cb * VB) * K;        // [V][K]
+    const float* Ip = A.seg + ((pair * A.S + ch / A.cps) * V + cb * VB) * K;   // [V][K]
+    idec = A.cdec[pair * A.nch + ch];
+#pragma unroll
+    for (int s = 0; s < KS; ++s)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int kk = 32 * s + 8 * g + 4 * h;
+        tR[s][h] = tI[s][h] = make_float4(0, 0, 0, 0);
+        if (hasv && kk < K) {
+          tR[s][h] = *(const float4*)(Rp + (unsigned)((16 * mv + n) * K + kk));
+          tI[s][h] = *(const float4*)(Ip + (unsigned)((16 * mv + n) * K + kk));
+        }
+      }
+  };
+  auto fetch_HR = [&](int blk) {
+    const long pair = (long)b * N + hb + blk / CB;
+    const int cb = blk % CB;
+    const float* Hp = A.ckpt + (pair * A.nch + ch) * K * V + cb * VB;          // [K][V]
+    const float* Rp = A.rloc + ((pair * A.nch + ch) * V + cb * VB) * K;        // [V][K]
+    const float* Ip = A.seg + ((pair * A.S + ch / A.cps) * V + cb * VB) * K;   // [V][K]
+#pragma unroll
+    for (int p = 0; p < MPW; ++p)
+#pragma unroll
+      for (int s = 0; s < VS; ++s) {
+        const int c = 32 * s + 8 * g, kr = 16 * (mk + p) + n;
+        const int kk = hasdq ? 16 * (mq + p) + n : kr;  // two K tiles: the waves of dk take H for <R, H>
+#pragma unroll
+        for (int e = 0; e < 8; ++e) hx[p][s][e] = rx[p][s][e] = ix[p][s][e] = 0.0f;
+        if ((hasdq || KM < NW) && kk < K && c < VB) {
+          const float4 a4 = *(const float4*)(Hp + (unsigned)(kk * V + c)), b4 = *(const float4*)(Hp + (unsigned)(kk * V + c + 4));
+          hx[p][s][0] = a4.x; hx[p][s][1] = a4.y; hx[p][s][2] = a4.z; hx[p][s][3] = a4.w;
+          hx[p][s][4] = b4.x; hx[p][s][5] = b4.y; hx[p][s][6] = b4.z; hx[p][s][7] = b4.w;
+        }
+        if (hasdk && kr < K && c < VB) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            rx[p][s][e] = Rp[(unsigned)((c + e) * K + kr)];
+            ix[p][s][e] = Ip[(unsigned)((c + e) * K + kr)];
+          }
+        }
+      }
+  };
+  float4 wr = make_float4(0, 0, 0, 0);
+  auto fetch_wr = [&](int blk) {
+    if (hasv) wr = *(const float4*)(A.w_r + (long)(hb + blk / CB) * V + (blk % CB) * VB + 16 * mv + 4 * g);
+  };
+  const bool tabler = w == NW - 1 && blocks > 0;
+  if (tabler) fetch_a(hb);
   {
     SsmPieces<BF16, L, KP, NTH> pk;
     const long off = row0 * krow + (long)grp * K;
     pk.load(BF16 ? (const void*)((const uint16_t*)A.k + off) : (const void*)((const float*)A.k + off), krow, K, rows,
             tid);
     fetch_q();
+    if (blocks > 0) fetch(0);
+    if (ONE) {  // in flight until the products take them
+      fetch_RT(0);
+      fetch_HR(0);
+      fetch_wr(0);
+    }
+    if (tabler) tables(tabs[0]);
     pk.store(sk, tid);
     pq.store(sq, tid);
+    if (ONE) {
+      pv.store(sv, tid);
+      pu.store(su, tid);
+    }
   }
-  if (w == NW - 1 && blocks > 0) tables(hb, tabs[0]);
   __syncthreads();
   // q k^T of this wave's row and column tiles, and q of its entering terms' rows: the same for all heads
   f32x4 qkr[NI], qkc[NI];
@@ -740,18 +822,68 @@ __global__ void __launch_bounds__(64 * kSsmBwdWaves, KP == 128 ? 1 : 2) m2rnn_ss
   // wave 0, lane t: what g and dD hold of the head's column blocks done so far
   double gsum = 0.0, dsum = 0.0;
 
+  // da, and the partial sums of dalpha, dbeta and dw_r, of a block whose products are done
+  auto finish = [&](int blk) {
+    const int head = hb + blk / CB, cb = blk % CB;
+    const SsmTab<L>& tab = tabs[(blk / CB) & 1];
+    if (w == 0) {
+      const int t = lane;
+      double row = 0.0, col = 0.0, diag = 0.0, aa = 0.0, bb = 0.0, through = 0.0, delta64 = 0.0;
+      if (t < L) {
+        row = rowp[t];
+        col = colp[t];
+        diag = dgp[t];
+        delta64 = tab.d[t];
+#pragma unroll
+        for (int m = 0; m < KM; ++m) {
+          aa += ap[m][t];
+          bb += bp[m][t];
+        }
+      }
+#pragma unroll
+      for (int m = 0; m < KM; ++m) through += rh[m];
+      through *= exp2((double)tab.chi[L - 1] + (double)tab.clo[L - 1]);
+      const double x = row - delta64 * (col - diag) + aa, y = delta64 * bb;
+      // sum over i >= t of x, sum over j < t of y, each without a subtraction that would leave a residue
+      const double sx64 = __shfl(prefix64(__shfl(x, 63 - lane)), 63 - lane);
+      gsum += sx64 + prefix64(dpp64<0x138, 0xF>(y)) + through;
+      dsum += col + bb;
+      if (cb == CB - 1) {
+        // sigma(z) = 1 - e^{-softplus(z)}
+        const float da = live ? (float)(dsum - (double)A.alpha[head] * gsum) * -expm1f(-(float)delta64) : 0.0f;
+        if (t < L && t0 + t < T) A.da[(row0 + t) * N + head] = da;
+        const double sb = prefix64(da), sa = prefix64(live ? -delta64 * gsum : 0.0);
+        if (lane == 63) {
+          float* o = A.part_gate + ((long)b * A.nch + ch) * 2 * N;
+          o[head] = (float)sb;
+          o[N + head] = (float)sa;
+        }
+        gsum = dsum = 0.0;
+      }
+    } else if (w == 1 && lane < VB) {
+      float sum = 0.0f;
+#pragma unroll
+      for (int i = 0; i < NI; ++i) sum += dwp[i][lane];
+      A.part_wr[((long)b * A.nch + ch) * vrow + (long)head * V + cb * VB + lane] = sum;
+    }
+  };
+
   for (int blk = 0; blk < blocks; ++blk) {
     const int head = hb + blk / CB, cb = blk % CB;
     const long pair = (long)b * N + head;
     const SsmTab<L>& tab = tabs[(blk / CB) & 1];
-    __syncthreads();  // the previous block's reads are done
-    g = fresh(g);
-    n = fresh(n);
-    tid = fresh(tid);
-    pv.store(sv, tid);
-    pu.store(su, tid);
-    __syncthreads();
-    if (AHEAD && blk + 1 < blocks) fetch(blk + 1);
+    if (!ONE) {
+      __syncthreads();  // the previous block's reads are done
+      g = fresh(g);
+      n = fresh(n);
+      tid = fresh(tid);
+      pv.store(sv, tid);
+      pu.store(su, tid);
+      __syncthreads();
+      if (AHEAD && blk + 1 < blocks) fetch(blk + 1);
+      fetch_wr(blk);
+      if (tabler && cb == CB - 1 && blk + 1 < blocks) fetch_a(head + 1);
+    }
 
     // rows It: X and the row sums of M
     if (hasI) {
@@ -790,6 +922,7 @@ __global__ void __launch_bounds__(64 * kSsmBwdWaves, KP == 128 ? 1 : 2) m2rnn_ss
     }
     g = fresh(g);
     n = fresh(n);
+    if (ONE) __syncthreads();  // q has been read: P takes its place
     // columns Jt: X, P and the column sums of M
     if (hasJ) {
       uint4 vo[VS][NP];
@@ -830,10 +963,8 @@ __global__ void __launch_bounds__(64 * kSsmBwdWaves, KP == 128 ? 1 : 2) m2rnn_ss
     }
     __syncthreads();
 
-    const float* Hp = A.ckpt + (pair * A.nch + ch) * K * V + cb * VB;          // [K][V]
-    const float* Rp = A.rloc + ((pair * A.nch + ch) * V + cb * VB) * K;        // [V][K]
-    const float* Ip = A.seg + ((pair * A.S + ch / A.cps) * V + cb * VB) * K;   // [V][K]
-    const float idec = exp2_(A.cdec[pair * A.nch + ch]);
+    if (!ONE) fetch_RT(blk);
+    const float dec = exp2_(idec);
     g = fresh(g);
     n = fresh(n);
     if (hasv) {
@@ -841,21 +972,11 @@ __global__ void __launch_bounds__(64 * kSsmBwdWaves, KP == 128 ? 1 : 2) m2rnn_ss
       uint4 Ro[KS][3];
 #pragma unroll
       for (int s = 0; s < KS; ++s) {
-        float x[8];
-        const int kk = 32 * s + 8 * g;
-        const unsigned at = (unsigned)((16 * mv + n) * K + kk);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          float4 a4 = make_float4(0, 0, 0, 0), i4 = a4;
-          if (kk + 4 * h < K) {
-            a4 = *(const float4*)(Rp + at + 4 * h);
-            i4 = *(const float4*)(Ip + at + 4 * h);
-          }
-          x[4 * h + 0] = __builtin_fmaf(idec, i4.x, a4.x);
-          x[4 * h + 1] = __builtin_fmaf(idec, i4.y, a4.y);
-          x[4 * h + 2] = __builtin_fmaf(idec, i4.z, a4.z);
-          x[4 * h + 3] = __builtin_fmaf(idec, i4.w, a4.w);
-        }
+        const float x[8] = {
+            __builtin_fmaf(dec, tI[s][0].x, tR[s][0].x), __builtin_fmaf(dec, tI[s][0].y, tR[s][0].y),
+            __builtin_fmaf(dec, tI[s][0].z, tR[s][0].z), __builtin_fmaf(dec, tI[s][0].w, tR[s][0].w),
+            __builtin_fmaf(dec, tI[s][1].x, tR[s][1].x), __builtin_fmaf(dec, tI[s][1].y, tR[s][1].y),
+            __builtin_fmaf(dec, tI[s][1].z, tR[s][1].z), __builtin_fmaf(dec, tI[s][1].w, tR[s][1].w)};
         split3x8(x, Ro[s]);
       }
       uint4 uo[NS][3];
@@ -863,9 +984,6 @@ __global__ void __launch_bounds__(64 * kSsmBwdWaves, KP == 128 ? 1 : 2) m2rnn_ss
       for (int s = 0; s < NS; ++s)
 #pragma unroll
         for (int i = 0; i < 3; ++i) uo[s][i] = lds_col(su + i * L * STV, STV, 32 * s, 16 * mv, g, n);
-      float wr[4];
-#pragma unroll
-      for (int r = 0; r < 4; ++r) wr[r] = A.w_r[(long)head * V + cb * VB + 16 * mv + 4 * g + r];
 #pragma unroll
       for (int p = 0; p < TPV; ++p) {
         const int J = jv0 + p;
@@ -898,45 +1016,29 @@ __global__ void __launch_bounds__(64 * kSsmBwdWaves, KP == 128 ? 1 : 2) m2rnn_ss
         const int t = t0 + 16 * J + n;
         if (t < T)
           *(float4*)(A.dv + ((long)b * T + t) * vrow + (long)head * V + cb * VB + 16 * mv + 4 * g) =
-              make_float4(dj * acc[0] + wr[0] * uj[0], dj * acc[1] + wr[1] * uj[1], dj * acc[2] + wr[2] * uj[2],
-                          dj * acc[3] + wr[3] * uj[3]);
+              make_float4(dj * acc[0] + wr.x * uj[0], dj * acc[1] + wr.y * uj[1], dj * acc[2] + wr.z * uj[2],
+                          dj * acc[3] + wr.w * uj[3]);
         const float sum = row16_sum4(uj[0] * vj[0], uj[1] * vj[1], uj[2] * vj[2], uj[3] * vj[3], lane);
         if ((n & 3) == 0) dwp[J][16 * mv + 4 * g + (n >> 2)] = sum;
       }
     }
     g = fresh(g);
     n = fresh(n);
+    if (!ONE) fetch_HR(blk);
 #pragma unroll
     for (int p = 0; p < MPW; ++p) {
       // the terms of H and R: rows kk of this wave's K tiles, columns i (j)
-      float x[VS][8], y[VS][8];
+      float y[VS][8];
 #pragma unroll
-      for (int s = 0; s < VS; ++s) {
-        const int c = 32 * s + 8 * g, kq = 16 * (mq + p) + n, kr = 16 * (mk + p) + n;
+      for (int s = 0; s < VS; ++s)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[s][e] = y[s][e] = 0.0f;
-        if ((hasdq || KM < NW) && c < VB) {
-          const int kk = hasdq ? kq : kr;  // two K tiles: the waves of dk take H for <R, H>
-          if (kk < K) {
-            const float4 a4 = *(const float4*)(Hp + (unsigned)(kk * V + c)), b4 = *(const float4*)(Hp + (unsigned)(kk * V + c + 4));
-            x[s][0] = a4.x; x[s][1] = a4.y; x[s][2] = a4.z; x[s][3] = a4.w;
-            x[s][4] = b4.x; x[s][5] = b4.y; x[s][6] = b4.z; x[s][7] = b4.w;
-          }
-        }
-        if (hasdk && kr < K && c < VB) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const unsigned at = (unsigned)((c + e) * K + kr);
-            y[s][e] = __builtin_fmaf(idec, Ip[at], Rp[at]);
-          }
-        }
-      }
+        for (int e = 0; e < 8; ++e) y[s][e] = __builtin_fmaf(dec, ix[p][s][e], rx[p][s][e]);
       if (hasdk) {
         double dot = 0.0;  // <R, H>: every step of the chunk gets it, so its error would add up in dalpha and dbeta
 #pragma unroll
         for (int s = 0; s < VS; ++s)
 #pragma unroll
-          for (int e = 0; e < 8; ++e) dot = __builtin_fma((double)x[s][e], (double)y[s][e], dot);
+          for (int e = 0; e < 8; ++e) dot = __builtin_fma((double)hx[p][s][e], (double)y[s][e], dot);
         dot = prefix64(dot);
         if (lane == 63) rh[mk + p] = dot;
         uint4 Ro[VS][3];
@@ -969,7 +1071,7 @@ __global__ void __launch_bounds__(64 * kSsmBwdWaves, KP == 128 ? 1 : 2) m2rnn_ss
       if (hasdq) {
         uint4 Ho[VS][3];
 #pragma unroll
-        for (int s = 0; s < VS; ++s) split3x8(x[s], Ho[s]);
+        for (int s = 0; s < VS; ++s) split3x8(hx[p][s], Ho[s]);
         double part[NI];
 #pragma unroll
         for (int I = 0; I < NI; ++I) {
@@ -995,56 +1097,20 @@ __global__ void __launch_bounds__(64 * kSsmBwdWaves, KP == 128 ? 1 : 2) m2rnn_ss
         put_group_sums<NI>(ap[mq + p], part, g, n);
       }
     }
-    if (w == NW - 1 && cb == CB - 1 && blk + 1 < blocks) tables(head + 1, tabs[(blk / CB + 1) & 1]);
-    if (!AHEAD && blk + 1 < blocks) fetch(blk + 1);
-    __syncthreads();
-
-    if (w == 0) {
-      const int t = lane;
-      double row = 0.0, col = 0.0, diag = 0.0, aa = 0.0, bb = 0.0, through = 0.0, delta64 = 0.0;
-      if (t < L) {
-        row = rowp[t];
-        col = colp[t];
-        diag = dgp[t];
-        delta64 = tab.d[t];
-#pragma unroll
-        for (int m = 0; m < KM; ++m) {
-          aa += ap[m][t];
-          bb += bp[m][t];
-        }
-      }
-#pragma unroll
-      for (int m = 0; m < KM; ++m) through += rh[m];
-      through *= exp2((double)tab.chi[L - 1] + (double)tab.clo[L - 1]);
-      const double x = row - delta64 * (col - diag) + aa, y = delta64 * bb;
-      // sum over i >= t of x, sum over j < t of y, each without a subtraction that would leave a residue
-      const double sx64 = __shfl(prefix64(__shfl(x, 63 - lane)), 63 - lane);
-      gsum += sx64 + prefix64(dpp64<0x138, 0xF>(y)) + through;
-      dsum += col + bb;
-      if (cb == CB - 1) {
-        const bool live = t < L && t0 + t < Tb;
-        // sigma(z) = 1 - e^{-softplus(z)}
-        const float da = live ? (float)(dsum - (double)A.alpha[head] * gsum) * -expm1f(-(float)delta64) : 0.0f;
-        if (t < L && t0 + t < T) A.da[(row0 + t) * N + head] = da;
-        const double sb = prefix64(da), sa = prefix64(live ? -delta64 * gsum : 0.0);
-        if (lane == 63) {
-          float* o = A.part_gate + ((long)b * A.nch + ch) * 2 * N;
-          o[head] = (float)sb;
-          o[N + head] = (float)sa;
-        }
-        gsum = dsum = 0.0;
-      }
-    } else if (w == 1 && lane < VB) {
-      float sum = 0.0f;
-#pragma unroll
-      for (int i = 0; i < NI; ++i) sum += dwp[i][lane];
-      A.part_wr[((long)b * A.nch + ch) * vrow + (long)head * V + cb * VB + lane] = sum;
+    if (!ONE) {
+      if (tabler && cb == CB - 1 && blk + 1 < blocks) tables(tabs[(blk / CB + 1) & 1]);
+      if (!AHEAD && blk + 1 < blocks) fetch(blk + 1);
+      if (blk + 1 == blocks) fetch_q();
+      __syncthreads();
+      finish(blk);
     }
   }
 
   // dq and dk: X of all heads times k and q, by step tiles, plus the terms of H and R, by K tiles, through LDS
-  fetch_q();
-  __syncthreads();
+  if (ONE || blocks == 0) {
+    if (!ONE) fetch_q();
+    __syncthreads();
+  }
   pq.store(sq, tid);
   float* const ex = (float*)su;  // [L][KP]
   const long plane = (long)hs * A.B * T * krow;
@@ -1093,6 +1159,7 @@ __global__ void __launch_bounds__(64 * kSsmBwdWaves, KP == 128 ? 1 : 2) m2rnn_ss
     }
     if (which == 0) __syncthreads();
   }
+  if (ONE) finish(0);
 }
 
 // ------------------------------------------------------------------ backward of narrow heads
