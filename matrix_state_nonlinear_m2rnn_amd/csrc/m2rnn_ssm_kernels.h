@@ -137,7 +137,9 @@ __global__ void __launch_bounds__(HPW * VB * 4) m2rnn_ssm_fwd_kernel(SsmArgs A) 
   __shared__ __attribute__((aligned(16))) float4 gbuf[SHARE_G ? NT * 64 : 1];
   __shared__ __attribute__((aligned(16))) uint2 pbuf[SHARE_P ? SETS * 3 * 2 * 64 : 1];
 
-  const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, n = lane & 15;
+  int tid = threadIdx.x;
+  const int lane = tid & 63;
+  int g = lane >> 4, n = lane & 15;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
   int unit, share;
   ssm_unit(A.HB * A.CB, A.B * A.G * A.S, unit, share);
@@ -214,6 +216,9 @@ __global__ void __launch_bounds__(HPW * VB * 4) m2rnn_ssm_fwd_kernel(SsmArgs A) 
       continue;
     }
     __syncthreads();  // the previous chunk's reads are done
+    tid = fresh(tid);
+    g = fresh(g);
+    n = fresh(n);
     pq.store(sq, tid);
     pk.store(sk, tid);
     pv.store(sv, tid);
@@ -417,7 +422,9 @@ __global__ void __launch_bounds__(HPW * VB * 4) m2rnn_ssm_state_kernel(SsmArgs A
   __shared__ __attribute__((aligned(16))) SsmTab<L> tab[HPW];
   __shared__ float sdec[HPW];
 
-  const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, n = lane & 15;
+  int tid = threadIdx.x;
+  const int lane = tid & 63;
+  int g = lane >> 4, n = lane & 15;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
   int unit, share;
   ssm_unit(A.HB * A.CB, A.B * A.G * A.S, unit, share);
@@ -468,7 +475,10 @@ __global__ void __launch_bounds__(HPW * VB * 4) m2rnn_ssm_state_kernel(SsmArgs A
         if (preps && lane == 0 && cb == 0) A.cdec[((long)b * A.N + head) * A.nch + ch] = (float)dec;
       }
     }
-    __syncthreads();
+    __syncthreads();  // the previous chunk's reads are done
+    tid = fresh(tid);
+    g = fresh(g);
+    n = fresh(n);
     if (preps) {
       float delta;
       double lg;
