@@ -41,6 +41,12 @@ __device__ __forceinline__ int fresh(int x) {
   return x;
 }
 
+// The same for a wave-uniform number: comparisons with it are made here, not kept as lane masks.
+__device__ __forceinline__ int fresh_s(int x) {
+  asm volatile("" : "+s"(x));
+  return x;
+}
+
 __device__ __forceinline__ float exp2_(float x) { return __builtin_amdgcn_exp2f(x); }
 
 // x = hi + mid + lo exactly; the three bf16 are the high halves of the words.
@@ -132,12 +138,20 @@ __device__ __forceinline__ double dpp64(double x) {
   const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(u >> 32), CTRL, ROWS, 0xF, false);
   return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
 }
+// The same with every row written and zeros where a lane has no source.
+template <int CTRL>
+__device__ __forceinline__ double dpp64_all(double x) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, x);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_mov_dpp((int)(uint32_t)u, CTRL, 0xF, 0xF, true);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_mov_dpp((int)(uint32_t)(u >> 32), CTRL, 0xF, 0xF, true);
+  return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+}
 // Inclusive prefix sum over the wave's 64 lanes (row shifts, then the row totals broadcast on).
 __device__ __forceinline__ double prefix64(double x) {
-  x += dpp64<0x111, 0xF>(x);
-  x += dpp64<0x112, 0xF>(x);
-  x += dpp64<0x114, 0xF>(x);
-  x += dpp64<0x118, 0xF>(x);
+  x += dpp64_all<0x111>(x);
+  x += dpp64_all<0x112>(x);
+  x += dpp64_all<0x114>(x);
+  x += dpp64_all<0x118>(x);
   x += dpp64<0x142, 0xA>(x);
   x += dpp64<0x143, 0xC>(x);
   return x;
@@ -149,16 +163,6 @@ __device__ __forceinline__ double lane64(double x, int lane) {
   return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
 }
 
-// row16_sum4 in fp64: lane n of a row of 16 gets the row's sum of x_{(n >> 2) & 3}.
-__device__ __forceinline__ double row16_sum4_64(const double (&x)[4], int lane) {
-  const bool b3 = (lane & 8) != 0, b2 = (lane & 4) != 0;
-  const double a0 = (b3 ? x[2] : x[0]) + dpp64<kDppRowMirror, 0xF>(b3 ? x[0] : x[2]);
-  const double a1 = (b3 ? x[3] : x[1]) + dpp64<kDppRowMirror, 0xF>(b3 ? x[1] : x[3]);
-  double c = (b2 ? a1 : a0) + dpp64<kDppRowHalfMirror, 0xF>(b2 ? a0 : a1);
-  c += dpp64<kDppQuadXor1, 0xF>(c);
-  c += dpp64<kDppQuadXor2, 0xF>(c);
-  return c;
-}
 // The two words of each of two doubles exchanged between the wave's halves (32) or between the odd rows
 // of 16 of the first and the even rows of the second (16), and added.
 template <bool HALVES>
@@ -182,6 +186,15 @@ __device__ __forceinline__ double group_sum64(double x) {
 // Four such sums at once: lane group g gets the one of x[g].
 __device__ __forceinline__ double group_sum64_4(const double (&x)[4]) {
   return swap_add64<false>(swap_add64<true>(x[0], x[2]), swap_add64<true>(x[1], x[3]));
+}
+
+// Sum over the wave, in every lane (rotations within the rows of 16, then across them).
+__device__ __forceinline__ double total64(double x) {
+  x += dpp64_all<0x128>(x);
+  x += dpp64_all<0x124>(x);
+  x += dpp64_all<0x122>(x);
+  x += dpp64_all<0x121>(x);
+  return group_sum64(x);
 }
 
 // out[16 I + n] = the sum of x[I] over the lane groups.

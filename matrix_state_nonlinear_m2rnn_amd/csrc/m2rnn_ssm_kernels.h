@@ -667,7 +667,7 @@ __global__ void __launch_bounds__(64 * kSsmBwdWaves, KP == 128 ? 1 : 2) m2rnn_ss
 
   // this wave's tiles: rows It, columns Jt of the triangle (four tiles: one of each; two: waves 0, 1 the
   // rows, 2, 3 the columns), K tiles m0 .. m0 + MPW - 1 (with two: waves 0, 1 for dq, 2, 3 for dk)
-  const int It = NI == 4 ? w : w, Jt = NI == 4 ? w : w - 2;
+  int It = w, Jt = NI == 4 ? w : w - 2;
   const bool hasI = It < NI, hasJ = Jt >= 0;
   const bool hasdq = KM >= NW || w < KM, hasdk = KM >= NW || w >= NW - KM;
   const int mq = KM >= NW ? w * MPW : w, mk = KM >= NW ? w * MPW : w - (NW - KM);
@@ -890,6 +890,8 @@ __global__ void __launch_bounds__(64 * kSsmBwdWaves, KP == 128 ? 1 : 2) m2rnn_ss
       pv.store(sv, tid);
       pu.store(su, tid);
       __syncthreads();
+      It = fresh_s(It);
+      Jt = fresh_s(Jt);
       if (AHEAD && blk + 1 < blocks) fetch(blk + 1);
       fetch_wr(blk);
       if (tabler && cb == CB - 1 && blk + 1 < blocks) fetch_a(head + 1);
@@ -918,14 +920,23 @@ __global__ void __launch_bounds__(64 * kSsmBwdWaves, KP == 128 ? 1 : 2) m2rnn_ss
         ssm_decay<L, false>(tab, It, J, g, n, d);
         const float4 dj = *(const float4*)&tab.d[16 * J + 4 * g];
         const float dl[4] = {dj.x, dj.y, dj.z, dj.w};
+        float m[4];
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          const float x0 = uv[r] * d[r], m = x0 * qkr[J][r];
+          const float x0 = uv[r] * d[r];
+          m[r] = x0 * qkr[J][r];
           xr[J][r] = __builtin_fmaf(x0, dl[r], xr[J][r]);
-          const bool diag = It == J && 4 * g + r == n;
-          if (diag) dgp[16 * It + n] = m;
-          row = __builtin_fma((double)(diag ? 0.0f : m), (double)dl[r], row);
         }
+        if (It == J) {  // the diagonal apart
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            if (4 * g + r == n) {
+              dgp[16 * It + n] = m[r];
+              m[r] = 0.0f;
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < 4; ++r) row = __builtin_fma((double)m[r], (double)dl[r], row);
       }
       row = group_sum64(row);
       if (g == 0) rowp[16 * It + n] = row;
@@ -1049,8 +1060,8 @@ __global__ void __launch_bounds__(64 * kSsmBwdWaves, KP == 128 ? 1 : 2) m2rnn_ss
         for (int s = 0; s < VS; ++s)
 #pragma unroll
           for (int e = 0; e < 8; ++e) dot = __builtin_fma((double)hx[p][s][e], (double)y[s][e], dot);
-        dot = prefix64(dot);
-        if (lane == 63) rh[mk + p] = dot;
+        dot = total64(dot);
+        if (lane == 0) rh[mk + p] = dot;
         uint4 Ro[VS][3];
 #pragma unroll
         for (int s = 0; s < VS; ++s) split3x8(y[s], Ro[s]);
@@ -1066,15 +1077,16 @@ __global__ void __launch_bounds__(64 * kSsmBwdWaves, KP == 128 ? 1 : 2) m2rnn_ss
             acc = mfma_planes<3, NP>(Ro[s], vo, acc);
           }
           const float ej = tab.w[16 * J + n], dj = tab.d[16 * J + n];
-          part[J] = 0.0;
+          float dot4 = 0.0f;
           float kv[4];
           lds_vals4<NP>(sk + (16 * J + n) * STK + 16 * (mk + p) + 4 * g, L * STK, kv);
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
             acc[r] *= ej;
-            part[J] = __builtin_fma((double)kv[r], (double)acc[r], part[J]);
+            dot4 = __builtin_fmaf(kv[r], acc[r], dot4);
             dki[p][J][r] = __builtin_fmaf(dj, acc[r], dki[p][J][r]);
           }
+          part[J] = dot4;
         }
         put_group_sums<NI>(bp[mk + p], part, g, n);
       }
@@ -1094,15 +1106,16 @@ __global__ void __launch_bounds__(64 * kSsmBwdWaves, KP == 128 ? 1 : 2) m2rnn_ss
             acc = mfma_planes<3, 3>(Ho[s], uo, acc);
           }
           const float e = tab.e[16 * I + n];
-          part[I] = 0.0;
+          float dot4 = 0.0f;
           float qf[4];
           planes_vals4<NP>(qv[p][I], qf);
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
             acc[r] *= e;
-            part[I] = __builtin_fma((double)qf[r], (double)acc[r], part[I]);
+            dot4 = __builtin_fmaf(qf[r], acc[r], dot4);
             dqi[p][I][r] += acc[r];
           }
+          part[I] = dot4;
         }
         put_group_sums<NI>(ap[mq + p], part, g, n);
       }
@@ -1399,6 +1412,7 @@ __global__ void __launch_bounds__(64 * kSsmBwdWaves, KP == 128 ? 1 : 2) m2rnn_ss
     uint16_t* const buf = pool + (it & 1) * BUF;
     const uint16_t *sv = buf + OV, *su = buf + OU, *sr = buf + OR;
     const int n = fresh(lane & 15), g = fresh(lane >> 4);  // (addresses formed per head, not held across them)
+    const int It = fresh_s(w), Jt = fresh_s(NI == 4 ? w : w - 2);
     if (w == 0 && h > hb) finish(h - 1);
 
     // rows It: X and the row sums of M
@@ -1418,14 +1432,23 @@ __global__ void __launch_bounds__(64 * kSsmBwdWaves, KP == 128 ? 1 : 2) m2rnn_ss
         ssm_decay<L, false>(tab, It, J, g, n, d);
         const float4 dj = *(const float4*)&tab.d[16 * J + 4 * g];
         const float dl[4] = {dj.x, dj.y, dj.z, dj.w};
+        float m[4];
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          const float x0 = uv[r] * d[r], m = x0 * qkr[J][r];
+          const float x0 = uv[r] * d[r];
+          m[r] = x0 * qkr[J][r];
           xr[J][r] = __builtin_fmaf(x0, dl[r], xr[J][r]);
-          const bool diag = It == J && 4 * g + r == n;
-          if (diag) sm.dg[16 * It + n] = m;
-          row = __builtin_fma((double)(diag ? 0.0f : m), (double)dl[r], row);
         }
+        if (It == J) {  // the diagonal apart
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            if (4 * g + r == n) {
+              sm.dg[16 * It + n] = m[r];
+              m[r] = 0.0f;
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < 4; ++r) row = __builtin_fma((double)m[r], (double)dl[r], row);
       }
       row = group_sum64(row);
       if (g == 0) sm.row[16 * It + n] = row;
@@ -1509,8 +1532,8 @@ __global__ void __launch_bounds__(64 * kSsmBwdWaves, KP == 128 ? 1 : 2) m2rnn_ss
         double dot = 0.0;  // <R, H>: every step of the chunk gets it, so its error would add up in dalpha and dbeta
 #pragma unroll
         for (int e = 0; e < 4; ++e) dot = __builtin_fma((double)hx[e], (double)rx[e], dot);
-        dot = prefix64(dot);
-        if (lane == 63) sm.rh[mk + p] = dot;
+        dot = total64(dot);
+        if (lane == 0) sm.rh[mk + p] = dot;
         double part[NI];
 #pragma unroll
         for (int J = 0; J < NI; ++J) {
@@ -1519,15 +1542,15 @@ __global__ void __launch_bounds__(64 * kSsmBwdWaves, KP == 128 ? 1 : 2) m2rnn_ss
           for (int i = 0; i < NP; ++i) vo[i] = *(const uint2*)(sv + (i * L + 16 * J + n) * STV + 4 * g);
           f32x4 acc = mfma16_planes<3, NP>(ro, vo, f32x4{0, 0, 0, 0});
           const float ej = tab.w[16 * J + n], dj = tab.d[16 * J + n];
-          float kv[4];
+          float kv[4], dot4 = 0.0f;
           lds_vals4<NP>(sk + (16 * J + n) * STK + 16 * (mk + p) + 4 * g, L * STK, kv);
-          part[J] = 0.0;
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
             acc[r] *= ej;
-            part[J] = __builtin_fma((double)kv[r], (double)acc[r], part[J]);
+            dot4 = __builtin_fmaf(kv[r], acc[r], dot4);
             dki[p][J][r] = __builtin_fmaf(dj, acc[r], dki[p][J][r]);
           }
+          part[J] = dot4;
         }
         put_group_sums<NI>(sm.b[mk + p], part, g, n);
       }
@@ -1542,15 +1565,15 @@ __global__ void __launch_bounds__(64 * kSsmBwdWaves, KP == 128 ? 1 : 2) m2rnn_ss
           for (int i = 0; i < 3; ++i) uo[i] = *(const uint2*)(su + (i * L + 16 * I + n) * STV + 4 * g);
           f32x4 acc = mfma16_planes<3, 3>(ho, uo, f32x4{0, 0, 0, 0});
           const float e = tab.e[16 * I + n];
-          float qf[4];
+          float qf[4], dot4 = 0.0f;
           lds_vals4<NP>(sq + (16 * I + n) * STK + 16 * (mq + p) + 4 * g, L * STK, qf);
-          part[I] = 0.0;
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
             acc[r] *= e;
-            part[I] = __builtin_fma((double)qf[r], (double)acc[r], part[I]);
+            dot4 = __builtin_fmaf(qf[r], acc[r], dot4);
             dqi[p][I][r] += acc[r];
           }
+          part[I] = dot4;
         }
         put_group_sums<NI>(sm.a[mq + p], part, g, n);
       }
