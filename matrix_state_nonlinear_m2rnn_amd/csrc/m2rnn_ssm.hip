@@ -12,6 +12,39 @@ namespace m2rnn {
 // Status of a HIP call, recording a failure for m2rnn_last_hip_error() (defined with it).
 int record_hip_status(hipError_t e);
 
+// The backward's partial sums over `parts` rows in one launch: gate [parts][2N] to dbeta, dalpha and wr
+// [parts][N V] to dw_r.  A workgroup takes 64 columns (of both arrays, one after the other), its 16 waves
+// every sixteenth row each; the waves' sums are added in order.
+__global__ void __launch_bounds__(1024) m2rnn_ssm_sums_kernel(const float* __restrict__ gate,
+                                                              const float* __restrict__ wr, long parts, int N, long NV,
+                                                              float* __restrict__ dbeta, float* __restrict__ dalpha,
+                                                              float* __restrict__ dw_r) {
+  __shared__ float red[16][64];
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  const long gate_groups = (2L * N + 63) / 64;
+  const bool g = blockIdx.x < gate_groups;
+  const long M = g ? 2L * N : NV, j = ((long)blockIdx.x - (g ? 0 : gate_groups)) * 64 + lane;
+  const float* src = g ? gate : wr;
+  float acc = 0.0f;
+  if (j < M) {
+#pragma unroll 8
+    for (long p = w; p < parts; p += 16) acc += src[p * M + j];
+  }
+  red[w][lane] = acc;
+  __syncthreads();
+  if (w == 0 && j < M) {
+    float s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) s += red[i][lane];
+    if (!g)
+      dw_r[j] = s;
+    else if (j < N)
+      dbeta[j] = s;
+    else
+      dalpha[j - N] = s;
+  }
+}
+
 // out = the sum of `planes` planes of `count` floats (count a multiple of 4), for dq and dk of heads that
 // share a query/key and were split over workgroups.
 __global__ void __launch_bounds__(256) m2rnn_ssm_planes_kernel(const float* __restrict__ dq_part,
@@ -48,6 +81,10 @@ constexpr long kSsmWaves = 3072;
 constexpr int kSsmMinChunks = 2;
 // Workgroups that the backward's launch aims for where a group's heads can be split.
 constexpr long kSsmBwdGroups = 512;
+
+// Rows of partial sums that one launch adds (one wave 1/16 of them after each other); more go through the
+// tree of slices, whose four launches take 21 us at 256 rows.
+constexpr long kSsmDirectParts = 2048;
 
 int check_ssm(const m2rnn_dims* d, int dtype) {
   if (!d) return M2RNN_EINVAL;
@@ -118,7 +155,7 @@ Plan make_plan(const m2rnn_dims* d, int dtype, bool bwd) {
     p.cdec = round_up256(pairs * A.nch * f);
     p.gate = round_up256((size_t)parts * 2 * A.N * f);
     p.wr = round_up256((size_t)parts * A.N * A.V * f);
-    p.scratch = round_up256(sum_rows_scratch(parts, (long)A.N * (A.V > 2 ? A.V : 2)) * f);
+    if (parts > kSsmDirectParts) p.scratch = round_up256(sum_rows_scratch(parts, (long)A.N * A.V) * f);
     if (A.HS > 1) p.planes = round_up256((size_t)2 * A.HS * A.B * A.T * A.G * A.K * f);
   }
   p.total = p.seg + p.segdec + p.rloc + p.cdec + p.gate + p.wr + p.scratch + p.planes;
@@ -296,8 +333,14 @@ int m2rnn_ssm_bwd(const m2rnn_dims* dims, int qkv_dtype, const void* q, const vo
                          s, (const float*)A.dq, (const float*)A.dk, A.HS, count, dq, dk);
     }
   }
-  sum_rows(A.part_gate, parts, 2L * A.N, dbeta, A.N, dalpha, scratch, s);
-  sum_rows(A.part_wr, parts, (long)A.N * A.V, dw_r, (long)A.N * A.V, nullptr, scratch, s);
+  const long NV = (long)A.N * A.V;
+  if (parts <= kSsmDirectParts) {
+    hipLaunchKernelGGL(m2rnn_ssm_sums_kernel, dim3((unsigned)(ceil_div(2L * A.N, 64) + ceil_div(NV, 64))), dim3(1024),
+                       0, s, (const float*)A.part_gate, (const float*)A.part_wr, parts, A.N, NV, dbeta, dalpha, dw_r);
+  } else {
+    sum_rows(A.part_gate, parts, 2L * A.N, dbeta, A.N, dalpha, scratch, s);
+    sum_rows(A.part_wr, parts, NV, dw_r, NV, nullptr, scratch, s);
+  }
   return status(hipGetLastError());
 }
 

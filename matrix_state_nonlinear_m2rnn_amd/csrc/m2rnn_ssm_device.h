@@ -70,6 +70,16 @@ __device__ __forceinline__ void split3x4(const float (&x)[4], uint2 (&p)[3]) {
 }
 __device__ __forceinline__ uint4 cat(uint2 a, uint2 b) { return make_uint4(a.x, a.y, b.x, b.y); }
 
+// Eight consecutive slots of an operand as its three planes.
+__device__ __forceinline__ void split3x8(const float (&x)[8], uint4 (&o)[3]) {
+  const float a[4] = {x[0], x[1], x[2], x[3]}, b[4] = {x[4], x[5], x[6], x[7]};
+  uint2 pa[3], pb[3];
+  split3x4(a, pa);
+  split3x4(b, pb);
+#pragma unroll
+  for (int p = 0; p < 3; ++p) o[p] = cat(pa[p], pb[p]);
+}
+
 // acc += sum of the plane products A[i] B[j], i + j <= 2, the small ones first.  NA, NB planes
 // (1: the operand is bf16 itself).
 template <int NA, int NB>
@@ -235,40 +245,32 @@ struct SsmTab {
   float e[L], w[L], x[L], d[L], chi[L], clo[L], f[NI > 1 ? NI - 1 : 1][L];
 };
 
-// One wave, lane j = step j of the chunk: its step size D_j and log2 f_j (both 0 past the sequence's
-// end and in the lanes past the chunk) in; the tables, and the chunk's log2 decay (uniform), out.
-// FULL false forms only the weight of each step in the state that leaves the chunk: D_j 2^{c_L - c_j}
-// forwards, 2^{c_j} in the reverse scan.
-template <int L, bool FULL, bool FD, bool REV>
-__device__ __forceinline__ double ssm_tables(SsmTab<L>& tab, int lane, float delta, double lg) {
+// One wave, lane j = step j of the chunk: its step size D_j and log2 f_j in (both 0 past the sequence's end
+// and in the lanes past the chunk).
+template <int L, bool FD>
+__device__ __forceinline__ void ssm_tables(SsmTab<L>& tab, int lane, float delta, double lg) {
   constexpr int NI = L / 16;
   const double c = prefix64(lg);
   const double cl = lane64(c, L - 1);
   double at[NI];
 #pragma unroll
   for (int I = 1; I < NI; ++I) at[I] = lane64(c, 16 * I - 1);
-  if (lane < L) {
-    if constexpr (FULL) {
-      double ref = 0.0;
+  if (lane >= L) return;
+  double ref = 0.0;
 #pragma unroll
-      for (int I = 1; I < NI; ++I) {
-        float fj = exp2_((float)(at[I] - c));
-        if constexpr (FD) fj *= delta;
-        tab.f[I - 1][lane] = fj;  // meant for lane < 16 I; finite or not, the others are never used
-        ref = lane >= 16 * I ? at[I] : ref;
-      }
-      tab.x[lane] = exp2_((float)(c - ref));
-      const float hi = (float)c;
-      tab.chi[lane] = hi;
-      tab.clo[lane] = (float)(c - (double)hi);
-      tab.d[lane] = delta;
-      tab.e[lane] = exp2_((float)c);
-      tab.w[lane] = (FD ? delta : 1.0f) * exp2_((float)(cl - c));
-    } else {
-      tab.w[lane] = REV ? exp2_((float)c) : delta * exp2_((float)(cl - c));
-    }
+  for (int I = 1; I < NI; ++I) {
+    float fj = exp2_((float)(at[I] - c));
+    if constexpr (FD) fj *= delta;
+    tab.f[I - 1][lane] = fj;  // meant for lane < 16 I; finite or not, the others are never used
+    ref = lane >= 16 * I ? at[I] : ref;
   }
-  return cl;
+  tab.x[lane] = exp2_((float)(c - ref));
+  const float hi = (float)c;
+  tab.chi[lane] = hi;
+  tab.clo[lane] = (float)(c - (double)hi);
+  tab.d[lane] = delta;
+  tab.e[lane] = exp2_((float)c);
+  tab.w[lane] = (FD ? delta : 1.0f) * exp2_((float)(cl - c));
 }
 
 // ------------------------------------------------------------------ staging a chunk
@@ -317,37 +319,6 @@ struct SsmPieces {
         split3x4(x, pl);
 #pragma unroll
         for (int q = 0; q < 3; ++q) *(uint2*)(d + q * L * ST) = pl[q];
-      }
-    }
-  }
-
-  // To LDS as three planes of the values times the weight of their row and head (VB columns a head).
-  template <int VB>
-  __device__ __forceinline__ void store_scaled(uint16_t* lds, const SsmTab<L>* tab, int tid) const {
-#pragma unroll
-    for (int p = 0; p < NP; ++p) {
-      const int i = tid + p * NTH;
-      const int row = i / PR, col = (i % PR) * VEC;
-      if ((L * PR) % NTH != 0 && i >= L * PR) continue;
-      const float w = tab[col / VB].w[row];
-      uint16_t* d = lds + row * ST + col;
-      const uint32_t u[4] = {r[p].x, r[p].y, r[p].z, r[p].w};
-#pragma unroll
-      for (int h = 0; h < VEC / 4; ++h) {
-        float x[4];
-        if constexpr (BF16) {
-          x[0] = w * bf16_lo_to_f32(u[2 * h]);
-          x[1] = w * bf16_hi_to_f32(u[2 * h]);
-          x[2] = w * bf16_lo_to_f32(u[2 * h + 1]);
-          x[3] = w * bf16_hi_to_f32(u[2 * h + 1]);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) x[e] = w * __uint_as_float(u[e]);
-        }
-        uint2 pl[3];
-        split3x4(x, pl);
-#pragma unroll
-        for (int q = 0; q < 3; ++q) *(uint2*)(d + 4 * h + q * L * ST) = pl[q];
       }
     }
   }

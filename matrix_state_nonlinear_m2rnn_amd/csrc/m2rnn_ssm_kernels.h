@@ -226,7 +226,7 @@ __global__ void __launch_bounds__(HPW * VB * 4) m2rnn_ssm_fwd_kernel(SsmArgs A) 
       float delta;
       double lg;
       ssm_gate(lane < L && t0 + lane < Tb, pa, alpha, beta, delta, lg);
-      ssm_tables<L, true, true, false>(tab[w / WPH], lane, delta, lg);
+      ssm_tables<L, true>(tab[w / WPH], lane, delta, lg);
     }
     __syncthreads();
     if (ch + 1 < ch1) fetch(ch + 1);
@@ -278,6 +278,25 @@ __global__ void __launch_bounds__(HPW * VB * 4) m2rnn_ssm_fwd_kernel(SsmArgs A) 
     for (int s = 0; s < NS; ++s)
 #pragma unroll
       for (int p = 0; p < NP; ++p) vop[s][p] = lds_col(sv + p * L * STV, STV, 32 * s, lc, g, n);
+    // the same values in fp32, in the operand's order
+    float vf[NS][8];
+#pragma unroll
+    for (int s = 0; s < NS; ++s) {
+      uint2 lo[NP], hi[NP];
+#pragma unroll
+      for (int p = 0; p < NP; ++p) {
+        lo[p] = make_uint2(vop[s][p].x, vop[s][p].y);
+        hi[p] = make_uint2(vop[s][p].z, vop[s][p].w);
+      }
+      float a4[4], b4[4];
+      planes_vals4<NP>(lo, a4);
+      planes_vals4<NP>(hi, b4);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        vf[s][e] = a4[e];
+        vf[s][4 + e] = b4[e];
+      }
+    }
     uint4 hp[KS][3];
 #pragma unroll
     for (int s = 0; s < KS; ++s) {
@@ -313,6 +332,9 @@ __global__ void __launch_bounds__(HPW * VB * 4) m2rnn_ssm_fwd_kernel(SsmArgs A) 
             po[p] = cat(pb[0], 2 * s + 1 <= I ? pb[64] : make_uint2(0, 0));
           }
         } else {
+          // (P is split here, in the wave that uses it.  Feeding the fp32 MFMA instead, which takes the accumulator's
+          // registers as they are, saves 24 VALU operations a tile but costs 4 dependent passes of 32 cycles: the
+          // padded batch of B4 N128 T4096 V=16 prompts took 83 us instead of 78.)
           uint2 half[2][3];
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf) {
@@ -361,28 +383,11 @@ __global__ void __launch_bounds__(HPW * VB * 4) m2rnn_ssm_fwd_kernel(SsmArgs A) 
       for (int r = 0; r < 4; ++r) H[m][r] *= dl;
 #pragma unroll
     for (int s = 0; s < NS; ++s) {
-      uint2 half[2][3];
-#pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        const float4 w4 = *(const float4*)&tb.w[32 * s + 16 * hf + 4 * g];
-        float x[4] = {0, 0, 0, 0};
-#pragma unroll
-        for (int p = NP - 1; p >= 0; --p) {
-          const uint32_t u0 = hf ? vop[s][p].z : vop[s][p].x, u1 = hf ? vop[s][p].w : vop[s][p].y;
-          x[0] += bf16_lo_to_f32(u0);
-          x[1] += bf16_hi_to_f32(u0);
-          x[2] += bf16_lo_to_f32(u1);
-          x[3] += bf16_hi_to_f32(u1);
-        }
-        x[0] *= w4.x;
-        x[1] *= w4.y;
-        x[2] *= w4.z;
-        x[3] *= w4.w;
-        split3x4(x, half[hf]);
-      }
+      const float4 w0 = *(const float4*)&tb.w[32 * s + 4 * g], w1 = *(const float4*)&tb.w[32 * s + 16 + 4 * g];
+      const float x[8] = {vf[s][0] * w0.x, vf[s][1] * w0.y, vf[s][2] * w0.z, vf[s][3] * w0.w,
+                          vf[s][4] * w1.x, vf[s][5] * w1.y, vf[s][6] * w1.z, vf[s][7] * w1.w};
       uint4 vs[3];
-#pragma unroll
-      for (int p = 0; p < 3; ++p) vs[p] = cat(half[0][p], half[1][p]);
+      split3x8(x, vs);
 #pragma unroll
       for (int m = 0; m < KM; ++m) {
         uint4 ko[NP];
@@ -410,17 +415,18 @@ __global__ void __launch_bounds__(HPW * VB * 4) m2rnn_ssm_fwd_kernel(SsmArgs A) 
 // REV = true: the gradient's state R, chunks last to first, seg = sum of the decayed q_i dy_i^T that
 // leaves the segment backwards, as [V,K]; before each chunk the part accumulated so far (what the
 // segment's later chunks send to it) goes to rloc, and its log2 decay to cdec.
-// Work split as in the forward; the weights multiply v (or dy) as it is staged.
+// Work split as in the forward.  The weights multiply v (or dy) in the operand.  dy, in fp32, goes straight
+// from HBM into the operands (a lane's column of 16, rows of 64 bytes), since its planes would need three
+// times v's LDS.  The decays of the next chunk are formed beside the products of this one.
 template <bool BF16, int KP, int VB, int HPW, bool REV>
 __global__ void __launch_bounds__(HPW * VB * 4) m2rnn_ssm_state_kernel(SsmArgs A) {
   constexpr int L = ssm_chunk<BF16>(), NS = L / 32, KM = KP / 16, NP = BF16 ? 1 : 3;
   constexpr int WPH = VB / 16, NW = HPW * WPH, NTH = 64 * NW, VT = HPW * VB;
   constexpr int STK = ssm_stride(KP), STV = ssm_stride(VT);
-  constexpr bool BF16V = BF16 && !REV;
   __shared__ __attribute__((aligned(16))) uint16_t sk[NP * L * STK];
-  __shared__ __attribute__((aligned(16))) uint16_t sv[3 * L * STV];
-  __shared__ __attribute__((aligned(16))) SsmTab<L> tab[HPW];
-  __shared__ float sdec[HPW];
+  __shared__ __attribute__((aligned(16))) uint16_t sv[REV ? 8 : NP * L * STV];
+  __shared__ __attribute__((aligned(16))) float weight[2][HPW][L];
+  __shared__ float sdec[2][HPW];
 
   int tid = threadIdx.x;
   const int lane = tid & 63;
@@ -435,15 +441,15 @@ __global__ void __launch_bounds__(HPW * VB * 4) m2rnn_ssm_state_kernel(SsmArgs A
   const int h0 = grp * hpg + (share / A.CB) * HPW;
   const int hn = min(HPW, (grp + 1) * hpg - h0);
   const int cb = share % A.CB;
-  const int head = h0 + w / WPH;
-  const bool mine = w / WPH < hn;
+  const int hw = w / WPH, head = h0 + hw;
+  const bool mine = hw < hn;
   const int c0 = cb * VB + (w % WPH) * 16, lc = w * 16;
   const int K = A.K, V = A.V, T = A.T;
   const int Tb = ssm_len(A, b);
   const long krow = (long)A.G * K, vrow = (long)A.N * V;
   const char* kbase = (const char*)(REV ? A.q : A.k) + (((long)b * T * A.G + grp) * K) * (BF16 ? 2 : 4);
-  const char* vbase = (const char*)(REV ? (const void*)A.dy : A.v) +
-                      ((long)b * T * vrow + (long)h0 * V + cb * VB) * (BF16V ? 2 : 4);
+  const char* vbase = (const char*)A.v + ((long)b * T * vrow + (long)h0 * V + cb * VB) * (BF16 ? 2 : 4);
+  const float* ubase = A.dy + (long)b * T * vrow + (long)head * V + c0;
   const int vcols = HPW > 1 ? hn * V : VB;
   const bool preps = w % WPH == 0;
   const float alpha = mine ? A.alpha[head] : 0.0f, beta = mine ? A.beta[head] : 0.0f;
@@ -453,19 +459,51 @@ __global__ void __launch_bounds__(HPW * VB * 4) m2rnn_ssm_state_kernel(SsmArgs A
 #pragma unroll
   for (int m = 0; m < KM; ++m) H[m] = f32x4{0, 0, 0, 0};
   SsmPieces<BF16, L, KP, NTH> pk;
-  SsmPieces<BF16V, L, VT, NTH> pv;
+  SsmPieces<BF16, L, VT, NTH> pv;
+  float pu[NS][8];
   float pa = 0.0f;
   auto fetch = [&](int ch) {
     const int t0 = ch * L, rows = min(L, Tb - t0);
     pk.load(kbase + (long)t0 * krow * (BF16 ? 2 : 4), krow, K, rows, tid);
-    pv.load(vbase + (long)t0 * vrow * (BF16V ? 2 : 4), vrow, vcols, rows, tid);
-    if (preps && mine && lane < rows) pa = A.a[((long)b * T + t0 + lane) * A.N + head];
+    if constexpr (REV) {
+      const float* u = ubase + (long)t0 * vrow;
+#pragma unroll
+      for (int s = 0; s < NS; ++s)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int j = 32 * s + 16 * (e / 4) + 4 * g + e % 4;
+          pu[s][e] = mine && j < rows ? u[j * vrow + n] : 0.0f;
+        }
+    } else {
+      pv.load(vbase + (long)t0 * vrow * (BF16 ? 2 : 4), vrow, vcols, rows, tid);
+    }
+  };
+  auto fetch_a = [&](int ch) {
+    const int t = ch * L + lane;
+    if (preps && mine && lane < L && t < Tb) pa = A.a[((long)b * T + t) * A.N + head];
+  };
+  // the weight of each step in the state that leaves chunk ch: D_j 2^{c_L - c_j}, in the reverse scan 2^{c_j}
+  double cl = 0.0;
+  auto weights = [&](int ch, int buf) {
+    if (!preps) return;
+    float delta;
+    double lg;
+    ssm_gate(lane < L && ch * L + lane < Tb, pa, alpha, beta, delta, lg);
+    const double c = prefix64(lg);
+    cl = lane64(c, L - 1);
+    if (lane < L) weight[buf][hw][lane] = REV ? exp2_((float)c) : delta * exp2_((float)(cl - c));
+    if (lane == 0) sdec[buf][hw] = exp2_((float)cl);
   };
   const int ch0 = s_ * A.cps, ch1 = min(A.nch, ch0 + A.cps);
-  const int first = REV ? ch1 - 1 : ch0, step = REV ? -1 : 1;
-  if (ch0 < ch1) fetch(first);
-  for (int c = 0; c < ch1 - ch0; ++c) {
-    const int ch = first + step * c, t0 = ch * L;
+  const int first = REV ? ch1 - 1 : ch0, step = REV ? -1 : 1, count = ch1 - ch0;
+  if (count > 0) {
+    fetch_a(first);
+    fetch(first);
+    weights(first, 0);
+    if (count > 1) fetch_a(first + step);
+  }
+  for (int c = 0; c < count; ++c) {
+    const int ch = first + step * c, buf = c & 1;
     if constexpr (REV) {
       if (mine) {
         float* o = A.rloc + ((((long)b * A.N + head) * A.nch + ch) * V + c0 + n) * K;
@@ -474,34 +512,56 @@ __global__ void __launch_bounds__(HPW * VB * 4) m2rnn_ssm_state_kernel(SsmArgs A
           if (16 * m + 4 * g < K) *(float4*)(o + 16 * m + 4 * g) = make_float4(H[m][0], H[m][1], H[m][2], H[m][3]);
         if (preps && lane == 0 && cb == 0) A.cdec[((long)b * A.N + head) * A.nch + ch] = (float)dec;
       }
+      dec += cl;
+    } else {
+      dec += cl;
     }
     __syncthreads();  // the previous chunk's reads are done
     tid = fresh(tid);
     g = fresh(g);
     n = fresh(n);
-    if (preps) {
-      float delta;
-      double lg;
-      ssm_gate(lane < L && t0 + lane < Tb, pa, alpha, beta, delta, lg);
-      const double cl = ssm_tables<L, false, false, REV>(tab[w / WPH], lane, delta, lg);
-      dec += cl;
-      if (lane == 0) sdec[w / WPH] = exp2_((float)cl);
-    }
     pk.store(sk, tid);
+    if constexpr (!REV) pv.store(sv, tid);
+    float x[NS][8];
+    if constexpr (REV) {
+#pragma unroll
+      for (int s = 0; s < NS; ++s)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[s][e] = pu[s][e];
+    }
     __syncthreads();
-    pv.template store_scaled<VB>(sv, tab, tid);
-    __syncthreads();
-    if (c + 1 < ch1 - ch0) fetch(ch + step);
-    const float dl = sdec[w / WPH];
+    if (c + 1 < count) fetch(ch + step);
+    const float dl = sdec[buf][hw];
 #pragma unroll
     for (int m = 0; m < KM; ++m)
 #pragma unroll
       for (int r = 0; r < 4; ++r) H[m][r] *= dl;
 #pragma unroll
     for (int s = 0; s < NS; ++s) {
-      uint4 vs[3];
+      if constexpr (!REV) {
+        uint2 lo[NP], hi[NP];
 #pragma unroll
-      for (int p = 0; p < 3; ++p) vs[p] = lds_col(sv + p * L * STV, STV, 32 * s, lc, g, n);
+        for (int p = 0; p < NP; ++p) {
+          const uint4 t = lds_col(sv + p * L * STV, STV, 32 * s, lc, g, n);
+          lo[p] = make_uint2(t.x, t.y);
+          hi[p] = make_uint2(t.z, t.w);
+        }
+        float a4[4], b4[4];
+        planes_vals4<NP>(lo, a4);
+        planes_vals4<NP>(hi, b4);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          x[s][e] = a4[e];
+          x[s][4 + e] = b4[e];
+        }
+      }
+      const float4 w0 = *(const float4*)&weight[buf][hw][32 * s + 4 * g];
+      const float4 w1 = *(const float4*)&weight[buf][hw][32 * s + 16 + 4 * g];
+      const float ws[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[s][e] *= ws[e];
+      uint4 vs[3];
+      split3x8(x[s], vs);
 #pragma unroll
       for (int m = 0; m < KM; ++m) {
         uint4 ko[NP];
@@ -509,6 +569,10 @@ __global__ void __launch_bounds__(HPW * VB * 4) m2rnn_ssm_state_kernel(SsmArgs A
         for (int p = 0; p < NP; ++p) ko[p] = lds_col(sk + p * L * STK, STK, 32 * s, 16 * m, g, n);
         H[m] = mfma_planes<NP, 3>(ko, vs, H[m]);
       }
+    }
+    if (c + 1 < count) {
+      weights(ch + step, buf ^ 1);
+      if (c + 2 < count) fetch_a(ch + 2 * step);
     }
   }
   if (mine) {
@@ -572,16 +636,6 @@ __global__ void __launch_bounds__(256) m2rnn_ssm_combine_kernel(SsmArgs A) {
 // ------------------------------------------------------------------ backward
 
 constexpr int kSsmBwdWaves = 4;
-
-// Eight consecutive slots of an operand as its three planes.
-__device__ __forceinline__ void split3x8(const float (&x)[8], uint4 (&o)[3]) {
-  const float a[4] = {x[0], x[1], x[2], x[3]}, b[4] = {x[4], x[5], x[6], x[7]};
-  uint2 pa[3], pb[3];
-  split3x4(a, pa);
-  split3x4(b, pb);
-#pragma unroll
-  for (int p = 0; p < 3; ++p) o[p] = cat(pa[p], pb[p]);
-}
 
 // The factors of ssm_decay with the roles turned: lane column j = 16 J + n, rows i = 16 I + 4 g + r.  The
 // same products and differences, so both tiles hold the same numbers.
@@ -695,7 +749,7 @@ __global__ void __launch_bounds__(64 * kSsmBwdWaves, KP == 128 ? 1 : 2) m2rnn_ss
     float delta;
     double lg;
     ssm_gate(live, pa, alpha, beta, delta, lg);
-    ssm_tables<L, true, false, false>(tab, lane, delta, lg);
+    ssm_tables<L, false>(tab, lane, delta, lg);
   };
   SsmPieces<BF16, L, KP, NTH> pq;
   auto fetch_q = [&]() {
@@ -1313,7 +1367,7 @@ __global__ void __launch_bounds__(64 * kSsmBwdWaves, KP == 128 ? 1 : 2) m2rnn_ss
     float delta;
     double lg;
     ssm_gate(live, pa, A.alpha[h], A.beta[h], delta, lg);
-    ssm_tables<L, true, false, false>(tabs[(h - hb) % 3], lane, delta, lg);
+    ssm_tables<L, false>(tabs[(h - hb) % 3], lane, delta, lg);
   };
   // da, and the partial sums of dalpha, dbeta and dw_r, of a head whose products are done
   auto finish = [&](int h) {

@@ -57,7 +57,7 @@ def test_steps_and_state_overlap():
 def test_workspaces():
     n = ctypes.c_size_t(0)
     L = m2.lib()
-    one = D(8, 4096, 64, 64, 64)      # enough pairs to fill the chip: no segments, no workspace
+    one = D(16, 4096, 64, 64, 64)      # enough pairs to fill the chip: no segments, no workspace
     assert L.m2rnn_ssm_fwd_workspace_size(ctypes.byref(one), 1, ctypes.byref(n)) == 0 and n.value == 0
     few = D(1, 4096, 2, 64, 64)       # time segments, whose entering states need room
     assert L.m2rnn_ssm_fwd_workspace_size(ctypes.byref(few), 1, ctypes.byref(n)) == 0

@@ -98,6 +98,7 @@ SIZES = [
     (1, 1, 1, 1, 16, 16), (2, 2, 2, 1, 16, 32), (1, 31, 3, 3, 32, 16), (2, 64, 2, 2, 64, 64), (1, 65, 5, 1, 64, 16),
     (1, 129, 2, 2, 64, 128), (2, 100, 6, 2, 48, 16), (1, 257, 4, 2, 128, 64), (1, 700, 2, 1, 80, 32),
     (1, 190, 3, 3, 128, 128), (3, 33, 9, 1, 16, 16), (1, 1100, 1, 1, 64, 64), (1, 96, 6, 3, 112, 32),
+    (64, 1030, 1, 1, 16, 16),  # thousands of chunks: the partial sums take the tree
 ]
 
 
