@@ -906,7 +906,7 @@ __global__ void __launch_bounds__(64 * kSsmBwdWaves, KP == 128 ? 1 : 2) m2rnn_ss
       }
 #pragma unroll
       for (int m = 0; m < KM; ++m) through += rh[m];
-      through *= exp2((double)tab.chi[L - 1] + (double)tab.clo[L - 1]);
+      through *= tab.e[L - 1];
       const double x = row - delta64 * (col - diag) + aa, y = delta64 * bb;
       // sum over i >= t of x, sum over j < t of y, each without a subtraction that would leave a residue
       const double sx64 = __shfl(prefix64(__shfl(x, 63 - lane)), 63 - lane);
@@ -1269,8 +1269,9 @@ __device__ __forceinline__ f32x4 mfma16_planes_turned(const uint2 (&A)[NA], cons
 // usually share a query/key: the walk over the heads is what counts, so everything in it runs one
 // head ahead.  A wave owns the same 16 steps as rows and as columns; with 16 value columns it forms
 // its dv tile from its own P, so nothing is exchanged within a head: v, dy and R of the next head
-// go to the other half of a double buffer while this one is computed, one barrier a head.  Wave 3
-// forms the next head's decay tables, wave 0 finishes the previous head's da, meanwhile.  R is read
+// go to the other half of a double buffer while this one is computed, one barrier a head.  Meanwhile wave 3
+// forms the next head's decay tables and wave 0 finishes the previous head's da, so waves 1 and 2 do
+// the staging (all four staging: 14.1 thousand cycles a head, of which waves 1 and 2 waited 2.6).  R is read
 // once, as planes in LDS that serve as R (transposing reads) and as R^T; H goes straight into the
 // operand of the wave that owns its 16 K rows.  X is summed over the heads in registers.
 template <bool BF16, int KP>
@@ -1279,7 +1280,8 @@ __global__ void __launch_bounds__(64 * kSsmBwdWaves, KP == 128 ? 1 : 2) m2rnn_ss
   constexpr int NW = kSsmBwdWaves, NTH = 64 * NW, V = 16;
   constexpr int STK = ssm_stride(KP), STV = ssm_stride(V), STR = ssm_stride(KP);
   constexpr int MPW = KM >= NW ? KM / NW : 1;
-  constexpr int RP = (V * KP / 4 + NTH - 1) / NTH;                   // pieces of R (4 values) per thread
+  constexpr int NST = NTH / 2;                                       // threads that stage: waves 1 and 2
+  constexpr int RP = (V * KP / 4 + NST - 1) / NST;                   // pieces of R (4 values) per thread
   constexpr int OV = 0, OU = NP * L * STV, OR = OU + 3 * L * STV, BUF = OR + 3 * V * STR;  // one buffer, in elements
   constexpr int POOL = 2 * BUF * 2 > L * KP * 4 ? 2 * BUF : L * KP * 2;
   struct Small {
@@ -1311,21 +1313,24 @@ __global__ void __launch_bounds__(64 * kSsmBwdWaves, KP == 128 ? 1 : 2) m2rnn_ss
   const int mq = KM >= NW ? w * MPW : w, mk = KM >= NW ? w * MPW : w - (NW - KM);
   const int mh = hasdq ? mq : mk;  // the K tiles whose H this wave reads
 
-  SsmPieces<BF16, L, V, NTH> pv;
-  SsmPieces<false, L, V, NTH> pu;
+  const bool stager = w == 1 || w == 2;
+  const int sid = tid - 64;
+  SsmPieces<BF16, L, V, NST> pv;
+  SsmPieces<false, L, V, NST> pu;
   float4 pr[RP], pi[RP];
   float idec;
   auto fetch = [&](int h) {  // v, dy, R of head h
+    if (!stager) return;
     const long off = row0 * vrow + (long)h * V;
-    pv.load(BF16 ? (const void*)((const uint16_t*)A.v + off) : (const void*)((const float*)A.v + off), vrow, V, rows, tid);
-    pu.load(A.dy + off, vrow, V, rows, tid);
+    pv.load(BF16 ? (const void*)((const uint16_t*)A.v + off) : (const void*)((const float*)A.v + off), vrow, V, rows, sid);
+    pu.load(A.dy + off, vrow, V, rows, sid);
     const long pair = (long)b * N + h;
     const float* Rp = A.rloc + (pair * A.nch + ch) * V * K;        // [V][K]
     const float* Ip = A.seg + (pair * A.S + ch / A.cps) * V * K;   // [V][K]
     idec = A.cdec[pair * A.nch + ch];
 #pragma unroll
     for (int p = 0; p < RP; ++p) {
-      const int i = tid + p * NTH, c = i / (KP / 4), kk = (i % (KP / 4)) * 4;
+      const int i = sid + p * NST, c = i / (KP / 4), kk = (i % (KP / 4)) * 4;
       pr[p] = pi[p] = make_float4(0, 0, 0, 0);
       if (c < V && kk < K) {
         pr[p] = *(const float4*)(Rp + (unsigned)(c * K + kk));
@@ -1334,12 +1339,13 @@ __global__ void __launch_bounds__(64 * kSsmBwdWaves, KP == 128 ? 1 : 2) m2rnn_ss
     }
   };
   auto stage = [&](uint16_t* buf) {
-    pv.store(buf + OV, tid);
-    pu.store(buf + OU, tid);
+    if (!stager) return;
+    pv.store(buf + OV, sid);
+    pu.store(buf + OU, sid);
     const float d = exp2_(idec);
 #pragma unroll
     for (int p = 0; p < RP; ++p) {
-      const int i = tid + p * NTH, c = i / (KP / 4), kk = (i % (KP / 4)) * 4;
+      const int i = sid + p * NST, c = i / (KP / 4), kk = (i % (KP / 4)) * 4;
       if (c < V) {
         const float x[4] = {__builtin_fmaf(d, pi[p].x, pr[p].x), __builtin_fmaf(d, pi[p].y, pr[p].y),
                             __builtin_fmaf(d, pi[p].z, pr[p].z), __builtin_fmaf(d, pi[p].w, pr[p].w)};
@@ -1350,8 +1356,9 @@ __global__ void __launch_bounds__(64 * kSsmBwdWaves, KP == 128 ? 1 : 2) m2rnn_ss
       }
     }
   };
-  float4 ph[MPW];
+  float4 ph[MPW], wr;
   auto fetch_H = [&](int h) {
+    wr = *(const float4*)(A.w_r + (long)h * V + 4 * g);
     const float* Hp = A.ckpt + (((long)b * N + h) * A.nch + ch) * K * V;  // [K][V]
 #pragma unroll
     for (int p = 0; p < MPW; ++p) {
@@ -1388,7 +1395,7 @@ __global__ void __launch_bounds__(64 * kSsmBwdWaves, KP == 128 ? 1 : 2) m2rnn_ss
     }
 #pragma unroll
     for (int m = 0; m < KM; ++m) through += sm.rh[m];
-    through *= exp2((double)tab.chi[L - 1] + (double)tab.clo[L - 1]);
+    through *= tab.e[L - 1];
     const double x = row - (double)delta * (col - diag) + aa, y = (double)delta * bb;
     const double gs = __shfl(prefix64(__shfl(x, 63 - lane)), 63 - lane) + prefix64(dpp64<0x138, 0xF>(y)) + through;
     // sigma(z) = 1 - e^{-softplus(z)}
@@ -1564,7 +1571,6 @@ __global__ void __launch_bounds__(64 * kSsmBwdWaves, KP == 128 ? 1 : 2) m2rnn_ss
       float uj[4], vj[4];
       lds_vals4<3>(su + (16 * Jt + n) * STV + 4 * g, L * STV, uj);
       lds_vals4<NP>(sv + (16 * Jt + n) * STV + 4 * g, L * STV, vj);
-      const float4 wr = *(const float4*)(A.w_r + (long)h * V + 4 * g);
       const int t = t0 + 16 * Jt + n;
       if (t < T)
         *(float4*)(A.dv + ((long)b * T + t) * vrow + (long)h * V + 4 * g) =
