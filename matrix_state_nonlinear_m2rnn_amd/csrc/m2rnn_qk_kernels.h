@@ -122,9 +122,9 @@ __global__ void __launch_bounds__(kBlkThreads) m2rnn_qk_norm_rope_kernel(QkArgs 
       const bool live = on && h < heads, isq = h < A.Nq;
       const long at = isq ? (tok * A.Nq + h) * A.K : (tok * A.Nk + (h - A.Nq)) * A.K;
       float x[8] = {0, 0, 0, 0, 0, 0, 0, 0}, g[8], gm[8];
-      if (live) {
+      if (live) {  // (plain loads: the two 8-byte pieces of a lane share lines; non-temporal ones took 120 us, not 110)
         const void* src = isq ? A.q : A.k;
-        const float4 x1 = load4_nt<BF16>(src, at + o1), x2 = load4_nt<BF16>(src, at + o2);
+        const float4 x1 = load4<BF16>(src, at + o1), x2 = load4<BF16>(src, at + o2);
         x[0] = x1.x; x[1] = x1.y; x[2] = x1.z; x[3] = x1.w;
         x[4] = x2.x; x[5] = x2.y; x[6] = x2.z; x[7] = x2.w;
       }
