@@ -76,7 +76,7 @@ constexpr int kMaxK = 128;
 
 // Waves that the forward and state launches aim for: three for each of the 1024 SIMDs, which is what their
 // registers and LDS let a CU hold (B2 N32 T16384 K=V=64: 242 us, against 253 with two and 272 with four).
-constexpr long kSsmWaves = 3072;
+constexpr long kSsmWaves = 3L * 1024;
 // A segment is at least this many chunks: shorter ones spend their time filling the pipeline.
 constexpr int kSsmMinChunks = 2;
 // Workgroups that the backward's launch aims for where a group's heads can be split.
