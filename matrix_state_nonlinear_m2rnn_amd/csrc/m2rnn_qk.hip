@@ -2,7 +2,6 @@
 #include <hip/hip_runtime.h>
 
 #include "../../include/m2rnn.h"
-#include "m2rnn_block_launch.h"
 #include "m2rnn_qk_kernels.h"
 
 using namespace m2rnn;
@@ -18,7 +17,9 @@ size_t round_up256(size_t x) { return (x + 255) & ~(size_t)255; }
 long ceil_div(long a, long b) { return (a + b - 1) / b; }
 
 constexpr long kQkWaves = 8192;      // waves that a launch aims for (heads of a token split over waves)
-constexpr long kQkMaxGroups = 2048;  // workgroups of the backward: each writes one row of partial sums
+// Workgroups of the backward, each of which writes one row of partial sums: four waves for each SIMD (16K tokens of
+// 16 + 4 heads, K = 128: 114 us; with twice as many groups 119 us and longer final sums, with half as many 139 us).
+constexpr long kQkMaxGroups = 1024;
 
 struct QkPlan {
   int LPH = 1, split = 1;
@@ -101,8 +102,7 @@ int m2rnn_qk_norm_rope_bwd_workspace_size(int64_t B, int64_t T, int64_t Nq, int6
   const int st = check_qk(B, T, Nq, Nk, K, 0, M2RNN_DTYPE_F32, 0.0f);
   if (st) return st;
   const QkPlan p = plan_qk(B * T, (int)(Nq + Nk), (int)K, true);
-  *bytes = round_up256((size_t)p.groups * 2 * K * sizeof(float)) +
-           round_up256(sum_rows_scratch(p.groups, 2 * K) * sizeof(float));
+  *bytes = round_up256((size_t)p.groups * 2 * K * sizeof(float));
   return M2RNN_OK;
 }
 
@@ -128,14 +128,14 @@ int m2rnn_qk_norm_rope_bwd(int64_t B, int64_t T, int64_t Nq, int64_t Nk, int64_t
   if (any && (!workspace || workspace_bytes < need || !al16(workspace))) return M2RNN_EWORKSPACE;
   hipStream_t s = (hipStream_t)stream;
   float* part = (float*)workspace;
-  float* scratch = any ? (float*)((char*)workspace + round_up256((size_t)p.groups * 2 * K * sizeof(float))) : nullptr;
   if (any) {
     QkArgs A{q, k, gamma_q, gamma_k, (const int*)pos, inv_freq, dq_out, dk_out, dq, dk, part, B * T,
              (int)Nq, (int)Nk, (int)K, (int)R / 2, p.split, eps};
     st = launch_qk(pick_qk<true>(dtype == M2RNN_DTYPE_BF16, p.LPH, interleaved != 0), p.groups, A, s);
     if (st) return st;
   }
-  sum_rows(part, any ? p.groups : 0, 2 * K, dgamma_q, K, dgamma_k, scratch, s);
+  hipLaunchKernelGGL(m2rnn_qk_sums_kernel, dim3((unsigned)(K / 8)), dim3(1024), 0, s, (const float*)part,
+                     any ? p.groups : 0, (int)K, dgamma_q, dgamma_k);
   return record_hip_status(hipGetLastError());
 }
 

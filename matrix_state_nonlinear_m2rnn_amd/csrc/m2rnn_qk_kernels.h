@@ -208,4 +208,28 @@ __global__ void __launch_bounds__(kBlkThreads) m2rnn_qk_norm_rope_kernel(QkArgs 
   }
 }
 
+// dgamma_q and dgamma_k from the workgroups' `parts` rows of 2K partial sums: a workgroup takes 16 columns
+// (64 bytes of a row), 64 threads every 64th row each, in fp64 and in a fixed order.  One launch of 5 us at
+// 1024 rows of 256 columns (the block operators' tree of slices takes two launches of 5 us each).
+__global__ void __launch_bounds__(1024) m2rnn_qk_sums_kernel(const float* __restrict__ part, long parts, int K,
+                                                             float* __restrict__ dgq, float* __restrict__ dgk) {
+  __shared__ double red[64][17];
+  const int col = threadIdx.x & 15, row = threadIdx.x >> 4;
+  const int j = blockIdx.x * 16 + col;  // 2K is a multiple of 16
+  double acc = 0.0;
+#pragma unroll 16
+  for (long p = row; p < parts; p += 64) acc += (double)part[p * 2 * K + j];
+  red[row][col] = acc;
+  __syncthreads();
+  if (threadIdx.x < 16) {
+    double t = 0.0;
+#pragma unroll 16
+    for (int i = 0; i < 64; ++i) t += red[i][threadIdx.x];
+    if (j < K)
+      dgq[j] = (float)t;
+    else
+      dgk[j - K] = (float)t;
+  }
+}
+
 }  // namespace m2rnn
