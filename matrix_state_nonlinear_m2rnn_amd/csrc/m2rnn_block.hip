@@ -102,11 +102,11 @@ size_t norm_ws_bytes(int64_t rows, int64_t D) {
   return round_up256((size_t)parts * D * sizeof(float)) + round_up256(reduce_scratch(parts, D) * sizeof(float));
 }
 
-// Steps per thread of the conv kernels: `base`, halved down to kConvChunkMin while the grid (one
+// Steps per thread of the conv kernels: `base`, halved down to `least` while the grid (one
 // wave per batch entry, chunk and 64 channel groups) would hold fewer than kConvMinWaves waves.
-int conv_chunk(int64_t B, int64_t T, int64_t C, int base) {
+int conv_chunk(int64_t B, int64_t T, int64_t C, int base, int least = kConvChunkMin) {
   int chunk = base;
-  while (chunk > kConvChunkMin && B * ceil_div(T, chunk) * ceil_div(C / 4, 64) < kConvMinWaves) chunk /= 2;
+  while (chunk > least && B * ceil_div(T, chunk) * ceil_div(C / 4, 64) < kConvMinWaves) chunk /= 2;
   return chunk;
 }
 
@@ -319,7 +319,7 @@ int m2rnn_conv4_silu_fwd_state(int64_t B, int64_t T, int64_t C, int dtype, const
   const uintptr_t in = (uintptr_t)win, out = (uintptr_t)win_out;
   if (win && in < out + bytes && out < in + bytes) return M2RNN_EINVAL;
   const int64_t Tc = T > 0 ? T : 1;
-  const int chunk = conv_chunk(B, Tc, C, kConvChunkFwd);
+  const int chunk = conv_chunk(B, Tc, C, kConvChunkFwd, kConvBatch);
   const long blocks = conv_blocks(B, Tc, C, chunk);
   const auto kern = dtype == M2RNN_DTYPE_BF16 ? &m2rnn_conv4_silu_state_kernel<true>
                                               : &m2rnn_conv4_silu_state_kernel<false>;
