@@ -391,7 +391,8 @@ int m2rnn_conv4_silu_bwd(int64_t B, int64_t T, int64_t C, int dtype, const void*
  *
  *   dims       as above, with K a multiple of 16 up to 128, and Nqk 0 (= N) or any divisor of N: query/key
  *              j serves the heads j N/Nqk .. (j + 1) N/Nqk - 1.  Tensors may exceed 4 GiB; B N (T / 32 + 64)
- *              must stay below 2^28.
+ *              must stay below 2^28, N at 2^20 at most, and in the backward, with c = B ceil(T / I) chunks (I: the
+ *              checkpoint interval), c at 65535 * 64 at most and c Nqk (Nqk = 0: c N) below 2^24.
  *   a          gate pre-activation [B,T,N] fp32; alpha, beta [N] fp32; w_r [N,V] fp32 (a, alpha, beta
  *              and lens 4-byte aligned, everything else 16-byte).
  *   lens       [B] int32 device array or NULL: the steps of each batch entry, clamped to [0, T] (NULL:
@@ -493,7 +494,7 @@ int m2rnn_qk_norm_rope_bwd(int64_t B, int64_t T, int64_t Nq, int64_t Nk, int64_t
  *              caller may combine the norms of several ranks).  No tensors: 0.
  *   out        NULL: in place.  Otherwise a host array of `count` device pointers (NULL entries: in place)
  *              of the tensors' own types and sizes.  An output that overlaps another output, another
- *              tensor, or a part of its own tensor is rejected (M2RNN_EINVAL).
+ *              tensor, the norm, or a part of its own tensor is rejected (M2RNN_EINVAL).
  *   max_norm   >= 0 (negative or NaN: M2RNN_EINVAL).
  * A norm that is not finite leaves the gradients unchanged (out of place: copied): the caller finds it
  * in `norm` and skips the step.

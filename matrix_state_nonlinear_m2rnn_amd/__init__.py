@@ -695,6 +695,8 @@ def _call_on(dev, stream):
     allocator is then only handed out again behind the call's own work."""
     import torch
     if stream is not None:
+        if stream.device != dev:
+            raise ValueError(f"stream is on {stream.device}, the inputs are on {dev}")
         return torch.cuda.stream(stream)  # sets the stream's device too
     if torch.cuda.current_device() == dev.index:
         return _HERE_ALREADY

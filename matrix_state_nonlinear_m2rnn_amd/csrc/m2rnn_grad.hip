@@ -80,15 +80,16 @@ int over_launches(const m2rnn_tensor* g, int64_t count, void* const* out, long p
   return flush();
 }
 
-// Whether two outputs share memory, or an output shares memory with another tensor's input, or
-// only a part of it with its own.
-bool overlaps(const m2rnn_tensor* g, int64_t count, void* const* out) {
+// Whether two outputs share memory, or an output shares memory with the norm, with another tensor's
+// input, or only a part of it with its own.
+bool overlaps(const m2rnn_tensor* g, int64_t count, void* const* out, const float* norm) {
   struct Span {
     uintptr_t at, end;
     bool written;
   };
   std::vector<Span> s;
-  s.reserve(2 * (size_t)count);
+  s.reserve(2 * (size_t)count + 1);
+  s.push_back({(uintptr_t)norm, (uintptr_t)(norm + 1), false});
   for (int64_t i = 0; i < count; ++i) {
     if (g[i].numel == 0) continue;
     const uintptr_t bytes = (uintptr_t)g[i].numel * elem(g[i].dtype);
@@ -154,7 +155,7 @@ int m2rnn_grad_clip(const m2rnn_tensor* grads, int64_t count, void* const* out, 
     in_place = in_place && out[i] == grads[i].data;
   }
   try {
-    if (overlaps(grads, count, out)) return M2RNN_EINVAL;
+    if (overlaps(grads, count, out, norm)) return M2RNN_EINVAL;
   } catch (const std::bad_alloc&) {
     return M2RNN_EUNSUPPORTED;
   }

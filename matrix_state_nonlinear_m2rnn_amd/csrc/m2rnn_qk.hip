@@ -18,7 +18,7 @@ long ceil_div(long a, long b) { return (a + b - 1) / b; }
 
 constexpr long kQkWaves = 8192;      // waves that a launch aims for (heads of a token split over waves)
 // Workgroups of the backward, each of which writes one row of partial sums: four waves for each SIMD (16K tokens of
-// 16 + 4 heads, K = 128: 114 us; with twice as many groups 119 us and longer final sums, with half as many 139 us).
+// 16 + 16 heads, K = 128: 114 us; with twice as many groups 119 us and longer final sums, with half as many 139 us).
 constexpr long kQkMaxGroups = 1024;
 
 struct QkPlan {
@@ -43,7 +43,7 @@ QkPlan plan_qk(long tokens, int heads, int K, bool bwd) {
   split = split > passes ? passes : split;
   p.split = (int)(split < 1 ? 1 : split);
   p.groups = ceil_div(tokens * p.split, kBlkThreads / 64);
-  const long most = bwd ? kQkMaxGroups : 2147483647L;
+  const long most = bwd ? kQkMaxGroups : 1L << 22;  // (a launch holds fewer than 2^32 threads)
   p.groups = p.groups > most ? most : p.groups;
   return p;
 }

@@ -72,6 +72,7 @@ size_t round_up256(size_t x) { return (x + 255) & ~(size_t)255; }
 long ceil_div(long a, long b) { return (a + b - 1) / b; }
 
 constexpr long kMaxGrid = 2147483647L;
+constexpr double kMaxThreads = 4294967295.0;  // of one launch
 constexpr int kMaxK = 128;
 
 // Waves that the forward and state launches aim for: three for each of the 1024 SIMDs, which is what their
@@ -94,11 +95,21 @@ int check_ssm(const m2rnn_dims* d, int dtype) {
   if (d->V != 16 && d->V != 32 && d->V != 64 && d->V != 128) return M2RNN_EUNSUPPORTED;
   if (d->K <= 0 || d->K % 16 != 0 || d->K > kMaxK) return M2RNN_EUNSUPPORTED;
   // the kernels number steps, heads and workgroups with ints
-  if (d->T > kMaxGrid - 128 || d->N > (1 << 24) || d->B > kMaxGrid) return M2RNN_EUNSUPPORTED;
+  if (d->T > kMaxGrid - 128 || d->N > (1 << 20) || d->B > kMaxGrid) return M2RNN_EUNSUPPORTED;
   if ((double)d->B * d->N * (ceil_div(d->T, 32) + 64) * 8 > (double)kMaxGrid) return M2RNN_EUNSUPPORTED;
-  // the backward's partial sums are rows per (b, chunk), 64 to a workgroup of a launch's second axis
-  if ((double)d->B * ceil_div(d->T, 32) > 65535.0 * 64.0) return M2RNN_EUNSUPPORTED;
   return M2RNN_OK;
+}
+
+// The backward's further limits: its partial sums are rows per (b, chunk), 64 to a workgroup of a launch's
+// second axis, and it has one workgroup for each (b, query/key, chunk) (and split of its heads, which only small
+// launches have).
+int check_ssm_bwd(const m2rnn_dims* d, int dtype) {
+  const int st = check_ssm(d, dtype);
+  if (st) return st;
+  const double chunks =
+      (double)d->B * ceil_div(d->T, dtype == M2RNN_DTYPE_BF16 ? ssm_chunk<true>() : ssm_chunk<false>());
+  if (chunks > 65535.0 * 64.0) return M2RNN_EUNSUPPORTED;
+  return chunks * (d->Nqk ? d->Nqk : d->N) * 64 * kSsmBwdWaves > kMaxThreads ? M2RNN_EUNSUPPORTED : M2RNN_OK;
 }
 
 struct Plan {
@@ -172,7 +183,8 @@ hipError_t launch(const void* kern, long grid, int block, SsmArgs A, hipStream_t
 }
 
 hipError_t launch_combine(const SsmArgs& A, bool rev, hipStream_t s) {
-  const long grid = (long)A.B * A.N * ceil_div((long)A.K * A.V, 256);
+  const long blocks = (long)A.B * A.N * ceil_div((long)A.K * A.V, 256);
+  const long grid = blocks < (1L << 22) ? blocks : 1L << 22;  // (a launch holds fewer than 2^32 threads)
   return launch(rev ? (const void*)&m2rnn_ssm_combine_kernel<true> : (const void*)&m2rnn_ssm_combine_kernel<false>,
                 grid, 256, A, s);
 }
@@ -260,7 +272,7 @@ int m2rnn_ssm_fwd_ckpt(const m2rnn_dims* dims, int qkv_dtype, const void* q, con
 
 int m2rnn_ssm_bwd_workspace_size(const m2rnn_dims* dims, int qkv_dtype, size_t* bytes) {
   if (!bytes) return M2RNN_EINVAL;
-  const int st = check_ssm(dims, qkv_dtype);
+  const int st = check_ssm_bwd(dims, qkv_dtype);
   if (st) return st;
   *bytes = make_plan(dims, qkv_dtype, true).total;
   return M2RNN_OK;
@@ -270,7 +282,7 @@ int m2rnn_ssm_bwd(const m2rnn_dims* dims, int qkv_dtype, const void* q, const vo
                   const float* alpha, const float* beta, const float* w_r, const int32_t* lens, const float* ckpt,
                   const float* dy, const float* dH_T, float* dq, float* dk, float* dv, float* da, float* dalpha,
                   float* dbeta, float* dw_r, float* dH0, void* workspace, size_t workspace_bytes, void* stream) {
-  const int st = check_ssm(dims, qkv_dtype);
+  const int st = check_ssm_bwd(dims, qkv_dtype);
   if (st) return st;
   if (dims->N == 0) return M2RNN_OK;
   if (!alpha || !beta || !w_r || !dalpha || !dbeta || !dw_r) return M2RNN_EINVAL;

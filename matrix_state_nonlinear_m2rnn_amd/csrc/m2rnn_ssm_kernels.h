@@ -603,34 +603,37 @@ template <bool REV>
 __global__ void __launch_bounds__(256) m2rnn_ssm_combine_kernel(SsmArgs A) {
   const long KV = (long)A.K * A.V;
   const unsigned per = (unsigned)((KV + 255) / 256);
-  const long e = (long)(blockIdx.x % per) * 256 + threadIdx.x;
-  const long pair = blockIdx.x / per;
-  if (e >= KV) return;
-  // the element's place in a [K,V] state
-  const long at = REV ? (e % A.K) * A.V + e / A.K : e;
-  const float* first = REV ? A.dH_T : A.H0;
-  float carry = first ? first[pair * KV + at] : 0.0f;
-  float* p = A.seg + pair * A.S * KV + e;
-  const float* d = A.segdec + pair * A.S;
-  // the segments' parts do not depend on the carry: eight of them in flight at a time
-  for (int i = 0; i < A.S; i += 8) {
-    float own[8], dec[8];
+  const long blocks = (long)A.B * A.N * per;
+  for (long blk = blockIdx.x; blk < blocks; blk += gridDim.x) {
+    const long e = (blk % per) * 256 + threadIdx.x;
+    const long pair = blk / per;
+    if (e >= KV) continue;
+    // the element's place in a [K,V] state
+    const long at = REV ? (e % A.K) * A.V + e / A.K : e;
+    const float* first = REV ? A.dH_T : A.H0;
+    float carry = first ? first[pair * KV + at] : 0.0f;
+    float* p = A.seg + pair * A.S * KV + e;
+    const float* d = A.segdec + pair * A.S;
+    // the segments' parts do not depend on the carry: eight of them in flight at a time
+    for (int i = 0; i < A.S; i += 8) {
+      float own[8], dec[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int s = REV ? A.S - 1 - i - j : i + j;
-      own[j] = i + j < A.S ? p[s * KV] : 0.0f;
-      dec[j] = i + j < A.S ? d[s] : 0.0f;
-    }
+      for (int j = 0; j < 8; ++j) {
+        const int s = REV ? A.S - 1 - i - j : i + j;
+        own[j] = i + j < A.S ? p[s * KV] : 0.0f;
+        dec[j] = i + j < A.S ? d[s] : 0.0f;
+      }
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int s = REV ? A.S - 1 - i - j : i + j;
-      if (i + j < A.S) {
-        p[s * KV] = carry;
-        carry = __builtin_fmaf(exp2_(dec[j]), carry, own[j]);
+      for (int j = 0; j < 8; ++j) {
+        const int s = REV ? A.S - 1 - i - j : i + j;
+        if (i + j < A.S) {
+          p[s * KV] = carry;
+          carry = __builtin_fmaf(exp2_(dec[j]), carry, own[j]);
+        }
       }
     }
+    if (REV && A.dH0) A.dH0[pair * KV + at] = carry;
   }
-  if (REV && A.dH0) A.dH0[pair * KV + at] = carry;
 }
 
 // ------------------------------------------------------------------ backward

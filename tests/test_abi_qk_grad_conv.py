@@ -73,6 +73,9 @@ def test_grad_lists():
     assert L.m2rnn_grad_clip(twice, 2, None, norm, F(1.0), None) == m2.M2RNN_EINVAL
     part = tensors((4096, 1000, 0), (8092, 10, 0))
     assert L.m2rnn_grad_clip(part, 2, None, norm, F(1.0), None) == m2.M2RNN_EINVAL
+    # the norm within what is scaled
+    assert L.m2rnn_grad_clip(ok, 2, None, P(4096 + 8), F(1.0), None) == m2.M2RNN_EINVAL
+    assert L.m2rnn_grad_clip(ok, 2, None, P((1 << 20) + 8), F(1.0), None) == m2.M2RNN_EINVAL
     outs = lambda *a: (P * len(a))(*a)  # noqa: E731
     assert L.m2rnn_grad_clip(ok, 2, outs(1 << 21, (1 << 21) + 3996), norm, F(1.0), None) == m2.M2RNN_EINVAL
     assert L.m2rnn_grad_clip(ok, 2, outs(1 << 20, 1 << 22), norm, F(1.0), None) == m2.M2RNN_EINVAL  # onto the other

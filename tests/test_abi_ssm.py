@@ -72,6 +72,24 @@ def test_workspaces():
     assert L.m2rnn_ssm_fwd_workspace_size(None, 1, ctypes.byref(n)) == m2.M2RNN_EINVAL
 
 
+def test_sizes_that_no_launch_holds():
+    n = ctypes.c_size_t(0)
+    L = m2.lib()
+    size = lambda *d, dt=1: L.m2rnn_ssm_bwd_workspace_size(ctypes.byref(D(*d)), dt, ctypes.byref(n))  # noqa: E731
+    # 2^24 workgroups of the backward, one for each query/key head and chunk
+    assert call("bwd", D(1 << 8, 1 << 16, 64, 16, 16), 1) == m2.M2RNN_EUNSUPPORTED
+    assert size(1 << 8, 1 << 16, 64, 16, 16) == m2.M2RNN_EUNSUPPORTED
+    assert size(1 << 8, 1 << 16, 32, 16, 16) == m2.M2RNN_OK
+    assert size(1 << 8, 1 << 16, 32, 16, 16, dt=0) == m2.M2RNN_EUNSUPPORTED  # chunks of half the length
+    assert size(1 << 8, 1 << 16, 64, 16, 16, 32) == m2.M2RNN_OK
+    # rows of its partial sums
+    assert size(1 << 11, 1 << 17, 1, 16, 16) == m2.M2RNN_EUNSUPPORTED
+    assert size((1 << 11) - 1, 1 << 17, 1, 16, 16) == m2.M2RNN_OK
+    assert L.m2rnn_ssm_fwd_workspace_size(ctypes.byref(D(1 << 11, 1 << 17, 1, 16, 16)), 1, ctypes.byref(n)) == 0
+    assert L.m2rnn_ssm_fwd_workspace_size(ctypes.byref(D(1, 1, (1 << 20) + 1, 16, 16)), 1,
+                                          ctypes.byref(n)) == m2.M2RNN_EUNSUPPORTED
+
+
 def test_checkpoint_interval():
     assert m2.ssm_checkpoint_interval(m2.DTYPE_BF16) == 64 and m2.ssm_checkpoint_interval(m2.DTYPE_F32) == 32
     n = ctypes.c_int64(0)

@@ -159,6 +159,34 @@ def test_decays_from_none_to_all(alpha, beta, a_std, dtype):
     check(run(on_gpu(d, dtype)), ref, tol)
 
 
+@pytest.mark.parametrize("lowest", [-float("inf"), -3.4028234663852886e38])
+def test_steps_masked_through_their_gate(lowest):
+    """a at the type's lowest value: D = 0 and f = 1, so the step leaves the state as it is, and the gradients
+    of what it would have written (k, v through the state, a) are zeros."""
+    torch = torch_cuda()
+    say(f"masked steps {lowest}")
+    d = make(2, 150, 4, 2, 32, 32, "f32", 77)
+    off = np.random.default_rng(3).random((2, 150, 4)) < 0.4
+    off[0, :, 0] = True                       # a head with every step masked
+    off[1, 64:128] = True                     # whole chunks
+    d["a"][off] = lowest
+    t = on_gpu(d, "f32")
+    import matrix_state_nonlinear_m2rnn_amd as m2
+    x = [t[n] for n in ("q", "k", "v", "a", "alpha", "beta", "w_r")]
+    y, H, ckpt = m2.m2rnn_ssm_fwd_ckpt(*x, t["H0"])
+    g = m2.m2rnn_ssm_bwd(*x, ckpt, t["dy"], t["dH_T"])
+    assert torch.equal(H[0, 0], t["H0"][0, 0])
+    at = torch.from_numpy(off).cuda()
+    assert bool((g["da"][at] == 0).all())
+    assert bool((g["dk"][1, 64:128] == 0).all())
+    # dv there is w_r (.) dy alone
+    assert torch.equal(g["dv"][1, 64:128], t["w_r"] * t["dy"][1, 64:128])
+    for n, z in [("y", y), ("H", H)] + list(g.items()):
+        assert bool(torch.isfinite(z).all()), n
+    y1, H1 = m2.m2rnn_ssm_step(*(z[:, 70].contiguous() if z.dim() > 2 else z for z in x), t["H0"])
+    assert torch.equal(H1[1], t["H0"][1]) and bool(torch.isfinite(y1).all())
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("size", [(1, 1, 1, 16, 16), (3, 4, 2, 48, 32), (2, 6, 1, 128, 128), (5, 2, 2, 64, 64)])
 def test_steps_follow_the_scan(size, dtype):
