@@ -1288,7 +1288,7 @@ __global__ void __launch_bounds__(64 * kSsmBwdWaves, KP == 128 ? 1 : 2) m2rnn_ss
   constexpr int OV = 0, OU = NP * L * STV, OR = OU + 3 * L * STV, BUF = OR + 3 * V * STR;  // one buffer, in elements
   constexpr int POOL = 2 * BUF * 2 > L * KP * 4 ? 2 * BUF : L * KP * 2;
   struct Small {
-    double row[L], col[L], a[KM][L], b[KM][L], rh[KM];
+    double row[L], col[L], a[KM][L], b[L], rh[KM][64];
     float dg[L], dw[NI][V];
   };
   __shared__ __attribute__((aligned(16))) uint16_t sk[NP * L * STK];
@@ -1390,17 +1390,16 @@ __global__ void __launch_bounds__(64 * kSsmBwdWaves, KP == 128 ? 1 : 2) m2rnn_ss
       col = sm.col[lane];
       diag = sm.dg[lane];
       delta = tab.d[lane];
+      bb = sm.b[lane];
 #pragma unroll
-      for (int m = 0; m < KM; ++m) {
-        aa += sm.a[m][lane];
-        bb += sm.b[m][lane];
-      }
+      for (int m = 0; m < KM; ++m) aa += sm.a[m][lane];
     }
+    // <R, H>, a term of every g_t, as 64 parts: lane l's part reaches the steps up to l with x and those past l with y
 #pragma unroll
-    for (int m = 0; m < KM; ++m) through += sm.rh[m];
+    for (int m = 0; m < KM; ++m) through += sm.rh[m][lane];
     through *= tab.e[L - 1];
-    const double x = row - (double)delta * (col - diag) + aa, y = (double)delta * bb;
-    const double gs = __shfl(prefix64(__shfl(x, 63 - lane)), 63 - lane) + prefix64(dpp64<0x138, 0xF>(y)) + through;
+    const double x = row - (double)delta * (col - diag) + aa + through, y = (double)delta * bb + through;
+    const double gs = __shfl(prefix64(__shfl(x, 63 - lane)), 63 - lane) + prefix64(dpp64<0x138, 0xF>(y));
     // sigma(z) = 1 - e^{-softplus(z)}
     const float da = live ? (float)(col + bb - (double)A.alpha[h] * gs) * -expm1f(-delta) : 0.0f;
     if (lane < L && t0 + lane < T) A.da[(row0 + lane) * N + h] = da;
@@ -1558,8 +1557,18 @@ __global__ void __launch_bounds__(64 * kSsmBwdWaves, KP == 128 ? 1 : 2) m2rnn_ss
         acc = mfma_planes<3, NP>(ro, ko, acc);
       }
       const float ej = tab.w[16 * Jt + n];
+      float uj[4], vj[4];
+      lds_vals4<3>(su + (16 * Jt + n) * STV + 4 * g, L * STV, uj);
+      lds_vals4<NP>(sv + (16 * Jt + n) * STV + 4 * g, L * STV, vj);
+      // k_j . R v_j as v_j . R^T k_j, whose right side is here
+      float bj = 0.0f;
 #pragma unroll
-      for (int r = 0; r < 4; ++r) acc[r] *= ej;
+      for (int r = 0; r < 4; ++r) {
+        acc[r] *= ej;
+        bj = __builtin_fmaf(acc[r], vj[r], bj);
+      }
+      const double bs = group_sum64((double)bj);
+      if (g == 0) sm.b[16 * Jt + n] = bs;
 #pragma unroll
       for (int s = 0; s < NS; ++s) {
         if (2 * s + 1 < Jt) continue;
@@ -1571,9 +1580,6 @@ __global__ void __launch_bounds__(64 * kSsmBwdWaves, KP == 128 ? 1 : 2) m2rnn_ss
         }
         acc = mfma_planes<3, 3>(uo, po, acc);
       }
-      float uj[4], vj[4];
-      lds_vals4<3>(su + (16 * Jt + n) * STV + 4 * g, L * STV, uj);
-      lds_vals4<NP>(sv + (16 * Jt + n) * STV + 4 * g, L * STV, vj);
       const int t = t0 + 16 * Jt + n;
       if (t < T)
         *(float4*)(A.dv + ((long)b * T + t) * vrow + (long)h * V + 4 * g) =
@@ -1595,27 +1601,17 @@ __global__ void __launch_bounds__(64 * kSsmBwdWaves, KP == 128 ? 1 : 2) m2rnn_ss
         double dot = 0.0;  // <R, H>: every step of the chunk gets it, so its error would add up in dalpha and dbeta
 #pragma unroll
         for (int e = 0; e < 4; ++e) dot = __builtin_fma((double)hx[e], (double)rx[e], dot);
-        dot = total64(dot);
-        if (lane == 0) sm.rh[mk + p] = dot;
-        double part[NI];
+        sm.rh[mk + p][lane] = dot;
 #pragma unroll
         for (int J = 0; J < NI; ++J) {
           uint2 vo[NP];
 #pragma unroll
           for (int i = 0; i < NP; ++i) vo[i] = *(const uint2*)(sv + (i * L + 16 * J + n) * STV + 4 * g);
-          f32x4 acc = mfma16_planes<3, NP>(ro, vo, f32x4{0, 0, 0, 0});
-          const float ej = tab.w[16 * J + n], dj = tab.d[16 * J + n];
-          float kv[4], dot4 = 0.0f;
-          lds_vals4<NP>(sk + (16 * J + n) * STK + 16 * (mk + p) + 4 * g, L * STK, kv);
+          const f32x4 acc = mfma16_planes<3, NP>(ro, vo, f32x4{0, 0, 0, 0});
+          const float ed = tab.w[16 * J + n] * tab.d[16 * J + n];
 #pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            acc[r] *= ej;
-            dot4 = __builtin_fmaf(kv[r], acc[r], dot4);
-            dki[p][J][r] = __builtin_fmaf(dj, acc[r], dki[p][J][r]);
-          }
-          part[J] = dot4;
+          for (int r = 0; r < 4; ++r) dki[p][J][r] = __builtin_fmaf(ed, acc[r], dki[p][J][r]);
         }
-        put_group_sums<NI>(sm.b[mk + p], part, g, n);
       }
       if (hasdq) {
         uint2 ho[3];
@@ -1626,17 +1622,16 @@ __global__ void __launch_bounds__(64 * kSsmBwdWaves, KP == 128 ? 1 : 2) m2rnn_ss
           uint2 uo[3];
 #pragma unroll
           for (int i = 0; i < 3; ++i) uo[i] = *(const uint2*)(su + (i * L + 16 * I + n) * STV + 4 * g);
-          f32x4 acc = mfma16_planes<3, 3>(ho, uo, f32x4{0, 0, 0, 0});
+          const f32x4 acc = mfma16_planes<3, 3>(ho, uo, f32x4{0, 0, 0, 0});
           const float e = tab.e[16 * I + n];
           float qf[4], dot4 = 0.0f;
           lds_vals4<NP>(sq + (16 * I + n) * STK + 16 * (mq + p) + 4 * g, L * STK, qf);
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
-            acc[r] *= e;
             dot4 = __builtin_fmaf(qf[r], acc[r], dot4);
-            dqi[p][I][r] += acc[r];
+            dqi[p][I][r] = __builtin_fmaf(e, acc[r], dqi[p][I][r]);
           }
-          part[I] = dot4;
+          part[I] = e * dot4;
         }
         put_group_sums<NI>(sm.a[mq + p], part, g, n);
       }
