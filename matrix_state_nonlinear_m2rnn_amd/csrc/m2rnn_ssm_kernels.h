@@ -491,11 +491,15 @@ __global__ void __launch_bounds__(HPW * VB * 4) m2rnn_ssm_state_kernel(SsmArgs A
     ssm_gate(lane < L && ch * L + lane < Tb, pa, alpha, beta, delta, lg);
     const double c = prefix64(lg);
     cl = lane64(c, L - 1);
-    if (lane < L) weight[buf][hw][lane] = REV ? exp2_((float)c) : delta * exp2_((float)(cl - c));
-    if (lane == 0) sdec[buf][hw] = exp2_((float)cl);
+    if constexpr (REV) {
+      if (lane < L) weight[buf][hw][lane] = exp2_((float)c);
+      if (lane == 0) sdec[buf][hw] = exp2_((float)cl);
+    } else {
+      if (lane < L) weight[buf][hw][lane] = delta * exp2_((float)(cl - c + dec));
+    }
   };
   const int ch0 = s_ * A.cps, ch1 = min(A.nch, ch0 + A.cps);
-  const int first = REV ? ch1 - 1 : ch0, step = REV ? -1 : 1, count = ch1 - ch0;
+  const int first = ch1 - 1, step = -1, count = ch1 - ch0;
   if (count > 0) {
     fetch_a(first);
     fetch(first);
@@ -512,10 +516,8 @@ __global__ void __launch_bounds__(HPW * VB * 4) m2rnn_ssm_state_kernel(SsmArgs A
           if (16 * m + 4 * g < K) *(float4*)(o + 16 * m + 4 * g) = make_float4(H[m][0], H[m][1], H[m][2], H[m][3]);
         if (preps && lane == 0 && cb == 0) A.cdec[((long)b * A.N + head) * A.nch + ch] = (float)dec;
       }
-      dec += cl;
-    } else {
-      dec += cl;
     }
+    dec += cl;
     __syncthreads();  // the previous chunk's reads are done
     tid = fresh(tid);
     g = fresh(g);
@@ -531,11 +533,13 @@ __global__ void __launch_bounds__(HPW * VB * 4) m2rnn_ssm_state_kernel(SsmArgs A
     }
     __syncthreads();
     if (c + 1 < count) fetch(ch + step);
-    const float dl = sdec[buf][hw];
+    if constexpr (REV) {
+      const float dl = sdec[buf][hw];
 #pragma unroll
-    for (int m = 0; m < KM; ++m)
+      for (int m = 0; m < KM; ++m)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) H[m][r] *= dl;
+        for (int r = 0; r < 4; ++r) H[m][r] *= dl;
+    }
 #pragma unroll
     for (int s = 0; s < NS; ++s) {
       if constexpr (!REV) {
