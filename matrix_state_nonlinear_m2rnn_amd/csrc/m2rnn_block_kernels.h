@@ -559,7 +559,8 @@ __global__ void __launch_bounds__(kBlkThreads) m2rnn_conv4_silu_bwd_kernel(const
 // The forward with the three inputs before the first step (win [B,3,C], oldest first; null: zeros) and
 // the window after each sequence's last step (of lens[b], clamped to [0, T]; null: T) out.  Steps
 // past a sequence's end are not read and give zeros.  Same layout as the forward; the threads of a
-// sequence's first chunk write its window.
+// sequence's first chunk write its window.  A short prompt is bound by latency (a prompt of 509 steps and
+// 2048 channels, fp32: 5.0 us with 4 steps a thread, 6.4 with the 16 that the forward stops at).
 template <bool BF16>
 __global__ void __launch_bounds__(kBlkThreads) m2rnn_conv4_silu_state_kernel(
     const void* __restrict__ x, const float* __restrict__ w, const float* __restrict__ bias,
@@ -632,7 +633,8 @@ __global__ void __launch_bounds__(kBlkThreads) m2rnn_conv4_silu_state_kernel(
   for (int t = max(t0, te); t < t1; ++t) store4_nt<BF16>(u, (row + t) * C + c, zero);
 }
 
-// One step: thread (b, 4 channels).  It reads its window before it writes the next, so win_out may be win.
+// One step: thread (b, 4 channels).  It reads its window before it writes the next, so win_out may be win.  1.5 to 2 us
+// for one sequence, a launch.
 template <bool BF16>
 __global__ void __launch_bounds__(kBlkThreads) m2rnn_conv4_silu_step_kernel(const void* x, const float* w,
                                                                              const float* bias, const void* win,

@@ -6,6 +6,9 @@
 // the device beforehand and a captured launch keeps its own list.  A workgroup takes one piece of one
 // tensor.  Squares are summed in fp64 (a gradient of 1e-25 or 1e25 neither vanishes nor overflows
 // when squared), in a fixed order: the same list gives the same bits.
+//
+// Measured, the gradients of 24 layers (4.07 GB in 288 fp32 tensors, three launches each): norm 0.60 ms, 6.8 TB/s;
+// scaling 1.59 ms, 5.1 TB/s read and written.  48 small tensors: 4.4 + 2.3 + 4.7 us, a launch each.
 #pragma once
 
 #include "m2rnn_stream.h"

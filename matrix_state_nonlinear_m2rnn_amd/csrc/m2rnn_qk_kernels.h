@@ -11,6 +11,10 @@
 // keys', and forms its pairs' sines and cosines once per token.  Angles are reduced to a quarter turn
 // in fp64 (a position of a million times the first frequency leaves no bit of an fp32 angle), then
 // the two series run in fp32.
+//
+// Measured: B2 T16384, 32 + 32 heads, K = R = 64, bf16: 104 to 108 us for 0.54 GB, 5.0 to 5.2 TB/s, the rate of a large
+// copy (4.8 to 5.0); the backward at B4 T4096, 16 + 16 heads, K = 128: 114 to 120 us and 5 us of sums, 5.6 TB/s.
+// Eight pairs a lane took 121 us, more waves or a prefetched next head no less.
 #pragma once
 
 #include "m2rnn_stream.h"

@@ -76,9 +76,10 @@ constexpr double kMaxThreads = 4294967295.0;  // of one launch
 constexpr int kMaxK = 128;
 
 // Waves that the forward and state launches aim for: three for each of the 1024 SIMDs, which is what their
-// registers and LDS let a CU hold (B2 N32 T16384 K=V=64: 242 us, against 253 with two and 272 with four).
+// registers and LDS let a CU hold (B2 N32 T16384 K=V=64, when the whole scan took 242 us: 253 with two, 272 with four).
 constexpr long kSsmWaves = 3L * 1024;
-// A segment is at least this many chunks: shorter ones spend their time filling the pipeline.
+// A segment is at least this many chunks: with single ones a prompt of 509 tokens (16 heads, K = V = 128, fp32) takes the
+// same time (32 us for its three kernels), with twice the segments' states to write and combine.
 constexpr int kSsmMinChunks = 2;
 // Workgroups that the backward's launch aims for where a group's heads can be split.
 constexpr long kSsmBwdGroups = 512;
@@ -232,9 +233,9 @@ int run_fwd(const m2rnn_dims* d, int dtype, const void* q, const void* k, const 
   return status(e);
 }
 
-template <int VC>
+template <int V>
 const void* step_kernel(bool bf16) {
-  return bf16 ? (const void*)&m2rnn_ssm_step_kernel<true, VC> : (const void*)&m2rnn_ssm_step_kernel<false, VC>;
+  return bf16 ? (const void*)&m2rnn_ssm_step_kernel<true, V> : (const void*)&m2rnn_ssm_step_kernel<false, V>;
 }
 
 }  // namespace
@@ -376,13 +377,12 @@ int m2rnn_ssm_step(const m2rnn_dims* dims, int qkv_dtype, const void* q, const v
   if (H_in && in != out && in < out + state && out < in + state) return M2RNN_EINVAL;
   const bool bf = qkv_dtype == M2RNN_DTYPE_BF16;
   const int N = (int)dims->N, G = dims->Nqk ? (int)dims->Nqk : N, K = (int)dims->K, V = (int)dims->V;
-  const int VC = V;
-  const void* kern = VC == 16 ? step_kernel<16>(bf)
-                     : VC == 32 ? step_kernel<32>(bf)
-                     : VC == 64 ? step_kernel<64>(bf)
-                                : step_kernel<128>(bf);
-  void* args[] = {&q, &k, &v, &a, &alpha, &beta, &w_r, &H_in, &H_out, &y, (void*)&N, (void*)&G, (void*)&K, (void*)&V};
-  return status(hipLaunchKernel(kern, dim3((unsigned)(pairs * (V / VC))), dim3(256), args, 0, (hipStream_t)stream));
+  const void* kern = V == 16 ? step_kernel<16>(bf)
+                     : V == 32 ? step_kernel<32>(bf)
+                     : V == 64 ? step_kernel<64>(bf)
+                               : step_kernel<128>(bf);
+  void* args[] = {&q, &k, &v, &a, &alpha, &beta, &w_r, &H_in, &H_out, &y, (void*)&N, (void*)&G, (void*)&K};
+  return status(hipLaunchKernel(kern, dim3((unsigned)pairs), dim3(256), args, 0, (hipStream_t)stream));
 }
 
 }  // extern "C"

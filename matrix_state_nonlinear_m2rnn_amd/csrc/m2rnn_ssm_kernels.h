@@ -122,6 +122,10 @@ __device__ __forceinline__ void ssm_gate(bool live, float a, float alpha, float 
 // accumulator layout; that layout is also the operand layout of H^T q, so the state never moves.
 // HPW > 1 (V = 16 heads sharing q and k): one wave per head, q k^T formed once for all of them.
 // Otherwise the waves of a head share its masked and decayed q k^T through LDS.
+//
+// Bound by HBM and issue together: at B2 N32 T16384 K=V=64 (bf16) the kernel takes 161 to 190 us for 0.67 GB, 3.5 to
+// 4.2 TB/s, with a SIMD's VALU busy 60% of the cycles and its MFMA 23%; B4 N128 T4096 K=64 V=16 with one
+// query/key takes 112 to 121 us (with checkpoints), VALU 70% (each head's decays and splits for 16 columns).
 template <bool BF16, int KP, int VB, int HPW>
 __global__ void __launch_bounds__(HPW * VB * 4) m2rnn_ssm_fwd_kernel(SsmArgs A) {
   constexpr int L = ssm_chunk<BF16>(), NI = L / 16, NS = L / 32, KS = KP / 32, KM = KP / 16, NP = BF16 ? 1 : 3;
@@ -411,13 +415,18 @@ __global__ void __launch_bounds__(HPW * VB * 4) m2rnn_ssm_fwd_kernel(SsmArgs A) 
 
 // ------------------------------------------------------------------ what a segment adds to the state
 
-// REV = false: seg = sum over the segment's steps of their decayed D_j k_j v_j^T, as [K,V].
-// REV = true: the gradient's state R, chunks last to first, seg = sum of the decayed q_i dy_i^T that
+// Both walk their segment's chunks last to first.
+// REV = false: seg = sum over the segment's steps of their decayed D_j k_j v_j^T, as [K,V].  A step's weight holds the
+// decay to the segment's end, so the sum is never decayed, and the rows read last are those that the forward
+// reads first (227 us for the 16K-token prompt, 231 in the forward's order with the state decayed each chunk).
+// REV = true: the gradient's state R, seg = sum of the decayed q_i dy_i^T that
 // leaves the segment backwards, as [V,K]; before each chunk the part accumulated so far (what the
 // segment's later chunks send to it) goes to rloc, and its log2 decay to cdec.
 // Work split as in the forward.  The weights multiply v (or dy) in the operand.  dy, in fp32, goes straight
 // from HBM into the operands (a lane's column of 16, rows of 64 bytes), since its planes would need three
-// times v's LDS.  The decays of the next chunk are formed beside the products of this one.
+// times v's LDS.  The decays of the next chunk are formed beside the products of this one.  Bound by
+// HBM and its latency: 66 to 72 us for k and v of B2 N32 T16384 K=V=64 (3.7 to 4.1 TB/s), 42 to 45 us for the
+// reverse pass of B4 N16 T4096 (0.17 GB read and written).  Two chunks in flight instead of one took 71 us.
 template <bool BF16, int KP, int VB, int HPW, bool REV>
 __global__ void __launch_bounds__(HPW * VB * 4) m2rnn_ssm_state_kernel(SsmArgs A) {
   constexpr int L = ssm_chunk<BF16>(), NS = L / 32, KM = KP / 16, NP = BF16 ? 1 : 3;
@@ -602,7 +611,8 @@ __global__ void __launch_bounds__(HPW * VB * 4) m2rnn_ssm_state_kernel(SsmArgs A
 
 // seg[s] <- the state that enters segment s, from the segments' own parts: forwards from H0 (first to
 // last), in the reverse scan from dH_T (last to first, [V,K]), which also leaves dH0.  One thread
-// per element of a pair's state; the segments are few and their reads independent of the carry.
+// per element of a pair's state; the segments are few and their reads independent of the carry.  6 to 10 us,
+// a launch and three or four dependent trips to memory.
 template <bool REV>
 __global__ void __launch_bounds__(256) m2rnn_ssm_combine_kernel(SsmArgs A) {
   const long KV = (long)A.K * A.V;
@@ -686,7 +696,11 @@ __device__ __forceinline__ void ssm_decay_col(const SsmTab<L>& tab, int I, int J
 // P, column sums of M), five tiles for every wave: formed in both orientations, X needs no exchange
 // and only P goes through LDS.  H and R come from HBM straight into operands: each wave takes 16
 // of the K rows of H and R for the terms that enter and leave, 16 value columns for dv.
-// ONE: the workgroup has one head of one block, so nothing lives from one pass of the loop to the next.
+// ONE: the workgroup has one head of one block, so nothing lives from one pass of the loop to the next (B4 N16 T4096
+// K=V=64, bf16: 162 to 170 us, 0.55 GB moved at 3.3 TB/s).  Neither HBM nor issue is full (VALU 42%, MFMA 16%, LDS 35% of
+// the cycles): two workgroups of four waves a CU, by registers and LDS, wait for their products and barriers.
+// With several heads or blocks (!ONE) about 50 registers spill at VB = 64: N16 in groups of 4 heads takes as long
+// as one query/key each (304 and 313 us for the whole training step), V = 128 1.8 times V = 64.
 template <bool BF16, int KP, int VB, bool ONE>
 __global__ void __launch_bounds__(64 * kSsmBwdWaves, KP == 128 ? 1 : 2) m2rnn_ssm_bwd_kernel(SsmArgs A) {
   constexpr int L = ssm_chunk<BF16>(), NI = L / 16, NS = L / 32, KS = KP / 32, KM = KP / 16, NP = BF16 ? 1 : 3;
@@ -1278,9 +1292,14 @@ __device__ __forceinline__ f32x4 mfma16_planes_turned(const uint2 (&A)[NA], cons
 // its dv tile from its own P, so nothing is exchanged within a head: v, dy and R of the next head
 // go to the other half of a double buffer while this one is computed, one barrier a head.  Meanwhile wave 3
 // forms the next head's decay tables and wave 0 finishes the previous head's da, so waves 1 and 2 do
-// the staging (all four staging: 14.1 thousand cycles a head, of which waves 1 and 2 waited 2.6).  R is read
-// once, as planes in LDS that serve as R (transposing reads) and as R^T; H goes straight into the
+// the staging (all four staging: 14.1 thousand cycles a head, of which waves 1 and 2 waited 2.6; every other
+// assignment of the three tasks took 14 to 40 us more).  R is read once, as planes in LDS that serve as R (transposing reads) and as R^T; H goes straight into the
 // operand of the wave that owns its 16 K rows.  X is summed over the heads in registers.
+//
+// B4 N128 T4096 K=64 V=16, one query/key: 356 to 386 us, 12.3 thousand cycles a head for the two workgroups of a CU.
+// Bound by issue and latency at two waves a SIMD (256 VGPRs): VALU 55%, MFMA 17%, LDS 36% of the cycles, HBM at
+// 2.9 TB/s.  Of it the columns with P and dv take a third, the terms of H and R 47 us, the rows 33, loads 27,
+// da 25, the tables 8, the fp64 sums 9.
 template <bool BF16, int KP>
 __global__ void __launch_bounds__(64 * kSsmBwdWaves, KP == 128 ? 1 : 2) m2rnn_ssm_bwd_narrow_kernel(SsmArgs A) {
   constexpr int L = ssm_chunk<BF16>(), NI = L / 16, NS = L / 32, KS = KP / 32, KM = KP / 16, NP = BF16 ? 1 : 3;
@@ -1702,23 +1721,22 @@ __global__ void __launch_bounds__(64 * kSsmBwdWaves, KP == 128 ? 1 : 2) m2rnn_ss
 // ------------------------------------------------------------------ one token
 
 // One step for every (b, n), the state in HBM: reads it, advances it and writes it back, in place or
-// not (a thread reads its own elements before it writes them).  One workgroup per pair and VC of its
-// V columns; a thread owns four columns of every (256 / (VC / 4))-th row, so a wave's accesses are
-// whole rows of the block, and the readout's sum over rows ends in LDS.
-template <bool BF16, int VC>
+// not (a thread reads its own elements before it writes them).  One workgroup per pair; a thread owns four
+// columns of every (256 / (V / 4))-th row, so a wave's accesses are whole rows, and the readout's sum over
+// rows ends in LDS.  Bound by HBM: 128 sequences of 32 heads at K = V = 64 take 22 to 24 us (5.7 to 6.1 TB/s
+// of state read and written); one sequence of 128 heads takes 4 us, a launch and two trips to memory.
+template <bool BF16, int V>
 __global__ void __launch_bounds__(256) m2rnn_ssm_step_kernel(const void* q, const void* k, const void* v,
                                                              const float* a, const float* alpha, const float* beta,
                                                              const float* w_r, const float* H_in, float* H_out,
-                                                             float* y, int N, int G, int K, int V) {
-  constexpr int VQ = VC / 4, RP = 256 / VQ;  // column groups; rows per pass
-  __shared__ __attribute__((aligned(16))) float red[4][VC];
+                                                             float* y, int N, int G, int K) {
+  constexpr int VQ = V / 4, RP = 256 / VQ;  // column groups; rows per pass
+  __shared__ __attribute__((aligned(16))) float red[4][V];
   const int tid = threadIdx.x, w = tid >> 6;
-  const int CB = V / VC;
-  const long pair = blockIdx.x / CB;
-  const int cb = blockIdx.x % CB;
+  const long pair = blockIdx.x;
   const int head = (int)(pair % N);
   const long qk = (pair / N * G + head / (N / G)) * K;
-  const int c = cb * VC + (tid % VQ) * 4;
+  const int c = (tid % VQ) * 4;
   const int r0 = tid / VQ;
   float delta;
   double lg;
@@ -1762,11 +1780,9 @@ __global__ void __launch_bounds__(256) m2rnn_ssm_step_kernel(const void* q, cons
   }
   if ((tid & 63) < VQ) *(float4*)&red[w][(tid & 63) * 4] = acc;
   __syncthreads();
-  if (tid < VC) {
-    const int col = cb * VC + tid;
-    y[pair * V + col] =
-        ((red[0][tid] + red[1][tid]) + (red[2][tid] + red[3][tid])) + w_r[(long)head * V + col] * val(v, pair * V + col);
-  }
+  if (tid < V)
+    y[pair * V + tid] =
+        ((red[0][tid] + red[1][tid]) + (red[2][tid] + red[3][tid])) + w_r[(long)head * V + tid] * val(v, pair * V + tid);
 }
 
 }  // namespace m2rnn
