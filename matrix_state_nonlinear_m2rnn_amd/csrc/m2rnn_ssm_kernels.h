@@ -699,7 +699,7 @@ __device__ __forceinline__ void ssm_decay_col(const SsmTab<L>& tab, int I, int J
 // ONE: the workgroup has one head of one block, so nothing lives from one pass of the loop to the next (B4 N16 T4096
 // K=V=64, bf16: 162 to 170 us, 0.55 GB moved at 3.3 TB/s).  Neither HBM nor issue is full (VALU 42%, MFMA 16%, LDS 35% of
 // the cycles): two workgroups of four waves a CU, by registers and LDS, wait for their products and barriers.
-// With several heads or blocks (!ONE) about 50 registers spill at VB = 64: N16 in groups of 4 heads takes as long
+// With several heads or blocks (!ONE) 38 registers spill at K = VB = 64: N16 in groups of 4 heads takes as long
 // as one query/key each (304 and 313 us for the whole training step), V = 128 1.8 times V = 64.
 template <bool BF16, int KP, int VB, bool ONE>
 __global__ void __launch_bounds__(64 * kSsmBwdWaves, KP == 128 ? 1 : 2) m2rnn_ssm_bwd_kernel(SsmArgs A) {

@@ -166,3 +166,50 @@ def test_serving_a_padded_batch():
         got = torch.cat(ys[b]).cpu().numpy()
         assert rel_l2(got, ref[0]) <= 2e-5 and rel_l2(H[b].cpu().numpy(), HT[0]) <= 2e-5
         say("sequence", b, rel_l2(got, ref[0]), rel_l2(H[b].cpu().numpy(), HT[0]))
+
+
+def test_tokens_from_a_captured_graph():
+    """A token's calls captured once, the windows, the state and the position advanced in place: each replay
+    is the next token, bit for bit what the eager calls give."""
+    torch = torch_cuda()
+    import matrix_state_nonlinear_m2rnn_amd as m2
+    B, S, N, G, K, V = 3, 6, 4, 2, 32, 16
+    say("ssm tokens, captured")
+    d = layer_inputs(B, S, N, G, K, V, seed=78)
+    t = {n: torch.from_numpy(x).cuda() for n, x in d.items()}
+    xs = [{x: t["x" + x][:, s].contiguous() for x in "qkv"} | {"a": t["a"][:, s].contiguous()} for s in range(S)]
+
+    def fresh_state():
+        return ({x: torch.zeros(B, 3, t["x" + x].shape[2], device="cuda") for x in "qkv"},
+                torch.zeros(B, N, K, V, device="cuda"), torch.full((B, 1), 500, dtype=torch.int32, device="cuda"))
+
+    def token(x, win, H, pos):
+        u = {c: m2.m2rnn_conv4_silu_step(x[c], t["w" + c], t["b" + c], win[c], win_out=win[c])[0] for c in "qkv"}
+        q, k = m2.m2rnn_qk_norm_rope_fwd(u["q"].view(B, 1, G, K), u["k"].view(B, 1, G, K), t["gq"], t["gk"], pos,
+                                         t["freq"], EPS)
+        y, _ = m2.m2rnn_ssm_step(q.view(B, G, K), k.view(B, G, K), u["v"].view(B, N, V), x["a"], t["alpha"],
+                                 t["beta"], t["w_r"], H, H_out=H)
+        pos += 1
+        return y
+    win, H, pos = fresh_state()
+    want = []
+    for x in xs:
+        y = token(x, win, H, pos)
+        want.append((y.clone(), H.clone(), {c: win[c].clone() for c in "qkv"}))
+    torch.cuda.synchronize()
+
+    win, H, pos = fresh_state()
+    now = {c: torch.empty_like(x) for c, x in xs[0].items()}
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=torch.cuda.Stream()):
+        y = token(now, win, H, pos)
+    for s in range(S):
+        for c, x in xs[s].items():
+            now[c].copy_(x)
+        y.fill_(float("nan"))
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, want[s][0]) and torch.equal(H, want[s][1]), s
+        assert all(torch.equal(win[c], want[s][2][c]) for c in "qkv"), s
+    assert int(pos[0, 0]) == 500 + S
