@@ -705,6 +705,18 @@ def _call_on(dev, stream):
     return torch.cuda.device(dev)
 
 
+def _out(t, name, dtype, shape, like):
+    """The caller's output tensor, checked, or a new one on the device of `like` (the cheapest way to one if
+    `like` has its shape and dtype)."""
+    import torch
+    if t is not None:
+        _require(t, name, dtype, shape, like.device)
+        return t
+    if like.dtype is dtype and like.shape == shape:
+        return torch.empty_like(like)
+    return torch.empty(shape, dtype=dtype, device=like.device)
+
+
 def _ssm_dims(q, k, v, a, alpha, beta, w_r, token):
     """Checks the scan's inputs and returns (dims, dtype code).  token: no time axis."""
     import torch
@@ -749,13 +761,9 @@ def _ssm_fwd(q, k, v, a, alpha, beta, w_r, H0, lens, y, H_T, ckpt, keep, return_
     if lens is not None:
         _require(lens, "lens", torch.int32, (B,), dev)
     with _call_on(dev, stream):
-        if y is None:
-            y = torch.empty((B, T, N, V), dtype=torch.float32, device=dev)
-        _require(y, "y", torch.float32, (B, T, N, V), dev)
-        if H_T is None and return_state:
-            H_T = torch.empty((B, N, K, V), dtype=torch.float32, device=dev)
-        if H_T is not None:
-            _require(H_T, "H_T", torch.float32, (B, N, K, V), dev)
+        y = _out(y, "y", torch.float32, (B, T, N, V), v)
+        if H_T is not None or return_state:
+            H_T = _out(H_T, "H_T", torch.float32, (B, N, K, V), v if H0 is None else H0)
         nbytes = _size_query("m2rnn_ssm_fwd_workspace_size", ctypes.byref(dims), dt)
         ws = _workspace(nbytes, dev, workspace)
         args = [ctypes.byref(dims), dt, _ptr(q), _ptr(k), _ptr(v), _ptr(a), _ptr(alpha), _ptr(beta), _ptr(w_r),
@@ -764,9 +772,7 @@ def _ssm_fwd(q, k, v, a, alpha, beta, w_r, H0, lens, y, H_T, ckpt, keep, return_
             _check("m2rnn_ssm_fwd", lib().m2rnn_ssm_fwd(*args, _ptr(ws), nbytes, _stream(stream)))
             return y, H_T
         shape = (B, N, -(-T // ssm_checkpoint_interval(dt)), K, V)
-        if ckpt is None:
-            ckpt = torch.empty(shape, dtype=torch.float32, device=dev)
-        _require(ckpt, "ckpt", torch.float32, shape, dev)
+        ckpt = _out(ckpt, "ckpt", torch.float32, shape, v)
         _check("m2rnn_ssm_fwd_ckpt", lib().m2rnn_ssm_fwd_ckpt(*args, _ptr(ckpt), _ptr(ws), nbytes, _stream(stream)))
         return y, H_T, ckpt
 
@@ -810,9 +816,10 @@ def m2rnn_ssm_bwd(q, k, v, a, alpha, beta, w_r, ckpt, dy, dH_T=None, *, lens=Non
         if out is None:
             out = {x: torch.empty(s, dtype=torch.float32, device=dev) if x != "dH0" or want_dH0 else None
                    for x, s in shapes.items()}
-        for x, s in shapes.items():
-            if x != "dH0" or out.get(x) is not None:
-                _require(out.get(x), x, torch.float32, s, dev)
+        else:
+            for x, s in shapes.items():
+                if x != "dH0" or out.get(x) is not None:
+                    _require(out.get(x), x, torch.float32, s, dev)
         nbytes = _size_query("m2rnn_ssm_bwd_workspace_size", ctypes.byref(dims), dt)
         ws = _workspace(nbytes, dev, workspace)
         _check("m2rnn_ssm_bwd", lib().m2rnn_ssm_bwd(
@@ -834,12 +841,8 @@ def m2rnn_ssm_step(q, k, v, a, alpha, beta, w_r, H=None, *, H_out=None, y=None, 
     if H is not None:
         _require(H, "H", torch.float32, (B, N, K, V), dev)
     with _call_on(dev, stream):
-        if H_out is None:
-            H_out = torch.empty((B, N, K, V), dtype=torch.float32, device=dev)
-        _require(H_out, "H_out", torch.float32, (B, N, K, V), dev)
-        if y is None:
-            y = torch.empty((B, N, V), dtype=torch.float32, device=dev)
-        _require(y, "y", torch.float32, (B, N, V), dev)
+        H_out = _out(H_out, "H_out", torch.float32, (B, N, K, V), v if H is None else H)
+        y = _out(y, "y", torch.float32, (B, N, V), v)
         _check("m2rnn_ssm_step", lib().m2rnn_ssm_step(
             ctypes.byref(dims), dt, _ptr(q), _ptr(k), _ptr(v), _ptr(a), _ptr(alpha), _ptr(beta), _ptr(w_r), _ptr(H),
             _ptr(H_out), _ptr(y), _stream(stream)))
@@ -862,12 +865,8 @@ def m2rnn_conv4_silu_fwd_state(x, w, bias=None, win=None, *, lens=None, u=None, 
     if lens is not None:
         _require(lens, "lens", torch.int32, (B,), dev)
     with _call_on(dev, stream):
-        if u is None:
-            u = torch.empty_like(x)
-        _require(u, "u", x.dtype, (B, T, C), dev)
-        if win_out is None:
-            win_out = torch.empty((B, 3, C), dtype=x.dtype, device=dev)
-        _require(win_out, "win_out", x.dtype, (B, 3, C), dev)
+        u = _out(u, "u", x.dtype, (B, T, C), x)
+        win_out = _out(win_out, "win_out", x.dtype, (B, 3, C), x if win is None else win)
         _check("m2rnn_conv4_silu_fwd_state", lib().m2rnn_conv4_silu_fwd_state(
             B, T, C, _dtype_code(x), _ptr(x), _ptr(w), _ptr(bias), _ptr(lens), _ptr(win), _ptr(u), _ptr(win_out),
             _stream(stream)))
@@ -884,12 +883,8 @@ def m2rnn_conv4_silu_step(x, w, bias=None, win=None, *, u=None, win_out=None, st
     dev = x.device
     _conv_inputs(x, w, bias, win, (B, C))
     with _call_on(dev, stream):
-        if u is None:
-            u = torch.empty_like(x)
-        _require(u, "u", x.dtype, (B, C), dev)
-        if win_out is None:
-            win_out = torch.empty((B, 3, C), dtype=x.dtype, device=dev)
-        _require(win_out, "win_out", x.dtype, (B, 3, C), dev)
+        u = _out(u, "u", x.dtype, (B, C), x)
+        win_out = _out(win_out, "win_out", x.dtype, (B, 3, C), x if win is None else win)
         _check("m2rnn_conv4_silu_step", lib().m2rnn_conv4_silu_step(
             B, C, _dtype_code(x), _ptr(x), _ptr(w), _ptr(bias), _ptr(win), _ptr(u), _ptr(win_out), _stream(stream)))
     return u, win_out
@@ -937,12 +932,8 @@ def m2rnn_qk_norm_rope_fwd(q, k, gamma_q, gamma_k, pos, inv_freq, eps: float = 1
     import torch
     B, T, Nq, Nk, K, R, dev = _qk_inputs(q, k, gamma_q, gamma_k, pos, inv_freq)
     with _call_on(dev, stream):
-        if q_out is None:
-            q_out = torch.empty_like(q)
-        if k_out is None:
-            k_out = torch.empty_like(k)
-        _require(q_out, "q_out", q.dtype, (B, T, Nq, K), dev)
-        _require(k_out, "k_out", q.dtype, (B, T, Nk, K), dev)
+        q_out = _out(q_out, "q_out", q.dtype, (B, T, Nq, K), q)
+        k_out = _out(k_out, "k_out", q.dtype, (B, T, Nk, K), k)
         _check("m2rnn_qk_norm_rope_fwd", lib().m2rnn_qk_norm_rope_fwd(
             B, T, Nq, Nk, K, R, int(interleaved), _dtype_code(q), _ptr(q), _ptr(k), _ptr(gamma_q), _ptr(gamma_k),
             _ptr(pos), _ptr(inv_freq), float(eps), _ptr(q_out), _ptr(k_out), _stream(stream)))
@@ -961,8 +952,9 @@ def m2rnn_qk_norm_rope_bwd(q, k, gamma_q, gamma_k, pos, inv_freq, dq_out, dk_out
     with _call_on(dev, stream):
         if out is None:
             out = {n: torch.empty(s, dtype=torch.float32, device=dev) for n, s in shapes.items()}
-        for n, s in shapes.items():
-            _require(out.get(n), n, torch.float32, s, dev)
+        else:
+            for n, s in shapes.items():
+                _require(out.get(n), n, torch.float32, s, dev)
         nbytes = _size_query("m2rnn_qk_norm_rope_bwd_workspace_size", B, T, Nq, Nk, K)
         ws = _workspace(nbytes, dev, workspace)
         _check("m2rnn_qk_norm_rope_bwd", lib().m2rnn_qk_norm_rope_bwd(
@@ -981,7 +973,7 @@ def _tensor_list(tensors, name):
     if not tensors:
         raise ValueError(f"{name} is empty")
     codes = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16}
-    if not all(isinstance(t, torch.Tensor) for t in tensors):
+    if not all(issubclass(c, torch.Tensor) for c in set(map(type, tensors))):
         raise TypeError(f"{name} must hold torch.Tensors")
     dev = tensors[0].device
     if dev.type != "cuda":
@@ -989,7 +981,8 @@ def _tensor_list(tensors, name):
     # a list of thousands of tensors is ordinary: whole-list checks first, the culprit only if one fails
     T = torch.Tensor
     dtypes = [t.dtype for t in tensors]
-    if not (codes.keys() >= set(dtypes) and set(map(T.get_device, tensors)) == {dev.index}
+    kinds = set(dtypes)
+    if not (codes.keys() >= kinds and set(map(T.get_device, tensors)) == {dev.index}
             and all(map(T.is_contiguous, tensors))):
         for i, t in enumerate(tensors):
             if t.dtype not in codes:
@@ -1001,7 +994,7 @@ def _tensor_list(tensors, name):
     arr = (ctypes.c_int64 * (3 * len(tensors)))()
     arr[0::3] = list(map(T.data_ptr, tensors))
     arr[1::3] = list(map(T.numel, tensors))
-    arr[2::3] = [codes[d] for d in dtypes]
+    arr[2::3] = [codes[dtypes[0]]] * len(tensors) if len(kinds) == 1 else [codes[d] for d in dtypes]
     return tensors, arr, dev
 
 
