@@ -104,13 +104,14 @@ __device__ __forceinline__ void lds_vals4(const uint16_t* p, int plane, float (&
   planes_vals4<NP>(u, o);
 }
 
-// The step size and log2 decay of lane j's step from its gate pre-activation (live: within the
-// sequence and the chunk).
-__device__ __forceinline__ void ssm_gate(bool live, float a, float alpha, float beta, float& delta, double& lg) {
-  delta = 0.0f;
+// The step size, its derivative by a and the log2 decay of lane j's step from its gate pre-activation (live:
+// within the sequence and the chunk).
+__device__ __forceinline__ void ssm_gate(bool live, float a, float alpha, float beta, float& delta, float& sigma,
+                                         double& lg) {
+  delta = sigma = 0.0f;
   lg = 0.0;
   if (live) {
-    delta = softplus_exact(a + beta);
+    softplus_sigma(a + beta, delta, sigma);
     lg = log2_decay(alpha, delta);
   }
 }
@@ -199,14 +200,13 @@ __global__ void __launch_bounds__(HPW * VB * 4) m2rnn_ssm_fwd_kernel(SsmArgs A) 
   for (int ch = ch0; ch < ch1; ++ch) {
     const int t0 = ch * L;
     if (A.ckpt && mine) {
-      float* o = A.ckpt + (((long)b * A.N + head) * A.nch + ch) * K * V + c0 + n;
+      float* o = A.ckpt + (((long)b * A.N + head) * A.nch + ch) * K * V;
 #pragma unroll
-      for (int m = 0; m < KM; ++m)
+      for (int m = 0; m < KM; ++m) {
+        if (16 * m >= K) break;
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int kk = 16 * m + 4 * g + r;
-          if (kk < K) o[(long)kk * V] = H[m][r];
-        }
+        for (int r = 0; r < 4; ++r) o[(unsigned)((16 * m + 4 * g + r) * V + c0 + n)] = H[m][r];
+      }
     }
     if (t0 >= Tb) {  // past the sequence's end (the same for the whole workgroup): zeros, the state as it is
       if (mine) {
@@ -227,9 +227,9 @@ __global__ void __launch_bounds__(HPW * VB * 4) m2rnn_ssm_fwd_kernel(SsmArgs A) 
     pk.store(sk, tid);
     pv.store(sv, tid);
     if (preps) {
-      float delta;
+      float delta, sigma;
       double lg;
-      ssm_gate(lane < L && t0 + lane < Tb, pa, alpha, beta, delta, lg);
+      ssm_gate(lane < L && t0 + lane < Tb, pa, alpha, beta, delta, sigma, lg);
       ssm_tables<L, true>(tab[w / WPH], lane, delta, lg);
     }
     __syncthreads();
@@ -495,9 +495,9 @@ __global__ void __launch_bounds__(HPW * VB * 4) m2rnn_ssm_state_kernel(SsmArgs A
   double cl = 0.0;
   auto weights = [&](int ch, int buf) {
     if (!preps) return;
-    float delta;
+    float delta, sigma;
     double lg;
-    ssm_gate(lane < L && ch * L + lane < Tb, pa, alpha, beta, delta, lg);
+    ssm_gate(lane < L && ch * L + lane < Tb, pa, alpha, beta, delta, sigma, lg);
     const double c = prefix64(lg);
     cl = lane64(c, L - 1);
     if constexpr (REV) {
@@ -717,7 +717,7 @@ __global__ void __launch_bounds__(64 * kSsmBwdWaves, KP == 128 ? 1 : 2) m2rnn_ss
   __shared__ __attribute__((aligned(16))) uint16_t sqp[QW > PW ? QW : PW];  // q before and after the heads, P between
   __shared__ __attribute__((aligned(16))) uint16_t sv[NP * L * STV];
   __shared__ __attribute__((aligned(16))) uint16_t su[XW];                 // u; dq's or dk's entering terms at the end
-  __shared__ __attribute__((aligned(16))) SsmTab<L> tabs[2];
+  __shared__ __attribute__((aligned(16))) SsmTabBwd<L> tabs[2];
   __shared__ double rowp[L], colp[L], ap[KM][L], bp[KM][L], rh[KM];
   __shared__ float dgp[L], dwp[NI][VB];
   uint16_t* const sq = sqp;
@@ -766,11 +766,12 @@ __global__ void __launch_bounds__(64 * kSsmBwdWaves, KP == 128 ? 1 : 2) m2rnn_ss
     alpha = A.alpha[h];
     beta = A.beta[h];
   };
-  auto tables = [&](SsmTab<L>& tab) {
-    float delta;
+  auto tables = [&](SsmTabBwd<L>& tab) {
+    float delta, sigma;
     double lg;
-    ssm_gate(live, pa, alpha, beta, delta, lg);
+    ssm_gate(live, pa, alpha, beta, delta, sigma, lg);
     ssm_tables<L, false>(tab, lane, delta, lg);
+    if (lane < L) tab.s[lane] = sigma;
   };
   SsmPieces<BF16, L, KP, NTH> pq;
   auto fetch_q = [&]() {
@@ -910,7 +911,7 @@ __global__ void __launch_bounds__(64 * kSsmBwdWaves, KP == 128 ? 1 : 2) m2rnn_ss
   // da, and the partial sums of dalpha, dbeta and dw_r, of a block whose products are done
   auto finish = [&](int blk) {
     const int head = hb + blk / CB, cb = blk % CB;
-    const SsmTab<L>& tab = tabs[(blk / CB) & 1];
+    const SsmTabBwd<L>& tab = tabs[(blk / CB) & 1];
     if (w == 0) {
       const int t = lane;
       double row = 0.0, col = 0.0, diag = 0.0, aa = 0.0, bb = 0.0, through = 0.0, delta64 = 0.0;
@@ -934,8 +935,7 @@ __global__ void __launch_bounds__(64 * kSsmBwdWaves, KP == 128 ? 1 : 2) m2rnn_ss
       gsum += sx64 + prefix64(dpp64<0x138, 0xF>(y)) + through;
       dsum += col + bb;
       if (cb == CB - 1) {
-        // sigma(z) = 1 - e^{-softplus(z)}
-        const float da = live ? (float)(dsum - (double)A.alpha[head] * gsum) * -expm1f(-(float)delta64) : 0.0f;
+        const float da = live ? (float)(dsum - (double)A.alpha[head] * gsum) * tab.s[t] : 0.0f;
         if (t < L && t0 + t < T) A.da[(row0 + t) * N + head] = da;
         const double sb = prefix64(da), sa = prefix64(live ? -delta64 * gsum : 0.0);
         if (lane == 63) {
@@ -956,7 +956,7 @@ __global__ void __launch_bounds__(64 * kSsmBwdWaves, KP == 128 ? 1 : 2) m2rnn_ss
   for (int blk = 0; blk < blocks; ++blk) {
     const int head = hb + blk / CB, cb = blk % CB;
     const long pair = (long)b * N + head;
-    const SsmTab<L>& tab = tabs[(blk / CB) & 1];
+    const SsmTabBwd<L>& tab = tabs[(blk / CB) & 1];
     if (!ONE) {
       __syncthreads();  // the previous block's reads are done
       g = fresh(g);
@@ -1317,7 +1317,7 @@ __global__ void __launch_bounds__(64 * kSsmBwdWaves, KP == 128 ? 1 : 2) m2rnn_ss
   __shared__ __attribute__((aligned(16))) uint16_t sk[NP * L * STK];
   __shared__ __attribute__((aligned(16))) uint16_t sq[NP * L * STK];
   __shared__ __attribute__((aligned(16))) uint16_t pool[POOL];  // the double buffer; at the end the exchange of dq, dk
-  __shared__ __attribute__((aligned(16))) SsmTab<L> tabs[3];
+  __shared__ __attribute__((aligned(16))) SsmTabBwd<L> tabs[3];
   __shared__ Small small[2];
 
   const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, n = lane & 15;
@@ -1397,15 +1397,17 @@ __global__ void __launch_bounds__(64 * kSsmBwdWaves, KP == 128 ? 1 : 2) m2rnn_ss
   float pa = 0.0f;
   auto fetch_a = [&](int h) { pa = live ? A.a[(row0 + lane) * N + h] : 0.0f; };
   auto tables = [&](int h) {
-    float delta;
+    float delta, sigma;
     double lg;
-    ssm_gate(live, pa, A.alpha[h], A.beta[h], delta, lg);
-    ssm_tables<L, false>(tabs[(h - hb) % 3], lane, delta, lg);
+    SsmTabBwd<L>& tab = tabs[(h - hb) % 3];
+    ssm_gate(live, pa, A.alpha[h], A.beta[h], delta, sigma, lg);
+    ssm_tables<L, false>(tab, lane, delta, lg);
+    if (lane < L) tab.s[lane] = sigma;
   };
   // da, and the partial sums of dalpha, dbeta and dw_r, of a head whose products are done
   auto finish = [&](int h) {
     const Small& sm = small[(h - hb) & 1];
-    const SsmTab<L>& tab = tabs[(h - hb) % 3];
+    const SsmTabBwd<L>& tab = tabs[(h - hb) % 3];
     double row = 0.0, col = 0.0, diag = 0.0, aa = 0.0, bb = 0.0, through = 0.0;
     float delta = 0.0f;
     if (lane < L) {
@@ -1423,8 +1425,7 @@ __global__ void __launch_bounds__(64 * kSsmBwdWaves, KP == 128 ? 1 : 2) m2rnn_ss
     through *= tab.e[L - 1];
     const double x = row - (double)delta * (col - diag) + aa + through, y = (double)delta * bb + through;
     const double gs = __shfl(prefix64(__shfl(x, 63 - lane)), 63 - lane) + prefix64(dpp64<0x138, 0xF>(y));
-    // sigma(z) = 1 - e^{-softplus(z)}
-    const float da = live ? (float)(col + bb - (double)A.alpha[h] * gs) * -expm1f(-delta) : 0.0f;
+    const float da = live ? (float)(col + bb - (double)A.alpha[h] * gs) * tab.s[lane] : 0.0f;
     if (lane < L && t0 + lane < T) A.da[(row0 + lane) * N + h] = da;
     const double sb = prefix64(da), sa = prefix64(live ? -(double)delta * gs : 0.0);
     if (lane == 63) {
@@ -1493,7 +1494,7 @@ __global__ void __launch_bounds__(64 * kSsmBwdWaves, KP == 128 ? 1 : 2) m2rnn_ss
 
   for (int h = hb; h < he; ++h) {
     const int it = h - hb;
-    const SsmTab<L>& tab = tabs[it % 3];
+    const SsmTabBwd<L>& tab = tabs[it % 3];
     Small& sm = small[it & 1];
     uint16_t* const buf = pool + (it & 1) * BUF;
     const uint16_t *sv = buf + OV, *su = buf + OU, *sr = buf + OR;
@@ -1738,9 +1739,9 @@ __global__ void __launch_bounds__(256) m2rnn_ssm_step_kernel(const void* q, cons
   const long qk = (pair / N * G + head / (N / G)) * K;
   const int c = (tid % VQ) * 4;
   const int r0 = tid / VQ;
-  float delta;
+  float delta, sigma;
   double lg;
-  ssm_gate(true, a[pair], alpha[head], beta[head], delta, lg);
+  ssm_gate(true, a[pair], alpha[head], beta[head], delta, sigma, lg);
   const float f = exp2_((float)lg);
   auto val = [](const void* p, long i) {
     if constexpr (BF16) return bf16_lo_to_f32(((const uint16_t*)p)[i]);
