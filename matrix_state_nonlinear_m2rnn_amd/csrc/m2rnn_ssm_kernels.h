@@ -475,14 +475,22 @@ __global__ void __launch_bounds__(HPW * VB * 4) m2rnn_ssm_state_kernel(SsmArgs A
     const int t0 = ch * L, rows = min(L, Tb - t0);
     pk.load(kbase + (long)t0 * krow * (BF16 ? 2 : 4), krow, K, rows, tid);
     if constexpr (REV) {
-      const float* u = ubase + (long)t0 * vrow;
+      const float* u = ubase + (long)(t0 + 4 * g) * vrow + n;
+      const int last = mine ? rows - 4 * g : 0;
+      if (mine && rows == L) {  // (whole chunks without a test for each row)
 #pragma unroll
-      for (int s = 0; s < NS; ++s)
+        for (int s = 0; s < NS; ++s)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int j = 32 * s + 16 * (e / 4) + 4 * g + e % 4;
-          pu[s][e] = mine && j < rows ? u[j * vrow + n] : 0.0f;
-        }
+          for (int e = 0; e < 8; ++e) pu[s][e] = u[(32 * s + 16 * (e / 4) + e % 4) * vrow];
+      } else {
+#pragma unroll
+        for (int s = 0; s < NS; ++s)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const int j = 32 * s + 16 * (e / 4) + e % 4;
+            pu[s][e] = j < last ? u[j * vrow] : 0.0f;
+          }
+      }
     } else {
       pv.load(vbase + (long)t0 * vrow * (BF16 ? 2 : 4), vrow, vcols, rows, tid);
     }
