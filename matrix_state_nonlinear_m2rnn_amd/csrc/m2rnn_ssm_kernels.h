@@ -14,6 +14,7 @@
 #pragma once
 
 #include "m2rnn_ssm_device.h"
+#include "m2rnn_stream.h"
 
 namespace m2rnn {
 
@@ -124,9 +125,9 @@ __device__ __forceinline__ void ssm_gate(bool live, float a, float alpha, float 
 // HPW > 1 (V = 16 heads sharing q and k): one wave per head, q k^T formed once for all of them.
 // Otherwise the waves of a head share its masked and decayed q k^T through LDS.
 //
-// Bound by HBM and issue together: at B2 N32 T16384 K=V=64 (bf16) the kernel takes 161 to 190 us for 0.67 GB, 3.5 to
-// 4.2 TB/s, with a SIMD's VALU busy 60% of the cycles and its MFMA 23%; B4 N128 T4096 K=64 V=16 with one
-// query/key takes 112 to 121 us (with checkpoints), VALU 70% (each head's decays and splits for 16 columns).
+// Bound by HBM and issue together: at B2 N32 T16384 K=V=64 (bf16) the kernel takes 157 to 190 us for 0.70 GB, 3.7 to
+// 4.4 TB/s, with a SIMD's VALU busy 59% of the cycles and its MFMA 24%; B4 N128 T4096 K=64 V=16 with one
+// query/key takes 100 to 106 us (with checkpoints), VALU 73% (each head's decays and splits for 16 columns).
 template <bool BF16, int KP, int VB, int HPW>
 __global__ void __launch_bounds__(HPW * VB * 4) m2rnn_ssm_fwd_kernel(SsmArgs A) {
   constexpr int L = ssm_chunk<BF16>(), NI = L / 16, NS = L / 32, KS = KP / 32, KM = KP / 16, NP = BF16 ? 1 : 3;
@@ -425,7 +426,7 @@ __global__ void __launch_bounds__(HPW * VB * 4) m2rnn_ssm_fwd_kernel(SsmArgs A) 
 // Work split as in the forward.  The weights multiply v (or dy) in the operand.  dy, in fp32, goes straight
 // from HBM into the operands (a lane's column of 16, rows of 64 bytes), since its planes would need three
 // times v's LDS.  The decays of the next chunk are formed beside the products of this one.  Bound by
-// HBM and its latency: 66 to 72 us for k and v of B2 N32 T16384 K=V=64 (3.7 to 4.1 TB/s), 42 to 45 us for the
+// HBM and its latency: 65 to 72 us for k and v of B2 N32 T16384 K=V=64 (3.8 to 4.2 TB/s), 43 to 45 us for the
 // reverse pass of B4 N16 T4096 (0.17 GB read and written).  Two chunks in flight instead of one took 71 us.
 template <bool BF16, int KP, int VB, int HPW, bool REV>
 __global__ void __launch_bounds__(HPW * VB * 4) m2rnn_ssm_state_kernel(SsmArgs A) {
@@ -705,10 +706,10 @@ __device__ __forceinline__ void ssm_decay_col(const SsmTab<L>& tab, int I, int J
 // and only P goes through LDS.  H and R come from HBM straight into operands: each wave takes 16
 // of the K rows of H and R for the terms that enter and leave, 16 value columns for dv.
 // ONE: the workgroup has one head of one block, so nothing lives from one pass of the loop to the next (B4 N16 T4096
-// K=V=64, bf16: 162 to 170 us, 0.55 GB moved at 3.3 TB/s).  Neither HBM nor issue is full (VALU 42%, MFMA 16%, LDS 35% of
+// K=V=64, bf16: 163 to 175 us, 0.58 GB moved at 3.4 TB/s).  Neither HBM nor issue is full (VALU 42%, MFMA 16%, LDS 35% of
 // the cycles): two workgroups of four waves a CU, by registers and LDS, wait for their products and barriers.
 // With several heads or blocks (!ONE) 38 registers spill at K = VB = 64: N16 in groups of 4 heads takes as long
-// as one query/key each (304 and 313 us for the whole training step), V = 128 1.8 times V = 64.
+// as one query/key each (both about 0.3 ms for the whole training step), V = 128 1.8 times V = 64.
 template <bool BF16, int KP, int VB, bool ONE>
 __global__ void __launch_bounds__(64 * kSsmBwdWaves, KP == 128 ? 1 : 2) m2rnn_ssm_bwd_kernel(SsmArgs A) {
   constexpr int L = ssm_chunk<BF16>(), NI = L / 16, NS = L / 32, KS = KP / 32, KM = KP / 16, NP = BF16 ? 1 : 3;
@@ -1302,11 +1303,13 @@ __device__ __forceinline__ f32x4 mfma16_planes_turned(const uint2 (&A)[NA], cons
 // forms the next head's decay tables and wave 0 finishes the previous head's da, so waves 1 and 2 do
 // the staging (all four staging: 14.1 thousand cycles a head, of which waves 1 and 2 waited 2.6; every other
 // assignment of the three tasks took 14 to 40 us more).  R is read once, as planes in LDS that serve as R (transposing reads) and as R^T; H goes straight into the
-// operand of the wave that owns its 16 K rows.  X is summed over the heads in registers.
+// operand of the wave that owns its 16 K rows.  X is summed over the heads in registers.  H and R, read
+// once, are loaded past the caches (571 us for the training step below, 576 without), which leaves v's and dy's
+// lines in L2 for the next head's part of them.
 //
-// B4 N128 T4096 K=64 V=16, one query/key: 356 to 386 us, 12.3 thousand cycles a head for the two workgroups of a CU.
-// Bound by issue and latency at two waves a SIMD (256 VGPRs): VALU 55%, MFMA 17%, LDS 36% of the cycles, HBM at
-// 2.9 TB/s.  Of it the columns with P and dv take a third, the terms of H and R 47 us, the rows 33, loads 27,
+// B4 N128 T4096 K=64 V=16, one query/key: 343 to 371 us, about 12 thousand cycles a head for the two workgroups of a CU.
+// Bound by issue and latency at two waves a SIMD (256 VGPRs): VALU 54%, MFMA 18%, LDS 36% of the cycles, HBM at
+// 2.9 TB/s.  Of 366 us the columns with P and dv took a third, the terms of H and R 47 us, the rows 33, loads 27,
 // da 25, the tables 8, the fp64 sums 9.
 template <bool BF16, int KP>
 __global__ void __launch_bounds__(64 * kSsmBwdWaves, KP == 128 ? 1 : 2) m2rnn_ssm_bwd_narrow_kernel(SsmArgs A) {
@@ -1367,7 +1370,7 @@ __global__ void __launch_bounds__(64 * kSsmBwdWaves, KP == 128 ? 1 : 2) m2rnn_ss
       const int i = sid + p * NST, c = i / (KP / 4), kk = (i % (KP / 4)) * 4;
       pr[p] = pi[p] = make_float4(0, 0, 0, 0);
       if (c < V && kk < K) {
-        pr[p] = *(const float4*)(Rp + (unsigned)(c * K + kk));
+        pr[p] = load4_nt<false>(Rp, (unsigned)(c * K + kk));
         pi[p] = *(const float4*)(Ip + (unsigned)(c * K + kk));
       }
     }
@@ -1398,7 +1401,7 @@ __global__ void __launch_bounds__(64 * kSsmBwdWaves, KP == 128 ? 1 : 2) m2rnn_ss
     for (int p = 0; p < MPW; ++p) {
       const int kk = 16 * (mh + p) + n;
       ph[p] = make_float4(0, 0, 0, 0);
-      if (kk < K) ph[p] = *(const float4*)(Hp + (unsigned)(kk * V + 4 * g));
+      if (kk < K) ph[p] = load4_nt<false>(Hp, (unsigned)(kk * V + 4 * g));
     }
   };
   const bool live = lane < L && t0 + lane < Tb;
@@ -1732,7 +1735,7 @@ __global__ void __launch_bounds__(64 * kSsmBwdWaves, KP == 128 ? 1 : 2) m2rnn_ss
 // One step for every (b, n), the state in HBM: reads it, advances it and writes it back, in place or
 // not (a thread reads its own elements before it writes them).  One workgroup per pair; a thread owns four
 // columns of every (256 / (V / 4))-th row, so a wave's accesses are whole rows, and the readout's sum over
-// rows ends in LDS.  Bound by HBM: 128 sequences of 32 heads at K = V = 64 take 22 to 24 us (5.7 to 6.1 TB/s
+// rows ends in LDS.  Bound by HBM: 128 sequences of 32 heads at K = V = 64 take 23 to 24 us (5.7 to 6.0 TB/s
 // of state read and written); one sequence of 128 heads takes 4 us, a launch and two trips to memory.
 template <bool BF16, int V>
 __global__ void __launch_bounds__(256) m2rnn_ssm_step_kernel(const void* q, const void* k, const void* v,
