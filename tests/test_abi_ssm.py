@@ -106,3 +106,21 @@ def test_binding_refuses_before_the_library():
         m2.m2rnn_ssm_fwd(torch.zeros(1, 4, 3, 16), torch.zeros(1, 4, 3, 16), v, a, n, n, torch.zeros(4, 16))
     with pytest.raises(ValueError):
         m2.m2rnn_ssm_step(q, q, v, a, n, n, torch.zeros(4, 16))
+
+
+def test_binding_refuses_foreign_streams_and_workspaces():
+    torch = pytest.importorskip("torch")
+
+    class Stream:
+        device = torch.device("cuda", 0)
+        cuda_stream = 0
+    with pytest.raises(ValueError):  # a stream of another device than the inputs'
+        m2._call_on(torch.device("cuda", 1), Stream())
+    cpu = torch.device("cpu")
+    assert m2._workspace(0, cpu, None) is None
+    assert m2._workspace(16, cpu, torch.empty(16, dtype=torch.uint8)).numel() == 16
+    for bad in (torch.empty(15, dtype=torch.uint8), torch.empty(1).expand(100), torch.empty(64, 2)[:, 0]):
+        with pytest.raises(ValueError):  # too small, or more elements than bytes behind them
+            m2._workspace(16, cpu, bad)
+    with pytest.raises(ValueError):  # on the host, for inputs on a GPU
+        m2._workspace(16, torch.device("cuda", 0), torch.empty(64))

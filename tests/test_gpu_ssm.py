@@ -285,3 +285,26 @@ def test_graph_streams_and_dirty_workspaces():
         torch.cuda.synchronize()
         graph.replay()
         same(rep)
+
+
+def test_two_calls_at_once():
+    """Training pairs issued together on two streams, each with its binding-made workspaces and outputs, give the
+    bits of their solo runs."""
+    torch = torch_cuda()
+    import matrix_state_nonlinear_m2rnn_amd as m2
+    say("ssm two streams")
+    sets = [on_gpu(make(2, 1500, 6, g, 64, V, "bf16", seed=40 + V), "bf16") for g, V in ((1, 16), (3, 64))]
+    solo = [run(t) for t in sets]
+    streams = [torch.cuda.Stream() for _ in sets]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(4):
+        for t, s, o in zip(sets, streams, got):
+            x = [t[n] for n in ("q", "k", "v", "a", "alpha", "beta", "w_r")]
+            y, H, ckpt = m2.m2rnn_ssm_fwd_ckpt(*x, t["H0"], stream=s)
+            o.append(({"y": y, "H_T": H}, m2.m2rnn_ssm_bwd(*x, ckpt, t["dy"], t["dH_T"], stream=s), ckpt))
+    torch.cuda.synchronize()
+    for ref, runs in zip(solo, got):
+        for fwd, bwd, _ in runs:
+            for n, r in ref.items():
+                assert torch.equal(fwd.get(n, bwd.get(n)), r), n
