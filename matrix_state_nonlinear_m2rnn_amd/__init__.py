@@ -9,7 +9,6 @@ call raises.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 import sys
@@ -195,12 +194,15 @@ def _stream(stream) -> Optional[int]:
 
 
 def _require(t, name, dtype, shape, device):
-    import torch
     # what a correct call passes, at little cost; anything else is told apart below
-    if isinstance(t, torch.Tensor) and t.shape == shape and t.device == device and t.is_contiguous():
+    try:
         d = t.dtype
-        if d is dtype or (type(dtype) is tuple and d in dtype):
+        if ((d is dtype or (type(dtype) is tuple and d in dtype)) and t.shape == shape and t.device == device
+                and t.is_contiguous()):
             return
+    except AttributeError:
+        pass
+    import torch
     if t is None:
         raise ValueError(f"{name} is required")
     if not isinstance(t, torch.Tensor):
@@ -689,7 +691,10 @@ def m2rnn_conv4_silu_bwd(x, w, bias, du, *, workspace=None, stream=None) -> Dict
 
 # ---------------------------------------------------------------- selective state space scan
 
-_HERE_ALREADY = contextlib.nullcontext()
+def _elsewhere(dev, stream) -> bool:
+    """Whether a call has to change the current device or stream: it then makes itself again within _call_on."""
+    import torch
+    return stream is not None or torch.cuda.current_device() != dev.index
 
 
 def _call_on(dev, stream):
@@ -700,18 +705,29 @@ def _call_on(dev, stream):
         if stream.device != dev:
             raise ValueError(f"stream is on {stream.device}, the inputs are on {dev}")
         return torch.cuda.stream(stream)  # sets the stream's device too
-    if torch.cuda.current_device() == dev.index:
-        return _HERE_ALREADY
     return torch.cuda.device(dev)
+
+
+_raw_stream = None
+
+
+def _stream_of(dev) -> int:
+    """The current stream of the inputs' device."""
+    global _raw_stream
+    if _raw_stream is None:
+        import torch
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                              lambda index: torch.cuda.current_stream(index).cuda_stream)
+    return _raw_stream(dev.index)
 
 
 def _out(t, name, dtype, shape, like):
     """The caller's output tensor, checked, or a new one on the device of `like` (the cheapest way to one if
     `like` has its shape and dtype)."""
-    import torch
     if t is not None:
         _require(t, name, dtype, shape, like.device)
         return t
+    import torch
     if like.dtype is dtype and like.shape == shape:
         return torch.empty_like(like)
     return torch.empty(shape, dtype=dtype, device=like.device)
@@ -760,21 +776,23 @@ def _ssm_fwd(q, k, v, a, alpha, beta, w_r, H0, lens, y, H_T, ckpt, keep, return_
         _require(H0, "H0", torch.float32, (B, N, K, V), dev)
     if lens is not None:
         _require(lens, "lens", torch.int32, (B,), dev)
-    with _call_on(dev, stream):
-        y = _out(y, "y", torch.float32, (B, T, N, V), v)
-        if H_T is not None or return_state:
-            H_T = _out(H_T, "H_T", torch.float32, (B, N, K, V), v if H0 is None else H0)
-        nbytes = _size_query("m2rnn_ssm_fwd_workspace_size", ctypes.byref(dims), dt)
-        ws = _workspace(nbytes, dev, workspace)
-        args = [ctypes.byref(dims), dt, _ptr(q), _ptr(k), _ptr(v), _ptr(a), _ptr(alpha), _ptr(beta), _ptr(w_r),
-                _ptr(lens), _ptr(H0), _ptr(y), _ptr(H_T)]
-        if not keep:
-            _check("m2rnn_ssm_fwd", lib().m2rnn_ssm_fwd(*args, _ptr(ws), nbytes, _stream(stream)))
-            return y, H_T
-        shape = (B, N, -(-T // ssm_checkpoint_interval(dt)), K, V)
-        ckpt = _out(ckpt, "ckpt", torch.float32, shape, v)
-        _check("m2rnn_ssm_fwd_ckpt", lib().m2rnn_ssm_fwd_ckpt(*args, _ptr(ckpt), _ptr(ws), nbytes, _stream(stream)))
-        return y, H_T, ckpt
+    if _elsewhere(dev, stream):
+        with _call_on(dev, stream):
+            return _ssm_fwd(q, k, v, a, alpha, beta, w_r, H0, lens, y, H_T, ckpt, keep, return_state, workspace, None)
+    y = _out(y, "y", torch.float32, (B, T, N, V), v)
+    if H_T is not None or return_state:
+        H_T = _out(H_T, "H_T", torch.float32, (B, N, K, V), v if H0 is None else H0)
+    nbytes = _size_query("m2rnn_ssm_fwd_workspace_size", ctypes.byref(dims), dt)
+    ws = _workspace(nbytes, dev, workspace)
+    args = [ctypes.byref(dims), dt, _ptr(q), _ptr(k), _ptr(v), _ptr(a), _ptr(alpha), _ptr(beta), _ptr(w_r),
+            _ptr(lens), _ptr(H0), _ptr(y), _ptr(H_T)]
+    if not keep:
+        _check("m2rnn_ssm_fwd", lib().m2rnn_ssm_fwd(*args, _ptr(ws), nbytes, _stream_of(dev)))
+        return y, H_T
+    shape = (B, N, -(-T // ssm_checkpoint_interval(dt)), K, V)
+    ckpt = _out(ckpt, "ckpt", torch.float32, shape, v)
+    _check("m2rnn_ssm_fwd_ckpt", lib().m2rnn_ssm_fwd_ckpt(*args, _ptr(ckpt), _ptr(ws), nbytes, _stream_of(dev)))
+    return y, H_T, ckpt
 
 
 def m2rnn_ssm_fwd(q, k, v, a, alpha, beta, w_r, H0=None, *, lens=None, y=None, H_T=None, return_state: bool = True,
@@ -812,19 +830,22 @@ def m2rnn_ssm_bwd(q, k, v, a, alpha, beta, w_r, ckpt, dy, dH_T=None, *, lens=Non
         _require(lens, "lens", torch.int32, (B,), dev)
     shapes = {"dq": (B, T, Nqk, K), "dk": (B, T, Nqk, K), "dv": (B, T, N, V), "da": (B, T, N), "dalpha": (N,),
               "dbeta": (N,), "dw_r": (N, V), "dH0": (B, N, K, V)}
-    with _call_on(dev, stream):
-        if out is None:
-            out = {x: torch.empty(s, dtype=torch.float32, device=dev) if x != "dH0" or want_dH0 else None
-                   for x, s in shapes.items()}
-        else:
-            for x, s in shapes.items():
-                if x != "dH0" or out.get(x) is not None:
-                    _require(out.get(x), x, torch.float32, s, dev)
-        nbytes = _size_query("m2rnn_ssm_bwd_workspace_size", ctypes.byref(dims), dt)
-        ws = _workspace(nbytes, dev, workspace)
-        _check("m2rnn_ssm_bwd", lib().m2rnn_ssm_bwd(
-            ctypes.byref(dims), dt, _ptr(q), _ptr(k), _ptr(v), _ptr(a), _ptr(alpha), _ptr(beta), _ptr(w_r), _ptr(lens),
-            _ptr(ckpt), _ptr(dy), _ptr(dH_T), *(_ptr(out.get(x)) for x in shapes), _ptr(ws), nbytes, _stream(stream)))
+    if _elsewhere(dev, stream):
+        with _call_on(dev, stream):
+            return m2rnn_ssm_bwd(q, k, v, a, alpha, beta, w_r, ckpt, dy, dH_T, lens=lens, want_dH0=want_dH0,
+                                 workspace=workspace, out=out)
+    if out is None:
+        out = {x: torch.empty(s, dtype=torch.float32, device=dev) if x != "dH0" or want_dH0 else None
+               for x, s in shapes.items()}
+    else:
+        for x, s in shapes.items():
+            if x != "dH0" or out.get(x) is not None:
+                _require(out.get(x), x, torch.float32, s, dev)
+    nbytes = _size_query("m2rnn_ssm_bwd_workspace_size", ctypes.byref(dims), dt)
+    ws = _workspace(nbytes, dev, workspace)
+    _check("m2rnn_ssm_bwd", lib().m2rnn_ssm_bwd(
+        ctypes.byref(dims), dt, _ptr(q), _ptr(k), _ptr(v), _ptr(a), _ptr(alpha), _ptr(beta), _ptr(w_r), _ptr(lens),
+        _ptr(ckpt), _ptr(dy), _ptr(dH_T), *(_ptr(out.get(x)) for x in shapes), _ptr(ws), nbytes, _stream_of(dev)))
     return out
 
 
@@ -840,12 +861,14 @@ def m2rnn_ssm_step(q, k, v, a, alpha, beta, w_r, H=None, *, H_out=None, y=None, 
     dev = q.device
     if H is not None:
         _require(H, "H", torch.float32, (B, N, K, V), dev)
-    with _call_on(dev, stream):
-        H_out = _out(H_out, "H_out", torch.float32, (B, N, K, V), v if H is None else H)
-        y = _out(y, "y", torch.float32, (B, N, V), v)
-        _check("m2rnn_ssm_step", lib().m2rnn_ssm_step(
-            ctypes.byref(dims), dt, _ptr(q), _ptr(k), _ptr(v), _ptr(a), _ptr(alpha), _ptr(beta), _ptr(w_r), _ptr(H),
-            _ptr(H_out), _ptr(y), _stream(stream)))
+    if _elsewhere(dev, stream):
+        with _call_on(dev, stream):
+            return m2rnn_ssm_step(q, k, v, a, alpha, beta, w_r, H, H_out=H_out, y=y)
+    H_out = _out(H_out, "H_out", torch.float32, (B, N, K, V), v if H is None else H)
+    y = _out(y, "y", torch.float32, (B, N, V), v)
+    _check("m2rnn_ssm_step", lib().m2rnn_ssm_step(
+        ctypes.byref(dims), dt, _ptr(q), _ptr(k), _ptr(v), _ptr(a), _ptr(alpha), _ptr(beta), _ptr(w_r), _ptr(H),
+        _ptr(H_out), _ptr(y), _stream_of(dev)))
     return y, H_out
 
 
@@ -864,12 +887,14 @@ def m2rnn_conv4_silu_fwd_state(x, w, bias=None, win=None, *, lens=None, u=None, 
     _conv_inputs(x, w, bias, win, (B, T, C))
     if lens is not None:
         _require(lens, "lens", torch.int32, (B,), dev)
-    with _call_on(dev, stream):
-        u = _out(u, "u", x.dtype, (B, T, C), x)
-        win_out = _out(win_out, "win_out", x.dtype, (B, 3, C), x if win is None else win)
-        _check("m2rnn_conv4_silu_fwd_state", lib().m2rnn_conv4_silu_fwd_state(
-            B, T, C, _dtype_code(x), _ptr(x), _ptr(w), _ptr(bias), _ptr(lens), _ptr(win), _ptr(u), _ptr(win_out),
-            _stream(stream)))
+    if _elsewhere(dev, stream):
+        with _call_on(dev, stream):
+            return m2rnn_conv4_silu_fwd_state(x, w, bias, win, lens=lens, u=u, win_out=win_out)
+    u = _out(u, "u", x.dtype, (B, T, C), x)
+    win_out = _out(win_out, "win_out", x.dtype, (B, 3, C), x if win is None else win)
+    _check("m2rnn_conv4_silu_fwd_state", lib().m2rnn_conv4_silu_fwd_state(
+        B, T, C, _dtype_code(x), _ptr(x), _ptr(w), _ptr(bias), _ptr(lens), _ptr(win), _ptr(u), _ptr(win_out),
+        _stream_of(dev)))
     return u, win_out
 
 
@@ -882,11 +907,13 @@ def m2rnn_conv4_silu_step(x, w, bias=None, win=None, *, u=None, win_out=None, st
     B, C = x.shape
     dev = x.device
     _conv_inputs(x, w, bias, win, (B, C))
-    with _call_on(dev, stream):
-        u = _out(u, "u", x.dtype, (B, C), x)
-        win_out = _out(win_out, "win_out", x.dtype, (B, 3, C), x if win is None else win)
-        _check("m2rnn_conv4_silu_step", lib().m2rnn_conv4_silu_step(
-            B, C, _dtype_code(x), _ptr(x), _ptr(w), _ptr(bias), _ptr(win), _ptr(u), _ptr(win_out), _stream(stream)))
+    if _elsewhere(dev, stream):
+        with _call_on(dev, stream):
+            return m2rnn_conv4_silu_step(x, w, bias, win, u=u, win_out=win_out)
+    u = _out(u, "u", x.dtype, (B, C), x)
+    win_out = _out(win_out, "win_out", x.dtype, (B, 3, C), x if win is None else win)
+    _check("m2rnn_conv4_silu_step", lib().m2rnn_conv4_silu_step(
+        B, C, _dtype_code(x), _ptr(x), _ptr(w), _ptr(bias), _ptr(win), _ptr(u), _ptr(win_out), _stream_of(dev)))
     return u, win_out
 
 
@@ -931,12 +958,15 @@ def m2rnn_qk_norm_rope_fwd(q, k, gamma_q, gamma_k, pos, inv_freq, eps: float = 1
     inv_freq [R/2] float64; pairs (p, p + R/2), or (2p, 2p + 1) if interleaved.  Returns (q_out, k_out)."""
     import torch
     B, T, Nq, Nk, K, R, dev = _qk_inputs(q, k, gamma_q, gamma_k, pos, inv_freq)
-    with _call_on(dev, stream):
-        q_out = _out(q_out, "q_out", q.dtype, (B, T, Nq, K), q)
-        k_out = _out(k_out, "k_out", q.dtype, (B, T, Nk, K), k)
-        _check("m2rnn_qk_norm_rope_fwd", lib().m2rnn_qk_norm_rope_fwd(
-            B, T, Nq, Nk, K, R, int(interleaved), _dtype_code(q), _ptr(q), _ptr(k), _ptr(gamma_q), _ptr(gamma_k),
-            _ptr(pos), _ptr(inv_freq), float(eps), _ptr(q_out), _ptr(k_out), _stream(stream)))
+    if _elsewhere(dev, stream):
+        with _call_on(dev, stream):
+            return m2rnn_qk_norm_rope_fwd(q, k, gamma_q, gamma_k, pos, inv_freq, eps, interleaved=interleaved,
+                                          q_out=q_out, k_out=k_out)
+    q_out = _out(q_out, "q_out", q.dtype, (B, T, Nq, K), q)
+    k_out = _out(k_out, "k_out", q.dtype, (B, T, Nk, K), k)
+    _check("m2rnn_qk_norm_rope_fwd", lib().m2rnn_qk_norm_rope_fwd(
+        B, T, Nq, Nk, K, R, int(interleaved), _dtype_code(q), _ptr(q), _ptr(k), _ptr(gamma_q), _ptr(gamma_k),
+        _ptr(pos), _ptr(inv_freq), float(eps), _ptr(q_out), _ptr(k_out), _stream_of(dev)))
     return q_out, k_out
 
 
@@ -949,18 +979,21 @@ def m2rnn_qk_norm_rope_bwd(q, k, gamma_q, gamma_k, pos, inv_freq, dq_out, dk_out
     _require(dq_out, "dq_out", torch.float32, (B, T, Nq, K), dev)
     _require(dk_out, "dk_out", torch.float32, (B, T, Nk, K), dev)
     shapes = {"dq": (B, T, Nq, K), "dk": (B, T, Nk, K), "dgamma_q": (K,), "dgamma_k": (K,)}
-    with _call_on(dev, stream):
-        if out is None:
-            out = {n: torch.empty(s, dtype=torch.float32, device=dev) for n, s in shapes.items()}
-        else:
-            for n, s in shapes.items():
-                _require(out.get(n), n, torch.float32, s, dev)
-        nbytes = _size_query("m2rnn_qk_norm_rope_bwd_workspace_size", B, T, Nq, Nk, K)
-        ws = _workspace(nbytes, dev, workspace)
-        _check("m2rnn_qk_norm_rope_bwd", lib().m2rnn_qk_norm_rope_bwd(
-            B, T, Nq, Nk, K, R, int(interleaved), _dtype_code(q), _ptr(q), _ptr(k), _ptr(gamma_q), _ptr(gamma_k),
-            _ptr(pos), _ptr(inv_freq), float(eps), _ptr(dq_out), _ptr(dk_out), *(_ptr(out[n]) for n in shapes),
-            _ptr(ws), nbytes, _stream(stream)))
+    if _elsewhere(dev, stream):
+        with _call_on(dev, stream):
+            return m2rnn_qk_norm_rope_bwd(q, k, gamma_q, gamma_k, pos, inv_freq, dq_out, dk_out, eps,
+                                          interleaved=interleaved, workspace=workspace, out=out)
+    if out is None:
+        out = {n: torch.empty(s, dtype=torch.float32, device=dev) for n, s in shapes.items()}
+    else:
+        for n, s in shapes.items():
+            _require(out.get(n), n, torch.float32, s, dev)
+    nbytes = _size_query("m2rnn_qk_norm_rope_bwd_workspace_size", B, T, Nq, Nk, K)
+    ws = _workspace(nbytes, dev, workspace)
+    _check("m2rnn_qk_norm_rope_bwd", lib().m2rnn_qk_norm_rope_bwd(
+        B, T, Nq, Nk, K, R, int(interleaved), _dtype_code(q), _ptr(q), _ptr(k), _ptr(gamma_q), _ptr(gamma_k),
+        _ptr(pos), _ptr(inv_freq), float(eps), _ptr(dq_out), _ptr(dk_out), *(_ptr(out[n]) for n in shapes),
+        _ptr(ws), nbytes, _stream_of(dev)))
     return out
 
 
@@ -998,13 +1031,13 @@ def _tensor_list(tensors, name):
     return tensors, arr, dev
 
 
-def _grad_norm(arr, count, dev, norm, workspace, stream):
+def _grad_norm(arr, count, dev, norm, workspace):
     import torch
     if norm is None:
         norm = torch.empty((), dtype=torch.float32, device=dev)
     nbytes = _size_query("m2rnn_grad_norm_workspace_size", arr, count)
     ws = _workspace(nbytes, dev, workspace)
-    _check("m2rnn_grad_norm", lib().m2rnn_grad_norm(arr, count, _ptr(norm), _ptr(ws), nbytes, _stream(stream)))
+    _check("m2rnn_grad_norm", lib().m2rnn_grad_norm(arr, count, _ptr(norm), _ptr(ws), nbytes, _stream_of(dev)))
     return norm
 
 
@@ -1020,8 +1053,10 @@ def m2rnn_grad_norm(grads, *, norm=None, workspace=None, stream=None):
     grads, arr, dev = _tensor_list(grads, "grads")
     if norm is not None:
         _require_scalar(norm, dev)
-    with _call_on(dev, stream):
-        return _grad_norm(arr, len(grads), dev, norm, workspace, stream)
+    if _elsewhere(dev, stream):
+        with _call_on(dev, stream):
+            return m2rnn_grad_norm(grads, norm=norm, workspace=workspace)
+    return _grad_norm(arr, len(grads), dev, norm, workspace)
 
 
 def m2rnn_grad_clip(grads, max_norm: float, *, norm=None, out=None, workspace=None, stream=None):
@@ -1040,12 +1075,15 @@ def m2rnn_grad_clip(grads, max_norm: float, *, norm=None, out=None, workspace=No
         _, dst_arr, dst_dev = _tensor_list(out, "out")
         if dst_dev != dev or dst_arr[1::3] != arr[1::3] or dst_arr[2::3] != arr[2::3]:
             raise ValueError("out must have the grads' sizes, dtypes and device")
-        dst = (ctypes.c_void_p * len(out))(*dst_arr[0::3])
+        dst = (ctypes.c_int64 * len(out))()
+        dst[:] = dst_arr[0::3]
     if norm is not None:
         _require_scalar(norm, dev)
-    with _call_on(dev, stream):
-        if norm is None:
-            norm = _grad_norm(arr, len(grads), dev, None, workspace, stream)
-        _check("m2rnn_grad_clip", lib().m2rnn_grad_clip(arr, len(grads), dst, _ptr(norm), float(max_norm),
-                                                        _stream(stream)))
+    if _elsewhere(dev, stream):
+        with _call_on(dev, stream):
+            return m2rnn_grad_clip(grads, max_norm, norm=norm, out=out, workspace=workspace)
+    if norm is None:
+        norm = _grad_norm(arr, len(grads), dev, None, workspace)
+    _check("m2rnn_grad_clip", lib().m2rnn_grad_clip(arr, len(grads), dst, _ptr(norm), float(max_norm),
+                                                    _stream_of(dev)))
     return norm
