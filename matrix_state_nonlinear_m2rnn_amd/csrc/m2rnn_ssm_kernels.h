@@ -1338,8 +1338,11 @@ __global__ void __launch_bounds__(64 * kSsmBwdWaves, KP == 128 ? 1 : 2) m2rnn_ss
   const int ch = unit % A.nch, bg = unit / A.nch;
   const int b = bg / A.G, grp = bg % A.G;
   const int K = A.K, T = A.T, N = A.N;
-  const int hpg = N / A.G, per = (hpg + A.HS - 1) / A.HS;
-  const int hb = grp * hpg + hs * per, he = min(grp * hpg + hpg, hb + per);
+  // this workgroup's heads: every HS-th of the group's, so that the workgroups of a chunk, which run side by side on
+  // one XCD, take the parts of a line of v, dy and dv (32 and 64 bytes a head) at about the same time (two runs of 64
+  // heads instead: 570 us for the training step of 128 heads, not 557)
+  const int hpg = N / A.G, heads = (hpg - hs + A.HS - 1) / A.HS;
+  auto head_of = [&](int it) { return grp * hpg + hs + it * A.HS; };
   const int t0 = ch * L;
   const int Tb = ssm_len(A, b);
   const int rows = min(L, Tb - t0);
@@ -1356,8 +1359,9 @@ __global__ void __launch_bounds__(64 * kSsmBwdWaves, KP == 128 ? 1 : 2) m2rnn_ss
   SsmPieces<false, L, V, NST> pu;
   float4 pr[RP], pi[RP];
   float idec;
-  auto fetch = [&](int h) {  // v, dy, R of head h
+  auto fetch = [&](int it) {  // v, dy, R of a head
     if (!stager) return;
+    const int h = head_of(it);
     const long off = row0 * vrow + (long)h * V;
     pv.load(BF16 ? (const void*)((const uint16_t*)A.v + off) : (const void*)((const float*)A.v + off), vrow, V, rows, sid);
     pu.load(A.dy + off, vrow, V, rows, sid);
@@ -1394,7 +1398,8 @@ __global__ void __launch_bounds__(64 * kSsmBwdWaves, KP == 128 ? 1 : 2) m2rnn_ss
     }
   };
   float4 ph[MPW], wr;
-  auto fetch_H = [&](int h) {
+  auto fetch_H = [&](int it) {
+    const int h = head_of(it);
     wr = *(const float4*)(A.w_r + (long)h * V + 4 * g);
     const float* Hp = A.ckpt + (((long)b * N + h) * A.nch + ch) * K * V;  // [K][V]
 #pragma unroll
@@ -1406,19 +1411,21 @@ __global__ void __launch_bounds__(64 * kSsmBwdWaves, KP == 128 ? 1 : 2) m2rnn_ss
   };
   const bool live = lane < L && t0 + lane < Tb;
   float pa = 0.0f;
-  auto fetch_a = [&](int h) { pa = live ? A.a[(row0 + lane) * N + h] : 0.0f; };
-  auto tables = [&](int h) {
+  auto fetch_a = [&](int it) { pa = live ? A.a[(row0 + lane) * N + head_of(it)] : 0.0f; };
+  auto tables = [&](int it) {
+    const int h = head_of(it);
     float delta, sigma;
     double lg;
-    SsmTabBwd<L>& tab = tabs[(h - hb) % 3];
+    SsmTabBwd<L>& tab = tabs[it % 3];
     ssm_gate(live, pa, A.alpha[h], A.beta[h], delta, sigma, lg);
     ssm_tables<L, false>(tab, lane, delta, lg);
     if (lane < L) tab.s[lane] = sigma;
   };
   // da, and the partial sums of dalpha, dbeta and dw_r, of a head whose products are done
-  auto finish = [&](int h) {
-    const Small& sm = small[(h - hb) & 1];
-    const SsmTabBwd<L>& tab = tabs[(h - hb) % 3];
+  auto finish = [&](int it) {
+    const int h = head_of(it);
+    const Small& sm = small[it & 1];
+    const SsmTabBwd<L>& tab = tabs[it % 3];
     double row = 0.0, col = 0.0, diag = 0.0, aa = 0.0, bb = 0.0, through = 0.0;
     float delta = 0.0f;
     if (lane < L) {
@@ -1452,10 +1459,8 @@ __global__ void __launch_bounds__(64 * kSsmBwdWaves, KP == 128 ? 1 : 2) m2rnn_ss
     }
   };
 
-  if (hb < he) {
-    fetch(hb);
-    if (w == NW - 1) fetch_a(hb);
-  }
+  fetch(0);
+  if (w == NW - 1) fetch_a(0);
   {
     SsmPieces<BF16, L, KP, NTH> pq, pk;
     const long off = row0 * krow + (long)grp * K;
@@ -1464,15 +1469,13 @@ __global__ void __launch_bounds__(64 * kSsmBwdWaves, KP == 128 ? 1 : 2) m2rnn_ss
     pk.store(sk, tid);
     pq.store(sq, tid);
   }
-  if (hb < he) {
-    if (w == NW - 1) {
-      tables(hb);
-      if (hb + 1 < he) fetch_a(hb + 1);
-    }
-    stage(pool);
-    fetch_H(hb);
-    if (hb + 1 < he) fetch(hb + 1);
+  if (w == NW - 1) {
+    tables(0);
+    if (1 < heads) fetch_a(1);
   }
+  stage(pool);
+  fetch_H(0);
+  if (1 < heads) fetch(1);
   __syncthreads();
   // q k^T of this wave's row and column tiles: the same for all heads
   f32x4 qkr[NI], qkc[NI], xr[NI], xc[NI], dqi[MPW][NI], dki[MPW][NI];
@@ -1503,15 +1506,15 @@ __global__ void __launch_bounds__(64 * kSsmBwdWaves, KP == 128 ? 1 : 2) m2rnn_ss
     }
   }
 
-  for (int h = hb; h < he; ++h) {
-    const int it = h - hb;
+  for (int it = 0; it < heads; ++it) {
+    const int h = head_of(it);
     const SsmTabBwd<L>& tab = tabs[it % 3];
     Small& sm = small[it & 1];
     uint16_t* const buf = pool + (it & 1) * BUF;
     const uint16_t *sv = buf + OV, *su = buf + OU, *sr = buf + OR;
     const int n = fresh(lane & 15), g = fresh(lane >> 4);  // (addresses formed per head, not held across them)
     const int It = fresh_s(w), Jt = fresh_s(NI == 4 ? w : w - 2);
-    if (w == 0 && h > hb) finish(h - 1);
+    if (w == 0 && it > 0) finish(it - 1);
 
     // rows It: X and the row sums of M
     if (hasI) {
@@ -1671,18 +1674,18 @@ __global__ void __launch_bounds__(64 * kSsmBwdWaves, KP == 128 ? 1 : 2) m2rnn_ss
         put_group_sums<NI>(sm.a[mq + p], part, g, n);
       }
     }
-    if (h + 1 < he) {
+    if (it + 1 < heads) {
       if (w == NW - 1) {
-        tables(h + 1);
-        if (h + 2 < he) fetch_a(h + 2);
+        tables(it + 1);
+        if (it + 2 < heads) fetch_a(it + 2);
       }
       stage(pool + ((it + 1) & 1) * BUF);
-      fetch_H(h + 1);
-      if (h + 2 < he) fetch(h + 2);
+      fetch_H(it + 1);
+      if (it + 2 < heads) fetch(it + 2);
     }
     __syncthreads();
   }
-  if (w == 0 && hb < he) finish(he - 1);
+  if (w == 0) finish(heads - 1);
 
   // dq and dk: X of all heads times k and q, by step tiles, plus the terms of H and R, by K tiles, through LDS
   float* const ex = (float*)pool;  // [L][KP]
