@@ -14,7 +14,6 @@
 #pragma once
 
 #include "m2rnn_ssm_device.h"
-#include "m2rnn_stream.h"
 
 namespace m2rnn {
 
@@ -1303,13 +1302,11 @@ __device__ __forceinline__ f32x4 mfma16_planes_turned(const uint2 (&A)[NA], cons
 // forms the next head's decay tables and wave 0 finishes the previous head's da, so waves 1 and 2 do
 // the staging (all four staging: 14.1 thousand cycles a head, of which waves 1 and 2 waited 2.6; every other
 // assignment of the three tasks took 14 to 40 us more).  R is read once, as planes in LDS that serve as R (transposing reads) and as R^T; H goes straight into the
-// operand of the wave that owns its 16 K rows.  X is summed over the heads in registers.  H and R, read
-// once, are loaded past the caches (571 us for the training step below, 576 without), which leaves v's and dy's
-// lines in L2 for the next head's part of them.
+// operand of the wave that owns its 16 K rows.  X is summed over the heads in registers.
 //
-// B4 N128 T4096 K=64 V=16, one query/key: 343 to 371 us, about 12 thousand cycles a head for the two workgroups of a CU.
-// Bound by issue and latency at two waves a SIMD (256 VGPRs): VALU 54%, MFMA 18%, LDS 36% of the cycles, HBM at
-// 2.9 TB/s.  Of 366 us the columns with P and dv took a third, the terms of H and R 47 us, the rows 33, loads 27,
+// B4 N128 T4096 K=64 V=16, one query/key: 344 to 366 us, 11.6 thousand cycles a head for the two workgroups of a CU.
+// Bound by issue and latency at two waves a SIMD (256 VGPRs): VALU 58%, MFMA 18%, LDS 38% of the cycles, HBM at
+// 2.4 TB/s.  Of an earlier 366 us the columns with P and dv took a third, the terms of H and R 47 us, the rows 33, loads 27,
 // da 25, the tables 8, the fp64 sums 9.
 template <bool BF16, int KP>
 __global__ void __launch_bounds__(64 * kSsmBwdWaves, KP == 128 ? 1 : 2) m2rnn_ssm_bwd_narrow_kernel(SsmArgs A) {
@@ -1374,7 +1371,7 @@ __global__ void __launch_bounds__(64 * kSsmBwdWaves, KP == 128 ? 1 : 2) m2rnn_ss
       const int i = sid + p * NST, c = i / (KP / 4), kk = (i % (KP / 4)) * 4;
       pr[p] = pi[p] = make_float4(0, 0, 0, 0);
       if (c < V && kk < K) {
-        pr[p] = load4_nt<false>(Rp, (unsigned)(c * K + kk));
+        pr[p] = *(const float4*)(Rp + (unsigned)(c * K + kk));
         pi[p] = *(const float4*)(Ip + (unsigned)(c * K + kk));
       }
     }
@@ -1406,7 +1403,7 @@ __global__ void __launch_bounds__(64 * kSsmBwdWaves, KP == 128 ? 1 : 2) m2rnn_ss
     for (int p = 0; p < MPW; ++p) {
       const int kk = 16 * (mh + p) + n;
       ph[p] = make_float4(0, 0, 0, 0);
-      if (kk < K) ph[p] = load4_nt<false>(Hp, (unsigned)(kk * V + 4 * g));
+      if (kk < K) ph[p] = *(const float4*)(Hp + (unsigned)(kk * V + 4 * g));
     }
   };
   const bool live = lane < L && t0 + lane < Tb;
