@@ -49,9 +49,9 @@ long piece_size(const m2rnn_tensor* g, int64_t count) {
 
 long pieces(int64_t numel, long piece) { return (numel + piece - 1) / piece; }
 
-// Calls f(args, workgroups, pieces before this launch) for each launch over the list.
+// Calls f(args, workgroups, pieces before this launch) for each launch over the list, from its end if `backwards`.
 template <typename F>
-int over_launches(const m2rnn_tensor* g, int64_t count, void* const* out, long piece, F&& f) {
+int over_launches(const m2rnn_tensor* g, int64_t count, void* const* out, long piece, bool backwards, F&& f) {
   GradArgs A{};
   A.piece = (int)piece;
   long before = 0, here = 0;
@@ -63,7 +63,8 @@ int over_launches(const m2rnn_tensor* g, int64_t count, void* const* out, long p
     std::fill(std::begin(A.bf16), std::end(A.bf16), 0u);
     return st;
   };
-  for (int64_t i = 0; i < count; ++i) {
+  for (int64_t j = 0; j < count; ++j) {
+    const int64_t i = backwards ? count - 1 - j : j;
     if (g[i].numel == 0) continue;
     const int t = A.tensors++;
     A.src[t] = g[i].data;
@@ -131,7 +132,7 @@ int m2rnn_grad_norm(const m2rnn_tensor* grads, int64_t count, float* norm, void*
   if (need > 0 && (!workspace || workspace_bytes < need || ((uintptr_t)workspace & 15u))) return M2RNN_EWORKSPACE;
   hipStream_t s = (hipStream_t)stream;
   double* part = (double*)workspace;
-  st = over_launches(grads, count, nullptr, piece_size(grads, count), [&](GradArgs& A, long groups, long before) {
+  st = over_launches(grads, count, nullptr, piece_size(grads, count), false, [&](GradArgs& A, long groups, long before) {
     A.part = part + before;
     hipLaunchKernelGGL(m2rnn_grad_norm_kernel, dim3((unsigned)groups), dim3(kBlkThreads), 0, s, A);
     return record_hip_status(hipGetLastError());
@@ -160,7 +161,9 @@ int m2rnn_grad_clip(const m2rnn_tensor* grads, int64_t count, void* const* out, 
     return M2RNN_EUNSUPPORTED;
   }
   hipStream_t s = (hipStream_t)stream;
-  return over_launches(grads, count, out, piece_size(grads, count), [&](GradArgs& A, long groups, long) {
+  // the tensors that the norm read last are the likeliest in the memory-side cache: they come first (4.07 GB: 2.19 ms
+  // with the norm, 2.21 in the norm's order)
+  return over_launches(grads, count, out, piece_size(grads, count), true, [&](GradArgs& A, long groups, long) {
     A.norm = norm;
     A.max_norm = max_norm;
     A.in_place = in_place;
