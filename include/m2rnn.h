@@ -369,7 +369,9 @@ int m2rnn_fwd_block(const m2rnn_dims* dims, int qkv_dtype, int math, int row_blo
  * x, u [B,T,C] in `dtype` (fp32 or bf16; u is rounded to nearest even for bf16), w [C,4] fp32,
  * bias [C] fp32 or NULL (none).  C a multiple of 4.  The backward takes du [B,T,C] fp32 and gives
  * dx [B,T,C], dw [C,4] and dbias [C] (NULL to skip) fp32, summed over batch and time.  Pointers
- * 16-byte aligned.
+ * 16-byte aligned.  T at most 2^31 - 257, B ceil(T/16) ceil(C/256) at most 2^31 - 1, and a launch holds fewer
+ * than 2^32 threads (B ceil(T/64) ceil(C/256) at most 2^26 - 4, in the backward with T/128); larger sizes:
+ * M2RNN_EUNSUPPORTED.
  */
 int m2rnn_conv4_silu_fwd(int64_t B, int64_t T, int64_t C, int dtype, const void* x, const float* w,
                          const float* bias, void* u, void* stream);
@@ -451,6 +453,7 @@ int m2rnn_ssm_step(const m2rnn_dims* dims, int qkv_dtype, const void* q, const v
  * In m2rnn_conv4_silu_fwd_state win and win_out must not overlap (M2RNN_EINVAL); T = 0 copies the
  * window.  m2rnn_conv4_silu_step takes x, u [B,C], and win_out may be win (any other overlap:
  * M2RNN_EINVAL).  x, u, win and win_out are aligned to four elements (8 bytes in bf16), w and bias to 16.
+ * Sizes as in m2rnn_conv4_silu_fwd; in the step, B C at most 2^34 - 1024.
  */
 int m2rnn_conv4_silu_fwd_state(int64_t B, int64_t T, int64_t C, int dtype, const void* x, const float* w,
                                const float* bias, const int32_t* lens, const void* win, void* u,

@@ -82,8 +82,9 @@ int check_conv(int64_t B, int64_t T, int64_t C, int dtype) {
   if (B < 0 || T < 0 || C <= 0) return M2RNN_EINVAL;
   if (dtype != M2RNN_DTYPE_F32 && dtype != M2RNN_DTYPE_BF16) return M2RNN_EINVAL;
   if (C % 4 != 0) return M2RNN_EUNSUPPORTED;
-  if (B > 2147483647 || T > 2147483647 || C > 2147483647) return M2RNN_EUNSUPPORTED;
-  // the kernels number their waves with an int
+  // the kernels number steps with an int, up to two chunks past the last one
+  if (B > 2147483647 || T > 2147483647 - 2 * kConvChunkBwd || C > 2147483647) return M2RNN_EUNSUPPORTED;
+  // and their waves too
   if ((double)B * ceil_div(T, kConvChunkMin) * ceil_div(C / 4, 64) > 2147483647.0) return M2RNN_EUNSUPPORTED;
   return M2RNN_OK;
 }
@@ -121,6 +122,9 @@ bool conv_aligned(int dtype, const void* x, const void* win, const void* u, cons
   const uintptr_t mask = dtype == M2RNN_DTYPE_BF16 ? 7 : 15;
   return (((uintptr_t)x | (uintptr_t)win | (uintptr_t)u | (uintptr_t)win_out) & mask) == 0;
 }
+
+// Whether a launch of so many workgroups stays below 2^32 threads.
+bool launchable(long blocks) { return blocks < (1L << 32) / kBlkThreads; }
 
 // Workgroups of the conv kernels: one wave per (b, chunk of `chunk` steps, 64 groups of 4 channels).
 long conv_blocks(int64_t B, int64_t T, int64_t C, int chunk) {
@@ -252,6 +256,7 @@ int m2rnn_conv4_silu_fwd(int64_t B, int64_t T, int64_t C, int dtype, const void*
   if (st) return st;
   const int chunk = conv_chunk(B, T, C, kConvChunkFwd);
   const long blocks = conv_blocks(B, T, C, chunk);
+  if (!launchable(blocks)) return M2RNN_EUNSUPPORTED;
   if (blocks == 0) return M2RNN_OK;
   if (!x || !w || !u) return M2RNN_EINVAL;
   const void* ps[] = {x, w, bias, u};
@@ -283,6 +288,7 @@ int m2rnn_conv4_silu_bwd(int64_t B, int64_t T, int64_t C, int dtype, const void*
   if (!w || !dw) return M2RNN_EINVAL;
   const int chunk = conv_chunk(B, T, C, kConvChunkBwd);
   const long blocks = conv_blocks(B, T, C, chunk);
+  if (!launchable(blocks)) return M2RNN_EUNSUPPORTED;
   if (blocks > 0 && (!x || !du || !dx)) return M2RNN_EINVAL;
   const void* ps[] = {x, w, bias, du, dx, dw, dbias};
   for (const void* p : ps)
@@ -310,6 +316,10 @@ int m2rnn_conv4_silu_fwd_state(int64_t B, int64_t T, int64_t C, int dtype, const
                                void* stream) {
   int st = check_conv(B, T, C, dtype);
   if (st) return st;
+  const int64_t Tc = T > 0 ? T : 1;
+  const int chunk = conv_chunk(B, Tc, C, kConvChunkFwd, kConvBatch);
+  const long blocks = conv_blocks(B, Tc, C, chunk);
+  if (!launchable(blocks)) return M2RNN_EUNSUPPORTED;
   if (B == 0) return M2RNN_OK;
   if (!w || !win_out || (T > 0 && (!x || !u))) return M2RNN_EINVAL;
   if (!conv_aligned(dtype, x, win, u, win_out) || !al16(w) || !al16(bias)) return M2RNN_EINVAL;
@@ -318,9 +328,6 @@ int m2rnn_conv4_silu_fwd_state(int64_t B, int64_t T, int64_t C, int dtype, const
   const uintptr_t bytes = (uintptr_t)B * 3 * C * (dtype == M2RNN_DTYPE_BF16 ? 2 : 4);
   const uintptr_t in = (uintptr_t)win, out = (uintptr_t)win_out;
   if (win && in < out + bytes && out < in + bytes) return M2RNN_EINVAL;
-  const int64_t Tc = T > 0 ? T : 1;
-  const int chunk = conv_chunk(B, Tc, C, kConvChunkFwd, kConvBatch);
-  const long blocks = conv_blocks(B, Tc, C, chunk);
   const auto kern = dtype == M2RNN_DTYPE_BF16 ? &m2rnn_conv4_silu_state_kernel<true>
                                               : &m2rnn_conv4_silu_state_kernel<false>;
   hipLaunchKernelGGL(kern, dim3((unsigned)blocks), dim3(kBlkThreads), 0, (hipStream_t)stream, x, w, bias,
@@ -332,6 +339,8 @@ int m2rnn_conv4_silu_step(int64_t B, int64_t C, int dtype, const void* x, const 
                           const void* win, void* u, void* win_out, void* stream) {
   int st = check_conv(B, 1, C, dtype);
   if (st) return st;
+  const long blocks = ceil_div(B * (C / 4), kBlkThreads);
+  if (!launchable(blocks)) return M2RNN_EUNSUPPORTED;
   if (B == 0) return M2RNN_OK;
   if (!x || !w || !u || !win_out) return M2RNN_EINVAL;
   if (!conv_aligned(dtype, x, win, u, win_out) || !al16(w) || !al16(bias)) return M2RNN_EINVAL;
@@ -340,8 +349,8 @@ int m2rnn_conv4_silu_step(int64_t B, int64_t C, int dtype, const void* x, const 
   if (win && in != out && in < out + bytes && out < in + bytes) return M2RNN_EINVAL;
   const auto kern = dtype == M2RNN_DTYPE_BF16 ? &m2rnn_conv4_silu_step_kernel<true>
                                               : &m2rnn_conv4_silu_step_kernel<false>;
-  hipLaunchKernelGGL(kern, dim3((unsigned)ceil_div(B * (C / 4), kBlkThreads)), dim3(kBlkThreads), 0,
-                     (hipStream_t)stream, x, w, bias, win, (long)B, (int)C, u, win_out);
+  hipLaunchKernelGGL(kern, dim3((unsigned)blocks), dim3(kBlkThreads), 0, (hipStream_t)stream, x, w, bias, win, (long)B,
+                     (int)C, u, win_out);
   return status(hipGetLastError());
 }
 

@@ -106,3 +106,25 @@ def test_conv_window():
         assert f(B=0) == m2.M2RNN_OK
     assert state(win=q, wo=q) == m2.M2RNN_EINVAL
     assert state(lens=P(258)) == m2.M2RNN_EINVAL
+
+
+def test_conv_sizes_that_no_launch_holds():
+    """Steps are numbered with ints, up to two chunks past the last one, and a launch holds fewer than 2^32 threads."""
+    L = m2.lib()
+    p, q = P(1 << 12), P(1 << 20)
+    calls = {
+        "fwd": lambda B, T, C: L.m2rnn_conv4_silu_fwd(B, T, C, 1, p, p, None, q, None),
+        "state": lambda B, T, C: L.m2rnn_conv4_silu_fwd_state(B, T, C, 1, p, p, None, None, None, q, q, None),
+        "bwd": lambda B, T, C: L.m2rnn_conv4_silu_bwd(B, T, C, 1, p, p, None, p, q, q, None, p, 1 << 40, None),
+        "step": lambda B, T, C: L.m2rnn_conv4_silu_step(B, C, 1, p, p, None, None, q, q, None),
+    }
+    last = (1 << 31) - 1
+    for name in ("fwd", "state", "bwd"):
+        for T in (last, last - 63, last - 255):
+            assert calls[name](1, T, 4) == m2.M2RNN_EUNSUPPORTED, (name, T)
+            assert calls[name](0, T, 4) == m2.M2RNN_EUNSUPPORTED, (name, T)
+        assert calls[name](1, 1 << 30, 4096) == m2.M2RNN_EUNSUPPORTED, name  # 2^27 waves or more
+    assert calls["step"](1 << 24, 1, 1024) == m2.M2RNN_EUNSUPPORTED         # 2^32 threads
+    assert calls["step"](1 << 31, 1, 4) == m2.M2RNN_EUNSUPPORTED
+    for name in ("fwd", "state"):
+        assert calls[name](0, last - 256, 4) == m2.M2RNN_OK                 # nothing to do, nothing launched
