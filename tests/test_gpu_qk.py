@@ -126,6 +126,37 @@ def test_rows_of_zeros_and_empty_batches():
     assert not g["dgamma_q"].any() and not g["dgamma_k"].any()
 
 
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("eps,scale", [(1e-30, 1.0), (1e-30, 1e15), (1e-6, 1e15), (1e-30, 1e-12), (1.0, 1e-18)])
+def test_magnitudes_and_small_eps(eps, scale, inter):
+    """Heads of 1e15 and of 1e-12, rows of zeros (padding) beside them: the same bounds as above."""
+    torch = torch_cuda()
+    import matrix_state_nonlinear_m2rnn_amd as m2
+    say("qk magnitudes", eps, scale, inter)
+    eps = float(np.float32(eps))
+    for B, T, Nq, Nk, K, R in ((2, 9, 5, 2, 64, 32), (1, 7, 3, 0, 16, 16), (1, 6, 1, 2, 112, 56)):
+        d = make(B, T, Nq, Nk, K, R, "f32", seed=K)
+        for x in ("q", "k"):
+            d[x] = (d[x] * np.float32(scale)).astype(np.float32)
+            d[x][:, 1:3] = 0.0
+        t = on_gpu(d, "f32")
+        args = (t["q"], t["k"], t["gq"], t["gk"], t["pos"], t["freq"])
+        qo, ko = m2.m2rnn_qk_norm_rope_fwd(*args, eps, interleaved=inter)
+        g = m2.m2rnn_qk_norm_rope_bwd(*args, t["dq"], t["dk"], eps, interleaved=inter)
+        for x, gamma, out, do, dx, dg in (("q", "gq", qo, "dq", g["dq"], g["dgamma_q"]),
+                                          ("k", "gk", ko, "dk", g["dk"], g["dgamma_k"])):
+            r = 1.0 / np.sqrt(np.mean(d[x].astype(np.float64) ** 2, axis=-1, keepdims=True) + eps)
+            ref = qk.norm_rope_fwd(d[x], d[gamma], d["pos"], d["freq"], eps, inter)
+            within(x + " out", out, ref, 24 * U * pair_sum(d[gamma] * d[x] * r, R, inter))
+            rdx, rdg = qk.norm_rope_bwd(d[x], d[gamma], d["pos"], d["freq"], eps, inter, d[do])
+            p = np.abs(d[gamma]) * pair_sum(d[do].astype(np.float64), R, inter)
+            within("d" + x, dx, rdx,
+                   64 * U * (r * p + r ** 3 * np.abs(d[x]) * np.mean(p * np.abs(d[x]), -1, keepdims=True)))
+            rows = B * T * d[x].shape[2]
+            within("dgamma " + x, dg, rdg,
+                   (rows + 64) * U * np.sum(p / np.abs(d[gamma]) * np.abs(d[x]) * r, axis=(0, 1, 2)))
+
+
 def test_graph_and_stream():
     torch = torch_cuda()
     import matrix_state_nonlinear_m2rnn_amd as m2
