@@ -471,7 +471,8 @@ int m2rnn_conv4_silu_step(int64_t B, int64_t C, int dtype, const void* x, const 
  *   [K] fp32; pos [B,T] int32 (any value, also negative); inv_freq [R/2] fp64, in radians per position.
  *   K a multiple of 16 up to 256, R a multiple of 8 up to K; Nq or Nk may be 0 (their pointers NULL).
  *   Angles are formed in fp64, so far positions keep their angle.  Pointers 16-byte aligned (pos 4).
- *   The squares of a head are summed in fp32 and must stay within it (|x| below 1e18).
+ *   eps >= 0 (a head of zeros with eps = 0 is 0/0: NaN); the squares of a head are summed in fp32 and must
+ *   stay within it (|x| below 1e18).
  * The backward takes the gradients of the outputs (fp32) and gives dq, dk (fp32) and dgamma_q, dgamma_k
  * [K], summed over batch, time and heads in a fixed order.
  */

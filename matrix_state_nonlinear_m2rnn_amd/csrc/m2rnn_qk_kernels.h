@@ -149,7 +149,8 @@ __global__ void __launch_bounds__(kBlkThreads) m2rnn_qk_norm_rope_kernel(QkArgs 
         ss = __builtin_fmaf(x[i], x[i], ss);
         gm[i] = isq ? gq[i] : gk[i];
       }
-      const float r = 1.0f / sqrtf(head_sum<LPH>(ss) * inv + A.eps);
+      const float root = sqrtf(head_sum<LPH>(ss) * inv + A.eps);
+      const float r = live ? 1.0f / root : 0.0f;  // (eps = 0: lanes without a feature would add 0 times infinity)
       float y[8], o[8];
       if constexpr (!BWD) {
 #pragma unroll
