@@ -409,8 +409,11 @@ int m2rnn_conv4_silu_bwd(int64_t B, int64_t T, int64_t C, int dtype, const void*
  *
  * Products run on the bf16 MFMA with fp32 accumulation, every computed fp32 operand (decayed scores,
  * states, gradients) and fp32 input split into three bf16 planes (24 bits), so results are those
- * of fp32 arithmetic; the sums of log decays within a chunk are formed in fp64.  Operands must lie
- * within the bf16 (= fp32) range; values below 2^-110 may lose low bits.
+ * of fp32 arithmetic; the sums of log decays within a chunk are formed in fp64.  Values below 2^-110
+ * may lose low bits.  a = -infinity masks a step (D = 0, f = 1).  Where any other value within a sequence is not
+ * finite, the forward's outputs that depend on it (y from its step on, H_T, later checkpoints) are not finite
+ * (an infinity may become NaN) and all others keep their bits; m2rnn_ssm_bwd expects finite values within the
+ * sequences, a = -infinity apart (one that is not may reach every gradient of its chunk and the sums over it).
  * Two calls on the same inputs give the same bits, and need not equal another segmentation's.
  *
  * m2rnn_ssm_bwd gives the gradients of L = sum <dy, y> + <dH_T, H_T>: dq, dk [B,T,Nqk,K] (summed

@@ -85,6 +85,26 @@ __device__ __forceinline__ void ssm_decay(const SsmTab<L>& tab, int I, int J, in
   }
 }
 
+// The forward's scores, tile (I, J) of q k^T times its decays and D_j (the table's f carries D_j).  Scores of later
+// steps are left out by selection, not by a factor 0, so what is not finite there stays there.
+template <int L>
+__device__ __forceinline__ void ssm_scores(const SsmTab<L>& tab, int I, int J, int g, int n, f32x4 qk, float (&o)[4]) {
+  if (I != J) {
+    ssm_decay<L, true>(tab, I, J, g, n, o);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) o[r] *= qk[r];
+  } else {
+    const float hi = tab.chi[16 * I + n], lo = tab.clo[16 * I + n];
+    const float4 h = *(const float4*)&tab.chi[16 * J + 4 * g];
+    const float4 l = *(const float4*)&tab.clo[16 * J + 4 * g];
+    const float4 d = *(const float4*)&tab.d[16 * J + 4 * g];
+    const float hj[4] = {h.x, h.y, h.z, h.w}, lj[4] = {l.x, l.y, l.z, l.w}, dj[4] = {d.x, d.y, d.z, d.w};
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      o[r] = 4 * g + r <= n ? qk[r] * (dj[r] * exp2_((hi - hj[r]) + (lo - lj[r]))) : 0.0f;
+  }
+}
+
 // Four values as NP bf16 planes put together again.
 template <int NP>
 __device__ __forceinline__ void planes_vals4(const uint2 (&u)[NP], float (&o)[4]) {
@@ -256,10 +276,8 @@ __global__ void __launch_bounds__(HPW * VB * 4) m2rnn_ssm_fwd_kernel(SsmArgs A) 
         int I, J;
         tri_tile(t, I, J);
         const f32x4 acc = qk_tile(I, J);
-        float d[4], x[4];
-        ssm_decay<L, true>(tb, I, J, g, n, d);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) x[r] = acc[r] * d[r];
+        float x[4];
+        ssm_scores<L>(tb, I, J, g, n, acc, x);
         uint2 pl[3];
         split3x4(x, pl);
         const int set = (I / 2) * (I / 2 + 1) + (I & 1) * (I / 2 + 1) + J / 2;
@@ -272,7 +290,11 @@ __global__ void __launch_bounds__(HPW * VB * 4) m2rnn_ssm_fwd_kernel(SsmArgs A) 
         int I, J;
         tri_tile(t, I, J);
         const f32x4 acc = qk_tile(I, J);
-        gbuf[t * 64 + lane] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+        // (later steps' products to zeros here, once for all heads: a factor 0 alone would let a NaN through)
+        float x[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) x[r] = I != J || 4 * g + r <= n ? acc[r] : 0.0f;
+        gbuf[t * 64 + lane] = make_float4(x[0], x[1], x[2], x[3]);
       }
       __syncthreads();
     }
@@ -312,6 +334,49 @@ __global__ void __launch_bounds__(HPW * VB * 4) m2rnn_ssm_fwd_kernel(SsmArgs A) 
 #pragma unroll
       for (int p = 0; p < 3; ++p) hp[s][p] = cat(x[p], y2[p]);
     }
+    // the state that leaves the chunk (the one that entered is in hp)
+    const float dl = tb.e[L - 1];
+#pragma unroll
+    for (int m = 0; m < KM; ++m)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) H[m][r] *= dl;
+#pragma unroll
+    for (int s = 0; s < NS; ++s) {
+      const float4 w0 = *(const float4*)&tb.w[32 * s + 4 * g], w1 = *(const float4*)&tb.w[32 * s + 16 + 4 * g];
+      const float x[8] = {vf[s][0] * w0.x, vf[s][1] * w0.y, vf[s][2] * w0.z, vf[s][3] * w0.w,
+                          vf[s][4] * w1.x, vf[s][5] * w1.y, vf[s][6] * w1.z, vf[s][7] * w1.w};
+      uint4 vs[3];
+      split3x8(x, vs);
+#pragma unroll
+      for (int m = 0; m < KM; ++m) {
+        uint4 ko[NP];
+#pragma unroll
+        for (int p = 0; p < NP; ++p) ko[p] = lds_col(sk + p * L * STK, STK, 32 * s, 16 * m, g, n);
+        H[m] = mfma_planes<NP, 3>(ko, vs, H[m]);
+      }
+    }
+    // A value of v that is not finite makes its column of the state NaN (also through a weight 0), but must not reach the
+    // steps before it, whose zero scores it meets in the same product.  The state shows such a chunk, so the others pay a
+    // comparison (0 to 2.5% of the kernel's time with the state formed before y): its products are taken without
+    // those values, and y is NaN from each column's first one on.
+    int bad = L;
+    const bool odd = __builtin_amdgcn_ballot_w64(H[0][0] != H[0][0]) != 0;
+    if (odd) {
+#pragma unroll
+      for (int s = 0; s < NS; ++s)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          if (fabsf(vf[s][e]) <= 3.4028234e38f) continue;
+          bad = min(bad, 32 * s + 16 * (e / 4) + 4 * g + e % 4);
+#pragma unroll
+          for (int p = 0; p < NP; ++p) {
+            unsigned* word = e / 2 == 0 ? &vop[s][p].x : e / 2 == 1 ? &vop[s][p].y : e / 2 == 2 ? &vop[s][p].z : &vop[s][p].w;
+            *word &= e % 2 ? 0x0000FFFFu : 0xFFFF0000u;
+          }
+        }
+      bad = min(bad, __shfl_xor(bad, 16));
+      bad = min(bad, __shfl_xor(bad, 32));
+    }
 #pragma unroll
     for (int I = 0; I < NI; ++I) {
       f32x4 acc = {0, 0, 0, 0};
@@ -344,17 +409,18 @@ __global__ void __launch_bounds__(HPW * VB * 4) m2rnn_ssm_fwd_kernel(SsmArgs A) 
           for (int hf = 0; hf < 2; ++hf) {
             const int J = 2 * s + hf;
             if (J <= I) {
-              f32x4 qk;
+              float x[4];
               if constexpr (SHARE_G) {
                 const float4 t4 = gbuf[(I * (I + 1) / 2 + J) * 64 + lane];
-                qk = f32x4{t4.x, t4.y, t4.z, t4.w};
+                float d[4];
+                ssm_decay<L, true>(tb, I, J, g, n, d);
+                x[0] = t4.x * d[0];
+                x[1] = t4.y * d[1];
+                x[2] = t4.z * d[2];
+                x[3] = t4.w * d[3];
               } else {
-                qk = qk_tile(I, J);
+                ssm_scores<L>(tb, I, J, g, n, qk_tile(I, J), x);
               }
-              float d[4], x[4];
-              ssm_decay<L, true>(tb, I, J, g, n, d);
-#pragma unroll
-              for (int r = 0; r < 4; ++r) x[r] = qk[r] * d[r];
               split3x4(x, half[hf]);
             } else {
 #pragma unroll
@@ -379,25 +445,16 @@ __global__ void __launch_bounds__(HPW * VB * 4) m2rnn_ssm_fwd_kernel(SsmArgs A) 
         *(float4*)(A.y + ((long)b * T + t) * vrow + (long)head * V + c0 + 4 * g) = o;
       }
     }
-    // the state that leaves the chunk
-    const float dl = tb.e[L - 1];
+    if (odd && mine) {  // (a lane's own stores to one address keep their order)
+      int first[4];
 #pragma unroll
-    for (int m = 0; m < KM; ++m)
+      for (int r = 0; r < 4; ++r) first[r] = __shfl(bad, 4 * g + r);
+      for (int I = 0; I < NI; ++I) {
+        const int t = t0 + 16 * I + n;
 #pragma unroll
-      for (int r = 0; r < 4; ++r) H[m][r] *= dl;
-#pragma unroll
-    for (int s = 0; s < NS; ++s) {
-      const float4 w0 = *(const float4*)&tb.w[32 * s + 4 * g], w1 = *(const float4*)&tb.w[32 * s + 16 + 4 * g];
-      const float x[8] = {vf[s][0] * w0.x, vf[s][1] * w0.y, vf[s][2] * w0.z, vf[s][3] * w0.w,
-                          vf[s][4] * w1.x, vf[s][5] * w1.y, vf[s][6] * w1.z, vf[s][7] * w1.w};
-      uint4 vs[3];
-      split3x8(x, vs);
-#pragma unroll
-      for (int m = 0; m < KM; ++m) {
-        uint4 ko[NP];
-#pragma unroll
-        for (int p = 0; p < NP; ++p) ko[p] = lds_col(sk + p * L * STK, STK, 32 * s, 16 * m, g, n);
-        H[m] = mfma_planes<NP, 3>(ko, vs, H[m]);
+        for (int r = 0; r < 4; ++r)
+          if (16 * I + n >= first[r] && t < Tb)
+            A.y[((long)b * T + t) * vrow + (long)head * V + c0 + 4 * g + r] = __builtin_nanf("");
       }
     }
   }
