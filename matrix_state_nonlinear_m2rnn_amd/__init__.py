@@ -999,12 +999,17 @@ def m2rnn_qk_norm_rope_bwd(q, k, gamma_q, gamma_k, pos, inv_freq, dq_out, dk_out
 
 # ---------------------------------------------------------------- gradient norm and clipping
 
-def _tensor_list(tensors, name):
-    """(the tensors, an array of m2rnn_tensor, their device) of a list of contiguous fp32/bf16 tensors."""
+def _tensor_list(tensors, name, norm=None):
+    """(the tensors, an array of m2rnn_tensor, their device) of a list of contiguous fp32/bf16 tensors; an empty
+    list is on the device of `norm`."""
     import torch
     tensors = list(tensors)
     if not tensors:
-        raise ValueError(f"{name} is empty")
+        if norm is None:
+            raise ValueError(f"{name} is empty: pass norm, whose device the call then takes")
+        if norm.device.type != "cuda":
+            raise ValueError("norm must be on a GPU (HIP) device")
+        return tensors, (ctypes.c_int64 * 1)(), norm.device
     codes = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16}
     if not all(issubclass(c, torch.Tensor) for c in set(map(type, tensors))):
         raise TypeError(f"{name} must hold torch.Tensors")
@@ -1049,8 +1054,9 @@ def _require_scalar(norm, dev):
 
 def m2rnn_grad_norm(grads, *, norm=None, workspace=None, stream=None):
     """The 2-norm over all elements of a list of contiguous fp32/bf16 tensors, as a float32 scalar on
-    their device."""
-    grads, arr, dev = _tensor_list(grads, "grads")
+    their device (written to `norm` if given).  An empty list, of a rank without gradients for instance, has norm 0 and
+    needs `norm`."""
+    grads, arr, dev = _tensor_list(grads, "grads", norm)
     if norm is not None:
         _require_scalar(norm, dev)
     if _elsewhere(dev, stream):
@@ -1063,8 +1069,8 @@ def m2rnn_grad_clip(grads, max_norm: float, *, norm=None, out=None, workspace=No
     """Scales the gradients by max_norm / norm where their norm exceeds max_norm, in place or into the
     tensors of `out`; returns the norm (float32 scalar on their device).  `norm`: an already known
     total (for instance combined over ranks), instead of these tensors' own.  A norm that is not finite
-    leaves the gradients as they are."""
-    grads, arr, dev = _tensor_list(grads, "grads")
+    leaves the gradients as they are.  An empty list needs `norm`, which is returned as it is."""
+    grads, arr, dev = _tensor_list(grads, "grads", norm)
     if not float(max_norm) >= 0.0:
         raise ValueError(f"max_norm must be >= 0, got {max_norm}")
     dst = None
@@ -1072,7 +1078,7 @@ def m2rnn_grad_clip(grads, max_norm: float, *, norm=None, out=None, workspace=No
         out = list(out)
         if len(out) != len(grads):
             raise ValueError(f"out has {len(out)} tensors, expected {len(grads)}")
-        _, dst_arr, dst_dev = _tensor_list(out, "out")
+        _, dst_arr, dst_dev = _tensor_list(out, "out", norm)
         if dst_dev != dev or dst_arr[1::3] != arr[1::3] or dst_arr[2::3] != arr[2::3]:
             raise ValueError("out must have the grads' sizes, dtypes and device")
         dst = (ctypes.c_int64 * len(out))()

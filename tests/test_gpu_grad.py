@@ -141,6 +141,27 @@ def test_a_given_norm_and_refusals():
         m2.m2rnn_grad_norm([])
 
 
+def test_empty_lists():
+    """A rank without gradients: norm 0, nothing to clip."""
+    torch = torch_cuda()
+    import matrix_state_nonlinear_m2rnn_amd as m2
+    norm = torch.full((), 7.0, device="cuda")
+    assert m2.m2rnn_grad_norm([], norm=norm) is norm and float(norm) == 0.0
+    norm.fill_(3.0)  # combined over ranks
+    for out in (None, []):
+        assert m2.m2rnn_grad_clip([], 1.0, norm=norm, out=out) is norm and float(norm) == 3.0
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    m2.m2rnn_grad_norm([], norm=norm, stream=s)
+    torch.cuda.synchronize()
+    assert float(norm) == 0.0
+    for bad in (lambda: m2.m2rnn_grad_norm([]), lambda: m2.m2rnn_grad_clip([], 1.0),
+                lambda: m2.m2rnn_grad_clip([], 1.0, norm=norm, out=[norm]), lambda: m2.m2rnn_grad_clip([norm], 1.0, out=[]),
+                lambda: m2.m2rnn_grad_norm([], norm=norm.cpu()), lambda: m2.m2rnn_grad_norm([], norm=norm.double())):
+        with pytest.raises(ValueError):
+            bad()
+
+
 def test_graph_and_stream():
     torch = torch_cuda()
     import matrix_state_nonlinear_m2rnn_amd as m2
