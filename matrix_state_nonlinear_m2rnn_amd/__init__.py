@@ -1009,7 +1009,7 @@ def _tensor_list(tensors, name, norm=None):
             raise ValueError(f"{name} is empty: pass norm, whose device the call then takes")
         if norm.device.type != "cuda":
             raise ValueError("norm must be on a GPU (HIP) device")
-        return tensors, (ctypes.c_int64 * 1)(), norm.device
+        return tensors, (ctypes.c_int64 * 0)(), norm.device
     codes = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16}
     if not all(issubclass(c, torch.Tensor) for c in set(map(type, tensors))):
         raise TypeError(f"{name} must hold torch.Tensors")
