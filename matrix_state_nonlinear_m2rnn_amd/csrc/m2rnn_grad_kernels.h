@@ -71,15 +71,28 @@ __device__ __forceinline__ void grad_each(u32x4 v, F&& f) {
     }
   }
 }
+// The clip factor as c * s, s a power of two: 1, or 2^-64 where the factor itself would be near or below fp32's smallest
+// normal number and lose bits (the products are then formed 2^64 larger, which no gradient within the norm overflows).
+struct GradFactor {
+  float c, s;
+  __device__ __forceinline__ float operator()(float x) const { return x * c * s; }
+};
+__device__ __forceinline__ GradFactor grad_factor(float norm, float max_norm) {
+  if (!(norm > max_norm && norm <= 3.4028234e38f)) return {1.0f, 1.0f};
+  const double f = (double)max_norm / (double)norm;
+  if (f < 0x1p-100) return {(float)(f * 0x1p64), 0x1p-64f};
+  return {(float)f, 1.0f};
+}
+
 template <bool BF16>
-__device__ __forceinline__ u32x4 grad_scaled(u32x4 v, float c) {
+__device__ __forceinline__ u32x4 grad_scaled(u32x4 v, GradFactor c) {
   u32x4 o;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     if constexpr (BF16)
-      o[i] = pack_bf16(bf16_lo_to_f32(v[i]) * c, bf16_hi_to_f32(v[i]) * c);
+      o[i] = pack_bf16(c(bf16_lo_to_f32(v[i])), c(bf16_hi_to_f32(v[i])));
     else
-      o[i] = __float_as_uint(__uint_as_float(v[i]) * c);
+      o[i] = __float_as_uint(c(__uint_as_float(v[i])));
   }
   return o;
 }
@@ -142,16 +155,16 @@ __global__ void __launch_bounds__(1024) m2rnn_grad_total_kernel(const double* pa
 }
 
 template <bool BF16>
-__device__ __forceinline__ void grad_scale(const char* p, char* o, long n, float c) {
+__device__ __forceinline__ void grad_scale(const char* p, char* o, long n, GradFactor c) {
   constexpr int E = BF16 ? 8 : 4, SZ = BF16 ? 2 : 4;
   long head = grad_head(p, SZ);
   // the vector path needs the same distance to a boundary on both sides
   if (head != grad_head(o, SZ)) {
-    for (long i = threadIdx.x; i < n; i += kBlkThreads) grad_put(o, i, grad_get(p, i, BF16) * c, BF16);
+    for (long i = threadIdx.x; i < n; i += kBlkThreads) grad_put(o, i, c(grad_get(p, i, BF16)), BF16);
     return;
   }
   head = head < n ? head : n;
-  if ((long)threadIdx.x < head) grad_put(o, threadIdx.x, grad_get(p, threadIdx.x, BF16) * c, BF16);
+  if ((long)threadIdx.x < head) grad_put(o, threadIdx.x, c(grad_get(p, threadIdx.x, BF16)), BF16);
   const long vecs = (n - head) / E;
   const u32x4* v = (const u32x4*)(p + head * SZ);
   u32x4* w = (u32x4*)(o + head * SZ);
@@ -159,15 +172,14 @@ __device__ __forceinline__ void grad_scale(const char* p, char* o, long n, float
   for (long i = threadIdx.x; i < vecs; i += kBlkThreads)
     __builtin_nontemporal_store(grad_scaled<BF16>(__builtin_nontemporal_load(v + i), c), w + i);
   const long tail = head + vecs * E + threadIdx.x;
-  if (tail < n) grad_put(o, tail, grad_get(p, tail, BF16) * c, BF16);
+  if (tail < n) grad_put(o, tail, c(grad_get(p, tail, BF16)), BF16);
 }
 
 // A norm that is not finite leaves the gradients as they are (the caller sees it in the norm and
 // skips the step), as does one within max_norm.
 __global__ void __launch_bounds__(kBlkThreads) m2rnn_grad_clip_kernel(GradArgs A) {
-  const float norm = *A.norm;
-  const float c = norm > A.max_norm && norm <= 3.4028234e38f ? (float)((double)A.max_norm / (double)norm) : 1.0f;
-  if (c == 1.0f && A.in_place) return;
+  const GradFactor c = grad_factor(*A.norm, A.max_norm);
+  if (c.c == 1.0f && c.s == 1.0f && A.in_place) return;
   const int t = grad_tensor(A, blockIdx.x);
   const long i0 = (long)(blockIdx.x - A.first[t]) * A.piece;
   const long n = min((long)A.piece, A.numel[t] - i0);

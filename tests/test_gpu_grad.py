@@ -98,6 +98,29 @@ def test_gradients_whose_squares_leave_fp32(scale):
         check(ts, max_norm, m2.m2rnn_grad_clip(ts, max_norm, out=out), out)
 
 
+@pytest.mark.parametrize("scale,max_norm", [(1e30, 1e-12), (1e25, 1e-14), (1e36, 1e-3), (1e30, 3e-1), (1.0, 1e-36)])
+@pytest.mark.parametrize("dtypes", ["fp32", "bf16"])
+def test_factors_near_the_smallest_number(scale, max_norm, dtypes):
+    """max_norm / norm near or below 2^-126: the clipped values are ordinary numbers and keep their bits.  (The
+    bound of values that are themselves below fp32's normal numbers is their spacing, 2^-149, once for each rounding.)"""
+    torch = torch_cuda()
+    import matrix_state_nonlinear_m2rnn_amd as m2
+    say("clip factor", scale, max_norm, dtypes)
+    ts = tensors([1000, 77, 4099], dtypes, 16, scale)
+    out = [torch.empty_like(t) for t in ts]
+    norm = m2.m2rnn_grad_clip(ts, max_norm, out=out)
+    n = norm64(ts)
+    assert abs(float(norm) - n) <= (2.0 ** -24 + 2.0 ** -30) * n
+    step = 2.0 ** -8 if dtypes == "bf16" else 0.0
+    for t, o in zip(ts, out):
+        ref = t.double() * (float(np.float32(max_norm)) / n)
+        # bf16's own smallest numbers are 2^-133 apart
+        least = 2 * 2.0 ** -149 + (2.0 ** -134 if dtypes == "bf16" else 0.0)
+        assert bool(((o.double() - ref).abs() <= (3 * 2.0 ** -24 + step) * ref.abs() + least).all())
+    m2.m2rnn_grad_clip(ts, max_norm)
+    assert all(torch.equal(a, b) for a, b in zip(ts, out))
+
+
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
 def test_a_norm_that_is_not_finite_leaves_the_gradients(bad):
     torch = torch_cuda()
