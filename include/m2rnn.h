@@ -499,7 +499,8 @@ int m2rnn_qk_norm_rope_bwd(int64_t B, int64_t T, int64_t Nq, int64_t Nk, int64_t
  * has any number of elements (also none), contiguous, aligned to its element, in fp32 or bf16.
  * Squares are summed in fp64 in a fixed order.
  *   norm       device fp32 scalar: m2rnn_grad_norm writes it, m2rnn_grad_clip reads it (in between a
- *              caller may combine the norms of several ranks).  No tensors: 0.
+ *              caller may combine the norms of several ranks).  No tensors: 0.  Not within a tensor of the
+ *              list (M2RNN_EINVAL).
  *   out        NULL: in place.  Otherwise a host array of `count` device pointers (NULL entries: in place)
  *              of the tensors' own types and sizes.  An output that overlaps another output, another
  *              tensor, the norm, or a part of its own tensor is rejected (M2RNN_EINVAL).

@@ -130,6 +130,10 @@ int m2rnn_grad_norm(const m2rnn_tensor* grads, int64_t count, float* norm, void*
   int st = m2rnn_grad_norm_workspace_size(grads, count, &need);
   if (st) return st;
   if (need > 0 && (!workspace || workspace_bytes < need || ((uintptr_t)workspace & 15u))) return M2RNN_EWORKSPACE;
+  for (int64_t i = 0; i < count; ++i) {  // the norm would be written over a gradient
+    const uintptr_t at = (uintptr_t)grads[i].data, end = at + (uintptr_t)grads[i].numel * elem(grads[i].dtype);
+    if (at < end && (uintptr_t)norm < end && at < (uintptr_t)(norm + 1)) return M2RNN_EINVAL;
+  }
   hipStream_t s = (hipStream_t)stream;
   double* part = (double*)workspace;
   st = over_launches(grads, count, nullptr, piece_size(grads, count), false, [&](GradArgs& A, long groups, long before) {

@@ -84,6 +84,13 @@ def test_grad_lists():
     assert L.m2rnn_grad_clip(ok, 0, None, norm, F(1.0), None) == m2.M2RNN_OK
 
 
+def test_norm_within_the_gradients():
+    L = m2.lib()
+    ok = tensors((4096, 1000, 0), (1 << 20, 6, 1), (None, 0, 0))
+    for at in (4096, 4096 + 3996, 1 << 20, (1 << 20) + 8):
+        assert L.m2rnn_grad_norm(ok, 3, P(at), P(512), 1 << 20, None) == m2.M2RNN_EINVAL, at
+
+
 def test_conv_window():
     L = m2.lib()
     p, q = P(1 << 12), P(1 << 20)
