@@ -573,15 +573,15 @@ __global__ void __launch_bounds__(HPW * VB * 4) m2rnn_ssm_state_kernel(SsmArgs A
     }
   };
   const int ch0 = s_ * A.cps, ch1 = min(A.nch, ch0 + A.cps);
-  const int first = ch1 - 1, step = -1, count = ch1 - ch0;
+  const int last = ch1 - 1, count = ch1 - ch0;
   if (count > 0) {
-    fetch_a(first);
-    fetch(first);
-    weights(first, 0);
-    if (count > 1) fetch_a(first + step);
+    fetch_a(last);
+    fetch(last);
+    weights(last, 0);
+    if (count > 1) fetch_a(last - 1);
   }
   for (int c = 0; c < count; ++c) {
-    const int ch = first + step * c, buf = c & 1;
+    const int ch = last - c, buf = c & 1;
     if constexpr (REV) {
       if (mine) {
         float* o = A.rloc + ((((long)b * A.N + head) * A.nch + ch) * V + c0 + n) * K;
@@ -606,7 +606,7 @@ __global__ void __launch_bounds__(HPW * VB * 4) m2rnn_ssm_state_kernel(SsmArgs A
         for (int e = 0; e < 8; ++e) x[s][e] = pu[s][e];
     }
     __syncthreads();
-    if (c + 1 < count) fetch(ch + step);
+    if (c + 1 < count) fetch(ch - 1);
     if constexpr (REV) {
       const float dl = sdec[buf][hw];
 #pragma unroll
@@ -649,8 +649,8 @@ __global__ void __launch_bounds__(HPW * VB * 4) m2rnn_ssm_state_kernel(SsmArgs A
       }
     }
     if (c + 1 < count) {
-      weights(ch + step, buf ^ 1);
-      if (c + 2 < count) fetch_a(ch + 2 * step);
+      weights(ch - 1, buf ^ 1);
+      if (c + 2 < count) fetch_a(ch - 2);
     }
   }
   if (mine) {
@@ -764,16 +764,17 @@ __device__ __forceinline__ void ssm_decay_col(const SsmTab<L>& tab, int I, int J
 // ONE: the workgroup has one head of one block, so nothing lives from one pass of the loop to the next (B4 N16 T4096
 // K=V=64, bf16: 163 to 175 us, 0.58 GB moved at 3.4 TB/s).  Neither HBM nor issue is full (VALU 42%, MFMA 16%, LDS 35% of
 // the cycles): two workgroups of four waves a CU, by registers and LDS, wait for their products and barriers.
-// With several heads or blocks (!ONE) 38 registers spill at K = VB = 64: N16 in groups of 4 heads takes as long
-// as one query/key each (both about 0.3 ms for the whole training step), V = 128 1.8 times V = 64.
+// With several heads or blocks (!ONE) 22 registers spill at K = VB = 64 in bf16: the call takes 195 us for N16 in groups
+// of 4 heads (213 with one query/key each) and 378 us at V = 128, 1.8 times V = 64.
 template <bool BF16, int KP, int VB, bool ONE>
 __global__ void __launch_bounds__(64 * kSsmBwdWaves, KP == 128 ? 1 : 2) m2rnn_ssm_bwd_kernel(SsmArgs A) {
   constexpr int L = ssm_chunk<BF16>(), NI = L / 16, NS = L / 32, KS = KP / 32, KM = KP / 16, NP = BF16 ? 1 : 3;
   constexpr int NW = kSsmBwdWaves, NTH = 64 * NW;
-  constexpr int VP = VB < 32 ? 32 : VB, VS = VP / 32, VM = VB / 16;  // columns in LDS, contraction steps, tiles
-  constexpr int STK = ssm_stride(KP), STV = ssm_stride(VP);
+  static_assert(VB == 32 || VB == 64, "heads of 16 columns have a kernel of their own");
+  constexpr int VS = VB / 32, VM = VB / 16;                          // contraction steps over the columns, their tiles
+  constexpr int STK = ssm_stride(KP), STV = ssm_stride(VB);
   constexpr int MPW = KM >= NW ? KM / NW : 1;                        // K tiles per wave
-  constexpr int TPV = VM * NI >= NW ? VM * NI / NW : 1;              // dv tiles per wave, one V tile
+  constexpr int TPV = VM * NI / NW;                                  // dv tiles per wave, one V tile
   constexpr bool AHEAD = VB <= 32;                                   // the next block's v and u fit in registers meanwhile
   constexpr int SETS = NI == 4 ? 6 : 2;                              // (J, s) operand sets of P
   constexpr int QW = NP * L * STK, PW = SETS * 3 * 2 * 64 * 4;       // elements of the q and P blocks
@@ -812,10 +813,12 @@ __global__ void __launch_bounds__(64 * kSsmBwdWaves, KP == 128 ? 1 : 2) m2rnn_ss
   const bool hasdq = KM >= NW || w < KM, hasdk = KM >= NW || w >= NW - KM;
   const int mq = KM >= NW ? w * MPW : w, mk = KM >= NW ? w * MPW : w - (NW - KM);
   const int mv = (w * TPV) / NI, jv0 = (w * TPV) % NI;
-  const bool hasv = w * TPV < VM * NI;
+  // Every wave has dv tiles.  With one head the test stays, as a branch around R's loads and the products of dv: without
+  // it the kernel takes 6% longer; with several heads 6% longer with it (38 registers spilled, not 22).
+  const bool hasv = !ONE || w * TPV < VM * NI;
 
-  SsmPieces<BF16, L, VP, NTH> pv;
-  SsmPieces<false, L, VP, NTH> pu;
+  SsmPieces<BF16, L, VB, NTH> pv;
+  SsmPieces<false, L, VB, NTH> pu;
   auto fetch = [&](int blk) {
     const int h = hb + blk / CB;
     const long off = row0 * vrow + (long)h * V + (blk % CB) * VB;
@@ -880,12 +883,12 @@ __global__ void __launch_bounds__(64 * kSsmBwdWaves, KP == 128 ? 1 : 2) m2rnn_ss
         const int kk = hasdq ? 16 * (mq + p) + n : kr;  // two K tiles: the waves of dk take H for <R, H>
 #pragma unroll
         for (int e = 0; e < 8; ++e) hx[p][s][e] = rx[p][s][e] = ix[p][s][e] = 0.0f;
-        if ((hasdq || KM < NW) && kk < K && c < VB) {
+        if ((hasdq || KM < NW) && kk < K) {
           const float4 a4 = *(const float4*)(Hp + (unsigned)(kk * V + c)), b4 = *(const float4*)(Hp + (unsigned)(kk * V + c + 4));
           hx[p][s][0] = a4.x; hx[p][s][1] = a4.y; hx[p][s][2] = a4.z; hx[p][s][3] = a4.w;
           hx[p][s][4] = b4.x; hx[p][s][5] = b4.y; hx[p][s][6] = b4.z; hx[p][s][7] = b4.w;
         }
-        if (hasdk && kr < K && c < VB) {
+        if (hasdk && kr < K) {
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             rx[p][s][e] = Rp[(unsigned)((c + e) * K + kr)];
