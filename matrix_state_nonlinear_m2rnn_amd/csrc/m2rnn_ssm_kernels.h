@@ -85,24 +85,12 @@ __device__ __forceinline__ void ssm_decay(const SsmTab<L>& tab, int I, int J, in
   }
 }
 
-// The forward's scores, tile (I, J) of q k^T times its decays and D_j (the table's f carries D_j).  Scores of later
-// steps are left out by selection, not by a factor 0, so what is not finite there stays there.
-template <int L>
-__device__ __forceinline__ void ssm_scores(const SsmTab<L>& tab, int I, int J, int g, int n, f32x4 qk, float (&o)[4]) {
-  if (I != J) {
-    ssm_decay<L, true>(tab, I, J, g, n, o);
+// q k^T of tile (I, J) with the products of later steps replaced by zeros: the factor 0 that they get alone would let
+// what is not finite there through, as NaN.
+__device__ __forceinline__ f32x4 ssm_causal(f32x4 x, int I, int J, int g, int n) {
 #pragma unroll
-    for (int r = 0; r < 4; ++r) o[r] *= qk[r];
-  } else {
-    const float hi = tab.chi[16 * I + n], lo = tab.clo[16 * I + n];
-    const float4 h = *(const float4*)&tab.chi[16 * J + 4 * g];
-    const float4 l = *(const float4*)&tab.clo[16 * J + 4 * g];
-    const float4 d = *(const float4*)&tab.d[16 * J + 4 * g];
-    const float hj[4] = {h.x, h.y, h.z, h.w}, lj[4] = {l.x, l.y, l.z, l.w}, dj[4] = {d.x, d.y, d.z, d.w};
-#pragma unroll
-    for (int r = 0; r < 4; ++r)
-      o[r] = 4 * g + r <= n ? qk[r] * (dj[r] * exp2_((hi - hj[r]) + (lo - lj[r]))) : 0.0f;
-  }
+  for (int r = 0; r < 4; ++r) x[r] = I != J || 4 * g + r <= n ? x[r] : 0.0f;
+  return x;
 }
 
 // Four values as NP bf16 planes put together again.
@@ -256,7 +244,7 @@ __global__ void __launch_bounds__(HPW * VB * 4) m2rnn_ssm_fwd_kernel(SsmArgs A) 
     if (ch + 1 < ch1) fetch(ch + 1);
 
     const SsmTab<L>& tb = tab[w / WPH];
-    // q k^T tile (I, J): lane column i, rows j
+    // q k^T tile (I, J) without later steps: lane column i, rows j
     auto qk_tile = [&](int I, int J) {
       f32x4 acc = {0, 0, 0, 0};
 #pragma unroll
@@ -269,15 +257,17 @@ __global__ void __launch_bounds__(HPW * VB * 4) m2rnn_ssm_fwd_kernel(SsmArgs A) 
         }
         acc = mfma_planes<NP, NP>(ko, qo, acc);
       }
-      return acc;
+      return ssm_causal(acc, I, J, g, n);
     };
     if constexpr (SHARE_P) {
       for (int t = w; t < NT; t += NW) {
         int I, J;
         tri_tile(t, I, J);
         const f32x4 acc = qk_tile(I, J);
-        float x[4];
-        ssm_scores<L>(tb, I, J, g, n, acc, x);
+        float d[4], x[4];
+        ssm_decay<L, true>(tb, I, J, g, n, d);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) x[r] = acc[r] * d[r];
         uint2 pl[3];
         split3x4(x, pl);
         const int set = (I / 2) * (I / 2 + 1) + (I & 1) * (I / 2 + 1) + J / 2;
@@ -290,11 +280,7 @@ __global__ void __launch_bounds__(HPW * VB * 4) m2rnn_ssm_fwd_kernel(SsmArgs A) 
         int I, J;
         tri_tile(t, I, J);
         const f32x4 acc = qk_tile(I, J);
-        // (later steps' products to zeros here, once for all heads: a factor 0 alone would let a NaN through)
-        float x[4];
-#pragma unroll
-        for (int r = 0; r < 4; ++r) x[r] = I != J || 4 * g + r <= n ? acc[r] : 0.0f;
-        gbuf[t * 64 + lane] = make_float4(x[0], x[1], x[2], x[3]);
+        gbuf[t * 64 + lane] = make_float4(acc[0], acc[1], acc[2], acc[3]);
       }
       __syncthreads();
     }
@@ -357,7 +343,7 @@ __global__ void __launch_bounds__(HPW * VB * 4) m2rnn_ssm_fwd_kernel(SsmArgs A) 
     }
     // A value of v that is not finite makes its column of the state NaN (also through a weight 0), but must not reach the
     // steps before it, whose zero scores it meets in the same product.  The state shows such a chunk, so the others pay a
-    // comparison (0 to 2.5% of the kernel's time with the state formed before y): its products are taken without
+    // comparison (0 to 3% of the call's time with the state formed before y): its products are taken without
     // those values, and y is NaN from each column's first one on.
     int bad = L;
     const bool odd = __builtin_amdgcn_ballot_w64(H[0][0] != H[0][0]) != 0;
@@ -409,18 +395,17 @@ __global__ void __launch_bounds__(HPW * VB * 4) m2rnn_ssm_fwd_kernel(SsmArgs A) 
           for (int hf = 0; hf < 2; ++hf) {
             const int J = 2 * s + hf;
             if (J <= I) {
-              float x[4];
+              f32x4 qk;
               if constexpr (SHARE_G) {
                 const float4 t4 = gbuf[(I * (I + 1) / 2 + J) * 64 + lane];
-                float d[4];
-                ssm_decay<L, true>(tb, I, J, g, n, d);
-                x[0] = t4.x * d[0];
-                x[1] = t4.y * d[1];
-                x[2] = t4.z * d[2];
-                x[3] = t4.w * d[3];
+                qk = f32x4{t4.x, t4.y, t4.z, t4.w};
               } else {
-                ssm_scores<L>(tb, I, J, g, n, qk_tile(I, J), x);
+                qk = qk_tile(I, J);
               }
+              float d[4], x[4];
+              ssm_decay<L, true>(tb, I, J, g, n, d);
+#pragma unroll
+              for (int r = 0; r < 4; ++r) x[r] = qk[r] * d[r];
               split3x4(x, half[hf]);
             } else {
 #pragma unroll
