@@ -14,7 +14,8 @@ int record_hip_status(hipError_t e);
 
 // The backward's partial sums over `parts` rows in one launch: gate [parts][2N] to dbeta, dalpha and wr
 // [parts][N V] to dw_r.  A workgroup takes 64 columns (of both arrays, one after the other), its 16 waves
-// every sixteenth row each; the waves' sums are added in order.
+// every sixteenth row each; the waves' sums are added in order.  The rows and their sums are fp32 (a
+// row of the gate is a chunk's sum in fp64, rounded once): at most 128 rows follow each other in a wave.
 __global__ void __launch_bounds__(1024) m2rnn_ssm_sums_kernel(const float* __restrict__ gate,
                                                               const float* __restrict__ wr, long parts, int N, long NV,
                                                               float* __restrict__ dbeta, float* __restrict__ dalpha,
@@ -75,13 +76,18 @@ constexpr long kMaxGrid = 2147483647L;
 constexpr double kMaxThreads = 4294967295.0;  // of one launch
 constexpr int kMaxK = 128;
 
-// Waves that the forward and state launches aim for: three for each of the 1024 SIMDs, which is what their
-// registers and LDS let a CU hold (B2 N32 T16384 K=V=64, when the whole scan took 242 us: 253 with two, 272 with four).
+// Waves that the forward and state launches aim for: three for each of the 1024 SIMDs, which is what registers and LDS
+// let a CU hold of the kernels at V = 64 and of the shared V = 16 with K <= 64 (B2 N32 T16384 K=V=64: 226 us; 358 with
+// one, 240 with two, 258 with four.  B4 N128 T4096 K=64 V=16 shared: 114; 193, 128, 120).  The kernels at K > 64 hold
+// one or two, those at V = 32 two, which the target does not look at: B4 N16 T4096 K=V=128 takes 187 us (366 in fp32), with
+// two 165 (318); N64 K=128 V=16 shared 117, with two 94; K=64 V=32 64 us with either (94 in fp32, with two 104).
 constexpr long kSsmWaves = 3L * 1024;
 // A segment is at least this many chunks: with single ones a prompt of 509 tokens (16 heads, K = V = 128, fp32) takes the
 // same time (32 us for its three kernels), with twice the segments' states to write and combine.
 constexpr int kSsmMinChunks = 2;
-// Workgroups that the backward's launch aims for where a group's heads can be split.
+// Workgroups that the backward's launch aims for where a group's heads can be split: two for each CU, which the kernels at
+// K <= 64 hold (B4 N128 T4096 K=64 V=16, one query/key: 410 us for the call, 589 with 256, 413 with 1024).  Those at K > 64
+// hold one and take about the same (N64 K=128 V=64, one query/key: 1228 us, 1212 with 256, 1242 with 1024).
 constexpr long kSsmBwdGroups = 512;
 
 // Rows of partial sums that one launch adds (one wave 1/16 of them after each other); more go through the

@@ -24,6 +24,8 @@ struct SsmArgs {
   const float *H0, *dy, *dH_T;             // [B,N,K,V], [B,T,N,V], [B,N,K,V]
   float *y, *H_T, *ckpt;                   // ckpt [B,N,nch,K,V]
   float* seg;                              // [B,N,S,K,V] ([V,K] in the reverse scan)
+  // log2 decays are summed in fp64 and kept in fp32: the rounding of x changes 2^x by |x| 2^-25 of it, next to nothing
+  // where 2^x still counts
   float* segdec;                           // [B,N,S] log2 decay of each segment
   float* rloc;                             // [B,N,nch,V,K] reverse: the part of the segment's later chunks
   float* cdec;                             // [B,N,nch] reverse: log2 decay from the chunk's end to the segment's
@@ -132,9 +134,9 @@ __device__ __forceinline__ void ssm_gate(bool live, float a, float alpha, float 
 // HPW > 1 (V = 16 heads sharing q and k): one wave per head, q k^T formed once for all of them.
 // Otherwise the waves of a head share its masked and decayed q k^T through LDS.
 //
-// Bound by HBM and issue together: at B2 N32 T16384 K=V=64 (bf16) the kernel takes 157 to 190 us for 0.70 GB, 3.7 to
-// 4.4 TB/s, with a SIMD's VALU busy 59% of the cycles and its MFMA 24%; B4 N128 T4096 K=64 V=16 with one
-// query/key takes 100 to 106 us (with checkpoints), VALU 73% (each head's decays and splits for 16 columns).
+// Bound by HBM and issue together: at B2 N32 T16384 K=V=64 (bf16) the kernel takes 159 us at best and 187 on average for
+// 0.69 GB, 3.7 to 4.4 TB/s, with a SIMD's VALU busy 61% of the cycles and its MFMA 24%; B4 N128 T4096 K=64 V=16 with one
+// query/key takes 102 to 106 us (with checkpoints), VALU 75% (each head's decays and splits for 16 columns).
 template <bool BF16, int KP, int VB, int HPW>
 __global__ void __launch_bounds__(HPW * VB * 4) m2rnn_ssm_fwd_kernel(SsmArgs A) {
   constexpr int L = ssm_chunk<BF16>(), NI = L / 16, NS = L / 32, KS = KP / 32, KM = KP / 16, NP = BF16 ? 1 : 3;
@@ -1349,7 +1351,8 @@ __device__ __forceinline__ f32x4 mfma16_planes_turned(const uint2 (&A)[NA], cons
 // assignment of the three tasks took 14 to 40 us more).  R is read once, as planes in LDS that serve as R (transposing reads) and as R^T; H goes straight into the
 // operand of the wave that owns its 16 K rows.  X is summed over the heads in registers.
 //
-// B4 N128 T4096 K=64 V=16, one query/key: 344 to 366 us, 11.6 thousand cycles a head for the two workgroups of a CU.
+// B4 N128 T4096 K=64 V=16, one query/key: 351 to 401 us, 368 on average, 11.6 thousand cycles a head for the two
+// workgroups of a CU.
 // Bound by issue and latency at two waves a SIMD (256 VGPRs): VALU 58%, MFMA 18%, LDS 38% of the cycles, HBM at
 // 2.4 TB/s.  Of an earlier 366 us the columns with P and dv took a third, the terms of H and R 47 us, the rows 33, loads 27,
 // da 25, the tables 8, the fp64 sums 9.
