@@ -692,7 +692,7 @@ def m2rnn_conv4_silu_bwd(x, w, bias, du, *, workspace=None, stream=None) -> Dict
 # ---------------------------------------------------------------- selective state space scan
 
 def _elsewhere(dev, stream) -> bool:
-    """Whether a call has to change the current device or stream: it then makes itself again within _call_on."""
+    """Whether a call has to change the current device or stream: it then makes itself again through _there."""
     import torch
     return stream is not None or torch.cuda.current_device() != dev.index
 
@@ -706,6 +706,35 @@ def _call_on(dev, stream):
             raise ValueError(f"stream is on {stream.device}, the inputs are on {dev}")
         return torch.cuda.stream(stream)  # sets the stream's device too
     return torch.cuda.device(dev)
+
+
+def _tensors_in(*values):
+    """The tensors of nested arguments or results."""
+    import torch
+    for x in values:
+        if isinstance(x, torch.Tensor):
+            yield x
+        elif isinstance(x, (list, tuple)):
+            yield from _tensors_in(*x)
+        elif isinstance(x, dict):
+            yield from _tensors_in(*x.values())
+
+
+def _there(dev, stream, f, *args, **kwargs):
+    """f(*args, **kwargs) on the device and stream of a call.  On a stream of its own the caching allocator learns that
+    the call's tensors are in use there, and its results on the caller's stream: memory of an input dropped right
+    after the call is not handed out while the call still reads it."""
+    import torch
+    with _call_on(dev, stream):
+        result = f(*args, **kwargs)
+    if stream is not None:
+        here = torch.cuda.current_stream(dev)
+        if here != stream:
+            for t in _tensors_in(args, kwargs):
+                t.record_stream(stream)
+            for t in _tensors_in(result):
+                t.record_stream(here)
+    return result
 
 
 _raw_stream = None
@@ -777,8 +806,8 @@ def _ssm_fwd(q, k, v, a, alpha, beta, w_r, H0, lens, y, H_T, ckpt, keep, return_
     if lens is not None:
         _require(lens, "lens", torch.int32, (B,), dev)
     if _elsewhere(dev, stream):
-        with _call_on(dev, stream):
-            return _ssm_fwd(q, k, v, a, alpha, beta, w_r, H0, lens, y, H_T, ckpt, keep, return_state, workspace, None)
+        return _there(dev, stream, _ssm_fwd, q, k, v, a, alpha, beta, w_r, H0, lens, y, H_T, ckpt, keep, return_state,
+                      workspace, None)
     y = _out(y, "y", torch.float32, (B, T, N, V), v)
     if H_T is not None or return_state:
         H_T = _out(H_T, "H_T", torch.float32, (B, N, K, V), v if H0 is None else H0)
@@ -831,9 +860,8 @@ def m2rnn_ssm_bwd(q, k, v, a, alpha, beta, w_r, ckpt, dy, dH_T=None, *, lens=Non
     shapes = {"dq": (B, T, Nqk, K), "dk": (B, T, Nqk, K), "dv": (B, T, N, V), "da": (B, T, N), "dalpha": (N,),
               "dbeta": (N,), "dw_r": (N, V), "dH0": (B, N, K, V)}
     if _elsewhere(dev, stream):
-        with _call_on(dev, stream):
-            return m2rnn_ssm_bwd(q, k, v, a, alpha, beta, w_r, ckpt, dy, dH_T, lens=lens, want_dH0=want_dH0,
-                                 workspace=workspace, out=out)
+        return _there(dev, stream, m2rnn_ssm_bwd, q, k, v, a, alpha, beta, w_r, ckpt, dy, dH_T, lens=lens,
+                      want_dH0=want_dH0, workspace=workspace, out=out)
     if out is None:
         out = {x: torch.empty(s, dtype=torch.float32, device=dev) if x != "dH0" or want_dH0 else None
                for x, s in shapes.items()}
@@ -862,8 +890,7 @@ def m2rnn_ssm_step(q, k, v, a, alpha, beta, w_r, H=None, *, H_out=None, y=None, 
     if H is not None:
         _require(H, "H", torch.float32, (B, N, K, V), dev)
     if _elsewhere(dev, stream):
-        with _call_on(dev, stream):
-            return m2rnn_ssm_step(q, k, v, a, alpha, beta, w_r, H, H_out=H_out, y=y)
+        return _there(dev, stream, m2rnn_ssm_step, q, k, v, a, alpha, beta, w_r, H, H_out=H_out, y=y)
     H_out = _out(H_out, "H_out", torch.float32, (B, N, K, V), v if H is None else H)
     y = _out(y, "y", torch.float32, (B, N, V), v)
     _check("m2rnn_ssm_step", lib().m2rnn_ssm_step(
@@ -888,8 +915,7 @@ def m2rnn_conv4_silu_fwd_state(x, w, bias=None, win=None, *, lens=None, u=None, 
     if lens is not None:
         _require(lens, "lens", torch.int32, (B,), dev)
     if _elsewhere(dev, stream):
-        with _call_on(dev, stream):
-            return m2rnn_conv4_silu_fwd_state(x, w, bias, win, lens=lens, u=u, win_out=win_out)
+        return _there(dev, stream, m2rnn_conv4_silu_fwd_state, x, w, bias, win, lens=lens, u=u, win_out=win_out)
     u = _out(u, "u", x.dtype, (B, T, C), x)
     win_out = _out(win_out, "win_out", x.dtype, (B, 3, C), x if win is None else win)
     _check("m2rnn_conv4_silu_fwd_state", lib().m2rnn_conv4_silu_fwd_state(
@@ -908,8 +934,7 @@ def m2rnn_conv4_silu_step(x, w, bias=None, win=None, *, u=None, win_out=None, st
     dev = x.device
     _conv_inputs(x, w, bias, win, (B, C))
     if _elsewhere(dev, stream):
-        with _call_on(dev, stream):
-            return m2rnn_conv4_silu_step(x, w, bias, win, u=u, win_out=win_out)
+        return _there(dev, stream, m2rnn_conv4_silu_step, x, w, bias, win, u=u, win_out=win_out)
     u = _out(u, "u", x.dtype, (B, C), x)
     win_out = _out(win_out, "win_out", x.dtype, (B, 3, C), x if win is None else win)
     _check("m2rnn_conv4_silu_step", lib().m2rnn_conv4_silu_step(
@@ -959,9 +984,8 @@ def m2rnn_qk_norm_rope_fwd(q, k, gamma_q, gamma_k, pos, inv_freq, eps: float = 1
     import torch
     B, T, Nq, Nk, K, R, dev = _qk_inputs(q, k, gamma_q, gamma_k, pos, inv_freq)
     if _elsewhere(dev, stream):
-        with _call_on(dev, stream):
-            return m2rnn_qk_norm_rope_fwd(q, k, gamma_q, gamma_k, pos, inv_freq, eps, interleaved=interleaved,
-                                          q_out=q_out, k_out=k_out)
+        return _there(dev, stream, m2rnn_qk_norm_rope_fwd, q, k, gamma_q, gamma_k, pos, inv_freq, eps,
+                      interleaved=interleaved, q_out=q_out, k_out=k_out)
     q_out = _out(q_out, "q_out", q.dtype, (B, T, Nq, K), q)
     k_out = _out(k_out, "k_out", q.dtype, (B, T, Nk, K), k)
     _check("m2rnn_qk_norm_rope_fwd", lib().m2rnn_qk_norm_rope_fwd(
@@ -980,9 +1004,8 @@ def m2rnn_qk_norm_rope_bwd(q, k, gamma_q, gamma_k, pos, inv_freq, dq_out, dk_out
     _require(dk_out, "dk_out", torch.float32, (B, T, Nk, K), dev)
     shapes = {"dq": (B, T, Nq, K), "dk": (B, T, Nk, K), "dgamma_q": (K,), "dgamma_k": (K,)}
     if _elsewhere(dev, stream):
-        with _call_on(dev, stream):
-            return m2rnn_qk_norm_rope_bwd(q, k, gamma_q, gamma_k, pos, inv_freq, dq_out, dk_out, eps,
-                                          interleaved=interleaved, workspace=workspace, out=out)
+        return _there(dev, stream, m2rnn_qk_norm_rope_bwd, q, k, gamma_q, gamma_k, pos, inv_freq, dq_out, dk_out, eps,
+                      interleaved=interleaved, workspace=workspace, out=out)
     if out is None:
         out = {n: torch.empty(s, dtype=torch.float32, device=dev) for n, s in shapes.items()}
     else:
@@ -1060,8 +1083,7 @@ def m2rnn_grad_norm(grads, *, norm=None, workspace=None, stream=None):
     if norm is not None:
         _require_scalar(norm, dev)
     if _elsewhere(dev, stream):
-        with _call_on(dev, stream):
-            return m2rnn_grad_norm(grads, norm=norm, workspace=workspace)
+        return _there(dev, stream, m2rnn_grad_norm, grads, norm=norm, workspace=workspace)
     return _grad_norm(arr, len(grads), dev, norm, workspace)
 
 
@@ -1086,8 +1108,7 @@ def m2rnn_grad_clip(grads, max_norm: float, *, norm=None, out=None, workspace=No
     if norm is not None:
         _require_scalar(norm, dev)
     if _elsewhere(dev, stream):
-        with _call_on(dev, stream):
-            return m2rnn_grad_clip(grads, max_norm, norm=norm, out=out, workspace=workspace)
+        return _there(dev, stream, m2rnn_grad_clip, grads, max_norm, norm=norm, out=out, workspace=workspace)
     if norm is None:
         norm = _grad_norm(arr, len(grads), dev, None, workspace)
     _check("m2rnn_grad_clip", lib().m2rnn_grad_clip(arr, len(grads), dst, _ptr(norm), float(max_norm),
