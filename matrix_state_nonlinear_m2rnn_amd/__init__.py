@@ -354,6 +354,8 @@ def m2rnn_fwd_ckpt(q, k, v, f, W, w_r, H0=None, *, math="auto", row_blocks: int 
     """m2rnn_fwd that also keeps the backward's checkpoints: returns (y, H_T, ckpt) with ckpt
     [B,N,ceil(T/I),K,V] fp32, the state entering every I-th step, I = m2rnn_checkpoint_interval
     (for m2rnn_bwd_ckpt)."""
+    if stream is not None:
+        return _again(m2rnn_fwd_ckpt, locals())
     import torch
     dims, dt, m, rb, y, H_T = _fwd_prepare(q, k, v, f, W, w_r, H0, y, H_T, math, row_blocks, True)
     shape = (dims.B, dims.N, checkpoint_count(dims.T, dims.V), dims.K, dims.V)
@@ -377,6 +379,8 @@ def m2rnn_fwd(q, k, v, f, W, w_r, H0=None, *, math="auto", row_blocks: int = 0, 
     fp32 or None.  Returns (y [B,T,N,V] fp32, H_T [B,N,K,V] fp32).  overlap: "auto" (one side stream
     per calling stream, made on first use), None (everything on the call's stream) or an Overlap.
     """
+    if stream is not None:
+        return _again(m2rnn_fwd, locals())
     y, H_T, _ = _call_fwd("m2rnn_fwd", q, k, v, f, W, w_r, H0, y, H_T, math, row_blocks, workspace, stream,
                           return_state, overlap)
     return y, H_T
@@ -387,6 +391,8 @@ def m2rnn_fwd_noalloc(q, k, v, f, W, w_r, H0=None, *, math="auto", row_blocks: i
     """m2rnn_fwd without a workspace: the library's fixed device array holds the partial readouts
     and the states between time segments (for callers that cannot allocate; pass y and H_T to
     allocate nothing here either).  Calls that overlap in time on one device race."""
+    if stream is not None:
+        return _again(m2rnn_fwd_noalloc, locals())
     dims, dt, m, rb, y, H_T = _fwd_prepare(q, k, v, f, W, w_r, H0, y, H_T, math, row_blocks, return_state)
     _check("m2rnn_fwd_noalloc", lib().m2rnn_fwd_noalloc(
         ctypes.byref(dims), dt, m, rb, _ptr(q), _ptr(k), _ptr(v), _ptr(f), _ptr(W), _ptr(w_r), _ptr(H0), _ptr(y),
@@ -402,6 +408,8 @@ def m2rnn_fwd_block(q, k, v, a, alpha, beta, W, w_r, gz, gamma, H0=None, *, eps:
     out = gamma (.) x / sqrt(mean x^2 + eps) with x = y (.) SiLU(gz) over the N V features of a
     token, formed by the pass that sums the readouts (y never goes to HBM).  a [B,T,N] fp32; alpha, beta [N] fp32;
     gz [B,T,N,V] fp32 or bf16; gamma [N,V] fp32; the rest as m2rnn_fwd.  Returns (out, H_T)."""
+    if stream is not None:
+        return _again(m2rnn_fwd_block, locals())
     import torch
     dims, dt, m, rb, out, H_T = _fwd_prepare(q, k, v, a, W, w_r, H0, out, H_T, math, row_blocks, return_state)
     dev = q.device
@@ -423,6 +431,8 @@ def m2rnn_fwd_block(q, k, v, a, alpha, beta, W, w_r, gz, gamma, H0=None, *, eps:
 def m2rnn_scan_fwd(q, k, v, f, W, w_r, H0=None, *, math="auto", row_blocks: int = 0, y=None, H_T=None,
                    workspace=None, stream=None, return_state: bool = True):
     """The scan launch of m2rnn_fwd alone; returns (y, H_T, workspace) for m2rnn_scan_fwd_finish."""
+    if stream is not None:
+        return _again(m2rnn_scan_fwd, locals())
     return _call_fwd("m2rnn_scan_fwd", q, k, v, f, W, w_r, H0, y, H_T, math, row_blocks, workspace, stream,
                      return_state)
 
@@ -430,6 +440,8 @@ def m2rnn_scan_fwd(q, k, v, f, W, w_r, H0=None, *, math="auto", row_blocks: int 
 def m2rnn_scan_fwd_finish(q, k, v, f, W, w_r, H0=None, *, math="auto", row_blocks: int = 0, y=None, H_T=None,
                           workspace=None, stream=None):
     """The second launch of m2rnn_fwd (sums partial readouts when the rows were split)."""
+    if stream is not None:
+        return _again(m2rnn_scan_fwd_finish, locals())
     y, H_T, _ = _call_fwd("m2rnn_scan_fwd_finish", q, k, v, f, W, w_r, H0, y, H_T, math, row_blocks, workspace,
                           stream, False)
     return y
@@ -480,6 +492,8 @@ def m2rnn_bwd_ckpt(q, k, v, f, W, w_r, ckpt, dy, dH_T=None, *, math="auto", grad
                    want_dH0: bool = True, workspace=None, stream=None, out=None) -> Dict[str, object]:
     """m2rnn_bwd from the checkpoints that m2rnn_fwd_ckpt kept (no forward re-run).  `out` may hold
     the gradient tensors to write (a dict as returned)."""
+    if stream is not None:
+        return _again(m2rnn_bwd_ckpt, locals())
     return _call_bwd_ckpt("m2rnn_bwd_ckpt", q, k, v, f, W, w_r, ckpt, dy, dH_T, math, grad_clip, want_dH0, workspace,
                           stream, out)
 
@@ -488,6 +502,8 @@ def m2rnn_scan_bwd(q, k, v, f, W, w_r, ckpt, dy, dH_T=None, *, math="auto", grad
                    want_dH0: bool = True, workspace=None, stream=None, out=None) -> Dict[str, object]:
     """The scale pass and the reverse scan of m2rnn_bwd_ckpt alone; m2rnn_scan_bwd_finish with the
     same workspace and outputs completes it."""
+    if stream is not None:
+        return _again(m2rnn_scan_bwd, locals())
     return _call_bwd_ckpt("m2rnn_scan_bwd", q, k, v, f, W, w_r, ckpt, dy, dH_T, math, grad_clip, want_dH0, workspace,
                           stream, out)
 
@@ -495,6 +511,8 @@ def m2rnn_scan_bwd(q, k, v, f, W, w_r, ckpt, dy, dH_T=None, *, math="auto", grad
 def m2rnn_scan_bwd_finish(q, k, v, f, W, w_r, ckpt, dy, dH_T=None, *, math="auto", grad_clip: float = 0.0,
                           workspace=None, stream=None, out=None) -> Dict[str, object]:
     """The fixed-order sums of m2rnn_bwd_ckpt's per-workgroup partials (after m2rnn_scan_bwd)."""
+    if stream is not None:
+        return _again(m2rnn_scan_bwd_finish, locals())
     return _call_bwd_ckpt("m2rnn_scan_bwd_finish", q, k, v, f, W, w_r, ckpt, dy, dH_T, math, grad_clip,
                           out.get("dH0") is not None, workspace, stream, out)
 
@@ -506,6 +524,8 @@ def m2rnn_bwd(q, k, v, f, W, w_r, H0, dy, dH_T=None, *, math="auto", grad_clip: 
     dq, dk have q's shape [B,T,Nqk,K]: with a shared query/key (Nqk = 1) they are summed over heads.
     grad_clip > 0 clamps, at every step, each element of the gradient sent back to the step's input
     state to [-grad_clip, grad_clip] (§2.3's per-step clipping); 0 gives the exact gradient."""
+    if stream is not None:
+        return _again(m2rnn_bwd, locals())
     import torch
     dims, dt, m, _, _, _ = _fwd_prepare(q, k, v, f, W, w_r, H0, None, None, math, 0, False)
     B, T, N, K, V, Nqk = dims.B, dims.T, dims.N, dims.K, dims.V, dims.Nqk
@@ -534,6 +554,8 @@ def m2rnn_decode_step(q, k, v, f, W, w_r, H=None, *, H_out=None, y=None, math="a
     w_r: [N,V]; H: the state [B,N,K,V] fp32 or None (zeros).  Returns (y [B,N,V], H_out
     [B,N,K,V]).  Pass ``H_out=H`` to update the state in place.
     """
+    if stream is not None:
+        return _again(m2rnn_decode_step, locals())
     import torch
     if q.dim() != 3 or v.dim() != 3:
         raise ValueError("q must be [B,Nqk,K] and v [B,N,V]")
@@ -588,6 +610,8 @@ def _size_query(name, *args) -> int:
 
 def m2rnn_gate_fwd(a, alpha, beta, *, f=None, stream=None):
     """Gate of the notes' §2.2 (Eq. 13/17): f = exp(-alpha softplus(a + beta)); a [B,T,N], alpha, beta [N]."""
+    if stream is not None:
+        return _again(m2rnn_gate_fwd, locals())
     import torch
     B, T, N = a.shape
     for name, t, shape in (("a", a, (B, T, N)), ("alpha", alpha, (N,)), ("beta", beta, (N,))):
@@ -601,6 +625,8 @@ def m2rnn_gate_fwd(a, alpha, beta, *, f=None, stream=None):
 
 def m2rnn_gate_bwd(a, alpha, beta, df, *, workspace=None, stream=None) -> Dict[str, object]:
     """da [B,T,N], dalpha, dbeta [N] of the gate for the upstream df."""
+    if stream is not None:
+        return _again(m2rnn_gate_bwd, locals())
     import torch
     B, T, N = a.shape
     for name, t, shape in (("a", a, (B, T, N)), ("alpha", alpha, (N,)), ("beta", beta, (N,)), ("df", df, (B, T, N))):
@@ -624,6 +650,8 @@ def _norm_dims(y, gamma):
 def m2rnn_out_norm_fwd(y, gz, gamma, eps: float = 1e-6, *, out=None, stream=None):
     """Output gate + RMSNorm (§2.3, step 4): gamma (.) x / sqrt(mean x^2 + eps), x = y (.) SiLU(gz),
     normalised over gamma's features (for y [B,T,N,V] and gamma [N,V]: all heads of a token)."""
+    if stream is not None:
+        return _again(m2rnn_out_norm_fwd, locals())
     import torch
     rows, D = _norm_dims(y, gamma)
     _require(y, "y", torch.float32, tuple(y.shape), y.device)
@@ -639,6 +667,8 @@ def m2rnn_out_norm_fwd(y, gz, gamma, eps: float = 1e-6, *, out=None, stream=None
 
 def m2rnn_out_norm_bwd(y, gz, gamma, dout, eps: float = 1e-6, *, workspace=None, stream=None) -> Dict[str, object]:
     """dy, dgz (fp32, shaped like y) and dgamma of the output gate + RMSNorm (Appendix C)."""
+    if stream is not None:
+        return _again(m2rnn_out_norm_bwd, locals())
     import torch
     rows, D = _norm_dims(y, gamma)
     _require(y, "y", torch.float32, tuple(y.shape), y.device)
@@ -656,6 +686,8 @@ def m2rnn_out_norm_bwd(y, gz, gamma, dout, eps: float = 1e-6, *, workspace=None,
 
 def m2rnn_conv4_silu_fwd(x, w, bias=None, *, u=None, stream=None):
     """Causal depthwise conv (kernel 4) + SiLU (§2.3, step 1): x [B,T,C] fp32/bf16, w [C,4], bias [C] or None."""
+    if stream is not None:
+        return _again(m2rnn_conv4_silu_fwd, locals())
     import torch
     B, T, C = x.shape
     _require(x, "x", (torch.float32, torch.bfloat16), (B, T, C), x.device)
@@ -672,6 +704,8 @@ def m2rnn_conv4_silu_fwd(x, w, bias=None, *, u=None, stream=None):
 
 def m2rnn_conv4_silu_bwd(x, w, bias, du, *, workspace=None, stream=None) -> Dict[str, object]:
     """dx [B,T,C] fp32, dw [C,4] and dbias [C] (None without a bias) of the causal conv4 + SiLU."""
+    if stream is not None:
+        return _again(m2rnn_conv4_silu_bwd, locals())
     import torch
     B, T, C = x.shape
     _require(x, "x", (torch.float32, torch.bfloat16), (B, T, C), x.device)
@@ -720,7 +754,7 @@ def _tensors_in(*values):
             yield from _tensors_in(*x.values())
 
 
-def _there(dev, stream, f, *args, **kwargs):
+def _there(dev, stream, f, /, *args, **kwargs):
     """f(*args, **kwargs) on the device and stream of a call.  On a stream of its own the caching allocator learns that
     the call's tensors are in use there, and its results on the caller's stream: memory of an input dropped right
     after the call is not handed out while the call still reads it."""
@@ -735,6 +769,14 @@ def _there(dev, stream, f, *args, **kwargs):
             for t in _tensors_in(result):
                 t.record_stream(here)
     return result
+
+
+def _again(f, arguments):
+    """f with its own `arguments` (all by name), on their `stream`: workspaces and results are then that stream's too."""
+    kwargs = dict(arguments)
+    stream = kwargs.pop("stream")
+    dev = next((t.device for t in _tensors_in(kwargs)), stream.device)
+    return _there(dev, stream, f, **kwargs)
 
 
 _raw_stream = None
