@@ -376,11 +376,4 @@ int launch_fwd_finish_norm(const float* part, int S, const void* v, bool v_bf16,
   return hipGetLastError();
 }
 
-size_t sum_rows_scratch(long parts, long M) { return reduce_scratch(parts, M); }
-
-void sum_rows(const float* part, long parts, long M, float* out0, long M0, float* out1, float* scratch,
-              hipStream_t stream) {
-  reduce_rows(part, parts, M, M, out0, M0, out1, scratch, stream);
-}
-
 }  // namespace m2rnn

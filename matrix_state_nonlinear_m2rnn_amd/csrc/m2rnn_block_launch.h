@@ -16,12 +16,4 @@ int launch_fwd_finish_norm(const float* part, int S, const void* v, bool v_bf16,
                            bool gz_bf16, const float* gamma, long B, long T, long t0, long len, int D, float eps,
                            float* out, hipStream_t stream);
 
-// Floats of scratch that sum_rows needs for `parts` rows of M columns.
-size_t sum_rows_scratch(long parts, long M);
-
-// Sums `parts` rows of M contiguous floats into one row by a fixed tree (zeros for no rows): columns
-// j < M0 to out0[j], the others to out1[j - M0].
-void sum_rows(const float* part, long parts, long M, float* out0, long M0, float* out1, float* scratch,
-              hipStream_t stream);
-
 }  // namespace m2rnn

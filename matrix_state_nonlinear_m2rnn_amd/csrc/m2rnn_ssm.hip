@@ -3,7 +3,6 @@
 #include <hip/hip_runtime.h>
 
 #include "../../include/m2rnn.h"
-#include "m2rnn_block_launch.h"
 #include "m2rnn_ssm_select.h"
 
 using namespace m2rnn;
@@ -12,37 +11,47 @@ namespace m2rnn {
 // Status of a HIP call, recording a failure for m2rnn_last_hip_error() (defined with it).
 int record_hip_status(hipError_t e);
 
-// The backward's partial sums over `parts` rows in one launch: gate [parts][2N] to dbeta, dalpha and wr
-// [parts][N V] to dw_r.  A workgroup takes 64 columns (of both arrays, one after the other), its 16 waves
-// every sixteenth row each; the waves' sums are added in order.  The rows and their sums are fp32 (a
-// row of the gate is a chunk's sum in fp64, rounded once): at most 128 rows follow each other in a wave.
-__global__ void __launch_bounds__(1024) m2rnn_ssm_sums_kernel(const float* __restrict__ gate,
-                                                              const float* __restrict__ wr, long parts, int N, long NV,
-                                                              float* __restrict__ dbeta, float* __restrict__ dalpha,
-                                                              float* __restrict__ dw_r) {
-  __shared__ float red[16][64];
+// Rows of partial sums that one workgroup adds (a wave 1/16 of them after each other); more go through a second launch.
+constexpr long kSsmSlice = 2048;
+
+// The backward's partial sums over `parts` rows: gate [parts][2N] to dbeta, dalpha and wr [parts][N V] to dw_r (W: the type of
+// its rows).  A workgroup takes 64 columns (of both arrays, one after the other) of a slice of rows, its 16 waves every
+// sixteenth row each; the waves' sums are added in order.  Everything is added in fp64: over a long sequence the terms of
+// these sums cancel, and fp32 rows and sums left five times the error of dbeta and dw_r.  With more than one
+// slice the slices' sums go to gate_out and wr_out, rows of another call.
+template <typename W>
+__global__ void __launch_bounds__(1024) m2rnn_ssm_sums_kernel(const double* __restrict__ gate, const W* __restrict__ wr,
+                                                              long parts, int N, long NV, double* __restrict__ gate_out,
+                                                              double* __restrict__ wr_out, float* __restrict__ dbeta,
+                                                              float* __restrict__ dalpha, float* __restrict__ dw_r) {
+  __shared__ double red[16][64];
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
   const long gate_groups = (2L * N + 63) / 64;
   const bool g = blockIdx.x < gate_groups;
   const long M = g ? 2L * N : NV, j = ((long)blockIdx.x - (g ? 0 : gate_groups)) * 64 + lane;
-  const float* src = g ? gate : wr;
-  float acc = 0.0f;
-  if (j < M) {
+  const long p0 = (long)blockIdx.y * kSsmSlice, p1 = p0 + kSsmSlice < parts ? p0 + kSsmSlice : parts;
+  double acc = 0.0;
+  if (j < M && g) {
 #pragma unroll 8
-    for (long p = w; p < parts; p += 16) acc += src[p * M + j];
+    for (long p = p0 + w; p < p1; p += 16) acc += gate[p * M + j];
+  } else if (j < M) {
+#pragma unroll 8
+    for (long p = p0 + w; p < p1; p += 16) acc += (double)wr[p * M + j];
   }
   red[w][lane] = acc;
   __syncthreads();
   if (w == 0 && j < M) {
-    float s = 0.0f;
+    double s = 0.0;
 #pragma unroll
     for (int i = 0; i < 16; ++i) s += red[i][lane];
-    if (!g)
-      dw_r[j] = s;
+    if (gridDim.y > 1)
+      (g ? gate_out : wr_out)[(long)blockIdx.y * M + j] = s;
+    else if (!g)
+      dw_r[j] = (float)s;
     else if (j < N)
-      dbeta[j] = s;
+      dbeta[j] = (float)s;
     else
-      dalpha[j - N] = s;
+      dalpha[j - N] = (float)s;
   }
 }
 
@@ -90,10 +99,6 @@ constexpr int kSsmMinChunks = 2;
 // hold one and take about the same (N64 K=128 V=64, one query/key: 1228 us, 1212 with 256, 1242 with 1024).
 constexpr long kSsmBwdGroups = 512;
 
-// Rows of partial sums that one launch adds (one wave 1/16 of them after each other); more go through the
-// tree of slices, whose four launches take 21 us at 256 rows.
-constexpr long kSsmDirectParts = 2048;
-
 int check_ssm(const m2rnn_dims* d, int dtype) {
   if (!d) return M2RNN_EINVAL;
   if (d->B < 0 || d->T < 0 || d->N < 0 || d->K < 0 || d->V < 0 || d->Nqk < 0) return M2RNN_EINVAL;
@@ -107,8 +112,8 @@ int check_ssm(const m2rnn_dims* d, int dtype) {
   return M2RNN_OK;
 }
 
-// The backward's further limits: its partial sums are rows per (b, chunk), 64 to a workgroup of a launch's
-// second axis, and it has one workgroup for each (b, query/key, chunk) (and split of its heads, which only small
+// The backward's further limits: its partial sums are rows per (b, chunk), which two launches of slices add up, and
+// it has one workgroup for each (b, query/key, chunk) (and split of its heads, which only small
 // launches have).
 int check_ssm_bwd(const m2rnn_dims* d, int dtype) {
   const int st = check_ssm(d, dtype);
@@ -171,9 +176,9 @@ Plan make_plan(const m2rnn_dims* d, int dtype, bool bwd) {
     const long parts = (long)A.B * A.nch;
     p.rloc = round_up256(pairs * A.nch * KV * f);
     p.cdec = round_up256(pairs * A.nch * f);
-    p.gate = round_up256((size_t)parts * 2 * A.N * f);
+    p.gate = round_up256((size_t)parts * 2 * A.N * sizeof(double));
     p.wr = round_up256((size_t)parts * A.N * A.V * f);
-    if (parts > kSsmDirectParts) p.scratch = round_up256(sum_rows_scratch(parts, (long)A.N * A.V) * f);
+    if (parts > kSsmSlice) p.scratch = round_up256((size_t)ceil_div(parts, kSsmSlice) * A.N * (2 + A.V) * sizeof(double));
     if (A.HS > 1) p.planes = round_up256((size_t)2 * A.HS * A.B * A.T * A.G * A.K * f);
   }
   p.total = p.seg + p.segdec + p.rloc + p.cdec + p.gate + p.wr + p.scratch + p.planes;
@@ -328,9 +333,9 @@ int m2rnn_ssm_bwd(const m2rnn_dims* dims, int qkv_dtype, const void* q, const vo
   A.segdec = part(p.segdec);
   A.rloc = part(p.rloc);
   A.cdec = part(p.cdec);
-  A.part_gate = part(p.gate);
+  A.part_gate = (double*)part(p.gate);
   A.part_wr = part(p.wr);
-  float* scratch = part(p.scratch);
+  double* scratch = (double*)part(p.scratch);
   float* planes = part(p.planes);
   const long count = (long)A.B * A.T * A.G * A.K;
   A.dq = A.HS > 1 ? planes : dq;
@@ -352,14 +357,15 @@ int m2rnn_ssm_bwd(const m2rnn_dims* dims, int qkv_dtype, const void* q, const vo
                          s, (const float*)A.dq, (const float*)A.dk, A.HS, count, dq, dk);
     }
   }
-  const long NV = (long)A.N * A.V;
-  if (parts <= kSsmDirectParts) {
-    hipLaunchKernelGGL(m2rnn_ssm_sums_kernel, dim3((unsigned)(ceil_div(2L * A.N, 64) + ceil_div(NV, 64))), dim3(1024),
-                       0, s, (const float*)A.part_gate, (const float*)A.part_wr, parts, A.N, NV, dbeta, dalpha, dw_r);
-  } else {
-    sum_rows(A.part_gate, parts, 2L * A.N, dbeta, A.N, dalpha, scratch, s);
-    sum_rows(A.part_wr, parts, NV, dw_r, NV, nullptr, scratch, s);
-  }
+  const long NV = (long)A.N * A.V, slices = ceil_div(parts, kSsmSlice);
+  const unsigned columns = (unsigned)(ceil_div(2L * A.N, 64) + ceil_div(NV, 64));
+  double *gate_sums = scratch, *wr_sums = scratch + slices * 2 * A.N;
+  hipLaunchKernelGGL(m2rnn_ssm_sums_kernel<float>, dim3(columns, (unsigned)(slices > 1 ? slices : 1)), dim3(1024), 0, s,
+                     (const double*)A.part_gate, (const float*)A.part_wr, parts, A.N, NV, gate_sums, wr_sums, dbeta, dalpha,
+                     dw_r);
+  if (slices > 1)
+    hipLaunchKernelGGL(m2rnn_ssm_sums_kernel<double>, dim3(columns), dim3(1024), 0, s, (const double*)gate_sums,
+                       (const double*)wr_sums, slices, A.N, NV, nullptr, nullptr, dbeta, dalpha, dw_r);
   return status(hipGetLastError());
 }
 

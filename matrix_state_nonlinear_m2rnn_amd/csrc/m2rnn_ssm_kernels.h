@@ -30,7 +30,8 @@ struct SsmArgs {
   float* rloc;                             // [B,N,nch,V,K] reverse: the part of the segment's later chunks
   float* cdec;                             // [B,N,nch] reverse: log2 decay from the chunk's end to the segment's
   float *dq, *dk, *dv, *da;                // dq, dk: HS planes of [B,T,G,K]
-  float *part_gate, *part_wr;              // [B nch][2N] (dbeta, dalpha), [B nch][N V]
+  double* part_gate;                       // [B nch][2N] (dbeta, dalpha)
+  float* part_wr;                          // [B nch][N V]
   float* dH0;
   int B, T, N, G, K, V;
   int S, cps, nch;                         // segments, chunks per segment, chunks
@@ -990,21 +991,21 @@ __global__ void __launch_bounds__(64 * kSsmBwdWaves, KP == 128 ? 1 : 2) m2rnn_ss
       gsum += sx64 + prefix64(dpp64<0x138, 0xF>(y)) + through;
       dsum += col + bb;
       if (cb == CB - 1) {
-        const float da = live ? (float)(dsum - (double)A.alpha[head] * gsum) * tab.s[t] : 0.0f;
-        if (t < L && t0 + t < T) A.da[(row0 + t) * N + head] = da;
+        const double da = live ? (dsum - (double)A.alpha[head] * gsum) * (double)tab.s[t] : 0.0;
+        if (t < L && t0 + t < T) A.da[(row0 + t) * N + head] = (float)da;
         const double sb = prefix64(da), sa = prefix64(live ? -delta64 * gsum : 0.0);
         if (lane == 63) {
-          float* o = A.part_gate + ((long)b * A.nch + ch) * 2 * N;
-          o[head] = (float)sb;
-          o[N + head] = (float)sa;
+          double* o = A.part_gate + ((long)b * A.nch + ch) * 2 * N;
+          o[head] = sb;
+          o[N + head] = sa;
         }
         gsum = dsum = 0.0;
       }
     } else if (w == 1 && lane < VB) {
-      float sum = 0.0f;
+      double sum = 0.0;
 #pragma unroll
-      for (int i = 0; i < NI; ++i) sum += dwp[i][lane];
-      A.part_wr[((long)b * A.nch + ch) * vrow + (long)head * V + cb * VB + lane] = sum;
+      for (int i = 0; i < NI; ++i) sum += (double)dwp[i][lane];
+      A.part_wr[((long)b * A.nch + ch) * vrow + (long)head * V + cb * VB + lane] = (float)sum;
     }
   };
 
@@ -1488,19 +1489,19 @@ __global__ void __launch_bounds__(64 * kSsmBwdWaves, KP == 128 ? 1 : 2) m2rnn_ss
     through *= tab.e[L - 1];
     const double x = row - (double)delta * (col - diag) + aa + through, y = (double)delta * bb + through;
     const double gs = __shfl(prefix64(__shfl(x, 63 - lane)), 63 - lane) + prefix64(dpp64<0x138, 0xF>(y));
-    const float da = live ? (float)(col + bb - (double)A.alpha[h] * gs) * tab.s[lane] : 0.0f;
-    if (lane < L && t0 + lane < T) A.da[(row0 + lane) * N + h] = da;
+    const double da = live ? (col + bb - (double)A.alpha[h] * gs) * (double)tab.s[lane] : 0.0;
+    if (lane < L && t0 + lane < T) A.da[(row0 + lane) * N + h] = (float)da;
     const double sb = prefix64(da), sa = prefix64(live ? -(double)delta * gs : 0.0);
     if (lane == 63) {
-      float* o = A.part_gate + ((long)b * A.nch + ch) * 2 * N;
-      o[h] = (float)sb;
-      o[N + h] = (float)sa;
+      double* o = A.part_gate + ((long)b * A.nch + ch) * 2 * N;
+      o[h] = sb;
+      o[N + h] = sa;
     }
     if (lane < V) {
-      float sum = 0.0f;
+      double sum = 0.0;
 #pragma unroll
-      for (int i = 0; i < NI; ++i) sum += sm.dw[i][lane];
-      A.part_wr[((long)b * A.nch + ch) * vrow + (long)h * V + lane] = sum;
+      for (int i = 0; i < NI; ++i) sum += (double)sm.dw[i][lane];
+      A.part_wr[((long)b * A.nch + ch) * vrow + (long)h * V + lane] = (float)sum;
     }
   };
 
