@@ -3,8 +3,8 @@
 //     (xn_a, xn_b) -> (xn_a cos t - xn_b sin t, xn_b cos t + xn_a sin t),   t = pos * inv_freq[p],
 // for the pairs p < R/2 of each head (a = p, b = p + R/2, or interleaved a = 2p, b = 2p + 1); the K - R last
 // features are normalised only.  Backward: gn = the upstream gradient rotated by -t, p = gamma gn,
-//     dx = r (p - xh sum_j(p_j xh_j) / K),   dgamma = sum gn xh,   xh = r x,   r = 1 / sqrt(mean x^2 + eps):
-// no power of r stands alone, so rows of 1e15 keep their projection and rows of zeros with a tiny eps stay finite.
+//     dx = r p - (r^2 sum_j(p_j x_j) / K) (r x),   dgamma = sum gn x r,   r = 1 / sqrt(mean x^2 + eps)
+// (no r^3: rows of 1e15 keep their projection, rows of zeros with a tiny eps stay finite).
 //
 // An HBM stream: each value is read and written once.  A lane holds 4 pairs (8 features) of a head, so
 // the rotation needs no other lane; K/8 lanes (rounded up to a power of two) hold a head and sum its
@@ -167,16 +167,15 @@ __global__ void __launch_bounds__(kBlkThreads) m2rnn_qk_norm_rope_kernel(QkArgs 
         float dot = 0.0f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          x[i] *= r;
-          const float t = y[i] * x[i];
+          const float t = y[i] * x[i] * r;
           aq[i] += isq ? t : 0.0f;
           ak[i] += isq ? 0.0f : t;
           y[i] *= gm[i];
           dot = __builtin_fmaf(y[i], x[i], dot);
         }
-        const float m = head_sum<LPH>(dot) * inv;
+        const float m = head_sum<LPH>(dot) * inv * r * r;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) o[i] = r * (y[i] - m * x[i]);
+        for (int i = 0; i < 8; ++i) o[i] = __builtin_fmaf(r, y[i], -(m * (x[i] * r)));
         if (live) {
           float* dst = (float*)(isq ? A.qo : A.ko);
           const float a4[4] = {o[0], o[1], o[2], o[3]}, b4[4] = {o[4], o[5], o[6], o[7]};
@@ -187,7 +186,8 @@ __global__ void __launch_bounds__(kBlkThreads) m2rnn_qk_norm_rope_kernel(QkArgs 
     }
   }
   if constexpr (BWD) {
-    // the workgroup's sums: lanes of the same unit, then its waves, in a fixed order
+    // the workgroup's sums: lanes of the same unit, then its waves, in a fixed order.  A lane's own sums over its tokens and
+    // these are fp32 (16K tokens of 32 heads: 16 terms a lane, then 32), the rows of the workgroups are added in fp64.
     __shared__ float red[kBlkThreads / 64][2][8 * LPH];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
