@@ -20,6 +20,9 @@ constexpr long kQkWaves = 8192;      // waves that a launch aims for (heads of a
 // Workgroups of the backward, each of which writes one row of partial sums: four waves for each SIMD (16K tokens of
 // 16 + 16 heads, K = 128: 114 us; with twice as many groups 119 us and longer final sums, with half as many 139 us).
 constexpr long kQkMaxGroups = 1024;
+// More than these where a lane would otherwise add more heads than this in fp32 (the rows are added in fp64): the sums of long
+// batches cancel.  1M tokens of 64 heads, K = 64, take 32 times the rows: 16 MB beside tens of GB of gradients.
+constexpr long kQkTerms = 64;
 
 struct QkPlan {
   int LPH = 1, split = 1;
@@ -43,7 +46,11 @@ QkPlan plan_qk(long tokens, int heads, int K, bool bwd) {
   split = split > passes ? passes : split;
   p.split = (int)(split < 1 ? 1 : split);
   p.groups = ceil_div(tokens * p.split, kBlkThreads / 64);
-  const long most = bwd ? kQkMaxGroups : 1L << 22;  // (a launch holds fewer than 2^32 threads)
+  long most = 1L << 22;  // (a launch holds fewer than 2^32 threads)
+  if (bwd) {
+    const long enough = ceil_div(tokens * passes, kQkTerms * (kBlkThreads / 64));
+    most = enough < kQkMaxGroups ? kQkMaxGroups : enough < most ? enough : most;
+  }
   p.groups = p.groups > most ? most : p.groups;
   return p;
 }

@@ -186,8 +186,8 @@ __global__ void __launch_bounds__(kBlkThreads) m2rnn_qk_norm_rope_kernel(QkArgs 
     }
   }
   if constexpr (BWD) {
-    // the workgroup's sums: lanes of the same unit, then its waves, in a fixed order.  A lane's own sums over its tokens and
-    // these are fp32 (16K tokens of 32 heads: 16 terms a lane, then 32), the rows of the workgroups are added in fp64.
+    // the workgroup's sums: lanes of the same unit, then its waves, in a fixed order.  A lane's own sums (of 64
+    // heads at most, by the launch plan) and these are fp32, the rows of the workgroups are added in fp64.
     __shared__ float red[kBlkThreads / 64][2][8 * LPH];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {

@@ -159,6 +159,31 @@ def test_magnitudes_and_small_eps(eps, scale, inter):
                    (rows + 64) * U * np.sum(p / np.abs(d[gamma]) * np.abs(d[x]) * r, axis=(0, 1, 2)))
 
 
+def test_scale_gradients_that_cancel():
+    """Two million tokens, the second half's gradients with the other sign.  A term x r of dgamma meets six roundings, its sum
+    in a lane is of 64 terms, half of each sign: so of 32 terms at most.  The bound is six standard deviations of roundings of
+    2^-24 of their values, evenly distributed."""
+    torch = torch_cuda()
+    import matrix_state_nonlinear_m2rnn_amd as m2
+    T, K = 1 << 21, 16
+    say("qk cancelling sums", T)
+    g = torch.Generator(device="cuda").manual_seed(2)
+    q = torch.empty(1, T, 1, K, device="cuda").normal_(generator=g).abs() + 1.0
+    k = torch.empty(1, T, 0, K, device="cuda")
+    gamma = torch.ones(K, device="cuda")
+    dq = torch.ones_like(q)
+    dq[:, T // 2:] = -1.0
+    pos = torch.zeros(1, T, dtype=torch.int32, device="cuda")
+    d = m2.m2rnn_qk_norm_rope_bwd(q, k, gamma, gamma, pos, torch.empty(0, dtype=torch.float64, device="cuda"), dq, k, 0.0)
+    x = q.double()[0, :, 0]
+    terms = x / x.pow(2).mean(-1, keepdim=True).sqrt()
+    ref = terms[:T // 2].sum(0) - terms[T // 2:].sum(0)
+    tol = 6 * U * torch.sqrt((terms ** 2).sum(0) * (6 ** 2 + 32 ** 2) / 3) + U * ref.abs()
+    worst = float(((d["dgamma_q"].double() - ref).abs() / tol).max())
+    say("dgamma worst error over its bound: %.3g" % worst)
+    assert worst <= 1.0
+
+
 def test_graph_and_stream():
     torch = torch_cuda()
     import matrix_state_nonlinear_m2rnn_amd as m2
