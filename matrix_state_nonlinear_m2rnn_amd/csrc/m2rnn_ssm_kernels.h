@@ -135,9 +135,9 @@ __device__ __forceinline__ void ssm_gate(bool live, float a, float alpha, float 
 // HPW > 1 (V = 16 heads sharing q and k): one wave per head, q k^T formed once for all of them.
 // Otherwise the waves of a head share its masked and decayed q k^T through LDS.
 //
-// Bound by HBM and issue together: at B2 N32 T16384 K=V=64 (bf16) the kernel takes 159 us at best and 187 on average for
+// Bound by HBM and issue together: at B2 N32 T16384 K=V=64 (bf16) the kernel takes 158 us at best and 185 on average for
 // 0.69 GB, 3.7 to 4.4 TB/s, with a SIMD's VALU busy 61% of the cycles and its MFMA 24%; B4 N128 T4096 K=64 V=16 with one
-// query/key takes 102 to 106 us (with checkpoints), VALU 75% (each head's decays and splits for 16 columns).
+// query/key takes 101 to 106 us (with checkpoints), VALU 75% (each head's decays and splits for 16 columns).
 template <bool BF16, int KP, int VB, int HPW>
 __global__ void __launch_bounds__(HPW * VB * 4) m2rnn_ssm_fwd_kernel(SsmArgs A) {
   constexpr int L = ssm_chunk<BF16>(), NI = L / 16, NS = L / 32, KS = KP / 32, KM = KP / 16, NP = BF16 ? 1 : 3;
@@ -1352,7 +1352,7 @@ __device__ __forceinline__ f32x4 mfma16_planes_turned(const uint2 (&A)[NA], cons
 // assignment of the three tasks took 14 to 40 us more).  R is read once, as planes in LDS that serve as R (transposing reads) and as R^T; H goes straight into the
 // operand of the wave that owns its 16 K rows.  X is summed over the heads in registers.
 //
-// B4 N128 T4096 K=64 V=16, one query/key: 351 to 401 us, 368 on average, 11.6 thousand cycles a head for the two
+// B4 N128 T4096 K=64 V=16, one query/key: 346 to 405 us, 367 on average, 11.6 thousand cycles a head for the two
 // workgroups of a CU.
 // Bound by issue and latency at two waves a SIMD (256 VGPRs): VALU 58%, MFMA 18%, LDS 38% of the cycles, HBM at
 // 2.4 TB/s.  Of an earlier 366 us the columns with P and dv took a third, the terms of H and R 47 us, the rows 33, loads 27,
