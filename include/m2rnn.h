@@ -62,8 +62,9 @@ typedef struct m2rnn_dims {
                   the gradients of the shared q and k, summed over the heads (§2.7). */
 } m2rnn_dims;
 
-/* dtype of q, k, v. */
-enum { M2RNN_DTYPE_F32 = 0, M2RNN_DTYPE_BF16 = 1 };
+/* dtype of q, k, v.  E4M3 (OCP 8-bit: 1 sign, 4 exponent and 3 mantissa bits, largest number 448) is an output of
+ * m2rnn_add_norm_fwd only. */
+enum { M2RNN_DTYPE_F32 = 0, M2RNN_DTYPE_BF16 = 1, M2RNN_DTYPE_E4M3 = 2 };
 
 /* How the per-step contraction H_{t-1} W runs on the matrix cores.  The state, the
  * accumulation and everything outside the contraction are fp32 in every mode.
@@ -98,7 +99,7 @@ enum {
  * change of an entry point's arguments, the patch number when entry points are added; a caller
  * built against this header should check that m2rnn_version() == M2RNN_VERSION before calling
  * anything else. */
-#define M2RNN_VERSION 401
+#define M2RNN_VERSION 402
 int m2rnn_version(void);
 
 /* Human-readable text for a status code (static storage). */
@@ -518,6 +519,87 @@ int m2rnn_grad_norm(const m2rnn_tensor* grads, int64_t count, float* norm, void*
                     size_t workspace_bytes, void* stream);
 int m2rnn_grad_clip(const m2rnn_tensor* grads, int64_t count, void* const* out, const float* norm,
                     float max_norm, void* stream);
+
+/*
+ * The entry of a layer (the pre-norm and the residual around a block): the residual stream takes a branch's
+ * output and the sum is normalised for the next branch,
+ *     h = res + x (rounded to the stream's type),   out = gamma (.) h / sqrt(mean_j h_j^2 + eps)
+ * over the D features of each of `rows` rows.  The norm is of h as it is kept.
+ *   x          [rows, D] in x_dtype; res [rows, D] in res_dtype (fp32 or bf16 each), or NULL: h = x, and h must
+ *              be NULL (res_dtype is then not used, but must be one of the two).
+ *   h          [rows, D] in res_dtype, or NULL to skip it.  May be res, or x of the same type (in place).
+ *   out        [rows, D] in out_dtype: fp32, bf16 or E4M3.
+ *   group      E4M3: the features that share a scale, 0 or D (one scale a row) or 128 (D a multiple of 128);
+ *              0 for the other types.
+ *   scale      E4M3: [rows, D / group] fp32, s = max(amax |.| / 448, 2^-126) over the group; out holds the
+ *              norm's values over s, rounded to nearest even, so values are out times scale.
+ *   D a multiple of 4 up to 16384; rows at most 2^31 - 1; eps >= 0.  Squares are summed in fp32 and must stay
+ *   within it (|h| below 1e18).  A row with a value that is not finite is not finite: NaN where the value, or
+ *   its group's scale, is.  Pointers 16-byte aligned (scale 4).  No output may overlap another array except as said.
+ * The backward takes h as kept (x without a residual), dout (fp32) and dh, the gradient that reaches h down the
+ * stream (fp32, or NULL: zeros), and gives dx [rows, D] fp32, which is the gradient of x and of res alike, and
+ * dgamma [D], summed over the rows in a fixed order.  dx may be dout or dh.
+ */
+int m2rnn_add_norm_fwd(int64_t rows, int64_t D, int x_dtype, const void* x, int res_dtype, const void* res,
+                       const float* gamma, float eps, void* h, int out_dtype, int64_t group, void* out, float* scale,
+                       void* stream);
+int m2rnn_add_norm_bwd_workspace_size(int64_t rows, int64_t D, size_t* bytes);
+int m2rnn_add_norm_bwd(int64_t rows, int64_t D, int h_dtype, const void* h, const float* gamma, float eps,
+                       const float* dout, const float* dh, float* dx, float* dgamma, void* workspace,
+                       size_t workspace_bytes, void* stream);
+
+/*
+ * Gated linear recurrence of channels: the blend and the gate of the M²RNN recurrence on a vector state, without
+ * the tanh, for the linear layers of a hybrid stack.  Per (b, d), from h_0 (zeros, or a given state),
+ *     f_t = exp(-alpha softplus(a_t + beta)),   h_t = f_t h_{t-1} + (1 - f_t) v_t,   y_t = h_t
+ *   v, a       [B,T,D] in `dtype` (fp32 or bf16); alpha, beta [D] fp32 (alpha >= 0 keeps f in [0, 1]; not checked,
+ *              computed as given); h0, h_T [B,D] fp32 (NULL: zeros; not written); y [B,T,D] fp32.
+ *   lens       [B] int32 device array or NULL, as in m2rnn_ssm_fwd: steps at or past a sequence's end change
+ *              nothing, their y and gradients are zeros, whatever v and a hold there.  h_T is the state after the
+ *              last step within.  T = 0: h_T = h0.
+ *   D a multiple of 4 up to 2^24, T at most 2^31, B D at most 2^35, and ceil(B D / 256) ceil(T / 64) below 2^23.
+ *   Pointers 16-byte aligned (lens 4).
+ * fp32 arithmetic; 1 - f is formed without cancellation.  A step masked through its gate (a = -infinity or the
+ * lowest number) holds the state, whatever v is.  Any other value that is not finite reaches its own channel of
+ * its own sequence from its step on (an infinity may become NaN), and nothing else.  Two calls on the same inputs
+ * give the same bits.
+ *
+ * m2rnn_gated_scan_bwd gives the gradients of L = sum <dy, y> + <dh_T, h_T> from the forward's inputs and its y:
+ * dv, da [B,T,D], dalpha, dbeta [D] (summed over batch and time), dh0 [B,D] (NULL to skip), all fp32.  It expects
+ * finite values within the sequences (masked steps apart: their a may be -infinity, their v anything).
+ * m2rnn_gated_scan_step is one step for every sequence: v, a [B,D], the state h [B,D] (NULL: zeros) to
+ * h_out [B,D] (which is the step's y too).  h_out may be h; any other overlap is rejected (M2RNN_EINVAL).
+ */
+int m2rnn_gated_scan_fwd_workspace_size(int64_t B, int64_t T, int64_t D, int dtype, size_t* bytes);
+int m2rnn_gated_scan_fwd(int64_t B, int64_t T, int64_t D, int dtype, const void* v, const void* a, const float* alpha,
+                         const float* beta, const int32_t* lens, const float* h0, float* y, float* h_T, void* workspace,
+                         size_t workspace_bytes, void* stream);
+int m2rnn_gated_scan_bwd_workspace_size(int64_t B, int64_t T, int64_t D, int dtype, size_t* bytes);
+int m2rnn_gated_scan_bwd(int64_t B, int64_t T, int64_t D, int dtype, const void* v, const void* a, const float* alpha,
+                         const float* beta, const int32_t* lens, const float* h0, const float* y, const float* dy,
+                         const float* dh_T, float* dv, float* da, float* dalpha, float* dbeta, float* dh0,
+                         void* workspace, size_t workspace_bytes, void* stream);
+int m2rnn_gated_scan_step(int64_t B, int64_t D, int dtype, const void* v, const void* a, const float* alpha,
+                          const float* beta, const float* h, float* h_out, void* stream);
+
+/*
+ * Orthogonalised update of matrices (W of all heads, projections), the step after the clipping for optimisers
+ * that take a matrix's update at equal singular values.  For each m x n matrix of a batch,
+ *     X = G / (||G||_F + eps),  then for each step, with A = X X^T over the shorter side (X transposed if m > n),
+ *     X <- a X + (b A + c A A) X
+ *   g, out     [batch, m, n] in `dtype` (fp32 or bf16); out may be g (any other overlap: M2RNN_EINVAL).
+ *   coefs      host array of `steps` triples (a, b, c), read during the call only.  Singular values must stay below
+ *              2 and |b| s^2 + |c| s^4 below 24 for those that occur (products run on split fp16 values); the usual
+ *              coefficients keep them below 1.25 and 12.  c = 0 (a cubic step) takes two products instead of three.
+ *   steps      1 to 64; m, n up to 65536, batch up to 65535, and less than 2^36 elements in all, sides rounded up
+ *              to 128.
+ * The norm is summed in fp64; products are those of fp32 (fp16 values in two parts, 22 bits, three passes with
+ * fp32 accumulation).  A matrix of zeros gives zeros (eps > 0); one with a value that is not finite is
+ * not finite.  Two calls on the same inputs give the same bits.  Pointers 16-byte aligned.
+ */
+int m2rnn_orthogonalize_workspace_size(int64_t batch, int64_t m, int64_t n, int dtype, size_t* bytes);
+int m2rnn_orthogonalize(int64_t batch, int64_t m, int64_t n, int dtype, const void* g, int64_t steps, const float* coefs,
+                        float eps, void* out, void* workspace, size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

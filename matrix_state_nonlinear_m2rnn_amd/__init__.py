@@ -25,6 +25,7 @@ M2RNN_EHIP = -4
 
 DTYPE_F32 = 0
 DTYPE_BF16 = 1
+DTYPE_E4M3 = 2
 MATH = {"auto": -1, "f32": 0, "f16x3": 1, "bf16x3": 2, "bf16": 3}
 BWD_CHECKPOINT = 64
 
@@ -42,6 +43,9 @@ EXPORTED = (
     "m2rnn_conv4_silu_fwd_state", "m2rnn_conv4_silu_step", "m2rnn_qk_norm_rope_fwd",
     "m2rnn_qk_norm_rope_bwd_workspace_size", "m2rnn_qk_norm_rope_bwd", "m2rnn_grad_norm_workspace_size",
     "m2rnn_grad_norm", "m2rnn_grad_clip",
+    "m2rnn_add_norm_fwd", "m2rnn_add_norm_bwd_workspace_size", "m2rnn_add_norm_bwd",
+    "m2rnn_gated_scan_fwd_workspace_size", "m2rnn_gated_scan_fwd", "m2rnn_gated_scan_bwd_workspace_size",
+    "m2rnn_gated_scan_bwd", "m2rnn_gated_scan_step", "m2rnn_orthogonalize_workspace_size", "m2rnn_orthogonalize",
 )
 
 
@@ -60,7 +64,7 @@ class M2RNNError(RuntimeError):
 _lib = None
 
 # The C ABI version these bindings are written for (M2RNN_VERSION in include/m2rnn.h).
-ABI_VERSION = 401
+ABI_VERSION = 402
 
 
 def lib() -> ctypes.CDLL:
@@ -152,6 +156,16 @@ def lib() -> ctypes.CDLL:
             ("m2rnn_grad_norm_workspace_size", [vp, i64, ctypes.POINTER(sz)]),
             ("m2rnn_grad_norm", [vp, i64, vp, vp, sz, vp]),
             ("m2rnn_grad_clip", [vp, i64, vp, vp, cf, vp]),
+            ("m2rnn_add_norm_fwd", [i64, i64, ci, vp, ci, vp, vp, cf, vp, ci, i64, vp, vp, vp]),
+            ("m2rnn_add_norm_bwd_workspace_size", [i64, i64, ctypes.POINTER(sz)]),
+            ("m2rnn_add_norm_bwd", [i64, i64, ci, vp, vp, cf, vp, vp, vp, vp, vp, sz, vp]),
+            ("m2rnn_gated_scan_fwd_workspace_size", [i64] * 3 + [ci, ctypes.POINTER(sz)]),
+            ("m2rnn_gated_scan_fwd", [i64] * 3 + [ci] + [vp] * 8 + [vp, sz, vp]),
+            ("m2rnn_gated_scan_bwd_workspace_size", [i64] * 3 + [ci, ctypes.POINTER(sz)]),
+            ("m2rnn_gated_scan_bwd", [i64] * 3 + [ci] + [vp] * 14 + [vp, sz, vp]),
+            ("m2rnn_gated_scan_step", [i64] * 2 + [ci] + [vp] * 6 + [vp]),
+            ("m2rnn_orthogonalize_workspace_size", [i64] * 3 + [ci, ctypes.POINTER(sz)]),
+            ("m2rnn_orthogonalize", [i64] * 3 + [ci, vp, i64, vp, cf, vp, vp, sz, vp]),
         ):
             fn = getattr(L, name)
             fn.restype = ci
@@ -1156,3 +1170,211 @@ def m2rnn_grad_clip(grads, max_norm: float, *, norm=None, out=None, workspace=No
     _check("m2rnn_grad_clip", lib().m2rnn_grad_clip(arr, len(grads), dst, _ptr(norm), float(max_norm),
                                                     _stream_of(dev)))
     return norm
+
+
+# ---------------------------------------------------------------- the residual's addition with the norm
+
+def _add_norm_rows(x, gamma):
+    D = gamma.numel()
+    if gamma.dim() != 1 or x.dim() < 1 or x.shape[-1] != D:
+        raise ValueError(f"gamma must be [D] and x [..., D]: got {tuple(gamma.shape)} and {tuple(x.shape)}")
+    if x.device.type != "cuda":
+        raise ValueError("inputs must be on a GPU (HIP) device")
+    return x.numel() // max(D, 1), D
+
+
+def m2rnn_add_norm_fwd(x, gamma, res=None, eps: float = 1e-6, *, out_dtype=None, group: int = 0, h=None, out=None,
+                       scale=None, stream=None) -> Tuple[object, object, object]:
+    """The entry of a layer: h = res + x in the residual stream's dtype (h = x without a residual) and
+    out = gamma (.) h / sqrt(mean h^2 + eps) over the last axis.
+
+    x, res: [..., D] (float32 or bfloat16, each its own); gamma: [D] float32.  out_dtype: float32, bfloat16 (x's
+    dtype by default) or float8_e4m3fn, whose scales (fp32, [..., D / group]) are one for each row (group=0) or one
+    for every 128 features (group=128): values are out times scale.  Returns (out, scale, h), with scale None for
+    the other dtypes.  Pass ``h=res`` to update the stream in place."""
+    import torch
+    rows, D = _add_norm_rows(x, gamma)
+    dev, shape = x.device, x.shape
+    _require(x, "x", (torch.float32, torch.bfloat16), shape, dev)
+    _require(gamma, "gamma", torch.float32, (D,), dev)
+    if res is not None:
+        _require(res, "res", (torch.float32, torch.bfloat16), shape, dev)
+    elif h is not None:
+        raise ValueError("h is the sum with a residual: without one it is x")
+    out_dtype = (x.dtype if out is None else out.dtype) if out_dtype is None else out_dtype
+    codes = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16, torch.float8_e4m3fn: DTYPE_E4M3}
+    if out_dtype not in codes:
+        raise TypeError(f"out_dtype must be float32, bfloat16 or float8_e4m3fn, got {out_dtype}")
+    q8 = out_dtype is torch.float8_e4m3fn
+    if scale is not None and not q8:
+        raise ValueError("scale is an output for float8_e4m3fn only")
+    if q8 and group not in (0, D) and (group != 128 or D % 128):
+        raise ValueError(f"group must be 0 (a row), or 128 if D is a multiple of it: got {group} for D = {D}")
+    if not q8 and group:
+        raise ValueError("group is for float8_e4m3fn only")
+    if _elsewhere(dev, stream):
+        return _there(dev, stream, m2rnn_add_norm_fwd, x, gamma, res, eps, out_dtype=out_dtype, group=group, h=h, out=out,
+                      scale=scale)
+    out = _out(out, "out", out_dtype, shape, x)
+    if q8:
+        scale = _out(scale, "scale", torch.float32, (*shape[:-1], D // (group or D) if D else 0), gamma)
+    if res is not None:
+        h = _out(h, "h", res.dtype, shape, res)
+    _check("m2rnn_add_norm_fwd", lib().m2rnn_add_norm_fwd(
+        rows, D, _dtype_code(x), _ptr(x), _dtype_code(x if res is None else res), _ptr(res), _ptr(gamma), float(eps),
+        _ptr(h), codes[out_dtype], int(group), _ptr(out), _ptr(scale), _stream_of(dev)))
+    return out, scale, x if res is None else h
+
+
+def m2rnn_add_norm_bwd(h, gamma, dout, dh=None, eps: float = 1e-6, *, workspace=None, stream=None,
+                       out=None) -> Dict[str, object]:
+    """Gradients of m2rnn_add_norm_fwd from h as it returned it: dx (fp32, the gradient of x and of the residual
+    alike, with dh, the gradient that reaches h down the stream, added) and dgamma.  dout, dh: fp32, like h.  `out` may
+    hold the tensors to write; its dx may be dout or dh."""
+    import torch
+    rows, D = _add_norm_rows(h, gamma)
+    dev, shape = h.device, h.shape
+    _require(h, "h", (torch.float32, torch.bfloat16), shape, dev)
+    _require(gamma, "gamma", torch.float32, (D,), dev)
+    _require(dout, "dout", torch.float32, shape, dev)
+    if dh is not None:
+        _require(dh, "dh", torch.float32, shape, dev)
+    if _elsewhere(dev, stream):
+        return _there(dev, stream, m2rnn_add_norm_bwd, h, gamma, dout, dh, eps, workspace=workspace, out=out)
+    if out is None:
+        out = {"dx": torch.empty_like(dout), "dgamma": torch.empty_like(gamma)}
+    else:
+        _require(out.get("dx"), "dx", torch.float32, shape, dev)
+        _require(out.get("dgamma"), "dgamma", torch.float32, (D,), dev)
+    nbytes = _size_query("m2rnn_add_norm_bwd_workspace_size", rows, D)
+    ws = _workspace(nbytes, dev, workspace)
+    _check("m2rnn_add_norm_bwd", lib().m2rnn_add_norm_bwd(
+        rows, D, _dtype_code(h), _ptr(h), _ptr(gamma), float(eps), _ptr(dout), _ptr(dh), _ptr(out["dx"]),
+        _ptr(out["dgamma"]), _ptr(ws), nbytes, _stream_of(dev)))
+    return out
+
+
+# ---------------------------------------------------------------- gated linear recurrence of channels
+
+def _gated_inputs(v, a, alpha, beta, state, name, lens, token):
+    import torch
+    if v.dim() != (2 if token else 3):
+        raise ValueError("v must be [B,D]" if token else "v must be [B,T,D]")
+    B, D = v.shape[0], v.shape[-1]
+    dev = v.device
+    if dev.type != "cuda":
+        raise ValueError("inputs must be on a GPU (HIP) device")
+    _require(v, "v", (torch.float32, torch.bfloat16), v.shape, dev)
+    _require(a, "a", v.dtype, v.shape, dev)
+    _require(alpha, "alpha", torch.float32, (D,), dev)
+    _require(beta, "beta", torch.float32, (D,), dev)
+    if state is not None:
+        _require(state, name, torch.float32, (B, D), dev)
+    if lens is not None:
+        _require(lens, "lens", torch.int32, (B,), dev)
+    return B, 1 if token else v.shape[1], D, dev
+
+
+def m2rnn_gated_scan_fwd(v, a, alpha, beta, h0=None, *, lens=None, y=None, h_T=None, return_state: bool = True,
+                         workspace=None, stream=None) -> Tuple[object, object]:
+    """Gated linear recurrence of channels: f = exp(-alpha softplus(a + beta)), h_t = f_t h_{t-1} + (1 - f_t) v_t,
+    y_t = h_t.
+
+    v, a: [B,T,D] (float32 or bfloat16, alike); alpha, beta: [D] float32; h0: [B,D] float32 or None; lens: [B] int32
+    or None (steps at or past a sequence's end change nothing and give y = 0).  Returns (y [B,T,D], h_T [B,D]),
+    float32."""
+    import torch
+    B, T, D, dev = _gated_inputs(v, a, alpha, beta, h0, "h0", lens, False)
+    if _elsewhere(dev, stream):
+        return _there(dev, stream, m2rnn_gated_scan_fwd, v, a, alpha, beta, h0, lens=lens, y=y, h_T=h_T,
+                      return_state=return_state, workspace=workspace)
+    y = _out(y, "y", torch.float32, (B, T, D), v)
+    if h_T is not None or return_state:
+        h_T = _out(h_T, "h_T", torch.float32, (B, D), v if h0 is None else h0)
+    dt = _dtype_code(v)
+    nbytes = _size_query("m2rnn_gated_scan_fwd_workspace_size", B, T, D, dt)
+    ws = _workspace(nbytes, dev, workspace)
+    _check("m2rnn_gated_scan_fwd", lib().m2rnn_gated_scan_fwd(
+        B, T, D, dt, _ptr(v), _ptr(a), _ptr(alpha), _ptr(beta), _ptr(lens), _ptr(h0), _ptr(y), _ptr(h_T), _ptr(ws),
+        nbytes, _stream_of(dev)))
+    return y, h_T
+
+
+def m2rnn_gated_scan_bwd(v, a, alpha, beta, y, dy, h0=None, dh_T=None, *, lens=None, want_dh0: bool = True,
+                         workspace=None, stream=None, out=None) -> Dict[str, object]:
+    """Gradients of L = sum <dy, y> + <dh_T, h_T> of the gated recurrence, from the forward's inputs (and lens) and
+    its y: dv, da, dalpha, dbeta, dh0 (None unless want_dh0), all float32.  `out` may hold the tensors to write."""
+    import torch
+    B, T, D, dev = _gated_inputs(v, a, alpha, beta, h0, "h0", lens, False)
+    _require(y, "y", torch.float32, (B, T, D), dev)
+    _require(dy, "dy", torch.float32, (B, T, D), dev)
+    if dh_T is not None:
+        _require(dh_T, "dh_T", torch.float32, (B, D), dev)
+    if _elsewhere(dev, stream):
+        return _there(dev, stream, m2rnn_gated_scan_bwd, v, a, alpha, beta, y, dy, h0, dh_T, lens=lens, want_dh0=want_dh0,
+                      workspace=workspace, out=out)
+    shapes = {"dv": (B, T, D), "da": (B, T, D), "dalpha": (D,), "dbeta": (D,), "dh0": (B, D)}
+    if out is None:
+        out = {x: torch.empty(s, dtype=torch.float32, device=dev) if x != "dh0" or want_dh0 else None
+               for x, s in shapes.items()}
+    else:
+        for x, s in shapes.items():
+            if x != "dh0" or out.get(x) is not None:
+                _require(out.get(x), x, torch.float32, s, dev)
+    dt = _dtype_code(v)
+    nbytes = _size_query("m2rnn_gated_scan_bwd_workspace_size", B, T, D, dt)
+    ws = _workspace(nbytes, dev, workspace)
+    _check("m2rnn_gated_scan_bwd", lib().m2rnn_gated_scan_bwd(
+        B, T, D, dt, _ptr(v), _ptr(a), _ptr(alpha), _ptr(beta), _ptr(lens), _ptr(h0), _ptr(y), _ptr(dy), _ptr(dh_T),
+        *(_ptr(out.get(x)) for x in shapes), _ptr(ws), nbytes, _stream_of(dev)))
+    return out
+
+
+def m2rnn_gated_scan_step(v, a, alpha, beta, h=None, *, h_out=None, stream=None):
+    """One step of the gated recurrence (decode): v, a [B,D], the state h [B,D] float32 or None (zeros).  Returns the
+    new state [B,D], which is the step's output too.  Pass ``h_out=h`` to update the state in place."""
+    import torch
+    B, _, D, dev = _gated_inputs(v, a, alpha, beta, h, "h", None, True)
+    if _elsewhere(dev, stream):
+        return _there(dev, stream, m2rnn_gated_scan_step, v, a, alpha, beta, h, h_out=h_out)
+    h_out = _out(h_out, "h_out", torch.float32, (B, D), v if h is None else h)
+    _check("m2rnn_gated_scan_step", lib().m2rnn_gated_scan_step(
+        B, D, _dtype_code(v), _ptr(v), _ptr(a), _ptr(alpha), _ptr(beta), _ptr(h), _ptr(h_out), _stream_of(dev)))
+    return h_out
+
+
+# ---------------------------------------------------------------- orthogonalised update
+
+ORTH_COEFS = (3.4445, -4.7750, 2.0315)
+
+
+def m2rnn_orthogonalize(g, steps: int = 5, coefs=ORTH_COEFS, eps: float = 1e-7, *, out=None, workspace=None, stream=None):
+    """The update g [..., m, n] (float32 or bfloat16) of one or more matrices with its singular values taken to about
+    1: X = g / (||g||_F + eps) for each matrix, then `steps` times X <- a X + (b A + c A A) X with A = X X^T.
+    coefs: (a, b, c), or one such triple for each step.  Returns the result in g's dtype; pass ``out=g`` for in place."""
+    import torch
+    if g.dim() < 2:
+        raise ValueError("g must be [..., m, n]")
+    dev, shape = g.device, g.shape
+    if dev.type != "cuda":
+        raise ValueError("inputs must be on a GPU (HIP) device")
+    _require(g, "g", (torch.float32, torch.bfloat16), shape, dev)
+    steps = int(steps)
+    rows = list(coefs)
+    rows = [rows] * steps if rows and not hasattr(rows[0], "__len__") else rows
+    if steps < 1 or len(rows) != steps or any(len(r) != 3 for r in rows):
+        raise ValueError("coefs must be (a, b, c) or one such triple for each of the steps (at least one)")
+    if _elsewhere(dev, stream):
+        return _there(dev, stream, m2rnn_orthogonalize, g, steps, coefs, eps, out=out, workspace=workspace)
+    out = _out(out, "out", g.dtype, shape, g)
+    m, n = shape[-2:]
+    batch = 1
+    for x in shape[:-2]:
+        batch *= x
+    dt = _dtype_code(g)
+    nbytes = _size_query("m2rnn_orthogonalize_workspace_size", batch, m, n, dt)
+    ws = _workspace(nbytes, dev, workspace)
+    arr = (ctypes.c_float * (3 * steps))(*(float(x) for r in rows for x in r))
+    _check("m2rnn_orthogonalize", lib().m2rnn_orthogonalize(batch, m, n, dt, _ptr(g), steps, arr, float(eps), _ptr(out),
+                                                            _ptr(ws), nbytes, _stream_of(dev)))
+    return out

@@ -32,6 +32,9 @@ SOURCES = [
     "m2rnn_ssm_bwd_f32.hip",
     "m2rnn_qk.hip",
     "m2rnn_grad.hip",
+    "m2rnn_norm.hip",
+    "m2rnn_gated.hip",
+    "m2rnn_orth.hip",
 ]
 
 # Packed fp32 VALU ops stay off: hipcc -O3 would otherwise form v_pk_{add,mul,fma}_f32.

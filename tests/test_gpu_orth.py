@@ -1,0 +1,117 @@
+"""The orthogonalised update on the GPU against the fp64 oracle.
+
+Tolerance: the oracle itself with roundings put in at random where the kernels round.  A stored matrix keeps 22 bits (an error
+of up to 2^-23 of each value), and a product over K terms is accumulated in fp32 in K/16 partial sums of each of three
+passes, which as a random walk is 2^-24 sqrt(3 K / 16) of its typical value, 2^-22 more for the pass that is left
+out.  Six times the difference that such roundings make (the larger of two draws), as a norm, plus half a bf16 step.
+"""
+import numpy as np
+import pytest
+
+from _gpu import say, torch_cuda
+from oracle import layer
+
+pytestmark = pytest.mark.gpu
+
+COEFS = (3.4445, -4.7750, 2.0315)
+
+
+def gradient(batch, m, n, seed, dtype):
+    import torch
+    r = np.random.default_rng(seed)
+    k = max(1, min(m, n) // 8)
+    g = (r.normal(0, 1, (batch, m, k)) * np.exp(-3.0 * np.arange(k) / k)) @ r.normal(0, 1, (batch, k, n)) + r.normal(0, 0.3, (batch, m, n))
+    t = torch.tensor(g * 1e-3, dtype=torch.float32, device="cuda")
+    return t.to(torch.bfloat16) if dtype == "bf16" else t
+
+
+def noisy(seed):
+    r = np.random.default_rng(seed)
+
+    def put(x, K):
+        e = x * r.uniform(-1, 1, x.shape) * 2.0 ** -23
+        if K:
+            e = e + r.normal(0, 1, x.shape) * np.sqrt(np.mean(x * x)) * (2.0 ** -22 + 2.0 ** -24 * np.sqrt(3 * K / 16))
+        return x + e
+    return put
+
+
+def check(g, out, steps=5, coefs=COEFS, eps=1e-7):
+    import torch
+    assert out.dtype == g.dtype and out.shape == g.shape
+    G, O = g.double().cpu().numpy(), out.double().cpu().numpy()
+    G, O = G.reshape(-1, *G.shape[-2:]), O.reshape(-1, *O.shape[-2:])
+    for b in range(G.shape[0]):
+        ref = layer.orthogonalize(G[b], steps, coefs, eps)
+        tol = 6 * max(np.linalg.norm(layer.orthogonalize(G[b], steps, coefs, eps, noisy(s)) - ref) for s in (1, 2))
+        tol += (2.0 ** -8 if g.dtype == torch.bfloat16 else 0.0) * np.linalg.norm(ref)
+        d = np.linalg.norm(O[b] - ref)
+        assert d <= tol, (b, d, tol, np.linalg.norm(ref))
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("batch,m,n", [(1, 1, 1), (2, 1, 7), (3, 16, 16), (5, 33, 17), (2, 64, 64), (3, 63, 65), (1, 64, 130),
+                                       (2, 128, 128), (1, 129, 515), (2, 300, 100), (1, 256, 1000), (1, 513, 400), (1, 1, 5000)])
+def test_against_the_oracle(batch, m, n, dtype):
+    torch = torch_cuda()
+    import matrix_state_nonlinear_m2rnn_amd as m2
+    say("orth", batch, m, n, dtype)
+    g = gradient(batch, m, n, m + n, dtype)
+    out = m2.m2rnn_orthogonalize(g)
+    check(g, out)
+    size = m2._size_query("m2rnn_orthogonalize_workspace_size", batch, m, n, m2._dtype_code(g))
+    again = m2.m2rnn_orthogonalize(g, workspace=torch.full((size + 16,), 255, dtype=torch.uint8, device="cuda"))
+    assert torch.equal(again, out)
+    assert m2.m2rnn_orthogonalize(g, out=g) is g and torch.equal(g, out)
+
+
+@pytest.mark.parametrize("m,n", [(16, 16), (64, 48), (40, 200), (128, 96), (140, 300)])
+def test_steps_and_coefficients(m, n):
+    torch = torch_cuda()
+    import matrix_state_nonlinear_m2rnn_amd as m2
+    say("orth coefs", m, n)
+    g = gradient(2, m, n, 3, "fp32")
+    check(g, m2.m2rnn_orthogonalize(g, 1), 1)
+    check(g, m2.m2rnn_orthogonalize(g, 8, (1.5, -0.5, 0.0), 1e-6), 8, (1.5, -0.5, 0.0), 1e-6)
+    rows = [(3.0, -3.5, 1.5), (1.5, -0.5, 0.0), (2.0, -1.5, 0.5)]
+    check(g, m2.m2rnn_orthogonalize(g, 3, rows), 3, rows)
+    # one matrix at a time, two leading axes: the same bits
+    a = m2.m2rnn_orthogonalize(g)
+    assert torch.equal(m2.m2rnn_orthogonalize(g[1].contiguous()), a[1])
+    assert torch.equal(m2.m2rnn_orthogonalize(g.view(1, 2, m, n)), a.view(1, 2, m, n))
+
+
+@pytest.mark.parametrize("m,n", [(24, 40), (64, 64), (150, 90)])
+def test_scales_and_values_that_are_not_finite(m, n):
+    """Any scale of the gradient gives the same result; zeros give zeros; one matrix that is not finite leaves the
+    others of the batch their bits."""
+    torch = torch_cuda()
+    import matrix_state_nonlinear_m2rnn_amd as m2
+    g = gradient(4, m, n, 5, "fp32")
+    a = m2.m2rnn_orthogonalize(g, eps=0.0)
+    for k in (-80, 60):  # squares far outside fp32
+        assert torch.equal(m2.m2rnn_orthogonalize(g * 2.0 ** k, eps=0.0), a)
+    b = g.clone()
+    b[0] = 0.0
+    b[2, m // 2, n // 2] = float("nan")
+    o, ref = m2.m2rnn_orthogonalize(b), m2.m2rnn_orthogonalize(g)
+    assert not o[0].any() and torch.equal(o[1], ref[1]) and torch.equal(o[3], ref[3])
+    assert not torch.isfinite(o[2]).any()
+    one = torch.zeros(1, m, n, device="cuda")
+    one[0, 3, 5] = -2e-3  # a single entry: rank one, all of the norm
+    check(one, m2.m2rnn_orthogonalize(one))
+
+
+def test_empty_and_refusals():
+    torch = torch_cuda()
+    import matrix_state_nonlinear_m2rnn_amd as m2
+    for shape in ((0, 4, 4), (2, 0, 4), (2, 4, 0)):
+        assert m2.m2rnn_orthogonalize(torch.zeros(shape, device="cuda")).shape == shape
+    g = torch.randn(8, 12, device="cuda")
+    for kw, err in ((dict(steps=0), ValueError), (dict(coefs=(1.0, 2.0)), ValueError), (dict(coefs=[COEFS] * 4), ValueError),
+                    (dict(steps=65), m2.M2RNNError), (dict(eps=-1.0), m2.M2RNNError), (dict(out=g.bfloat16()), TypeError)):
+        with pytest.raises(err):
+            m2.m2rnn_orthogonalize(g, **kw)
+    for bad, err in ((g.half(), TypeError), (g.t(), ValueError), (g[0], ValueError)):
+        with pytest.raises(err):
+            m2.m2rnn_orthogonalize(bad)
