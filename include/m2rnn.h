@@ -557,10 +557,10 @@ int m2rnn_add_norm_bwd(int64_t rows, int64_t D, int h_dtype, const void* h, cons
  *   lens       [B] int32 device array or NULL, as in m2rnn_ssm_fwd: steps at or past a sequence's end change
  *              nothing, their y and gradients are zeros, whatever v and a hold there.  h_T is the state after the
  *              last step within.  T = 0: h_T = h0.
- *   D a multiple of 4 up to 2^24, T at most 2^31, B D at most 2^35, and ceil(B D / 256) ceil(T / 64) below 2^23.
+ *   D a multiple of 4 up to 2^24, T at most 2^30, B D at most 2^35, and ceil(B D / 256) ceil(T / 32) below 2^23.
  *   Pointers 16-byte aligned (lens 4).
- * fp32 arithmetic; 1 - f is formed without cancellation.  A step masked through its gate (a = -infinity or the
- * lowest number) holds the state, whatever v is.  Any other value that is not finite reaches its own channel of
+ * fp32 arithmetic; 1 - f is formed without cancellation.  A step whose 1 - f is zero (a = -infinity or the lowest
+ * number: masked through its gate; alpha = 0) holds the state, whatever v is.  Any other value that is not finite reaches its own channel of
  * its own sequence from its step on (an infinity may become NaN), and nothing else.  Two calls on the same inputs
  * give the same bits.
  *

@@ -5,24 +5,32 @@
 //     da_t = -alpha sigma(a_t + beta) G_t,  dalpha = -sum s G,  dbeta = sum da,  dh_0 = C_1.
 //
 // The recurrence is linear in h, so a stretch of steps is one map h -> P h + l with P = exp(-sum of alpha s): a
-// workgroup takes a chunk of 64 steps of 256 channels (8 waves of 8 steps each; a lane has 4 neighbouring channels), each
-// lane runs its 8 steps from zero, the waves' maps are joined in LDS, and the lane runs its steps again from the state that
-// enters them.
+// workgroup takes a chunk of 64 steps (backward: 32) of 256 channels, 8 waves of 8 (4) steps each; a lane has 4
+// neighbouring channels.  Each lane runs its steps from zero, the waves' maps are joined in LDS, and the lane runs its
+// steps again from the state that enters them.  The inputs are read once: a workgroup keeps its chunk in registers until it
+// knows the state that enters it.  It leaves its chunk's map in memory, and takes the maps of the chunks before it in its
+// group and the state that enters the group, which the last workgroup of the group before leaves; all joins have a
+// fixed order.
+//
+// Workgroups take chunks by a ticket, all channels of a chunk before the next chunk.  One waits only for smaller
+// tickets, whose workgroups are running and do not wait for it, so every wait ends.  Each word that is waited for says
+// itself whether it has been written (a clearing launch sets all bits of it), so no order of memory operations is needed.
 //
 // Precision.  A gate next to 1 keeps its digits as i = 1 - f (a series in alpha s), and f h is then h - i h: f
 // itself, rounded to fp32, would be wrong by 2^-25 the same way at every step of a constant gate, 3e-4 of the memory's
-// length at i = 1e-4.  Steps with s = 0 (a masked through -infinity or the lowest number, or past the sequence's
+// length at i = 1e-4.  Steps with i = 0 (a masked through -infinity or the lowest number, or past the sequence's
 // end) hold the state whatever v is.
 #pragma once
 
-#include "m2rnn_ssm_device.h"
 #include "m2rnn_stream.h"
 
 namespace m2rnn {
 
-constexpr int kGatedSteps = 8;                         // steps of a lane
-constexpr int kGatedWaves = 8;                         // waves of a workgroup
-constexpr int kGatedChunk = kGatedSteps * kGatedWaves; // steps of a workgroup
+constexpr int kGatedWaves = 8;                        // waves of a workgroup
+constexpr int kGatedStepsFwd = 8, kGatedStepsBwd = 4; // steps of a lane (128 registers: two workgroups a CU)
+constexpr int kGatedGroup = 16;                       // chunks of a group at most
+constexpr int kGatedLook = 8;                         // maps that are looked at together
+constexpr int kGatedPolls = 1 << 22;                  // looks at a word that is waited for: seconds, where microseconds do
 
 struct GatedArgs {
   const void *v, *a;                 // [B,T,D]
@@ -30,36 +38,56 @@ struct GatedArgs {
   const int* lens;                   // [B] or NULL
   const float* h0;                   // [B,D] or NULL
   float *y, *h_T;                    // [B,T,D], [B,D]
-  float2* agg;                       // [chunks][B D]: (sum of alpha s, l) of each chunk; then x = the state that enters it
-  long T, cols;                      // cols = B D
-  int D, chunks;
+  unsigned long long* maps;          // [chunks][blocks][4][64]: (P as a Decay, l) of each chunk, by channel and lane
+  unsigned long long* entry;         // [groups of chunks][blocks][4][64]: the state that enters each group but the first
+  unsigned* ticket;
+  long T, cols, blocks;              // cols = B D; blocks of 64 lanes of 4 channels
+  int D, chunks, group;              // chunks of a group
   // backward
   const float *yin, *dy, *dh_T;      // the forward's y; dh_T NULL: zeros
   float *dv, *da, *dh0;
   float2* part;                      // [chunks][B D]: dalpha, dbeta of each chunk
+  long first_words;                  // words that the clearing launch sets, from maps on
 };
 
-// What multiplies h: f itself, or i = 1 - f where it is small.
+// softplus(z) and sigma(z) to a few ulp also where they are small: t = e^-|z| (the exponential's argument in two parts),
+// softplus = max(z, 0) + 2 atanh(s), s = t / (2 + t) <= 1/3, atanh(s) / s in s^2 by a polynomial through the Chebyshev
+// points (off by less than 2^-25).  SG: sigma too.
+template <bool SG>
+__device__ __forceinline__ float gated_softplus(float z, float& sg) {
+  constexpr float kL = 1.4426950408889634f, kLlo = (float)(1.4426950408889634 - (double)kL);
+  const float m = fminf(fabsf(z), 128.0f), x = m * -kL;
+  float t = __builtin_amdgcn_exp2f(x);
+  t = __builtin_fmaf(t, (__builtin_fmaf(m, -kL, -x) - m * kLlo) * 0.69314718f, t);
+  const float s = t * __builtin_amdgcn_rcpf(2.0f + t), s2 = s * s, d = s + s;
+  float p = __builtin_fmaf(0.13425749f, s2, 0.141183099f);
+  p = __builtin_fmaf(p, s2, 0.200037803f);
+  p = __builtin_fmaf(p, s2, 0.333333202f);
+  if constexpr (SG) {
+    const float r = __builtin_amdgcn_rcpf(1.0f + t);
+    sg = z < 0.0f ? t * r : r;
+  }
+  return (z < 0.0f ? 0.0f : z) + __builtin_fmaf(d, s2 * p, d);  // (NaN stays NaN)
+}
+
+// What multiplies h: f itself, or -i = f - 1 where f is next to 1 (its sign bit tells them apart; a mask for each step
+// of a lane would not fit the scalar registers).
 struct Decay {
   float c;
-  bool near;
-  __device__ __forceinline__ float operator()(float h) const { return __builtin_fmaf(c, h, near ? h : 0.0f); }
+  __device__ __forceinline__ float operator()(float h) const {
+    return __builtin_fmaf(c, h, __float_as_int(c) < 0 ? h : 0.0f);
+  }
+  __device__ __forceinline__ float i() const { return __float_as_int(c) < 0 ? -c : 1.0f - c; }
 };
 
-// The decay of alpha s = x (any sign), and i = 1 - e^-x.
-__device__ __forceinline__ Decay decay_of(float x, float& i) {
+// The decay of alpha s = x; i = 1 - f next to 1 is x times a polynomial through the Chebyshev points (2^-28).
+__device__ __forceinline__ Decay decay_of(float x) {
+  float p = __builtin_fmaf(0.00751360622f, x, -0.0414906541f);
+  p = __builtin_fmaf(p, x, 0.166651082f);
+  p = __builtin_fmaf(p, x, -0.499999515f);
+  p = __builtin_fmaf(p, x, 0.999999998f);
   Decay d;
-  d.near = fabsf(x) < 0.25f;
-  // x (1 - x/2 (1 - x/3 (1 - ... x/7))): the first term left out is below 2^-29
-  float p = __builtin_fmaf(x, -1.0f / 7.0f, 1.0f);
-  p = __builtin_fmaf(x * (-1.0f / 6.0f), p, 1.0f);
-  p = __builtin_fmaf(x * (-1.0f / 5.0f), p, 1.0f);
-  p = __builtin_fmaf(x * (-1.0f / 4.0f), p, 1.0f);
-  p = __builtin_fmaf(x * (-1.0f / 3.0f), p, 1.0f);
-  p = __builtin_fmaf(x * (-1.0f / 2.0f), p, 1.0f);
-  const float f = exp2_(x * -1.4426950408889634f);
-  i = d.near ? x * p : 1.0f - f;
-  d.c = d.near ? -i : f;
+  d.c = __float_as_uint(x) < __float_as_uint(0.25f) ? -x * p : __builtin_amdgcn_exp2f(x * -1.4426950408889634f);
   return d;
 }
 
@@ -70,12 +98,19 @@ __device__ __forceinline__ void gated_load(const void* p, long at, float (&o)[4]
   o[0] = t.x; o[1] = t.y; o[2] = t.z; o[3] = t.w;
 }
 
+// x y, and 0 where either is 0, whatever the other is.
+__device__ __forceinline__ float mul_or_0(float x, float y) {
+  float z;
+  asm("v_mul_legacy_f32 %0, %1, %2" : "=v"(z) : "v"(x), "v"(y));
+  return z;
+}
+
 // A lane's place: its 4 channels, its sequence and its steps.
 struct GatedLane {
   long col;     // b D + d
   long base;    // offset of (b, 0, d)
   int d;
-  long len;     // steps of the sequence
+  int len;      // steps of the sequence
   bool on;
 };
 __device__ __forceinline__ GatedLane gated_lane(const GatedArgs& A, long block) {
@@ -88,53 +123,145 @@ __device__ __forceinline__ GatedLane gated_lane(const GatedArgs& A, long block) 
   L.base = b * A.T * A.D + L.d;
   long n = A.lens ? (long)A.lens[b] : A.T;
   n = n < 0 ? 0 : n > A.T ? A.T : n;
-  L.len = L.on ? n : 0;
+  L.len = L.on ? (int)n : 0;
   return L;
 }
 
-// The waves' maps in LDS: (sum of alpha s, l) by wave and channel.
+// The waves' maps in LDS by wave and channel: the sum of alpha s, P, and l, whose place the state that enters the
+// wave's steps takes.
 struct GatedJoin {
-  float x[kGatedWaves][4][64], l[kGatedWaves][4][64];
+  float x[kGatedWaves][4][64], c[kGatedWaves][4][64], l[kGatedWaves][4][64];
+  unsigned ticket;
 };
 
-// OUT false: the chunks' maps to agg.  true: y, from the states that enter the chunks (agg.x).
-template <bool BF16, bool OUT>
-__global__ void __launch_bounds__(64 * kGatedWaves) m2rnn_gated_fwd_kernel(GatedArgs A) {
+// Sets the words that will be waited for and the ticket's counter.
+__global__ void __launch_bounds__(kBlkThreads) m2rnn_gated_clear_kernel(GatedArgs A) {
+  const long step = (long)gridDim.x * kBlkThreads;
+  for (long i = (long)blockIdx.x * kBlkThreads + threadIdx.x; i < A.first_words; i += step) A.maps[i] = ~0ull;
+  if (blockIdx.x == 0 && threadIdx.x == 0) *A.ticket = 0;
+}
+
+// A map or a state as a word that is not all ones: its high half is never the NaN with all bits set.
+__device__ __forceinline__ unsigned long long gated_word(float c, float l) {
+  const uint32_t hi = c != c ? 0x7FC00000u : __float_as_uint(c);
+  return (unsigned long long)hi << 32 | __float_as_uint(l);
+}
+__device__ __forceinline__ void gated_put(unsigned long long* p, unsigned long long w) {
+  __hip_atomic_store(p, w, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ unsigned long long gated_get(const unsigned long long* p) {
+  return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+// The chunk of a workgroup in the order of the recurrence (0: first; the backward's first is the last in time), and its block.
+__device__ __forceinline__ void gated_place(const GatedArgs& A, GatedJoin& J, long& order, long& block) {
+  long id = blockIdx.x;
+  if (A.chunks > 1) {
+    if (threadIdx.x == 0) J.ticket = atomicAdd(A.ticket, 1u);
+    __syncthreads();
+    id = (long)(unsigned)__builtin_amdgcn_readfirstlane((int)J.ticket);
+  }
+  order = id / A.blocks;
+  block = id % A.blocks;
+}
+
+// The states that enter the waves' steps to J.l, from the waves' maps (BACK: the last wave's steps are the first).
+// Waves 0 to 3 take a channel each; the state behind the last chunk goes to `last`.
+template <bool BACK>
+__device__ __forceinline__ void gated_enter(const GatedArgs& A, GatedJoin& J, long order, long block, int lane, int w,
+                                            const GatedLane& L, const float* first, float* last) {
+  if (w < 4) {
+    float x = 0.0f, sum = 0.0f;
+#pragma unroll
+    for (int j = 0; j < kGatedWaves; ++j) {
+      const int k = BACK ? kGatedWaves - 1 - j : j;
+      x += J.x[k][w][lane];
+      sum = Decay{J.c[k][w][lane]}(sum) + J.l[k][w][lane];
+    }
+    const Decay all = decay_of(x);
+    const long at = (block * 4 + w) * 64, row = A.blocks * 256;
+    const int group = (int)order / A.group, before = (int)order % A.group;
+    const bool end = order + 1 == A.chunks, group_end = before + 1 == A.group;
+    if (!end && !group_end) gated_put(A.maps + order * row + at + lane, gated_word(all.c, sum));
+    float h = 0.0f;
+    if (group > 0) {
+      const unsigned long long* src = A.entry + group * row + at;
+      unsigned long long word;
+      for (int polls = 0; polls < kGatedPolls; ++polls) {
+        word = gated_get(src + lane);
+        if (__builtin_amdgcn_ballot_w64((uint32_t)(word >> 32) == 0xFFFFFFFFu) == 0) break;
+        __builtin_amdgcn_s_sleep(1);
+      }
+      h = __uint_as_float((uint32_t)word);
+    } else if (first && L.on) {
+      h = first[L.col + w];
+    }
+    for (int j0 = 0; j0 < before; j0 += kGatedLook) {
+      const unsigned long long* src = A.maps + ((long)group * A.group + j0) * row + at;
+      unsigned long long word[kGatedLook];
+      for (int polls = 0; polls < kGatedPolls; ++polls) {
+        bool there = true;
+#pragma unroll
+        for (int j = 0; j < kGatedLook; ++j)
+          if (j0 + j < before) word[j] = gated_get(src + j * row + lane);
+#pragma unroll
+        for (int j = 0; j < kGatedLook; ++j)
+          if (j0 + j < before) there = there && (uint32_t)(word[j] >> 32) != 0xFFFFFFFFu;
+        if (__builtin_amdgcn_ballot_w64(!there) == 0) break;
+        __builtin_amdgcn_s_sleep(1);
+      }
+#pragma unroll
+      for (int j = 0; j < kGatedLook; ++j)
+        if (j0 + j < before)
+          h = Decay{__uint_as_float((uint32_t)(word[j] >> 32))}(h) + __uint_as_float((uint32_t)word[j]);
+    }
+    if (group_end && !end) gated_put(A.entry + (group + 1) * row + at + lane, gated_word(0.0f, all(h) + sum));
+    if (end && last && L.on) last[L.col + w] = all(h) + sum;
+#pragma unroll
+    for (int j = 0; j < kGatedWaves; ++j) {
+      const int k = BACK ? kGatedWaves - 1 - j : j;
+      const float l = J.l[k][w][lane];
+      J.l[k][w][lane] = h;
+      h = Decay{J.c[k][w][lane]}(h) + l;
+    }
+  }
+  __syncthreads();
+}
+
+template <bool BF16>
+__global__ void __launch_bounds__(64 * kGatedWaves, 4) m2rnn_gated_fwd_kernel(GatedArgs A) {
+  constexpr int NS = kGatedStepsFwd;
   __shared__ GatedJoin J;
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-  const long blocks = (A.cols / 4 + 63) / 64;
-  const long chunk = blockIdx.x / blocks;
-  const GatedLane L = gated_lane(A, blockIdx.x % blocks);
-  const long t0 = chunk * kGatedChunk + w * kGatedSteps;
-  Decay dec[kGatedSteps][4];
-  float b[kGatedSteps][4];
-  float al[4], be[4], sum[4], l[4];
+  long chunk, block;
+  gated_place(A, J, chunk, block);
+  const GatedLane L = gated_lane(A, block);
+  const int t0 = ((int)chunk * kGatedWaves + w) * NS;
+  Decay dec[NS][4];
+  float b[NS][4], sum[4], l[4];
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    al[e] = A.alpha[L.d + e];
-    be[e] = A.beta[L.d + e];
-    sum[e] = l[e] = 0.0f;
-  }
+  for (int e = 0; e < 4; ++e) sum[e] = l[e] = 0.0f;
   const bool some = __builtin_amdgcn_ballot_w64(t0 < L.len) != 0;  // whether any lane has a step in here
   if (some) {
-    float va[kGatedSteps][4];
+    float va[NS][4], al[4], be[4];
 #pragma unroll
-    for (int i = 0; i < kGatedSteps; ++i) {
+    for (int i = 0; i < NS; ++i) {
       const long t = t0 + i < A.T ? t0 + i : A.T - 1;
       gated_load<BF16>(A.a, L.base + t * A.D, va[i]);
       gated_load<BF16>(A.v, L.base + t * A.D, b[i]);
     }
+    gated_load<false>(A.alpha, L.d, al);
+    gated_load<false>(A.beta, L.d, be);
 #pragma unroll
-    for (int i = 0; i < kGatedSteps; ++i) {
+    for (int i = 0; i < NS; ++i) {
       const bool live = t0 + i < L.len;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        float s, sg, in;
-        softplus_sigma(va[i][e] + be[e], s, sg);
-        s = live ? s : 0.0f;
-        const float x = s == 0.0f ? 0.0f : al[e] * s;
-        dec[i][e] = decay_of(x, in);
-        b[i][e] = s == 0.0f ? 0.0f : in * b[i][e];
+        float sg;
+        const float s = gated_softplus<false>(va[i][e] + be[e], sg);
+        const float x = live ? al[e] * s : 0.0f;
+        dec[i][e] = decay_of(x);
+        b[i][e] = mul_or_0(dec[i][e].i(), b[i][e]);  // (0 times anything is 0)
         sum[e] += x;
         l[e] = dec[i][e](l[e]) + b[i][e];
       }
@@ -143,115 +270,65 @@ __global__ void __launch_bounds__(64 * kGatedWaves) m2rnn_gated_fwd_kernel(Gated
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     J.x[w][e][lane] = sum[e];
+    J.c[w][e][lane] = decay_of(sum[e]).c;
     J.l[w][e][lane] = l[e];
   }
   __syncthreads();
-  if constexpr (!OUT) {
-    if (w == 0 && L.on) {
-      float4 o[2];
-      float* q = (float*)o;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        float x = 0.0f, h = 0.0f, in;
-#pragma unroll
-        for (int j = 0; j < kGatedWaves; ++j) {
-          h = decay_of(J.x[j][e][lane], in)(h) + J.l[j][e][lane];
-          x += J.x[j][e][lane];
-        }
-        q[2 * e] = x;
-        q[2 * e + 1] = h;
-      }
-      float4* dst = (float4*)(A.agg + chunk * A.cols + L.col);
-      dst[0] = o[0];
-      dst[1] = o[1];
-    }
-    return;
-  }
+  gated_enter<false>(A, J, chunk, block, lane, w, L, A.h0, A.h_T);
   if (!L.on) return;
   float h[4];
 #pragma unroll
-  for (int e = 0; e < 4; ++e) h[e] = A.agg[chunk * A.cols + L.col + e].x;
-  for (int j = 0; j < w; ++j) {
-    float in;
+  for (int e = 0; e < 4; ++e) h[e] = J.l[w][e][lane];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) h[e] = decay_of(J.x[j][e][lane], in)(h[e]) + J.l[j][e][lane];
-  }
-#pragma unroll
-  for (int i = 0; i < kGatedSteps; ++i) {
+  for (int i = 0; i < NS; ++i) {
     const long t = t0 + i;
     float o[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       if (some) h[e] = dec[i][e](h[e]) + b[i][e];
-      o[e] = t < L.len ? h[e] : 0.0f;
+      o[e] = t0 + i < L.len ? h[e] : 0.0f;
     }
     if (t < A.T) store4_nt<false>(A.y, L.base + t * A.D, o);
   }
 }
 
-// The state that enters each chunk, from the chunks' maps (forward: from the first chunk on and h_T at the end;
-// backward: from the last chunk on and dh0).  A thread per channel.
-template <bool BACK>
-__global__ void __launch_bounds__(kBlkThreads) m2rnn_gated_join_kernel(float2* agg, long cols, int chunks,
-                                                                       const float* first, float* last) {
-  const long c = (long)blockIdx.x * kBlkThreads + threadIdx.x;
-  if (c >= cols) return;
-  float h = first ? first[c] : 0.0f;
-  for (int j = 0; j < chunks; j += 8) {
-    float2 m[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int k = j + i < chunks ? j + i : chunks - 1;
-      m[i] = agg[(BACK ? chunks - 1 - k : k) * cols + c];
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if (j + i >= chunks) break;
-      float in;
-      agg[(BACK ? chunks - 1 - (j + i) : j + i) * cols + c].x = h;
-      h = decay_of(m[i].x, in)(h) + m[i].y;
-    }
-  }
-  if (last) last[c] = h;
-}
-
-// OUT false: the chunks' reverse maps C -> P C + l to agg.  true: the gradients, from the C that enter the chunks.
-template <bool BF16, bool OUT>
-__global__ void __launch_bounds__(64 * kGatedWaves) m2rnn_gated_bwd_kernel(GatedArgs A) {
+template <bool BF16>
+__global__ void __launch_bounds__(64 * kGatedWaves, 4) m2rnn_gated_bwd_kernel(GatedArgs A) {
+  constexpr int NS = kGatedStepsBwd;
   __shared__ GatedJoin J;
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-  const long blocks = (A.cols / 4 + 63) / 64;
-  const long chunk = blockIdx.x / blocks;
-  const GatedLane L = gated_lane(A, blockIdx.x % blocks);
-  const long t0 = chunk * kGatedChunk + w * kGatedSteps;
-  Decay dec[kGatedSteps][4];
-  float s[kGatedSteps][4], u[kGatedSteps][4], raw[kGatedSteps][4];
-  float al[4], be[4], sum[4], l[4];
+  long order, block;
+  gated_place(A, J, order, block);
+  const long chunk = A.chunks - 1 - order;
+  const GatedLane L = gated_lane(A, block);
+  const int t0 = ((int)chunk * kGatedWaves + w) * NS;
+  Decay dec[NS][4];
+  float s[NS][4], sg[NS][4], u[NS][4];
+  float al[4], sum[4], l[4];
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    al[e] = A.alpha[L.d + e];
-    be[e] = A.beta[L.d + e];
-    sum[e] = l[e] = 0.0f;
-  }
+  for (int e = 0; e < 4; ++e) sum[e] = l[e] = 0.0f;
   const bool some = __builtin_amdgcn_ballot_w64(t0 < L.len) != 0;
   if (some) {
+    float be[4];
 #pragma unroll
-    for (int i = 0; i < kGatedSteps; ++i) {
+    for (int i = 0; i < NS; ++i) {
       const long t = t0 + i < A.T ? t0 + i : A.T - 1;
-      gated_load<BF16>(A.a, L.base + t * A.D, raw[i]);
+      gated_load<BF16>(A.a, L.base + t * A.D, s[i]);
       gated_load<false>(A.dy, L.base + t * A.D, u[i]);
     }
+    gated_load<false>(A.alpha, L.d, al);
+    gated_load<false>(A.beta, L.d, be);
 #pragma unroll
-    for (int i = kGatedSteps - 1; i >= 0; --i) {
+    for (int i = NS - 1; i >= 0; --i) {
       const bool live = t0 + i < L.len;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        float sg, in;
-        softplus_sigma(raw[i][e] + be[e], s[i][e], sg);
+        s[i][e] = gated_softplus<true>(s[i][e] + be[e], sg[i][e]);
         s[i][e] = live ? s[i][e] : 0.0f;
+        sg[i][e] = live ? sg[i][e] : 0.0f;
         u[i][e] = live ? u[i][e] : 0.0f;
-        const float x = s[i][e] == 0.0f ? 0.0f : al[e] * s[i][e];
-        dec[i][e] = decay_of(x, in);
+        const float x = live ? al[e] * s[i][e] : 0.0f;
+        dec[i][e] = decay_of(x);
         sum[e] += x;
         l[e] = dec[i][e](l[e] + u[i][e]);
       }
@@ -260,45 +337,21 @@ __global__ void __launch_bounds__(64 * kGatedWaves) m2rnn_gated_bwd_kernel(Gated
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     J.x[w][e][lane] = sum[e];
+    J.c[w][e][lane] = decay_of(sum[e]).c;
     J.l[w][e][lane] = l[e];
   }
   __syncthreads();
-  if constexpr (!OUT) {
-    if (w == 0 && L.on) {
-      float4 o[2];
-      float* q = (float*)o;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        float x = 0.0f, c = 0.0f, in;
-#pragma unroll
-        for (int j = kGatedWaves - 1; j >= 0; --j) {
-          c = decay_of(J.x[j][e][lane], in)(c) + J.l[j][e][lane];
-          x += J.x[j][e][lane];
-        }
-        q[2 * e] = x;
-        q[2 * e + 1] = c;
-      }
-      float4* dst = (float4*)(A.agg + chunk * A.cols + L.col);
-      dst[0] = o[0];
-      dst[1] = o[1];
-    }
-    return;
-  }
+  gated_enter<true>(A, J, order, block, lane, w, L, A.dh_T, A.dh0);
   float C[4], gal[4], gbe[4];
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
-    C[e] = A.agg[chunk * A.cols + L.col + e].x;
+    C[e] = J.l[w][e][lane];
     gal[e] = gbe[e] = 0.0f;
   }
-  for (int j = kGatedWaves - 1; j > w; --j) {
-    float in;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) C[e] = decay_of(J.x[j][e][lane], in)(C[e]) + J.l[j][e][lane];
-  }
   if (some) {
-    float v[kGatedSteps][4], hb[kGatedSteps][4];
+    float v[NS][4], hb[NS][4];
 #pragma unroll
-    for (int i = 0; i < kGatedSteps; ++i) {
+    for (int i = 0; i < NS; ++i) {
       const long t = t0 + i < A.T ? t0 + i : A.T - 1;
       gated_load<BF16>(A.v, L.base + t * A.D, v[i]);
       if (t > 0) {
@@ -311,20 +364,16 @@ __global__ void __launch_bounds__(64 * kGatedWaves) m2rnn_gated_bwd_kernel(Gated
       }
     }
 #pragma unroll
-    for (int i = kGatedSteps - 1; i >= 0; --i) {
+    for (int i = NS - 1; i >= 0; --i) {
       const long t = t0 + i;
       float dv[4], da[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        float sp, sg, in;
-        softplus_sigma(raw[i][e] + be[e], sp, sg);
-        const bool held = s[i][e] == 0.0f;
-        decay_of(held ? 0.0f : al[e] * s[i][e], in);
         const float R = C[e] + u[i][e];
         C[e] = dec[i][e](R);
-        const float G = held ? 0.0f : C[e] * (hb[i][e] - v[i][e]);
-        dv[e] = held ? 0.0f : in * R;
-        da[e] = held ? 0.0f : -al[e] * sg * G;
+        const float G = sg[i][e] == 0.0f ? 0.0f : C[e] * (hb[i][e] - v[i][e]);  // (held: whatever v is)
+        dv[e] = dec[i][e].i() * R;
+        da[e] = -al[e] * sg[i][e] * G;
         gal[e] = __builtin_fmaf(-s[i][e], G, gal[e]);
         gbe[e] += da[e];
       }
@@ -335,17 +384,16 @@ __global__ void __launch_bounds__(64 * kGatedWaves) m2rnn_gated_bwd_kernel(Gated
     }
   } else if (L.on) {
     const float none[4] = {0, 0, 0, 0};
-    for (int i = 0; i < kGatedSteps; ++i)
+    for (int i = 0; i < NS; ++i)
       if (t0 + i < A.T) {
-        store4_nt<false>(A.dv, L.base + (t0 + i) * A.D, none);
-        store4_nt<false>(A.da, L.base + (t0 + i) * A.D, none);
+        store4_nt<false>(A.dv, L.base + (long)(t0 + i) * A.D, none);
+        store4_nt<false>(A.da, L.base + (long)(t0 + i) * A.D, none);
       }
   }
-  __syncthreads();
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
+  for (int e = 0; e < 4; ++e) {  // (J.x and J.c were read before the last barrier)
     J.x[w][e][lane] = gal[e];
-    J.l[w][e][lane] = gbe[e];
+    J.c[w][e][lane] = gbe[e];
   }
   __syncthreads();
   if (w < 4 && L.on) {  // wave e adds channel e's sums
@@ -353,7 +401,7 @@ __global__ void __launch_bounds__(64 * kGatedWaves) m2rnn_gated_bwd_kernel(Gated
 #pragma unroll
     for (int j = 0; j < kGatedWaves; ++j) {
       x += J.x[j][w][lane];
-      y += J.l[j][w][lane];
+      y += J.c[j][w][lane];
     }
     A.part[chunk * A.cols + L.col + w] = make_float2(x, y);
   }
@@ -388,6 +436,12 @@ __global__ void __launch_bounds__(1024) m2rnn_gated_sums_kernel(const float2* __
   }
 }
 
+// A state (NULL: zeros) as it is.
+__global__ void __launch_bounds__(kBlkThreads) m2rnn_gated_state_kernel(const float* from, float* to, long n) {
+  const long step = (long)gridDim.x * kBlkThreads;
+  for (long i = (long)blockIdx.x * kBlkThreads + threadIdx.x; i < n; i += step) to[i] = from ? from[i] : 0.0f;
+}
+
 // One step: h_out = f h + (1 - f) v, four channels a thread.
 template <bool BF16>
 __global__ void __launch_bounds__(kBlkThreads) m2rnn_gated_step_kernel(const void* v, const void* a, const float* alpha,
@@ -406,10 +460,9 @@ __global__ void __launch_bounds__(kBlkThreads) m2rnn_gated_step_kernel(const voi
     float* q = (float*)&o;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      float s, sg, in;
-      softplus_sigma(va[e] + be[e], s, sg);
-      const Decay f = decay_of(s == 0.0f ? 0.0f : al[e] * s, in);
-      q[e] = f(hh[e]) + (s == 0.0f ? 0.0f : in * vv[e]);
+      float sg;
+      const Decay f = decay_of(al[e] * gated_softplus<false>(va[e] + be[e], sg));
+      q[e] = f(hh[e]) + mul_or_0(f.i(), vv[e]);
     }
     *(float4*)(h_out + c) = o;
   }

@@ -62,15 +62,28 @@ __device__ __forceinline__ uint32_t umax_(uint32_t a, uint32_t b) { return a > b
 
 // The largest of the magnitudes' bits over half a wave (a group of 128) or over the whole row.  As whole numbers NaN
 // is larger than every magnitude, so it is not lost.
+template <int CTRL>
+__device__ __forceinline__ uint32_t max_with(uint32_t m) {
+  return umax_(m, __float_as_uint(dpp_all<CTRL>(__uint_as_float(m))));
+}
+__device__ __forceinline__ uint32_t row16_max(uint32_t m) {
+  m = max_with<kDppQuadXor1>(m);
+  m = max_with<kDppQuadXor2>(m);
+  m = max_with<kDppRowHalfMirror>(m);
+  return max_with<kDppRowMirror>(m);
+}
 __device__ __forceinline__ uint32_t group_max(uint32_t m) {
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) m = umax_(m, (uint32_t)__shfl_xor((int)m, d));
-  return m;
+  m = row16_max(m);
+  return umax_(m, (uint32_t)__shfl_xor((int)m, 16));
 }
 template <int LPR>
 __device__ __forceinline__ uint32_t row_max(uint32_t m, uint32_t (&red)[kBlkThreads / 64]) {
-#pragma unroll
-  for (int d = 1; d < (LPR < 64 ? LPR : 64); d <<= 1) m = umax_(m, (uint32_t)__shfl_xor((int)m, d));
+  if constexpr (LPR == 4) return max_with<kDppQuadXor2>(max_with<kDppQuadXor1>(m));
+  m = row16_max(m);
+  if constexpr (LPR >= 64) {
+    m = umax_(m, (uint32_t)__shfl_xor((int)m, 16));
+    m = umax_(m, (uint32_t)__shfl_xor((int)m, 32));
+  }
   if constexpr (LPR == 256) {
     if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = m;
     __syncthreads();
@@ -83,11 +96,16 @@ __device__ __forceinline__ float e4m3_scale(uint32_t amax_bits) {
   const float s = __uint_as_float(amax_bits) / 448.0f;
   return s < 0x1p-126f ? 0x1p-126f : s;  // (NaN stays NaN)
 }
-// Four values over s as e4m3, in one word.
-__device__ __forceinline__ uint32_t pack_e4m3(const float (&y)[4], float s) {
-  int w = 0;
-  w = __builtin_amdgcn_cvt_pk_fp8_f32(y[0] / s, y[1] / s, w, false);
-  return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(y[2] / s, y[3] / s, w, true);
+// Four values over s as e4m3, in one word: times 1/s with the product's error taken out.
+__device__ __forceinline__ uint32_t pack_e4m3(const float (&y)[4], float s, float inv) {
+  float q[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float t = y[e] * inv;
+    q[e] = __builtin_fmaf(__builtin_fmaf(-t, s, y[e]), inv, t);
+  }
+  const int w = __builtin_amdgcn_cvt_pk_fp8_f32(q[0], q[1], 0, false);
+  return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(q[2], q[3], w, true);
 }
 
 template <int NG, int LPR>
@@ -170,11 +188,11 @@ __global__ void __launch_bounds__(kBlkThreads) m2rnn_add_norm_kernel(NormArgs A)
     } else {
       uint32_t* q = (uint32_t*)A.out;
       if (A.group == A.D) {
-        const float s = e4m3_scale(row_max<LPR>(most, redm));  // (the next row writes redm behind row_sum's barrier)
+        const float s = e4m3_scale(row_max<LPR>(most, redm)), si = 1.0f / s;  // (the next row writes redm behind row_sum's barrier)
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
           const int i = 4 * (g * LPR + unit);
-          if (on && i < A.D) q[(at + i) / 4] = pack_e4m3(h[g], s);
+          if (on && i < A.D) q[(at + i) / 4] = pack_e4m3(h[g], s, si);
         }
         if (on && unit == 0) A.scale[row] = s;
       } else {
@@ -184,9 +202,9 @@ __global__ void __launch_bounds__(kBlkThreads) m2rnn_add_norm_kernel(NormArgs A)
           uint32_t m = 0;
 #pragma unroll
           for (int e = 0; e < 4; ++e) m = umax_(m, __float_as_uint(h[g][e]) & 0x7FFFFFFFu);
-          const float s = e4m3_scale(group_max(m));
+          const float s = e4m3_scale(group_max(m)), si = 1.0f / s;
           if (on && i < A.D) {
-            q[(at + i) / 4] = pack_e4m3(h[g], s);
+            q[(at + i) / 4] = pack_e4m3(h[g], s, si);
             if ((unit & 31) == 0) A.scale[row * (A.D / 128) + i / 128] = s;
           }
         }
