@@ -17,12 +17,8 @@
 
 namespace m2rnn {
 
-typedef float f32x16 __attribute__((ext_vector_type(16)));
-
 constexpr float kOrthX = 4096.0f, kOrthA = 4096.0f, kOrthB = 2048.0f;
-constexpr int kOrthTile = 128;   // side of a workgroup's tile; sides are padded to it with zeros
-constexpr int kOrthK = 32;       // contraction of a stage
-constexpr int kOrthThreads = 256;
+constexpr int kOrthK = 32;  // contraction of a stage
 
 // Two fp16 planes of a matrix [rows][ld].
 struct Planes {
@@ -63,11 +59,12 @@ __global__ void __launch_bounds__(256) m2rnn_orth_squares_kernel(const void* g, 
   if (threadIdx.x == 0) part[(long)blockIdx.y * gridDim.x + blockIdx.x] = (red[0] + red[1]) + (red[2] + red[3]);
 }
 
-// X_0 times kOrthX as planes [mp][np] and their transposes [np][mp], zeros past m x n; m x n is G or, `tall`, its
-// transpose.  A workgroup takes 64 x 64.
+// X_0 times kOrthX in fp32, as planes [mp][np] and their transposes [np][mp], zeros past m x n; m x n is G or, `tall`,
+// its transpose.  A workgroup takes 64 x 64.
 template <bool BF16>
 __global__ void __launch_bounds__(256) m2rnn_orth_split_kernel(const void* g, int m, int n, int mp, int np, int tall,
-                                                               const double* part, int parts, float eps, Planes X, Planes XT) {
+                                                               const double* part, int parts, float eps, float* X32, Planes X,
+                                                               Planes XT) {
   __shared__ float tile[64][65];
   const long z = blockIdx.z;
   double ss = 0.0;
@@ -86,12 +83,14 @@ __global__ void __launch_bounds__(256) m2rnn_orth_split_kernel(const void* g, in
   const long plane = z * mp * np;
   for (int i = ty; i < 64; i += 4) {
     uint16_t hi, lo;
+    const long o = plane + (long)(r0 + i) * np + c0 + tx, ot = plane + (long)(c0 + i) * mp + r0 + tx;
+    X32[o] = tile[i][tx];
     split_f16(tile[i][tx], hi, lo);
-    X.hi[plane + (long)(r0 + i) * np + c0 + tx] = hi;
-    X.lo[plane + (long)(r0 + i) * np + c0 + tx] = lo;
+    X.hi[o] = hi;
+    X.lo[o] = lo;
     split_f16(tile[tx][i], hi, lo);
-    XT.hi[plane + (long)(c0 + i) * mp + r0 + tx] = hi;
-    XT.lo[plane + (long)(c0 + i) * mp + r0 + tx] = lo;
+    XT.hi[ot] = hi;
+    XT.lo[ot] = lo;
   }
 }
 
@@ -100,143 +99,193 @@ enum { ORTH_GRAM = 0, ORTH_POLY = 1, ORTH_NEXT = 2, ORTH_LAST = 3 };
 
 struct OrthArgs {
   Planes M, N;        // [rows][K], [cols][K]
-  Planes E;           // POLY: A, NEXT and LAST: X, [rows][cols]
+  Planes E;           // POLY: A
+  float* X32;         // NEXT and LAST: X in fp32 (NEXT: and X')
   Planes O, OT;       // outputs [rows][cols] and [cols][rows]
   void* out;          // LAST: [m][n], or [n][m] if tall
+  float* part;        // [batch][splits][tiles][waves] wave tiles of partial sums, if the contraction is split
   int rows, cols, K;  // padded
   int m, n;
   int tall, out_bf16;
+  int splits, tiles;
   float ca, cb, cc;
 };
 
-__device__ __forceinline__ f32x16 mfma32_f16(uint4 a, uint4 b, f32x16 c) {
-  return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+// Four rows of one column of a product: rows r .. r + 3, column c.  `mirror`: the transposed place is written too.
+template <int EPI>
+__device__ __forceinline__ void orth_finish(const OrthArgs& A, long z, int r, int c, const f32x4& acc, bool mirror) {
+  const long eo = z * A.rows * A.cols;
+  uint16_t hi[4], lo[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    float x = acc[e];
+    const long at = eo + (long)(r + e) * A.cols + c;
+    if constexpr (EPI == ORTH_GRAM) {
+      x *= kOrthA / (kOrthX * kOrthX);
+    } else if constexpr (EPI == ORTH_POLY) {
+      const float a = join_f16(A.E.hi[at], A.E.lo[at]);
+      x = __builtin_fmaf(A.cb * (kOrthB / kOrthA), a, A.cc * (kOrthB / (kOrthA * kOrthA)) * x);
+    } else {
+      x = __builtin_fmaf(A.ca, A.X32[at], x * (1.0f / kOrthB));
+    }
+    if constexpr (EPI == ORTH_LAST) {
+      x *= 1.0f / kOrthX;
+      if (r + e < A.m && c < A.n) {
+        const long o = z * A.m * A.n + (A.tall ? (long)c * A.m + r + e : (long)(r + e) * A.n + c);
+        if (A.out_bf16)
+          ((__bf16*)A.out)[o] = (__bf16)x;
+        else
+          ((float*)A.out)[o] = x;
+      }
+    } else {
+      if constexpr (EPI == ORTH_NEXT) A.X32[at] = x;
+      split_f16(x, hi[e], lo[e]);
+      A.O.hi[at] = hi[e];
+      A.O.lo[at] = lo[e];
+    }
+  }
+  if constexpr (EPI != ORTH_LAST) {
+    if (mirror) {
+      const long at = eo + (long)c * A.rows + r;
+      *(uint2*)(A.OT.hi + at) = make_uint2(hi[0] | (uint32_t)hi[1] << 16, hi[2] | (uint32_t)hi[3] << 16);
+      *(uint2*)(A.OT.lo + at) = make_uint2(lo[0] | (uint32_t)lo[1] << 16, lo[2] | (uint32_t)lo[3] << 16);
+    }
+  }
 }
 
-// One 128 x 128 tile of M N^T.  Four waves of 64 x 64, 32x32x16 MFMA.  A stage is 32 of the contraction: 64 bytes of
-// each row of the four planes, in 16-byte units; unit u of row r is stored at u ^ ((r >> 1) & 3), so that the eight rows
-// that a read touches at a time cover all banks.
-template <int EPI>
-__global__ void __launch_bounds__(kOrthThreads) m2rnn_orth_product_kernel(OrthArgs A) {
-  constexpr bool SYM = EPI == ORTH_GRAM || EPI == ORTH_POLY;
-  __shared__ uint4 lds[2][4][kOrthTile * 4];  // [buffer][M hi, M lo, N hi, N lo][row][unit]
-  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-  int bi = blockIdx.y, bj = blockIdx.x;
-  if constexpr (SYM) {  // tiles of the lower triangle, numbered by rows
-    const int id = blockIdx.x;
+// The place of tile number `id`: the lower triangle by rows (SYM), or bands of four rows, column by column.
+template <bool SYM>
+__device__ __forceinline__ void orth_place(int id, int gi, int gj, int& bi, int& bj) {
+  if constexpr (SYM) {
     bi = (int)((sqrtf(8.0f * (float)id + 1.0f) - 1.0f) * 0.5f);
     while ((bi + 1) * (bi + 2) / 2 <= id) ++bi;
     while (bi * (bi + 1) / 2 > id) --bi;
     bj = id - bi * (bi + 1) / 2;
+  } else {
+    const int band = id / (4 * gj), in = id % (4 * gj);
+    const int high = gi - 4 * band < 4 ? gi - 4 * band : 4;
+    bi = 4 * band + in % high;
+    bj = in / high;
   }
+}
+
+// Tiles are dealt to the 8 XCDs in turn; each XCD takes a run of neighbouring ones, so that they share rows in its L2.
+__device__ __forceinline__ int orth_turn(int id, int total) {
+  const int q = total / 8, r = total % 8, x = id % 8;
+  return x * q + (x < r ? x : r) + id / 8;
+}
+
+// One T x T tile of M N^T, or its part of a split contraction.  WR x WC waves, 16x16x32 MFMA.  A stage is 32 of the
+// contraction: 64 bytes of each row of the four planes, in 16-byte units, brought to LDS past the registers while the stage
+// before is multiplied; unit u of row r lies at u ^ ((r >> 1) & 3), so that the eight rows that a read touches at a time
+// cover all banks.  The three passes of a stage are summed by themselves, from zero, and added to the tile's sum once:
+// one rounding at the sum's size for each stage instead of three.
+template <int T, int WR, int WC, int EPI, bool SPLIT>
+__global__ void __launch_bounds__(64 * WR * WC) m2rnn_orth_product_kernel(OrthArgs A) {
+  constexpr bool SYM = EPI == ORTH_GRAM || EPI == ORTH_POLY;
+  constexpr int NI = T / WR / 16, NJ = T / WC / 16, WAVES = WR * WC;
+  constexpr int PER = 4 * (T / 16) / WAVES;  // 16-row pieces of a plane's stage that a wave brings
+  static_assert((T / 16) % PER == 0, "a wave brings pieces of one plane");
+  extern __shared__ uint4 lds[];  // [buffer][M hi, M lo, N hi, N lo][row][unit]
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int tile = orth_turn(blockIdx.x, A.tiles);
+  int bi, bj;
+  orth_place<SYM>(tile, A.rows / T, A.cols / T, bi, bj);
   const long z = blockIdx.z;
-  const int r0 = bi * kOrthTile, c0 = bj * kOrthTile;
-  const long mo = z * A.rows * A.K + (long)r0 * A.K, no = z * A.cols * A.K + (long)c0 * A.K;
-  const uint16_t* src[4] = {A.M.hi + mo, A.M.lo + mo, A.N.hi + no, A.N.lo + no};
-  // this thread's two units of each plane's stage
-  const int row = threadIdx.x >> 2, unit = threadIdx.x & 3;
-  const int slot0 = row * 4 + (unit ^ ((row >> 1) & 3)), slot1 = slot0 + 64 * 4;  // (64 rows on: the same exchange)
-  const long off0 = (long)row * A.K + unit * 8, off1 = off0 + 64L * A.K;
-  uint4 pre[8];
-  auto fetch = [&](int k) {
+  const int r0 = bi * T, c0 = bj * T;
+  const int stages = A.K / kOrthK;
+  const int first = SPLIT ? (int)((long)stages * blockIdx.y / A.splits) : 0;
+  const int last = SPLIT ? (int)((long)stages * (blockIdx.y + 1) / A.splits) : stages;
+  const int plane = w * PER / (T / 16), piece = w * PER % (T / 16);
+  const uint16_t* src = plane < 2 ? (plane == 0 ? A.M.hi : A.M.lo) + (z * A.rows + r0) * A.K
+                                  : (plane == 2 ? A.N.hi : A.N.lo) + (z * A.cols + c0) * A.K;
+  src += (long)piece * 16 * A.K + (long)(lane >> 2) * A.K + ((lane & 3) ^ ((lane >> 3) & 3)) * 8;
+  auto fetch = [&](int buf, int stage) {
 #pragma unroll
-    for (int p = 0; p < 4; ++p) {
-      pre[2 * p] = *(const uint4*)(src[p] + off0 + k);
-      pre[2 * p + 1] = *(const uint4*)(src[p] + off1 + k);
-    }
+    for (int i = 0; i < PER; ++i)
+      __builtin_amdgcn_global_load_lds(
+          (const __attribute__((address_space(1))) uint32_t*)(src + (long)i * 16 * A.K + (long)stage * kOrthK),
+          (__attribute__((address_space(3))) uint32_t*)(lds + (buf * 4 + plane) * T * 4 + (piece + i) * 64), 16, 0, 0);
   };
-  auto put = [&](int buf) {
+  f32x4 acc[NI][NJ];
 #pragma unroll
-    for (int p = 0; p < 4; ++p) {
-      lds[buf][p][slot0] = pre[2 * p];
-      lds[buf][p][slot1] = pre[2 * p + 1];
+  for (int i = 0; i < NI; ++i)
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+  const int n = lane & 15, g = lane >> 4;
+  const int wr = (w / WC) * (T / WR), wc = (w % WC) * (T / WC);
+  const int unit = n * 4 + (g ^ ((n >> 1) & 3));  // (16 rows on: the same exchange)
+  fetch(0, first);
+  for (int s = first; s < last; ++s) {
+    const int buf = (s - first) & 1;
+    __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0): this wave's pieces have arrived
+    lds_barrier();
+    if (s + 1 < last) fetch(buf ^ 1, s + 1);
+    const uint4* mhi = lds + buf * 16 * T + wr * 4 + unit;
+    const uint4* mlo = mhi + T * 4;
+    const uint4* nhi = lds + buf * 16 * T + 8 * T + wc * 4 + unit;
+    const uint4* nlo = nhi + T * 4;
+    uint4 nh[NJ], nl[NJ];
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      nh[j] = nhi[j * 64];
+      nl[j] = nlo[j * 64];
     }
-  };
-  f32x16 acc[2][2];
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < NI; ++i) {
+      const uint4 mh = mhi[i * 64], ml = mlo[i * 64];
+      f32x4 t[NJ];
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+      for (int j = 0; j < NJ; ++j) t[j] = mfma_f16(ml, nh[j], f32x4{0, 0, 0, 0});
 #pragma unroll
-      for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
-  const int wr = (w >> 1) * 64, wc = (w & 1) * 64, l32 = lane & 31, half = lane >> 5;
-  fetch(0);
-  put(0);
-  __syncthreads();
-  int buf = 0;
-  for (int k = 0; k < A.K; k += kOrthK, buf ^= 1) {
-    const bool more = k + kOrthK < A.K;
-    if (more) fetch(k + kOrthK);
+      for (int j = 0; j < NJ; ++j) t[j] = mfma_f16(mh, nl[j], t[j]);
 #pragma unroll
-    for (int kk = 0; kk < 2; ++kk) {
-      uint4 mh[2], ml[2], nh[2], nl[2];
+      for (int j = 0; j < NJ; ++j) t[j] = mfma_f16(mh, nh[j], t[j]);
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int r = wr + 32 * i + l32, c = wc + 32 * i + l32;
-        const int ur = r * 4 + ((2 * kk + half) ^ ((r >> 1) & 3)), uc = c * 4 + ((2 * kk + half) ^ ((c >> 1) & 3));
-        mh[i] = lds[buf][0][ur];
-        ml[i] = lds[buf][1][ur];
-        nh[i] = lds[buf][2][uc];
-        nl[i] = lds[buf][3][uc];
-      }
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          acc[i][j] = mfma32_f16(mh[i], nl[j], acc[i][j]);
-          acc[i][j] = mfma32_f16(ml[i], nh[j], acc[i][j]);
-          acc[i][j] = mfma32_f16(mh[i], nh[j], acc[i][j]);
-        }
+      for (int j = 0; j < NJ; ++j) acc[i][j] += t[j];
     }
-    if (more) put(buf ^ 1);
-    __syncthreads();
   }
-  // lane l, register 4q + e: row 8q + 4 (l / 32) + e, column l % 32 of a 32 x 32 tile
-  const long eo = z * A.rows * A.cols;
+  // lane (g, n), register e: row 4 g + e, column n of a 16 x 16 tile
+  if constexpr (SPLIT) {
+    float4* dst = (float4*)A.part + (((z * A.splits + blockIdx.y) * A.tiles + tile) * WAVES + w) * (NI * NJ * 64) + lane;
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < NI; ++i)
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+      for (int j = 0; j < NJ; ++j)
+        dst[(i * NJ + j) * 64] = make_float4(acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]);
+  } else {
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int r = r0 + wr + 32 * i + 8 * q + 4 * half, c = c0 + wc + 32 * j + l32;
-        uint16_t hi[4], lo[4];
+    for (int i = 0; i < NI; ++i)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float x = acc[i][j][4 * q + e];
-          const long at = eo + (long)(r + e) * A.cols + c;
-          if constexpr (EPI == ORTH_GRAM) {
-            x *= kOrthA / (kOrthX * kOrthX);
-          } else if constexpr (EPI == ORTH_POLY) {
-            const float a = join_f16(A.E.hi[at], A.E.lo[at]);
-            x = __builtin_fmaf(A.cb * (kOrthB / kOrthA), a, A.cc * (kOrthB / (kOrthA * kOrthA)) * x);
-          } else {
-            const float x0 = join_f16(A.E.hi[at], A.E.lo[at]);
-            x = __builtin_fmaf(A.ca, x0, x * (1.0f / kOrthB));
-          }
-          if constexpr (EPI == ORTH_LAST) {
-            x *= 1.0f / kOrthX;
-            if (r + e < A.m && c < A.n) {
-              const long o = z * A.m * A.n + (A.tall ? (long)c * A.m + r + e : (long)(r + e) * A.n + c);
-              if (A.out_bf16)
-                ((__bf16*)A.out)[o] = (__bf16)x;
-              else
-                ((float*)A.out)[o] = x;
-            }
-          } else {
-            split_f16(x, hi[e], lo[e]);
-            A.O.hi[at] = hi[e];
-            A.O.lo[at] = lo[e];
-          }
-        }
-        if constexpr (EPI != ORTH_LAST) {
-          if (!SYM || bi != bj) {
-            const long at = eo + (long)c * A.rows + r;
-            *(uint2*)(A.OT.hi + at) = make_uint2(hi[0] | (uint32_t)hi[1] << 16, hi[2] | (uint32_t)hi[3] << 16);
-            *(uint2*)(A.OT.lo + at) = make_uint2(lo[0] | (uint32_t)lo[1] << 16, lo[2] | (uint32_t)lo[3] << 16);
-          }
-        }
-      }
+      for (int j = 0; j < NJ; ++j)
+        orth_finish<EPI>(A, z, r0 + wr + 16 * i + 4 * g, c0 + wc + 16 * j + n, acc[i][j], !SYM || bi != bj);
+  }
+}
+
+// The parts of a split contraction added in order, and the epilogue.  A wave takes one row of a wave tile's 16 x 16 tiles.
+template <int T, int WR, int WC, int EPI>
+__global__ void __launch_bounds__(256) m2rnn_orth_join_kernel(OrthArgs A) {
+  constexpr bool SYM = EPI == ORTH_GRAM || EPI == ORTH_POLY;
+  constexpr int NI = T / WR / 16, NJ = T / WC / 16, WAVES = WR * WC;
+  const int lane = threadIdx.x & 63;
+  const long z = blockIdx.z;
+  const int item = __builtin_amdgcn_readfirstlane((int)(blockIdx.x * 4 + (threadIdx.x >> 6)));
+  if (item >= A.tiles * WAVES * NI) return;
+  const int i = item % NI, w = item / NI % WAVES, tile = item / (NI * WAVES);
+  int bi, bj;
+  orth_place<SYM>(tile, A.rows / T, A.cols / T, bi, bj);
+  const int n = lane & 15, g = lane >> 4;
+  const int r = bi * T + (w / WC) * (T / WR) + 16 * i + 4 * g, c = bj * T + (w % WC) * (T / WC) + n;
+  f32x4 acc[NJ];
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) acc[j] = f32x4{0, 0, 0, 0};
+  for (int s = 0; s < A.splits; ++s) {
+    const f32x4* src = (const f32x4*)A.part + (((z * A.splits + s) * A.tiles + tile) * WAVES + w) * (NI * NJ * 64) + i * NJ * 64 + lane;
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) acc[j] += src[j * 64];
+  }
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) orth_finish<EPI>(A, z, r, c + 16 * j, acc[j], !SYM || bi != bj);
 }
 
 }  // namespace m2rnn
