@@ -105,11 +105,10 @@ template <int T, int WR, int WC, int EPI>
 int product_of(OrthArgs& A, long batch, hipStream_t s) {
   void* args[] = {&A};
   const dim3 grid((unsigned)A.tiles, (unsigned)A.splits, (unsigned)batch), block(64 * WR * WC);
-  const size_t lds = 2 * 4 * T * 4 * sizeof(uint4);
   const void* one = (const void*)&m2rnn_orth_product_kernel<T, WR, WC, EPI, false>;
-  if (A.splits == 1) return record_hip_status(hipLaunchKernel(one, grid, block, args, lds, s));
+  if (A.splits == 1) return record_hip_status(hipLaunchKernel(one, grid, block, args, 0, s));
   const void* some = (const void*)&m2rnn_orth_product_kernel<T, WR, WC, EPI, true>;
-  const int st = record_hip_status(hipLaunchKernel(some, grid, block, args, lds, s));
+  const int st = record_hip_status(hipLaunchKernel(some, grid, block, args, 0, s));
   if (st) return st;
   const long items = (long)A.tiles * (T / 16) * WC;
   return record_hip_status(hipLaunchKernel((const void*)&m2rnn_orth_join_kernel<T, WR, WC, EPI>,

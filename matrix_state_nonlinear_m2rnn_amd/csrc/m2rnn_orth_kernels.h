@@ -111,44 +111,56 @@ struct OrthArgs {
   float ca, cb, cc;
 };
 
-// Four rows of one column of a product: rows r .. r + 3, column c.  `mirror`: the transposed place is written too.
-template <int EPI>
-__device__ __forceinline__ void orth_finish(const OrthArgs& A, long z, int r, int c, const f32x4& acc, bool mirror) {
-  const long eo = z * A.rows * A.cols;
-  uint16_t hi[4], lo[4];
+// A lane's part of NJ 16 x 16 tiles side by side: rows r .. r + 3 of the columns c + 16 j.  `mirror`: the transposed place
+// is written too.  What the epilogue reads is loaded before anything is stored.
+template <int EPI, int NJ>
+__device__ __forceinline__ void orth_finish(const OrthArgs& A, long z, int r, int c, const f32x4 (&acc)[NJ], bool mirror) {
+  const long eo = z * A.rows * A.cols + (long)r * A.cols + c;
+  float x[NJ][4];
+  if constexpr (EPI != ORTH_GRAM) {
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    float x = acc[e];
-    const long at = eo + (long)(r + e) * A.cols + c;
-    if constexpr (EPI == ORTH_GRAM) {
-      x *= kOrthA / (kOrthX * kOrthX);
-    } else if constexpr (EPI == ORTH_POLY) {
-      const float a = join_f16(A.E.hi[at], A.E.lo[at]);
-      x = __builtin_fmaf(A.cb * (kOrthB / kOrthA), a, A.cc * (kOrthB / (kOrthA * kOrthA)) * x);
-    } else {
-      x = __builtin_fmaf(A.ca, A.X32[at], x * (1.0f / kOrthB));
-    }
-    if constexpr (EPI == ORTH_LAST) {
-      x *= 1.0f / kOrthX;
-      if (r + e < A.m && c < A.n) {
-        const long o = z * A.m * A.n + (A.tall ? (long)c * A.m + r + e : (long)(r + e) * A.n + c);
-        if (A.out_bf16)
-          ((__bf16*)A.out)[o] = (__bf16)x;
-        else
-          ((float*)A.out)[o] = x;
+    for (int j = 0; j < NJ; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const long at = eo + (long)e * A.cols + 16 * j;
+        x[j][e] = EPI == ORTH_POLY ? join_f16(A.E.hi[at], A.E.lo[at]) : A.X32[at];
       }
-    } else {
-      if constexpr (EPI == ORTH_NEXT) A.X32[at] = x;
-      split_f16(x, hi[e], lo[e]);
-      A.O.hi[at] = hi[e];
-      A.O.lo[at] = lo[e];
-    }
   }
-  if constexpr (EPI != ORTH_LAST) {
-    if (mirror) {
-      const long at = eo + (long)c * A.rows + r;
-      *(uint2*)(A.OT.hi + at) = make_uint2(hi[0] | (uint32_t)hi[1] << 16, hi[2] | (uint32_t)hi[3] << 16);
-      *(uint2*)(A.OT.lo + at) = make_uint2(lo[0] | (uint32_t)lo[1] << 16, lo[2] | (uint32_t)lo[3] << 16);
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) {
+    uint16_t hi[4], lo[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      float y = acc[j][e];
+      const long at = eo + (long)e * A.cols + 16 * j;
+      if constexpr (EPI == ORTH_GRAM)
+        y *= kOrthA / (kOrthX * kOrthX);
+      else if constexpr (EPI == ORTH_POLY)
+        y = __builtin_fmaf(A.cb * (kOrthB / kOrthA), x[j][e], A.cc * (kOrthB / (kOrthA * kOrthA)) * y);
+      else
+        y = __builtin_fmaf(A.ca, x[j][e], y * (1.0f / kOrthB));
+      if constexpr (EPI == ORTH_LAST) {
+        y *= 1.0f / kOrthX;
+        if (r + e < A.m && c + 16 * j < A.n) {
+          const long o = z * A.m * A.n + (A.tall ? (long)(c + 16 * j) * A.m + r + e : (long)(r + e) * A.n + c + 16 * j);
+          if (A.out_bf16)
+            ((__bf16*)A.out)[o] = (__bf16)y;
+          else
+            ((float*)A.out)[o] = y;
+        }
+      } else {
+        if constexpr (EPI == ORTH_NEXT) A.X32[at] = y;
+        split_f16(y, hi[e], lo[e]);
+        A.O.hi[at] = hi[e];
+        A.O.lo[at] = lo[e];
+      }
+    }
+    if constexpr (EPI != ORTH_LAST) {
+      if (mirror) {
+        const long at = z * A.rows * A.cols + (long)(c + 16 * j) * A.rows + r;
+        *(uint2*)(A.OT.hi + at) = make_uint2(hi[0] | (uint32_t)hi[1] << 16, hi[2] | (uint32_t)hi[3] << 16);
+        *(uint2*)(A.OT.lo + at) = make_uint2(lo[0] | (uint32_t)lo[1] << 16, lo[2] | (uint32_t)lo[3] << 16);
+      }
     }
   }
 }
@@ -175,6 +187,14 @@ __device__ __forceinline__ int orth_turn(int id, int total) {
   return x * q + (x < r ? x : r) + id / 8;
 }
 
+// 16 bytes of each lane to LDS, lane after lane from `to` (the same in all lanes) on, past the registers.  The builtin for this
+// makes the compiler wait for it before any read of LDS, also of the other buffer; here the caller waits (vmcnt).  Nothing else in
+// the kernels that call it uses m0.
+__device__ __forceinline__ void load_to_lds(const void* from, const void* to) {
+  const uint32_t at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)to;
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(at), "v"(from) : "memory");
+}
+
 // One T x T tile of M N^T, or its part of a split contraction.  WR x WC waves, 16x16x32 MFMA.  A stage is 32 of the
 // contraction: 64 bytes of each row of the four planes, in 16-byte units, brought to LDS past the registers while the stage
 // before is multiplied; unit u of row r lies at u ^ ((r >> 1) & 3), so that the eight rows that a read touches at a time
@@ -186,7 +206,7 @@ __global__ void __launch_bounds__(64 * WR * WC) m2rnn_orth_product_kernel(OrthAr
   constexpr int NI = T / WR / 16, NJ = T / WC / 16, WAVES = WR * WC;
   constexpr int PER = 4 * (T / 16) / WAVES;  // 16-row pieces of a plane's stage that a wave brings
   static_assert((T / 16) % PER == 0, "a wave brings pieces of one plane");
-  extern __shared__ uint4 lds[];  // [buffer][M hi, M lo, N hi, N lo][row][unit]
+  __shared__ uint4 lds[2 * 4 * T * 4];  // [buffer][M hi, M lo, N hi, N lo][row][unit]
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int tile = orth_turn(blockIdx.x, A.tiles);
   int bi, bj;
@@ -203,9 +223,7 @@ __global__ void __launch_bounds__(64 * WR * WC) m2rnn_orth_product_kernel(OrthAr
   auto fetch = [&](int buf, int stage) {
 #pragma unroll
     for (int i = 0; i < PER; ++i)
-      __builtin_amdgcn_global_load_lds(
-          (const __attribute__((address_space(1))) uint32_t*)(src + (long)i * 16 * A.K + (long)stage * kOrthK),
-          (__attribute__((address_space(3))) uint32_t*)(lds + (buf * 4 + plane) * T * 4 + (piece + i) * 64), 16, 0, 0);
+      load_to_lds(src + (long)i * 16 * A.K + (long)stage * kOrthK, lds + (buf * 4 + plane) * T * 4 + (piece + i) * 64);
   };
   f32x4 acc[NI][NJ];
 #pragma unroll
@@ -225,24 +243,35 @@ __global__ void __launch_bounds__(64 * WR * WC) m2rnn_orth_product_kernel(OrthAr
     const uint4* mlo = mhi + T * 4;
     const uint4* nhi = lds + buf * 16 * T + 8 * T + wc * 4 + unit;
     const uint4* nlo = nhi + T * 4;
-    uint4 nh[NJ], nl[NJ];
+    uint4 nh[NJ], nl[NJ], mh[2], ml[2];
+    f32x4 t[2][NJ];
+    mh[0] = mhi[0];
+    ml[0] = mlo[0];
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
       nh[j] = nhi[j * 64];
       nl[j] = nlo[j * 64];
     }
+    // a row of tiles at a time: the next row's operands are read, and the last row's sums added, beside its products
 #pragma unroll
-    for (int i = 0; i < NI; ++i) {
-      const uint4 mh = mhi[i * 64], ml = mlo[i * 64];
-      f32x4 t[NJ];
+    for (int i = 0; i <= NI; ++i) {
+      if (i + 1 < NI) {
+        mh[(i + 1) & 1] = mhi[(i + 1) * 64];
+        ml[(i + 1) & 1] = mlo[(i + 1) * 64];
+      }
+      if (i < NI) {
 #pragma unroll
-      for (int j = 0; j < NJ; ++j) t[j] = mfma_f16(ml, nh[j], f32x4{0, 0, 0, 0});
+        for (int j = 0; j < NJ; ++j) t[i & 1][j] = mfma_f16(ml[i & 1], nh[j], f32x4{0, 0, 0, 0});
 #pragma unroll
-      for (int j = 0; j < NJ; ++j) t[j] = mfma_f16(mh, nl[j], t[j]);
+        for (int j = 0; j < NJ; ++j) t[i & 1][j] = mfma_f16(mh[i & 1], nl[j], t[i & 1][j]);
 #pragma unroll
-      for (int j = 0; j < NJ; ++j) t[j] = mfma_f16(mh, nh[j], t[j]);
+        for (int j = 0; j < NJ; ++j) t[i & 1][j] = mfma_f16(mh[i & 1], nh[j], t[i & 1][j]);
+      }
+      if (i > 0) {
 #pragma unroll
-      for (int j = 0; j < NJ; ++j) acc[i][j] += t[j];
+        for (int j = 0; j < NJ; ++j) acc[i - 1][j] += t[(i - 1) & 1][j];
+      }
+      __builtin_amdgcn_sched_barrier(0);
     }
   }
   // lane (g, n), register e: row 4 g + e, column n of a 16 x 16 tile
@@ -256,9 +285,7 @@ __global__ void __launch_bounds__(64 * WR * WC) m2rnn_orth_product_kernel(OrthAr
   } else {
 #pragma unroll
     for (int i = 0; i < NI; ++i)
-#pragma unroll
-      for (int j = 0; j < NJ; ++j)
-        orth_finish<EPI>(A, z, r0 + wr + 16 * i + 4 * g, c0 + wc + 16 * j + n, acc[i][j], !SYM || bi != bj);
+      orth_finish<EPI, NJ>(A, z, r0 + wr + 16 * i + 4 * g, c0 + wc + n, acc[i], !SYM || bi != bj);
   }
 }
 
@@ -284,8 +311,7 @@ __global__ void __launch_bounds__(256) m2rnn_orth_join_kernel(OrthArgs A) {
 #pragma unroll
     for (int j = 0; j < NJ; ++j) acc[j] += src[j * 64];
   }
-#pragma unroll
-  for (int j = 0; j < NJ; ++j) orth_finish<EPI>(A, z, r, c + 16 * j, acc[j], !SYM || bi != bj);
+  orth_finish<EPI, NJ>(A, z, r, c, acc, !SYM || bi != bj);
 }
 
 }  // namespace m2rnn
