@@ -20,10 +20,16 @@ namespace m2rnn {
 constexpr float kOrthX = 4096.0f, kOrthA = 4096.0f, kOrthB = 2048.0f;
 constexpr int kOrthK = 32;  // contraction of a stage
 
-// Two fp16 planes of a matrix [rows][ld].
+// Two fp16 planes of a matrix [rows][ld], in blocks of 16 rows by 32 columns (1 KB, in the order that a product's stage has
+// in LDS), so that a wave brings a block as whole lines.
 struct Planes {
   uint16_t *hi, *lo;
 };
+// Where element (r, c) lies.  Within a block, 16-byte unit u of row r is at u ^ ((r >> 1) & 3): the eight rows that a
+// read of an operand touches at a time cover all banks.
+__device__ __forceinline__ long plane_at(int r, int c, int ld) {
+  return ((long)(r >> 4) * (ld >> 5) + (c >> 5)) * 512 + ((r & 15) * 4 + (((c >> 3) & 3) ^ ((r >> 1) & 3))) * 8 + (c & 7);
+}
 
 __device__ __forceinline__ void split_f16(float x, uint16_t& hi, uint16_t& lo) {
   const _Float16 h = (_Float16)x;
@@ -59,7 +65,7 @@ __global__ void __launch_bounds__(256) m2rnn_orth_squares_kernel(const void* g, 
   if (threadIdx.x == 0) part[(long)blockIdx.y * gridDim.x + blockIdx.x] = (red[0] + red[1]) + (red[2] + red[3]);
 }
 
-// X_0 times kOrthX in fp32, as planes [mp][np] and their transposes [np][mp], zeros past m x n; m x n is G or, `tall`,
+// X_0 times kOrthX in fp32 [mp][np], as planes and the transpose's planes, zeros past m x n; m x n is G or, `tall`,
 // its transpose.  A workgroup takes 64 x 64.
 template <bool BF16>
 __global__ void __launch_bounds__(256) m2rnn_orth_split_kernel(const void* g, int m, int n, int mp, int np, int tall,
@@ -83,8 +89,8 @@ __global__ void __launch_bounds__(256) m2rnn_orth_split_kernel(const void* g, in
   const long plane = z * mp * np;
   for (int i = ty; i < 64; i += 4) {
     uint16_t hi, lo;
-    const long o = plane + (long)(r0 + i) * np + c0 + tx, ot = plane + (long)(c0 + i) * mp + r0 + tx;
-    X32[o] = tile[i][tx];
+    const long o = plane + plane_at(r0 + i, c0 + tx, np), ot = plane + plane_at(c0 + i, r0 + tx, mp);
+    X32[plane + (long)(r0 + i) * np + c0 + tx] = tile[i][tx];
     split_f16(tile[i][tx], hi, lo);
     X.hi[o] = hi;
     X.lo[o] = lo;
@@ -98,10 +104,10 @@ __global__ void __launch_bounds__(256) m2rnn_orth_split_kernel(const void* g, in
 enum { ORTH_GRAM = 0, ORTH_POLY = 1, ORTH_NEXT = 2, ORTH_LAST = 3 };
 
 struct OrthArgs {
-  Planes M, N;        // [rows][K], [cols][K]
+  Planes M, N;        // rows x K, cols x K
   Planes E;           // POLY: A
-  float* X32;         // NEXT and LAST: X in fp32 (NEXT: and X')
-  Planes O, OT;       // outputs [rows][cols] and [cols][rows]
+  float* X32;         // NEXT and LAST: X in fp32 (NEXT: and X'), [rows][cols]
+  Planes O, OT;       // outputs rows x cols and cols x rows
   void* out;          // LAST: [m][n], or [n][m] if tall
   float* part;        // [batch][splits][tiles][waves] wave tiles of partial sums, if the contraction is split
   int rows, cols, K;  // padded
@@ -115,15 +121,19 @@ struct OrthArgs {
 // is written too.  What the epilogue reads is loaded before anything is stored.
 template <int EPI, int NJ>
 __device__ __forceinline__ void orth_finish(const OrthArgs& A, long z, int r, int c, const f32x4 (&acc)[NJ], bool mirror) {
-  const long eo = z * A.rows * A.cols + (long)r * A.cols + c;
+  const long zo = z * A.rows * A.cols, eo = zo + (long)r * A.cols + c;
   float x[NJ][4];
   if constexpr (EPI != ORTH_GRAM) {
 #pragma unroll
     for (int j = 0; j < NJ; ++j)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const long at = eo + (long)e * A.cols + 16 * j;
-        x[j][e] = EPI == ORTH_POLY ? join_f16(A.E.hi[at], A.E.lo[at]) : A.X32[at];
+        if constexpr (EPI == ORTH_POLY) {
+          const long at = zo + plane_at(r + e, c + 16 * j, A.cols);
+          x[j][e] = join_f16(A.E.hi[at], A.E.lo[at]);
+        } else {
+          x[j][e] = A.X32[eo + (long)e * A.cols + 16 * j];
+        }
       }
   }
 #pragma unroll
@@ -132,7 +142,6 @@ __device__ __forceinline__ void orth_finish(const OrthArgs& A, long z, int r, in
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       float y = acc[j][e];
-      const long at = eo + (long)e * A.cols + 16 * j;
       if constexpr (EPI == ORTH_GRAM)
         y *= kOrthA / (kOrthX * kOrthX);
       else if constexpr (EPI == ORTH_POLY)
@@ -149,15 +158,16 @@ __device__ __forceinline__ void orth_finish(const OrthArgs& A, long z, int r, in
             ((float*)A.out)[o] = y;
         }
       } else {
-        if constexpr (EPI == ORTH_NEXT) A.X32[at] = y;
+        if constexpr (EPI == ORTH_NEXT) A.X32[eo + (long)e * A.cols + 16 * j] = y;
         split_f16(y, hi[e], lo[e]);
+        const long at = zo + plane_at(r + e, c + 16 * j, A.cols);
         A.O.hi[at] = hi[e];
         A.O.lo[at] = lo[e];
       }
     }
     if constexpr (EPI != ORTH_LAST) {
       if (mirror) {
-        const long at = z * A.rows * A.cols + (long)(c + 16 * j) * A.rows + r;
+        const long at = zo + plane_at(c + 16 * j, r, A.rows);  // (four neighbours: r is a multiple of 4)
         *(uint2*)(A.OT.hi + at) = make_uint2(hi[0] | (uint32_t)hi[1] << 16, hi[2] | (uint32_t)hi[3] << 16);
         *(uint2*)(A.OT.lo + at) = make_uint2(lo[0] | (uint32_t)lo[1] << 16, lo[2] | (uint32_t)lo[3] << 16);
       }
@@ -196,9 +206,8 @@ __device__ __forceinline__ void load_to_lds(const void* from, const void* to) {
 }
 
 // One T x T tile of M N^T, or its part of a split contraction.  WR x WC waves, 16x16x32 MFMA.  A stage is 32 of the
-// contraction: 64 bytes of each row of the four planes, in 16-byte units, brought to LDS past the registers while the stage
-// before is multiplied; unit u of row r lies at u ^ ((r >> 1) & 3), so that the eight rows that a read touches at a time
-// cover all banks.  The three passes of a stage are summed by themselves, from zero, and added to the tile's sum once:
+// contraction: a column of blocks of the four planes, brought to LDS past the registers while the stage before is
+// multiplied.  The three passes of a stage are summed by themselves, from zero, and added to the tile's sum once:
 // one rounding at the sum's size for each stage instead of three.
 template <int T, int WR, int WC, int EPI, bool SPLIT>
 __global__ void __launch_bounds__(64 * WR * WC) m2rnn_orth_product_kernel(OrthArgs A) {
@@ -219,11 +228,11 @@ __global__ void __launch_bounds__(64 * WR * WC) m2rnn_orth_product_kernel(OrthAr
   const int plane = w * PER / (T / 16), piece = w * PER % (T / 16);
   const uint16_t* src = plane < 2 ? (plane == 0 ? A.M.hi : A.M.lo) + (z * A.rows + r0) * A.K
                                   : (plane == 2 ? A.N.hi : A.N.lo) + (z * A.cols + c0) * A.K;
-  src += (long)piece * 16 * A.K + (long)(lane >> 2) * A.K + ((lane & 3) ^ ((lane >> 3) & 3)) * 8;
+  src += (long)piece * 16 * A.K + lane * 8;
   auto fetch = [&](int buf, int stage) {
 #pragma unroll
     for (int i = 0; i < PER; ++i)
-      load_to_lds(src + (long)i * 16 * A.K + (long)stage * kOrthK, lds + (buf * 4 + plane) * T * 4 + (piece + i) * 64);
+      load_to_lds(src + (long)i * 16 * A.K + (long)stage * 512, lds + (buf * 4 + plane) * T * 4 + (piece + i) * 64);
   };
   f32x4 acc[NI][NJ];
 #pragma unroll
