@@ -15,8 +15,7 @@ int record_hip_status(hipError_t e);
 namespace {
 
 constexpr long kOrthMaxSide = 65536;
-constexpr long kOrthMaxSteps = 64;
-constexpr long kOrthParts = 256;  // partial sums of squares of a matrix at most
+constexpr long kOrthParts = 1024;  // partial sums of squares of a matrix at most
 constexpr int kOrthPad = 128;     // what the refusals round sides up to
 constexpr int kOrthSplits = 16;   // parts of a contraction at most
 
@@ -88,7 +87,7 @@ struct Plan {
         next = w;
       }
     }
-    each = std::max(ceil_div(ceil_div(m * n, kOrthParts), 256), 16L) * 256;
+    each = std::max(ceil_div(ceil_div(m * n, kOrthParts), 1024), 4L) * 1024;
     parts = ceil_div(m * n, each);
     part_bytes = round_up256((size_t)batch * parts * sizeof(double));
     x_bytes = round_up256((size_t)batch * mp * np * 2);
@@ -126,6 +125,18 @@ int product(int shape, const Cut& cut, OrthArgs& A, long batch, hipStream_t s) {
   }
 }
 
+// The kernel that takes a matrix of m x n (m <= n) through all steps in one workgroup; NULL: none does.
+const void* small_kernel(long m, long n, unsigned& threads) {
+  threads = 256;
+  if (n <= 32) return (const void*)&m2rnn_orth_small_kernel<32, 32, 2, 2>;
+  if (n <= 64) return (const void*)&m2rnn_orth_small_kernel<64, 64, 2, 2>;
+  if (m <= 64 && n <= 128) return (const void*)&m2rnn_orth_small_kernel<64, 128, 2, 2>;
+  threads = 512;
+  if (n <= 128) return (const void*)&m2rnn_orth_small_kernel<128, 128, 2, 4>;
+  if (m <= 64 && n <= 256) return (const void*)&m2rnn_orth_small_kernel<64, 256, 2, 4>;
+  return nullptr;
+}
+
 }  // namespace
 
 extern "C" {
@@ -134,7 +145,9 @@ int m2rnn_orthogonalize_workspace_size(int64_t batch, int64_t m, int64_t n, int 
   if (!bytes) return M2RNN_EINVAL;
   const int st = check_orth(batch, m, n, dtype);
   if (st) return st;
-  *bytes = batch > 0 && m > 0 && n > 0 ? Plan(batch, m, n).bytes() : 0;
+  unsigned threads;
+  const bool small = small_kernel(std::min(m, n), std::max(m, n), threads) != nullptr;
+  *bytes = batch > 0 && m > 0 && n > 0 && !small ? Plan(batch, m, n).bytes() : 0;
   return M2RNN_OK;
 }
 
@@ -148,6 +161,14 @@ int m2rnn_orthogonalize(int64_t batch, int64_t m, int64_t n, int dtype, const vo
   const bool bf16 = dtype == M2RNN_DTYPE_BF16;
   const uintptr_t size = (uintptr_t)(batch * m * n * (bf16 ? 2 : 4)), x = (uintptr_t)g, y = (uintptr_t)out;
   if (x != y && x < y + size && y < x + size) return M2RNN_EINVAL;
+  unsigned threads;
+  if (const void* small = small_kernel(std::min(m, n), std::max(m, n), threads)) {
+    OrthCoefs c{};
+    std::copy(coefs, coefs + 3 * steps, c.c);
+    int lo = (int)std::min(m, n), hi = (int)std::max(m, n), turned = m > n, half = bf16, count = (int)steps;
+    void* args[] = {&g, &out, &lo, &hi, &turned, &half, &count, &c, &eps};
+    return record_hip_status(hipLaunchKernel(small, dim3((unsigned)batch), dim3(threads), args, 0, (hipStream_t)stream));
+  }
   const Plan p(batch, m, n);
   if (!workspace || workspace_bytes < p.bytes() || !al16(workspace)) return M2RNN_EWORKSPACE;
   hipStream_t s = (hipStream_t)stream;

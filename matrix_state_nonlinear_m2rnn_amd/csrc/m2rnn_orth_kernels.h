@@ -13,7 +13,8 @@
 // and A stay below 6.4e3 and those of B below 2.7e4 (fp16 ends at 6.5e4), and entries down to 2^-15 keep both planes whole.
 #pragma once
 
-#include "m2rnn_device.h"
+#include "m2rnn_ssm_device.h"
+#include "m2rnn_stream.h"
 
 namespace m2rnn {
 
@@ -47,19 +48,34 @@ __device__ __forceinline__ float load1(const void* p, long i) {
   return ((const float*)p)[i];
 }
 
-// Partial sums of squares of a matrix in fp64: workgroup (p, matrix) of `parts`.
+__device__ __forceinline__ double wave_sum(double x) {
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) x += __shfl_xor(x, d);
+  return x;
+}
+
+// Partial sums of squares of a matrix in fp64: workgroup (p, matrix) of `parts`.  Four elements a load where a matrix's
+// size keeps them aligned, four loads in flight.
 template <bool BF16>
 __global__ void __launch_bounds__(256) m2rnn_orth_squares_kernel(const void* g, long mn, long each, double* part) {
   __shared__ double red[4];
   const long first = (long)blockIdx.x * each, last = first + each < mn ? first + each : mn;
   const long at = (long)blockIdx.y * mn;
   double acc = 0.0;
-  for (long i = first + threadIdx.x; i < last; i += 256) {
-    const double x = (double)load1<BF16>(g, at + i);
-    acc += x * x;
+  if (mn % 4 == 0) {
+#pragma unroll 4
+    for (long i = first + 4 * threadIdx.x; i < last; i += 1024) {
+      const float4 x = load4<BF16>(g, at + i);
+      acc += ((double)x.x * x.x + (double)x.y * x.y) + ((double)x.z * x.z + (double)x.w * x.w);
+    }
+  } else {
+#pragma unroll 8
+    for (long i = first + threadIdx.x; i < last; i += 256) {
+      const double x = (double)load1<BF16>(g, at + i);
+      acc += x * x;
+    }
   }
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) acc += __shfl_xor(acc, d);
+  acc = wave_sum(acc);
   if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = acc;
   __syncthreads();
   if (threadIdx.x == 0) part[(long)blockIdx.y * gridDim.x + blockIdx.x] = (red[0] + red[1]) + (red[2] + red[3]);
@@ -72,13 +88,18 @@ __global__ void __launch_bounds__(256) m2rnn_orth_split_kernel(const void* g, in
                                                                const double* part, int parts, float eps, float* X32, Planes X,
                                                                Planes XT) {
   __shared__ float tile[64][65];
+  __shared__ double red[4];
   const long z = blockIdx.z;
   double ss = 0.0;
-  for (int i = 0; i < parts; ++i) ss += part[z * parts + i];
-  const double scale = (double)kOrthX / (sqrt(ss) + (double)eps);
+  for (int i = threadIdx.x; i < parts; i += 256) ss += part[z * parts + i];
+  ss = wave_sum(ss);
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = ss;
+  __syncthreads();
+  const double scale = (double)kOrthX / (sqrt((red[0] + red[1]) + (red[2] + red[3])) + (double)eps);
   const int r0 = blockIdx.y * 64, c0 = blockIdx.x * 64;
   const int tx = threadIdx.x & 63, ty = threadIdx.x >> 6;
   const long at = z * m * n;
+#pragma unroll 8
   for (int i = ty; i < 64; i += 4) {  // (i, tx) along G's own rows
     const int r = tall ? r0 + tx : r0 + i, c = tall ? c0 + i : c0 + tx;
     float x = 0.0f;
@@ -87,18 +108,30 @@ __global__ void __launch_bounds__(256) m2rnn_orth_split_kernel(const void* g, in
   }
   __syncthreads();
   const long plane = z * mp * np;
-  for (int i = ty; i < 64; i += 4) {
-    uint16_t hi, lo;
-    const long o = plane + plane_at(r0 + i, c0 + tx, np), ot = plane + plane_at(c0 + i, r0 + tx, mp);
-    X32[plane + (long)(r0 + i) * np + c0 + tx] = tile[i][tx];
-    split_f16(tile[i][tx], hi, lo);
-    X.hi[o] = hi;
-    X.lo[o] = lo;
-    split_f16(tile[tx][i], hi, lo);
-    XT.hi[ot] = hi;
-    XT.lo[ot] = lo;
+#pragma unroll 4
+  for (int i = ty; i < 64; i += 4) X32[plane + (long)(r0 + i) * np + c0 + tx] = tile[i][tx];
+  // 8 blocks of the planes and 8 of the transpose's, two of each a wave, a lane the unit that lies at its place
+  const int row = tx >> 2, unit = (tx & 3) ^ ((tx >> 3) & 3);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const bool turned = k >= 2;
+    const int id = 2 * ty + (k & 1), br = 16 * (id >> 1), bc = 32 * (id & 1);
+    alignas(16) uint16_t hi[8], lo[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int r = br + row, c = bc + 8 * unit + e;
+      split_f16(turned ? tile[c][r] : tile[r][c], hi[e], lo[e]);
+    }
+    const long o = plane + (turned ? plane_at(c0 + br, r0 + bc, mp) : plane_at(r0 + br, c0 + bc, np)) + tx * 8;
+    *(uint4*)((turned ? XT.hi : X.hi) + o) = *(const uint4*)hi;
+    *(uint4*)((turned ? XT.lo : X.lo) + o) = *(const uint4*)lo;
   }
 }
+
+constexpr int kOrthMaxSteps = 64;
+struct OrthCoefs {
+  float c[3 * kOrthMaxSteps];
+};
 
 // What a product's epilogue does with its tile.
 enum { ORTH_GRAM = 0, ORTH_POLY = 1, ORTH_NEXT = 2, ORTH_LAST = 3 };
@@ -321,6 +354,176 @@ __global__ void __launch_bounds__(256) m2rnn_orth_join_kernel(OrthArgs A) {
     for (int j = 0; j < NJ; ++j) acc[j] += src[j * 64];
   }
   orth_finish<EPI, NJ>(A, z, r, c, acc, !SYM || bi != bj);
+}
+
+// Small matrices: one workgroup takes a matrix through all its steps, X in registers (fp32) and as planes in LDS, A and
+// then B as planes in LDS.  MP x NP the padded size; WR x WC waves over the 16 x 16 tiles of A and of X.  X's columns are
+// read transposed.
+template <int MP, int NP, int WR, int WC>
+__global__ void __launch_bounds__(64 * WR * WC) m2rnn_orth_small_kernel(const void* gin, void* out, int m, int n, int tall,
+                                                                        int bf16, int steps, OrthCoefs coefs, float eps) {
+  constexpr int SX = ssm_stride(NP), SA = ssm_stride(MP);
+  constexpr int AI = MP / 16 / WR, AJ = MP / 16 / WC, XJ = NP / 16 / WC;
+  __shared__ uint16_t xp[2][MP * SX], ap[2][MP * SA];
+  __shared__ double red[WR * WC];
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int g = lane >> 4, l = lane & 15;
+  const int r0 = (w / WC) * (MP / WR), ca = (w % WC) * (MP / WC), cx = (w % WC) * (NP / WC);
+  const long at = (long)blockIdx.x * m * n;
+  float x[AI][XJ][4];
+  double ss = 0.0;
+#pragma unroll
+  for (int i = 0; i < AI; ++i)
+#pragma unroll
+    for (int j = 0; j < XJ; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int r = r0 + 16 * i + 4 * g + e, c = cx + 16 * j + l;
+        float t = 0.0f;
+        if (r < m && c < n) {
+          const long o = at + (tall ? (long)c * m + r : (long)r * n + c);
+          t = bf16 ? load1<true>(gin, o) : load1<false>(gin, o);
+        }
+        x[i][j][e] = t;
+        ss += (double)t * (double)t;
+      }
+  ss = wave_sum(ss);
+  if (lane == 0) red[w] = ss;
+  __syncthreads();
+  ss = 0.0;
+#pragma unroll
+  for (int i = 0; i < WR * WC; ++i) ss += red[i];
+  const double scale = (double)kOrthX / (sqrt(ss) + (double)eps);
+  auto put_x = [&]() {
+#pragma unroll
+    for (int i = 0; i < AI; ++i)
+#pragma unroll
+      for (int j = 0; j < XJ; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int o = (r0 + 16 * i + 4 * g + e) * SX + cx + 16 * j + l;
+          split_f16(x[i][j][e], xp[0][o], xp[1][o]);
+        }
+  };
+#pragma unroll
+  for (int i = 0; i < AI; ++i)
+#pragma unroll
+    for (int j = 0; j < XJ; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[i][j][e] = (float)((double)x[i][j][e] * scale);
+  put_x();
+  // the sum of rows of P times rows of Q over K columns, for this wave's AI x AJ tiles of A
+  auto rows_by_rows = [&](const uint16_t (*p)[MP * SX], const uint16_t (*q)[MP * SA], int st, int K, f32x4 (&acc)[AI][AJ]) {
+    const uint16_t* hi = p ? p[0] : q[0];
+    const uint16_t* lo = p ? p[1] : q[1];
+#pragma unroll
+    for (int i = 0; i < AI; ++i)
+#pragma unroll
+      for (int j = 0; j < AJ; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+    for (int k = 0; k < K; k += 32) {
+      uint4 nh[AJ], nl[AJ];
+#pragma unroll
+      for (int j = 0; j < AJ; ++j) {
+        nh[j] = lds_row(hi, st, ca + 16 * j, k, g, l);
+        nl[j] = lds_row(lo, st, ca + 16 * j, k, g, l);
+      }
+#pragma unroll
+      for (int i = 0; i < AI; ++i) {
+        const uint4 mh = lds_row(hi, st, r0 + 16 * i, k, g, l), ml = lds_row(lo, st, r0 + 16 * i, k, g, l);
+#pragma unroll
+        for (int j = 0; j < AJ; ++j) {
+          f32x4 t = mfma_f16(ml, nh[j], f32x4{0, 0, 0, 0});
+          t = mfma_f16(mh, nl[j], t);
+          acc[i][j] += mfma_f16(mh, nh[j], t);
+        }
+      }
+    }
+  };
+  auto put_a = [&](const float (&v)[AI][AJ][4]) {
+#pragma unroll
+    for (int i = 0; i < AI; ++i)
+#pragma unroll
+      for (int j = 0; j < AJ; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int o = (r0 + 16 * i + 4 * g + e) * SA + ca + 16 * j + l;
+          split_f16(v[i][j][e], ap[0][o], ap[1][o]);
+        }
+  };
+  __syncthreads();
+  for (int s = 0; s < steps; ++s) {
+    const float fa = coefs.c[3 * s], fb = coefs.c[3 * s + 1], fc = coefs.c[3 * s + 2];
+    f32x4 acc[AI][AJ];
+    float a[AI][AJ][4];
+    rows_by_rows(xp, nullptr, SX, NP, acc);
+#pragma unroll
+    for (int i = 0; i < AI; ++i)
+#pragma unroll
+      for (int j = 0; j < AJ; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) a[i][j][e] = acc[i][j][e] * (kOrthA / (kOrthX * kOrthX));
+    put_a(a);
+    __syncthreads();
+    rows_by_rows(nullptr, ap, SA, MP, acc);  // (A is symmetric)
+#pragma unroll
+    for (int i = 0; i < AI; ++i)
+#pragma unroll
+      for (int j = 0; j < AJ; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          a[i][j][e] = __builtin_fmaf(fb * (kOrthB / kOrthA), a[i][j][e], fc * (kOrthB / (kOrthA * kOrthA)) * acc[i][j][e]);
+    __syncthreads();
+    put_a(a);
+    __syncthreads();
+    f32x4 y[AI][XJ];
+#pragma unroll
+    for (int i = 0; i < AI; ++i)
+#pragma unroll
+      for (int j = 0; j < XJ; ++j) y[i][j] = f32x4{0, 0, 0, 0};
+    for (int k = 0; k < MP; k += 32) {
+      uint4 nh[XJ], nl[XJ];
+#pragma unroll
+      for (int j = 0; j < XJ; ++j) {
+        nh[j] = lds_col(xp[0], SX, k, cx + 16 * j, g, l);
+        nl[j] = lds_col(xp[1], SX, k, cx + 16 * j, g, l);
+      }
+#pragma unroll
+      for (int i = 0; i < AI; ++i) {
+        const uint4 mh = lds_row_acc(ap[0], SA, r0 + 16 * i, k, g, l), ml = lds_row_acc(ap[1], SA, r0 + 16 * i, k, g, l);
+#pragma unroll
+        for (int j = 0; j < XJ; ++j) {
+          f32x4 t = mfma_f16(ml, nh[j], f32x4{0, 0, 0, 0});
+          t = mfma_f16(mh, nl[j], t);
+          y[i][j] += mfma_f16(mh, nh[j], t);
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < AI; ++i)
+#pragma unroll
+      for (int j = 0; j < XJ; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[i][j][e] = __builtin_fmaf(fa, x[i][j][e], y[i][j][e] * (1.0f / kOrthB));
+    __syncthreads();
+    if (s + 1 < steps) put_x();
+    __syncthreads();
+  }
+#pragma unroll
+  for (int i = 0; i < AI; ++i)
+#pragma unroll
+    for (int j = 0; j < XJ; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int r = r0 + 16 * i + 4 * g + e, c = cx + 16 * j + l;
+        if (r < m && c < n) {
+          const long o = at + (tall ? (long)c * m + r : (long)r * n + c);
+          const float v = x[i][j][e] * (1.0f / kOrthX);
+          if (bf16)
+            ((__bf16*)out)[o] = (__bf16)v;
+          else
+            ((float*)out)[o] = v;
+        }
+      }
 }
 
 }  // namespace m2rnn

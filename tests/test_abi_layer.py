@@ -92,7 +92,7 @@ def orth(batch=2, m=64, n=64, dt=0, g=MB, steps=5, coefs=True, eps=1e-7, out=2 *
     (dict(batch=-1), EINVAL), (dict(m=-1), EINVAL), (dict(dt=2), EINVAL), (dict(steps=0), EINVAL), (dict(steps=65), EUNS),
     (dict(coefs=False), EINVAL), (dict(eps=-1.0), EINVAL), (dict(eps=float("nan")), EINVAL), (dict(m=65537), EUNS),
     (dict(batch=65536), EUNS), (dict(batch=1000, m=16384, n=16384), EUNS), (dict(g=0), EINVAL), (dict(out=0), EINVAL),
-    (dict(g=MB + 4), EINVAL), (dict(out=MB + 64), EINVAL), (dict(ws=0), EWS), (dict(bytes_=64), EWS), (dict(ws=16 * MB + 4), EWS),
+    (dict(g=MB + 4), EINVAL), (dict(out=MB + 64), EINVAL), (dict(ws=0, m=300), EWS), (dict(bytes_=64, m=300), EWS), (dict(ws=16 * MB + 4, m=300), EWS),
     (dict(batch=0), OK), (dict(n=0), OK)])
 def test_orthogonalize_arguments(kw, status):
     assert orth(**kw) == status
