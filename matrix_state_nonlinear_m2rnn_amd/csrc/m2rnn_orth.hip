@@ -17,7 +17,6 @@ namespace {
 constexpr long kOrthMaxSide = 65536;
 constexpr long kOrthParts = 1024;  // partial sums of squares of a matrix at most
 constexpr int kOrthPad = 128;     // what the refusals round sides up to
-constexpr int kOrthSplits = 16;   // parts of a contraction at most
 
 bool al16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 size_t round_up256(size_t x) { return (x + 255) & ~(size_t)255; }
@@ -33,29 +32,56 @@ int check_orth(int64_t batch, int64_t m, int64_t n, int dtype) {
   return M2RNN_OK;
 }
 
-// How a product is cut: tile side, workgroups that a CU holds, and a stage's time when it holds them (us).
+// Tiles that a product is cut into: their sides, workgroups that a CU holds, and a stage's time (us) where it holds one,
+// two, ... of them (measured over products of 192 to 8192 a side).
 struct Shape {
-  int T, held;
-  double stage;
+  int TM, TN, held;
+  double stage[4];
 };
-constexpr Shape kShapes[] = {{256, 1, 1.6}, {128, 2, 0.9}, {64, 4, 0.8}};
+constexpr Shape kShapes[] = {
+    {256, 256, 1, {2.2}}, {128, 128, 2, {0.95, 1.2}}, {128, 64, 3, {0.65, 0.9, 1.15}}, {64, 64, 4, {0.4, 0.52, 0.75, 1.05}}};
+constexpr int kShapeCount = sizeof(kShapes) / sizeof(kShapes[0]);
 
+// How a product runs: its tiles, the parts of its contraction, and the time that this should take (us).
 struct Cut {
-  int splits = 1, tiles = 1;
+  int shape = 0, splits = 1, tiles = 1;
   double us = 0.0;
 };
-Cut cut_product(const Shape& h, long batch, long rows, long cols, long K, bool sym) {
-  const long gi = rows / h.T, gj = cols / h.T, stages = K / kOrthK;
+
+// The time of `groups` workgroups of `stages` stages: whole rounds of what the CUs hold, then the rest.
+double rounds_us(const Shape& h, double groups, double stages) {
+  const double load = groups / 256.0;
+  const double full = (double)(long)(load / h.held);
+  const double rest = load - full * h.held;
+  double us = full * h.stage[h.held - 1];
+  if (rest > 0.0) {
+    const int low = rest < 1.0 ? 1 : (int)rest;
+    const double at = rest < 1.0 || low >= h.held ? 0.0 : rest - low;
+    us += h.stage[low - 1] + (at > 0.0 ? at * (h.stage[low] - h.stage[low - 1]) : 0.0);
+  }
+  return us * stages;
+}
+
+Cut cut_product(long batch, long rows, long cols, long K, bool sym) {
   Cut best;
-  best.tiles = (int)(sym ? gi * (gi + 1) / 2 : gi * gj);
-  for (int s = 1; s <= kOrthSplits && s <= stages; ++s) {
-    const long groups = best.tiles * batch * s;
-    if (s > 1 && groups > 2L * 256 * h.held) break;
-    double us = (double)ceil_div(groups, 256L * h.held) * ((double)ceil_div(stages, s) * h.stage + 2.0) + 4.0;
-    if (s > 1) us += 5.0 + (double)groups * h.T * h.T * 8.0 / 4e6;  // the parts written and read, one more launch
-    if (s == 1 || us < best.us) {
-      best.splits = s;
-      best.us = us;
+  const long stages = K / kOrthK;
+  for (int i = 0; i < kShapeCount; ++i) {
+    const Shape& h = kShapes[i];
+    if (rows % h.TM || cols % h.TN) continue;
+    const long gi = rows / h.TM, gj = cols / h.TN;
+    const long tiles = sym ? gi * (gi + 1) / 2 * (h.TM / h.TN) : gi * gj;
+    for (int s : {1, 2, 3, 4, 6, 8, 12, 16}) {
+      if (s > stages) break;
+      const double groups = (double)tiles * batch * s;
+      if (s > 1 && groups > 256.0 * h.held) break;
+      double us = rounds_us(h, groups, (double)ceil_div(stages, s)) + 6.0;
+      if (s > 1) us += 4.0 + groups * h.TM * h.TN * 8.0 / 4e6;  // the parts written and read, one more launch
+      if (best.us == 0.0 || us < best.us) {
+        best.shape = i;
+        best.splits = s;
+        best.tiles = (int)tiles;
+        best.us = us;
+      }
     }
   }
   return best;
@@ -64,27 +90,29 @@ Cut cut_product(const Shape& h, long batch, long rows, long cols, long K, bool s
 // Sizes with m the shorter side, padded, and the workspace's parts.
 struct Plan {
   long m, n, mp = 0, np = 0, parts, each;
-  int shape = 0;
   Cut gram, poly, next;
   size_t part_bytes, x_bytes, a_bytes, split_bytes;  // partial sums of squares; one fp16 plane of X, of A; split products
   Plan(int64_t batch, int64_t rows, int64_t cols) {
     m = std::min(rows, cols);
     n = std::max(rows, cols);
     double best = 0.0;
-    for (int i = 0; i < 3; ++i) {
-      const Shape& h = kShapes[i];
-      const long a = ceil_div(m, h.T) * h.T, b = ceil_div(n, h.T) * h.T;
-      const Cut x = cut_product(h, batch, a, a, b, true), y = cut_product(h, batch, a, a, a, true),
-                w = cut_product(h, batch, a, b, a, false);
-      const double us = x.us + y.us + w.us;
-      if (i == 0 || us < best) {
-        best = us;
-        shape = i;
-        mp = a;
-        np = b;
-        gram = x;
-        poly = y;
-        next = w;
+    for (long pm = 64, a, last_a = 0; pm <= 256; pm *= 2, last_a = a) {
+      a = ceil_div(m, pm) * pm;
+      if (a == last_a) continue;
+      const Cut y = cut_product(batch, a, a, a, true);
+      for (long pn = 64, b, last_b = 0; pn <= 256; pn *= 2, last_b = b) {
+        b = ceil_div(n, pn) * pn;
+        if (b == last_b) continue;
+        const Cut x = cut_product(batch, a, a, b, true), w = cut_product(batch, a, b, a, false);
+        const double us = x.us + y.us + w.us;
+        if (mp == 0 || us < best) {
+          best = us;
+          mp = a;
+          np = b;
+          gram = x;
+          poly = y;
+          next = w;
+        }
       }
     }
     each = std::max(ceil_div(ceil_div(m * n, kOrthParts), 1024), 4L) * 1024;
@@ -95,33 +123,34 @@ struct Plan {
     split_bytes = 0;
     for (const Cut* c : {&gram, &poly, &next})
       if (c->splits > 1)
-        split_bytes = std::max(split_bytes, (size_t)batch * c->splits * c->tiles * kShapes[shape].T * kShapes[shape].T * 4);
+        split_bytes = std::max(split_bytes, (size_t)batch * c->splits * c->tiles * kShapes[c->shape].TM * kShapes[c->shape].TN * 4);
   }
   size_t bytes() const { return part_bytes + 8 * x_bytes + 4 * a_bytes + split_bytes; }
 };
 
-template <int T, int WR, int WC, int EPI>
+template <int TM, int TN, int WR, int WC, int EPI>
 int product_of(OrthArgs& A, long batch, hipStream_t s) {
   void* args[] = {&A};
   const dim3 grid((unsigned)A.tiles, (unsigned)A.splits, (unsigned)batch), block(64 * WR * WC);
-  const void* one = (const void*)&m2rnn_orth_product_kernel<T, WR, WC, EPI, false>;
+  const void* one = (const void*)&m2rnn_orth_product_kernel<TM, TN, WR, WC, EPI, false>;
   if (A.splits == 1) return record_hip_status(hipLaunchKernel(one, grid, block, args, 0, s));
-  const void* some = (const void*)&m2rnn_orth_product_kernel<T, WR, WC, EPI, true>;
+  const void* some = (const void*)&m2rnn_orth_product_kernel<TM, TN, WR, WC, EPI, true>;
   const int st = record_hip_status(hipLaunchKernel(some, grid, block, args, 0, s));
   if (st) return st;
-  const long items = (long)A.tiles * (T / 16) * WC;
-  return record_hip_status(hipLaunchKernel((const void*)&m2rnn_orth_join_kernel<T, WR, WC, EPI>,
+  const long items = (long)A.tiles * (TM / 16) * WC;
+  return record_hip_status(hipLaunchKernel((const void*)&m2rnn_orth_join_kernel<TM, TN, WR, WC, EPI>,
                                            dim3((unsigned)ceil_div(items, 4), 1, (unsigned)batch), dim3(256), args, 0, s));
 }
 
 template <int EPI>
-int product(int shape, const Cut& cut, OrthArgs& A, long batch, hipStream_t s) {
+int product(const Cut& cut, OrthArgs& A, long batch, hipStream_t s) {
   A.splits = cut.splits;
   A.tiles = cut.tiles;
-  switch (shape) {
-    case 0: return product_of<256, 2, 4, EPI>(A, batch, s);
-    case 1: return product_of<128, 2, 2, EPI>(A, batch, s);
-    default: return product_of<64, 2, 2, EPI>(A, batch, s);
+  switch (cut.shape) {
+    case 0: return product_of<256, 256, 2, 4, EPI>(A, batch, s);
+    case 1: return product_of<128, 128, 2, 2, EPI>(A, batch, s);
+    case 2: return product_of<128, 64, 2, 2, EPI>(A, batch, s);
+    default: return product_of<64, 64, 2, 2, EPI>(A, batch, s);
   }
 }
 
@@ -202,20 +231,24 @@ int m2rnn_orthogonalize(int64_t batch, int64_t m, int64_t n, int dtype, const vo
     const float* c = coefs + 3 * i;
     OrthArgs A{};
     A.part = (float*)at;
+    const bool cubic = c[2] == 0.0f;  // B = b A
     A.M = A.N = X;
-    A.O = A.OT = P;
+    A.O = A.OT = cubic ? Q : P;
     A.rows = A.cols = (int)p.mp;
     A.K = (int)p.np;
-    st = product<ORTH_GRAM>(p.shape, p.gram, A, batch, s);
-    if (st) break;
-    A.M = A.N = A.E = P;
-    A.O = A.OT = Q;
-    A.K = (int)p.mp;
-    A.cb = c[1];
-    A.cc = c[2];
-    st = product<ORTH_POLY>(p.shape, p.poly, A, batch, s);
+    A.cb = cubic ? c[1] * kOrthB : kOrthA;
+    st = product<ORTH_GRAM>(p.gram, A, batch, s);
+    if (!st && !cubic) {
+      A.M = A.N = A.E = P;
+      A.O = A.OT = Q;
+      A.K = (int)p.mp;
+      A.cb = c[1];
+      A.cc = c[2];
+      st = product<ORTH_POLY>(p.poly, A, batch, s);
+    }
     if (st) break;
     A.M = Q;
+    A.K = (int)p.mp;
     A.N = XT;
     A.X32 = X32;
     A.O = X;
@@ -227,7 +260,7 @@ int m2rnn_orthogonalize(int64_t batch, int64_t m, int64_t n, int dtype, const vo
     A.n = (int)p.n;
     A.tall = tall;
     A.out_bf16 = bf16;
-    st = i + 1 < steps ? product<ORTH_NEXT>(p.shape, p.next, A, batch, s) : product<ORTH_LAST>(p.shape, p.next, A, batch, s);
+    st = i + 1 < steps ? product<ORTH_NEXT>(p.next, A, batch, s) : product<ORTH_LAST>(p.next, A, batch, s);
     std::swap(XT, YT);
   }
   return st;

@@ -176,7 +176,7 @@ __device__ __forceinline__ void orth_finish(const OrthArgs& A, long z, int r, in
     for (int e = 0; e < 4; ++e) {
       float y = acc[j][e];
       if constexpr (EPI == ORTH_GRAM)
-        y *= kOrthA / (kOrthX * kOrthX);
+        y *= A.cb * (1.0f / (kOrthX * kOrthX));  // (A, or B of a cubic step, times its power of two)
       else if constexpr (EPI == ORTH_POLY)
         y = __builtin_fmaf(A.cb * (kOrthB / kOrthA), x[j][e], A.cc * (kOrthB / (kOrthA * kOrthA)) * y);
       else
@@ -208,14 +208,16 @@ __device__ __forceinline__ void orth_finish(const OrthArgs& A, long z, int r, in
   }
 }
 
-// The place of tile number `id`: the lower triangle by rows (SYM), or bands of four rows, column by column.
-template <bool SYM>
+// The place of tile number `id` of TM x TN tiles: those that touch the lower triangle by rows (SYM, Q = TM / TN of them for
+// each row before), or bands of four rows, column by column.
+template <bool SYM, int Q>
 __device__ __forceinline__ void orth_place(int id, int gi, int gj, int& bi, int& bj) {
   if constexpr (SYM) {
-    bi = (int)((sqrtf(8.0f * (float)id + 1.0f) - 1.0f) * 0.5f);
-    while ((bi + 1) * (bi + 2) / 2 <= id) ++bi;
-    while (bi * (bi + 1) / 2 > id) --bi;
-    bj = id - bi * (bi + 1) / 2;
+    const int k = id / Q;
+    bi = (int)((sqrtf(8.0f * (float)k + 1.0f) - 1.0f) * 0.5f);
+    while ((bi + 1) * (bi + 2) / 2 * Q <= id) ++bi;
+    while (bi * (bi + 1) / 2 * Q > id) --bi;
+    bj = id - bi * (bi + 1) / 2 * Q;
   } else {
     const int band = id / (4 * gj), in = id % (4 * gj);
     const int high = gi - 4 * band < 4 ? gi - 4 * band : 4;
@@ -238,34 +240,42 @@ __device__ __forceinline__ void load_to_lds(const void* from, const void* to) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(at), "v"(from) : "memory");
 }
 
-// One T x T tile of M N^T, or its part of a split contraction.  WR x WC waves, 16x16x32 MFMA.  A stage is 32 of the
-// contraction: a column of blocks of the four planes, brought to LDS past the registers while the stage before is
-// multiplied.  The three passes of a stage are summed by themselves, from zero, and added to the tile's sum once:
-// one rounding at the sum's size for each stage instead of three.
-template <int T, int WR, int WC, int EPI, bool SPLIT>
+// One TM x TN tile of M N^T, or its part of a split contraction.  WR x WC waves, 16x16x32 MFMA.  A stage is 32 of the
+// contraction: a column of blocks of the four planes, brought to LDS past the registers.  The three passes of a stage are
+// summed by themselves, from zero, and added to the tile's sum once: one rounding at the sum's size for each stage
+// instead of three.
+// LDS holds two stages; the next one is on its way beside the products.  (Three stages, with the barrier in the middle of one
+// and the operands read across the stages' border, ran no faster: 256 x 128 tiles 250 us where 256 x 256 take 232, 64 x 64 equal.)
+template <int TM, int TN, int WR, int WC, int EPI, bool SPLIT>
 __global__ void __launch_bounds__(64 * WR * WC) m2rnn_orth_product_kernel(OrthArgs A) {
   constexpr bool SYM = EPI == ORTH_GRAM || EPI == ORTH_POLY;
-  constexpr int NI = T / WR / 16, NJ = T / WC / 16, WAVES = WR * WC;
-  constexpr int PER = 4 * (T / 16) / WAVES;  // 16-row pieces of a plane's stage that a wave brings
-  static_assert((T / 16) % PER == 0, "a wave brings pieces of one plane");
-  __shared__ uint4 lds[2 * 4 * T * 4];  // [buffer][M hi, M lo, N hi, N lo][row][unit]
+  constexpr int NI = TM / WR / 16, NJ = TN / WC / 16, WAVES = WR * WC;
+  constexpr int BM = TM / 16, BN = TN / 16, PER = 2 * (BM + BN) / WAVES;  // blocks of a plane's stage; those that a wave brings
+  constexpr int STAGE = 8 * (TM + TN);                                    // 16-byte units
+  static_assert(2 * (BM + BN) % WAVES == 0 && TM % TN == 0, "whole blocks for each wave, whole tiles on the diagonal");
+  __shared__ uint4 lds[2 * STAGE];  // [buffer][M hi, M lo, N hi, N lo][row][unit]
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int tile = orth_turn(blockIdx.x, A.tiles);
   int bi, bj;
-  orth_place<SYM>(tile, A.rows / T, A.cols / T, bi, bj);
+  orth_place<SYM, TM / TN>(tile, A.rows / TM, A.cols / TN, bi, bj);
   const long z = blockIdx.z;
-  const int r0 = bi * T, c0 = bj * T;
+  const int r0 = bi * TM, c0 = bj * TN;
   const int stages = A.K / kOrthK;
   const int first = SPLIT ? (int)((long)stages * blockIdx.y / A.splits) : 0;
   const int last = SPLIT ? (int)((long)stages * (blockIdx.y + 1) / A.splits) : stages;
-  const int plane = w * PER / (T / 16), piece = w * PER % (T / 16);
-  const uint16_t* src = plane < 2 ? (plane == 0 ? A.M.hi : A.M.lo) + (z * A.rows + r0) * A.K
-                                  : (plane == 2 ? A.N.hi : A.N.lo) + (z * A.cols + c0) * A.K;
-  src += (long)piece * 16 * A.K + lane * 8;
+  const uint16_t* src[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int id = w * PER + i;  // the block's number in a stage, by planes
+    const bool right = id >= 2 * BM;
+    const int in = right ? id - 2 * BM : id, most = right ? BN : BM;
+    const int lo = in >= most, blk = in - lo * most;
+    const Planes& P = right ? A.N : A.M;
+    src[i] = (lo ? P.lo : P.hi) + ((z * (right ? A.cols : A.rows) + (right ? c0 : r0) + 16 * blk) * A.K + lane * 8);
+  }
   auto fetch = [&](int buf, int stage) {
 #pragma unroll
-    for (int i = 0; i < PER; ++i)
-      load_to_lds(src + (long)i * 16 * A.K + (long)stage * 512, lds + (buf * 4 + plane) * T * 4 + (piece + i) * 64);
+    for (int i = 0; i < PER; ++i) load_to_lds(src[i] + (long)stage * 512, lds + buf * STAGE + (w * PER + i) * 64);
   };
   f32x4 acc[NI][NJ];
 #pragma unroll
@@ -273,49 +283,48 @@ __global__ void __launch_bounds__(64 * WR * WC) m2rnn_orth_product_kernel(OrthAr
 #pragma unroll
     for (int j = 0; j < NJ; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
   const int n = lane & 15, g = lane >> 4;
-  const int wr = (w / WC) * (T / WR), wc = (w % WC) * (T / WC);
+  const int wr = (w / WC) * (TM / WR), wc = (w % WC) * (TN / WC);
   const int unit = n * 4 + (g ^ ((n >> 1) & 3));  // (16 rows on: the same exchange)
+  const uint4 *pm = lds + wr * 4 + unit, *pn = lds + 8 * TM + wc * 4 + unit;
+  uint4 nh[NJ], nl[NJ], mh[2], ml[2];
+  auto read_m = [&](int buf, int i) {
+    mh[i & 1] = pm[buf * STAGE + i * 64];
+    ml[i & 1] = pm[buf * STAGE + 4 * TM + i * 64];
+  };
+  f32x4 t[2][NJ];
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) t[1][j] = f32x4{0, 0, 0, 0};
+  static_assert(NI % 2 == 0, "the rows' operands and sums take turns");
   fetch(0, first);
   for (int s = first; s < last; ++s) {
     const int buf = (s - first) & 1;
-    __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0): this wave's pieces have arrived
-    lds_barrier();
+    __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0): this wave's blocks have arrived
+    lds_barrier();                       // and all waves'; the other buffer has been read by all
     if (s + 1 < last) fetch(buf ^ 1, s + 1);
-    const uint4* mhi = lds + buf * 16 * T + wr * 4 + unit;
-    const uint4* mlo = mhi + T * 4;
-    const uint4* nhi = lds + buf * 16 * T + 8 * T + wc * 4 + unit;
-    const uint4* nlo = nhi + T * 4;
-    uint4 nh[NJ], nl[NJ], mh[2], ml[2];
-    f32x4 t[2][NJ];
-    mh[0] = mhi[0];
-    ml[0] = mlo[0];
+    read_m(buf, 0);
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
-      nh[j] = nhi[j * 64];
-      nl[j] = nlo[j * 64];
+      nh[j] = pn[buf * STAGE + j * 64];
+      nl[j] = pn[buf * STAGE + 4 * TN + j * 64];
     }
     // a row of tiles at a time: the next row's operands are read, and the last row's sums added, beside its products
 #pragma unroll
-    for (int i = 0; i <= NI; ++i) {
-      if (i + 1 < NI) {
-        mh[(i + 1) & 1] = mhi[(i + 1) * 64];
-        ml[(i + 1) & 1] = mlo[(i + 1) * 64];
-      }
-      if (i < NI) {
+    for (int i = 0; i < NI; ++i) {
+      if (i + 1 < NI) read_m(buf, i + 1);
+      __builtin_amdgcn_sched_barrier(0);  // reads stay before: the compiler would leave them for the end, to be waited for
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) t[i & 1][j] = mfma_f16(ml[i & 1], nh[j], f32x4{0, 0, 0, 0});
+      for (int j = 0; j < NJ; ++j) acc[i == 0 ? NI - 1 : i - 1][j] += t[(i & 1) ^ 1][j];
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) t[i & 1][j] = mfma_f16(mh[i & 1], nl[j], t[i & 1][j]);
+      for (int j = 0; j < NJ; ++j) t[i & 1][j] = mfma_f16(ml[i & 1], nh[j], f32x4{0, 0, 0, 0});
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) t[i & 1][j] = mfma_f16(mh[i & 1], nh[j], t[i & 1][j]);
-      }
-      if (i > 0) {
+      for (int j = 0; j < NJ; ++j) t[i & 1][j] = mfma_f16(mh[i & 1], nl[j], t[i & 1][j]);
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) acc[i - 1][j] += t[(i - 1) & 1][j];
-      }
+      for (int j = 0; j < NJ; ++j) t[i & 1][j] = mfma_f16(mh[i & 1], nh[j], t[i & 1][j]);
       __builtin_amdgcn_sched_barrier(0);
     }
   }
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) acc[NI - 1][j] += t[1][j];
   // lane (g, n), register e: row 4 g + e, column n of a 16 x 16 tile
   if constexpr (SPLIT) {
     float4* dst = (float4*)A.part + (((z * A.splits + blockIdx.y) * A.tiles + tile) * WAVES + w) * (NI * NJ * 64) + lane;
@@ -327,24 +336,24 @@ __global__ void __launch_bounds__(64 * WR * WC) m2rnn_orth_product_kernel(OrthAr
   } else {
 #pragma unroll
     for (int i = 0; i < NI; ++i)
-      orth_finish<EPI, NJ>(A, z, r0 + wr + 16 * i + 4 * g, c0 + wc + n, acc[i], !SYM || bi != bj);
+      orth_finish<EPI, NJ>(A, z, r0 + wr + 16 * i + 4 * g, c0 + wc + n, acc[i], !SYM || bj < bi * (TM / TN));
   }
 }
 
 // The parts of a split contraction added in order, and the epilogue.  A wave takes one row of a wave tile's 16 x 16 tiles.
-template <int T, int WR, int WC, int EPI>
+template <int TM, int TN, int WR, int WC, int EPI>
 __global__ void __launch_bounds__(256) m2rnn_orth_join_kernel(OrthArgs A) {
   constexpr bool SYM = EPI == ORTH_GRAM || EPI == ORTH_POLY;
-  constexpr int NI = T / WR / 16, NJ = T / WC / 16, WAVES = WR * WC;
+  constexpr int NI = TM / WR / 16, NJ = TN / WC / 16, WAVES = WR * WC;
   const int lane = threadIdx.x & 63;
   const long z = blockIdx.z;
   const int item = __builtin_amdgcn_readfirstlane((int)(blockIdx.x * 4 + (threadIdx.x >> 6)));
   if (item >= A.tiles * WAVES * NI) return;
   const int i = item % NI, w = item / NI % WAVES, tile = item / (NI * WAVES);
   int bi, bj;
-  orth_place<SYM>(tile, A.rows / T, A.cols / T, bi, bj);
+  orth_place<SYM, TM / TN>(tile, A.rows / TM, A.cols / TN, bi, bj);
   const int n = lane & 15, g = lane >> 4;
-  const int r = bi * T + (w / WC) * (T / WR) + 16 * i + 4 * g, c = bj * T + (w % WC) * (T / WC) + n;
+  const int r = bi * TM + (w / WC) * (TM / WR) + 16 * i + 4 * g, c = bj * TN + (w % WC) * (TN / WC) + n;
   f32x4 acc[NJ];
 #pragma unroll
   for (int j = 0; j < NJ; ++j) acc[j] = f32x4{0, 0, 0, 0};
@@ -353,18 +362,19 @@ __global__ void __launch_bounds__(256) m2rnn_orth_join_kernel(OrthArgs A) {
 #pragma unroll
     for (int j = 0; j < NJ; ++j) acc[j] += src[j * 64];
   }
-  orth_finish<EPI, NJ>(A, z, r, c, acc, !SYM || bi != bj);
+  orth_finish<EPI, NJ>(A, z, r, c, acc, !SYM || bj < bi * (TM / TN));
 }
 
 // Small matrices: one workgroup takes a matrix through all its steps, X in registers (fp32) and as planes in LDS, A and
-// then B as planes in LDS.  MP x NP the padded size; WR x WC waves over the 16 x 16 tiles of A and of X.  X's columns are
-// read transposed.
+// then B as planes in LDS.  MP x NP the padded size; WR x WC waves over the 16 x 16 tiles of A and of X.  A lane holds four
+// rows of a column, which are neighbours in the transpose: X lies transposed in LDS (its rows are read by transposing
+// reads), and A and B are symmetric.
 template <int MP, int NP, int WR, int WC>
 __global__ void __launch_bounds__(64 * WR * WC) m2rnn_orth_small_kernel(const void* gin, void* out, int m, int n, int tall,
                                                                         int bf16, int steps, OrthCoefs coefs, float eps) {
-  constexpr int SX = ssm_stride(NP), SA = ssm_stride(MP);
+  constexpr int ST = ssm_stride(MP);  // elements between rows of the transpose of X, and of A
   constexpr int AI = MP / 16 / WR, AJ = MP / 16 / WC, XJ = NP / 16 / WC;
-  __shared__ uint16_t xp[2][MP * SX], ap[2][MP * SA];
+  __shared__ __attribute__((aligned(16))) uint16_t xp[2][NP * ST], ap[2][MP * ST];
   __shared__ double red[WR * WC];
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int g = lane >> 4, l = lane & 15;
@@ -394,16 +404,19 @@ __global__ void __launch_bounds__(64 * WR * WC) m2rnn_orth_small_kernel(const vo
 #pragma unroll
   for (int i = 0; i < WR * WC; ++i) ss += red[i];
   const double scale = (double)kOrthX / (sqrt(ss) + (double)eps);
+  // four rows of a column as one write for each plane
+  auto put4 = [&](const float (&v)[4], uint16_t* hi, uint16_t* lo, int row, int col) {
+    uint16_t h[4], t[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) split_f16(v[e], h[e], t[e]);
+    *(uint2*)(hi + row * ST + col) = make_uint2(h[0] | (uint32_t)h[1] << 16, h[2] | (uint32_t)h[3] << 16);
+    *(uint2*)(lo + row * ST + col) = make_uint2(t[0] | (uint32_t)t[1] << 16, t[2] | (uint32_t)t[3] << 16);
+  };
   auto put_x = [&]() {
 #pragma unroll
     for (int i = 0; i < AI; ++i)
 #pragma unroll
-      for (int j = 0; j < XJ; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int o = (r0 + 16 * i + 4 * g + e) * SX + cx + 16 * j + l;
-          split_f16(x[i][j][e], xp[0][o], xp[1][o]);
-        }
+      for (int j = 0; j < XJ; ++j) put4(x[i][j], xp[0], xp[1], cx + 16 * j + l, r0 + 16 * i + 4 * g);
   };
 #pragma unroll
   for (int i = 0; i < AI; ++i)
@@ -412,30 +425,34 @@ __global__ void __launch_bounds__(64 * WR * WC) m2rnn_orth_small_kernel(const vo
 #pragma unroll
       for (int e = 0; e < 4; ++e) x[i][j][e] = (float)((double)x[i][j][e] * scale);
   put_x();
-  // the sum of rows of P times rows of Q over K columns, for this wave's AI x AJ tiles of A
-  auto rows_by_rows = [&](const uint16_t (*p)[MP * SX], const uint16_t (*q)[MP * SA], int st, int K, f32x4 (&acc)[AI][AJ]) {
-    const uint16_t* hi = p ? p[0] : q[0];
-    const uint16_t* lo = p ? p[1] : q[1];
+  // this wave's AI x AJ tiles of X X^T (X's rows read from the transpose's columns) or of A A^T
+  auto square = [&](auto of_x, f32x4 (&acc)[AI][AJ]) {
+    constexpr bool X = decltype(of_x)::value;
+    const uint16_t *hi = X ? xp[0] : ap[0], *lo = X ? xp[1] : ap[1];
+    auto operand = [&](const uint16_t* p, int r, int k) { return X ? lds_col(p, ST, k, r, g, l) : lds_row(p, ST, r, k, g, l); };
 #pragma unroll
     for (int i = 0; i < AI; ++i)
 #pragma unroll
       for (int j = 0; j < AJ; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
-    for (int k = 0; k < K; k += 32) {
+    for (int k = 0; k < (X ? NP : MP); k += 32) {
       uint4 nh[AJ], nl[AJ];
 #pragma unroll
       for (int j = 0; j < AJ; ++j) {
-        nh[j] = lds_row(hi, st, ca + 16 * j, k, g, l);
-        nl[j] = lds_row(lo, st, ca + 16 * j, k, g, l);
+        nh[j] = operand(hi, ca + 16 * j, k);
+        nl[j] = operand(lo, ca + 16 * j, k);
       }
 #pragma unroll
       for (int i = 0; i < AI; ++i) {
-        const uint4 mh = lds_row(hi, st, r0 + 16 * i, k, g, l), ml = lds_row(lo, st, r0 + 16 * i, k, g, l);
+        const uint4 mh = operand(hi, r0 + 16 * i, k), ml = operand(lo, r0 + 16 * i, k);
+        f32x4 t[AJ];
 #pragma unroll
-        for (int j = 0; j < AJ; ++j) {
-          f32x4 t = mfma_f16(ml, nh[j], f32x4{0, 0, 0, 0});
-          t = mfma_f16(mh, nl[j], t);
-          acc[i][j] += mfma_f16(mh, nh[j], t);
-        }
+        for (int j = 0; j < AJ; ++j) t[j] = mfma_f16(ml, nh[j], f32x4{0, 0, 0, 0});
+#pragma unroll
+        for (int j = 0; j < AJ; ++j) t[j] = mfma_f16(mh, nl[j], t[j]);
+#pragma unroll
+        for (int j = 0; j < AJ; ++j) t[j] = mfma_f16(mh, nh[j], t[j]);
+#pragma unroll
+        for (int j = 0; j < AJ; ++j) acc[i][j] += t[j];
       }
     }
   };
@@ -443,36 +460,34 @@ __global__ void __launch_bounds__(64 * WR * WC) m2rnn_orth_small_kernel(const vo
 #pragma unroll
     for (int i = 0; i < AI; ++i)
 #pragma unroll
-      for (int j = 0; j < AJ; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int o = (r0 + 16 * i + 4 * g + e) * SA + ca + 16 * j + l;
-          split_f16(v[i][j][e], ap[0][o], ap[1][o]);
-        }
+      for (int j = 0; j < AJ; ++j) put4(v[i][j], ap[0], ap[1], ca + 16 * j + l, r0 + 16 * i + 4 * g);
   };
   __syncthreads();
   for (int s = 0; s < steps; ++s) {
     const float fa = coefs.c[3 * s], fb = coefs.c[3 * s + 1], fc = coefs.c[3 * s + 2];
     f32x4 acc[AI][AJ];
     float a[AI][AJ][4];
-    rows_by_rows(xp, nullptr, SX, NP, acc);
+    square(std::true_type{}, acc);
 #pragma unroll
     for (int i = 0; i < AI; ++i)
 #pragma unroll
       for (int j = 0; j < AJ; ++j)
 #pragma unroll
         for (int e = 0; e < 4; ++e) a[i][j][e] = acc[i][j][e] * (kOrthA / (kOrthX * kOrthX));
-    put_a(a);
-    __syncthreads();
-    rows_by_rows(nullptr, ap, SA, MP, acc);  // (A is symmetric)
+    if (fc != 0.0f) {
+      put_a(a);
+      __syncthreads();
+      square(std::false_type{}, acc);
+      __syncthreads();
+    }
 #pragma unroll
     for (int i = 0; i < AI; ++i)
 #pragma unroll
       for (int j = 0; j < AJ; ++j)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          a[i][j][e] = __builtin_fmaf(fb * (kOrthB / kOrthA), a[i][j][e], fc * (kOrthB / (kOrthA * kOrthA)) * acc[i][j][e]);
-    __syncthreads();
+          a[i][j][e] = __builtin_fmaf(fb * (kOrthB / kOrthA), a[i][j][e],
+                                      fc == 0.0f ? 0.0f : fc * (kOrthB / (kOrthA * kOrthA)) * acc[i][j][e]);
     put_a(a);
     __syncthreads();
     f32x4 y[AI][XJ];
@@ -484,18 +499,21 @@ __global__ void __launch_bounds__(64 * WR * WC) m2rnn_orth_small_kernel(const vo
       uint4 nh[XJ], nl[XJ];
 #pragma unroll
       for (int j = 0; j < XJ; ++j) {
-        nh[j] = lds_col(xp[0], SX, k, cx + 16 * j, g, l);
-        nl[j] = lds_col(xp[1], SX, k, cx + 16 * j, g, l);
+        nh[j] = lds_row(xp[0], ST, cx + 16 * j, k, g, l);
+        nl[j] = lds_row(xp[1], ST, cx + 16 * j, k, g, l);
       }
 #pragma unroll
       for (int i = 0; i < AI; ++i) {
-        const uint4 mh = lds_row_acc(ap[0], SA, r0 + 16 * i, k, g, l), ml = lds_row_acc(ap[1], SA, r0 + 16 * i, k, g, l);
+        const uint4 mh = lds_row(ap[0], ST, r0 + 16 * i, k, g, l), ml = lds_row(ap[1], ST, r0 + 16 * i, k, g, l);
+        f32x4 t[XJ];
 #pragma unroll
-        for (int j = 0; j < XJ; ++j) {
-          f32x4 t = mfma_f16(ml, nh[j], f32x4{0, 0, 0, 0});
-          t = mfma_f16(mh, nl[j], t);
-          y[i][j] += mfma_f16(mh, nh[j], t);
-        }
+        for (int j = 0; j < XJ; ++j) t[j] = mfma_f16(ml, nh[j], f32x4{0, 0, 0, 0});
+#pragma unroll
+        for (int j = 0; j < XJ; ++j) t[j] = mfma_f16(mh, nl[j], t[j]);
+#pragma unroll
+        for (int j = 0; j < XJ; ++j) t[j] = mfma_f16(mh, nh[j], t[j]);
+#pragma unroll
+        for (int j = 0; j < XJ; ++j) y[i][j] += t[j];
       }
     }
 #pragma unroll
