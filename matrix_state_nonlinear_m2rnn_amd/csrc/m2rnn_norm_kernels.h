@@ -7,8 +7,9 @@
 // r = 1 / sqrt(mean h^2 + eps) and dh the gradient that reaches h down the stream.
 //
 // HBM streams: a row is read once and kept in registers between its sums and its scaling.  LPR lanes hold a row
-// (several rows a wave for narrow ones, a wave or a workgroup for wide ones), a lane 4 neighbouring features at a time,
-// so a group of 128 features is half a wave.
+// (several rows a wave for narrow ones, a wave or a workgroup for wide ones), a lane 8 neighbouring features at a time, so a
+// group of 128 features is 16 lanes (4 at a time, and half a wave, where something read is fp32, D is no multiple of 8, rows are
+// narrow, and in the backward).
 #pragma once
 
 #include "m2rnn_stream.h"
@@ -208,6 +209,116 @@ __global__ void __launch_bounds__(kBlkThreads) m2rnn_add_norm_kernel(NormArgs A)
             if ((unit & 31) == 0) A.scale[row * (A.D / 128) + i / 128] = s;
           }
         }
+      }
+    }
+  }
+}
+
+// Eight neighbouring bf16 values as they are in memory.
+struct Raw8 {
+  uint4 w;
+  __device__ __forceinline__ void load(const void* p, long at) {
+    typedef unsigned u4v __attribute__((ext_vector_type(4)));
+    const u4v t = __builtin_nontemporal_load((const u4v*)((const uint16_t*)p + at));
+    w = make_uint4(t[0], t[1], t[2], t[3]);
+  }
+  __device__ __forceinline__ float operator[](int e) const {
+    const uint32_t u = e < 2 ? w.x : e < 4 ? w.y : e < 6 ? w.z : w.w;
+    return e & 1 ? bf16_hi_to_f32(u) : bf16_lo_to_f32(u);
+  }
+};
+__device__ __forceinline__ void store8_nt(void* p, bool bf16, long at, const float (&v)[8]) {
+  typedef unsigned u4v __attribute__((ext_vector_type(4)));
+  if (bf16) {
+    const u4v w = {pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7])};
+    __builtin_nontemporal_store(w, (u4v*)((uint16_t*)p + at));
+  } else {
+    const f32x4 a = {v[0], v[1], v[2], v[3]}, b = {v[4], v[5], v[6], v[7]};
+    __builtin_nontemporal_store(a, (f32x4*)((float*)p + at));
+    __builtin_nontemporal_store(b, (f32x4*)((float*)p + at) + 1);
+  }
+}
+
+// The same for bf16 inputs: 8 features at a time, and a row's loads in flight beside the row before's sums and stores (a
+// bf16 row has half the bytes: without this 32768 rows of 2048 in bf16 took 165 us, nearly as long as in fp32).
+template <int LPR, int NG, bool RES, bool Q8>
+__global__ void __launch_bounds__(kBlkThreads) m2rnn_add_norm8_kernel(NormArgs A) {
+  constexpr int RPB = kBlkThreads / LPR;
+  __shared__ float red[2][kBlkThreads / 64];
+  __shared__ uint32_t redm[kBlkThreads / 64];
+  const int unit = threadIdx.x % LPR, sub = threadIdx.x / LPR;
+  float gm[NG][8];
+  Raw8 x[NG] = {}, res[RES ? NG : 1] = {};
+  auto fetch = [&](long row) {
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+      const int i = 8 * (g * LPR + unit);
+      if (i < A.D) {
+        x[g].load(A.x, row * A.D + i);
+        if constexpr (RES) res[g].load(A.res, row * A.D + i);
+      }
+    }
+  };
+  long r0 = (long)blockIdx.x * RPB;
+  const long step = (long)gridDim.x * RPB;
+  fetch(r0 + sub < A.rows ? r0 + sub : A.rows - 1);  // (lanes without a row take the last one and store nothing)
+#pragma unroll
+  for (int g = 0; g < NG; ++g)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) gm[g][e] = 8 * (g * LPR + unit) < A.D ? A.gamma[8 * (g * LPR + unit) + e] : 0.0f;
+  const float inv = 1.0f / (float)A.D;
+  for (int turn = 0; r0 < A.rows; r0 += step, turn ^= 1) {
+    const bool on = r0 + sub < A.rows;
+    const long row = on ? r0 + sub : A.rows - 1, at = row * A.D;
+    float h[NG][8], ss = 0.0f;
+#pragma unroll
+    for (int g = 0; g < NG; ++g)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        h[g][e] = x[g][e];
+        if constexpr (RES) h[g][e] = (float)(__bf16)(h[g][e] + res[g][e]);
+        ss = __builtin_fmaf(h[g][e], h[g][e], ss);
+      }
+    if (r0 + step < A.rows) fetch(r0 + step + sub < A.rows ? r0 + step + sub : A.rows - 1);
+    if (RES && A.h && on) {
+#pragma unroll
+      for (int g = 0; g < NG; ++g)
+        if (8 * (g * LPR + unit) < A.D) store8_nt(A.h, true, at + 8 * (g * LPR + unit), h[g]);
+    }
+    const float r = 1.0f / sqrtf(row_sum<LPR>(ss, red, turn) * inv + A.eps);
+    uint32_t most[NG], all = 0;
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+      most[g] = 0;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        h[g][e] = h[g][e] * r * gm[g][e];
+        if constexpr (Q8) most[g] = umax_(most[g], __float_as_uint(h[g][e]) & 0x7FFFFFFFu);
+      }
+      all = umax_(all, most[g]);
+    }
+    if constexpr (!Q8) {
+#pragma unroll
+      for (int g = 0; g < NG; ++g)
+        if (on && 8 * (g * LPR + unit) < A.D) store8_nt(A.out, A.out_bf16, at + 8 * (g * LPR + unit), h[g]);
+    } else {
+      const bool whole = A.group == A.D;
+      float s = 0.0f, si = 0.0f;
+      if (whole) {
+        s = e4m3_scale(row_max<LPR>(all, redm));  // (the next row writes redm behind row_sum's barrier)
+        si = 1.0f / s;
+        if (on && unit == 0) A.scale[row] = s;
+      }
+#pragma unroll
+      for (int g = 0; g < NG; ++g) {
+        const int i = 8 * (g * LPR + unit);
+        if (!whole) {
+          s = e4m3_scale(row16_max(most[g]));
+          si = 1.0f / s;
+          if (on && i < A.D && (unit & 15) == 0) A.scale[row * (A.D / 128) + i / 128] = s;
+        }
+        const float lo[4] = {h[g][0], h[g][1], h[g][2], h[g][3]}, hi[4] = {h[g][4], h[g][5], h[g][6], h[g][7]};
+        if (on && i < A.D) *(uint2*)((uint8_t*)A.out + at + i) = make_uint2(pack_e4m3(lo, s, si), pack_e4m3(hi, s, si));
       }
     }
   }
