@@ -1174,6 +1174,11 @@ def m2rnn_grad_clip(grads, max_norm: float, *, norm=None, out=None, workspace=No
 
 # ---------------------------------------------------------------- the residual's addition with the norm
 
+def _all_plain(dev, *tensors) -> bool:
+    """Whether all tensors (None: left out) are contiguous and on a GPU device `dev`: the checks' quick way out."""
+    return dev.type == "cuda" and all(t is None or (t.device == dev and t.is_contiguous()) for t in tensors)
+
+
 def _add_norm_rows(x, gamma):
     D = gamma.numel()
     if gamma.dim() != 1 or x.dim() < 1 or x.shape[-1] != D:
@@ -1181,6 +1186,9 @@ def _add_norm_rows(x, gamma):
     if x.device.type != "cuda":
         raise ValueError("inputs must be on a GPU (HIP) device")
     return x.numel() // max(D, 1), D
+
+
+_norm_out_codes = {}
 
 
 def m2rnn_add_norm_fwd(x, gamma, res=None, eps: float = 1e-6, *, out_dtype=None, group: int = 0, h=None, out=None,
@@ -1195,34 +1203,51 @@ def m2rnn_add_norm_fwd(x, gamma, res=None, eps: float = 1e-6, *, out_dtype=None,
     import torch
     rows, D = _add_norm_rows(x, gamma)
     dev, shape = x.device, x.shape
-    _require(x, "x", (torch.float32, torch.bfloat16), shape, dev)
-    _require(gamma, "gamma", torch.float32, (D,), dev)
-    if res is not None:
-        _require(res, "res", (torch.float32, torch.bfloat16), shape, dev)
-    elif h is not None:
+    if not _norm_out_codes:
+        _norm_out_codes.update({torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16, torch.float8_e4m3fn: DTYPE_E4M3})
+    codes = _norm_out_codes
+    xc, rc = codes.get(x.dtype, -1), 0 if res is None else codes.get(res.dtype, -1)
+    if not (0 <= xc < 2 and 0 <= rc < 2 and gamma.dtype is torch.float32 and (res is None or res.shape == shape)
+            and _all_plain(dev, x, gamma, res)):
+        _require(x, "x", (torch.float32, torch.bfloat16), shape, dev)
+        _require(gamma, "gamma", torch.float32, (D,), dev)
+        if res is not None:
+            _require(res, "res", (torch.float32, torch.bfloat16), shape, dev)
+    if res is None and h is not None:
         raise ValueError("h is the sum with a residual: without one it is x")
     out_dtype = (x.dtype if out is None else out.dtype) if out_dtype is None else out_dtype
-    codes = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16, torch.float8_e4m3fn: DTYPE_E4M3}
-    if out_dtype not in codes:
+    code = codes.get(out_dtype)
+    if code is None:
         raise TypeError(f"out_dtype must be float32, bfloat16 or float8_e4m3fn, got {out_dtype}")
-    q8 = out_dtype is torch.float8_e4m3fn
+    q8 = code == DTYPE_E4M3
     if scale is not None and not q8:
         raise ValueError("scale is an output for float8_e4m3fn only")
-    if q8 and group not in (0, D) and (group != 128 or D % 128):
-        raise ValueError(f"group must be 0 (a row), or 128 if D is a multiple of it: got {group} for D = {D}")
-    if not q8 and group:
-        raise ValueError("group is for float8_e4m3fn only")
+    if group:
+        if not q8:
+            raise ValueError("group is for float8_e4m3fn only")
+        if group != D and (group != 128 or D % 128):
+            raise ValueError(f"group must be 0 (a row), or 128 if D is a multiple of it: got {group} for D = {D}")
     if _elsewhere(dev, stream):
         return _there(dev, stream, m2rnn_add_norm_fwd, x, gamma, res, eps, out_dtype=out_dtype, group=group, h=h, out=out,
                       scale=scale)
-    out = _out(out, "out", out_dtype, shape, x)
+    if out is None:
+        out = torch.empty_like(x, dtype=out_dtype)
+    else:
+        _require(out, "out", out_dtype, shape, dev)
     if q8:
-        scale = _out(scale, "scale", torch.float32, (*shape[:-1], D // (group or D) if D else 0), gamma)
+        parts = (*shape[:-1], D // (group or D) if D else 0)
+        if scale is None:
+            scale = gamma.new_empty(parts)
+        else:
+            _require(scale, "scale", torch.float32, parts, dev)
     if res is not None:
-        h = _out(h, "h", res.dtype, shape, res)
+        if h is None:
+            h = torch.empty_like(res)
+        elif h is not res:
+            _require(h, "h", res.dtype, shape, dev)
     _check("m2rnn_add_norm_fwd", lib().m2rnn_add_norm_fwd(
-        rows, D, _dtype_code(x), _ptr(x), _dtype_code(x if res is None else res), _ptr(res), _ptr(gamma), float(eps),
-        _ptr(h), codes[out_dtype], int(group), _ptr(out), _ptr(scale), _stream_of(dev)))
+        rows, D, xc, x.data_ptr(), rc, _ptr(res), gamma.data_ptr(), eps, _ptr(h), code, group, out.data_ptr(), _ptr(scale),
+        _stream_of(dev)))
     return out, scale, x if res is None else h
 
 
@@ -1258,21 +1283,27 @@ def m2rnn_add_norm_bwd(h, gamma, dout, dh=None, eps: float = 1e-6, *, workspace=
 
 def _gated_inputs(v, a, alpha, beta, state, name, lens, token):
     import torch
-    if v.dim() != (2 if token else 3):
+    shape, dev = v.shape, v.device
+    if len(shape) != (2 if token else 3):
         raise ValueError("v must be [B,D]" if token else "v must be [B,T,D]")
-    B, D = v.shape[0], v.shape[-1]
-    dev = v.device
-    if dev.type != "cuda":
-        raise ValueError("inputs must be on a GPU (HIP) device")
-    _require(v, "v", (torch.float32, torch.bfloat16), v.shape, dev)
-    _require(a, "a", v.dtype, v.shape, dev)
-    _require(alpha, "alpha", torch.float32, (D,), dev)
-    _require(beta, "beta", torch.float32, (D,), dev)
-    if state is not None:
-        _require(state, name, torch.float32, (B, D), dev)
-    if lens is not None:
-        _require(lens, "lens", torch.int32, (B,), dev)
-    return B, 1 if token else v.shape[1], D, dev
+    B, D = shape[0], shape[-1]
+    f32, of = torch.float32, v.dtype
+    if not ((of is torch.bfloat16 or of is f32) and a.dtype is of and a.shape == shape and alpha.dtype is f32
+            and beta.dtype is f32 and alpha.shape == (D,) and beta.shape == (D,)
+            and (state is None or (state.dtype is f32 and state.shape == (B, D)))
+            and (lens is None or (lens.dtype is torch.int32 and lens.shape == (B,)))
+            and _all_plain(dev, v, a, alpha, beta, state, lens)):
+        if dev.type != "cuda":
+            raise ValueError("inputs must be on a GPU (HIP) device")
+        _require(v, "v", (f32, torch.bfloat16), shape, dev)
+        _require(a, "a", of, shape, dev)
+        _require(alpha, "alpha", f32, (D,), dev)
+        _require(beta, "beta", f32, (D,), dev)
+        if state is not None:
+            _require(state, name, f32, (B, D), dev)
+        if lens is not None:
+            _require(lens, "lens", torch.int32, (B,), dev)
+    return B, 1 if token else shape[1], D, dev
 
 
 def m2rnn_gated_scan_fwd(v, a, alpha, beta, h0=None, *, lens=None, y=None, h_T=None, return_state: bool = True,
@@ -1337,9 +1368,13 @@ def m2rnn_gated_scan_step(v, a, alpha, beta, h=None, *, h_out=None, stream=None)
     B, _, D, dev = _gated_inputs(v, a, alpha, beta, h, "h", None, True)
     if _elsewhere(dev, stream):
         return _there(dev, stream, m2rnn_gated_scan_step, v, a, alpha, beta, h, h_out=h_out)
-    h_out = _out(h_out, "h_out", torch.float32, (B, D), v if h is None else h)
+    if h_out is None:
+        h_out = torch.empty_like(v if h is None else h, dtype=torch.float32)
+    elif h_out is not h:
+        _require(h_out, "h_out", torch.float32, (B, D), dev)
     _check("m2rnn_gated_scan_step", lib().m2rnn_gated_scan_step(
-        B, D, _dtype_code(v), _ptr(v), _ptr(a), _ptr(alpha), _ptr(beta), _ptr(h), _ptr(h_out), _stream_of(dev)))
+        B, D, DTYPE_BF16 if v.dtype is torch.bfloat16 else DTYPE_F32, v.data_ptr(), a.data_ptr(), alpha.data_ptr(),
+        beta.data_ptr(), _ptr(h), h_out.data_ptr(), _stream_of(dev)))
     return h_out
 
 

@@ -50,13 +50,15 @@ bool all_bf16(int x_dtype, const void* res, int res_dtype) {
   return x_dtype == M2RNN_DTYPE_BF16 && (!res || res_dtype == M2RNN_DTYPE_BF16);
 }
 
-Plan plan_norm(long rows, long D, bool bwd, bool wide) {
+// A wave takes a row of up to wave_most features, else a workgroup: 32768 rows of 2048 take 136 us by workgroups and 158 by waves
+// where x is bf16 and the stream fp32, 194 and 187 where both are fp32, 107 and 101 in the backward.
+Plan plan_norm(long rows, long D, bool bwd, bool wide, long wave_most) {
   Plan p;
   p.VEC = wide && D % 8 == 0 && D > 64 ? 8 : 4;
   if (p.VEC == 8) {
     p.LPR = D <= 128 ? 16 : D <= 512 || (rows > kNormFewRows && D <= 2048) ? 64 : 256;
   } else {
-    p.LPR = D <= 16 ? 4 : D <= 64 ? 16 : (D <= 256 || (rows > kNormFewRows && D <= 2048)) ? 64 : 256;
+    p.LPR = D <= 16 ? 4 : D <= 64 ? 16 : (D <= 256 || (rows > kNormFewRows && D <= wave_most)) ? 64 : 256;
   }
   p.NG = 1;
   while ((long)p.VEC * p.LPR * p.NG < D) p.NG *= 2;
@@ -164,7 +166,7 @@ int m2rnn_add_norm_fwd(int64_t rows, int64_t D, int x_dtype, const void* x, int 
       meet(out, no, gamma, ng) || meet(scale, ns, x, nx) || meet(scale, ns, res, nr) || meet(scale, ns, h, nr) ||
       meet(scale, ns, out, no) || meet(scale, ns, gamma, ng))
     return M2RNN_EINVAL;
-  const Plan p = plan_norm(rows, D, false, all_bf16(x_dtype, res, res_dtype));
+  const Plan p = plan_norm(rows, D, false, all_bf16(x_dtype, res, res_dtype), x_dtype == M2RNN_DTYPE_BF16 ? 1024 : 2048);
   NormArgs A{x, res, gamma, h, out, scale, rows, (int)D, (int)group, x_dtype == M2RNN_DTYPE_BF16,
              res_dtype == M2RNN_DTYPE_BF16, out_dtype == M2RNN_DTYPE_BF16, eps};
   const void* kern = p.VEC == 8 ? pick8(p, res != nullptr, q8) : pick<Fwd>(p, q8);
@@ -175,7 +177,7 @@ int m2rnn_add_norm_bwd_workspace_size(int64_t rows, int64_t D, size_t* bytes) {
   if (!bytes) return M2RNN_EINVAL;
   const int st = check_norm(rows, D, 0.0f);
   if (st) return st;
-  *bytes = round_up256((size_t)plan_norm(rows, D, true, false).groups * D * sizeof(float));
+  *bytes = round_up256((size_t)plan_norm(rows, D, true, false, 2048).groups * D * sizeof(float));
   return M2RNN_OK;
 }
 
@@ -197,7 +199,7 @@ int m2rnn_add_norm_bwd(int64_t rows, int64_t D, int h_dtype, const void* h, cons
   st = m2rnn_add_norm_bwd_workspace_size(rows, D, &need);
   if (st) return st;
   if (need > 0 && (!workspace || workspace_bytes < need || !al16(workspace))) return M2RNN_EWORKSPACE;
-  const Plan p = plan_norm(rows, D, true, false);
+  const Plan p = plan_norm(rows, D, true, false, 2048);
   hipStream_t s = (hipStream_t)stream;
   if (rows > 0) {
     NormBwdArgs A{h, gamma, dout, dh, dx, (float*)workspace, rows, (int)D, h_dtype == M2RNN_DTYPE_BF16, eps};
