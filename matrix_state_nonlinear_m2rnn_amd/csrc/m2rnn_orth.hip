@@ -38,8 +38,11 @@ struct Shape {
   int TM, TN, held;
   double stage[4];
 };
-constexpr Shape kShapes[] = {
-    {256, 256, 1, {2.2}}, {128, 128, 2, {0.95, 1.2}}, {128, 64, 3, {0.65, 0.9, 1.15}}, {64, 64, 4, {0.4, 0.52, 0.75, 1.05}}};
+constexpr Shape kShapes[] = {{256, 256, 1, {2.15}},
+                             {128, 128, 2, {0.78, 1.22}},
+                             {128, 64, 3, {0.5, 0.63, 1.08}},
+                             {64, 64, 4, {0.4, 0.45, 0.55, 0.85}},
+                             {64, 64, 2, {0.3, 0.5}}};  // five stages in LDS
 constexpr int kShapeCount = sizeof(kShapes) / sizeof(kShapes[0]);
 
 // How a product runs: its tiles, the parts of its contraction, and the time that this should take (us).
@@ -48,18 +51,10 @@ struct Cut {
   double us = 0.0;
 };
 
-// The time of `groups` workgroups of `stages` stages: whole rounds of what the CUs hold, then the rest.
-double rounds_us(const Shape& h, double groups, double stages) {
-  const double load = groups / 256.0;
-  const double full = (double)(long)(load / h.held);
-  const double rest = load - full * h.held;
-  double us = full * h.stage[h.held - 1];
-  if (rest > 0.0) {
-    const int low = rest < 1.0 ? 1 : (int)rest;
-    const double at = rest < 1.0 || low >= h.held ? 0.0 : rest - low;
-    us += h.stage[low - 1] + (at > 0.0 ? at * (h.stage[low] - h.stage[low - 1]) : 0.0);
-  }
-  return us * stages;
+// The time of `groups` workgroups of `stages` stages: whole rounds of what the CUs hold, then the fullest CU of the rest.
+double rounds_us(const Shape& h, long groups, long stages) {
+  const long load = ceil_div(groups, 256), full = load / h.held, rest = load % h.held;
+  return (full * h.stage[h.held - 1] + (rest ? h.stage[rest - 1] : 0.0)) * stages;
 }
 
 Cut cut_product(long batch, long rows, long cols, long K, bool sym) {
@@ -72,10 +67,10 @@ Cut cut_product(long batch, long rows, long cols, long K, bool sym) {
     const long tiles = sym ? gi * (gi + 1) / 2 * (h.TM / h.TN) : gi * gj;
     for (int s : {1, 2, 3, 4, 6, 8, 12, 16}) {
       if (s > stages) break;
-      const double groups = (double)tiles * batch * s;
-      if (s > 1 && groups > 256.0 * h.held) break;
-      double us = rounds_us(h, groups, (double)ceil_div(stages, s)) + 6.0;
-      if (s > 1) us += 4.0 + groups * h.TM * h.TN * 8.0 / 4e6;  // the parts written and read, one more launch
+      const long groups = tiles * batch * s;
+      if (s > 1 && groups > 256L * h.held) break;
+      double us = rounds_us(h, groups, ceil_div(stages, s)) + 6.0;
+      if (s > 1) us += 4.0 + (double)groups * h.TM * h.TN * 8.0 / 4e6;  // the parts written and read, one more launch
       if (best.us == 0.0 || us < best.us) {
         best.shape = i;
         best.splits = s;
@@ -128,13 +123,13 @@ struct Plan {
   size_t bytes() const { return part_bytes + 8 * x_bytes + 4 * a_bytes + split_bytes; }
 };
 
-template <int TM, int TN, int WR, int WC, int EPI>
+template <int TM, int TN, int WR, int WC, int BUFS, int EPI>
 int product_of(OrthArgs& A, long batch, hipStream_t s) {
   void* args[] = {&A};
   const dim3 grid((unsigned)A.tiles, (unsigned)A.splits, (unsigned)batch), block(64 * WR * WC);
-  const void* one = (const void*)&m2rnn_orth_product_kernel<TM, TN, WR, WC, EPI, false>;
+  const void* one = (const void*)&m2rnn_orth_product_kernel<TM, TN, WR, WC, BUFS, EPI, false>;
   if (A.splits == 1) return record_hip_status(hipLaunchKernel(one, grid, block, args, 0, s));
-  const void* some = (const void*)&m2rnn_orth_product_kernel<TM, TN, WR, WC, EPI, true>;
+  const void* some = (const void*)&m2rnn_orth_product_kernel<TM, TN, WR, WC, BUFS, EPI, true>;
   const int st = record_hip_status(hipLaunchKernel(some, grid, block, args, 0, s));
   if (st) return st;
   const long items = (long)A.tiles * (TM / 16) * WC;
@@ -147,10 +142,11 @@ int product(const Cut& cut, OrthArgs& A, long batch, hipStream_t s) {
   A.splits = cut.splits;
   A.tiles = cut.tiles;
   switch (cut.shape) {
-    case 0: return product_of<256, 256, 2, 4, EPI>(A, batch, s);
-    case 1: return product_of<128, 128, 2, 2, EPI>(A, batch, s);
-    case 2: return product_of<128, 64, 2, 2, EPI>(A, batch, s);
-    default: return product_of<64, 64, 2, 2, EPI>(A, batch, s);
+    case 0: return product_of<256, 256, 2, 4, 2, EPI>(A, batch, s);
+    case 1: return product_of<128, 128, 2, 2, 2, EPI>(A, batch, s);
+    case 2: return product_of<128, 64, 2, 2, 2, EPI>(A, batch, s);
+    case 3: return product_of<64, 64, 2, 2, 2, EPI>(A, batch, s);
+    default: return product_of<64, 64, 2, 2, 5, EPI>(A, batch, s);
   }
 }
 

@@ -244,16 +244,16 @@ __device__ __forceinline__ void load_to_lds(const void* from, const void* to) {
 // contraction: a column of blocks of the four planes, brought to LDS past the registers.  The three passes of a stage are
 // summed by themselves, from zero, and added to the tile's sum once: one rounding at the sum's size for each stage
 // instead of three.
-// LDS holds two stages; the next one is on its way beside the products.  (Three stages, with the barrier in the middle of one
-// and the operands read across the stages' border, ran no faster: 256 x 128 tiles 250 us where 256 x 256 take 232, 64 x 64 equal.)
-template <int TM, int TN, int WR, int WC, int EPI, bool SPLIT>
+// LDS holds BUFS stages, all but the one that is multiplied on their way.  Two where a CU holds several workgroups, or a
+// tile leaves no room for more; more for the only workgroup of a CU, whose stages would otherwise each wait for memory.
+template <int TM, int TN, int WR, int WC, int BUFS, int EPI, bool SPLIT>
 __global__ void __launch_bounds__(64 * WR * WC) m2rnn_orth_product_kernel(OrthArgs A) {
   constexpr bool SYM = EPI == ORTH_GRAM || EPI == ORTH_POLY;
   constexpr int NI = TM / WR / 16, NJ = TN / WC / 16, WAVES = WR * WC;
   constexpr int BM = TM / 16, BN = TN / 16, PER = 2 * (BM + BN) / WAVES;  // blocks of a plane's stage; those that a wave brings
   constexpr int STAGE = 8 * (TM + TN);                                    // 16-byte units
   static_assert(2 * (BM + BN) % WAVES == 0 && TM % TN == 0, "whole blocks for each wave, whole tiles on the diagonal");
-  __shared__ uint4 lds[2 * STAGE];  // [buffer][M hi, M lo, N hi, N lo][row][unit]
+  __shared__ uint4 lds[BUFS * STAGE];  // [buffer][M hi, M lo, N hi, N lo][row][unit]
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int tile = orth_turn(blockIdx.x, A.tiles);
   int bi, bj;
@@ -295,12 +295,18 @@ __global__ void __launch_bounds__(64 * WR * WC) m2rnn_orth_product_kernel(OrthAr
 #pragma unroll
   for (int j = 0; j < NJ; ++j) t[1][j] = f32x4{0, 0, 0, 0};
   static_assert(NI % 2 == 0, "the rows' operands and sums take turns");
-  fetch(0, first);
-  for (int s = first; s < last; ++s) {
-    const int buf = (s - first) & 1;
-    __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0): this wave's blocks have arrived
-    lds_barrier();                       // and all waves'; the other buffer has been read by all
-    if (s + 1 < last) fetch(buf ^ 1, s + 1);
+  static_assert((BUFS - 2) * PER < 16, "a wait's count");
+#pragma unroll
+  for (int i = 0; i < BUFS - 1; ++i)
+    if (first + i < last) fetch(i, first + i);
+  int buf = 0;
+  for (int s = first; s < last; ++s, buf = buf + 1 == BUFS ? 0 : buf + 1) {
+    if (s + BUFS - 1 <= last)
+      __builtin_amdgcn_s_waitcnt(0x0f70 | (BUFS - 2) * PER);  // this wave's blocks have arrived (vmcnt: not those of later stages)
+    else
+      __builtin_amdgcn_s_waitcnt(0x0f70);  // (fewer are on their way: all of them)
+    lds_barrier();  // and all waves'; the buffer of the stage before has been read by all
+    if (s + BUFS - 1 < last) fetch(buf == 0 ? BUFS - 1 : buf - 1, s + BUFS - 1);
     read_m(buf, 0);
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
