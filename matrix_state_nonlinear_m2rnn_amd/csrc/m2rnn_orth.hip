@@ -153,13 +153,60 @@ int product(const Cut& cut, OrthArgs& A, long batch, hipStream_t s) {
 // The kernel that takes a matrix of m x n (m <= n) through all steps in one workgroup; NULL: none does.
 const void* small_kernel(long m, long n, unsigned& threads) {
   threads = 256;
-  if (n <= 32) return (const void*)&m2rnn_orth_small_kernel<32, 32, 2, 2>;
   if (n <= 64) return (const void*)&m2rnn_orth_small_kernel<64, 64, 2, 2>;
   if (m <= 64 && n <= 128) return (const void*)&m2rnn_orth_small_kernel<64, 128, 2, 2>;
   threads = 512;
   if (n <= 128) return (const void*)&m2rnn_orth_small_kernel<128, 128, 2, 4>;
   if (m <= 64 && n <= 256) return (const void*)&m2rnn_orth_small_kernel<64, 256, 2, 4>;
   return nullptr;
+}
+
+// Thin matrices: one wave up to 64 columns, one workgroup of 8 up to 512, else tiles of 512 over up to kThinGroups of them.
+constexpr long kThinRows = 32, kThinTile = 512, kThinGroups = 64;
+struct ThinPlan {
+  long tiles, groups, parts, each;
+  size_t square_bytes, x_bytes, sum_bytes;
+  ThinPlan(int64_t batch, long m, long n) {
+    tiles = ceil_div(n, kThinTile);
+    groups = std::min(tiles, kThinGroups);
+    each = std::max(ceil_div(ceil_div(m * n, kOrthParts), 1024), 4L) * 1024;
+    parts = ceil_div(m * n, each);
+    const bool one = tiles == 1;
+    square_bytes = one ? 0 : round_up256((size_t)batch * parts * sizeof(double));
+    x_bytes = one ? 0 : (size_t)batch * tiles * kThinTile * kThinRows * 4;
+    sum_bytes = one ? 0 : (size_t)2 * batch * groups * kThinRows * kThinRows * 4;
+  }
+  size_t bytes() const { return square_bytes + x_bytes + sum_bytes; }
+};
+
+template <int M>
+int thin_all(ThinArgs& A, OrthCoefs& c, int64_t batch, hipStream_t s) {
+  void* args[] = {&A, &c};
+  const void* kern = A.n <= 64 ? (const void*)&m2rnn_orth_thin_kernel<M, 1, THIN_ALL> : (const void*)&m2rnn_orth_thin_kernel<M, 8, THIN_ALL>;
+  return record_hip_status(hipLaunchKernel(kern, dim3(1, (unsigned)batch), dim3(A.n <= 64 ? 64 : 512), args, 0, s));
+}
+
+template <int M>
+int thin_steps(ThinArgs& A, OrthCoefs& c, const ThinPlan& p, int64_t batch, hipStream_t s) {
+  void* args[] = {&A, &c};
+  const dim3 grid((unsigned)p.groups, (unsigned)batch);
+  int st = record_hip_status(hipLaunchKernel((const void*)&m2rnn_orth_thin_kernel<M, 8, THIN_FIRST>, grid, dim3(512), args, 0, s));
+  for (int i = 0; i < A.steps && !st; ++i) {
+    A.turn ^= 1;
+    A.ca = c.c[3 * i];
+    A.cb = c.c[3 * i + 1];
+    A.cc = c.c[3 * i + 2];
+    const void* kern = i + 1 < A.steps ? (const void*)&m2rnn_orth_thin_kernel<M, 8, THIN_MIDDLE>
+                                       : (const void*)&m2rnn_orth_thin_kernel<M, 8, THIN_LAST>;
+    st = record_hip_status(hipLaunchKernel(kern, grid, dim3(512), args, 0, s));
+  }
+  return st;
+}
+
+template <bool BF16>
+int squares(const void* g, long mn, long each, long parts, int64_t batch, double* part, hipStream_t s) {
+  hipLaunchKernelGGL(m2rnn_orth_squares_kernel<BF16>, dim3((unsigned)parts, (unsigned)batch), dim3(256), 0, s, g, mn, each, part);
+  return record_hip_status(hipGetLastError());
 }
 
 }  // namespace
@@ -170,9 +217,14 @@ int m2rnn_orthogonalize_workspace_size(int64_t batch, int64_t m, int64_t n, int 
   if (!bytes) return M2RNN_EINVAL;
   const int st = check_orth(batch, m, n, dtype);
   if (st) return st;
+  *bytes = 0;
+  if (batch == 0 || m == 0 || n == 0) return M2RNN_OK;
+  const long lo = std::min(m, n), hi = std::max(m, n);
   unsigned threads;
-  const bool small = small_kernel(std::min(m, n), std::max(m, n), threads) != nullptr;
-  *bytes = batch > 0 && m > 0 && n > 0 && !small ? Plan(batch, m, n).bytes() : 0;
+  if (lo <= kThinRows)
+    *bytes = ThinPlan(batch, lo, hi).bytes();
+  else if (!small_kernel(lo, hi, threads))
+    *bytes = Plan(batch, m, n).bytes();
   return M2RNN_OK;
 }
 
@@ -186,11 +238,36 @@ int m2rnn_orthogonalize(int64_t batch, int64_t m, int64_t n, int dtype, const vo
   const bool bf16 = dtype == M2RNN_DTYPE_BF16;
   const uintptr_t size = (uintptr_t)(batch * m * n * (bf16 ? 2 : 4)), x = (uintptr_t)g, y = (uintptr_t)out;
   if (x != y && x < y + size && y < x + size) return M2RNN_EINVAL;
+  OrthCoefs c{};
+  std::copy(coefs, coefs + 3 * steps, c.c);
+  int lo = (int)std::min(m, n), hi = (int)std::max(m, n), turned = m > n, half = bf16, count = (int)steps;
+  if (lo <= kThinRows) {
+    const ThinPlan p(batch, lo, hi);
+    if (p.bytes() > 0 && (!workspace || workspace_bytes < p.bytes() || !al16(workspace))) return M2RNN_EWORKSPACE;
+    hipStream_t s = (hipStream_t)stream;
+    char* at = (char*)workspace;
+    ThinArgs A{};
+    A.g = g;
+    A.out = out;
+    A.squares = (const double*)at;
+    A.X = (float*)(at + p.square_bytes);
+    A.part = (float*)(at + p.square_bytes + p.x_bytes);
+    A.m = lo;
+    A.n = hi;
+    A.tall = turned;
+    A.bf16 = half;
+    A.tiles = (int)p.tiles;
+    A.parts = (int)p.parts;
+    A.steps = count;
+    A.eps = eps;
+    if (p.tiles == 1) return lo <= 16 ? thin_all<16>(A, c, batch, s) : thin_all<32>(A, c, batch, s);
+    st = bf16 ? squares<true>(g, (long)m * n, p.each, p.parts, batch, (double*)at, s)
+              : squares<false>(g, (long)m * n, p.each, p.parts, batch, (double*)at, s);
+    if (st) return st;
+    return lo <= 16 ? thin_steps<16>(A, c, p, batch, s) : thin_steps<32>(A, c, p, batch, s);
+  }
   unsigned threads;
-  if (const void* small = small_kernel(std::min(m, n), std::max(m, n), threads)) {
-    OrthCoefs c{};
-    std::copy(coefs, coefs + 3 * steps, c.c);
-    int lo = (int)std::min(m, n), hi = (int)std::max(m, n), turned = m > n, half = bf16, count = (int)steps;
+  if (const void* small = small_kernel(lo, hi, threads)) {
     void* args[] = {&g, &out, &lo, &hi, &turned, &half, &count, &c, &eps};
     return record_hip_status(hipLaunchKernel(small, dim3((unsigned)batch), dim3(threads), args, 0, (hipStream_t)stream));
   }
@@ -211,35 +288,36 @@ int m2rnn_orthogonalize(int64_t batch, int64_t m, int64_t n, int dtype, const vo
   Planes XT = planes(p.x_bytes), YT = planes(p.x_bytes);
   const Planes P = planes(p.a_bytes), Q = planes(p.a_bytes);
   const int tall = m > n;
-  const dim3 parts((unsigned)p.parts, (unsigned)batch);
   const dim3 split((unsigned)(p.np / 64), (unsigned)(p.mp / 64), (unsigned)batch);
   if (bf16) {
-    hipLaunchKernelGGL(m2rnn_orth_squares_kernel<true>, parts, dim3(256), 0, s, g, p.m * p.n, p.each, part);
+    st = squares<true>(g, p.m * p.n, p.each, p.parts, batch, part, s);
+    if (st) return st;
     hipLaunchKernelGGL(m2rnn_orth_split_kernel<true>, split, dim3(256), 0, s, g, (int)p.m, (int)p.n, (int)p.mp, (int)p.np,
                        tall, (const double*)part, (int)p.parts, eps, X32, X, XT);
   } else {
-    hipLaunchKernelGGL(m2rnn_orth_squares_kernel<false>, parts, dim3(256), 0, s, g, p.m * p.n, p.each, part);
+    st = squares<false>(g, p.m * p.n, p.each, p.parts, batch, part, s);
+    if (st) return st;
     hipLaunchKernelGGL(m2rnn_orth_split_kernel<false>, split, dim3(256), 0, s, g, (int)p.m, (int)p.n, (int)p.mp, (int)p.np,
                        tall, (const double*)part, (int)p.parts, eps, X32, X, XT);
   }
   st = record_hip_status(hipGetLastError());
   for (int64_t i = 0; i < steps && !st; ++i) {
-    const float* c = coefs + 3 * i;
+    const float *f = c.c + 3 * i;
     OrthArgs A{};
     A.part = (float*)at;
-    const bool cubic = c[2] == 0.0f;  // B = b A
+    const bool cubic = f[2] == 0.0f;  // B = b A
     A.M = A.N = X;
     A.O = A.OT = cubic ? Q : P;
     A.rows = A.cols = (int)p.mp;
     A.K = (int)p.np;
-    A.cb = cubic ? c[1] * kOrthB : kOrthA;
+    A.cb = cubic ? f[1] * kOrthB : kOrthA;
     st = product<ORTH_GRAM>(p.gram, A, batch, s);
     if (!st && !cubic) {
       A.M = A.N = A.E = P;
       A.O = A.OT = Q;
       A.K = (int)p.mp;
-      A.cb = c[1];
-      A.cc = c[2];
+      A.cb = f[1];
+      A.cc = f[2];
       st = product<ORTH_POLY>(p.poly, A, batch, s);
     }
     if (st) break;
@@ -250,7 +328,7 @@ int m2rnn_orthogonalize(int64_t batch, int64_t m, int64_t n, int dtype, const vo
     A.O = X;
     A.OT = YT;
     A.cols = (int)p.np;
-    A.ca = c[0];
+    A.ca = f[0];
     A.out = out;
     A.m = (int)p.m;
     A.n = (int)p.n;

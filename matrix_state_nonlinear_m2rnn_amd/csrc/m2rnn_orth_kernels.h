@@ -550,4 +550,234 @@ __global__ void __launch_bounds__(64 * WR * WC) m2rnn_orth_small_kernel(const vo
       }
 }
 
+// Thin matrices (the shorter side at most 32): the fp32 MFMA, whose rate no longer matters, and no splitting: with few rows the
+// 22 bits of split values would show (a single row of 100: 1.5e-6 off where fp32 products are 6e-7).
+//
+// A wave holds M rows (16 or 32) by 64 columns of X in accumulator order: lane (h, i) has row i, and in register r of
+// each M columns column thin_col(r, h).  That is an operand of X X^T over those columns, in some order that is the same on
+// both sides.  A comes out in the same order and is symmetric, so its registers are operands of A A, and B's of
+// (B X)^T = X^T B, whose other operand, X by columns, comes from LDS; the result has X's order again.
+template <int M>
+struct Thin {
+  static constexpr int H = 64 / M, NR = M * M / 64, NC = 64 / M;  // lanes of a row; registers of M columns; those of a wave
+  static constexpr int ST = 68;                                   // floats between rows in LDS
+  typedef float acc_t __attribute__((ext_vector_type(NR)));
+  static __device__ __forceinline__ acc_t mfma(float a, float b, acc_t c) {
+    if constexpr (M == 32)
+      return __builtin_amdgcn_mfma_f32_32x32x2f32(a, b, c, 0, 0, 0);
+    else
+      return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0);
+  }
+  static __device__ __forceinline__ acc_t zero() {
+    acc_t z;
+#pragma unroll
+    for (int r = 0; r < NR; ++r) z[r] = 0.0f;
+    return z;
+  }
+  static __device__ __forceinline__ int col(int r, int h) { return 4 * H * (r / 4) + 4 * h + r % 4; }
+};
+
+struct ThinArgs {
+  const void* g;
+  void* out;
+  float* X;              // several workgroups: X, [batch][tiles][waves] in the waves' order
+  float* part;           // and the partial sums of A, [2][batch][workgroups][lane][NR], the halves in turn
+  const double* squares; // and the partial sums of squares [batch][parts]
+  int m, n, tall, bf16;  // m x n with m the shorter side; g and out are its transpose if tall
+  int tiles, parts, steps;
+  float eps, ca, cb, cc;
+  int turn;
+};
+
+enum { THIN_ALL = 0, THIN_FIRST = 1, THIN_MIDDLE = 2, THIN_LAST = 3 };
+
+// THIN_ALL: one workgroup takes a matrix of up to 64 WAVES columns through all steps.  The others: a step's launch, where a
+// workgroup takes every gridDim.x-th tile of 64 WAVES columns: FIRST forms X_0 and its A, MIDDLE applies the step that the
+// last launch's A gives and sums the next A, LAST applies the last one.
+template <int M, int WAVES, int MODE>
+__global__ void __launch_bounds__(64 * WAVES) m2rnn_orth_thin_kernel(ThinArgs A, OrthCoefs coefs) {
+  typedef Thin<M> T;
+  constexpr int NR = T::NR, NC = T::NC, H = T::H;
+  __shared__ float xs[WAVES][M * T::ST];
+  __shared__ float4 sums[WAVES][NR / 4][64];
+  __shared__ double red[WAVES];
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int i = lane % M, h = lane / M;
+  const long z = blockIdx.y;
+  const long at = z * A.m * A.n;
+  float x[NC][NR];
+  auto place = [&](int tile, int ch, int r) { return (tile * WAVES + w) * 64 + ch * M + T::col(r, h); };  // the column
+  auto where = [&](int c) { return at + (A.tall ? (long)c * A.m + i : (long)i * A.n + c); };
+  auto load_g = [&](int tile) {
+#pragma unroll
+    for (int ch = 0; ch < NC; ++ch)
+#pragma unroll
+      for (int r = 0; r < NR; ++r) {
+        const int c = place(tile, ch, r);
+        x[ch][r] = 0.0f;
+        if (i < A.m && c < A.n) x[ch][r] = A.bf16 ? load1<true>(A.g, where(c)) : load1<false>(A.g, where(c));
+      }
+  };
+  auto store_out = [&](int tile) {
+#pragma unroll
+    for (int ch = 0; ch < NC; ++ch)
+#pragma unroll
+      for (int r = 0; r < NR; ++r) {
+        const int c = place(tile, ch, r);
+        if (i < A.m && c < A.n) {
+          if (A.bf16)
+            ((__bf16*)A.out)[where(c)] = (__bf16)x[ch][r];
+          else
+            ((float*)A.out)[where(c)] = x[ch][r];
+        }
+      }
+  };
+  auto kept = [&](int tile) { return (float4*)A.X + ((z * A.tiles + tile) * WAVES + w) * (NC * NR / 4 * 64) + lane; };
+  auto scale_by = [&](double f) {
+#pragma unroll
+    for (int ch = 0; ch < NC; ++ch)
+#pragma unroll
+      for (int r = 0; r < NR; ++r) x[ch][r] = (float)((double)x[ch][r] * f);
+  };
+  auto add_gram = [&](typename T::acc_t a) {
+#pragma unroll
+    for (int ch = 0; ch < NC; ++ch)
+#pragma unroll
+      for (int r = 0; r < NR; ++r) a = T::mfma(x[ch][r], x[ch][r], a);
+    return a;
+  };
+  // the waves' a added, in each of them
+  auto over_waves = [&](typename T::acc_t a) {
+    if constexpr (WAVES == 1) return a;
+    __syncthreads();  // the sums of the time before have been read
+#pragma unroll
+    for (int q = 0; q < NR / 4; ++q) sums[w][q][lane] = make_float4(a[4 * q], a[4 * q + 1], a[4 * q + 2], a[4 * q + 3]);
+    __syncthreads();
+    a = T::zero();
+#pragma unroll
+    for (int v = 0; v < WAVES; ++v)
+#pragma unroll
+      for (int q = 0; q < NR / 4; ++q) {
+        const float4 t = sums[v][q][lane];
+        a[4 * q] += t.x;
+        a[4 * q + 1] += t.y;
+        a[4 * q + 2] += t.z;
+        a[4 * q + 3] += t.w;
+      }
+    return a;
+  };
+  auto poly = [&](typename T::acc_t a, float b, float c) {
+    typename T::acc_t sq = T::zero();
+#pragma unroll
+    for (int r = 0; r < NR; ++r) sq = T::mfma(a[r], a[r], sq);
+#pragma unroll
+    for (int r = 0; r < NR; ++r) a[r] = c == 0.0f ? b * a[r] : __builtin_fmaf(b, a[r], c * sq[r]);
+    return a;
+  };
+  auto apply = [&](typename T::acc_t B, float ca) {
+    float* mine = xs[w];
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
+    __builtin_amdgcn_wave_barrier();  // the wave's reads of the time before
+#pragma unroll
+    for (int ch = 0; ch < NC; ++ch)
+#pragma unroll
+      for (int r = 0; r < NR; r += 4)
+        *(float4*)(mine + i * T::ST + ch * M + T::col(r, h)) =
+            make_float4(x[ch][r], x[ch][r + 1], x[ch][r + 2], x[ch][r + 3]);
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int ch = 0; ch < NC; ++ch) {
+      typename T::acc_t y = T::zero();
+#pragma unroll
+      for (int r = 0; r < NR; ++r) y = T::mfma(mine[T::col(r, h) * T::ST + ch * M + i], B[r], y);
+#pragma unroll
+      for (int r = 0; r < NR; ++r) x[ch][r] = __builtin_fmaf(ca, x[ch][r], y[r]);
+    }
+  };
+  if constexpr (MODE == THIN_ALL) {
+    load_g(0);
+    double ss = 0.0;
+#pragma unroll
+    for (int ch = 0; ch < NC; ++ch)
+#pragma unroll
+      for (int r = 0; r < NR; ++r) ss += (double)x[ch][r] * (double)x[ch][r];
+    ss = wave_sum(ss);
+    if (lane == 0) red[w] = ss;
+    __syncthreads();
+    ss = 0.0;
+#pragma unroll
+    for (int v = 0; v < WAVES; ++v) ss += red[v];
+    scale_by(1.0 / (sqrt(ss) + (double)A.eps));
+    for (int s = 0; s < A.steps; ++s)
+      apply(poly(over_waves(add_gram(T::zero())), coefs.c[3 * s + 1], coefs.c[3 * s + 2]), coefs.c[3 * s]);
+    store_out(0);
+  } else {
+    const long half = (long)gridDim.y * gridDim.x * 64 * NR;
+    typename T::acc_t a = T::zero(), B = T::zero();
+    double f = 0.0;
+    if constexpr (MODE == THIN_FIRST) {
+      for (int k = lane; k < A.parts; k += 64) f += A.squares[z * A.parts + k];
+      f = 1.0 / (sqrt(wave_sum(f)) + (double)A.eps);
+    } else {
+      // the last launch's sums of A: a wave takes every WAVES-th, in fp64
+      double t[NR];
+#pragma unroll
+      for (int r = 0; r < NR; ++r) t[r] = 0.0;
+      const float4* p = (const float4*)(A.part + (A.turn ^ 1) * half) + z * gridDim.x * (16 * NR) + lane * (NR / 4);
+      for (int k = w; k < (int)gridDim.x; k += WAVES)
+#pragma unroll
+        for (int q = 0; q < NR / 4; ++q) {
+          const float4 v = p[k * (16 * NR) + q];
+          t[4 * q] += (double)v.x;
+          t[4 * q + 1] += (double)v.y;
+          t[4 * q + 2] += (double)v.z;
+          t[4 * q + 3] += (double)v.w;
+        }
+#pragma unroll
+      for (int r = 0; r < NR; ++r) a[r] = (float)t[r];
+      B = poly(over_waves(a), A.cb, A.cc);
+      a = T::zero();
+    }
+    for (int tile = blockIdx.x; tile < A.tiles; tile += gridDim.x) {
+      if constexpr (MODE == THIN_FIRST) {
+        load_g(tile);
+        scale_by(f);
+      } else {
+        const float4* src = kept(tile);
+#pragma unroll
+        for (int ch = 0; ch < NC; ++ch)
+#pragma unroll
+          for (int q = 0; q < NR / 4; ++q) {
+            const float4 v = src[(ch * (NR / 4) + q) * 64];
+            x[ch][4 * q] = v.x;
+            x[ch][4 * q + 1] = v.y;
+            x[ch][4 * q + 2] = v.z;
+            x[ch][4 * q + 3] = v.w;
+          }
+        apply(B, A.ca);
+      }
+      if constexpr (MODE == THIN_LAST) {
+        store_out(tile);
+      } else {
+        a = add_gram(a);
+        float4* dst = kept(tile);
+#pragma unroll
+        for (int ch = 0; ch < NC; ++ch)
+#pragma unroll
+          for (int q = 0; q < NR / 4; ++q)
+            dst[(ch * (NR / 4) + q) * 64] = make_float4(x[ch][4 * q], x[ch][4 * q + 1], x[ch][4 * q + 2], x[ch][4 * q + 3]);
+      }
+    }
+    if constexpr (MODE != THIN_LAST) {
+      a = over_waves(a);
+      if (w == 0) {
+        float4* p = (float4*)(A.part + A.turn * half) + (z * gridDim.x + blockIdx.x) * (16 * NR) + lane * (NR / 4);
+#pragma unroll
+        for (int q = 0; q < NR / 4; ++q) p[q] = make_float4(a[4 * q], a[4 * q + 1], a[4 * q + 2], a[4 * q + 3]);
+      }
+    }
+  }
+}
+
 }  // namespace m2rnn

@@ -51,7 +51,8 @@ def check(g, out, steps=5, coefs=COEFS, eps=1e-7):
 
 @pytest.mark.parametrize("dtype", ["fp32", "bf16"])
 @pytest.mark.parametrize("batch,m,n", [(1, 1, 1), (2, 1, 7), (3, 16, 16), (5, 33, 17), (2, 64, 64), (3, 63, 65), (1, 64, 130),
-                                       (2, 128, 128), (1, 129, 515), (2, 300, 100), (1, 256, 1000), (1, 513, 400), (1, 1, 5000)])
+                                       (2, 128, 128), (1, 129, 515), (2, 300, 100), (1, 256, 1000), (1, 513, 400), (1, 1, 5000), (2, 16, 513),
+                                       (1, 2000, 32), (3, 17, 700), (2, 3, 512), (1, 5, 40000)])
 def test_against_the_oracle(batch, m, n, dtype):
     torch = torch_cuda()
     import matrix_state_nonlinear_m2rnn_amd as m2
@@ -65,7 +66,7 @@ def test_against_the_oracle(batch, m, n, dtype):
     assert m2.m2rnn_orthogonalize(g, out=g) is g and torch.equal(g, out)
 
 
-@pytest.mark.parametrize("m,n", [(16, 16), (64, 48), (40, 200), (128, 96), (140, 300)])
+@pytest.mark.parametrize("m,n", [(16, 16), (12, 600), (64, 48), (40, 200), (128, 96), (140, 300)])
 def test_steps_and_coefficients(m, n):
     torch = torch_cuda()
     import matrix_state_nonlinear_m2rnn_amd as m2
@@ -81,7 +82,7 @@ def test_steps_and_coefficients(m, n):
     assert torch.equal(m2.m2rnn_orthogonalize(g.view(1, 2, m, n)), a.view(1, 2, m, n))
 
 
-@pytest.mark.parametrize("m,n", [(24, 40), (64, 64), (150, 90)])
+@pytest.mark.parametrize("m,n", [(24, 40), (700, 8), (64, 64), (150, 90)])
 def test_scales_and_values_that_are_not_finite(m, n):
     """Any scale of the gradient gives the same result; zeros give zeros; one matrix that is not finite leaves the
     others of the batch their bits."""
