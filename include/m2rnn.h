@@ -556,7 +556,7 @@ int m2rnn_add_norm_bwd(int64_t rows, int64_t D, int h_dtype, const void* h, cons
  *              computed as given); h0, h_T [B,D] fp32 (NULL: zeros; not written); y [B,T,D] fp32.
  *   lens       [B] int32 device array or NULL, as in m2rnn_ssm_fwd: steps at or past a sequence's end change
  *              nothing, their y and gradients are zeros, whatever v and a hold there.  h_T is the state after the
- *              last step within.  T = 0: h_T = h0.
+ *              last step within (that step's y, bit for bit).  T = 0: h_T = h0.
  *   D a multiple of 4 up to 2^24, T at most 2^30, B D at most 2^35, and ceil(B D / 256) ceil(T / 32) below 2^23.
  *   Pointers 16-byte aligned (lens 4).
  * fp32 arithmetic; 1 - f is formed without cancellation.  A step whose 1 - f is zero (a = -infinity or the lowest

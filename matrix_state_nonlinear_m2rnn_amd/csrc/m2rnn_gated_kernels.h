@@ -166,10 +166,10 @@ __device__ __forceinline__ void gated_place(const GatedArgs& A, GatedJoin& J, lo
 }
 
 // The states that enter the waves' steps to J.l, from the waves' maps (BACK: the last wave's steps are the first).
-// Waves 0 to 3 take a channel each; the state behind the last chunk goes to `last`.
+// Waves 0 to 3 take a channel each.
 template <bool BACK>
 __device__ __forceinline__ void gated_enter(const GatedArgs& A, GatedJoin& J, long order, long block, int lane, int w,
-                                            const GatedLane& L, const float* first, float* last) {
+                                            const GatedLane& L, const float* first) {
   if (w < 4) {
     float x = 0.0f, sum = 0.0f;
 #pragma unroll
@@ -216,7 +216,6 @@ __device__ __forceinline__ void gated_enter(const GatedArgs& A, GatedJoin& J, lo
           h = Decay{__uint_as_float((uint32_t)(word[j] >> 32))}(h) + __uint_as_float((uint32_t)word[j]);
     }
     if (group_end && !end) gated_put(A.entry + (group + 1) * row + at + lane, gated_word(0.0f, all(h) + sum));
-    if (end && last && L.on) last[L.col + w] = all(h) + sum;
 #pragma unroll
     for (int j = 0; j < kGatedWaves; ++j) {
       const int k = BACK ? kGatedWaves - 1 - j : j;
@@ -274,7 +273,7 @@ __global__ void __launch_bounds__(64 * kGatedWaves, 4) m2rnn_gated_fwd_kernel(Ga
     J.l[w][e][lane] = l[e];
   }
   __syncthreads();
-  gated_enter<false>(A, J, chunk, block, lane, w, L, A.h0, A.h_T);
+  gated_enter<false>(A, J, chunk, block, lane, w, L, A.h0);
   if (!L.on) return;
   float h[4];
 #pragma unroll
@@ -290,6 +289,9 @@ __global__ void __launch_bounds__(64 * kGatedWaves, 4) m2rnn_gated_fwd_kernel(Ga
     }
     if (t < A.T) store4_nt<false>(A.y, L.base + t * A.D, o);
   }
+  // the wave with the sequence's last step (its first ones, if it has none) has the state behind it: later steps hold it
+  const int end = L.len > 0 ? L.len - 1 : 0;
+  if (A.h_T && end >= t0 && end < t0 + NS) store4<false>(A.h_T, L.col, make_float4(h[0], h[1], h[2], h[3]));
 }
 
 template <bool BF16>
@@ -341,7 +343,7 @@ __global__ void __launch_bounds__(64 * kGatedWaves, 4) m2rnn_gated_bwd_kernel(Ga
     J.l[w][e][lane] = l[e];
   }
   __syncthreads();
-  gated_enter<true>(A, J, order, block, lane, w, L, A.dh_T, A.dh0);
+  gated_enter<true>(A, J, order, block, lane, w, L, A.dh_T);
   float C[4], gal[4], gbe[4];
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
@@ -390,6 +392,7 @@ __global__ void __launch_bounds__(64 * kGatedWaves, 4) m2rnn_gated_bwd_kernel(Ga
         store4_nt<false>(A.da, L.base + (long)(t0 + i) * A.D, none);
       }
   }
+  if (A.dh0 && L.on && t0 == 0) store4<false>(A.dh0, L.col, make_float4(C[0], C[1], C[2], C[3]));
 #pragma unroll
   for (int e = 0; e < 4; ++e) {  // (J.x and J.c were read before the last barrier)
     J.x[w][e][lane] = gal[e];

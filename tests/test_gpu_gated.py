@@ -85,6 +85,8 @@ def test_forward_and_backward(B, T, D, dtype, lens, h0, far):
     ry, rh, before, (s, sg, f, i, z), E, Eb, e, ends = terms(*args, n)
     near(y, ry, E)
     near(hT, rh, e)
+    for b, k in enumerate(ends):  # the last step's y, bit for bit
+        assert torch.equal(hT[b], y[b, int(k) - 1] if k > 0 else hT[b] * 0 if s0 is None else s0[b])
     if lens is not None:
         for b, k in enumerate(ends):
             assert not y[b, int(k):].any()
