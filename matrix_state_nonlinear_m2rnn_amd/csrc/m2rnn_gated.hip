@@ -79,7 +79,7 @@ int launch(const void* kern, long groups, int threads, GatedArgs& A, hipStream_t
 // The sizes and the workspace of a call, and the clearing launch.
 int begin(GatedArgs& A, int64_t B, int64_t T, int64_t D, int steps, void* workspace, hipStream_t s) {
   const Layout ws(B, T, D, steps);
-  A.T = T;
+  A.T = (int)T;
   A.cols = B * D;
   A.blocks = blocks(B, D);
   A.D = (int)D;

@@ -41,8 +41,8 @@ struct GatedArgs {
   unsigned long long* maps;          // [chunks][blocks][4][64]: (P as a Decay, l) of each chunk, by channel and lane
   unsigned long long* entry;         // [groups of chunks][blocks][4][64]: the state that enters each group but the first
   unsigned* ticket;
-  long T, cols, blocks;              // cols = B D; blocks of 64 lanes of 4 channels
-  int D, chunks, group;              // chunks of a group
+  long cols, blocks;                 // cols = B D; blocks of 64 lanes of 4 channels
+  int T, D, chunks, group;           // group: chunks of a group
   // backward
   const float *yin, *dy, *dh_T;      // the forward's y; dh_T NULL: zeros
   float *dv, *da, *dh0;
@@ -86,16 +86,23 @@ __device__ __forceinline__ Decay decay_of(float x) {
   p = __builtin_fmaf(p, x, 0.166651082f);
   p = __builtin_fmaf(p, x, -0.499999515f);
   p = __builtin_fmaf(p, x, 0.999999998f);
+  // (made opaque, both sides are formed and one is chosen; the compiler would branch for each value)
+  const float near = opaque1(-x * p), far = opaque1(__builtin_amdgcn_exp2f(x * -1.4426950408889634f));
   Decay d;
-  d.c = __float_as_uint(x) < __float_as_uint(0.25f) ? -x * p : __builtin_amdgcn_exp2f(x * -1.4426950408889634f);
+  d.c = __float_as_uint(x) < __float_as_uint(0.25f) ? near : far;
   return d;
 }
 
-// Four neighbouring channels of step t (read at t clamped into the tensor).
+// Four neighbouring channels of an array of fp32 or bf16.
 template <bool BF16>
 __device__ __forceinline__ void gated_load(const void* p, long at, float (&o)[4]) {
   const float4 t = load4<BF16>(p, at);
   o[0] = t.x; o[1] = t.y; o[2] = t.z; o[3] = t.w;
+}
+// An array as a lane sees it: its own first element, so that a step's offset is the same in all lanes (and stays scalar).
+template <bool BF16>
+__device__ __forceinline__ const void* lane_base(const void* p, long base) {
+  return (const char*)p + base * (BF16 ? 2 : 4);
 }
 
 // x y, and 0 where either is 0, whatever the other is.
@@ -121,9 +128,9 @@ __device__ __forceinline__ GatedLane gated_lane(const GatedArgs& A, long block) 
   const long b = L.col / A.D;
   L.d = (int)(L.col % A.D);
   L.base = b * A.T * A.D + L.d;
-  long n = A.lens ? (long)A.lens[b] : A.T;
+  int n = A.lens ? A.lens[b] : A.T;
   n = n < 0 ? 0 : n > A.T ? A.T : n;
-  L.len = L.on ? (int)n : 0;
+  L.len = L.on ? n : 0;
   return L;
 }
 
@@ -154,7 +161,7 @@ __device__ __forceinline__ unsigned long long gated_get(const unsigned long long
 }
 
 // The chunk of a workgroup in the order of the recurrence (0: first; the backward's first is the last in time), and its block.
-__device__ __forceinline__ void gated_place(const GatedArgs& A, GatedJoin& J, long& order, long& block) {
+__device__ __forceinline__ bool gated_place(const GatedArgs& A, GatedJoin& J, long& order, long& block) {
   long id = blockIdx.x;
   if (A.chunks > 1) {
     if (threadIdx.x == 0) J.ticket = atomicAdd(A.ticket, 1u);
@@ -163,6 +170,7 @@ __device__ __forceinline__ void gated_place(const GatedArgs& A, GatedJoin& J, lo
   }
   order = id / A.blocks;
   block = id % A.blocks;
+  return order < A.chunks;  // (always, unless two calls share a workspace at once)
 }
 
 // The states that enter the waves' steps to J.l, from the waves' maps (BACK: the last wave's steps are the first).
@@ -233,7 +241,7 @@ __global__ void __launch_bounds__(64 * kGatedWaves, 4) m2rnn_gated_fwd_kernel(Ga
   __shared__ GatedJoin J;
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   long chunk, block;
-  gated_place(A, J, chunk, block);
+  if (!gated_place(A, J, chunk, block)) return;
   const GatedLane L = gated_lane(A, block);
   const int t0 = ((int)chunk * kGatedWaves + w) * NS;
   Decay dec[NS][4];
@@ -245,9 +253,9 @@ __global__ void __launch_bounds__(64 * kGatedWaves, 4) m2rnn_gated_fwd_kernel(Ga
     float va[NS][4], al[4], be[4];
 #pragma unroll
     for (int i = 0; i < NS; ++i) {
-      const long t = t0 + i < A.T ? t0 + i : A.T - 1;
-      gated_load<BF16>(A.a, L.base + t * A.D, va[i]);
-      gated_load<BF16>(A.v, L.base + t * A.D, b[i]);
+      const long at = (long)(t0 + i < A.T ? t0 + i : A.T - 1) * A.D;
+      gated_load<BF16>(lane_base<BF16>(A.a, L.base), at, va[i]);
+      gated_load<BF16>(lane_base<BF16>(A.v, L.base), at, b[i]);
     }
     gated_load<false>(A.alpha, L.d, al);
     gated_load<false>(A.beta, L.d, be);
@@ -258,7 +266,7 @@ __global__ void __launch_bounds__(64 * kGatedWaves, 4) m2rnn_gated_fwd_kernel(Ga
       for (int e = 0; e < 4; ++e) {
         float sg;
         const float s = gated_softplus<false>(va[i][e] + be[e], sg);
-        const float x = live ? al[e] * s : 0.0f;
+        const float xs = opaque1(al[e] * s), x = live ? xs : 0.0f;  // (opaque: no branch)
         dec[i][e] = decay_of(x);
         b[i][e] = mul_or_0(dec[i][e].i(), b[i][e]);  // (0 times anything is 0)
         sum[e] += x;
@@ -280,14 +288,14 @@ __global__ void __launch_bounds__(64 * kGatedWaves, 4) m2rnn_gated_fwd_kernel(Ga
   for (int e = 0; e < 4; ++e) h[e] = J.l[w][e][lane];
 #pragma unroll
   for (int i = 0; i < NS; ++i) {
-    const long t = t0 + i;
+    const int t = t0 + i;
     float o[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       if (some) h[e] = dec[i][e](h[e]) + b[i][e];
-      o[e] = t0 + i < L.len ? h[e] : 0.0f;
+      o[e] = t < L.len ? h[e] : 0.0f;
     }
-    if (t < A.T) store4_nt<false>(A.y, L.base + t * A.D, o);
+    if (t < A.T) store4_nt<false>((void*)lane_base<false>(A.y, L.base), (long)t * A.D, o);
   }
   // the wave with the sequence's last step (its first ones, if it has none) has the state behind it: later steps hold it
   const int end = L.len > 0 ? L.len - 1 : 0;
@@ -300,7 +308,7 @@ __global__ void __launch_bounds__(64 * kGatedWaves, 4) m2rnn_gated_bwd_kernel(Ga
   __shared__ GatedJoin J;
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   long order, block;
-  gated_place(A, J, order, block);
+  if (!gated_place(A, J, order, block)) return;
   const long chunk = A.chunks - 1 - order;
   const GatedLane L = gated_lane(A, block);
   const int t0 = ((int)chunk * kGatedWaves + w) * NS;
@@ -314,9 +322,9 @@ __global__ void __launch_bounds__(64 * kGatedWaves, 4) m2rnn_gated_bwd_kernel(Ga
     float be[4];
 #pragma unroll
     for (int i = 0; i < NS; ++i) {
-      const long t = t0 + i < A.T ? t0 + i : A.T - 1;
-      gated_load<BF16>(A.a, L.base + t * A.D, s[i]);
-      gated_load<false>(A.dy, L.base + t * A.D, u[i]);
+      const long at = (long)(t0 + i < A.T ? t0 + i : A.T - 1) * A.D;
+      gated_load<BF16>(lane_base<BF16>(A.a, L.base), at, s[i]);
+      gated_load<false>(lane_base<false>(A.dy, L.base), at, u[i]);
     }
     gated_load<false>(A.alpha, L.d, al);
     gated_load<false>(A.beta, L.d, be);
@@ -325,11 +333,13 @@ __global__ void __launch_bounds__(64 * kGatedWaves, 4) m2rnn_gated_bwd_kernel(Ga
       const bool live = t0 + i < L.len;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        s[i][e] = gated_softplus<true>(s[i][e] + be[e], sg[i][e]);
-        s[i][e] = live ? s[i][e] : 0.0f;
-        sg[i][e] = live ? sg[i][e] : 0.0f;
+        float g;
+        const float p = opaque1(gated_softplus<true>(s[i][e] + be[e], g));  // (opaque: no branch)
+        g = opaque1(g);
+        s[i][e] = live ? p : 0.0f;
+        sg[i][e] = live ? g : 0.0f;
         u[i][e] = live ? u[i][e] : 0.0f;
-        const float x = live ? al[e] * s[i][e] : 0.0f;
+        const float xs = opaque1(al[e] * p), x = live ? xs : 0.0f;
         dec[i][e] = decay_of(x);
         sum[e] += x;
         l[e] = dec[i][e](l[e] + u[i][e]);
@@ -354,10 +364,10 @@ __global__ void __launch_bounds__(64 * kGatedWaves, 4) m2rnn_gated_bwd_kernel(Ga
     float v[NS][4], hb[NS][4];
 #pragma unroll
     for (int i = 0; i < NS; ++i) {
-      const long t = t0 + i < A.T ? t0 + i : A.T - 1;
-      gated_load<BF16>(A.v, L.base + t * A.D, v[i]);
+      const int t = t0 + i < A.T ? t0 + i : A.T - 1;
+      gated_load<BF16>(lane_base<BF16>(A.v, L.base), (long)t * A.D, v[i]);
       if (t > 0) {
-        gated_load<false>(A.yin, L.base + (t - 1) * A.D, hb[i]);
+        gated_load<false>(lane_base<false>(A.yin, L.base), (long)(t - 1) * A.D, hb[i]);
       } else if (A.h0) {
         gated_load<false>(A.h0, L.col, hb[i]);
       } else {
@@ -367,7 +377,7 @@ __global__ void __launch_bounds__(64 * kGatedWaves, 4) m2rnn_gated_bwd_kernel(Ga
     }
 #pragma unroll
     for (int i = NS - 1; i >= 0; --i) {
-      const long t = t0 + i;
+      const int t = t0 + i;
       float dv[4], da[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
@@ -380,8 +390,8 @@ __global__ void __launch_bounds__(64 * kGatedWaves, 4) m2rnn_gated_bwd_kernel(Ga
         gbe[e] += da[e];
       }
       if (L.on && t < A.T) {
-        store4_nt<false>(A.dv, L.base + t * A.D, dv);
-        store4_nt<false>(A.da, L.base + t * A.D, da);
+        store4_nt<false>((void*)lane_base<false>(A.dv, L.base), (long)t * A.D, dv);
+        store4_nt<false>((void*)lane_base<false>(A.da, L.base), (long)t * A.D, da);
       }
     }
   } else if (L.on) {
