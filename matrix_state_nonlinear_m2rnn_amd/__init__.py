@@ -1246,7 +1246,7 @@ def m2rnn_add_norm_fwd(x, gamma, res=None, eps: float = 1e-6, *, out_dtype=None,
         elif h is not res:
             _require(h, "h", res.dtype, shape, dev)
     _check("m2rnn_add_norm_fwd", lib().m2rnn_add_norm_fwd(
-        rows, D, xc, x.data_ptr(), rc, _ptr(res), gamma.data_ptr(), eps, _ptr(h), code, group, out.data_ptr(), _ptr(scale),
+        rows, D, xc, x.data_ptr(), rc, _ptr(res), gamma.data_ptr(), float(eps), _ptr(h), code, group, out.data_ptr(), _ptr(scale),
         _stream_of(dev)))
     return out, scale, x if res is None else h
 

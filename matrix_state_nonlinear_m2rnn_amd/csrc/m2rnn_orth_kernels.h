@@ -9,8 +9,9 @@
 // Precision.  Fp32 values are split into two fp16 planes x = hi + lo (22 bits) and a product takes three passes of the
 // fp16 MFMA with fp32 accumulation (lo lo, below 2^-22 of the product, is left out): the error is that of fp32
 // products, at eight times the fp32 MFMA's rate over three.  Values are kept times a power of two that holds fp16's range:
-// X and A times 2^12, B times 2^11.  With singular values up to 1.25 (the usual coefficients' largest) the entries of X
-// and A stay below 6.4e3 and those of B below 2.7e4 (fp16 ends at 6.5e4), and entries down to 2^-15 keep both planes whole.
+// X and A times 2^12, B times 2^11.  With singular values up to 1.21 (the usual coefficients' largest) the entries of X,
+// A and B = b A + c A A (its eigenvalues stay within 2.9) are below 6e3 (fp16 ends at 6.5e4), and entries down to 2^-15
+// keep both planes whole.
 #pragma once
 
 #include "m2rnn_ssm_device.h"
