@@ -593,7 +593,7 @@ int m2rnn_gated_scan_step(int64_t B, int64_t D, int dtype, const void* v, const 
  *              there; the usual coefficients keep them below 1.21 and 2.9).  With a shorter side of 32 at most products
  *              are in fp32 and there is no such bound.  c = 0 (a cubic step) takes two products instead of three.
  *   steps      1 to 64; m, n up to 65536, batch up to 65535, and less than 2^36 elements in all, sides rounded up
- *              to 128.
+ *              to 64.
  * The norm is summed in fp64; products are those of fp32 (with a shorter side above 32: fp16 values in two parts, 22
  * bits, three passes with fp32 accumulation).  A matrix of zeros gives zeros (eps > 0); one with a value that is not finite is
  * not finite.  Two calls on the same inputs give the same bits.  Pointers 16-byte aligned.

@@ -16,7 +16,7 @@ namespace {
 
 constexpr long kOrthMaxSide = 65536;
 constexpr long kOrthParts = 1024;  // partial sums of squares of a matrix at most
-constexpr int kOrthPad = 128;     // what the refusals round sides up to
+constexpr long kOrthPad = 64;     // sides are rounded up to it
 
 bool al16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 size_t round_up256(size_t x) { return (x + 255) & ~(size_t)255; }
@@ -32,22 +32,25 @@ int check_orth(int64_t batch, int64_t m, int64_t n, int dtype) {
   return M2RNN_OK;
 }
 
-// Tiles that a product is cut into: their sides, workgroups that a CU holds, and a stage's time (us) where it holds one,
-// two, ... of them (measured over products of 192 to 8192 a side).
+// Tiles that a product is cut into: their sides, workgroups that a CU holds, a stage's time (us) where it holds one, two, ...
+// of them, and the operations a us that all CUs together reach (the card's power, then); measured over products of 192 to 8192 a
+// side.
 struct Shape {
   int TM, TN, held;
-  double stage[4];
+  double stage[4], rate;
 };
-constexpr Shape kShapes[] = {{256, 256, 1, {2.15}},
-                             {128, 128, 2, {0.78, 1.22}},
-                             {128, 64, 3, {0.5, 0.63, 1.08}},
-                             {64, 64, 4, {0.4, 0.45, 0.55, 0.85}},
-                             {64, 64, 2, {0.3, 0.5}}};  // five stages in LDS
+constexpr Shape kShapes[] = {{256, 256, 1, {2.15}, 9.6e8},
+                             {192, 192, 1, {1.35}, 9.6e8},
+                             {128, 128, 2, {0.95, 1.25}, 9.5e8},
+                             {128, 64, 3, {0.5, 0.63, 1.0}, 8.8e8},
+                             {96, 96, 3, {0.6, 0.87, 1.28}, 9.2e8},
+                             {64, 64, 4, {0.4, 0.45, 0.55, 0.85}, 8.4e8},
+                             {64, 64, 2, {0.3, 0.5}, 8.4e8}};  // five stages in LDS
 constexpr int kShapeCount = sizeof(kShapes) / sizeof(kShapes[0]);
 
 // How a product runs: its tiles, the parts of its contraction, and the time that this should take (us).
 struct Cut {
-  int shape = 0, splits = 1, tiles = 1;
+  int shape = 0, splits = 1, tiles = 1, gi = 1, gj = 1;
   double us = 0.0;
 };
 
@@ -62,19 +65,21 @@ Cut cut_product(long batch, long rows, long cols, long K, bool sym) {
   const long stages = K / kOrthK;
   for (int i = 0; i < kShapeCount; ++i) {
     const Shape& h = kShapes[i];
-    if (rows % h.TM || cols % h.TN) continue;
-    const long gi = rows / h.TM, gj = cols / h.TN;
+    const long gi = ceil_div(rows, h.TM), gj = ceil_div(cols, h.TN);
     const long tiles = sym ? gi * (gi + 1) / 2 * (h.TM / h.TN) : gi * gj;
     for (int s : {1, 2, 3, 4, 6, 8, 12, 16}) {
       if (s > stages) break;
       const long groups = tiles * batch * s;
       if (s > 1 && groups > 256L * h.held) break;
-      double us = rounds_us(h, groups, ceil_div(stages, s)) + 6.0;
+      const double work = (double)tiles * batch * h.TM * h.TN * K * 6.0;
+      double us = std::max(rounds_us(h, groups, ceil_div(stages, s)), work / h.rate) + 6.0;
       if (s > 1) us += 4.0 + (double)groups * h.TM * h.TN * 8.0 / 4e6;  // the parts written and read, one more launch
       if (best.us == 0.0 || us < best.us) {
         best.shape = i;
         best.splits = s;
         best.tiles = (int)tiles;
+        best.gi = (int)gi;
+        best.gj = (int)gj;
         best.us = us;
       }
     }
@@ -82,39 +87,28 @@ Cut cut_product(long batch, long rows, long cols, long K, bool sym) {
   return best;
 }
 
-// Sizes with m the shorter side, padded, and the workspace's parts.
+// Sizes with m the shorter side, rounded up (what a contraction takes), the arrays' sides (what all products' tiles cover:
+// what lies past the rounded sides is never part of a contraction), and the workspace's parts.
 struct Plan {
-  long m, n, mp = 0, np = 0, parts, each;
+  long m, n, mp, np, ma, na, parts, each;
   Cut gram, poly, next;
   size_t part_bytes, x_bytes, a_bytes, split_bytes;  // partial sums of squares; one fp16 plane of X, of A; split products
   Plan(int64_t batch, int64_t rows, int64_t cols) {
     m = std::min(rows, cols);
     n = std::max(rows, cols);
-    double best = 0.0;
-    for (long pm = 64, a, last_a = 0; pm <= 256; pm *= 2, last_a = a) {
-      a = ceil_div(m, pm) * pm;
-      if (a == last_a) continue;
-      const Cut y = cut_product(batch, a, a, a, true);
-      for (long pn = 64, b, last_b = 0; pn <= 256; pn *= 2, last_b = b) {
-        b = ceil_div(n, pn) * pn;
-        if (b == last_b) continue;
-        const Cut x = cut_product(batch, a, a, b, true), w = cut_product(batch, a, b, a, false);
-        const double us = x.us + y.us + w.us;
-        if (mp == 0 || us < best) {
-          best = us;
-          mp = a;
-          np = b;
-          gram = x;
-          poly = y;
-          next = w;
-        }
-      }
-    }
+    mp = ceil_div(m, kOrthPad) * kOrthPad;
+    np = ceil_div(n, kOrthPad) * kOrthPad;
+    gram = cut_product(batch, mp, mp, np, true);
+    poly = cut_product(batch, mp, mp, mp, true);
+    next = cut_product(batch, mp, np, mp, false);
+    ma = na = 0;
+    for (const Cut* c : {&gram, &poly, &next}) ma = std::max(ma, (long)c->gi * kShapes[c->shape].TM);
+    na = (long)next.gj * kShapes[next.shape].TN;
     each = std::max(ceil_div(ceil_div(m * n, kOrthParts), 1024), 4L) * 1024;
     parts = ceil_div(m * n, each);
     part_bytes = round_up256((size_t)batch * parts * sizeof(double));
-    x_bytes = round_up256((size_t)batch * mp * np * 2);
-    a_bytes = round_up256((size_t)batch * mp * mp * 2);
+    x_bytes = round_up256((size_t)batch * ma * na * 2);
+    a_bytes = round_up256((size_t)batch * ma * ma * 2);
     split_bytes = 0;
     for (const Cut* c : {&gram, &poly, &next})
       if (c->splits > 1)
@@ -141,11 +135,15 @@ template <int EPI>
 int product(const Cut& cut, OrthArgs& A, long batch, hipStream_t s) {
   A.splits = cut.splits;
   A.tiles = cut.tiles;
+  A.gi = cut.gi;
+  A.gj = cut.gj;
   switch (cut.shape) {
     case 0: return product_of<256, 256, 2, 4, 2, EPI>(A, batch, s);
-    case 1: return product_of<128, 128, 2, 2, 2, EPI>(A, batch, s);
-    case 2: return product_of<128, 64, 2, 2, 2, EPI>(A, batch, s);
-    case 3: return product_of<64, 64, 2, 2, 2, EPI>(A, batch, s);
+    case 1: return product_of<192, 192, 2, 4, 2, EPI>(A, batch, s);
+    case 2: return product_of<128, 128, 2, 2, 2, EPI>(A, batch, s);
+    case 3: return product_of<128, 64, 2, 2, 2, EPI>(A, batch, s);
+    case 4: return product_of<96, 96, 2, 2, 2, EPI>(A, batch, s);
+    case 5: return product_of<64, 64, 2, 2, 2, EPI>(A, batch, s);
     default: return product_of<64, 64, 2, 2, 5, EPI>(A, batch, s);
   }
 }
@@ -292,12 +290,12 @@ int m2rnn_orthogonalize(int64_t batch, int64_t m, int64_t n, int dtype, const vo
   if (bf16) {
     st = squares<true>(g, p.m * p.n, p.each, p.parts, batch, part, s);
     if (st) return st;
-    hipLaunchKernelGGL(m2rnn_orth_split_kernel<true>, split, dim3(256), 0, s, g, (int)p.m, (int)p.n, (int)p.mp, (int)p.np,
+    hipLaunchKernelGGL(m2rnn_orth_split_kernel<true>, split, dim3(256), 0, s, g, (int)p.m, (int)p.n, (int)p.ma, (int)p.na,
                        tall, (const double*)part, (int)p.parts, eps, X32, X, XT);
   } else {
     st = squares<false>(g, p.m * p.n, p.each, p.parts, batch, part, s);
     if (st) return st;
-    hipLaunchKernelGGL(m2rnn_orth_split_kernel<false>, split, dim3(256), 0, s, g, (int)p.m, (int)p.n, (int)p.mp, (int)p.np,
+    hipLaunchKernelGGL(m2rnn_orth_split_kernel<false>, split, dim3(256), 0, s, g, (int)p.m, (int)p.n, (int)p.ma, (int)p.na,
                        tall, (const double*)part, (int)p.parts, eps, X32, X, XT);
   }
   st = record_hip_status(hipGetLastError());
@@ -308,13 +306,15 @@ int m2rnn_orthogonalize(int64_t batch, int64_t m, int64_t n, int dtype, const vo
     const bool cubic = f[2] == 0.0f;  // B = b A
     A.M = A.N = X;
     A.O = A.OT = cubic ? Q : P;
-    A.rows = A.cols = (int)p.mp;
+    A.rows = A.cols = (int)p.ma;
+    A.ld = (int)p.na;
     A.K = (int)p.np;
     A.cb = cubic ? f[1] * kOrthB : kOrthA;
     st = product<ORTH_GRAM>(p.gram, A, batch, s);
     if (!st && !cubic) {
       A.M = A.N = A.E = P;
       A.O = A.OT = Q;
+      A.ld = (int)p.ma;
       A.K = (int)p.mp;
       A.cb = f[1];
       A.cc = f[2];
@@ -322,12 +322,13 @@ int m2rnn_orthogonalize(int64_t batch, int64_t m, int64_t n, int dtype, const vo
     }
     if (st) break;
     A.M = Q;
+    A.ld = (int)p.ma;
     A.K = (int)p.mp;
     A.N = XT;
     A.X32 = X32;
     A.O = X;
     A.OT = YT;
-    A.cols = (int)p.np;
+    A.cols = (int)p.na;
     A.ca = f[0];
     A.out = out;
     A.m = (int)p.m;

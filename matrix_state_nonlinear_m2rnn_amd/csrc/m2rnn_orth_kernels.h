@@ -82,10 +82,10 @@ __global__ void __launch_bounds__(256) m2rnn_orth_squares_kernel(const void* g, 
   if (threadIdx.x == 0) part[(long)blockIdx.y * gridDim.x + blockIdx.x] = (red[0] + red[1]) + (red[2] + red[3]);
 }
 
-// X_0 times kOrthX in fp32 [mp][np], as planes and the transpose's planes, zeros past m x n; m x n is G or, `tall`,
-// its transpose.  A workgroup takes 64 x 64.
+// X_0 times kOrthX in fp32 [ma][na], as planes and the transpose's planes, zeros past m x n up to whole workgroups, which take
+// 64 x 64; m x n is G or, `tall`, its transpose.
 template <bool BF16>
-__global__ void __launch_bounds__(256) m2rnn_orth_split_kernel(const void* g, int m, int n, int mp, int np, int tall,
+__global__ void __launch_bounds__(256) m2rnn_orth_split_kernel(const void* g, int m, int n, int ma, int na, int tall,
                                                                const double* part, int parts, float eps, float* X32, Planes X,
                                                                Planes XT) {
   __shared__ float tile[64][65];
@@ -108,9 +108,9 @@ __global__ void __launch_bounds__(256) m2rnn_orth_split_kernel(const void* g, in
     tile[tall ? tx : i][tall ? i : tx] = x;
   }
   __syncthreads();
-  const long plane = z * mp * np;
+  const long plane = z * ma * na;
 #pragma unroll 4
-  for (int i = ty; i < 64; i += 4) X32[plane + (long)(r0 + i) * np + c0 + tx] = tile[i][tx];
+  for (int i = ty; i < 64; i += 4) X32[plane + (long)(r0 + i) * na + c0 + tx] = tile[i][tx];
   // 8 blocks of the planes and 8 of the transpose's, two of each a wave, a lane the unit that lies at its place
   const int row = tx >> 2, unit = (tx & 3) ^ ((tx >> 3) & 3);
 #pragma unroll
@@ -123,7 +123,7 @@ __global__ void __launch_bounds__(256) m2rnn_orth_split_kernel(const void* g, in
       const int r = br + row, c = bc + 8 * unit + e;
       split_f16(turned ? tile[c][r] : tile[r][c], hi[e], lo[e]);
     }
-    const long o = plane + (turned ? plane_at(c0 + br, r0 + bc, mp) : plane_at(r0 + br, c0 + bc, np)) + tx * 8;
+    const long o = plane + (turned ? plane_at(c0 + br, r0 + bc, ma) : plane_at(r0 + br, c0 + bc, na)) + tx * 8;
     *(uint4*)((turned ? XT.hi : X.hi) + o) = *(const uint4*)hi;
     *(uint4*)((turned ? XT.lo : X.lo) + o) = *(const uint4*)lo;
   }
@@ -138,13 +138,14 @@ struct OrthCoefs {
 enum { ORTH_GRAM = 0, ORTH_POLY = 1, ORTH_NEXT = 2, ORTH_LAST = 3 };
 
 struct OrthArgs {
-  Planes M, N;        // rows x K, cols x K
+  Planes M, N;        // rows x ld, cols x ld, of which the contraction takes K
   Planes E;           // POLY: A
   float* X32;         // NEXT and LAST: X in fp32 (NEXT: and X'), [rows][cols]
   Planes O, OT;       // outputs rows x cols and cols x rows
   void* out;          // LAST: [m][n], or [n][m] if tall
   float* part;        // [batch][splits][tiles][waves] wave tiles of partial sums, if the contraction is split
-  int rows, cols, K;  // padded
+  int rows, cols, ld; // the arrays' sides: at least what the tiles cover
+  int K, gi, gj;      // the contraction's length; rows and columns of tiles
   int m, n;
   int tall, out_bf16;
   int splits, tiles;
@@ -258,7 +259,7 @@ __global__ void __launch_bounds__(64 * WR * WC) m2rnn_orth_product_kernel(OrthAr
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int tile = orth_turn(blockIdx.x, A.tiles);
   int bi, bj;
-  orth_place<SYM, TM / TN>(tile, A.rows / TM, A.cols / TN, bi, bj);
+  orth_place<SYM, TM / TN>(tile, A.gi, A.gj, bi, bj);
   const long z = blockIdx.z;
   const int r0 = bi * TM, c0 = bj * TN;
   const int stages = A.K / kOrthK;
@@ -272,7 +273,7 @@ __global__ void __launch_bounds__(64 * WR * WC) m2rnn_orth_product_kernel(OrthAr
     const int in = right ? id - 2 * BM : id, most = right ? BN : BM;
     const int lo = in >= most, blk = in - lo * most;
     const Planes& P = right ? A.N : A.M;
-    src[i] = (lo ? P.lo : P.hi) + ((z * (right ? A.cols : A.rows) + (right ? c0 : r0) + 16 * blk) * A.K + lane * 8);
+    src[i] = (lo ? P.lo : P.hi) + ((z * (right ? A.cols : A.rows) + (right ? c0 : r0) + 16 * blk) * A.ld + lane * 8);
   }
   auto fetch = [&](int buf, int stage) {
 #pragma unroll
@@ -292,10 +293,11 @@ __global__ void __launch_bounds__(64 * WR * WC) m2rnn_orth_product_kernel(OrthAr
     mh[i & 1] = pm[buf * STAGE + i * 64];
     ml[i & 1] = pm[buf * STAGE + 4 * TM + i * 64];
   };
-  f32x4 t[2][NJ];
+  constexpr int NT = 2 + NI % 2;  // rows' sums that take turns; the last row's is added in the next stage
+  f32x4 t[NT][NJ];
 #pragma unroll
-  for (int j = 0; j < NJ; ++j) t[1][j] = f32x4{0, 0, 0, 0};
-  static_assert(NI % 2 == 0, "the rows' operands and sums take turns");
+  for (int j = 0; j < NJ; ++j) t[NT - 1][j] = f32x4{0, 0, 0, 0};
+  static_assert(NI % NT == 0, "the last row has the last place");
   static_assert((BUFS - 2) * PER < 16, "a wait's count");
 #pragma unroll
   for (int i = 0; i < BUFS - 1; ++i)
@@ -320,18 +322,18 @@ __global__ void __launch_bounds__(64 * WR * WC) m2rnn_orth_product_kernel(OrthAr
       if (i + 1 < NI) read_m(buf, i + 1);
       __builtin_amdgcn_sched_barrier(0);  // reads stay before: the compiler would leave them for the end, to be waited for
 #pragma unroll
-      for (int j = 0; j < NJ; ++j) acc[i == 0 ? NI - 1 : i - 1][j] += t[(i & 1) ^ 1][j];
+      for (int j = 0; j < NJ; ++j) acc[i == 0 ? NI - 1 : i - 1][j] += t[(i + NT - 1) % NT][j];
 #pragma unroll
-      for (int j = 0; j < NJ; ++j) t[i & 1][j] = mfma_f16(ml[i & 1], nh[j], f32x4{0, 0, 0, 0});
+      for (int j = 0; j < NJ; ++j) t[i % NT][j] = mfma_f16(ml[i & 1], nh[j], f32x4{0, 0, 0, 0});
 #pragma unroll
-      for (int j = 0; j < NJ; ++j) t[i & 1][j] = mfma_f16(mh[i & 1], nl[j], t[i & 1][j]);
+      for (int j = 0; j < NJ; ++j) t[i % NT][j] = mfma_f16(mh[i & 1], nl[j], t[i % NT][j]);
 #pragma unroll
-      for (int j = 0; j < NJ; ++j) t[i & 1][j] = mfma_f16(mh[i & 1], nh[j], t[i & 1][j]);
+      for (int j = 0; j < NJ; ++j) t[i % NT][j] = mfma_f16(mh[i & 1], nh[j], t[i % NT][j]);
       __builtin_amdgcn_sched_barrier(0);
     }
   }
 #pragma unroll
-  for (int j = 0; j < NJ; ++j) acc[NI - 1][j] += t[1][j];
+  for (int j = 0; j < NJ; ++j) acc[NI - 1][j] += t[NT - 1][j];
   // lane (g, n), register e: row 4 g + e, column n of a 16 x 16 tile
   if constexpr (SPLIT) {
     float4* dst = (float4*)A.part + (((z * A.splits + blockIdx.y) * A.tiles + tile) * WAVES + w) * (NI * NJ * 64) + lane;
@@ -358,7 +360,7 @@ __global__ void __launch_bounds__(256) m2rnn_orth_join_kernel(OrthArgs A) {
   if (item >= A.tiles * WAVES * NI) return;
   const int i = item % NI, w = item / NI % WAVES, tile = item / (NI * WAVES);
   int bi, bj;
-  orth_place<SYM, TM / TN>(tile, A.rows / TM, A.cols / TN, bi, bj);
+  orth_place<SYM, TM / TN>(tile, A.gi, A.gj, bi, bj);
   const int n = lane & 15, g = lane >> 4;
   const int r = bi * TM + (w / WC) * (TM / WR) + 16 * i + 4 * g, c = bj * TN + (w % WC) * (TN / WC) + n;
   f32x4 acc[NJ];

@@ -82,6 +82,20 @@ def test_steps_and_coefficients(m, n):
     assert torch.equal(m2.m2rnn_orthogonalize(g.view(1, 2, m, n)), a.view(1, 2, m, n))
 
 
+@pytest.mark.parametrize("m,n,dtype", [(1990, 2110, "fp32"), (2950, 2900, "bf16"), (2620, 2700, "fp32"), (600, 9000, "fp32")])
+def test_large_tiles_that_end_inside(m, n, dtype):
+    """Sizes whose products take each of the larger tiles, of which the last ones end past the matrix."""
+    torch = torch_cuda()
+    import matrix_state_nonlinear_m2rnn_amd as m2
+    say("orth tiles", m, n, dtype)
+    g = gradient(1, m, n, m + n, dtype)
+    out = m2.m2rnn_orthogonalize(g, 2)
+    check(g, out, 2)
+    size = m2._size_query("m2rnn_orthogonalize_workspace_size", 1, m, n, m2._dtype_code(g))
+    again = m2.m2rnn_orthogonalize(g, 2, workspace=torch.full((size + 16,), 255, dtype=torch.uint8, device="cuda"))
+    assert torch.equal(again, out)
+
+
 @pytest.mark.parametrize("m,n", [(24, 40), (700, 8), (64, 64), (150, 90)])
 def test_scales_and_values_that_are_not_finite(m, n):
     """Any scale of the gradient gives the same result; zeros give zeros; one matrix that is not finite leaves the
