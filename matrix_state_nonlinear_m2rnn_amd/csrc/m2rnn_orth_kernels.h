@@ -310,11 +310,18 @@ __global__ void __launch_bounds__(64 * WR * WC) m2rnn_orth_product_kernel(OrthAr
       __builtin_amdgcn_s_waitcnt(0x0f70);  // (fewer are on their way: all of them)
     lds_barrier();  // and all waves'; the buffer of the stage before has been read by all
     if (s + BUFS - 1 < last) fetch(buf == 0 ? BUFS - 1 : buf - 1, s + BUFS - 1);
-    read_m(buf, 0);
+    // in the order in which they are needed: all waves read at once here, and the first products wait for two of these
+    ml[0] = pm[buf * STAGE + 4 * TM];
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
       nh[j] = pn[buf * STAGE + j * 64];
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    mh[0] = pm[buf * STAGE];
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
       nl[j] = pn[buf * STAGE + 4 * TN + j * 64];
+      __builtin_amdgcn_sched_barrier(0);
     }
     // a row of tiles at a time: the next row's operands are read, and the last row's sums added, beside its products
 #pragma unroll
