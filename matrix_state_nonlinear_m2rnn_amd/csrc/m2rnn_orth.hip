@@ -114,7 +114,7 @@ struct Plan {
       if (c->splits > 1)
         split_bytes = std::max(split_bytes, (size_t)batch * c->splits * c->tiles * kShapes[c->shape].TM * kShapes[c->shape].TN * 4);
   }
-  size_t bytes() const { return part_bytes + 8 * x_bytes + 4 * a_bytes + split_bytes; }
+  size_t bytes() const { return part_bytes + 4 * x_bytes + 4 * a_bytes + split_bytes; }
 };
 
 template <int TM, int TN, int WR, int WC, int BUFS, int EPI>
@@ -280,10 +280,7 @@ int m2rnn_orthogonalize(int64_t batch, int64_t m, int64_t n, int dtype, const vo
     at += 2 * bytes;
     return q;
   };
-  float* X32 = (float*)at;
-  at += 2 * p.x_bytes;
-  const Planes X = planes(p.x_bytes);
-  Planes XT = planes(p.x_bytes), YT = planes(p.x_bytes);
+  Planes X = planes(p.x_bytes), Y = planes(p.x_bytes);
   const Planes P = planes(p.a_bytes), Q = planes(p.a_bytes);
   const int tall = m > n;
   const dim3 split((unsigned)(p.np / 64), (unsigned)(p.mp / 64), (unsigned)batch);
@@ -291,12 +288,12 @@ int m2rnn_orthogonalize(int64_t batch, int64_t m, int64_t n, int dtype, const vo
     st = squares<true>(g, p.m * p.n, p.each, p.parts, batch, part, s);
     if (st) return st;
     hipLaunchKernelGGL(m2rnn_orth_split_kernel<true>, split, dim3(256), 0, s, g, (int)p.m, (int)p.n, (int)p.ma, (int)p.na,
-                       tall, (const double*)part, (int)p.parts, eps, X32, X, XT);
+                       tall, (const double*)part, (int)p.parts, eps, X);
   } else {
     st = squares<false>(g, p.m * p.n, p.each, p.parts, batch, part, s);
     if (st) return st;
     hipLaunchKernelGGL(m2rnn_orth_split_kernel<false>, split, dim3(256), 0, s, g, (int)p.m, (int)p.n, (int)p.ma, (int)p.na,
-                       tall, (const double*)part, (int)p.parts, eps, X32, X, XT);
+                       tall, (const double*)part, (int)p.parts, eps, X);
   }
   st = record_hip_status(hipGetLastError());
   for (int64_t i = 0; i < steps && !st; ++i) {
@@ -305,7 +302,7 @@ int m2rnn_orthogonalize(int64_t batch, int64_t m, int64_t n, int dtype, const vo
     A.part = (float*)at;
     const bool cubic = f[2] == 0.0f;  // B = b A
     A.M = A.N = X;
-    A.O = A.OT = cubic ? Q : P;
+    A.O = cubic ? Q : P;
     A.rows = A.cols = (int)p.ma;
     A.ld = (int)p.na;
     A.K = (int)p.np;
@@ -313,7 +310,7 @@ int m2rnn_orthogonalize(int64_t batch, int64_t m, int64_t n, int dtype, const vo
     st = product<ORTH_GRAM>(p.gram, A, batch, s);
     if (!st && !cubic) {
       A.M = A.N = A.E = P;
-      A.O = A.OT = Q;
+      A.O = Q;
       A.ld = (int)p.ma;
       A.K = (int)p.mp;
       A.cb = f[1];
@@ -324,10 +321,8 @@ int m2rnn_orthogonalize(int64_t batch, int64_t m, int64_t n, int dtype, const vo
     A.M = Q;
     A.ld = (int)p.ma;
     A.K = (int)p.mp;
-    A.N = XT;
-    A.X32 = X32;
-    A.O = X;
-    A.OT = YT;
+    A.N = X;
+    A.O = Y;
     A.cols = (int)p.na;
     A.ca = f[0];
     A.out = out;
@@ -336,7 +331,7 @@ int m2rnn_orthogonalize(int64_t batch, int64_t m, int64_t n, int dtype, const vo
     A.tall = tall;
     A.out_bf16 = bf16;
     st = i + 1 < steps ? product<ORTH_NEXT>(p.next, A, batch, s) : product<ORTH_LAST>(p.next, A, batch, s);
-    std::swap(XT, YT);
+    std::swap(X, Y);
   }
   return st;
 }

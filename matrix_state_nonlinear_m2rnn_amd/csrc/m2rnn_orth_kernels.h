@@ -3,9 +3,9 @@
 // which takes every singular value s of X to a s + b s^3 + c s^5 and leaves the singular vectors: with the usual
 // coefficients all of them end near 1.
 //
-// Three matrix products a step, all of the form M N^T over rows that are contiguous along the contraction:
+// Three matrix products a step:
 //     (1) A = X X^T (symmetric: its lower tiles, each written twice), (2) B = b A + c A A^T (likewise),
-//     (3) X' = a X + B (X^T)^T, for which X^T is kept beside X.
+//     (3) X' = a X + B X, whose right operand goes along X's columns (transposing reads).
 // Precision.  Fp32 values are split into two fp16 planes x = hi + lo (22 bits) and a product takes three passes of the
 // fp16 MFMA with fp32 accumulation (lo lo, below 2^-22 of the product, is left out): the error is that of fp32
 // products, at eight times the fp32 MFMA's rate over three.  Values are kept times a power of two that holds fp16's range:
@@ -27,10 +27,12 @@ constexpr int kOrthK = 32;  // contraction of a stage
 struct Planes {
   uint16_t *hi, *lo;
 };
-// Where element (r, c) lies.  Within a block, 16-byte unit u of row r is at u ^ ((r >> 1) & 3): the eight rows that a
-// read of an operand touches at a time cover all banks.
+// Within a block, 16-byte unit u of row r is at u ^ plane_turn(r): the eight rows that a read of an operand touches at a
+// time, and the four half rows of a transposing read, cover all banks.
+__device__ __forceinline__ int plane_turn(int r) { return (r & 2) | ((r >> 2) & 1); }
+// Where element (r, c) lies.
 __device__ __forceinline__ long plane_at(int r, int c, int ld) {
-  return ((long)(r >> 4) * (ld >> 5) + (c >> 5)) * 512 + ((r & 15) * 4 + (((c >> 3) & 3) ^ ((r >> 1) & 3))) * 8 + (c & 7);
+  return ((long)(r >> 4) * (ld >> 5) + (c >> 5)) * 512 + ((r & 15) * 4 + (((c >> 3) & 3) ^ plane_turn(r))) * 8 + (c & 7);
 }
 
 __device__ __forceinline__ void split_f16(float x, uint16_t& hi, uint16_t& lo) {
@@ -82,12 +84,11 @@ __global__ void __launch_bounds__(256) m2rnn_orth_squares_kernel(const void* g, 
   if (threadIdx.x == 0) part[(long)blockIdx.y * gridDim.x + blockIdx.x] = (red[0] + red[1]) + (red[2] + red[3]);
 }
 
-// X_0 times kOrthX in fp32 [ma][na], as planes and the transpose's planes, zeros past m x n up to whole workgroups, which take
-// 64 x 64; m x n is G or, `tall`, its transpose.
+// X_0 times kOrthX as planes [ma][na], zeros past m x n up to whole workgroups, which take 64 x 64; m x n is G or, `tall`, its
+// transpose.
 template <bool BF16>
 __global__ void __launch_bounds__(256) m2rnn_orth_split_kernel(const void* g, int m, int n, int ma, int na, int tall,
-                                                               const double* part, int parts, float eps, float* X32, Planes X,
-                                                               Planes XT) {
+                                                               const double* part, int parts, float eps, Planes X) {
   __shared__ float tile[64][65];
   __shared__ double red[4];
   const long z = blockIdx.z;
@@ -108,24 +109,17 @@ __global__ void __launch_bounds__(256) m2rnn_orth_split_kernel(const void* g, in
     tile[tall ? tx : i][tall ? i : tx] = x;
   }
   __syncthreads();
-  const long plane = z * ma * na;
-#pragma unroll 4
-  for (int i = ty; i < 64; i += 4) X32[plane + (long)(r0 + i) * na + c0 + tx] = tile[i][tx];
-  // 8 blocks of the planes and 8 of the transpose's, two of each a wave, a lane the unit that lies at its place
-  const int row = tx >> 2, unit = (tx & 3) ^ ((tx >> 3) & 3);
+  // 8 blocks of the planes, two of them a wave, a lane the unit that lies at its place
+  const int row = tx >> 2, unit = (tx & 3) ^ plane_turn(row);
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const bool turned = k >= 2;
-    const int id = 2 * ty + (k & 1), br = 16 * (id >> 1), bc = 32 * (id & 1);
+  for (int k = 0; k < 2; ++k) {
+    const int id = 2 * ty + k, br = 16 * (id >> 1), bc = 32 * (id & 1);
     alignas(16) uint16_t hi[8], lo[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int r = br + row, c = bc + 8 * unit + e;
-      split_f16(turned ? tile[c][r] : tile[r][c], hi[e], lo[e]);
-    }
-    const long o = plane + (turned ? plane_at(c0 + br, r0 + bc, ma) : plane_at(r0 + br, c0 + bc, na)) + tx * 8;
-    *(uint4*)((turned ? XT.hi : X.hi) + o) = *(const uint4*)hi;
-    *(uint4*)((turned ? XT.lo : X.lo) + o) = *(const uint4*)lo;
+    for (int e = 0; e < 8; ++e) split_f16(tile[br + row][bc + 8 * unit + e], hi[e], lo[e]);
+    const long o = z * ma * na + plane_at(r0 + br, c0 + bc, na) + tx * 8;
+    *(uint4*)(X.hi + o) = *(const uint4*)hi;
+    *(uint4*)(X.lo + o) = *(const uint4*)lo;
   }
 }
 
@@ -138,10 +132,9 @@ struct OrthCoefs {
 enum { ORTH_GRAM = 0, ORTH_POLY = 1, ORTH_NEXT = 2, ORTH_LAST = 3 };
 
 struct OrthArgs {
-  Planes M, N;        // rows x ld, cols x ld, of which the contraction takes K
+  Planes M, N;        // rows x ld and cols x ld (NEXT and LAST: ld x cols), of which the contraction takes K
   Planes E;           // POLY: A
-  float* X32;         // NEXT and LAST: X in fp32 (NEXT: and X'), [rows][cols]
-  Planes O, OT;       // outputs rows x cols and cols x rows
+  Planes O;           // the output, rows x cols
   void* out;          // LAST: [m][n], or [n][m] if tall
   float* part;        // [batch][splits][tiles][waves] wave tiles of partial sums, if the contraction is split
   int rows, cols, ld; // the arrays' sides: at least what the tiles cover
@@ -152,23 +145,19 @@ struct OrthArgs {
   float ca, cb, cc;
 };
 
-// A lane's part of NJ 16 x 16 tiles side by side: rows r .. r + 3 of the columns c + 16 j.  `mirror`: the transposed place
-// is written too.  What the epilogue reads is loaded before anything is stored.
+// GRAM and POLY: a lane's part of NJ 16 x 16 tiles side by side, rows r .. r + 3 of the columns c + 16 j.  `mirror`: the
+// transposed place is written too.  What the epilogue reads is loaded before anything is stored.
 template <int EPI, int NJ>
-__device__ __forceinline__ void orth_finish(const OrthArgs& A, long z, int r, int c, const f32x4 (&acc)[NJ], bool mirror) {
-  const long zo = z * A.rows * A.cols, eo = zo + (long)r * A.cols + c;
+__device__ __forceinline__ void orth_square(const OrthArgs& A, long z, int r, int c, const f32x4 (&acc)[NJ], bool mirror) {
+  const long zo = z * A.rows * A.cols;
   float x[NJ][4];
-  if constexpr (EPI != ORTH_GRAM) {
+  if constexpr (EPI == ORTH_POLY) {
 #pragma unroll
     for (int j = 0; j < NJ; ++j)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        if constexpr (EPI == ORTH_POLY) {
-          const long at = zo + plane_at(r + e, c + 16 * j, A.cols);
-          x[j][e] = join_f16(A.E.hi[at], A.E.lo[at]);
-        } else {
-          x[j][e] = A.X32[eo + (long)e * A.cols + 16 * j];
-        }
+        const long at = zo + plane_at(r + e, c + 16 * j, A.cols);
+        x[j][e] = join_f16(A.E.hi[at], A.E.lo[at]);
       }
   }
 #pragma unroll
@@ -179,35 +168,81 @@ __device__ __forceinline__ void orth_finish(const OrthArgs& A, long z, int r, in
       float y = acc[j][e];
       if constexpr (EPI == ORTH_GRAM)
         y *= A.cb * (1.0f / (kOrthX * kOrthX));  // (A, or B of a cubic step, times its power of two)
-      else if constexpr (EPI == ORTH_POLY)
-        y = __builtin_fmaf(A.cb * (kOrthB / kOrthA), x[j][e], A.cc * (kOrthB / (kOrthA * kOrthA)) * y);
       else
-        y = __builtin_fmaf(A.ca, x[j][e], y * (1.0f / kOrthB));
-      if constexpr (EPI == ORTH_LAST) {
-        y *= 1.0f / kOrthX;
-        if (r + e < A.m && c + 16 * j < A.n) {
-          const long o = z * A.m * A.n + (A.tall ? (long)(c + 16 * j) * A.m + r + e : (long)(r + e) * A.n + c + 16 * j);
-          if (A.out_bf16)
-            ((__bf16*)A.out)[o] = (__bf16)y;
-          else
-            ((float*)A.out)[o] = y;
-        }
-      } else {
-        if constexpr (EPI == ORTH_NEXT) A.X32[eo + (long)e * A.cols + 16 * j] = y;
-        split_f16(y, hi[e], lo[e]);
-        const long at = zo + plane_at(r + e, c + 16 * j, A.cols);
-        A.O.hi[at] = hi[e];
-        A.O.lo[at] = lo[e];
-      }
+        y = __builtin_fmaf(A.cb * (kOrthB / kOrthA), x[j][e], A.cc * (kOrthB / (kOrthA * kOrthA)) * y);
+      split_f16(y, hi[e], lo[e]);
+      const long at = zo + plane_at(r + e, c + 16 * j, A.cols);
+      A.O.hi[at] = hi[e];
+      A.O.lo[at] = lo[e];
     }
-    if constexpr (EPI != ORTH_LAST) {
-      if (mirror) {
-        const long at = zo + plane_at(c + 16 * j, r, A.rows);  // (four neighbours: r is a multiple of 4)
-        *(uint2*)(A.OT.hi + at) = make_uint2(hi[0] | (uint32_t)hi[1] << 16, hi[2] | (uint32_t)hi[3] << 16);
-        *(uint2*)(A.OT.lo + at) = make_uint2(lo[0] | (uint32_t)lo[1] << 16, lo[2] | (uint32_t)lo[3] << 16);
-      }
+    if (mirror) {
+      const long at = zo + plane_at(c + 16 * j, r, A.rows);  // (four neighbours: r is a multiple of 4)
+      *(uint2*)(A.O.hi + at) = make_uint2(hi[0] | (uint32_t)hi[1] << 16, hi[2] | (uint32_t)hi[3] << 16);
+      *(uint2*)(A.O.lo + at) = make_uint2(lo[0] | (uint32_t)lo[1] << 16, lo[2] | (uint32_t)lo[3] << 16);
     }
   }
+}
+
+// NEXT and LAST: a lane's part of NJ 16 x 16 tiles side by side, of row r the columns c + 16 j to c + 16 j + 3.
+template <int EPI, int NJ>
+__device__ __forceinline__ void orth_next(const OrthArgs& A, long z, int r, int c, const f32x4 (&acc)[NJ]) {
+  const long zo = z * A.rows * A.cols;
+  uint2 h[NJ], l[NJ];
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) {
+    const long at = zo + plane_at(r, c + 16 * j, A.cols);
+    h[j] = *(const uint2*)(A.N.hi + at);
+    l[j] = *(const uint2*)(A.N.lo + at);
+  }
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) {
+    float y[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const uint32_t hi = e < 2 ? h[j].x : h[j].y, lo = e < 2 ? l[j].x : l[j].y;
+      y[e] = __builtin_fmaf(A.ca, join_f16((uint16_t)(e & 1 ? hi >> 16 : hi), (uint16_t)(e & 1 ? lo >> 16 : lo)), acc[j][e] * (1.0f / kOrthB));
+    }
+    if constexpr (EPI == ORTH_LAST) {
+      const int col = c + 16 * j;
+      const long o = z * A.m * A.n + (A.tall ? (long)col * A.m + r : (long)r * A.n + col), step = A.tall ? A.m : 1;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) y[e] *= 1.0f / kOrthX;
+      if (!A.tall && A.n % 4 == 0) {  // (aligned)
+        if (r < A.m && col < A.n) {
+          if (A.out_bf16)
+            *(uint2*)((uint16_t*)A.out + o) = make_uint2(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]));
+          else
+            *(float4*)((float*)A.out + o) = make_float4(y[0], y[1], y[2], y[3]);
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (r < A.m && col + e < A.n) {
+            if (A.out_bf16)
+              ((__bf16*)A.out)[o + e * step] = (__bf16)y[e];
+            else
+              ((float*)A.out)[o + e * step] = y[e];
+          }
+      }
+    } else {
+      uint16_t hi[4], lo[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) split_f16(y[e], hi[e], lo[e]);
+      const long at = zo + plane_at(r, c + 16 * j, A.cols);
+      *(uint2*)(A.O.hi + at) = make_uint2(hi[0] | (uint32_t)hi[1] << 16, hi[2] | (uint32_t)hi[3] << 16);
+      *(uint2*)(A.O.lo + at) = make_uint2(lo[0] | (uint32_t)lo[1] << 16, lo[2] | (uint32_t)lo[3] << 16);
+    }
+  }
+}
+
+// A row of a wave's 16 x 16 tiles from (rb, cb) on, lane (g, n): GRAM and POLY hold rows 4 g + e of column n, NEXT and LAST
+// columns 4 g + e of row n.
+template <int EPI, int NJ>
+__device__ __forceinline__ void orth_finish(const OrthArgs& A, long z, int rb, int cb, int g, int n, const f32x4 (&acc)[NJ], bool mirror) {
+  if constexpr (EPI == ORTH_GRAM || EPI == ORTH_POLY)
+    orth_square<EPI, NJ>(A, z, rb + 4 * g, cb + n, acc, mirror);
+  else
+    orth_next<EPI, NJ>(A, z, rb + n, cb + 4 * g, acc);
 }
 
 // The place of tile number `id` of TM x TN tiles: those that touch the lower triangle by rows (SYM, Q = TM / TN of them for
@@ -242,15 +277,16 @@ __device__ __forceinline__ void load_to_lds(const void* from, const void* to) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(at), "v"(from) : "memory");
 }
 
-// One TM x TN tile of M N^T, or its part of a split contraction.  WR x WC waves, 16x16x32 MFMA.  A stage is 32 of the
-// contraction: a column of blocks of the four planes, brought to LDS past the registers.  The three passes of a stage are
+// One TM x TN tile of M N^T (NEXT and LAST: M N), or its part of a split contraction.  WR x WC waves, 16x16x32 MFMA.  A stage
+// is 32 of the contraction: a column of blocks of M's planes, and of N's (M N: two rows of them), brought to LDS past the
+// registers.  The three passes of a stage are
 // summed by themselves, from zero, and added to the tile's sum once: one rounding at the sum's size for each stage
 // instead of three.
 // LDS holds BUFS stages, all but the one that is multiplied on their way.  Two where a CU holds several workgroups, or a
 // tile leaves no room for more; more for the only workgroup of a CU, whose stages would otherwise each wait for memory.
 template <int TM, int TN, int WR, int WC, int BUFS, int EPI, bool SPLIT>
 __global__ void __launch_bounds__(64 * WR * WC) m2rnn_orth_product_kernel(OrthArgs A) {
-  constexpr bool SYM = EPI == ORTH_GRAM || EPI == ORTH_POLY;
+  constexpr bool SYM = EPI == ORTH_GRAM || EPI == ORTH_POLY;  // and M N^T
   constexpr int NI = TM / WR / 16, NJ = TN / WC / 16, WAVES = WR * WC;
   constexpr int BM = TM / 16, BN = TN / 16, PER = 2 * (BM + BN) / WAVES;  // blocks of a plane's stage; those that a wave brings
   constexpr int STAGE = 8 * (TM + TN);                                    // 16-byte units
@@ -266,18 +302,30 @@ __global__ void __launch_bounds__(64 * WR * WC) m2rnn_orth_product_kernel(OrthAr
   const int first = SPLIT ? (int)((long)stages * blockIdx.y / A.splits) : 0;
   const int last = SPLIT ? (int)((long)stages * (blockIdx.y + 1) / A.splits) : stages;
   const uint16_t* src[PER];
+  long step[PER];
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
     const int id = w * PER + i;  // the block's number in a stage, by planes
     const bool right = id >= 2 * BM;
     const int in = right ? id - 2 * BM : id, most = right ? BN : BM;
     const int lo = in >= most, blk = in - lo * most;
-    const Planes& P = right ? A.N : A.M;
-    src[i] = (lo ? P.lo : P.hi) + ((z * (right ? A.cols : A.rows) + (right ? c0 : r0) + 16 * blk) * A.ld + lane * 8);
+    const uint16_t* plane = right ? (lo ? A.N.lo : A.N.hi) : lo ? A.M.lo : A.M.hi;
+    long at;
+    if (right && !SYM) {  // block 2 j + k: columns 32 j on, rows 16 k on
+      at = z * A.ld * A.cols + ((blk & 1) * (A.cols >> 5) + (c0 >> 5) + (blk >> 1)) * 512L;
+      step[i] = A.cols * 32L;
+    } else {
+      at = (z * (right ? A.cols : A.rows) + (right ? c0 : r0) + 16 * blk) * A.ld;
+      step[i] = 512;
+    }
+    src[i] = plane + at + first * step[i] + lane * 8;
   }
-  auto fetch = [&](int buf, int stage) {
+  auto fetch = [&](int buf) {  // the next stage
 #pragma unroll
-    for (int i = 0; i < PER; ++i) load_to_lds(src[i] + (long)stage * 512, lds + buf * STAGE + (w * PER + i) * 64);
+    for (int i = 0; i < PER; ++i) {
+      load_to_lds(src[i], lds + buf * STAGE + (w * PER + i) * 64);
+      src[i] += step[i];
+    }
   };
   f32x4 acc[NI][NJ];
 #pragma unroll
@@ -286,8 +334,33 @@ __global__ void __launch_bounds__(64 * WR * WC) m2rnn_orth_product_kernel(OrthAr
     for (int j = 0; j < NJ; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
   const int n = lane & 15, g = lane >> 4;
   const int wr = (w / WC) * (TM / WR), wc = (w % WC) * (TN / WC);
-  const int unit = n * 4 + (g ^ ((n >> 1) & 3));  // (16 rows on: the same exchange)
+  const int unit = n * 4 + (g ^ plane_turn(n));  // (16 rows on: the same exchange)
   const uint4 *pm = lds + wr * 4 + unit, *pn = lds + 8 * TM + wc * 4 + unit;
+  // M N: a transposing read gives a lane of group g four rows from 8 g on of column n, and the next one the four behind;
+  // lane n of the group brings eight bytes of row n / 4.  Even and odd tiles of 16 columns are a block's halves (a wave may
+  // begin with either).
+  typedef __attribute__((address_space(3))) const char* lds_bytes;
+  lds_bytes pt[2][2];
+  {
+    const int odd = (wc >> 4) & 1, at = (g >> 1) * 1024 + (8 * (g & 1) + (n >> 2)) * 64 + (((n >> 1) & 1) ^ (n >> 3 << 1)) * 16 + (n & 1) * 8;
+    const lds_bytes base = (lds_bytes)(lds + 8 * TM) + (wc >> 5) * 2048;
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+      const int half = at ^ ((p ^ odd) * 32);
+      pt[p][0] = base + (p & odd) * 2048 + half;
+      pt[p][1] = base + (p & odd) * 2048 + (half ^ 16) + 256;
+    }
+  }
+  auto read_n = [&](int buf, int lo, int j) {
+    if constexpr (SYM) return pn[buf * STAGE + lo * 4 * TN + j * 64];
+    typedef short v4s __attribute__((ext_vector_type(4)));
+    typedef __attribute__((address_space(3))) v4s* lds_v4s;
+    const int at = (buf * STAGE + lo * 4 * TN) * 16 + (j >> 1) * 2048;
+    const v4s a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s)(pt[j & 1][0] + at));
+    const v4s b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s)(pt[j & 1][1] + at));
+    return cat(__builtin_bit_cast(uint2, a), __builtin_bit_cast(uint2, b));
+  };
+  auto times = [&](const uint4& m, const uint4& k, const f32x4& c) { return SYM ? mfma_f16(m, k, c) : mfma_f16(k, m, c); };
   uint4 nh[NJ], nl[NJ], mh[2], ml[2];
   auto read_m = [&](int buf, int i) {
     mh[i & 1] = pm[buf * STAGE + i * 64];
@@ -301,7 +374,7 @@ __global__ void __launch_bounds__(64 * WR * WC) m2rnn_orth_product_kernel(OrthAr
   static_assert((BUFS - 2) * PER < 16, "a wait's count");
 #pragma unroll
   for (int i = 0; i < BUFS - 1; ++i)
-    if (first + i < last) fetch(i, first + i);
+    if (first + i < last) fetch(i);
   int buf = 0;
   for (int s = first; s < last; ++s, buf = buf + 1 == BUFS ? 0 : buf + 1) {
     if (s + BUFS - 1 <= last)
@@ -309,18 +382,18 @@ __global__ void __launch_bounds__(64 * WR * WC) m2rnn_orth_product_kernel(OrthAr
     else
       __builtin_amdgcn_s_waitcnt(0x0f70);  // (fewer are on their way: all of them)
     lds_barrier();  // and all waves'; the buffer of the stage before has been read by all
-    if (s + BUFS - 1 < last) fetch(buf == 0 ? BUFS - 1 : buf - 1, s + BUFS - 1);
+    if (s + BUFS - 1 < last) fetch(buf == 0 ? BUFS - 1 : buf - 1);
     // in the order in which they are needed: all waves read at once here, and the first products wait for two of these
     ml[0] = pm[buf * STAGE + 4 * TM];
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
-      nh[j] = pn[buf * STAGE + j * 64];
+      nh[j] = read_n(buf, 0, j);
       __builtin_amdgcn_sched_barrier(0);
     }
     mh[0] = pm[buf * STAGE];
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
-      nl[j] = pn[buf * STAGE + 4 * TN + j * 64];
+      nl[j] = read_n(buf, 1, j);
       __builtin_amdgcn_sched_barrier(0);
     }
     // a row of tiles at a time: the next row's operands are read, and the last row's sums added, beside its products
@@ -331,17 +404,16 @@ __global__ void __launch_bounds__(64 * WR * WC) m2rnn_orth_product_kernel(OrthAr
 #pragma unroll
       for (int j = 0; j < NJ; ++j) acc[i == 0 ? NI - 1 : i - 1][j] += t[(i + NT - 1) % NT][j];
 #pragma unroll
-      for (int j = 0; j < NJ; ++j) t[i % NT][j] = mfma_f16(ml[i & 1], nh[j], f32x4{0, 0, 0, 0});
+      for (int j = 0; j < NJ; ++j) t[i % NT][j] = times(ml[i & 1], nh[j], f32x4{0, 0, 0, 0});
 #pragma unroll
-      for (int j = 0; j < NJ; ++j) t[i % NT][j] = mfma_f16(mh[i & 1], nl[j], t[i % NT][j]);
+      for (int j = 0; j < NJ; ++j) t[i % NT][j] = times(mh[i & 1], nl[j], t[i % NT][j]);
 #pragma unroll
-      for (int j = 0; j < NJ; ++j) t[i % NT][j] = mfma_f16(mh[i & 1], nh[j], t[i % NT][j]);
+      for (int j = 0; j < NJ; ++j) t[i % NT][j] = times(mh[i & 1], nh[j], t[i % NT][j]);
       __builtin_amdgcn_sched_barrier(0);
     }
   }
 #pragma unroll
   for (int j = 0; j < NJ; ++j) acc[NI - 1][j] += t[NT - 1][j];
-  // lane (g, n), register e: row 4 g + e, column n of a 16 x 16 tile
   if constexpr (SPLIT) {
     float4* dst = (float4*)A.part + (((z * A.splits + blockIdx.y) * A.tiles + tile) * WAVES + w) * (NI * NJ * 64) + lane;
 #pragma unroll
@@ -352,7 +424,7 @@ __global__ void __launch_bounds__(64 * WR * WC) m2rnn_orth_product_kernel(OrthAr
   } else {
 #pragma unroll
     for (int i = 0; i < NI; ++i)
-      orth_finish<EPI, NJ>(A, z, r0 + wr + 16 * i + 4 * g, c0 + wc + n, acc[i], !SYM || bj < bi * (TM / TN));
+      orth_finish<EPI, NJ>(A, z, r0 + wr + 16 * i, c0 + wc, g, n, acc[i], bj < bi * (TM / TN));
   }
 }
 
@@ -369,7 +441,7 @@ __global__ void __launch_bounds__(256) m2rnn_orth_join_kernel(OrthArgs A) {
   int bi, bj;
   orth_place<SYM, TM / TN>(tile, A.gi, A.gj, bi, bj);
   const int n = lane & 15, g = lane >> 4;
-  const int r = bi * TM + (w / WC) * (TM / WR) + 16 * i + 4 * g, c = bj * TN + (w % WC) * (TN / WC) + n;
+  const int r = bi * TM + (w / WC) * (TM / WR) + 16 * i, c = bj * TN + (w % WC) * (TN / WC);
   f32x4 acc[NJ];
 #pragma unroll
   for (int j = 0; j < NJ; ++j) acc[j] = f32x4{0, 0, 0, 0};
@@ -378,7 +450,7 @@ __global__ void __launch_bounds__(256) m2rnn_orth_join_kernel(OrthArgs A) {
 #pragma unroll
     for (int j = 0; j < NJ; ++j) acc[j] += src[j * 64];
   }
-  orth_finish<EPI, NJ>(A, z, r, c, acc, !SYM || bj < bi * (TM / TN));
+  orth_finish<EPI, NJ>(A, z, r, c, g, n, acc, bj < bi * (TM / TN));
 }
 
 // Small matrices: one workgroup takes a matrix through all its steps, X in registers (fp32) and as planes in LDS, A and
