@@ -27,9 +27,10 @@ constexpr int kOrthK = 32;  // contraction of a stage
 struct Planes {
   uint16_t *hi, *lo;
 };
-// Within a block, 16-byte unit u of row r is at u ^ plane_turn(r): the eight rows that a read of an operand touches at a
-// time, and the four half rows of a transposing read, cover all banks.
-__device__ __forceinline__ int plane_turn(int r) { return (r & 2) | ((r >> 2) & 1); }
+// Within a block, 16-byte unit u of row r is at u ^ plane_turn(r): the lanes that the LDS serves together then touch all
+// banks, where an operand is read along its rows (0-3 and 12-15 of one unit with 4-11 of the next: 238 bytes a clock,
+// 123 with unit u at u) and by transposing reads (rows r and r + 8 of one half: 137 and 125).
+__device__ __forceinline__ int plane_turn(int r) { return (r >> 2) & 2; }
 // Where element (r, c) lies.
 __device__ __forceinline__ long plane_at(int r, int c, int ld) {
   return ((long)(r >> 4) * (ld >> 5) + (c >> 5)) * 512 + ((r & 15) * 4 + (((c >> 3) & 3) ^ plane_turn(r))) * 8 + (c & 7);
@@ -340,24 +341,20 @@ __global__ void __launch_bounds__(64 * WR * WC) m2rnn_orth_product_kernel(OrthAr
   // lane n of the group brings eight bytes of row n / 4.  Even and odd tiles of 16 columns are a block's halves (a wave may
   // begin with either).
   typedef __attribute__((address_space(3))) const char* lds_bytes;
-  lds_bytes pt[2][2];
+  lds_bytes pt[2];
   {
-    const int odd = (wc >> 4) & 1, at = (g >> 1) * 1024 + (8 * (g & 1) + (n >> 2)) * 64 + (((n >> 1) & 1) ^ (n >> 3 << 1)) * 16 + (n & 1) * 8;
-    const lds_bytes base = (lds_bytes)(lds + 8 * TM) + (wc >> 5) * 2048;
+    const int row = 8 * (g & 1) + (n >> 2), odd = (wc >> 4) & 1;
+    const int at = (g >> 1) * 1024 + row * 64 + (((n >> 1) & 1) ^ plane_turn(row)) * 16 + (n & 1) * 8;
 #pragma unroll
-    for (int p = 0; p < 2; ++p) {
-      const int half = at ^ ((p ^ odd) * 32);
-      pt[p][0] = base + (p & odd) * 2048 + half;
-      pt[p][1] = base + (p & odd) * 2048 + (half ^ 16) + 256;
-    }
+    for (int p = 0; p < 2; ++p) pt[p] = (lds_bytes)(lds + 8 * TM) + ((wc >> 5) + (p & odd)) * 2048 + (at ^ ((p ^ odd) * 32));
   }
   auto read_n = [&](int buf, int lo, int j) {
     if constexpr (SYM) return pn[buf * STAGE + lo * 4 * TN + j * 64];
     typedef short v4s __attribute__((ext_vector_type(4)));
     typedef __attribute__((address_space(3))) v4s* lds_v4s;
     const int at = (buf * STAGE + lo * 4 * TN) * 16 + (j >> 1) * 2048;
-    const v4s a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s)(pt[j & 1][0] + at));
-    const v4s b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s)(pt[j & 1][1] + at));
+    const v4s a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s)(pt[j & 1] + at));
+    const v4s b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s)(pt[j & 1] + at + 256));  // (plane_turn is the same there)
     return cat(__builtin_bit_cast(uint2, a), __builtin_bit_cast(uint2, b));
   };
   auto times = [&](const uint4& m, const uint4& k, const f32x4& c) { return SYM ? mfma_f16(m, k, c) : mfma_f16(k, m, c); };
