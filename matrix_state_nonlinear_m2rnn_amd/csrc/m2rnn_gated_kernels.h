@@ -16,6 +16,10 @@
 // tickets, whose workgroups are running and do not wait for it, so every wait ends.  Each word that is waited for says
 // itself whether it has been written (a clearing launch sets all bits of it), so no order of memory operations is needed.
 //
+// Measured: 2 x 16384 steps of 2048 channels in bf16 take 133 us (4.0 TB/s; VALU 81% of the cycles, which the exponentials and
+// polynomials of each gate take; 260 us by three launches that read the inputs twice), the backward of 4 x 4096 steps 138 us
+// (5.2 TB/s, v and a read again).
+//
 // Precision.  A gate next to 1 keeps its digits as i = 1 - f (a series in alpha s), and f h is then h - i h: f
 // itself, rounded to fp32, would be wrong by 2^-25 the same way at every step of a constant gate, 3e-4 of the memory's
 // length at i = 1e-4.  Steps with i = 0 (a masked through -infinity or the lowest number, or past the sequence's

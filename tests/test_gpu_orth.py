@@ -96,6 +96,21 @@ def test_large_tiles_that_end_inside(m, n, dtype):
     assert torch.equal(again, out)
 
 
+def test_offsets_past_2_31():
+    """A batch whose planes end past 2^31 elements: its first and last matrices."""
+    torch = torch_cuda()
+    import matrix_state_nonlinear_m2rnn_amd as m2
+    batch, m, n = 35200, 140, 300
+    if torch.cuda.get_device_properties(0).total_memory < 64 << 30:
+        pytest.skip("needs 64 GB")
+    g = torch.empty(batch, m, n, dtype=torch.bfloat16, device="cuda").normal_(generator=torch.Generator("cuda").manual_seed(9))
+    out = m2.m2rnn_orthogonalize(g)
+    for part in (slice(0, 2), slice(batch - 2, batch)):
+        check(g[part], out[part])
+    del g, out
+    torch.cuda.empty_cache()
+
+
 @pytest.mark.parametrize("m,n", [(24, 40), (700, 8), (64, 64), (150, 90)])
 def test_scales_and_values_that_are_not_finite(m, n):
     """Any scale of the gradient gives the same result; zeros give zeros; one matrix that is not finite leaves the
