@@ -16,7 +16,7 @@
 // tickets, whose workgroups are running and do not wait for it, so every wait ends.  Each word that is waited for says
 // itself whether it has been written (a clearing launch sets all bits of it), so no order of memory operations is needed.
 //
-// Measured: 2 x 16384 steps of 2048 channels in bf16 take 133 us (4.0 TB/s; VALU 81% of the cycles, which the exponentials and
+// Measured: 2 x 16384 steps of 2048 channels in bf16 take 131 us (4.1 TB/s; VALU 80% of the cycles, which the exponentials and
 // polynomials of each gate take; 260 us by three launches that read the inputs twice), the backward of 4 x 4096 steps 138 us
 // (5.2 TB/s, v and a read again).
 //
@@ -252,7 +252,8 @@ __global__ void __launch_bounds__(64 * kGatedWaves, 4) m2rnn_gated_fwd_kernel(Ga
   float b[NS][4], sum[4], l[4];
 #pragma unroll
   for (int e = 0; e < 4; ++e) sum[e] = l[e] = 0.0f;
-  const bool some = __builtin_amdgcn_ballot_w64(t0 < L.len) != 0;  // whether any lane has a step in here
+  const bool some = __builtin_amdgcn_ballot_w64(t0 < L.len) != 0;          // whether any lane has a step in here
+  const bool all = __builtin_amdgcn_ballot_w64(t0 + NS > L.len) == 0;     // whether all lanes have all of them
   if (some) {
     float va[NS][4], al[4], be[4];
 #pragma unroll
@@ -290,16 +291,25 @@ __global__ void __launch_bounds__(64 * kGatedWaves, 4) m2rnn_gated_fwd_kernel(Ga
   float h[4];
 #pragma unroll
   for (int e = 0; e < 4; ++e) h[e] = J.l[w][e][lane];
+  if (all) {
 #pragma unroll
-  for (int i = 0; i < NS; ++i) {
-    const int t = t0 + i;
-    float o[4];
+    for (int i = 0; i < NS; ++i) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      if (some) h[e] = dec[i][e](h[e]) + b[i][e];
-      o[e] = t < L.len ? h[e] : 0.0f;
+      for (int e = 0; e < 4; ++e) h[e] = dec[i][e](h[e]) + b[i][e];
+      store4_nt<false>((void*)lane_base<false>(A.y, L.base), (long)(t0 + i) * A.D, h);
     }
-    if (t < A.T) store4_nt<false>((void*)lane_base<false>(A.y, L.base), (long)t * A.D, o);
+  } else {
+#pragma unroll
+    for (int i = 0; i < NS; ++i) {
+      const int t = t0 + i;
+      float o[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (some) h[e] = dec[i][e](h[e]) + b[i][e];
+        o[e] = t < L.len ? h[e] : 0.0f;
+      }
+      if (t < A.T) store4_nt<false>((void*)lane_base<false>(A.y, L.base), (long)t * A.D, o);
+    }
   }
   // the wave with the sequence's last step (its first ones, if it has none) has the state behind it: later steps hold it
   const int end = L.len > 0 ? L.len - 1 : 0;
