@@ -60,7 +60,9 @@ double rounds_us(const Shape& h, long groups, long stages) {
   return (full * h.stage[h.held - 1] + (rest ? h.stage[rest - 1] : 0.0)) * stages;
 }
 
-Cut cut_product(long batch, long rows, long cols, long K, bool sym) {
+// How a product of K terms runs; `cut`: its contraction may be cut (X X^T: the longer side.  For the others it is the shorter
+// one, and over matrices of 64 to 16384 rows a cut never paid).
+Cut cut_product(long batch, long rows, long cols, long K, bool sym, bool cut) {
   Cut best;
   const long stages = K / kOrthK;
   for (int i = 0; i < kShapeCount; ++i) {
@@ -68,7 +70,7 @@ Cut cut_product(long batch, long rows, long cols, long K, bool sym) {
     const long gi = ceil_div(rows, h.TM), gj = ceil_div(cols, h.TN);
     const long tiles = sym ? gi * (gi + 1) / 2 * (h.TM / h.TN) : gi * gj;
     for (int s : {1, 2, 3, 4, 6, 8, 12, 16}) {
-      if (s > stages) break;
+      if (s > stages || (s > 1 && !cut)) break;
       const long groups = tiles * batch * s;
       if (s > 1 && groups > 256L * h.held) break;
       const double work = (double)tiles * batch * h.TM * h.TN * K * 6.0;
@@ -98,9 +100,9 @@ struct Plan {
     n = std::max(rows, cols);
     mp = ceil_div(m, kOrthPad) * kOrthPad;
     np = ceil_div(n, kOrthPad) * kOrthPad;
-    gram = cut_product(batch, mp, mp, np, true);
-    poly = cut_product(batch, mp, mp, mp, true);
-    next = cut_product(batch, mp, np, mp, false);
+    gram = cut_product(batch, mp, mp, np, true, true);
+    poly = cut_product(batch, mp, mp, mp, true, false);
+    next = cut_product(batch, mp, np, mp, false, false);
     ma = na = 0;
     for (const Cut* c : {&gram, &poly, &next}) ma = std::max(ma, (long)c->gi * kShapes[c->shape].TM);
     na = (long)next.gj * kShapes[next.shape].TN;
@@ -109,10 +111,8 @@ struct Plan {
     part_bytes = round_up256((size_t)batch * parts * sizeof(double));
     x_bytes = round_up256((size_t)batch * ma * na * 2);
     a_bytes = round_up256((size_t)batch * ma * ma * 2);
-    split_bytes = 0;
-    for (const Cut* c : {&gram, &poly, &next})
-      if (c->splits > 1)
-        split_bytes = std::max(split_bytes, (size_t)batch * c->splits * c->tiles * kShapes[c->shape].TM * kShapes[c->shape].TN * 4);
+    const Shape& h = kShapes[gram.shape];
+    split_bytes = gram.splits > 1 ? (size_t)batch * gram.splits * gram.tiles * h.TM * h.TN * 4 : 0;
   }
   size_t bytes() const { return part_bytes + 4 * x_bytes + 4 * a_bytes + split_bytes; }
 };
@@ -122,13 +122,17 @@ int product_of(OrthArgs& A, long batch, hipStream_t s) {
   void* args[] = {&A};
   const dim3 grid((unsigned)A.tiles, (unsigned)A.splits, (unsigned)batch), block(64 * WR * WC);
   const void* one = (const void*)&m2rnn_orth_product_kernel<TM, TN, WR, WC, BUFS, EPI, false>;
-  if (A.splits == 1) return record_hip_status(hipLaunchKernel(one, grid, block, args, 0, s));
-  const void* some = (const void*)&m2rnn_orth_product_kernel<TM, TN, WR, WC, BUFS, EPI, true>;
-  const int st = record_hip_status(hipLaunchKernel(some, grid, block, args, 0, s));
-  if (st) return st;
-  const long items = (long)A.tiles * (TM / 16) * WC;
-  return record_hip_status(hipLaunchKernel((const void*)&m2rnn_orth_join_kernel<TM, TN, WR, WC, EPI>,
-                                           dim3((unsigned)ceil_div(items, 4), 1, (unsigned)batch), dim3(256), args, 0, s));
+  if constexpr (EPI == ORTH_GRAM) {
+    if (A.splits > 1) {
+      const void* some = (const void*)&m2rnn_orth_product_kernel<TM, TN, WR, WC, BUFS, EPI, true>;
+      const int st = record_hip_status(hipLaunchKernel(some, grid, block, args, 0, s));
+      if (st) return st;
+      const long items = (long)A.tiles * (TM / 16) * WC;
+      return record_hip_status(hipLaunchKernel((const void*)&m2rnn_orth_join_kernel<TM, TN, WR, WC>,
+                                               dim3((unsigned)ceil_div(items, 4), 1, (unsigned)batch), dim3(256), args, 0, s));
+    }
+  }
+  return record_hip_status(hipLaunchKernel(one, grid, block, args, 0, s));
 }
 
 template <int EPI>

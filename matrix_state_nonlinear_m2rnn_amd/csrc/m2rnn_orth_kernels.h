@@ -201,7 +201,8 @@ __device__ __forceinline__ void orth_next(const OrthArgs& A, long z, int r, int 
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const uint32_t hi = e < 2 ? h[j].x : h[j].y, lo = e < 2 ? l[j].x : l[j].y;
-      y[e] = __builtin_fmaf(A.ca, join_f16((uint16_t)(e & 1 ? hi >> 16 : hi), (uint16_t)(e & 1 ? lo >> 16 : lo)), acc[j][e] * (1.0f / kOrthB));
+      const float x = join_f16((uint16_t)(e & 1 ? hi >> 16 : hi), (uint16_t)(e & 1 ? lo >> 16 : lo));
+      y[e] = __builtin_fmaf(A.ca, x, acc[j][e] * (1.0f / kOrthB));
     }
     if constexpr (EPI == ORTH_LAST) {
       const int col = c + 16 * j;
@@ -278,7 +279,7 @@ __device__ __forceinline__ void load_to_lds(const void* from, const void* to) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(at), "v"(from) : "memory");
 }
 
-// One TM x TN tile of M N^T (NEXT and LAST: M N), or its part of a split contraction.  WR x WC waves, 16x16x32 MFMA.  A stage
+// One TM x TN tile of M N^T (NEXT and LAST: M N), or its part of a split contraction (GRAM).  WR x WC waves, 16x16x32 MFMA.  A stage
 // is 32 of the contraction: a column of blocks of M's planes, and of N's (M N: two rows of them), brought to LDS past the
 // registers.  The three passes of a stage are
 // summed by themselves, from zero, and added to the tile's sum once: one rounding at the sum's size for each stage
@@ -428,10 +429,9 @@ __global__ void __launch_bounds__(64 * WR * WC) m2rnn_orth_product_kernel(OrthAr
   }
 }
 
-// The parts of a split contraction added in order, and the epilogue.  A wave takes one row of a wave tile's 16 x 16 tiles.
-template <int TM, int TN, int WR, int WC, int EPI>
+// The parts of X X^T's split contraction added in order, and its epilogue.  A wave takes one row of a wave tile's 16 x 16 tiles.
+template <int TM, int TN, int WR, int WC>
 __global__ void __launch_bounds__(256) m2rnn_orth_join_kernel(OrthArgs A) {
-  constexpr bool SYM = EPI == ORTH_GRAM || EPI == ORTH_POLY;
   constexpr int NI = TM / WR / 16, NJ = TN / WC / 16, WAVES = WR * WC;
   const int lane = threadIdx.x & 63;
   const long z = blockIdx.z;
@@ -439,7 +439,7 @@ __global__ void __launch_bounds__(256) m2rnn_orth_join_kernel(OrthArgs A) {
   if (item >= A.tiles * WAVES * NI) return;
   const int i = item % NI, w = item / NI % WAVES, tile = item / (NI * WAVES);
   int bi, bj;
-  orth_place<SYM, TM / TN>(tile, A.gi, A.gj, bi, bj);
+  orth_place<true, TM / TN>(tile, A.gi, A.gj, bi, bj);
   const int n = lane & 15, g = lane >> 4;
   const int r = bi * TM + (w / WC) * (TM / WR) + 16 * i, c = bj * TN + (w % WC) * (TN / WC);
   f32x4 acc[NJ];
@@ -450,7 +450,7 @@ __global__ void __launch_bounds__(256) m2rnn_orth_join_kernel(OrthArgs A) {
 #pragma unroll
     for (int j = 0; j < NJ; ++j) acc[j] += src[j * 64];
   }
-  orth_finish<EPI, NJ>(A, z, r, c, g, n, acc, bj < bi * (TM / TN));
+  orth_finish<ORTH_GRAM, NJ>(A, z, r, c, g, n, acc, bj < bi * (TM / TN));
 }
 
 // Small matrices (768 of 64 x 64: 30 us, where the launches of the larger ones' kernels took 1253; LDS and VALU at 55 to 60%
