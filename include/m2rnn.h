@@ -560,9 +560,9 @@ int m2rnn_add_norm_bwd(int64_t rows, int64_t D, int h_dtype, const void* h, cons
  *   D a multiple of 4 up to 2^24, T at most 2^30, B D at most 2^35, and ceil(B D / 256) ceil(T / 32) below 2^23.
  *   Pointers 16-byte aligned (lens 4).
  * fp32 arithmetic; 1 - f is formed without cancellation.  A step whose 1 - f is zero (a = -infinity or the lowest
- * number: masked through its gate; alpha = 0) holds the state, whatever v is.  Any other value that is not finite reaches its own channel of
- * its own sequence from its step on (an infinity may become NaN), and nothing else.  Two calls on the same inputs
- * give the same bits.
+ * number: masked through its gate; alpha = 0) holds the state, whatever v is.  Any other value that is not finite
+ * reaches its own channel of its own sequence from its step on (an infinity may become NaN), and nothing else.  Two
+ * calls on the same inputs give the same bits.
  *
  * m2rnn_gated_scan_bwd gives the gradients of L = sum <dy, y> + <dh_T, h_T> from the forward's inputs and its y:
  * dv, da [B,T,D], dalpha, dbeta [D] (summed over batch and time), dh0 [B,D] (NULL to skip), all fp32.  It expects
@@ -595,8 +595,9 @@ int m2rnn_gated_scan_step(int64_t B, int64_t D, int dtype, const void* v, const 
  *   steps      1 to 64; m, n up to 65536, batch up to 65535, and less than 2^36 elements in all, sides rounded up
  *              to 64.
  * The norm is summed in fp64; products are those of fp32 (with a shorter side above 32: fp16 values in two parts, 22
- * bits, three passes with fp32 accumulation).  A matrix of zeros gives zeros (eps > 0); one with a value that is not finite is
- * not finite.  Two calls on the same inputs give the same bits.  Pointers 16-byte aligned.
+ * bits, three passes with fp32 accumulation).  A matrix of zeros gives zeros (eps > 0); one with a value that is not
+ * finite, or past the bound above, is not finite.  Two calls on the same inputs give the same bits.  Pointers 16-byte
+ * aligned.
  */
 int m2rnn_orthogonalize_workspace_size(int64_t batch, int64_t m, int64_t n, int dtype, size_t* bytes);
 int m2rnn_orthogonalize(int64_t batch, int64_t m, int64_t n, int dtype, const void* g, int64_t steps, const float* coefs,
