@@ -596,8 +596,8 @@ int m2rnn_gated_scan_step(int64_t B, int64_t D, int dtype, const void* v, const 
  *              to 64.
  * The norm is summed in fp64; products are those of fp32 (with a shorter side above 32: fp16 values in two parts, 22
  * bits, three passes with fp32 accumulation).  A matrix of zeros gives zeros (eps > 0); one with a value that is not
- * finite, or past the bound above, is not finite.  Two calls on the same inputs give the same bits.  Pointers 16-byte
- * aligned.
+ * finite is not finite, nor is one whose entries pass fp16 (entries are at most as large as the bound above says).  Two
+ * calls on the same inputs give the same bits.  Pointers 16-byte aligned.
  */
 int m2rnn_orthogonalize_workspace_size(int64_t batch, int64_t m, int64_t n, int dtype, size_t* bytes);
 int m2rnn_orthogonalize(int64_t batch, int64_t m, int64_t n, int dtype, const void* g, int64_t steps, const float* coefs,

@@ -132,6 +132,18 @@ def test_scales_and_values_that_are_not_finite(m, n):
     check(one, m2.m2rnn_orthogonalize(one))
 
 
+@pytest.mark.parametrize("m,n", [(64, 64), (100, 128), (160, 200)])
+def test_past_the_bound_is_not_finite(m, n):
+    """A product that fp16 cannot hold gives no number that could be taken for a result; thin matrices have no such bound."""
+    torch = torch_cuda()
+    import matrix_state_nonlinear_m2rnn_amd as m2
+    g = torch.zeros(1, m, n, device="cuda")
+    g[0, 1, 2] = 1.0  # one singular value, 1: B has an entry of 1000
+    assert not torch.isfinite(m2.m2rnn_orthogonalize(g, 1, (1.0, 1000.0, 0.0))).all()
+    thin = g[:, :16].contiguous()
+    assert float(m2.m2rnn_orthogonalize(thin, 1, (1.0, 1000.0, 0.0))[0, 1, 2]) == pytest.approx(1001.0, rel=1e-5)
+
+
 def test_empty_and_refusals():
     torch = torch_cuda()
     import matrix_state_nonlinear_m2rnn_amd as m2
