@@ -594,10 +594,11 @@ int m2rnn_gated_scan_step(int64_t B, int64_t D, int dtype, const void* v, const 
  *              are in fp32 and there is no such bound.  c = 0 (a cubic step) takes two products instead of three.
  *   steps      1 to 64; m, n up to 65536, batch up to 65535, and less than 2^36 elements in all, sides rounded up
  *              to 64.
- * The norm is summed in fp64; products are those of fp32 (with a shorter side above 32: fp16 values in two parts, 22
- * bits, three passes with fp32 accumulation).  A matrix of zeros gives zeros (eps > 0); one with a value that is not
- * finite is not finite, nor is one whose entries pass fp16 (entries are at most as large as the bound above says).  Two
- * calls on the same inputs give the same bits.  Pointers 16-byte aligned.
+ * The norm is summed in fp64, X is kept in fp32, and products are those of fp32 (with a shorter side above 32: fp16 values
+ * in two parts, 22 bits, each row and column at a power of two of its own, three passes with fp32 accumulation): an
+ * entry's error is relative to its row and its column, however much smaller than others these are.  A matrix of zeros
+ * gives zeros (eps > 0); one with a value that is not finite is not finite; past the bound above a result is right or not
+ * finite.  Two calls on the same inputs give the same bits.  Pointers 16-byte aligned.
  */
 int m2rnn_orthogonalize_workspace_size(int64_t batch, int64_t m, int64_t n, int dtype, size_t* bytes);
 int m2rnn_orthogonalize(int64_t batch, int64_t m, int64_t n, int dtype, const void* g, int64_t steps, const float* coefs,

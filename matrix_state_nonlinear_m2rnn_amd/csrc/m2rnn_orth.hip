@@ -2,6 +2,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <cmath>
 
 #include "../../include/m2rnn.h"
 #include "m2rnn_orth_kernels.h"
@@ -15,7 +16,8 @@ int record_hip_status(hipError_t e);
 namespace {
 
 constexpr long kOrthMaxSide = 65536;
-constexpr long kOrthParts = 1024;  // partial sums of squares of a matrix at most
+constexpr long kOrthParts = 1024;  // partial sums of squares of a thin matrix at most
+constexpr long kOrthNorms = 512;   // workgroups that a matrix's norms are dealt to, unless 64 rows each are fewer
 constexpr long kOrthPad = 64;     // sides are rounded up to it
 
 bool al16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
@@ -92,9 +94,11 @@ Cut cut_product(long batch, long rows, long cols, long K, bool sym, bool cut) {
 // Sizes with m the shorter side, rounded up (what a contraction takes), the arrays' sides (what all products' tiles cover:
 // what lies past the rounded sides is never part of a contraction), and the workspace's parts.
 struct Plan {
-  long m, n, mp, np, ma, na, parts, each;
+  long m, n, mp, np, ma, na, gx, gy, each, sums;
   Cut gram, poly, next;
-  size_t part_bytes, x_bytes, a_bytes, split_bytes;  // partial sums of squares; one fp16 plane of X, of A; split products
+  size_t row_bytes, col_bytes, all_bytes, scale_bytes;    // partial sums of squares in fp64, and the matrices' scales
+  size_t d_bytes, e_bytes, square_bytes;                  // the rows' and columns' scales; their sums of squares in fp32
+  size_t x_bytes, a_bytes, split_bytes;                   // one fp16 plane of X, of A; split products
   Plan(int64_t batch, int64_t rows, int64_t cols) {
     m = std::min(rows, cols);
     n = std::max(rows, cols);
@@ -106,21 +110,35 @@ struct Plan {
     ma = na = 0;
     for (const Cut* c : {&gram, &poly, &next}) ma = std::max(ma, (long)c->gi * kShapes[c->shape].TM);
     na = (long)next.gj * kShapes[next.shape].TN;
-    each = std::max(ceil_div(ceil_div(m * n, kOrthParts), 1024), 4L) * 1024;
-    parts = ceil_div(m * n, each);
-    part_bytes = round_up256((size_t)batch * parts * sizeof(double));
+    gx = ceil_div(cols, 256);
+    each = ceil_div(ceil_div(rows, 64), std::max(kOrthNorms / gx, 1L)) * 64;
+    gy = ceil_div(rows, each);
+    row_bytes = round_up256((size_t)batch * gx * rows * sizeof(double));
+    col_bytes = round_up256((size_t)batch * gy * cols * sizeof(double));
+    all_bytes = round_up256((size_t)batch * gx * gy * sizeof(double));
+    scale_bytes = round_up256((size_t)batch * sizeof(double));
+    sums = (long)next.gi * 2;  // (all shapes have two rows of waves)
+    d_bytes = round_up256((size_t)batch * ma * sizeof(float));
+    e_bytes = round_up256((size_t)batch * na * sizeof(float));
+    square_bytes = round_up256((size_t)batch * sums * na * sizeof(float));
     x_bytes = round_up256((size_t)batch * ma * na * 2);
     a_bytes = round_up256((size_t)batch * ma * ma * 2);
     const Shape& h = kShapes[gram.shape];
     split_bytes = gram.splits > 1 ? (size_t)batch * gram.splits * gram.tiles * h.TM * h.TN * 4 : 0;
   }
-  size_t bytes() const { return part_bytes + 4 * x_bytes + 4 * a_bytes + split_bytes; }
+  // X in fp32, R, two of C; the two scales of rows and columns, the diagonal
+  size_t bytes() const {
+    return row_bytes + col_bytes + all_bytes + scale_bytes + 3 * d_bytes + 2 * e_bytes + square_bytes + 8 * x_bytes + 4 * a_bytes +
+           split_bytes;
+  }
 };
 
 template <int TM, int TN, int WR, int WC, int BUFS, int EPI>
 int product_of(OrthArgs& A, long batch, hipStream_t s) {
   void* args[] = {&A};
-  const dim3 grid((unsigned)A.tiles, (unsigned)A.splits, (unsigned)batch), block(64 * WR * WC);
+  static_assert(WR == 2, "Plan::sums");
+  const unsigned more = EPI == ORTH_GRAM && A.en ? (unsigned)ceil_div(A.K, 64 * WR * WC) : 0;  // the next columns' scales
+  const dim3 grid((unsigned)A.tiles + more, (unsigned)A.splits, (unsigned)batch), block(64 * WR * WC);
   const void* one = (const void*)&m2rnn_orth_product_kernel<TM, TN, WR, WC, BUFS, EPI, false>;
   if constexpr (EPI == ORTH_GRAM) {
     if (A.splits > 1) {
@@ -150,6 +168,20 @@ int product(const Cut& cut, OrthArgs& A, long batch, hipStream_t s) {
     case 5: return product_of<64, 64, 2, 2, 2, EPI>(A, batch, s);
     default: return product_of<64, 64, 2, 2, 5, EPI>(A, batch, s);
   }
+}
+
+// What D^-1 B is kept times: 2^7 leaves |b s + c s^3| up to 500.  With |b s^2 + c s^4| below 24, b s is at most sqrt(48 |b|).
+float orth_unit(float b) {
+  float u = 128.0f;
+  while (!(std::sqrt(48.0f * std::fabs(b)) * u < 65000.0f) && u > 0x1p-40f) u *= 0.5f;
+  return u;
+}
+// No row or column of X grows by more than 2^this in a step: they are multiplied by matrices whose singular values are
+// |a + b s^2 + c s^4|.
+int orth_grow(float a) {
+  int k = 5;
+  while (std::ldexp(1.0f, k) < std::fabs(a) + 24.0f && k < 40) ++k;
+  return k;
 }
 
 // The kernel that takes a matrix of m x n (m <= n) through all steps in one workgroup; NULL: none does.
@@ -242,6 +274,7 @@ int m2rnn_orthogonalize(int64_t batch, int64_t m, int64_t n, int dtype, const vo
   if (x != y && x < y + size && y < x + size) return M2RNN_EINVAL;
   OrthCoefs c{};
   std::copy(coefs, coefs + 3 * steps, c.c);
+  for (int64_t i = 0; i < steps; ++i) c.unit[i] = orth_unit(coefs[3 * i + 1]);
   int lo = (int)std::min(m, n), hi = (int)std::max(m, n), turned = m > n, half = bf16, count = (int)steps;
   if (lo <= kThinRows) {
     const ThinPlan p(batch, lo, hi);
@@ -277,65 +310,92 @@ int m2rnn_orthogonalize(int64_t batch, int64_t m, int64_t n, int dtype, const vo
   if (!workspace || workspace_bytes < p.bytes() || !al16(workspace)) return M2RNN_EWORKSPACE;
   hipStream_t s = (hipStream_t)stream;
   char* at = (char*)workspace;
-  double* part = (double*)at;
-  at += p.part_bytes;
-  auto planes = [&](size_t bytes) {
-    Planes q{(uint16_t*)at, (uint16_t*)(at + bytes)};
-    at += 2 * bytes;
+  auto take = [&](size_t bytes) {
+    char* q = at;
+    at += bytes;
     return q;
   };
-  Planes X = planes(p.x_bytes), Y = planes(p.x_bytes);
+  auto planes = [&](size_t bytes) { return Planes{(uint16_t*)take(bytes), (uint16_t*)take(bytes)}; };
+  const OrthNorms N{(double*)take(p.row_bytes), (double*)take(p.col_bytes), (double*)take(p.all_bytes)};
+  double* scale = (double*)take(p.scale_bytes);
+  float *d = (float*)take(p.d_bytes), *dn = (float*)take(p.d_bytes), *diag = (float*)take(p.d_bytes);
+  float *e = (float*)take(p.e_bytes), *en = (float*)take(p.e_bytes);
+  float* sums = (float*)take(p.square_bytes);
+  float* X = (float*)take(2 * p.x_bytes);
+  const Planes R = planes(p.x_bytes);
+  Planes C = planes(p.x_bytes), Cn = planes(p.x_bytes);
   const Planes P = planes(p.a_bytes), Q = planes(p.a_bytes);
   const int tall = m > n;
-  const dim3 split((unsigned)(p.np / 64), (unsigned)(p.mp / 64), (unsigned)batch);
-  if (bf16) {
-    st = squares<true>(g, p.m * p.n, p.each, p.parts, batch, part, s);
-    if (st) return st;
-    hipLaunchKernelGGL(m2rnn_orth_split_kernel<true>, split, dim3(256), 0, s, g, (int)p.m, (int)p.n, (int)p.ma, (int)p.na,
-                       tall, (const double*)part, (int)p.parts, eps, X);
-  } else {
-    st = squares<false>(g, p.m * p.n, p.each, p.parts, batch, part, s);
-    if (st) return st;
-    hipLaunchKernelGGL(m2rnn_orth_split_kernel<false>, split, dim3(256), 0, s, g, (int)p.m, (int)p.n, (int)p.ma, (int)p.na,
-                       tall, (const double*)part, (int)p.parts, eps, X);
-  }
+  const dim3 of_norms((unsigned)p.gx, (unsigned)p.gy, (unsigned)batch);
+  const dim3 of_split((unsigned)(p.np / 64), (unsigned)(p.mp / 64), (unsigned)batch);
+  if (bf16)
+    hipLaunchKernelGGL(m2rnn_orth_norms_kernel<true>, of_norms, dim3(256), 0, s, g, (int)m, (int)n, (int)p.each, N);
+  else
+    hipLaunchKernelGGL(m2rnn_orth_norms_kernel<false>, of_norms, dim3(256), 0, s, g, (int)m, (int)n, (int)p.each, N);
+  st = record_hip_status(hipGetLastError());
+  if (st) return st;
+  hipLaunchKernelGGL(m2rnn_orth_scales_kernel, dim3((unsigned)ceil_div(p.mp + p.np, 256), (unsigned)batch), dim3(256), 0, s, N, (int)p.gx,
+                     (int)p.gy, (int)p.m, (int)p.n, (int)p.mp, (int)p.np, (int)p.ma, (int)p.na, tall, eps, scale, d, e);
+  st = record_hip_status(hipGetLastError());
+  if (st) return st;
+  if (bf16)
+    hipLaunchKernelGGL(m2rnn_orth_split_kernel<true>, of_split, dim3(256), 0, s, g, (int)p.m, (int)p.n, (int)p.ma, (int)p.na, tall, scale,
+                       d, e, X, R, C);
+  else
+    hipLaunchKernelGGL(m2rnn_orth_split_kernel<false>, of_split, dim3(256), 0, s, g, (int)p.m, (int)p.n, (int)p.ma, (int)p.na, tall, scale,
+                       d, e, X, R, C);
   st = record_hip_status(hipGetLastError());
   for (int64_t i = 0; i < steps && !st; ++i) {
-    const float *f = c.c + 3 * i;
+    const float *f = c.c + 3 * i, unit = c.unit[i];
+    const bool cubic = f[2] == 0.0f, last = i + 1 == steps;  // cubic: B = b A
     OrthArgs A{};
     A.part = (float*)at;
-    const bool cubic = f[2] == 0.0f;  // B = b A
-    A.M = A.N = X;
+    A.d = d;
+    A.e = e;
+    A.en = last ? nullptr : en;
+    A.diag = diag;
+    A.squares = sums;
+    A.sums = i == 0 ? 0 : (int)p.sums;
+    A.mp = (int)p.mp;
+    A.grow = orth_grow(f[0]);
+    A.M = A.N = R;
     A.O = cubic ? Q : P;
     A.rows = A.cols = (int)p.ma;
     A.ld = (int)p.na;
     A.K = (int)p.np;
-    A.cb = cubic ? f[1] * kOrthB : kOrthA;
+    A.cb = cubic ? f[1] * unit : kOrthA;
     st = product<ORTH_GRAM>(p.gram, A, batch, s);
     if (!st && !cubic) {
       A.M = A.N = A.E = P;
       A.O = Q;
       A.ld = (int)p.ma;
       A.K = (int)p.mp;
-      A.cb = f[1];
-      A.cc = f[2];
+      A.cb = f[1] * (unit / kOrthA);
+      A.cc = f[2] * (unit / (kOrthA * kOrthA));
       st = product<ORTH_POLY>(p.poly, A, batch, s);
     }
     if (st) break;
     A.M = Q;
     A.ld = (int)p.ma;
     A.K = (int)p.mp;
-    A.N = X;
-    A.O = Y;
+    A.N = C;
+    A.O = R;
+    A.C = Cn;
+    A.X = X;
+    A.dn = dn;
+    A.sums = (int)p.sums;
     A.cols = (int)p.na;
     A.ca = f[0];
+    A.unit = 1.0f / (unit * kOrthX);
     A.out = out;
     A.m = (int)p.m;
     A.n = (int)p.n;
     A.tall = tall;
     A.out_bf16 = bf16;
-    st = i + 1 < steps ? product<ORTH_NEXT>(p.next, A, batch, s) : product<ORTH_LAST>(p.next, A, batch, s);
-    std::swap(X, Y);
+    st = last ? product<ORTH_LAST>(p.next, A, batch, s) : product<ORTH_NEXT>(p.next, A, batch, s);
+    std::swap(C, Cn);
+    std::swap(d, dn);
+    std::swap(e, en);
   }
   return st;
 }

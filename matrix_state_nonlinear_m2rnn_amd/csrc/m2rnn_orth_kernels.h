@@ -6,12 +6,18 @@
 // Three matrix products a step:
 //     (1) A = X X^T (symmetric: its lower tiles, each written twice), (2) B = b A + c A A^T (likewise),
 //     (3) X' = a X + B X, whose right operand goes along X's columns (transposing reads).
-// Precision.  Fp32 values are split into two fp16 planes x = hi + lo (22 bits) and a product takes three passes of the
-// fp16 MFMA with fp32 accumulation (lo lo, below 2^-22 of the product, is left out): the error is that of fp32
-// products, at eight times the fp32 MFMA's rate over three.  Values are kept times a power of two that holds fp16's range:
-// X and A times 2^12, B times 2^11.  With singular values up to 1.21 (the usual coefficients' largest) the entries of X,
-// A and B = b A + c A A (its eigenvalues stay within 2.9) are below 6e3 (fp16 ends at 6.5e4), and entries down to 2^-15
-// keep both planes whole.
+// Precision.  X is kept in fp32.  What a product multiplies is split into two fp16 planes x = hi + lo (22 bits), and it takes
+// three passes of the fp16 MFMA with fp32 accumulation (lo lo, below 2^-22 of the product, is left out): the error is that of
+// fp32 products, at eight times the fp32 MFMA's rate over three.
+//
+// fp16 has no exponents to spare (2^15 down to where lo ends, 2^-24), and rows and columns of a gradient may be far smaller than
+// others, so each row and column has a power of two of its own: with D and E above the norms of X's rows and columns,
+//     R = D^-1 X and C = X E^-1      the operands of (1) and of (3), no entry above 1 (both are planes; with one set, of X
+//                                    itself, half the rows times 1e-5 were off by 1e-4, times 1e-12 by all of it),
+//     S = R R^T,  D^-1 A = S D       whose rows have the size of R's (entries stay below X's largest singular value),
+//     D^-1 B = b (D^-1 A) + c (D^-1 A)(D^-1 A)^T D,   X' = a X + D (D^-1 B) C E.
+// So errors of an entry are relative to its row and its column, as fp32 products' are.  Planes are kept times 2^15 (R, C), 2^14
+// (D^-1 A) and 2^7 or less (D^-1 B, whose rows are at most |b s + c s^3|).
 #pragma once
 
 #include "m2rnn_ssm_device.h"
@@ -19,8 +25,23 @@
 
 namespace m2rnn {
 
-constexpr float kOrthX = 4096.0f, kOrthA = 4096.0f, kOrthB = 2048.0f;
+constexpr float kOrthX = 32768.0f, kOrthA = 16384.0f;
 constexpr int kOrthK = 32;  // contraction of a stage
+
+// The power of two above |x|, from 2^-100 to 2^100 (also of zeros and what is not finite), and its inverse.
+__device__ __forceinline__ float pow2_above(float x) {
+  const int e = ((int)(__float_as_uint(x) >> 23) & 255) + 1;
+  return __uint_as_float((uint32_t)(e < 27 ? 27 : e > 227 ? 227 : e) << 23);
+}
+__device__ __forceinline__ float pow2_inverse(float p) { return __uint_as_float((254u << 23) - __float_as_uint(p)); }
+// The next scale of a row or column whose values, over the scale p, have squares that add up to `squares`, and may grow by 2^grow in the
+// step that is being taken: the power of two above their norm, times 2^grow (2^k above the square root: half the exponent).  Less than
+// 2^-48 counts as that much: a row of zeros keeps a scale.
+__device__ __forceinline__ float next_scale(float p, float squares, int grow) {
+  const int k = ((int)(__float_as_uint(fmaxf(squares, 0x1p-48f)) >> 23) - 127) >> 1;
+  const int e = (int)(__float_as_uint(p) >> 23) + k + 1 + grow;
+  return __uint_as_float((uint32_t)(e < 27 ? 27 : e > 227 ? 227 : e) << 23);
+}
 
 // Two fp16 planes of a matrix [rows][ld], in blocks of 16 rows by 32 columns (1 KB, in the order that a product's stage has
 // in LDS), so that a wave brings a block as whole lines.
@@ -44,6 +65,12 @@ __device__ __forceinline__ void split_f16(float x, uint16_t& hi, uint16_t& lo) {
 }
 __device__ __forceinline__ float join_f16(uint16_t hi, uint16_t lo) {
   return (float)__builtin_bit_cast(_Float16, hi) + (float)__builtin_bit_cast(_Float16, lo);
+}
+
+// The e-th of four values whose halves are side by side.
+__device__ __forceinline__ float half_of(uint2 hi, uint2 lo, int e) {
+  const uint32_t h = e < 2 ? hi.x : hi.y, l = e < 2 ? lo.x : lo.y;
+  return join_f16((uint16_t)(e & 1 ? h >> 16 : h), (uint16_t)(e & 1 ? l >> 16 : l));
 }
 
 template <bool BF16>
@@ -85,20 +112,113 @@ __global__ void __launch_bounds__(256) m2rnn_orth_squares_kernel(const void* g, 
   if (threadIdx.x == 0) part[(long)blockIdx.y * gridDim.x + blockIdx.x] = (red[0] + red[1]) + (red[2] + red[3]);
 }
 
-// X_0 times kOrthX as planes [ma][na], zeros past m x n up to whole workgroups, which take 64 x 64; m x n is G or, `tall`, its
-// transpose.
+// Partial sums of squares in fp64 of G's rows, of its columns and of all of it, G [rows][cols] as it lies: workgroup
+// (x, y, matrix) takes 256 columns and `each` rows (a multiple of 64).
+struct OrthNorms {
+  double *row, *col, *all;  // [batch][gridDim.x][rows], [batch][gridDim.y][cols], [batch][gridDim.y gridDim.x]
+};
 template <bool BF16>
-__global__ void __launch_bounds__(256) m2rnn_orth_split_kernel(const void* g, int m, int n, int ma, int na, int tall,
-                                                               const double* part, int parts, float eps, Planes X) {
-  __shared__ float tile[64][65];
+__global__ void __launch_bounds__(256) m2rnn_orth_norms_kernel(const void* g, int rows, int cols, int each, OrthNorms N) {
+  __shared__ double part[4][16][65];
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  const long z = blockIdx.z, at = z * rows * cols;
+  const bool wide = cols % 4 == 0;  // (aligned)
+  const int c0 = blockIdx.x * 256 + (wide ? 4 * lane : lane), step = wide ? 1 : 64;  // a lane's columns: c0 + k step
+  const int first = blockIdx.y * each, last = first + each < rows ? first + each : rows;
+  double* of_rows = N.row + (z * gridDim.x + blockIdx.x) * rows;
+  double cs[4] = {0, 0, 0, 0};
+  for (int r0 = first; r0 < last; r0 += 64) {
+    float x[16][4];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const int r = r0 + 16 * w + i;
+      const long o = at + (long)r * cols + c0;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) x[i][k] = 0.0f;
+      if (r < last) {
+        if (wide) {
+          if (c0 < cols) {
+            const float4 t = load4<BF16>(g, o);
+            x[i][0] = t.x; x[i][1] = t.y; x[i][2] = t.z; x[i][3] = t.w;
+          }
+        } else {
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (c0 + 64 * k < cols) x[i][k] = load1<BF16>(g, o + 64 * k);
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      double s = 0.0;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const double q = (double)x[i][k] * (double)x[i][k];
+        cs[k] += q;
+        s += q;
+      }
+      part[w][i][lane] = s;
+    }
+    __syncthreads();
+    double s = 0.0;  // four lanes a row
+#pragma unroll
+    for (int k = 0; k < 16; ++k) s += part[w][lane >> 2][16 * (lane & 3) + k];
+    s += __shfl_xor(s, 1);
+    s += __shfl_xor(s, 2);
+    const int r = r0 + 16 * w + (lane >> 2);
+    if ((lane & 3) == 0 && r < last) of_rows[r] = s;
+    __syncthreads();
+  }
+  double* sum = &part[0][0][0];  // [4][256]
+#pragma unroll
+  for (int k = 0; k < 4; ++k) sum[w * 256 + (wide ? 4 * lane + k : lane + 64 * k)] = cs[k];
+  __syncthreads();
+  const int t = threadIdx.x, c = blockIdx.x * 256 + t;
+  double s = (sum[t] + sum[256 + t]) + (sum[512 + t] + sum[768 + t]);
+  if (c < cols) N.col[(z * gridDim.y + blockIdx.y) * cols + c] = s;
+  s = wave_sum(s);  // (columns past the end are zeros)
+  if (lane == 0) sum[1024 + w] = s;
+  __syncthreads();
+  if (t == 0) N.all[(z * gridDim.y + blockIdx.y) * gridDim.x + blockIdx.x] = (sum[1024] + sum[1025]) + (sum[1026] + sum[1027]);
+}
+
+// X_0's scale 1 / (||G||_F + eps) for each matrix, and the powers of two above the norms of its rows (d) and columns (e): a thread
+// each, of the mp rows and np columns.  gx, gy: the workgroups that the sums are of.  m x n is G or, `tall`, its transpose.
+__global__ void __launch_bounds__(256) m2rnn_orth_scales_kernel(OrthNorms N, int gx, int gy, int m, int n, int mp, int np, int ma, int na,
+                                                                int tall, float eps, double* scale, float* d, float* e) {
   __shared__ double red[4];
-  const long z = blockIdx.z;
+  const long z = blockIdx.y;
   double ss = 0.0;
-  for (int i = threadIdx.x; i < parts; i += 256) ss += part[z * parts + i];
+  for (int i = threadIdx.x; i < gx * gy; i += 256) ss += N.all[z * gx * gy + i];
   ss = wave_sum(ss);
   if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = ss;
   __syncthreads();
-  const double scale = (double)kOrthX / (sqrt((red[0] + red[1]) + (red[2] + red[3])) + (double)eps);
+  const double f = 1.0 / (sqrt((red[0] + red[1]) + (red[2] + red[3])) + (double)eps);
+  if (blockIdx.x == 0 && threadIdx.x == 0) scale[z] = f;
+  const int t = blockIdx.x * 256 + threadIdx.x;
+  const bool row = t < mp;
+  const int i = row ? t : t - mp;
+  if (!row && i >= np) return;
+  double s = 0.0;
+  if (i < (row ? m : n)) {
+    const bool of_rows = row != (tall != 0);  // whether it is a row of G
+    const int parts = of_rows ? gx : gy, side = row ? m : n;
+    const double* p = (of_rows ? N.row : N.col) + z * parts * side + i;
+#pragma unroll 16
+    for (int k = 0; k < parts; ++k) s += p[(long)k * side];
+  }
+  (row ? d + z * ma : e + z * na)[i] = pow2_above((float)(sqrt(s) * f));
+}
+
+// X_0 in fp32 and as planes R and C, [ma][na], zeros past m x n up to whole workgroups, which take 64 x 64; m x n is G or, `tall`, its
+// transpose.
+template <bool BF16>
+__global__ void __launch_bounds__(256) m2rnn_orth_split_kernel(const void* g, int m, int n, int ma, int na, int tall,
+                                                               const double* scale, const float* d, const float* e, float* X, Planes R,
+                                                               Planes C) {
+  __shared__ float tile[64][65];
+  const long z = blockIdx.z;
+  const double f = scale[z];
   const int r0 = blockIdx.y * 64, c0 = blockIdx.x * 64;
   const int tx = threadIdx.x & 63, ty = threadIdx.x >> 6;
   const long at = z * m * n;
@@ -106,27 +226,36 @@ __global__ void __launch_bounds__(256) m2rnn_orth_split_kernel(const void* g, in
   for (int i = ty; i < 64; i += 4) {  // (i, tx) along G's own rows
     const int r = tall ? r0 + tx : r0 + i, c = tall ? c0 + i : c0 + tx;
     float x = 0.0f;
-    if (r < m && c < n) x = (float)((double)load1<BF16>(g, at + (tall ? (long)c * m + r : (long)r * n + c)) * scale);
+    if (r < m && c < n) x = (float)((double)load1<BF16>(g, at + (tall ? (long)c * m + r : (long)r * n + c)) * f);
     tile[tall ? tx : i][tall ? i : tx] = x;
   }
   __syncthreads();
+#pragma unroll 8
+  for (int i = ty; i < 64; i += 4) X[(z * ma + r0 + i) * na + c0 + tx] = tile[i][tx];
   // 8 blocks of the planes, two of them a wave, a lane the unit that lies at its place
   const int row = tx >> 2, unit = (tx & 3) ^ plane_turn(row);
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
     const int id = 2 * ty + k, br = 16 * (id >> 1), bc = 32 * (id & 1);
-    alignas(16) uint16_t hi[8], lo[8];
+    const float rd = kOrthX * pow2_inverse(d[z * ma + r0 + br + row]);
+    alignas(16) uint16_t hi[8], lo[8], chi[8], clo[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) split_f16(tile[br + row][bc + 8 * unit + e], hi[e], lo[e]);
+    for (int q = 0; q < 8; ++q) {
+      const float x = tile[br + row][bc + 8 * unit + q];
+      split_f16(x * rd, hi[q], lo[q]);
+      split_f16(x * (kOrthX * pow2_inverse(e[z * na + c0 + bc + 8 * unit + q])), chi[q], clo[q]);
+    }
     const long o = z * ma * na + plane_at(r0 + br, c0 + bc, na) + tx * 8;
-    *(uint4*)(X.hi + o) = *(const uint4*)hi;
-    *(uint4*)(X.lo + o) = *(const uint4*)lo;
+    *(uint4*)(R.hi + o) = *(const uint4*)hi;
+    *(uint4*)(R.lo + o) = *(const uint4*)lo;
+    *(uint4*)(C.hi + o) = *(const uint4*)chi;
+    *(uint4*)(C.lo + o) = *(const uint4*)clo;
   }
 }
 
 constexpr int kOrthMaxSteps = 64;
 struct OrthCoefs {
-  float c[3 * kOrthMaxSteps];
+  float c[3 * kOrthMaxSteps], unit[kOrthMaxSteps];  // unit: what D^-1 B is kept times
 };
 
 // What a product's epilogue does with its tile.
@@ -134,16 +263,24 @@ enum { ORTH_GRAM = 0, ORTH_POLY = 1, ORTH_NEXT = 2, ORTH_LAST = 3 };
 
 struct OrthArgs {
   Planes M, N;        // rows x ld and cols x ld (NEXT and LAST: ld x cols), of which the contraction takes K
-  Planes E;           // POLY: A
-  Planes O;           // the output, rows x cols
+  Planes E;           // POLY: D^-1 A
+  Planes O, C;        // the outputs, rows x cols: GRAM and POLY one, NEXT R and C
+  float* X;           // NEXT and LAST: X [rows][cols], the step before's (NEXT: the next one's in its place)
   void* out;          // LAST: [m][n], or [n][m] if tall
   float* part;        // [batch][splits][tiles][waves] wave tiles of partial sums, if the contraction is split
+  const float *d, *e; // the scales of X's rows [batch][ma] and columns [batch][na]
+  float *dn, *en;     // those of the next X: dn is written by NEXT, en by GRAM
+  float* diag;        // [batch][ma]: the diagonal of S = R R^T, written by GRAM, read by NEXT
+  float* squares;     // [batch][sums][na]: sums of squares of X E^-1 over some rows each, written by NEXT, read by the next GRAM
+  int sums;           // how many there are (0: none yet, the norms are those of the scales)
   int rows, cols, ld; // the arrays' sides: at least what the tiles cover
   int K, gi, gj;      // the contraction's length; rows and columns of tiles
-  int m, n;
+  int m, n, mp;       // X's sides, the shorter one rounded up
   int tall, out_bf16;
   int splits, tiles;
-  float ca, cb, cc;
+  float ca, cb, cc;   // NEXT and LAST: a.  GRAM: what S D is multiplied by.  POLY: b and c with the planes' units
+  float unit;         // NEXT and LAST: 1 over the units of the product's operands
+  int grow;           // no row or column grows by more than 2^grow within a step
 };
 
 // GRAM and POLY: a lane's part of NJ 16 x 16 tiles side by side, rows r .. r + 3 of the columns c + 16 j.  `mirror`: the
@@ -151,7 +288,13 @@ struct OrthArgs {
 template <int EPI, int NJ>
 __device__ __forceinline__ void orth_square(const OrthArgs& A, long z, int r, int c, const f32x4 (&acc)[NJ], bool mirror) {
   const long zo = z * A.rows * A.cols;
-  float x[NJ][4];
+  const float* d = A.d + z * A.rows;
+  const float4 t4 = *(const float4*)(d + r);
+  const float dr[4] = {t4.x, t4.y, t4.z, t4.w};
+  float x[NJ][4], dc[NJ];
+  uint2 mh[NJ], ml[NJ];
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) dc[j] = d[c + 16 * j];
   if constexpr (EPI == ORTH_POLY) {
 #pragma unroll
     for (int j = 0; j < NJ; ++j)
@@ -160,55 +303,95 @@ __device__ __forceinline__ void orth_square(const OrthArgs& A, long z, int r, in
         const long at = zo + plane_at(r + e, c + 16 * j, A.cols);
         x[j][e] = join_f16(A.E.hi[at], A.E.lo[at]);
       }
+    if (mirror) {
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) {
+        const long at = zo + plane_at(c + 16 * j, r, A.rows);  // (four neighbours: r is a multiple of 4)
+        mh[j] = *(const uint2*)(A.E.hi + at);
+        ml[j] = *(const uint2*)(A.E.lo + at);
+      }
+    }
   }
 #pragma unroll
   for (int j = 0; j < NJ; ++j) {
-    uint16_t hi[4], lo[4];
+    float s[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      float y = acc[j][e];
-      if constexpr (EPI == ORTH_GRAM)
-        y *= A.cb * (1.0f / (kOrthX * kOrthX));  // (A, or B of a cubic step, times its power of two)
-      else
-        y = __builtin_fmaf(A.cb * (kOrthB / kOrthA), x[j][e], A.cc * (kOrthB / (kOrthA * kOrthA)) * y);
-      split_f16(y, hi[e], lo[e]);
+      s[e] = acc[j][e] * (EPI == ORTH_GRAM ? 1.0f / (kOrthX * kOrthX) : A.cc);
+      float y = s[e] * dc[j];
+      if constexpr (EPI == ORTH_GRAM) {
+        if (r + e == c + 16 * j) A.diag[z * A.rows + r + e] = s[e];
+        y *= A.cb;  // (D^-1 A, or D^-1 B of a cubic step)
+      } else {
+        y = __builtin_fmaf(A.cb, x[j][e], y);
+      }
+      uint16_t hi, lo;
+      split_f16(y, hi, lo);
       const long at = zo + plane_at(r + e, c + 16 * j, A.cols);
-      A.O.hi[at] = hi[e];
-      A.O.lo[at] = lo[e];
+      A.O.hi[at] = hi;
+      A.O.lo[at] = lo;
     }
     if (mirror) {
-      const long at = zo + plane_at(c + 16 * j, r, A.rows);  // (four neighbours: r is a multiple of 4)
+      uint16_t hi[4], lo[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        float y = s[e] * dr[e];
+        if constexpr (EPI == ORTH_GRAM)
+          y *= A.cb;
+        else
+          y = __builtin_fmaf(A.cb, half_of(mh[j], ml[j], e), y);
+        split_f16(y, hi[e], lo[e]);
+      }
+      const long at = zo + plane_at(c + 16 * j, r, A.rows);
       *(uint2*)(A.O.hi + at) = make_uint2(hi[0] | (uint32_t)hi[1] << 16, hi[2] | (uint32_t)hi[3] << 16);
       *(uint2*)(A.O.lo + at) = make_uint2(lo[0] | (uint32_t)lo[1] << 16, lo[2] | (uint32_t)lo[3] << 16);
     }
   }
 }
 
-// NEXT and LAST: a lane's part of NJ 16 x 16 tiles side by side, of row r the columns c + 16 j to c + 16 j + 3.
+// GRAM's further workgroups: the scales of the next X's columns, from the norms of this one's.
+__device__ __forceinline__ void orth_columns(const OrthArgs& A, long z, int c) {
+  if (c >= A.K) return;
+  const float* p = A.squares + z * A.sums * A.ld + c;
+  float s = A.sums == 0 ? 0.5f : 0.0f;  // (the first scales are above the norms themselves)
+#pragma unroll 8
+  for (int i = 0; i < A.sums; ++i) s += p[(long)i * A.ld];
+  A.en[z * A.ld + c] = next_scale(A.e[z * A.ld + c], s, A.grow);
+}
+
+// Sum over the 16 lanes of a row of lanes, in each of them.
+__device__ __forceinline__ float row16_sum(float x) {
+  x += dpp_all<kDppQuadXor1>(x);
+  x += dpp_all<kDppQuadXor2>(x);
+  x += dpp_all<kDppRowHalfMirror>(x);
+  return x + dpp_all<kDppRowMirror>(x);
+}
+
+// NEXT and LAST: a lane's part of NJ 16 x 16 tiles side by side, of row r the columns c + 16 j to c + 16 j + 3, which have the scales
+// e and (NEXT) en.  NEXT: adds to sq the squares for the columns' norms; `keep`: writes the row's new scale.
 template <int EPI, int NJ>
-__device__ __forceinline__ void orth_next(const OrthArgs& A, long z, int r, int c, const f32x4 (&acc)[NJ]) {
-  const long zo = z * A.rows * A.cols;
-  uint2 h[NJ], l[NJ];
+__device__ __forceinline__ void orth_next(const OrthArgs& A, long z, int r, int c, const f32x4 (&acc)[NJ], const float4 (&e)[NJ],
+                                          const float4 (&en)[NJ], f32x4 (&sq)[NJ], bool keep) {
+  float* X = A.X + (z * A.rows + r) * A.cols + c;
+  const float d = A.d[z * A.rows + r], f = d * A.unit;
+  float4 x[NJ];
 #pragma unroll
-  for (int j = 0; j < NJ; ++j) {
-    const long at = zo + plane_at(r, c + 16 * j, A.cols);
-    h[j] = *(const uint2*)(A.N.hi + at);
-    l[j] = *(const uint2*)(A.N.lo + at);
+  for (int j = 0; j < NJ; ++j) x[j] = *(const float4*)(X + 16 * j);
+  float rd = 0.0f;
+  if constexpr (EPI == ORTH_NEXT) {
+    const float dn = next_scale(d, A.diag[z * A.rows + r], A.grow);
+    if (keep) A.dn[z * A.rows + r] = dn;
+    rd = kOrthX * pow2_inverse(dn);
   }
 #pragma unroll
   for (int j = 0; j < NJ; ++j) {
-    float y[4];
+    float y[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
+    const float ec[4] = {e[j].x, e[j].y, e[j].z, e[j].w};
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const uint32_t hi = e < 2 ? h[j].x : h[j].y, lo = e < 2 ? l[j].x : l[j].y;
-      const float x = join_f16((uint16_t)(e & 1 ? hi >> 16 : hi), (uint16_t)(e & 1 ? lo >> 16 : lo));
-      y[e] = __builtin_fmaf(A.ca, x, acc[j][e] * (1.0f / kOrthB));
-    }
+    for (int q = 0; q < 4; ++q) y[q] = __builtin_fmaf(A.ca, y[q], acc[j][q] * f * ec[q]);
     if constexpr (EPI == ORTH_LAST) {
       const int col = c + 16 * j;
       const long o = z * A.m * A.n + (A.tall ? (long)col * A.m + r : (long)r * A.n + col), step = A.tall ? A.m : 1;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) y[e] *= 1.0f / kOrthX;
       if (!A.tall && A.n % 4 == 0) {  // (aligned)
         if (r < A.m && col < A.n) {
           if (A.out_bf16)
@@ -218,33 +401,33 @@ __device__ __forceinline__ void orth_next(const OrthArgs& A, long z, int r, int 
         }
       } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (r < A.m && col + e < A.n) {
+        for (int q = 0; q < 4; ++q)
+          if (r < A.m && col + q < A.n) {
             if (A.out_bf16)
-              ((__bf16*)A.out)[o + e * step] = (__bf16)y[e];
+              ((__bf16*)A.out)[o + q * step] = (__bf16)y[q];
             else
-              ((float*)A.out)[o + e * step] = y[e];
+              ((float*)A.out)[o + q * step] = y[q];
           }
       }
     } else {
-      uint16_t hi[4], lo[4];
+      const float en4[4] = {en[j].x, en[j].y, en[j].z, en[j].w};
+      uint16_t hi[4], lo[4], chi[4], clo[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) split_f16(y[e], hi[e], lo[e]);
-      const long at = zo + plane_at(r, c + 16 * j, A.cols);
+      for (int q = 0; q < 4; ++q) {
+        const float t = y[q] * pow2_inverse(en4[q]);
+        const float u = r < A.mp ? t : 0.0f;  // (nothing is known of rows past them)
+        sq[j][q] = __builtin_fmaf(u, u, sq[j][q]);
+        split_f16(y[q] * rd, hi[q], lo[q]);
+        split_f16(t * kOrthX, chi[q], clo[q]);
+      }
+      *(float4*)(X + 16 * j) = make_float4(y[0], y[1], y[2], y[3]);
+      const long at = z * A.rows * A.cols + plane_at(r, c + 16 * j, A.cols);
       *(uint2*)(A.O.hi + at) = make_uint2(hi[0] | (uint32_t)hi[1] << 16, hi[2] | (uint32_t)hi[3] << 16);
       *(uint2*)(A.O.lo + at) = make_uint2(lo[0] | (uint32_t)lo[1] << 16, lo[2] | (uint32_t)lo[3] << 16);
+      *(uint2*)(A.C.hi + at) = make_uint2(chi[0] | (uint32_t)chi[1] << 16, chi[2] | (uint32_t)chi[3] << 16);
+      *(uint2*)(A.C.lo + at) = make_uint2(clo[0] | (uint32_t)clo[1] << 16, clo[2] | (uint32_t)clo[3] << 16);
     }
   }
-}
-
-// A row of a wave's 16 x 16 tiles from (rb, cb) on, lane (g, n): GRAM and POLY hold rows 4 g + e of column n, NEXT and LAST
-// columns 4 g + e of row n.
-template <int EPI, int NJ>
-__device__ __forceinline__ void orth_finish(const OrthArgs& A, long z, int rb, int cb, int g, int n, const f32x4 (&acc)[NJ], bool mirror) {
-  if constexpr (EPI == ORTH_GRAM || EPI == ORTH_POLY)
-    orth_square<EPI, NJ>(A, z, rb + 4 * g, cb + n, acc, mirror);
-  else
-    orth_next<EPI, NJ>(A, z, rb + n, cb + 4 * g, acc);
 }
 
 // The place of tile number `id` of TM x TN tiles: those that touch the lower triangle by rows (SYM, Q = TM / TN of them for
@@ -298,10 +481,16 @@ __global__ void __launch_bounds__(64 * WR * WC) m2rnn_orth_product_kernel(OrthAr
   static_assert(2 * (BM + BN) % WAVES == 0 && TM % TN == 0, "whole blocks for each wave, whole tiles on the diagonal");
   __shared__ uint4 lds[BUFS * STAGE];  // [buffer][M hi, M lo, N hi, N lo][row][unit]
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const long z = blockIdx.z;
+  if constexpr (EPI == ORTH_GRAM) {
+    if ((int)blockIdx.x >= A.tiles) {
+      if (blockIdx.y == 0) orth_columns(A, z, ((int)blockIdx.x - A.tiles) * 64 * WAVES + (int)threadIdx.x);
+      return;
+    }
+  }
   const int tile = orth_turn(blockIdx.x, A.tiles);
   int bi, bj;
   orth_place<SYM, TM / TN>(tile, A.gi, A.gj, bi, bj);
-  const long z = blockIdx.z;
   const int r0 = bi * TM, c0 = bj * TN;
   const int stages = A.K / kOrthK;
   const int first = SPLIT ? (int)((long)stages * blockIdx.y / A.splits) : 0;
@@ -422,10 +611,33 @@ __global__ void __launch_bounds__(64 * WR * WC) m2rnn_orth_product_kernel(OrthAr
 #pragma unroll
       for (int j = 0; j < NJ; ++j)
         dst[(i * NJ + j) * 64] = make_float4(acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]);
-  } else {
+  } else if constexpr (SYM) {  // lane (g, n) has rows 4 g + e of column n
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      orth_square<EPI, NJ>(A, z, r0 + wr + 16 * i + 4 * g, c0 + wc + n, acc[i], bj < bi * (TM / TN));
+      if constexpr (EPI == ORTH_POLY && NI > 6) __builtin_amdgcn_sched_barrier(0);  // (all rows' loads at once would not fit the registers)
+    }
+  } else {  // lane (g, n) has columns 4 g + e of row n
+    const int c = c0 + wc + 4 * g;
+    float4 e[NJ], en[NJ];
+    f32x4 sq[NJ];
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      e[j] = *(const float4*)(A.e + z * A.cols + c + 16 * j);
+      en[j] = EPI == ORTH_NEXT ? *(const float4*)(A.en + z * A.cols + c + 16 * j) : e[j];
+      sq[j] = f32x4{0, 0, 0, 0};
+    }
 #pragma unroll
     for (int i = 0; i < NI; ++i)
-      orth_finish<EPI, NJ>(A, z, r0 + wr + 16 * i, c0 + wc, g, n, acc[i], bj < bi * (TM / TN));
+      orth_next<EPI, NJ>(A, z, r0 + wr + 16 * i + n, c, acc[i], e, en, sq, bj == 0 && wc == 0 && g == 0);
+    if constexpr (EPI == ORTH_NEXT) {
+      float* to = A.squares + (z * A.sums + bi * WR + w / WC) * A.cols + c;
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) {
+        const float4 t = make_float4(row16_sum(sq[j][0]), row16_sum(sq[j][1]), row16_sum(sq[j][2]), row16_sum(sq[j][3]));
+        if (n == 0) *(float4*)(to + 16 * j) = t;
+      }
+    }
   }
 }
 
@@ -450,14 +662,14 @@ __global__ void __launch_bounds__(256) m2rnn_orth_join_kernel(OrthArgs A) {
 #pragma unroll
     for (int j = 0; j < NJ; ++j) acc[j] += src[j * 64];
   }
-  orth_finish<ORTH_GRAM, NJ>(A, z, r, c, g, n, acc, bj < bi * (TM / TN));
+  orth_square<ORTH_GRAM, NJ>(A, z, r + 4 * g, c + n, acc, bj < bi * (TM / TN));
 }
 
 // Small matrices (768 of 64 x 64: 30 us, where the launches of the larger ones' kernels took 1253; LDS and VALU at 55 to 60%
-// of the cycles): one workgroup takes a matrix through all its steps, X in registers (fp32) and as planes in LDS, A and
-// then B as planes in LDS.  MP x NP the padded size; WR x WC waves over the 16 x 16 tiles of A and of X.  A lane holds four
+// of the cycles): one workgroup takes a matrix through all its steps, X in registers (fp32) and as planes in LDS (R, then C in its
+// place), D^-1 A and then D^-1 B as planes in LDS.  MP x NP the padded size; WR x WC waves over the 16 x 16 tiles of A and of X.  A lane holds four
 // rows of a column, which are neighbours in the transpose: X lies transposed in LDS (its rows are read by transposing
-// reads), and A and B are symmetric.
+// reads), and S = R R^T and (D^-1 A) (D^-1 A)^T are symmetric.
 template <int MP, int NP, int WR, int WC>
 __global__ void __launch_bounds__(64 * WR * WC) m2rnn_orth_small_kernel(const void* gin, void* out, int m, int n, int tall,
                                                                         int bf16, int steps, OrthCoefs coefs, float eps) {
@@ -465,6 +677,7 @@ __global__ void __launch_bounds__(64 * WR * WC) m2rnn_orth_small_kernel(const vo
   constexpr int AI = MP / 16 / WR, AJ = MP / 16 / WC, XJ = NP / 16 / WC;
   __shared__ __attribute__((aligned(16))) uint16_t xp[2][NP * ST], ap[2][MP * ST];
   __shared__ double red[WR * WC];
+  __shared__ __attribute__((aligned(16))) float of_rows[2][WC][MP], of_cols[2][WR][NP];  // [largest values or sums of squares]
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int g = lane >> 4, l = lane & 15;
   const int r0 = (w / WC) * (MP / WR), ca = (w % WC) * (MP / WC), cx = (w % WC) * (NP / WC);
@@ -492,7 +705,7 @@ __global__ void __launch_bounds__(64 * WR * WC) m2rnn_orth_small_kernel(const vo
   ss = 0.0;
 #pragma unroll
   for (int i = 0; i < WR * WC; ++i) ss += red[i];
-  const double scale = (double)kOrthX / (sqrt(ss) + (double)eps);
+  const double scale = 1.0 / (sqrt(ss) + (double)eps);
   // four rows of a column as one write for each plane
   auto put4 = [&](const float (&v)[4], uint16_t* hi, uint16_t* lo, int row, int col) {
     uint16_t h[4], t[4];
@@ -501,20 +714,108 @@ __global__ void __launch_bounds__(64 * WR * WC) m2rnn_orth_small_kernel(const vo
     *(uint2*)(hi + row * ST + col) = make_uint2(h[0] | (uint32_t)h[1] << 16, h[2] | (uint32_t)h[3] << 16);
     *(uint2*)(lo + row * ST + col) = make_uint2(t[0] | (uint32_t)t[1] << 16, t[2] | (uint32_t)t[3] << 16);
   };
-  auto put_x = [&]() {
-#pragma unroll
-    for (int i = 0; i < AI; ++i)
-#pragma unroll
-      for (int j = 0; j < XJ; ++j) put4(x[i][j], xp[0], xp[1], cx + 16 * j + l, r0 + 16 * i + 4 * g);
-  };
 #pragma unroll
   for (int i = 0; i < AI; ++i)
 #pragma unroll
     for (int j = 0; j < XJ; ++j)
 #pragma unroll
       for (int e = 0; e < 4; ++e) x[i][j][e] = (float)((double)x[i][j][e] * scale);
-  put_x();
-  // this wave's AI x AJ tiles of X X^T (X's rows read from the transpose's columns) or of A A^T
+  // The scales of this lane's rows and columns.  post: each wave's part of the rows' and columns' largest values (MOST), or of
+  // their sums of squares over the scales that they have; take, behind a barrier: the powers of two above them, or above the norms.
+  float d[AI][4], ec[XJ];
+  auto post = [&](auto most) {
+    constexpr bool MOST = decltype(most)::value;
+    float rows[AI][4], cols[XJ];
+#pragma unroll
+    for (int i = 0; i < AI; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) rows[i][e] = 0.0f;
+#pragma unroll
+    for (int j = 0; j < XJ; ++j) {
+      cols[j] = 0.0f;
+      const float by = MOST ? 1.0f : pow2_inverse(ec[j]);
+#pragma unroll
+      for (int i = 0; i < AI; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if constexpr (MOST) {
+            rows[i][e] = fmaxf(rows[i][e], fabsf(x[i][j][e]));
+            cols[j] = fmaxf(cols[j], fabsf(x[i][j][e]));
+          } else {
+            const float r = x[i][j][e] * pow2_inverse(d[i][e]), c = x[i][j][e] * by;
+            rows[i][e] = __builtin_fmaf(r, r, rows[i][e]);
+            cols[j] = __builtin_fmaf(c, c, cols[j]);
+          }
+        }
+    }
+    auto with = [](float p, float q) { return MOST ? fmaxf(p, q) : p + q; };
+#pragma unroll
+    for (int i = 0; i < AI; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        float r = rows[i][e];
+        r = with(r, dpp_all<kDppQuadXor1>(r));
+        r = with(r, dpp_all<kDppQuadXor2>(r));
+        r = with(r, dpp_all<kDppRowHalfMirror>(r));
+        r = with(r, dpp_all<kDppRowMirror>(r));
+        rows[i][e] = r;
+      }
+#pragma unroll
+    for (int i = 0; i < AI; ++i)
+      if (l == 0) *(float4*)&of_rows[MOST][w % WC][r0 + 16 * i + 4 * g] = make_float4(rows[i][0], rows[i][1], rows[i][2], rows[i][3]);
+#pragma unroll
+    for (int j = 0; j < XJ; ++j) {
+      float c = cols[j];
+      c = with(c, __shfl_xor(c, 16));
+      c = with(c, __shfl_xor(c, 32));
+      if (g == 0) of_cols[MOST][w / WC][cx + 16 * j + l] = c;
+    }
+  };
+  auto take = [&](auto most) {
+    constexpr bool MOST = decltype(most)::value;
+    auto with = [](float p, float q) { return MOST ? fmaxf(p, q) : p + q; };
+#pragma unroll
+    for (int i = 0; i < AI; ++i) {
+      float r[4] = {0, 0, 0, 0};
+#pragma unroll
+      for (int k = 0; k < WC; ++k) {
+        const float4 t = *(const float4*)&of_rows[MOST][k][r0 + 16 * i + 4 * g];
+        r[0] = with(r[0], t.x);
+        r[1] = with(r[1], t.y);
+        r[2] = with(r[2], t.z);
+        r[3] = with(r[3], t.w);
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) d[i][e] = MOST ? pow2_above(r[e]) : next_scale(d[i][e], r[e], 0);
+    }
+#pragma unroll
+    for (int j = 0; j < XJ; ++j) {
+      float c = 0.0f;
+#pragma unroll
+      for (int k = 0; k < WR; ++k) c = with(c, of_cols[MOST][k][cx + 16 * j + l]);
+      ec[j] = MOST ? pow2_above(c) : next_scale(ec[j], c, 0);
+    }
+  };
+  // X's planes: R (by rows) or C
+  auto put_x = [&](auto by_rows) {
+#pragma unroll
+    for (int i = 0; i < AI; ++i)
+#pragma unroll
+      for (int j = 0; j < XJ; ++j) {
+        float v[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = x[i][j][e] * (kOrthX * pow2_inverse(decltype(by_rows)::value ? d[i][e] : ec[j]));
+        put4(v, xp[0], xp[1], cx + 16 * j + l, r0 + 16 * i + 4 * g);
+      }
+  };
+  post(std::true_type{});
+  __syncthreads();
+  take(std::true_type{});
+  post(std::false_type{});
+  __syncthreads();
+  take(std::false_type{});
+  put_x(std::true_type{});
+  // this wave's AI x AJ tiles of R R^T (R's rows read from the transpose's columns) or of (D^-1 A) (D^-1 A)^T
   auto square = [&](auto of_x, f32x4 (&acc)[AI][AJ]) {
     constexpr bool X = decltype(of_x)::value;
     const uint16_t *hi = X ? xp[0] : ap[0], *lo = X ? xp[1] : ap[1];
@@ -553,7 +854,8 @@ __global__ void __launch_bounds__(64 * WR * WC) m2rnn_orth_small_kernel(const vo
   };
   __syncthreads();
   for (int s = 0; s < steps; ++s) {
-    const float fa = coefs.c[3 * s], fb = coefs.c[3 * s + 1], fc = coefs.c[3 * s + 2];
+    const float fa = coefs.c[3 * s], fb = coefs.c[3 * s + 1], fc = coefs.c[3 * s + 2], unit = coefs.unit[s];
+    const float back = 1.0f / (unit * kOrthX);
     f32x4 acc[AI][AJ];
     float a[AI][AJ][4];
     square(std::true_type{}, acc);
@@ -562,11 +864,12 @@ __global__ void __launch_bounds__(64 * WR * WC) m2rnn_orth_small_kernel(const vo
 #pragma unroll
       for (int j = 0; j < AJ; ++j)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) a[i][j][e] = acc[i][j][e] * (kOrthA / (kOrthX * kOrthX));
+        for (int e = 0; e < 4; ++e) a[i][j][e] = acc[i][j][e] * (kOrthA / (kOrthX * kOrthX)) * d[i][e];
     if (fc != 0.0f) {
       put_a(a);
       __syncthreads();
       square(std::false_type{}, acc);
+      put_x(std::false_type{});  // (all waves have read R)
       __syncthreads();
     }
 #pragma unroll
@@ -575,10 +878,14 @@ __global__ void __launch_bounds__(64 * WR * WC) m2rnn_orth_small_kernel(const vo
       for (int j = 0; j < AJ; ++j)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          a[i][j][e] = __builtin_fmaf(fb * (kOrthB / kOrthA), a[i][j][e],
-                                      fc == 0.0f ? 0.0f : fc * (kOrthB / (kOrthA * kOrthA)) * acc[i][j][e]);
+          a[i][j][e] = __builtin_fmaf(fb * (unit / kOrthA), a[i][j][e],
+                                      fc == 0.0f ? 0.0f : fc * (unit / (kOrthA * kOrthA)) * acc[i][j][e] * d[i][e]);
     put_a(a);
     __syncthreads();
+    if (fc == 0.0f) {
+      put_x(std::false_type{});
+      __syncthreads();
+    }
     f32x4 y[AI][XJ];
 #pragma unroll
     for (int i = 0; i < AI; ++i)
@@ -610,10 +917,14 @@ __global__ void __launch_bounds__(64 * WR * WC) m2rnn_orth_small_kernel(const vo
 #pragma unroll
       for (int j = 0; j < XJ; ++j)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) x[i][j][e] = __builtin_fmaf(fa, x[i][j][e], y[i][j][e] * (1.0f / kOrthB));
-    __syncthreads();
-    if (s + 1 < steps) put_x();
-    __syncthreads();
+        for (int e = 0; e < 4; ++e) x[i][j][e] = __builtin_fmaf(fa, x[i][j][e], y[i][j][e] * (d[i][e] * back) * ec[j]);
+    if (s + 1 < steps) {
+      post(std::false_type{});
+      __syncthreads();
+      take(std::false_type{});
+      put_x(std::true_type{});
+      __syncthreads();
+    }
   }
 #pragma unroll
   for (int i = 0; i < AI; ++i)
@@ -624,7 +935,7 @@ __global__ void __launch_bounds__(64 * WR * WC) m2rnn_orth_small_kernel(const vo
         const int r = r0 + 16 * i + 4 * g + e, c = cx + 16 * j + l;
         if (r < m && c < n) {
           const long o = at + (tall ? (long)c * m + r : (long)r * n + c);
-          const float v = x[i][j][e] * (1.0f / kOrthX);
+          const float v = x[i][j][e];
           if (bf16)
             ((__bf16*)out)[o] = (__bf16)v;
           else

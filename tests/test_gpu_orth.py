@@ -157,3 +157,52 @@ def test_empty_and_refusals():
     for bad, err in ((g.half(), TypeError), (g.t(), ValueError), (g[0], ValueError)):
         with pytest.raises(err):
             m2.m2rnn_orthogonalize(bad)
+
+
+def noisy_by_rows_and_columns(seed):
+    """As noisy, but a product's roundings are relative to its row and its column: their root mean squares over the whole's take the
+    place of the matrix's."""
+    r = np.random.default_rng(seed)
+
+    def put(x, K):
+        e = x * r.uniform(-1, 1, x.shape) * 2.0 ** -23
+        if K:
+            q = np.sqrt(np.mean(x * x, 1, keepdims=True)) * np.sqrt(np.mean(x * x, 0, keepdims=True)) / np.sqrt(np.mean(x * x))
+            e = e + r.normal(0, 1, x.shape) * q * (2.0 ** -22 + 2.0 ** -24 * np.sqrt(3 * K / 16))
+        return x + e
+    return put
+
+
+@pytest.mark.parametrize("size", [1e-3, 1e-7, 1e-14])
+@pytest.mark.parametrize("m,n,dtype", [(20, 700, "fp32"), (700, 16, "fp32"), (48, 60, "fp32"), (64, 100, "bf16"), (120, 100, "fp32"),
+                                       (60, 250, "fp32"), (150, 300, "fp32"), (500, 260, "fp32"), (256, 512, "bf16")])
+def test_rows_and_columns_far_smaller_than_the_others(m, n, dtype, size):
+    """Rows (of tokens that are rare, of heads hardly used), columns, and both, far smaller than the others: each keeps the digits
+    that it has by itself.  The update takes them as they are, and so do products in fp32."""
+    torch = torch_cuda()
+    import matrix_state_nonlinear_m2rnn_amd as m2
+    say("orth sizes", m, n, dtype, size)
+    r = np.random.default_rng(m + n)
+    for what in ("rows", "columns", "both"):
+        rows, cols = r.permutation(m)[: m // 2], r.permutation(n)[: n // 2]
+        G = r.normal(0, 1e-3, (m, n))
+        if what != "columns":
+            G[rows] *= size
+        if what != "rows":
+            G[:, cols] *= size
+        g = torch.tensor(G, dtype=torch.float32, device="cuda")
+        g = g.bfloat16() if dtype == "bf16" else g
+        G = g.double().cpu().numpy()
+        for steps, coefs in ((5, COEFS), (9, (1.5, -0.5, 0.0))):
+            O = m2.m2rnn_orthogonalize(g, steps, coefs).double().cpu().numpy()
+            ref = layer.orthogonalize(G, steps, coefs, 1e-7)
+            off = [layer.orthogonalize(G, steps, coefs, 1e-7, noisy_by_rows_and_columns(s)) - ref for s in (1, 2)]
+            small_r, small_c = np.zeros(m, bool), np.zeros(n, bool)
+            small_r[rows], small_c[cols] = what != "columns", what != "rows"
+            for a in {False, what != "columns"}:
+                for b in {False, what != "rows"}:
+                    part = np.ix_(small_r == a, small_c == b)
+                    tol = 6 * max(np.linalg.norm(x[part]) for x in off)
+                    tol += (2.0 ** -8 if dtype == "bf16" else 2.0 ** -24) * np.linalg.norm(ref[part])
+                    d = np.linalg.norm((O - ref)[part])
+                    assert d <= tol, (what, steps, a, b, d, tol, np.linalg.norm(ref[part]))
