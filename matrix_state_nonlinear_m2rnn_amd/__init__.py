@@ -1400,7 +1400,7 @@ def m2rnn_orthogonalize(g, steps: int = 5, coefs=ORTH_COEFS, eps: float = 1e-7, 
     if steps < 1 or len(rows) != steps or any(len(r) != 3 for r in rows):
         raise ValueError("coefs must be (a, b, c) or one such triple for each of the steps (at least one)")
     if _elsewhere(dev, stream):
-        return _there(dev, stream, m2rnn_orthogonalize, g, steps, coefs, eps, out=out, workspace=workspace)
+        return _there(dev, stream, m2rnn_orthogonalize, g, steps, rows, eps, out=out, workspace=workspace)
     out = _out(out, "out", g.dtype, shape, g)
     m, n = shape[-2:]
     batch = 1

@@ -159,6 +159,22 @@ def test_empty_and_refusals():
             m2.m2rnn_orthogonalize(bad)
 
 
+def test_coefficients_that_can_be_read_once():
+    """An iterator of coefficients gives what a list of them gives, on the current stream and on another."""
+    torch = torch_cuda()
+    import matrix_state_nonlinear_m2rnn_amd as m2
+    g = gradient(1, 20, 30, 7, "fp32")
+    rows = [(3.0, -3.5, 1.5), (1.5, -0.5, 0.0), (2.0, -1.5, 0.5)]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for given, steps in ((lambda: rows, 3), (lambda: COEFS, 5)):
+        ref = m2.m2rnn_orthogonalize(g, steps, given())
+        assert torch.equal(m2.m2rnn_orthogonalize(g, steps, iter(given())), ref)
+        out = m2.m2rnn_orthogonalize(g, steps, iter(given()), stream=side)
+        torch.cuda.synchronize()
+        assert torch.equal(out, ref)
+
+
 def noisy_by_rows_and_columns(seed):
     """As noisy, but a product's roundings are relative to its row and its column: their root mean squares over the whole's take the
     place of the matrix's."""
