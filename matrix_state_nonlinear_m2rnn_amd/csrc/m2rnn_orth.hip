@@ -18,11 +18,9 @@ namespace {
 constexpr long kOrthMaxSide = 65536;
 constexpr long kOrthParts = 1024;  // partial sums of squares of a thin matrix at most
 constexpr long kOrthNorms = 512;   // workgroups that a matrix's norms are dealt to, unless 64 rows each are fewer
-constexpr long kOrthPad = 64;     // sides are rounded up to it
 
 bool al16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 size_t round_up256(size_t x) { return (x + 255) & ~(size_t)255; }
-long ceil_div(long a, long b) { return (a + b - 1) / b; }
 
 int check_orth(int64_t batch, int64_t m, int64_t n, int dtype) {
   if (batch < 0 || m < 0 || n < 0) return M2RNN_EINVAL;
@@ -34,79 +32,14 @@ int check_orth(int64_t batch, int64_t m, int64_t n, int dtype) {
   return M2RNN_OK;
 }
 
-// Tiles that a product is cut into: their sides, workgroups that a CU holds, a stage's time (us) where it holds one, two, ...
-// of them, and the operations a us that all CUs together reach (the card's power, then); measured over products of 192 to 8192 a
-// side.
-struct Shape {
-  int TM, TN, held;
-  double stage[4], rate;
-};
-constexpr Shape kShapes[] = {{256, 256, 1, {2.15}, 9.6e8},
-                             {192, 192, 1, {1.35}, 9.6e8},
-                             {128, 128, 2, {0.95, 1.25}, 9.5e8},
-                             {128, 64, 3, {0.5, 0.63, 1.0}, 8.8e8},
-                             {96, 96, 3, {0.6, 0.87, 1.28}, 9.2e8},
-                             {64, 64, 4, {0.4, 0.45, 0.55, 0.85}, 8.4e8},
-                             {64, 64, 2, {0.3, 0.5}, 8.4e8}};  // five stages in LDS
-constexpr int kShapeCount = sizeof(kShapes) / sizeof(kShapes[0]);
-
-// How a product runs: its tiles, the parts of its contraction, and the time that this should take (us).
-struct Cut {
-  int shape = 0, splits = 1, tiles = 1, gi = 1, gj = 1;
-  double us = 0.0;
-};
-
-// The time of `groups` workgroups of `stages` stages: whole rounds of what the CUs hold, then the fullest CU of the rest.
-double rounds_us(const Shape& h, long groups, long stages) {
-  const long load = ceil_div(groups, 256), full = load / h.held, rest = load % h.held;
-  return (full * h.stage[h.held - 1] + (rest ? h.stage[rest - 1] : 0.0)) * stages;
-}
-
-// How a product of K terms runs; `cut`: its contraction may be cut (X X^T: the longer side.  For the others it is the shorter
-// one, and over matrices of 64 to 16384 rows a cut never paid).
-Cut cut_product(long batch, long rows, long cols, long K, bool sym, bool cut) {
-  Cut best;
-  const long stages = K / kOrthK;
-  for (int i = 0; i < kShapeCount; ++i) {
-    const Shape& h = kShapes[i];
-    const long gi = ceil_div(rows, h.TM), gj = ceil_div(cols, h.TN);
-    const long tiles = sym ? gi * (gi + 1) / 2 * (h.TM / h.TN) : gi * gj;
-    for (int s : {1, 2, 3, 4, 6, 8, 12, 16}) {
-      if (s > stages || (s > 1 && !cut)) break;
-      const long groups = tiles * batch * s;
-      if (s > 1 && groups > 256L * h.held) break;
-      const double work = (double)tiles * batch * h.TM * h.TN * K * 6.0;
-      double us = std::max(rounds_us(h, groups, ceil_div(stages, s)), work / h.rate) + 6.0;
-      if (s > 1) us += 4.0 + (double)groups * h.TM * h.TN * 8.0 / 4e6;  // the parts written and read, one more launch
-      if (best.us == 0.0 || us < best.us) {
-        best.shape = i;
-        best.splits = s;
-        best.tiles = (int)tiles;
-        best.gi = (int)gi;
-        best.gj = (int)gj;
-        best.us = us;
-      }
-    }
-  }
-  return best;
-}
-
-// Sizes with m the shorter side, rounded up (what a contraction takes), the arrays' sides (what all products' tiles cover:
-// what lies past the rounded sides is never part of a contraction), and the workspace's parts.
-struct Plan {
-  long m, n, mp, np, ma, na, gx, gy, each, sums;
-  Cut gram, poly, next;
+// The arrays' sides (what all products' tiles cover: what lies past the rounded sides is never part of a contraction) and the
+// workspace's parts.
+struct Plan : OrthCuts {
+  long ma, na, gx, gy, each, sums;
   size_t row_bytes, col_bytes, all_bytes, scale_bytes;    // partial sums of squares in fp64, and the matrices' scales
   size_t d_bytes, e_bytes, square_bytes;                  // the rows' and columns' scales; their sums of squares in fp32
   size_t x_bytes, a_bytes, split_bytes;                   // one fp16 plane of X, of A; split products
-  Plan(int64_t batch, int64_t rows, int64_t cols) {
-    m = std::min(rows, cols);
-    n = std::max(rows, cols);
-    mp = ceil_div(m, kOrthPad) * kOrthPad;
-    np = ceil_div(n, kOrthPad) * kOrthPad;
-    gram = cut_product(batch, mp, mp, np, true, true);
-    poly = cut_product(batch, mp, mp, mp, true, false);
-    next = cut_product(batch, mp, np, mp, false, false);
+  Plan(int64_t batch, int64_t rows, int64_t cols) : OrthCuts(batch, rows, cols) {
     ma = na = 0;
     for (const Cut* c : {&gram, &poly, &next}) ma = std::max(ma, (long)c->gi * kShapes[c->shape].TM);
     na = (long)next.gj * kShapes[next.shape].TN;
@@ -123,7 +56,7 @@ struct Plan {
     square_bytes = round_up256((size_t)batch * sums * na * sizeof(float));
     x_bytes = round_up256((size_t)batch * ma * na * 2);
     a_bytes = round_up256((size_t)batch * ma * ma * 2);
-    const Shape& h = kShapes[gram.shape];
+    const OrthShape& h = kShapes[gram.shape];
     split_bytes = gram.splits > 1 ? (size_t)batch * gram.splits * gram.tiles * h.TM * h.TN * 4 : 0;
   }
   // X in fp32, R, two of C; the two scales of rows and columns, the diagonal

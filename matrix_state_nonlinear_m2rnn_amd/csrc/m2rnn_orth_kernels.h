@@ -20,13 +20,13 @@
 // (D^-1 A) and 2^7 or less (D^-1 B, whose rows are at most |b s + c s^3|).
 #pragma once
 
+#include "m2rnn_orth_plan.h"
 #include "m2rnn_ssm_device.h"
 #include "m2rnn_stream.h"
 
 namespace m2rnn {
 
 constexpr float kOrthX = 32768.0f, kOrthA = 16384.0f;
-constexpr int kOrthK = 32;  // contraction of a stage
 
 // The power of two above |x|, from 2^-100 to 2^100 (also of zeros and what is not finite), and its inverse.
 __device__ __forceinline__ float pow2_above(float x) {
