@@ -559,10 +559,12 @@ int m2rnn_add_norm_bwd(int64_t rows, int64_t D, int h_dtype, const void* h, cons
  *              last step within (that step's y, bit for bit).  T = 0: h_T = h0.
  *   D a multiple of 4 up to 2^24, T at most 2^30, B D at most 2^35, and ceil(B D / 256) ceil(T / 32) below 2^23.
  *   Pointers 16-byte aligned (lens 4).
- * fp32 arithmetic; 1 - f is formed without cancellation.  A step whose 1 - f is zero (a = -infinity or the lowest
- * number: masked through its gate; alpha = 0) holds the state, whatever v is.  Any other value that is not finite
- * reaches its own channel of its own sequence from its step on (an infinity may become NaN), and nothing else.  Two
- * calls on the same inputs give the same bits.
+ * fp32 arithmetic; 1 - f is formed without cancellation (where alpha < 0: from the rounded f).  A step whose 1 - f is
+ * zero (a = -infinity or the lowest number: masked through its gate; alpha = 0) holds the state, whatever v is.  Any
+ * other value that is not finite reaches its own channel of its own sequence from its step on (an infinity may become
+ * NaN), and nothing else.  Two calls on the same inputs give the same bits.  Where there are several chunks a workgroup
+ * waits for those before its own, within the launch; a wait that is not served within seconds (a workspace that another
+ * call writes at the same time) ends, and the outputs behind it are then NaN, with no other sign of it.
  *
  * m2rnn_gated_scan_bwd gives the gradients of L = sum <dy, y> + <dh_T, h_T> from the forward's inputs and its y:
  * dv, da [B,T,D], dalpha, dbeta [D] (summed over batch and time), dh0 [B,D] (NULL to skip), all fp32.  It expects
