@@ -103,10 +103,12 @@ int product(const Cut& cut, OrthArgs& A, long batch, hipStream_t s) {
   }
 }
 
-// What D^-1 B is kept times: 2^7 leaves |b s + c s^3| up to 500.  With |b s^2 + c s^4| below 24, b s is at most sqrt(48 |b|).
-float orth_unit(float b) {
+// What D^-1 B is kept times: 2^7 leaves |b s + c s^3| up to 500, less for steps whose factors are so large that it could pass that where
+// |b s^2 + c s^4| is below 24: with either term below 48, b s is at most sqrt(48 |b|) and c s^3 at most (48^3 |c|)^(1/4).
+float orth_unit(float b, float c) {
+  const float most = std::sqrt(48.0f * std::fabs(b)) + 18.24f * std::sqrt(std::sqrt(std::fabs(c)));
   float u = 128.0f;
-  while (!(std::sqrt(48.0f * std::fabs(b)) * u < 65000.0f) && u > 0x1p-40f) u *= 0.5f;
+  while (!(most * u < 65000.0f) && u > 0x1p-40f) u *= 0.5f;
   return u;
 }
 // No row or column of X grows by more than 2^this in a step: they are multiplied by matrices whose singular values are
@@ -207,7 +209,7 @@ int m2rnn_orthogonalize(int64_t batch, int64_t m, int64_t n, int dtype, const vo
   if (x != y && x < y + size && y < x + size) return M2RNN_EINVAL;
   OrthCoefs c{};
   std::copy(coefs, coefs + 3 * steps, c.c);
-  for (int64_t i = 0; i < steps; ++i) c.unit[i] = orth_unit(coefs[3 * i + 1]);
+  for (int64_t i = 0; i < steps; ++i) c.unit[i] = orth_unit(coefs[3 * i + 1], coefs[3 * i + 2]);
   int lo = (int)std::min(m, n), hi = (int)std::max(m, n), turned = m > n, half = bf16, count = (int)steps;
   if (lo <= kThinRows) {
     const ThinPlan p(batch, lo, hi);

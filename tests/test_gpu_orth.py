@@ -159,6 +159,21 @@ def test_empty_and_refusals():
             m2.m2rnn_orthogonalize(bad)
 
 
+@pytest.mark.parametrize("m,n", [(30, 40), (48, 60), (120, 128), (60, 250), (150, 300), (400, 260)])
+def test_coefficients_within_their_bounds(m, n):
+    """Steps that grow X many times over and cubic ones with large factors, at singular values where they are within the bounds."""
+    torch_cuda()
+    import matrix_state_nonlinear_m2rnn_amd as m2
+    say("orth bounds", m, n)
+    g = gradient(1, m, n, 6, "fp32")
+    norm = float(g.double().norm())
+    for rows, over in (([(6.0, -14.0, 9.0), (1.5, -0.5, 0.0)], 1), ([(30.0, 0.0, 0.0), (2.0, -1.5, 0.5)], 25),
+                       ([(1.5, -6000.0, 0.0)], 70), ([(40.0, -200000.0, 0.0), (1.5, -0.5, 0.0)], 400), ([(0.0, 1.0, 2.0)], 1),
+                       ([(1.0, 0.0, 20.0), (0.5, 0.0, 0.0)], 2), ([(1.0, 0.0, 3e8)], 70)):
+        eps = (over - 1) * norm  # no singular value above 1 / over
+        check(g, m2.m2rnn_orthogonalize(g, len(rows), rows, eps), len(rows), rows, eps)
+
+
 def test_coefficients_that_can_be_read_once():
     """An iterator of coefficients gives what a list of them gives, on the current stream and on another."""
     torch = torch_cuda()
