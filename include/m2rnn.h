@@ -534,7 +534,7 @@ int m2rnn_grad_clip(const m2rnn_tensor* grads, int64_t count, void* const* out, 
  *   scale      E4M3: [rows, D / group] fp32, s = max(amax |.| / 448, 2^-126) over the group; out holds the
  *              norm's values over s, rounded to nearest even, so values are out times scale.
  *   D a multiple of 4 up to 16384; rows at most 2^31 - 1; eps >= 0.  Squares are summed in fp32 and must stay
- *   within it (|h| below 1e18).  A row with a value that is not finite is not finite: NaN where the value, or
+ *   within it (|h| below 1e18, and above 1e-18 where eps is so small that they count).  A row with a value that is not finite is not finite: NaN where the value, or
  *   its group's scale, is.  Pointers 16-byte aligned (scale 4).  No output may overlap another array except as said.
  * The backward takes h as kept (x without a residual), dout (fp32) and dh, the gradient that reaches h down the
  * stream (fp32, or NULL: zeros), and gives dx [rows, D] fp32, which is the gradient of x and of res alike, and

@@ -36,7 +36,7 @@ int check_orth(int64_t batch, int64_t m, int64_t n, int dtype) {
 // workspace's parts.
 struct Plan : OrthCuts {
   long ma, na, gx, gy, each, sums;
-  size_t row_bytes, col_bytes, all_bytes, scale_bytes;    // partial sums of squares in fp64, and the matrices' scales
+  size_t part_bytes, row_bytes, col_bytes, scale_bytes;   // partial sums of squares and largest values, and the matrices' scales
   size_t d_bytes, e_bytes, square_bytes;                  // the rows' and columns' scales; their sums of squares in fp32
   size_t x_bytes, a_bytes, split_bytes;                   // one fp16 plane of X, of A; split products
   Plan(int64_t batch, int64_t rows, int64_t cols) : OrthCuts(batch, rows, cols) {
@@ -46,9 +46,9 @@ struct Plan : OrthCuts {
     gx = ceil_div(cols, 256);
     each = ceil_div(ceil_div(rows, 64), std::max(kOrthNorms / gx, 1L)) * 64;
     gy = ceil_div(rows, each);
-    row_bytes = round_up256((size_t)batch * gx * rows * sizeof(double));
-    col_bytes = round_up256((size_t)batch * gy * cols * sizeof(double));
-    all_bytes = round_up256((size_t)batch * gx * gy * sizeof(double));
+    part_bytes = round_up256((size_t)batch * gx * gy * sizeof(double));
+    row_bytes = round_up256((size_t)batch * gx * rows * sizeof(float));
+    col_bytes = round_up256((size_t)batch * gy * cols * sizeof(float));
     scale_bytes = round_up256((size_t)batch * sizeof(double));
     sums = (long)next.gi * 2;  // (all shapes have two rows of waves)
     d_bytes = round_up256((size_t)batch * ma * sizeof(float));
@@ -61,7 +61,7 @@ struct Plan : OrthCuts {
   }
   // X in fp32, R, two of C; the two scales of rows and columns, the diagonal
   size_t bytes() const {
-    return row_bytes + col_bytes + all_bytes + scale_bytes + 3 * d_bytes + 2 * e_bytes + square_bytes + 8 * x_bytes + 4 * a_bytes +
+    return part_bytes + row_bytes + col_bytes + scale_bytes + 3 * d_bytes + 2 * e_bytes + square_bytes + 8 * x_bytes + 4 * a_bytes +
            split_bytes;
   }
 };
@@ -251,7 +251,7 @@ int m2rnn_orthogonalize(int64_t batch, int64_t m, int64_t n, int dtype, const vo
     return q;
   };
   auto planes = [&](size_t bytes) { return Planes{(uint16_t*)take(bytes), (uint16_t*)take(bytes)}; };
-  const OrthNorms N{(double*)take(p.row_bytes), (double*)take(p.col_bytes), (double*)take(p.all_bytes)};
+  const OrthNorms N{(double*)take(p.part_bytes), (float*)take(p.row_bytes), (float*)take(p.col_bytes)};
   double* scale = (double*)take(p.scale_bytes);
   float *d = (float*)take(p.d_bytes), *dn = (float*)take(p.d_bytes), *diag = (float*)take(p.d_bytes);
   float *e = (float*)take(p.e_bytes), *en = (float*)take(p.e_bytes);
@@ -263,10 +263,9 @@ int m2rnn_orthogonalize(int64_t batch, int64_t m, int64_t n, int dtype, const vo
   const int tall = m > n;
   const dim3 of_norms((unsigned)p.gx, (unsigned)p.gy, (unsigned)batch);
   const dim3 of_split((unsigned)(p.np / 64), (unsigned)(p.mp / 64), (unsigned)batch);
-  if (bf16)
-    hipLaunchKernelGGL(m2rnn_orth_norms_kernel<true>, of_norms, dim3(256), 0, s, g, (int)m, (int)n, (int)p.each, N);
-  else
-    hipLaunchKernelGGL(m2rnn_orth_norms_kernel<false>, of_norms, dim3(256), 0, s, g, (int)m, (int)n, (int)p.each, N);
+  const auto norms = n % 4 == 0 ? (bf16 ? &m2rnn_orth_norms_kernel<true, true> : &m2rnn_orth_norms_kernel<false, true>)
+                                : (bf16 ? &m2rnn_orth_norms_kernel<true, false> : &m2rnn_orth_norms_kernel<false, false>);
+  hipLaunchKernelGGL(norms, of_norms, dim3(256), 0, s, g, (int)m, (int)n, (int)p.each, N);
   st = record_hip_status(hipGetLastError());
   if (st) return st;
   hipLaunchKernelGGL(m2rnn_orth_scales_kernel, dim3((unsigned)ceil_div(p.mp + p.np, 256), (unsigned)batch), dim3(256), 0, s, N, (int)p.gx,

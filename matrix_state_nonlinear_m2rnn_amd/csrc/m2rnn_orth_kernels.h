@@ -11,7 +11,7 @@
 // fp32 products, at eight times the fp32 MFMA's rate over three.
 //
 // fp16 has no exponents to spare (2^15 down to where lo ends, 2^-24), and rows and columns of a gradient may be far smaller than
-// others, so each row and column has a power of two of its own: with D and E above the norms of X's rows and columns,
+// others, so each row and column has a power of two of its own: with D and E no less than the norms of X's rows and columns,
 //     R = D^-1 X and C = X E^-1      the operands of (1) and of (3), no entry above 1 (both are planes; with one set, of X
 //                                    itself, half the rows times 1e-5 were off by 1e-4, times 1e-12 by all of it),
 //     S = R R^T,  D^-1 A = S D       whose rows have the size of R's (entries stay below X's largest singular value),
@@ -112,84 +112,85 @@ __global__ void __launch_bounds__(256) m2rnn_orth_squares_kernel(const void* g, 
   if (threadIdx.x == 0) part[(long)blockIdx.y * gridDim.x + blockIdx.x] = (red[0] + red[1]) + (red[2] + red[3]);
 }
 
-// Partial sums of squares in fp64 of G's rows, of its columns and of all of it, G [rows][cols] as it lies: workgroup
-// (x, y, matrix) takes 256 columns and `each` rows (a multiple of 64).
-struct OrthNorms {
-  double *row, *col, *all;  // [batch][gridDim.x][rows], [batch][gridDim.y][cols], [batch][gridDim.y gridDim.x]
-};
-template <bool BF16>
-__global__ void __launch_bounds__(256) m2rnn_orth_norms_kernel(const void* g, int rows, int cols, int each, OrthNorms N) {
-  __shared__ double part[4][16][65];
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  const long z = blockIdx.z, at = z * rows * cols;
-  const bool wide = cols % 4 == 0;  // (aligned)
-  const int c0 = blockIdx.x * 256 + (wide ? 4 * lane : lane), step = wide ? 1 : 64;  // a lane's columns: c0 + k step
-  const int first = blockIdx.y * each, last = first + each < rows ? first + each : rows;
-  double* of_rows = N.row + (z * gridDim.x + blockIdx.x) * rows;
-  double cs[4] = {0, 0, 0, 0};
-  for (int r0 = first; r0 < last; r0 += 64) {
-    float x[16][4];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const int r = r0 + 16 * w + i;
-      const long o = at + (long)r * cols + c0;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) x[i][k] = 0.0f;
-      if (r < last) {
-        if (wide) {
-          if (c0 < cols) {
-            const float4 t = load4<BF16>(g, o);
-            x[i][0] = t.x; x[i][1] = t.y; x[i][2] = t.z; x[i][3] = t.w;
-          }
-        } else {
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            if (c0 + 64 * k < cols) x[i][k] = load1<BF16>(g, o + 64 * k);
-        }
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      double s = 0.0;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const double q = (double)x[i][k] * (double)x[i][k];
-        cs[k] += q;
-        s += q;
-      }
-      part[w][i][lane] = s;
-    }
-    __syncthreads();
-    double s = 0.0;  // four lanes a row
-#pragma unroll
-    for (int k = 0; k < 16; ++k) s += part[w][lane >> 2][16 * (lane & 3) + k];
-    s += __shfl_xor(s, 1);
-    s += __shfl_xor(s, 2);
-    const int r = r0 + 16 * w + (lane >> 2);
-    if ((lane & 3) == 0 && r < last) of_rows[r] = s;
-    __syncthreads();
-  }
-  double* sum = &part[0][0][0];  // [4][256]
-#pragma unroll
-  for (int k = 0; k < 4; ++k) sum[w * 256 + (wide ? 4 * lane + k : lane + 64 * k)] = cs[k];
-  __syncthreads();
-  const int t = threadIdx.x, c = blockIdx.x * 256 + t;
-  double s = (sum[t] + sum[256 + t]) + (sum[512 + t] + sum[768 + t]);
-  if (c < cols) N.col[(z * gridDim.y + blockIdx.y) * cols + c] = s;
-  s = wave_sum(s);  // (columns past the end are zeros)
-  if (lane == 0) sum[1024 + w] = s;
-  __syncthreads();
-  if (t == 0) N.all[(z * gridDim.y + blockIdx.y) * gridDim.x + blockIdx.x] = (sum[1024] + sum[1025]) + (sum[1026] + sum[1027]);
+// A power of two that is no less than the norm of `count` values of X_0 (a row or a column) of magnitude `most` at most: their root's
+// share, or 1, which is X_0's own norm.
+__device__ __forceinline__ float first_scale(float most, int count) {
+  const int root = (33 - __clz(count - 1)) >> 1;  // 2^root >= sqrt(count)
+  return fminf(pow2_above(most) * __uint_as_float((uint32_t)(127 + root) << 23), 1.0f);
 }
 
-// X_0's scale 1 / (||G||_F + eps) for each matrix, and the powers of two above the norms of its rows (d) and columns (e): a thread
-// each, of the mp rows and np columns.  gx, gy: the workgroups that the sums are of.  m x n is G or, `tall`, its transpose.
+// What X_0's scales come from, over G [rows][cols] as it lies: the partial sums of squares (fp64), and the largest magnitudes of its
+// rows and columns within a workgroup's 256 columns and `each` rows (a multiple of 64).
+struct OrthNorms {
+  double* squares;   // [batch][gridDim.y gridDim.x]
+  float *row, *col;  // [batch][gridDim.x][rows], [batch][gridDim.y][cols]
+};
+// WIDE: columns in multiples of four, of which a lane takes four neighbours; else every 64th.
+template <bool BF16, bool WIDE>
+__global__ void __launch_bounds__(256) m2rnn_orth_norms_kernel(const void* g, int rows, int cols, int each, OrthNorms N) {
+  __shared__ float most[4][256];
+  __shared__ double red[4];
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  const long z = blockIdx.z, at = z * rows * cols;
+  const int c0 = blockIdx.x * 256 + (WIDE ? 4 * lane : lane);
+  const int first = blockIdx.y * each, last = first + each < rows ? first + each : rows;
+  float* of_rows = N.row + (z * gridDim.x + blockIdx.x) * rows;
+  float of_col[4] = {0, 0, 0, 0};
+  double acc = 0.0;
+  for (int r0 = first + 16 * w; r0 < last; r0 += 64) {
+    float x[16][4], of_row = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {  // (places past the end take the first column or the last row, and count as zeros)
+      const long o = at + (long)(r0 + i < last ? r0 + i : last - 1) * cols;
+      if constexpr (WIDE) {
+        const float4 t = load4<BF16>(g, o + (c0 < cols ? c0 : 0));
+        x[i][0] = t.x; x[i][1] = t.y; x[i][2] = t.z; x[i][3] = t.w;
+      } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) x[i][k] = load1<BF16>(g, o + (c0 + 64 * k < cols ? c0 + 64 * k : 0));
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) x[i][k] = r0 + i < last && c0 + (WIDE ? 0 : 64 * k) < cols ? x[i][k] : 0.0f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      float m = 0.0f;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        acc += (double)x[i][k] * (double)x[i][k];
+        m = fmaxf(m, fabsf(x[i][k]));
+        of_col[k] = fmaxf(of_col[k], fabsf(x[i][k]));
+      }
+      m = fmaxf(m, dpp_all<kDppQuadXor1>(m));
+      m = fmaxf(m, dpp_all<kDppQuadXor2>(m));
+      m = fmaxf(m, dpp_all<kDppRowHalfMirror>(m));
+      m = fmaxf(m, dpp_all<kDppRowMirror>(m));
+      m = fmaxf(m, __shfl_xor(m, 16));
+      m = fmaxf(m, __shfl_xor(m, 32));
+      if (lane == i) of_row = m;
+    }
+    if (lane < 16 && r0 + lane < last) of_rows[r0 + lane] = of_row;
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k) most[w][WIDE ? 4 * lane + k : lane + 64 * k] = of_col[k];
+  acc = wave_sum(acc);
+  if (lane == 0) red[w] = acc;
+  __syncthreads();
+  const int t = threadIdx.x, c = blockIdx.x * 256 + t;
+  if (c < cols) N.col[(z * gridDim.y + blockIdx.y) * cols + c] = fmaxf(fmaxf(most[0][t], most[1][t]), fmaxf(most[2][t], most[3][t]));
+  if (t == 0) N.squares[(z * gridDim.y + blockIdx.y) * gridDim.x + blockIdx.x] = (red[0] + red[1]) + (red[2] + red[3]);
+}
+
+// X_0's scale 1 / (||G||_F + eps) for each matrix, and the first scales of its rows (d) and columns (e): a thread each, of the mp rows
+// and np columns.  gx, gy: the workgroups that N is of.  m x n is G or, `tall`, its transpose.
 __global__ void __launch_bounds__(256) m2rnn_orth_scales_kernel(OrthNorms N, int gx, int gy, int m, int n, int mp, int np, int ma, int na,
                                                                 int tall, float eps, double* scale, float* d, float* e) {
   __shared__ double red[4];
   const long z = blockIdx.y;
   double ss = 0.0;
-  for (int i = threadIdx.x; i < gx * gy; i += 256) ss += N.all[z * gx * gy + i];
+  for (int i = threadIdx.x; i < gx * gy; i += 256) ss += N.squares[z * gx * gy + i];
   ss = wave_sum(ss);
   if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = ss;
   __syncthreads();
@@ -199,15 +200,15 @@ __global__ void __launch_bounds__(256) m2rnn_orth_scales_kernel(OrthNorms N, int
   const bool row = t < mp;
   const int i = row ? t : t - mp;
   if (!row && i >= np) return;
-  double s = 0.0;
+  float most = 0.0f;
   if (i < (row ? m : n)) {
     const bool of_rows = row != (tall != 0);  // whether it is a row of G
     const int parts = of_rows ? gx : gy, side = row ? m : n;
-    const double* p = (of_rows ? N.row : N.col) + z * parts * side + i;
+    const float* p = (of_rows ? N.row : N.col) + z * parts * side + i;
 #pragma unroll 16
-    for (int k = 0; k < parts; ++k) s += p[(long)k * side];
+    for (int k = 0; k < parts; ++k) most = fmaxf(most, p[(long)k * side]);
   }
-  (row ? d + z * ma : e + z * na)[i] = pow2_above((float)(sqrt(s) * f));
+  (row ? d + z * ma : e + z * na)[i] = first_scale((float)((double)most * f), row ? n : m);
 }
 
 // X_0 in fp32 and as planes R and C, [ma][na], zeros past m x n up to whole workgroups, which take 64 x 64; m x n is G or, `tall`, its
@@ -353,7 +354,7 @@ __device__ __forceinline__ void orth_square(const OrthArgs& A, long z, int r, in
 __device__ __forceinline__ void orth_columns(const OrthArgs& A, long z, int c) {
   if (c >= A.K) return;
   const float* p = A.squares + z * A.sums * A.ld + c;
-  float s = A.sums == 0 ? 0.5f : 0.0f;  // (the first scales are above the norms themselves)
+  float s = A.sums == 0 ? 0.5f : 0.0f;  // (the first scales bound the norms themselves)
 #pragma unroll 8
   for (int i = 0; i < A.sums; ++i) s += p[(long)i * A.ld];
   A.en[z * A.ld + c] = next_scale(A.e[z * A.ld + c], s, A.grow);
@@ -677,7 +678,7 @@ __global__ void __launch_bounds__(64 * WR * WC) m2rnn_orth_small_kernel(const vo
   constexpr int AI = MP / 16 / WR, AJ = MP / 16 / WC, XJ = NP / 16 / WC;
   __shared__ __attribute__((aligned(16))) uint16_t xp[2][NP * ST], ap[2][MP * ST];
   __shared__ double red[WR * WC];
-  __shared__ __attribute__((aligned(16))) float of_rows[2][WC][MP], of_cols[2][WR][NP];  // [largest values or sums of squares]
+  __shared__ __attribute__((aligned(16))) float of_rows[WC][MP], of_cols[WR][NP];
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int g = lane >> 4, l = lane & 15;
   const int r0 = (w / WC) * (MP / WR), ca = (w % WC) * (MP / WC), cx = (w % WC) * (NP / WC);
@@ -720,11 +721,12 @@ __global__ void __launch_bounds__(64 * WR * WC) m2rnn_orth_small_kernel(const vo
     for (int j = 0; j < XJ; ++j)
 #pragma unroll
       for (int e = 0; e < 4; ++e) x[i][j][e] = (float)((double)x[i][j][e] * scale);
-  // The scales of this lane's rows and columns.  post: each wave's part of the rows' and columns' largest values (MOST), or of
-  // their sums of squares over the scales that they have; take, behind a barrier: the powers of two above them, or above the norms.
+  // The scales of this lane's rows and columns.  post: each wave's part of the rows' and columns' largest values (FIRST), or of their
+  // sums of squares over the scales that they have; take, behind a barrier: the scales.
   float d[AI][4], ec[XJ];
-  auto post = [&](auto most) {
-    constexpr bool MOST = decltype(most)::value;
+  auto post = [&](auto first) {
+    constexpr bool FIRST = decltype(first)::value;
+    auto with = [](float p, float q) { return FIRST ? fmaxf(p, q) : p + q; };
     float rows[AI][4], cols[XJ];
 #pragma unroll
     for (int i = 0; i < AI; ++i)
@@ -733,12 +735,12 @@ __global__ void __launch_bounds__(64 * WR * WC) m2rnn_orth_small_kernel(const vo
 #pragma unroll
     for (int j = 0; j < XJ; ++j) {
       cols[j] = 0.0f;
-      const float by = MOST ? 1.0f : pow2_inverse(ec[j]);
+      const float by = FIRST ? 1.0f : pow2_inverse(ec[j]);
 #pragma unroll
       for (int i = 0; i < AI; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          if constexpr (MOST) {
+          if constexpr (FIRST) {
             rows[i][e] = fmaxf(rows[i][e], fabsf(x[i][j][e]));
             cols[j] = fmaxf(cols[j], fabsf(x[i][j][e]));
           } else {
@@ -748,52 +750,49 @@ __global__ void __launch_bounds__(64 * WR * WC) m2rnn_orth_small_kernel(const vo
           }
         }
     }
-    auto with = [](float p, float q) { return MOST ? fmaxf(p, q) : p + q; };
 #pragma unroll
-    for (int i = 0; i < AI; ++i)
+    for (int i = 0; i < AI; ++i) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         float r = rows[i][e];
         r = with(r, dpp_all<kDppQuadXor1>(r));
         r = with(r, dpp_all<kDppQuadXor2>(r));
         r = with(r, dpp_all<kDppRowHalfMirror>(r));
-        r = with(r, dpp_all<kDppRowMirror>(r));
-        rows[i][e] = r;
+        rows[i][e] = with(r, dpp_all<kDppRowMirror>(r));
       }
-#pragma unroll
-    for (int i = 0; i < AI; ++i)
-      if (l == 0) *(float4*)&of_rows[MOST][w % WC][r0 + 16 * i + 4 * g] = make_float4(rows[i][0], rows[i][1], rows[i][2], rows[i][3]);
+      if (l == 0) *(float4*)&of_rows[w % WC][r0 + 16 * i + 4 * g] = make_float4(rows[i][0], rows[i][1], rows[i][2], rows[i][3]);
+    }
 #pragma unroll
     for (int j = 0; j < XJ; ++j) {
       float c = cols[j];
       c = with(c, __shfl_xor(c, 16));
       c = with(c, __shfl_xor(c, 32));
-      if (g == 0) of_cols[MOST][w / WC][cx + 16 * j + l] = c;
+      if (g == 0) of_cols[w / WC][cx + 16 * j + l] = c;
     }
   };
-  auto take = [&](auto most) {
-    constexpr bool MOST = decltype(most)::value;
-    auto with = [](float p, float q) { return MOST ? fmaxf(p, q) : p + q; };
+  auto take = [&](auto first) {
+    constexpr bool FIRST = decltype(first)::value;
+    auto with = [](float p, float q) { return FIRST ? fmaxf(p, q) : p + q; };
 #pragma unroll
     for (int i = 0; i < AI; ++i) {
       float r[4] = {0, 0, 0, 0};
 #pragma unroll
       for (int k = 0; k < WC; ++k) {
-        const float4 t = *(const float4*)&of_rows[MOST][k][r0 + 16 * i + 4 * g];
+        const float4 t = *(const float4*)&of_rows[k][r0 + 16 * i + 4 * g];
         r[0] = with(r[0], t.x);
         r[1] = with(r[1], t.y);
         r[2] = with(r[2], t.z);
         r[3] = with(r[3], t.w);
       }
 #pragma unroll
-      for (int e = 0; e < 4; ++e) d[i][e] = MOST ? pow2_above(r[e]) : next_scale(d[i][e], r[e], 0);
+      for (int e = 0; e < 4; ++e) d[i][e] = FIRST ? first_scale(r[e], NP) : next_scale(d[i][e], r[e], 0);
     }
 #pragma unroll
     for (int j = 0; j < XJ; ++j) {
       float c = 0.0f;
 #pragma unroll
-      for (int k = 0; k < WR; ++k) c = with(c, of_cols[MOST][k][cx + 16 * j + l]);
-      ec[j] = MOST ? pow2_above(c) : next_scale(ec[j], c, 0);
+      for (int k = 0; k < WR; ++k) c = with(c, of_cols[k][cx + 16 * j + l]);
+      ec[j] = FIRST ? first_scale(c, MP) : next_scale(ec[j], c, 0);
     }
   };
   // X's planes: R (by rows) or C
@@ -811,9 +810,6 @@ __global__ void __launch_bounds__(64 * WR * WC) m2rnn_orth_small_kernel(const vo
   post(std::true_type{});
   __syncthreads();
   take(std::true_type{});
-  post(std::false_type{});
-  __syncthreads();
-  take(std::false_type{});
   put_x(std::true_type{});
   // this wave's AI x AJ tiles of R R^T (R's rows read from the transpose's columns) or of (D^-1 A) (D^-1 A)^T
   auto square = [&](auto of_x, f32x4 (&acc)[AI][AJ]) {
