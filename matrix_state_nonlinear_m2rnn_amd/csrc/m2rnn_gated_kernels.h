@@ -18,8 +18,8 @@
 // A wait gives up after kGatedPolls looks (seconds, where microseconds do; only a workspace that two calls share can bring it there): the
 // word is then taken as it is, all bits set, so c and l are NaN, and so are the chunk's outputs and the states it hands on.
 //
-// Measured: 2 x 16384 steps of 2048 channels in bf16 take 131 us (4.1 TB/s; VALU 80% of the cycles, which the exponentials and
-// polynomials of each gate take; 260 us by three launches that read the inputs twice), the backward of 4 x 4096 steps 138 us
+// Measured: 2 x 16384 steps of 2048 channels in bf16 take 131 us with the clearing launch (4.1 TB/s; VALU 80% of the cycles, which the exponentials and
+// polynomials of each gate take; 260 us by three launches that read the inputs twice), the backward of 4 x 4096 steps 136 to 138 us
 // (5.2 TB/s, v and a read again).
 //
 // Precision.  A gate next to 1 keeps its digits as i = 1 - f (a series in alpha s), and f h is then h - i h: f

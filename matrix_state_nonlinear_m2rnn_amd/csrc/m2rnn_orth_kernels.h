@@ -465,12 +465,12 @@ __device__ __forceinline__ void load_to_lds(const void* from, const void* to) {
 
 // One TM x TN tile of M N^T (NEXT and LAST: M N), or its part of a split contraction (GRAM).  WR x WC waves, 16x16x32 MFMA.  A stage
 // is 32 of the contraction: a column of blocks of M's planes, and of N's (M N: two rows of them), brought to LDS past the
-// registers.  The three passes of a stage are
-// summed by themselves, from zero, and added to the tile's sum once: one rounding at the sum's size for each stage
-// instead of three.
-// Measured, five steps: 8192 x 2048 takes 171 to 186 us for B X by 256 x 256 tiles (1.1 to 1.2 PFLOP/s of the three passes; MFMA 62%
-// of the cycles, the card's power), 111 to 118 for X X^T; 2176 x 2048 takes 60 to 65 us by 96 x 96 tiles (0.88 PFLOP/s) and 40
-// for a symmetric product by 64 x 64 (0.65).
+// registers.  The three passes of a stage are summed by themselves, from zero, and added to the tile's sum once: one rounding at the sum's
+// size for each stage instead of three.
+// Measured, of 8192 x 2048: B X by 256 x 256 tiles 183 to 190 us in the last step (1.1 PFLOP/s of the three passes; MFMA 58% of the
+// cycles, the card's power) and 216 to 225 in the others, which write X and both operands of the next step at the end, when all
+// CUs write (134 MB more than X's two planes alone, 40 us); X X^T 113 to 120.  Of 2176 x 2048: B X 61 to 65 and 66 to 71 us by 96 x 96
+// tiles (0.84 and 0.78 PFLOP/s), 41 to 44 for a symmetric product by 64 x 64 (0.62).
 // LDS holds BUFS stages, all but the one that is multiplied on their way.  Two where a CU holds several workgroups, or a
 // tile leaves no room for more; more for the only workgroup of a CU, whose stages would otherwise each wait for memory.
 template <int TM, int TN, int WR, int WC, int BUFS, int EPI, bool SPLIT>
@@ -666,11 +666,12 @@ __global__ void __launch_bounds__(256) m2rnn_orth_join_kernel(OrthArgs A) {
   orth_square<ORTH_GRAM, NJ>(A, z, r + 4 * g, c + n, acc, bj < bi * (TM / TN));
 }
 
-// Small matrices (768 of 64 x 64: 30 us, where the launches of the larger ones' kernels took 1253; LDS and VALU at 55 to 60%
-// of the cycles): one workgroup takes a matrix through all its steps, X in registers (fp32) and as planes in LDS (R, then C in its
-// place), D^-1 A and then D^-1 B as planes in LDS.  MP x NP the padded size; WR x WC waves over the 16 x 16 tiles of A and of X.  A lane holds four
-// rows of a column, which are neighbours in the transpose: X lies transposed in LDS (its rows are read by transposing
-// reads), and S = R R^T and (D^-1 A) (D^-1 A)^T are symmetric.
+// Small matrices (768 of 64 x 64: 39 us, of which 9 are the scales and the second set of planes; the launches of the larger
+// ones' kernels took 1253; LDS and VALU at 54 and 62% of the cycles): one workgroup takes a matrix through all its steps, X in
+// registers (fp32) and as planes in LDS (R, then C in its place), D^-1 A and then D^-1 B as planes in LDS.  MP x NP the padded
+// size; WR x WC waves over the 16 x 16 tiles of A and of X.  A lane holds four rows of a column, which are neighbours in the
+// transpose: X lies transposed in LDS (its rows are read by transposing reads), and S = R R^T and (D^-1 A) (D^-1 A)^T are
+// symmetric.
 template <int MP, int NP, int WR, int WC>
 __global__ void __launch_bounds__(64 * WR * WC) m2rnn_orth_small_kernel(const void* gin, void* out, int m, int n, int tall,
                                                                         int bf16, int steps, OrthCoefs coefs, float eps) {
